@@ -8,7 +8,9 @@ step of the computation runs in the library's CUDA kernels; nothing falls
 back to PyTorch or the CPU.
 
 Layout: q, k, v, o, dO, dq, dk, dv are ``[B, H, N, D]`` contiguous CUDA
-tensors; lse and delta are ``[B, H, N]`` float32.
+tensors; lse and delta are ``[B, H, N]`` float32.  The windowed and
+shared-prefix calls take grouped heads: q, o, dO, dq with Hq heads, k, v, dk,
+dv with Hkv heads, Hq a multiple of Hkv.
 """
 from __future__ import annotations
 
@@ -22,8 +24,10 @@ from ._native import FA_BF16, FA_F32, FAError
 
 __all__ = ["fa_forward", "fa_backward_dq", "fa_backward_dkdv", "fa_backward_atomic", "fa_decode", "fa_decode_workspace_bytes",
            "fa_decode_noalloc",
+           "fa_window_forward", "fa_window_backward_dq", "fa_window_backward_dkdv", "fa_window_backward_workspace_bytes",
+           "fa_window_decode", "fa_window_decode_workspace_bytes", "fa_prefix_decode", "fa_prefix_decode_workspace_bytes",
            "fa_device_status", "fa_selftest_timeout", "FAError", "FA_BF16", "FA_F32", "attention_flops",
-           "attention"]
+           "attention", "window_attention"]
 
 _DT = {torch.bfloat16: FA_BF16, torch.float32: FA_F32}
 
@@ -199,6 +203,200 @@ def fa_decode_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torc
     return o, lse
 
 
+def _bf16(t: torch.Tensor, name: str, shape) -> None:
+    """t is a contiguous bf16 CUDA tensor of this shape on the current device."""
+    _tensor(t, name, torch.bfloat16, shape)
+
+
+def _tensor(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _grouped(q: torch.Tensor, k: torch.Tensor):
+    """Sizes (B, Hq, Nq, D, Hkv, rows of k) of grouped-head tensors."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"q and k must have 4 dimensions, got {list(q.shape)} and {list(k.shape)}")
+    (B, Hq, Nq, D), (_, Hkv, rows, _) = q.shape, k.shape
+    if Hkv < 1 or Hq % Hkv != 0:
+        raise ValueError(f"q's {Hq} heads must be a multiple of k's {Hkv}")
+    return B, Hq, Nq, D, Hkv, rows
+
+
+def _c_int(x: int) -> int:
+    """A window or sink count as a C int (anything longer than every sequence is the same mask)."""
+    return max(-1, min(int(x), (1 << 31) - 1))
+
+
+def _empty(shape, dtype: torch.dtype, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """Memory of the stream that the call runs on, so that the allocator hands it on in that stream's order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device="cuda")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device="cuda")
+
+
+def _size_query(name: str, *sizes: int) -> int:
+    import ctypes
+    out = ctypes.c_size_t(0)
+    _native.check(getattr(_native.load(), name)(*sizes, ctypes.byref(out)), name)
+    return int(out.value)
+
+
+def _workspace(workspace: Optional[torch.Tensor], need: int, stream: Optional[torch.cuda.Stream]):
+    """(pointer, bytes) of the caller's workspace or of a new one; the tensor is returned to keep it alive."""
+    if workspace is None:
+        workspace = _empty((max(need, 16),), torch.uint8, stream)
+    elif not workspace.is_cuda or workspace.device.index != torch.cuda.current_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def fa_window_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, sinks: int = 0,
+                      scale: Optional[float] = None, kv_len: Optional[int] = None, o: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """Windowed attention (fa_window_forward): q [B, Hq, Nq, D] are the last Nq of Nk positions; a row at position p
+    sees key j iff j <= p and (j < sinks or j > p - window).
+
+    k, v are [B, Hkv, rows, D]; the first kv_len rows (default: all) of each head are the Nk keys.  bf16.
+    Returns (o, lse)."""
+    B, Hq, Nq, D, Hkv, rows = _grouped(q, k)
+    Nk = rows if kv_len is None else int(kv_len)
+    for t, n, h, r in ((q, "q", Hq, Nq), (k, "k", Hkv, rows), (v, "v", Hkv, rows)):
+        _bf16(t, n, (B, h, r, D))
+    o = _empty(q.shape, q.dtype, stream) if o is None else o
+    lse = _empty((B, Hq, Nq), torch.float32, stream) if lse is None else lse
+    _bf16(o, "o", q.shape)
+    _tensor(lse, "lse", torch.float32, (B, Hq, Nq))
+    rc = _native.load().fa_window_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, Nk, rows, D,
+                                          _c_int(window), _c_int(sinks), _scale(scale, D), FA_BF16, _stream_ptr(stream))
+    _native.check(rc, "fa_window_forward")
+    return o, lse
+
+
+def fa_window_backward_dq(q, k, v, o, dO, lse, window: int, sinks: int = 0, scale: Optional[float] = None,
+                          grad_dtype: torch.dtype = torch.float32, dq: Optional[torch.Tensor] = None,
+                          delta: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """delta = rowsum(dO * O) and dQ of windowed attention (fa_window_backward_dq).  Returns (dq, delta)."""
+    B, Hq, Nq, D, Hkv, Nk = _grouped(q, k)
+    for t, n, h, r in ((q, "q", Hq, Nq), (k, "k", Hkv, Nk), (v, "v", Hkv, Nk), (o, "o", Hq, Nq), (dO, "dO", Hq, Nq)):
+        _bf16(t, n, (B, h, r, D))
+    _tensor(lse, "lse", torch.float32, (B, Hq, Nq))
+    dq = _empty(q.shape, grad_dtype, stream) if dq is None else dq
+    delta = _empty((B, Hq, Nq), torch.float32, stream) if delta is None else delta
+    code = _dtype_code(dq)
+    _tensor(dq, "dq", dq.dtype, q.shape)
+    _tensor(delta, "delta", torch.float32, (B, Hq, Nq))
+    rc = _native.load().fa_window_backward_dq(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dO), _ptr(lse), _ptr(delta),
+                                              _ptr(dq), B, Hq, Hkv, Nq, Nk, D, _c_int(window), _c_int(sinks),
+                                              _scale(scale, D), FA_BF16, code, _stream_ptr(stream))
+    _native.check(rc, "fa_window_backward_dq")
+    return dq, delta
+
+
+def fa_window_backward_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, D: int, window: int,
+                                       sinks: int) -> int:
+    """Workspace bytes fa_window_backward_dkdv needs (may be 0)."""
+    return _size_query("fa_window_backward_workspace_bytes", B, Hq, Hkv, Nq, Nk, D, _c_int(window),
+                       _c_int(sinks))
+
+
+def fa_window_backward_dkdv(q, k, v, dO, lse, delta, window: int, sinks: int = 0, scale: Optional[float] = None,
+                            grad_dtype: torch.dtype = torch.float32, dk: Optional[torch.Tensor] = None,
+                            dv: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                            stream: Optional[torch.cuda.Stream] = None):
+    """dK and dV of windowed attention, summed over each key head's query heads (fa_window_backward_dkdv).
+
+    A workspace of fa_window_backward_workspace_bytes(...) bytes is allocated here when the caller passes none.
+    Returns (dk, dv)."""
+    B, Hq, Nq, D, Hkv, Nk = _grouped(q, k)
+    for t, n, h, r in ((q, "q", Hq, Nq), (k, "k", Hkv, Nk), (v, "v", Hkv, Nk), (dO, "dO", Hq, Nq)):
+        _bf16(t, n, (B, h, r, D))
+    _tensor(lse, "lse", torch.float32, (B, Hq, Nq))
+    _tensor(delta, "delta", torch.float32, (B, Hq, Nq))
+    dk = _empty(k.shape, grad_dtype, stream) if dk is None else dk
+    dv = _empty(k.shape, grad_dtype, stream) if dv is None else dv
+    code = _dtype_code(dk)
+    _tensor(dk, "dk", dk.dtype, k.shape)
+    _tensor(dv, "dv", dk.dtype, k.shape)
+    need = fa_window_backward_workspace_bytes(B, Hq, Hkv, Nq, Nk, D, _c_int(window), _c_int(sinks))
+    workspace, nbytes = _workspace(workspace, need, stream)
+    rc = _native.load().fa_window_backward_dkdv(_ptr(q), _ptr(k), _ptr(v), _ptr(dO), _ptr(lse), _ptr(delta), _ptr(dk),
+                                                _ptr(dv), B, Hq, Hkv, Nq, Nk, D, _c_int(window), _c_int(sinks),
+                                                _scale(scale, D), FA_BF16, code, _ptr(workspace), nbytes,
+                                                _stream_ptr(stream))
+    _native.check(rc, "fa_window_backward_dkdv")
+    return dk, dv
+
+
+def _rows_and_cache(q, k, v, lens, o, lse, stream):
+    B, Hq, n_q, D, Hkv, N = _grouped(q, k)
+    for t, n, h, r in ((q, "q", Hq, n_q), (k, "k", Hkv, N), (v, "v", Hkv, N)):
+        _bf16(t, n, (B, h, r, D))
+    if lens is not None:
+        _tensor(lens, "lens", torch.int32, (B,))
+    o = _empty(q.shape, q.dtype, stream) if o is None else o
+    lse = _empty((B, Hq, n_q), torch.float32, stream) if lse is None else lse
+    _bf16(o, "o", q.shape)
+    _tensor(lse, "lse", torch.float32, (B, Hq, n_q))
+    return (B, Hq, Hkv, n_q), N, D, o, lse
+
+
+def fa_window_decode_workspace_bytes(B: int, Hq: int, Hkv: int, n_q: int, N: int, D: int, window: int,
+                                     sinks: int) -> int:
+    """Workspace bytes fa_window_decode needs (may be 0)."""
+    return _size_query("fa_window_decode_workspace_bytes", B, Hq, Hkv, n_q, N, D, _c_int(window),
+                       _c_int(sinks))
+
+
+def fa_window_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, sinks: int = 0,
+                     lens: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                     o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """The n_q <= 16 newest rows q [B, Hq, n_q, D] of each sequence against its cache k, v [B, Hkv, N, D], windowed
+    (fa_window_decode).  lens: int32 CUDA tensor [B], the keys each sequence holds (default N).  Returns (o, lse)."""
+    heads, N, D, o, lse = _rows_and_cache(q, k, v, lens, o, lse, stream)
+    need = fa_window_decode_workspace_bytes(*heads, N, D, _c_int(window), _c_int(sinks))
+    workspace, nbytes = _workspace(workspace, need, stream)
+    rc = _native.load().fa_window_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(lens), _ptr(o), _ptr(lse), *heads, N, D,
+                                         _c_int(window), _c_int(sinks), _scale(scale, D), _ptr(workspace), nbytes,
+                                         _stream_ptr(stream))
+    _native.check(rc, "fa_window_decode")
+    return o, lse
+
+
+def fa_prefix_decode_workspace_bytes(B: int, Hq: int, Hkv: int, n_q: int, P: int, N: int, D: int) -> int:
+    """Workspace bytes fa_prefix_decode needs."""
+    return _size_query("fa_prefix_decode_workspace_bytes", B, Hq, Hkv, n_q, P, N, D)
+
+
+def fa_prefix_decode(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     lens: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                     o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """The n_q <= 16 newest rows q [B, Hq, n_q, D] of each sequence against the prefix k_prefix, v_prefix [Hkv, P, D]
+    that all sequences share, and against the sequence's own cache k, v [B, Hkv, N, D] behind it, of which lens[b]
+    keys are held (int32 CUDA tensor; default N) (fa_prefix_decode).  Returns (o, lse)."""
+    heads, N, D, o, lse = _rows_and_cache(q, k, v, lens, o, lse, stream)
+    if k_prefix.dim() != 3:
+        raise ValueError(f"k_prefix must be [Hkv, P, D], got {list(k_prefix.shape)}")
+    P = k_prefix.shape[1]
+    _bf16(k_prefix, "k_prefix", (heads[2], P, D))
+    _bf16(v_prefix, "v_prefix", (heads[2], P, D))
+    workspace, nbytes = _workspace(workspace, fa_prefix_decode_workspace_bytes(*heads, P, N, D), stream)
+    rc = _native.load().fa_prefix_decode(_ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(k), _ptr(v), _ptr(lens), _ptr(o),
+                                         _ptr(lse), *heads, P, N, D, _scale(scale, D), _ptr(workspace), nbytes,
+                                         _stream_ptr(stream))
+    _native.check(rc, "fa_prefix_decode")
+    return o, lse
+
+
 def fa_device_status(stream: Optional[torch.cuda.Stream] = None) -> int:
     """Synchronise the stream and return (and clear) the device status word."""
     return _native.load().fa_device_status(_stream_ptr(stream))
@@ -216,4 +414,4 @@ def attention_flops(B: int, H: int, N: int, D: int, causal: bool, pass_: str = "
     return f / 2 if causal else f
 
 
-from .autograd import attention  # noqa: E402  (differentiable wrapper over the functions above)
+from .autograd import attention, window_attention  # noqa: E402  (differentiable wrapper over the functions above)

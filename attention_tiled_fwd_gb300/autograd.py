@@ -6,7 +6,8 @@ records what the split backward needs: its ``backward`` runs fa_backward_dq
 current stream -- the training-step integration that the MLX port of
 "Learning Metal with FlashAttention" lacks (its custom kernel has no
 backward).  Inputs are ``[B, H, N, D]`` bf16 CUDA tensors, D any multiple of
-8 up to 256; gradients come back in the inputs' dtype.  Nothing here computes attention:
+8 up to 256; gradients come back in the inputs' dtype.  ``window_attention`` is
+the same for windowed attention with grouped heads.  Nothing here computes attention:
 every step runs in the library's kernels.
 """
 from __future__ import annotations
@@ -15,7 +16,8 @@ from typing import Optional
 
 import torch
 
-from . import fa_backward_dkdv, fa_backward_dq, fa_forward
+from . import (fa_backward_dkdv, fa_backward_dq, fa_forward, fa_window_backward_dkdv, fa_window_backward_dq,
+               fa_window_forward)
 
 
 class _Attention(torch.autograd.Function):
@@ -41,3 +43,31 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
               scale: Optional[float] = None) -> torch.Tensor:
     """O = softmax(scale Q K^T) V (scale defaults to 1/sqrt(D)), differentiable in q, k and v."""
     return _Attention.apply(q, k, v, bool(causal), scale)
+
+
+class _WindowAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, window: int, sinks: int, scale: Optional[float]):
+        q, k, v = (t.contiguous() for t in (q, k, v))
+        o, lse = fa_window_forward(q, k, v, window, sinks, scale=scale)
+        ctx.save_for_backward(q, k, v, o, lse)
+        ctx.mask, ctx.scale = (window, sinks), scale
+        return o
+
+    @staticmethod
+    def backward(ctx, dO):
+        q, k, v, o, lse = ctx.saved_tensors
+        dO = dO.to(q.dtype).contiguous()
+        dq, delta = fa_window_backward_dq(q, k, v, o, dO, lse, *ctx.mask, scale=ctx.scale, grad_dtype=q.dtype)
+        dk = dv = None
+        if ctx.needs_input_grad[1] or ctx.needs_input_grad[2]:
+            dk, dv = fa_window_backward_dkdv(q, k, v, dO, lse, delta, *ctx.mask, scale=ctx.scale, grad_dtype=q.dtype)
+        return dq, dk, dv, None, None, None
+
+
+def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, sinks: int = 0,
+                     scale: Optional[float] = None) -> torch.Tensor:
+    """Windowed attention, differentiable in q, k and v: q [B, Hq, Nq, D] are the last Nq positions of k, v
+    [B, Hkv, Nk, D] (bf16 CUDA tensors, Hq a multiple of Hkv); a row at position p sees key j iff j <= p and
+    (j < sinks or j > p - window)."""
+    return _WindowAttention.apply(q, k, v, int(window), int(sinks), scale)

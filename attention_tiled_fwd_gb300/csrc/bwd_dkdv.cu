@@ -56,6 +56,7 @@
 // measured 15 % slower.)
 #include "fa_internal.h"
 #include "sm100_ptx.cuh"
+#include "win.cuh"
 #include <cmath>
 
 namespace fa {
@@ -91,7 +92,9 @@ struct DkdvSmem {
 // kStatSlots: query tiles whose L / D are staged ahead.
 // VK: the two CTAs of a key tile split the gradients rather than their columns (grid y = 0 keeps all of
 // dV, y = 1 all of dK); the dV CTA computes no dP^T, and neither repeats the other's product.
-template <int D, int DO, int NB, int NSLOT, int kStatSlots, bool VK>
+// WIN: windowed attention (win.cuh): a key tile meets the rows of every query head of its group whose window (or
+// the sinks) holds one of its keys; those tiles start at the first such row.
+template <int D, int DO, int NB, int NSLOT, int kStatSlots, bool VK, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
@@ -140,12 +143,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int epi_abort;  // a compute warp's wait ran out: the epilogue stores nothing
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int rank, bh;
-    tile_order((a.N + kBN - 1) / kBN, a.B * a.H, a.causal, a.head_group, &rank, &bh);
+    tile_order(((WIN ? a.win.Nk : a.N) + kBN - 1) / kBN, a.B * (WIN ? a.win.Hkv : a.H), a.causal, a.head_group, &rank,
+               &bh);
     const int k_tile = rank;  // causal: key tile 0 has the most query tiles
     const int N = a.N;
     const int n_q_total = (N + kBQ - 1) / kBQ;
     const int q_begin = a.causal ? (k_tile * kBN) / kBQ : 0;
-    const int n_q = n_q_total - q_begin;  // >= 1
+    const WinRows rows = WIN ? win_rows(a, k_tile * kBN, kBN, kBQ) : WinRows{0, 0, 0};
+    const int n_q = WIN ? rows.n : n_q_total - q_begin;  // >= 1 (WIN: or 0, and then the gradients are 0)
     const int do0 = VK ? 0 : blockIdx.y * DO;  // first dV / dK column of this CTA
     const bool role_dv = VK && blockIdx.y == 0;  // VK: this CTA keeps dV only
     const bool role_dk = VK && blockIdx.y == 1;  // VK: this CTA keeps dK only
@@ -200,8 +205,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_3d(v_s + p * (kBN * 128), &tmap_v, kv_full, p * 64, k_tile * kBN, bh);
             }
         }
-        const float *lse_g = a.lse + (size_t)bh * N;
-        const float *del_g = a.delta + (size_t)bh * N;
+        const float *lse_g = a.lse + (WIN ? 0 : (size_t)bh * N);
+        const float *del_g = a.delta + (WIN ? 0 : (size_t)bh * N);
         int last_round[NSLOT];
 #pragma unroll
         for (int s = 0; s < NSLOT; ++s) last_round[s] = -1;
@@ -216,7 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int p = 0; p < kPanels; ++p)
                     tma_load_3d(dst + p * (kBQ * 128), map, &slot_full[slot], p * 64,
-                                (q_begin + (idx >> 1)) * kBQ, bh);
+                                WIN ? rows.row0(idx >> 1, kBQ) : (q_begin + (idx >> 1)) * kBQ,
+                                WIN ? win_query_slice(a, bh, rows, idx >> 1) : bh);
             }
 #pragma unroll
             for (int s = 0; s < NSLOT; ++s)
@@ -227,7 +233,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = warp_wait(&stat_empty[ss], (sr & 1) ^ 1, a.status, kSiteStats))) break;
             // lane l copies words l, l + 32, ... of the slot's [L_i | D_i]: each copy instruction writes 32
             // consecutive words of shared memory (one bank each) from 32 consecutive floats
-            const int q0 = (q_begin + i) * kBQ;
+            const int q0 = WIN ? rows.row0(i, kBQ) : (q_begin + i) * kBQ;
+            const size_t slice = WIN ? (size_t)win_query_slice(a, bh, rows, i) * N : 0;
             float *dst = stat_s + ss * 2 * kBQ;
 #pragma unroll
             for (int e = 0; e < 2 * kBQ / 32; ++e) {
@@ -236,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int q = q0 + (is_l ? w : w - kBQ);
                 const bool valid = q < N;
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst + w)),
-                             "l"((is_l ? lse_g : del_g) + (valid ? q : 0)), "r"(valid ? 4 : 0)
+                             "l"((is_l ? lse_g : del_g) + slice + (valid ? q : 0)), "r"(valid ? 4 : 0)
                              : "memory");
             }
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&stat_full[ss]))
@@ -373,9 +380,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             const float4 *ls4 = reinterpret_cast<const float4 *>(stat_s + ss * 2 * kBQ + g * kHalf);
             const float4 *ds4 = reinterpret_cast<const float4 *>(stat_s + ss * 2 * kBQ + kBQ + g * kHalf);
-            const int q0 = qt * kBQ + g * kHalf;  // first query of this thread's half
+            const int q0 = (WIN ? rows.row0(i, kBQ) : qt * kBQ) + g * kHalf;  // first query of this thread's range
             // visible iff key <= query (causal), query < N and key < N
-            const bool need_mask = (q0 + kHalf > N) || (a.causal && key > q0) || (key >= N);
+            const bool need_mask = WIN ? q0 + kHalf > N || !sees_all(a, key, q0, kHalf)
+                                       : (q0 + kHalf > N) || (a.causal && key > q0) || (key >= N);
+            const uint32_t seen = WIN ? seen_by(a, key, q0) : 0u;
             const bool any_mask = __any_sync(0xffffffffu, need_mask);
 
             ok = mbar_wait(&s_full[b], (i / NB) & 1, a.status, kSiteSFull);
@@ -407,7 +416,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int t = 0; t < 4; ++t) {
                             const int qq = q0 + 4 * q4 + t;
-                            if (qq >= N || key >= N || (a.causal && qq < key)) p[t] = 0.f;
+                            if (WIN ? !(seen & (1u << (4 * q4 + t)))
+                                    : qq >= N || key >= N || (a.causal && qq < key))
+                                p[t] = 0.f;
                         }
                     }
                     p2[2 * q4] = f2_pack(p[0], p[1]);
@@ -454,6 +465,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok) {
             ok = mbar_wait(final_bar, 0, a.status, kSiteDone);
+            // no product has waited for K and V when no row meets them: their loads must still have landed
+            // before the epilogue stages into their memory
+            if (WIN && ok && n_q == 0) ok = mbar_wait(kv_full, 0, a.status, kSiteKV);
             ok = __all_sync(0xffffffffu, ok);
         }
         // Epilogue: dV and dK (dK times the scale its dS^T operands left out) are staged in the K / V tiles'
@@ -480,7 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(tmem + lane_base + col + ch * 32, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int t = 0; t < 32; ++t) v[t] = __float_as_uint(__uint_as_float(v[t]) * osc);
+                for (int t = 0; t < 32; ++t)
+                    v[t] = WIN && n_q == 0 ? 0u : __float_as_uint(__uint_as_float(v[t]) * osc);
                 const int oc = c0 + ch * 32;  // column within this CTA's DO columns
                 if (a.grad_bf16) {
                     uint8_t *prow = stage + (oc / 64) * (kBN * 128);
@@ -525,29 +540,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, int DO, int NB, int NSLOT, int STATS, bool VK = false>
+template <int D, int DO, int NB, int NSLOT, int STATS, bool WIN, bool VK = false>
 cudaError_t launch_spec(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                         const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv, cudaStream_t s) {
     using L = DkdvSmem<D, NSLOT, STATS>;
     static_assert(L::kAlloc <= 232448, "shared memory budget");
-    auto kern = bwd_dkdv_kernel<D, DO, NB, NSLOT, STATS, VK>;
+    auto kern = bwd_dkdv_kernel<D, DO, NB, NSLOT, STATS, VK, WIN>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
-    dim3 grid(((a.N + kBN - 1) / kBN) * a.H * a.B, VK ? 2 : D / DO);
+    dim3 grid(WIN ? ((a.win.Nk + kBN - 1) / kBN) * a.win.Hkv * a.B : ((a.N + kBN - 1) / kBN) * a.H * a.B,
+              VK ? 2 : D / DO);
     kern<<<grid, kThreads, L::kAlloc, s>>>(tq, tk, tv, tdo, tdk, tdv, a);
     return cudaGetLastError();
+}
+
+template <bool WIN>
+cudaError_t launch_width(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                         const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv, cudaStream_t s) {
+    switch (kernel_head_dim(a.D)) {
+        case 128: return launch_spec<128, 128, 2, 8, 4, WIN>(a, tq, tk, tv, tdo, tdk, tdv, s);
+        case 192: return launch_spec<192, 192, 1, 5, 4, WIN>(a, tq, tk, tv, tdo, tdk, tdv, s);
+        case 256: return launch_spec<256, 256, 2, 3, 3, WIN, true>(a, tq, tk, tv, tdo, tdk, tdv, s);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_bwd_dkdv(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                            const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv, cudaStream_t s) {
-    switch (kernel_head_dim(a.D)) {
-        case 128: return launch_spec<128, 128, 2, 8, 4>(a, tq, tk, tv, tdo, tdk, tdv, s);
-        case 192: return launch_spec<192, 192, 1, 5, 4>(a, tq, tk, tv, tdo, tdk, tdv, s);
-        case 256: return launch_spec<256, 256, 2, 3, 3, true>(a, tq, tk, tv, tdo, tdk, tdv, s);
-        default: return cudaErrorInvalidValue;
-    }
+                            const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv, cudaStream_t s,
+                            bool win) {
+    return win ? launch_width<true>(a, tq, tk, tv, tdo, tdk, tdv, s)
+               : launch_width<false>(a, tq, tk, tv, tdo, tdk, tdv, s);
 }
 
 }  // namespace fa

@@ -27,6 +27,7 @@
 // thread owning one key row (its TMEM lane).
 #include "fa_internal.h"
 #include "sm100_ptx.cuh"
+#include "win.cuh"
 #include <cmath>
 
 namespace fa {
@@ -61,6 +62,9 @@ struct Q128Smem {
     static constexpr int kAlloc = kTmemHolderOff + 16 + 1024;
 };
 
+// WIN: windowed attention (win.cuh): a key tile meets the rows of every query head of its group whose window (or
+// the sinks) holds one of its keys; those tiles start at the first such row.
+template <bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dkdv_q128_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                          const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
@@ -99,12 +103,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int epi_abort;  // a compute warp's wait ran out: the epilogue stores nothing
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int rank, bh;
-    tile_order((a.N + kBN - 1) / kBN, a.B * a.H, a.causal, a.head_group, &rank, &bh);
+    tile_order(((WIN ? a.win.Nk : a.N) + kBN - 1) / kBN, a.B * (WIN ? a.win.Hkv : a.H), a.causal, a.head_group, &rank,
+               &bh);
     const int k_tile = rank;  // causal: key tile 0 has the most query tiles
     const int N = a.N;
     const int n_q_total = (N + kBQ - 1) / kBQ;
     const int q_begin = a.causal ? k_tile : 0;  // kBQ == kBN
-    const int n_q = n_q_total - q_begin;       // >= 1
+    const WinRows rows = WIN ? win_rows(a, k_tile * kBN, kBN, kBQ) : WinRows{0, 0, 0};
+    const int n_q = WIN ? rows.n : n_q_total - q_begin;  // >= 1 (WIN: or 0, and then the gradients are 0)
 
     if (threadIdx.x == 0) {
         epi_abort = 0;
@@ -150,8 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(k_s, &tmap_k, kv_full, 0, k_tile * kBN, bh);
             tma_load_3d(v_s, &tmap_v, kv_full, 0, k_tile * kBN, bh);
         }
-        const float *lse_g = a.lse + (size_t)bh * N;
-        const float *del_g = a.delta + (size_t)bh * N;
+        const float *lse_g = a.lse + (WIN ? 0 : (size_t)bh * N);
+        const float *del_g = a.delta + (WIN ? 0 : (size_t)bh * N);
         int last_round[kNSlot];
 #pragma unroll
         for (int s = 0; s < kNSlot; ++s) last_round[s] = -1;
@@ -162,7 +168,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 const CUtensorMap *map = (idx & 1) ? &tmap_do : &tmap_q;
                 mbar_arrive_expect_tx(&slot_full[slot], L::kTileBytes);
-                tma_load_3d(slots + slot * L::kTileBytes, map, &slot_full[slot], 0, (q_begin + (idx >> 1)) * kBQ, bh);
+                tma_load_3d(slots + slot * L::kTileBytes, map, &slot_full[slot], 0,
+                            WIN ? rows.row0(idx >> 1, kBQ) : (q_begin + (idx >> 1)) * kBQ,
+                            WIN ? win_query_slice(a, bh, rows, idx >> 1) : bh);
             }
 #pragma unroll
             for (int s = 0; s < kNSlot; ++s)
@@ -173,7 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = warp_wait(&stat_empty[ss], (sr & 1) ^ 1, a.status, kSiteStats))) break;
             // lane l copies words l, l + 32, ... of the slot's [L_i | D_i]: each copy instruction writes 32
             // consecutive words of shared memory (one bank each) from 32 consecutive floats
-            const int q0 = (q_begin + i) * kBQ;
+            const int q0 = WIN ? rows.row0(i, kBQ) : (q_begin + i) * kBQ;
+            const size_t slice = WIN ? (size_t)win_query_slice(a, bh, rows, i) * N : 0;
             float *dst = stat_s + ss * 2 * kBQ;
 #pragma unroll
             for (int e = 0; e < 2 * kBQ / 32; ++e) {
@@ -182,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int q = q0 + (is_l ? w : w - kBQ);
                 const bool valid = q < N;
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst + w)),
-                             "l"((is_l ? lse_g : del_g) + (valid ? q : 0)), "r"(valid ? 4 : 0)
+                             "l"((is_l ? lse_g : del_g) + slice + (valid ? q : 0)), "r"(valid ? 4 : 0)
                              : "memory");
             }
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&stat_full[ss]))
@@ -300,9 +309,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             const float4 *ls4 = reinterpret_cast<const float4 *>(stat_s + ss * 2 * kBQ + g * kSpan);
             const float4 *ds4 = reinterpret_cast<const float4 *>(stat_s + ss * 2 * kBQ + kBQ + g * kSpan);
-            const int q0 = qt * kBQ + g * kSpan;  // first query of this thread's range
+            const int q0 = (WIN ? rows.row0(i, kBQ) : qt * kBQ) + g * kSpan;  // first query of this thread's range
             // visible iff key <= query (causal), query < N and key < N
-            const bool need_mask = (q0 + kSpan > N) || (a.causal && key > q0) || (key >= N);
+            const bool need_mask = WIN ? q0 + kSpan > N || !sees_all(a, key, q0, kSpan)
+                                       : (q0 + kSpan > N) || (a.causal && key > q0) || (key >= N);
+            const uint32_t seen = WIN ? seen_by(a, key, q0) : 0u;
             const bool any_mask = __any_sync(0xffffffffu, need_mask);
 
             ok = mbar_wait(&s_full[b], (i >> 1) & 1, a.status, kSiteSFull);
@@ -330,7 +341,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int t = 0; t < 4; ++t) {
                             const int qq = q0 + 4 * q4 + t;
-                            if (qq >= N || key >= N || (a.causal && qq < key)) p[t] = 0.f;
+                            if (WIN ? !(seen & (1u << (4 * q4 + t)))
+                                    : qq >= N || key >= N || (a.causal && qq < key))
+                                p[t] = 0.f;
                         }
                     }
                     pk[2 * q4] = pack_bf16x2(p[0], p[1]);
@@ -377,6 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok) {
             ok = mbar_wait(final_bar, 0, a.status, kSiteDone);
+            // no product has waited for K and V when no row meets them: their loads must still have landed
+            // before the epilogue stages into their memory
+            if (WIN && ok && n_q == 0) ok = mbar_wait(kv_full, 0, a.status, kSiteKV);
             ok = __all_sync(0xffffffffu, ok);
         }
         // Epilogue: dV and dK (dK times the scale its dS^T operands left out) are staged in the K / V tiles'
@@ -395,7 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(tmem + lane_base + (is_dv ? kColDV : kColDK) + c0, v);
             tmem_wait_ld();
 #pragma unroll
-            for (int t = 0; t < 32; ++t) v[t] = __float_as_uint(__uint_as_float(v[t]) * osc);
+            for (int t = 0; t < 32; ++t)
+                v[t] = WIN && n_q == 0 ? 0u : __float_as_uint(__uint_as_float(v[t]) * osc);
             uint8_t *stage = smem + (is_dv ? 0 : n_panels) * (kBN * 128) + r * 128;
             const int sw = r & 7;
             if (a.grad_bf16) {
@@ -441,14 +458,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 cudaError_t launch_bwd_dkdv_q128(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk,
                                  const CUtensorMap &tv, const CUtensorMap &tdo, const CUtensorMap &tdk,
-                                 const CUtensorMap &tdv, cudaStream_t s) {
+                                 const CUtensorMap &tdv, cudaStream_t s, bool win) {
     using L = Q128Smem;
     static_assert(L::kAlloc <= 232448, "shared memory budget");
     if (kernel_head_dim(a.D) != kD) return cudaErrorInvalidValue;
-    auto kern = bwd_dkdv_q128_kernel;
+    auto kern = win ? bwd_dkdv_q128_kernel<true> : bwd_dkdv_q128_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
-    dim3 grid(((a.N + kBN - 1) / kBN) * a.H * a.B);
+    dim3 grid(win ? ((a.win.Nk + kBN - 1) / kBN) * a.win.Hkv * a.B : ((a.N + kBN - 1) / kBN) * a.H * a.B);
     kern<<<grid, kThreads, L::kAlloc, s>>>(tq, tk, tv, tdo, tdk, tdv, a);
     return cudaGetLastError();
 }

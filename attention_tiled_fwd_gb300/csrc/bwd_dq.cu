@@ -54,6 +54,7 @@
 // slower: the tensor core did 5/3 of the useful products.)
 #include "fa_internal.h"
 #include "sm100_ptx.cuh"
+#include "win.cuh"
 #include <cmath>
 
 namespace fa {
@@ -91,8 +92,9 @@ struct DqSmem {
 
 // D: the contraction width the kernel is built for (64-column panels); DQ: the columns of dQ one
 // CTA accumulates (D here; D / DQ CTAs per query tile, grid y choosing the columns); QT: Q kept in
-// TMEM as the A operand of S (else S reads Q from shared memory).
-template <int D, int DQ, bool QT, int NSLOT>
+// TMEM as the A operand of S (else S reads Q from shared memory); WIN: windowed attention (win.cuh): the key
+// tiles are those of key_span, a query head reads its group's key head, and the mask is the window's.
+template <int D, int DQ, bool QT, int NSLOT, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
@@ -143,7 +145,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q_tile = (a.N + kBM - 1) / kBM - 1 - rank;  // causal: the last query tile has the most keys
     const int N = a.N;
     const int kv_end = a.causal ? min(N, (q_tile + 1) * kBM) : N;
-    const int n_kv = (kv_end + kBN - 1) / kBN;  // >= 1
+    // WIN: position of the tile's first row, its key tiles, its key slice
+    const int pos0 = WIN ? a.win.Nk - N + q_tile * kBM : 0;
+    const KeySpan span = WIN ? key_span(pos0, min(a.win.Nk, pos0 + kBM) - 1, a.win.window, a.win.sinks, kBN)
+                             : KeySpan{0, 0, 0};
+    const int kv_bh = WIN ? bh / a.H * a.win.Hkv + bh % a.H / (a.H / a.win.Hkv) : bh;
+    const int n_kv = WIN ? span.n : (kv_end + kBN - 1) / kBN;  // >= 1
     const int dq0 = blockIdx.y * DQ;            // first dQ column of this CTA
     const int Dr = a.D;                         // row stride and real columns (<= D; the rest are zeros)
 
@@ -207,7 +214,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive_expect_tx(&slot_full[slot], L::kTileBytes);
 #pragma unroll
                 for (int p = 0; p < kPanels; ++p)
-                    tma_load_3d(dst + p * (kBN * 128), map, &slot_full[slot], p * 64, (idx >> 1) * kBN, bh);
+                    tma_load_3d(dst + p * (kBN * 128), map, &slot_full[slot], p * 64,
+                                WIN ? span.key0(idx >> 1, kBN) : (idx >> 1) * kBN, kv_bh);
 #pragma unroll
                 for (int s = 0; s < NSLOT; ++s)
                     if (s == slot) last_round[s] = round;
@@ -418,8 +426,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = mbar_wait(&s_full[sb], sph, a.status, kSiteSFull);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             tc_fence_after();
-            const int key0 = j * kBN + g * kHalf;
-            const bool need_mask = (key0 + kHalf > N) || (a.causal && key0 + kHalf - 1 > q_tile * kBM);
+            const int key0 = (WIN ? span.key0(j, kBN) : j * kBN) + g * kHalf;
+            const int window = WIN ? span.window_in(j, a.win.window) : 0;
+            const bool need_mask =
+                WIN ? !all_seen(pos0, pos0 + kBM - 1, key0, key0 + kHalf - 1, window, a.win.sinks)
+                    : (key0 + kHalf > N) || (a.causal && key0 + kHalf - 1 > q_tile * kBM);
+            static_assert(!WIN || kHalf == 32, "one mask word per thread and tile");
+            const uint32_t seen = WIN && need_mask ? seen_keys(pos0 + r, key0, window, a.win.sinks) : 0u;
             // dS[j % 2] was last read by dQ_{j-2}
             if (j >= 2) {
                 ok = mbar_wait(&dq_done[b], ((j - 2) >> 1) & 1, a.status, kSiteDqDone);
@@ -440,8 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p0 = ex2_approx(p0);
                     p1 = ex2_approx(p1);
                     if (need_mask) {
-                        if (key0 + i > lim) p0 = 0.f;
-                        if (key0 + i + 1 > lim) p1 = 0.f;
+                        if (WIN ? !(seen & (1u << i)) : key0 + i > lim) p0 = 0.f;
+                        if (WIN ? !(seen & (2u << i)) : key0 + i + 1 > lim) p1 = 0.f;
                     }
                     dsk[i / 2] = f2_to_bf16x2(
                         f2_mul(f2_sub(f2_pack(__uint_as_float(praw[i]), __uint_as_float(praw[i + 1])), d2), f2_pack(p0, p1)));
@@ -464,8 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p0 = ex2_approx(p0);
                     p1 = ex2_approx(p1);
                     if (need_mask) {
-                        if (key0 + i > lim) p0 = 0.f;
-                        if (key0 + i + 1 > lim) p1 = 0.f;
+                        if (WIN ? !(seen & (1u << i)) : key0 + i > lim) p0 = 0.f;
+                        if (WIN ? !(seen & (2u << i)) : key0 + i + 1 > lim) p1 = 0.f;
                     }
                     p2[i / 2] = f2_pack(p0, p1);
                 }
@@ -555,12 +568,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, int DQ, bool QT, int NSLOT>
+template <int D, int DQ, bool QT, int NSLOT, bool WIN>
 cudaError_t launch_spec(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                         const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, cudaStream_t s) {
     using L = DqSmem<D, NSLOT>;
     static_assert(L::kAlloc <= 232448, "shared memory budget");
-    auto kern = bwd_dq_kernel<D, DQ, QT, NSLOT>;
+    auto kern = bwd_dq_kernel<D, DQ, QT, NSLOT, WIN>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
     dim3 grid(((a.N + kBM - 1) / kBM) * a.H * a.B, D / DQ);
@@ -568,16 +581,23 @@ cudaError_t launch_spec(const BwdArgs &a, const CUtensorMap &tq, const CUtensorM
     return cudaGetLastError();
 }
 
+template <bool WIN>
+cudaError_t launch_width(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                         const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, cudaStream_t s) {
+    switch (kernel_head_dim(a.D)) {
+        case 128: return launch_spec<128, 128, true, 8, WIN>(a, tq, tk, tv, tdo, to, tdq, s);
+        case 192: return launch_spec<192, 192, false, 4, WIN>(a, tq, tk, tv, tdo, to, tdq, s);  // 3, 5 slots slower
+        case 256: return launch_spec<256, 256, false, 3, WIN>(a, tq, tk, tv, tdo, to, tdq, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_bwd_dq(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                          const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, cudaStream_t s) {
-    switch (kernel_head_dim(a.D)) {
-        case 128: return launch_spec<128, 128, true, 8>(a, tq, tk, tv, tdo, to, tdq, s);
-        case 192: return launch_spec<192, 192, false, 4>(a, tq, tk, tv, tdo, to, tdq, s);  // 3, 5 slots slower
-        case 256: return launch_spec<256, 256, false, 3>(a, tq, tk, tv, tdo, to, tdq, s);
-        default: return cudaErrorInvalidValue;
-    }
+                          const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, cudaStream_t s,
+                          bool win) {
+    return win ? launch_width<true>(a, tq, tk, tv, tdo, to, tdq, s) : launch_width<false>(a, tq, tk, tv, tdo, to, tdq, s);
 }
 
 }  // namespace fa

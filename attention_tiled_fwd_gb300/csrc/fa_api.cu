@@ -9,6 +9,7 @@
 #include "../../include/fa.h"
 #include "fa_internal.h"
 #include "sm100_ptx.cuh"
+#include "win_decode.cuh"
 
 #include <algorithm>
 #include <atomic>
@@ -137,16 +138,22 @@ int encode_3d(CUtensorMap *map, const void *base, int BH, int N, int D, int box_
     return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
-// [B*H, N, D] bf16 tensor, box {64, rows, 1}, 128-byte swizzle, zero fill out of bounds.
-int encode_bf16_3d(CUtensorMap *map, const void *base, int BH, int N, int D, int box_rows) {
-    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)BH};
-    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)N * D * 2};
+// [slices, rows, D] bf16 tensor whose slices lie slice_rows rows apart, box {64, box_rows, 1}, 128-byte swizzle,
+// zero fill out of bounds.
+int encode_rows(CUtensorMap *map, const void *base, int slices, int rows, int slice_rows, int D, int box_rows) {
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)slices};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)slice_rows * D * 2};
     cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
                           estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
+// [B*H, N, D] bf16 tensor, box {64, rows, 1}, 128-byte swizzle, zero fill out of bounds.
+int encode_bf16_3d(CUtensorMap *map, const void *base, int BH, int N, int D, int box_rows) {
+    return encode_rows(map, base, BH, N, N, D, box_rows);
 }
 
 float log2e() { return 1.4426950408889634f; }
@@ -390,11 +397,341 @@ extern "C" int fa_decode_noalloc(const void *q, const void *k, const void *v, vo
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+// ---------------------------------------------------------------- windowed and shared-prefix attention
+namespace {
+// Sizes and mask of windowed attention: 1 <= Nq <= Nk, Hq a multiple of Hkv.
+int check_window(int B, int Hq, int Hkv, int Nq, int Nk, int kv_rows, int D, int window, int sinks, float scale) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Nk < 1 || D < 1) return FA_ERR_SHAPE;
+    if (B > 65535 || Hq > 65535 || Hq % Hkv != 0) return FA_ERR_SHAPE;
+    if (Nq > Nk || kv_rows < Nk || Nk > kMaxPositions) return FA_ERR_SHAPE;
+    if (window < 1 || sinks < 0) return FA_ERR_SHAPE;
+    const long long max = (1ll << 31) - 1;
+    if ((long long)B * Hq * Nq > max || (long long)B * Hkv * kv_rows > max) return FA_ERR_SHAPE;
+    if (!std::isfinite(scale) || scale <= 0.f) return FA_ERR_SCALE;  // the masks are -inf in units of the scale
+    if (!bf16_head_dim_ok(D)) return FA_ERR_HEAD_DIM;
+    return FA_OK;
+}
+
+WinArgs window_args(int Hkv, int Nk, int window, int sinks) {
+    WinArgs w{Hkv, Nk, std::min(window, Nk), std::min(sinks, Nk)};
+    if (w.window == Nk) w.sinks = 0;  // every earlier key is in the window
+    return w;
+}
+
+// How the forward's blocks pair their query tiles: one tile each while every tile can have an SM of its own;
+// else two heads of a group (they read the same keys), or neighbouring rows where a group's heads do not pair.
+int window_pairing(int B, int Hq, int Hkv, int Nq, int num_sms) {
+    if ((long long)B * Hq * ((Nq + 127) / 128) <= num_sms) return kOneTile;
+    return (Hq / Hkv) % 2 == 0 ? kTwoHeads : kTwoRowTiles;
+}
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// lens: null, or 4-byte aligned device memory.
+int check_lens(const int *lens) {
+    if (!lens) return FA_OK;
+    if (!aligned4(lens)) return FA_ERR_ALIGN;
+    return check_device_ptr(lens);
+}
+
+// Partials of `rows` rows: O [rows][slots][D], then (m, l) [rows][slots].
+size_t partials_bytes(size_t rows, int slots, int D) { return rows * slots * ((size_t)D * 4 + 8); }
+}  // namespace
+
+extern "C" int fa_window_forward(const void *q, const void *k, const void *v, void *o, float *lse, int B, int Hq, int Hkv,
+                                 int Nq, int Nk, int kv_rows, int D, int window, int sinks, float scale, int dtype,
+                                 void *stream) {
+    if (dtype != FA_BF16) return FA_ERR_DTYPE;
+    int rc = check_window(B, Hq, Hkv, Nq, Nk, kv_rows, D, window, sinks, scale);
+    if (rc != FA_OK) return rc;
+    rc = check_ptrs({q, k, v, o, lse});
+    if (rc != FA_OK) return rc;
+    int dev;
+    DeviceState *st;
+    rc = device_state(&dev, &st);
+    if (rc != FA_OK) return rc;
+    const WinArgs w = window_args(Hkv, Nk, window, sinks);
+    SpanArgs a{};
+    a.o = o;
+    a.lse = lse;
+    a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.Nq = Nq, a.Nk = Nk, a.D = D;
+    a.window = w.window, a.sinks = w.sinks;
+    a.scale_log2 = scale * log2e();
+    a.status = st->status_word;
+    a.num_sms = st->num_sms;
+    a.pairing = window_pairing(B, Hq, Hkv, Nq, st->num_sms);
+    // sink tiles read through maps that end at the last sink
+    const int bn = fwd_block_n(kernel_head_dim(D)), sink_rows = w.sinks > 0 ? w.sinks : Nk;
+    CUtensorMap tq, tk, tv, tks, tvs, to;
+    if (encode_rows(&tq, q, B * Hq, Nq, Nq, D, 128) != FA_OK ||
+        encode_rows(&tk, k, B * Hkv, Nk, kv_rows, D, bn) != FA_OK ||
+        encode_rows(&tv, v, B * Hkv, Nk, kv_rows, D, bn) != FA_OK ||
+        encode_rows(&tks, k, B * Hkv, sink_rows, kv_rows, D, bn) != FA_OK ||
+        encode_rows(&tvs, v, B * Hkv, sink_rows, kv_rows, D, bn) != FA_OK ||
+        encode_rows(&to, o, B * Hq, Nq, Nq, D, 128) != FA_OK)
+        return FA_ERR_CUDA;
+    cudaError_t e = launch_win_fwd(a, tq, tk, tv, tks, tvs, to, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+extern "C" int fa_window_backward_dq(const void *q, const void *k, const void *v, const void *o, const void *dO,
+                                     const float *lse, float *delta, void *dq, int B, int Hq, int Hkv, int Nq, int Nk,
+                                     int D, int window, int sinks, float scale, int dtype, int grad_dtype,
+                                     void *stream) {
+    if (dtype != FA_BF16 || (grad_dtype != FA_BF16 && grad_dtype != FA_F32)) return FA_ERR_DTYPE;
+    int rc = check_window(B, Hq, Hkv, Nq, Nk, Nk, D, window, sinks, scale);
+    if (rc != FA_OK) return rc;
+    rc = check_ptrs({q, k, v, o, dO, lse, delta, dq});
+    if (rc != FA_OK) return rc;
+    int dev;
+    DeviceState *st;
+    rc = device_state(&dev, &st);
+    if (rc != FA_OK) return rc;
+    BwdArgs a{q, k, v, o, dO, lse, delta, dq, nullptr, nullptr, B, Hq, Nq, D, scale, scale * log2e(), 1,
+              grad_dtype == FA_BF16 ? 1 : 0, st->status_word, B * Hq, window_args(Hkv, Nk, window, sinks)};
+    CUtensorMap tq, tk, tv, tdo, to, tdq;
+    const int Dk = kernel_head_dim(D);
+    const int kv_box = Dk == 64 ? 128 : kDqKRows;
+    if (encode_rows(&tq, q, B * Hq, Nq, Nq, D, 128) != FA_OK ||
+        encode_rows(&tk, k, B * Hkv, Nk, Nk, D, kv_box) != FA_OK ||
+        encode_rows(&tv, v, B * Hkv, Nk, Nk, D, kv_box) != FA_OK ||
+        encode_rows(&tdo, dO, B * Hq, Nq, Nq, D, 128) != FA_OK || encode_rows(&to, o, B * Hq, Nq, Nq, D, 128) != FA_OK ||
+        encode_3d(&tdq, dq, B * Hq, Nq, D, 128, grad_dtype == FA_F32) != FA_OK)
+        return FA_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = Dk == 64 ? launch_bwd_dq_k128(a, tq, tk, tv, tdo, to, tdq, s, true)
+                             : launch_bwd_dq(a, tq, tk, tv, tdo, to, tdq, s, true);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+extern "C" int fa_window_backward_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int D, int window, int sinks,
+                                                  size_t *bytes) {
+    if (!bytes) return FA_ERR_NULL;
+    int rc = check_window(B, Hq, Hkv, Nq, Nk, Nk, D, window, sinks, 1.f);
+    if (rc != FA_OK) return rc;
+    *bytes = 0;
+    return FA_OK;
+}
+
+extern "C" int fa_window_backward_dkdv(const void *q, const void *k, const void *v, const void *dO, const float *lse,
+                                       const float *delta, void *dk, void *dv, int B, int Hq, int Hkv, int Nq, int Nk,
+                                       int D, int window, int sinks, float scale, int dtype, int grad_dtype,
+                                       void *workspace, size_t workspace_bytes, void *stream) {
+    if (dtype != FA_BF16 || (grad_dtype != FA_BF16 && grad_dtype != FA_F32)) return FA_ERR_DTYPE;
+    int rc = check_window(B, Hq, Hkv, Nq, Nk, Nk, D, window, sinks, scale);
+    if (rc != FA_OK) return rc;
+    rc = check_ptrs({q, k, v, dO, lse, delta, dk, dv});
+    if (rc != FA_OK) return rc;
+    int dev;
+    DeviceState *st;
+    rc = device_state(&dev, &st);
+    if (rc != FA_OK) return rc;
+    BwdArgs a{q, k, v, nullptr, dO, lse, const_cast<float *>(delta), nullptr, dk, dv, B, Hq, Nq, D, scale,
+              scale * log2e(), 1, grad_dtype == FA_BF16 ? 1 : 0, st->status_word, B * Hkv,
+              window_args(Hkv, Nk, window, sinks)};
+    CUtensorMap tq, tk, tv, tdo, tdk, tdv;
+    const int Dk = kernel_head_dim(D);
+    const int q_box = Dk == 64 ? 128 : kDkdvQRows;
+    if (encode_rows(&tq, q, B * Hq, Nq, Nq, D, q_box) != FA_OK || encode_rows(&tk, k, B * Hkv, Nk, Nk, D, 128) != FA_OK ||
+        encode_rows(&tv, v, B * Hkv, Nk, Nk, D, 128) != FA_OK || encode_rows(&tdo, dO, B * Hq, Nq, Nq, D, q_box) != FA_OK ||
+        encode_3d(&tdk, dk, B * Hkv, Nk, D, 128, grad_dtype == FA_F32) != FA_OK ||
+        encode_3d(&tdv, dv, B * Hkv, Nk, D, 128, grad_dtype == FA_F32) != FA_OK)
+        return FA_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = Dk == 64 ? launch_bwd_dkdv_q128(a, tq, tk, tv, tdo, tdk, tdv, s, true)
+                             : launch_bwd_dkdv(a, tq, tk, tv, tdo, tdk, tdv, s, true);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+namespace {
+constexpr int kMaxDecodeRows = 16;  // new rows per sequence
+
+int check_rows(int B, int Hq, int Hkv, int n_q, int N, int D, float scale) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || n_q < 1 || N < 1 || D < 1) return FA_ERR_SHAPE;
+    if (B > 65535 || Hq > 65535 || Hq % Hkv != 0 || n_q > kMaxDecodeRows || N > kMaxPositions) return FA_ERR_SHAPE;
+    const long long max = (1ll << 31) - 1;
+    if ((long long)B * Hkv * N > max || (long long)B * Hq * n_q > max) return FA_ERR_SHAPE;
+    if (!std::isfinite(scale) || scale <= 0.f) return FA_ERR_SCALE;
+    if (D != 64 && D != 128 && D != 256) return FA_ERR_HEAD_DIM;
+    return FA_OK;
+}
+
+// CTAs per (sequence, key head, row tile) of windowed decode.
+int token_splits(int B, int Hq, int Hkv, int n_q, int N, int D, const WinArgs &w, int num_sms) {
+    // the most key tiles any sequence can need: a cache full of keys, or the window of the n_q rows and the sinks
+    const int bn = win_decode_tile_keys();
+    const KeySpan sp = key_span(std::max(0, N - n_q), N - 1, w.window, w.sinks, bn);
+    return win_decode_splits(B, Hkv, Hq / Hkv * n_q, sp.n, D, num_sms);
+}
+
+size_t token_workspace(int B, int Hq, int n_q, int D, int splits) {
+    return splits > 1 ? partials_bytes((size_t)B * Hq * n_q, splits, D) : 0;
+}
+
+int check_token(int B, int Hq, int Hkv, int n_q, int N, int D, int window, int sinks, float scale) {
+    int rc = check_rows(B, Hq, Hkv, n_q, N, D, scale);
+    if (rc == FA_OK && (window < 1 || sinks < 0 || n_q > N)) rc = FA_ERR_SHAPE;
+    return rc;
+}
+}  // namespace
+
+extern "C" int fa_window_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q, int N, int D, int window, int sinks,
+                                                size_t *bytes) {
+    if (!bytes) return FA_ERR_NULL;
+    int rc = check_token(B, Hq, Hkv, n_q, N, D, window, sinks, 1.f);
+    if (rc != FA_OK) return rc;
+    const WinArgs w = window_args(Hkv, N, window, sinks);
+    *bytes = token_workspace(B, Hq, n_q, D, token_splits(B, Hq, Hkv, n_q, N, D, w, current_num_sms()));
+    return FA_OK;
+}
+
+extern "C" int fa_window_decode(const void *q, const void *k, const void *v, const int *lens, void *o, float *lse, int B,
+                                int Hq, int Hkv, int n_q, int N, int D, int window, int sinks, float scale,
+                                void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = check_token(B, Hq, Hkv, n_q, N, D, window, sinks, scale);
+    if (rc != FA_OK) return rc;
+    rc = check_ptrs({q, k, v, o, lse});
+    if (rc != FA_OK) return rc;
+    rc = check_lens(lens);
+    if (rc != FA_OK) return rc;
+    int dev;
+    DeviceState *st;
+    rc = device_state(&dev, &st);
+    if (rc != FA_OK) return rc;
+    const WinArgs w = window_args(Hkv, N, window, sinks);
+    const int splits = token_splits(B, Hq, Hkv, n_q, N, D, w, st->num_sms);
+    const size_t need = token_workspace(B, Hq, n_q, D, splits);
+    if (need > 0) {
+        rc = check_ptrs({workspace});
+        if (rc != FA_OK) return rc;
+        if (workspace_bytes < need) return FA_ERR_WORKSPACE;
+    }
+    const size_t rows = (size_t)B * Hq * n_q;
+    float *part_o = need > 0 ? static_cast<float *>(workspace) : nullptr;
+    float2 *part_ml = need > 0 ? reinterpret_cast<float2 *>(part_o + rows * splits * D) : nullptr;
+    WinDecodeArgs a{q, lens, o, lse, B, Hkv, Hq / Hkv * n_q, n_q, N, D, w.window, w.sinks, scale * log2e(),
+                    st->status_word, splits, splits, 0, part_o, part_ml};
+    CUtensorMap tk, tv;
+    if (encode_rows(&tk, k, B * Hkv, N, N, D, win_decode_tile_keys()) != FA_OK ||
+        encode_rows(&tv, v, B * Hkv, N, N, D, win_decode_tile_keys()) != FA_OK)
+        return FA_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_win_decode(a, tk, tv, s);
+    if (e == cudaSuccess && part_o) e = launch_win_join(part_o, part_ml, o, lse, (long long)rows, splits, D, s);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+namespace {
+// How shared-prefix decode cuts its work: the prefix into chunks for packed 128-row query tiles, the sequences'
+// own caches into `own` CTAs each.
+struct PrefixPlan {
+    int R, rb, nb, m_tiles, splits, chunk_tiles, own;
+    int slots() const { return splits + own; }
+};
+
+PrefixPlan prefix_plan(int B, int Hq, int Hkv, int n_q, int P, int N, int D, int num_sms) {
+    PrefixPlan p;
+    p.R = Hq / Hkv * n_q;
+    p.rb = std::min(p.R, 128);
+    p.nb = std::min(128 / p.rb, B);
+    p.m_tiles = p.R <= 128 ? (B + p.nb - 1) / p.nb : B * ((p.R + 127) / 128);
+    const int bn = fwd_block_n(kernel_head_dim(D)), tiles = (P + bn - 1) / bn;
+    const int per_block = kernel_head_dim(D) <= 128 ? 2 : 1;  // query tiles a block streams the chunk past
+    const long long units = (long long)Hkv * ((p.m_tiles + per_block - 1) / per_block);
+    // the chunk count that minimises waves of CTAs x (tiles per chunk + a block's fixed cost, about 3 tiles)
+    long long best = 0;
+    p.splits = 1;
+    p.chunk_tiles = tiles;
+    for (int s = 1; s <= tiles && (s == 1 || units * s <= 4ll * num_sms); ++s) {
+        const int c = (tiles + s - 1) / s;
+        if ((tiles + c - 1) / c != s) continue;  // the same chunks as a smaller count
+        const long long cost = (units * s + num_sms - 1) / num_sms * (c + 3);
+        if (s == 1 || cost < best) {
+            best = cost;
+            p.splits = s;
+            p.chunk_tiles = c;
+        }
+    }
+    p.own = win_decode_splits(B, Hkv, p.R, (N + win_decode_tile_keys() - 1) / win_decode_tile_keys(), D, num_sms);
+    return p;
+}
+
+int check_prefix(int B, int Hq, int Hkv, int n_q, int P, int N, int D, float scale) {
+    int rc = check_rows(B, Hq, Hkv, n_q, N, D, scale);
+    if (rc == FA_OK && (P < 1 || P > kMaxPositions || (long long)Hkv * P > (1ll << 31) - 1)) rc = FA_ERR_SHAPE;
+    return rc;
+}
+}  // namespace
+
+extern "C" int fa_prefix_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q, int P, int N, int D, size_t *bytes) {
+    if (!bytes) return FA_ERR_NULL;
+    int rc = check_prefix(B, Hq, Hkv, n_q, P, N, D, 1.f);
+    if (rc != FA_OK) return rc;
+    const PrefixPlan p = prefix_plan(B, Hq, Hkv, n_q, P, N, D, current_num_sms());
+    *bytes = partials_bytes((size_t)B * Hq * n_q, p.slots(), D);
+    return FA_OK;
+}
+
+extern "C" int fa_prefix_decode(const void *q, const void *k_prefix, const void *v_prefix, const void *k, const void *v,
+                                const int *lens, void *o, float *lse, int B, int Hq, int Hkv, int n_q, int P, int N,
+                                int D, float scale, void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = check_prefix(B, Hq, Hkv, n_q, P, N, D, scale);
+    if (rc != FA_OK) return rc;
+    rc = check_ptrs({q, k_prefix, v_prefix, k, v, o, lse, workspace});
+    if (rc != FA_OK) return rc;
+    rc = check_lens(lens);
+    if (rc != FA_OK) return rc;
+    int dev;
+    DeviceState *st;
+    rc = device_state(&dev, &st);
+    if (rc != FA_OK) return rc;
+    const PrefixPlan p = prefix_plan(B, Hq, Hkv, n_q, P, N, D, st->num_sms);
+    const size_t rows = (size_t)B * Hq * n_q;
+    if (workspace_bytes < partials_bytes(rows, p.slots(), D)) return FA_ERR_WORKSPACE;
+    float *part_o = static_cast<float *>(workspace);
+    float2 *part_ml = reinterpret_cast<float2 *>(part_o + rows * p.slots() * D);
+
+    SpanArgs a{};
+    a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.Nq = n_q, a.Nk = P, a.D = D;
+    a.window = P;
+    a.scale_log2 = scale * log2e();
+    a.status = st->status_word;
+    a.num_sms = st->num_sms;
+    a.R = p.R, a.rb = p.rb, a.nb = p.nb, a.m_tiles = p.m_tiles;
+    a.splits = p.splits, a.chunk_tiles = p.chunk_tiles;
+    a.slots = p.slots();
+    a.part_o = part_o, a.part_ml = part_ml;
+    // the rows of a key head: [B, Hkv, R, D], boxes of rb rows of nb sequences
+    CUtensorMap tq, tkp, tvp, tk, tv;
+    {
+        cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.R, (cuuint64_t)Hkv, (cuuint64_t)B};
+        cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)p.R * D * 2, (cuuint64_t)Hkv * p.R * D * 2};
+        cuuint32_t box[4] = {64, (cuuint32_t)p.rb, 1, (cuuint32_t)p.nb};
+        cuuint32_t estr[4] = {1, 1, 1, 1};
+        if (g_encode(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(q), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return FA_ERR_CUDA;
+    }
+    const int bn = fwd_block_n(kernel_head_dim(D)), own_box = win_decode_tile_keys();
+    if (encode_rows(&tkp, k_prefix, Hkv, P, P, D, bn) != FA_OK || encode_rows(&tvp, v_prefix, Hkv, P, P, D, bn) != FA_OK ||
+        encode_rows(&tk, k, B * Hkv, N, N, D, own_box) != FA_OK || encode_rows(&tv, v, B * Hkv, N, N, D, own_box) != FA_OK)
+        return FA_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_win_fwd(a, tq, tkp, tvp, tkp, tvp, tkp, s);
+    if (e != cudaSuccess) return FA_ERR_CUDA;
+    WinDecodeArgs d{q, lens, nullptr, nullptr, B, Hkv, p.R, n_q, N, D, N, 0, scale * log2e(), st->status_word, p.own,
+                    p.slots(), p.splits, part_o, part_ml};
+    e = launch_win_decode(d, tk, tv, s);
+    if (e == cudaSuccess) e = launch_win_join(part_o, part_ml, o, lse, (long long)rows, p.slots(), D, s);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 extern "C" const char *fa_status_string(int status) {
     switch (status) {
         case FA_OK: return "ok";
         case FA_ERR_NULL: return "a required pointer is NULL";
-        case FA_ERR_SHAPE: return "invalid shape (B, H, N must be >= 1 and within index limits)";
+        case FA_ERR_SHAPE: return "invalid shape (sizes must be >= 1, within index limits and fit together)";
         case FA_ERR_HEAD_DIM: return "head dimension not supported for this dtype / pass";
         case FA_ERR_DTYPE: return "unsupported dtype or grad_dtype";
         case FA_ERR_ALIGN: return "pointer not 16-byte aligned";
@@ -403,7 +740,7 @@ extern "C" const char *fa_status_string(int status) {
         case FA_ERR_TIMEOUT: return "a bounded in-kernel wait ran out";
         case FA_ERR_DEVICE_PTR: return "pointer is not device-accessible memory";
         case FA_ERR_DEVICE: return "current device is not sm_103 (GB300)";
-        case FA_ERR_WORKSPACE: return "workspace smaller than fa_decode_workspace_bytes() requires";
+        case FA_ERR_WORKSPACE: return "workspace smaller than its size query requires";
         case FA_ERR_SCRATCH_LIMIT:
             return "sizes need more than FA_DECODE_NOALLOC_SCRATCH_BYTES of scratch; use fa_decode with a workspace";
         default: return "unknown status";

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "win.cuh"
+
 namespace fa {
 
 // Spec table of the bf16 forward: query rows per CTA, keys per K/V tile, K/V
@@ -103,7 +105,43 @@ struct BwdArgs {
     int grad_bf16;  // 1: gradients stored as bf16, 0: fp32
     int *status;
     int head_group;  // heads per group of the causal work order (tile_order_at)
+    WinArgs win;     // windowed kernels (WIN = true) only; N is then the query rows
 };
+
+#ifdef __CUDACC__
+// The query rows of windowed attention that keys k0 .. k0 + bk - 1 meet: rows from `first` on in `per_head`
+// tiles of bq rows, for each of the key head's query heads; n tiles in all.
+struct WinRows {
+    int first, per_head, n;
+    __device__ __forceinline__ int row0(int i, int bq) const { return first + i % per_head * bq; }
+};
+
+__device__ __forceinline__ WinRows win_rows(const BwdArgs &a, int k0, int bk, int bq) {
+    const int off = a.win.Nk - a.N;  // position of row 0
+    WinRows r;
+    r.first = max(0, k0 - off);
+    const int end = k0 < a.win.sinks ? a.N : min(a.N, k0 + bk - 1 + a.win.window - off);
+    r.per_head = end > r.first ? (end - r.first + bq - 1) / bq : 0;
+    r.n = r.per_head * (a.H / a.win.Hkv);
+    return r;
+}
+
+// Query slice (batch and query head) of tile i of key slice kv_bh.
+__device__ __forceinline__ int win_query_slice(const BwdArgs &a, int kv_bh, const WinRows &rows, int i) {
+    return kv_bh * (a.H / a.win.Hkv) + i / rows.per_head;
+}
+
+// bit i: query row q0 + i exists and sees key
+__device__ __forceinline__ uint32_t seen_by(const BwdArgs &a, int key, int q0) {
+    return key < a.win.Nk ? seeing_positions(key, a.win.Nk - a.N + q0, a.win.window, a.win.sinks) & low_bits(a.N - q0) : 0u;
+}
+
+// query rows q0 .. q0 + n - 1 all see key
+__device__ __forceinline__ bool sees_all(const BwdArgs &a, int key, int q0, int n) {
+    const int p0 = a.win.Nk - a.N + q0;
+    return key < a.win.Nk && all_seen(p0, p0 + n - 1, key, key, a.win.window, a.win.sinks);
+}
+#endif
 
 // 5-GEMM comparator backward (bwd_atomic.cu): a.dq is the fp32 accumulator
 // (B*H*N*D floats), dq_out the gradient in grad dtype; D = 128 only.
@@ -155,20 +193,24 @@ cudaError_t launch_fwd_bf16_duo(const FwdArgs &a, const CUtensorMap &tq, const C
 // and dQ's (grad dtype, 128-byte boxes of 128 rows, 128-byte swizzle: the TMA stores of the epilogue).
 cudaError_t launch_bwd_dq(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk,
                           const CUtensorMap &tv, const CUtensorMap &tdo, const CUtensorMap &to,
-                          const CUtensorMap &tdq, cudaStream_t s);
+                          const CUtensorMap &tdq, cudaStream_t s,
+                          bool win = false);
 // bwd_dq_k128.cu: the dQ kernel for D = 64 with 128-row K / V tiles (TMA boxes of 128 rows)
 cudaError_t launch_bwd_dq_k128(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk,
                                const CUtensorMap &tv, const CUtensorMap &tdo, const CUtensorMap &to,
-                               const CUtensorMap &tdq, cudaStream_t s);
+                               const CUtensorMap &tdq, cudaStream_t s,
+                          bool win = false);
 // The dK/dV kernels also take dK's and dV's tensor maps (grad dtype, 128-byte boxes of 128 rows, 128-byte
 // swizzle: the TMA stores of the epilogue).
 // bwd_dkdv_q128.cu: the dK/dV kernel for D = 64 with 128-row Q / dO tiles (TMA boxes of 128 rows)
 cudaError_t launch_bwd_dkdv_q128(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk,
                                  const CUtensorMap &tv, const CUtensorMap &tdo, const CUtensorMap &tdk,
-                                 const CUtensorMap &tdv, cudaStream_t s);
+                                 const CUtensorMap &tdv, cudaStream_t s,
+                          bool win = false);
 cudaError_t launch_bwd_dkdv(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk,
                             const CUtensorMap &tv, const CUtensorMap &tdo, const CUtensorMap &tdk,
-                            const CUtensorMap &tdv, cudaStream_t s);
+                            const CUtensorMap &tdv, cudaStream_t s,
+                          bool win = false);
 cudaError_t launch_selftest_timeout(int *status, int limit_us, cudaStream_t s);
 
 // Head dimension a bf16 kernel is built for: the smallest of 64, 128, 192, 256 that holds D.  Any

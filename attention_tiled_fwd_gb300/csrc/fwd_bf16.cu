@@ -41,9 +41,17 @@
 //   softmax writes P_j into P[j % 2] after waiting for PV_{j-2} (per-buffer
 //   barrier pv_done[j % 2]), and issuer A writes S_{j+2} into S[j % 2] after the
 //   softmax finished reading S_j.
+//
+// The same kernel serves windowed attention and the shared prefix at D = 192 and
+// 256 (Args = SpanArgs, win.cuh): the key tiles are those of key_span from their
+// own first key on, the mask is the window's, a query head reads its group's key
+// head; with PREFIX the 128 rows are packed from several sequences, every CTA
+// takes one chunk of the prefix and writes the row's partial (O, m, l).
 #include "fa_internal.h"
 #include "sm100_ptx.cuh"
+#include "win.cuh"
 #include <cmath>
+#include <type_traits>
 
 namespace fa {
 namespace {
@@ -74,11 +82,15 @@ struct FwdSmem {
     static constexpr int kAlloc = kBytes + 1024;  // slack for 1024-byte alignment of the base
 };
 
-template <int D, int BN, int NSLOT>
+// Args: FwdArgs, or SpanArgs for windowed attention (PREFIX: the shared prefix), which also reads the sink
+// tiles' tensor maps tmap_ks and tmap_vs.
+template <int D, int BN, int NSLOT, class Args, bool PREFIX>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                    const __grid_constant__ CUtensorMap tmap_v, FwdArgs a) {
+                    const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_ks,
+                    const __grid_constant__ CUtensorMap tmap_vs, Args a) {
     using L = FwdSmem<D, BN, NSLOT>;
+    constexpr bool kSpan = std::is_same<Args, SpanArgs>::value;
     constexpr int kPanels = L::kPanels;
     constexpr uint32_t kTmemCols = 512;
     constexpr uint32_t kColS0 = 0, kColS1 = BN, kColO = 2 * BN, kColP0 = 2 * BN + D, kColP1 = kColP0 + BN / 2;
@@ -104,12 +116,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kTmemHolderOff);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int rank, bh;
-    tile_order((a.N + kBM - 1) / kBM, a.B * a.H, a.causal, a.head_group, &rank, &bh);
-    const int q_tile = (a.N + kBM - 1) / kBM - 1 - rank;  // causal: the last query tile has the most keys
-    const int N = a.N;
-    const int kv_end = a.causal ? min(N, (q_tile + 1) * kBM) : N;
-    const int n_kv = (kv_end + BN - 1) / BN;  // >= 1 because q_tile * kBM < N
+    // bh: query slice; kv_bh: key slice; N: query rows; n_kv >= 1 key tiles, tile j from key key0(j) on
+    int bh, kv_bh, q_tile, N, n_kv;
+    int chunk = 0, b0 = 0, r0 = 0;  // PREFIX: the chunk of the prefix, the packed tile's first sequence and row
+    KeySpan span{0, 0, 0};
+    if constexpr (!kSpan) {
+        int rank;
+        tile_order((a.N + kBM - 1) / kBM, a.B * a.H, a.causal, a.head_group, &rank, &bh);
+        q_tile = (a.N + kBM - 1) / kBM - 1 - rank;  // causal: the last query tile has the most keys
+        N = a.N;
+        kv_bh = bh;
+        const int kv_end = a.causal ? min(N, (q_tile + 1) * kBM) : N;
+        n_kv = (kv_end + BN - 1) / BN;  // >= 1 because q_tile * kBM < N
+    } else if constexpr (PREFIX) {
+        q_tile = blockIdx.x % a.m_tiles;
+        const int rest = blockIdx.x / a.m_tiles;
+        chunk = rest % a.splits;
+        bh = kv_bh = rest / a.splits;
+        N = a.Nk;
+        span.lo = chunk * a.chunk_tiles * BN;
+        n_kv = min(a.chunk_tiles, (N + BN - 1) / BN - chunk * a.chunk_tiles);
+        const int row_tiles = (a.R + a.rb - 1) / a.rb;
+        b0 = q_tile / row_tiles * a.nb;
+        r0 = q_tile % row_tiles * a.rb;
+    } else {
+        N = a.Nq;
+        bh = blockIdx.x % (a.B * a.Hq);
+        q_tile = (N + kBM - 1) / kBM - 1 - blockIdx.x / (a.B * a.Hq);
+        kv_bh = bh / a.Hq * a.Hkv + bh % a.Hq / (a.Hq / a.Hkv);
+        const int p0 = a.Nk - N + q_tile * kBM;
+        span = key_span(p0, min(a.Nk, p0 + kBM) - 1, a.window, a.sinks, BN);
+        n_kv = span.n;
+    }
+    auto key0_of = [&](int j) { return kSpan ? span.key0(j, BN) : j * BN; };
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -143,10 +182,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_prefetch_desc(&tmap_q);
             tma_prefetch_desc(&tmap_k);
             tma_prefetch_desc(&tmap_v);
-            mbar_arrive_expect_tx(q_full, L::kQBytes);
+            if constexpr (PREFIX) {
+                mbar_arrive_expect_tx(q_full, a.rb * a.nb * D * 2);
 #pragma unroll
-            for (int p = 0; p < kPanels; ++p)
-                tma_load_3d(q_s + p * (kBM * 128), &tmap_q, q_full, p * 64, q_tile * kBM, bh);
+                for (int p = 0; p < kPanels; ++p)
+                    tma_load_4d(q_s + p * (kBM * 128), &tmap_q, q_full, p * 64, r0, kv_bh, b0);
+            } else {
+                mbar_arrive_expect_tx(q_full, L::kQBytes);
+#pragma unroll
+                for (int p = 0; p < kPanels; ++p)
+                    tma_load_3d(q_s + p * (kBM * 128), &tmap_q, q_full, p * 64, q_tile * kBM, bh);
+            }
             int last_round[NSLOT];
 #pragma unroll
             for (int s = 0; s < NSLOT; ++s) last_round[s] = -1;
@@ -154,11 +200,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int slot = idx % NSLOT, round = idx / NSLOT;
                 if (!mbar_wait(&slot_empty[slot], (round & 1) ^ 1, a.status, kSiteSlotEmpty)) break;
                 uint8_t *dst = slots + slot * L::kSlotBytes;
-                const CUtensorMap *map = (idx & 1) ? &tmap_v : &tmap_k;
+                const bool sink = kSpan && (idx >> 1) < span.n_sink;  // keys past the last sink read as zeros
+                const CUtensorMap *map = (idx & 1) ? (sink ? &tmap_vs : &tmap_v) : (sink ? &tmap_ks : &tmap_k);
                 mbar_arrive_expect_tx(&slot_full[slot], L::kSlotBytes);
 #pragma unroll
                 for (int p = 0; p < kPanels; ++p)
-                    tma_load_3d(dst + p * (BN * 128), map, &slot_full[slot], p * 64, (idx >> 1) * BN, bh);
+                    tma_load_3d(dst + p * (BN * 128), map, &slot_full[slot], p * 64, key0_of(idx >> 1), kv_bh);
 #pragma unroll
                 for (int s = 0; s < NSLOT; ++s)
                     if (s == slot) last_round[s] = round;
@@ -253,13 +300,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int ch = 0; ch < HB / 32; ++ch) tmem_ld32(tmem + lane_base + s_col + ch * 32, raw + ch * 32);
             tmem_wait_ld();
-            const int key0 = j * BN + g * HB;
-            const bool need_mask = (key0 + HB > N) || (a.causal && key0 + HB - 1 > q_tile * kBM);
-            if (need_mask) {
-                const int lim = a.causal ? min(N - 1, row) : N - 1;  // last visible key
+            const int key0 = key0_of(j) + g * HB;
+            if constexpr (kSpan) {
+                static_assert(!kSpan || HB == 32, "one mask word per half tile");
+                const int p0 = a.Nk - N + q_tile * kBM, window = span.window_in(j, a.window);
+                const bool need_mask = PREFIX ? key0 + HB > N
+                                              : !all_seen(p0, p0 + kBM - 1, key0, key0 + HB - 1, window, a.sinks);
+                if (need_mask) {
+                    const uint32_t seen = PREFIX ? low_bits(N - key0) : seen_keys(p0 + r, key0, window, a.sinks);
 #pragma unroll
-                for (int i = 0; i < HB; ++i)
-                    if (key0 + i > lim) raw[i] = 0xff800000u;  // -inf
+                    for (int i = 0; i < HB; ++i)
+                        if (!(seen & (1u << (i & 31)))) raw[i] = 0xff800000u;  // -inf
+                }
+            } else {
+                const bool need_mask = (key0 + HB > N) || (a.causal && key0 + HB - 1 > q_tile * kBM);
+                if (need_mask) {
+                    const int lim = a.causal ? min(N - 1, row) : N - 1;  // last visible key
+#pragma unroll
+                    for (int i = 0; i < HB; ++i)
+                        if (key0 + i > lim) raw[i] = 0xff800000u;  // -inf
+                }
             }
             // row max over this half (scale > 0 commutes with max): four chains of three-input maxima
             float mx[4];
@@ -350,6 +410,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
             const float l_row = l + lsum[(g ^ 1) * kBM + r];
             tc_fence_after();
+            if constexpr (PREFIX) {
+                // this chunk's partial of the row: O unnormalised, m (log2 units) and l
+                const int b = b0 + r / a.rb, rr = r0 + r % a.rb;
+                const bool valid = r < a.rb * a.nb && b < a.B && rr < a.R;
+                const size_t slot = (((size_t)b * a.Hkv + kv_bh) * a.R + rr) * a.slots + chunk;
+                uint32_t ov[32];
+#pragma unroll
+                for (int ch = 0; ch < HD / 32; ++ch) {
+                    tmem_ld32(tmem + lane_base + kColO + g * HD + ch * 32, ov);
+                    tmem_wait_ld();
+                    if (valid) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.part_o + slot * a.D + g * HD + ch * 32);
+#pragma unroll
+                        for (int v4 = 0; v4 < 8; ++v4)
+                            dst[v4] = make_uint4(ov[4 * v4], ov[4 * v4 + 1], ov[4 * v4 + 2], ov[4 * v4 + 3]);
+                    }
+                }
+                if (valid && g == 0) a.part_ml[slot] = make_float2(m, l_row);
+            } else {
             const float inv_l = 1.f / l_row;
             // row stride and stored columns: the caller's D (at most this kernel's D; the columns past it
             // hold zeros from the TMA's out-of-bounds fill)
@@ -375,6 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (row < N && g == 0) a.lse[(size_t)bh * N + row] = (m + __log2f(l_row)) * 0.69314718055994531f;
+            }
         }
     }
 
@@ -391,15 +471,40 @@ cudaError_t launch_spec(const FwdArgs &a, const CUtensorMap &tq, const CUtensorM
                         cudaStream_t s) {
     using L = FwdSmem<D, BN, NSLOT>;
     static_assert(L::kAlloc <= 232448, "shared memory budget");
-    auto kern = fwd_bf16_kernel<D, BN, NSLOT>;
+    auto kern = fwd_bf16_kernel<D, BN, NSLOT, FwdArgs, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
     dim3 grid(((a.N + kBM - 1) / kBM) * a.H * a.B);
-    kern<<<grid, kThreads, L::kAlloc, s>>>(tq, tk, tv, a);
+    kern<<<grid, kThreads, L::kAlloc, s>>>(tq, tk, tv, tk, tv, a);
+    return cudaGetLastError();
+}
+
+template <int D, int BN, int NSLOT, bool PREFIX>
+cudaError_t launch_span(const SpanArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                        const CUtensorMap &tks, const CUtensorMap &tvs, cudaStream_t s) {
+    using L = FwdSmem<D, BN, NSLOT>;
+    auto kern = fwd_bf16_kernel<D, BN, NSLOT, SpanArgs, PREFIX>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+    if (e != cudaSuccess) return e;
+    const int grid = PREFIX ? a.m_tiles * a.splits * a.Hkv : ((a.Nq + kBM - 1) / kBM) * a.Hq * a.B;
+    kern<<<grid, kThreads, L::kAlloc, s>>>(tq, tk, tv, tks, tvs, a);
     return cudaGetLastError();
 }
 
 }  // namespace
+
+cudaError_t launch_win_fwd_wide(const SpanArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                                const CUtensorMap &tks, const CUtensorMap &tvs, cudaStream_t s) {
+    const bool prefix = a.part_o != nullptr;
+    switch (kernel_head_dim(a.D)) {
+        case 192:
+            return prefix ? cudaErrorInvalidValue : launch_span<192, 64, fwd_nslot(192), false>(a, tq, tk, tv, tks, tvs, s);
+        case 256:
+            return prefix ? launch_span<256, 64, fwd_nslot(256), true>(a, tq, tk, tv, tks, tvs, s)
+                          : launch_span<256, 64, fwd_nslot(256), false>(a, tq, tk, tv, tks, tvs, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
 
 cudaError_t launch_fwd_bf16(const FwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                             const CUtensorMap &to, cudaStream_t s) {

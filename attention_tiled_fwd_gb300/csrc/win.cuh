@@ -1,0 +1,92 @@
+// win.cuh -- windowed attention: which keys a tile of query rows reads, and
+// which of them each row sees.
+//
+// Row i of N_q query rows sits at position p = i + N_k - N_q and sees key j iff
+//   j <= p  and  (j < sinks  or  j > p - window):
+// the `window` last keys up to its own and the first `sinks` keys.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+namespace fa {
+
+// The longest key range windowed attention takes: sums and differences of two positions and a window
+// then stay inside 32 bits.
+constexpr int kMaxPositions = 1 << 29;
+
+// The key tiles (bn keys each) that positions p0 .. p1 read: n_sink tiles from key 0 on, then tiles from
+// key lo on, n in all.  A window tile starts at the first key that p0 sees rather than at a multiple of
+// bn, so a tile of 128 rows reads window + 127 keys and not up to bn - 1 more.  Where the window reaches the
+// sinks there is one range from key 0 (n_sink = 0); otherwise the sink tiles stand for the sinks alone (their
+// window is 0: a key that a sink tile and a window tile both hold counts in the window tile), so every key that
+// the tiles stand for is seen by one of the positions or by a later one.
+struct KeySpan {
+    int n_sink, lo, n;
+    __host__ __device__ int key0(int j, int bn) const { return j < n_sink ? j * bn : lo + (j - n_sink) * bn; }
+    __host__ __device__ int window_in(int j, int window) const { return j < n_sink ? 0 : window; }
+};
+
+__host__ __device__ inline KeySpan key_span(int p0, int p1, int window, int sinks, int bn) {
+    KeySpan s;
+    const int lo = p0 - window + 1;
+    const bool gap = lo > sinks;
+    s.n_sink = gap ? (sinks + bn - 1) / bn : 0;
+    s.lo = gap ? lo : 0;
+    s.n = s.n_sink + (p1 + 1 - s.lo + bn - 1) / bn;
+    return s;
+}
+
+// bits [0, n) of a word
+__host__ __device__ inline uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+// bit i: position p sees key k0 + i (i < 32)
+__host__ __device__ inline uint32_t seen_keys(int p, int k0, int window, int sinks) {
+    return low_bits(p + 1 - k0) & (~low_bits(p - window + 1 - k0) | low_bits(sinks - k0));
+}
+
+// every one of positions p0 .. p1 sees every one of keys k0 .. k1
+__host__ __device__ inline bool all_seen(int p0, int p1, int k0, int k1, int window, int sinks) {
+    return k1 <= p0 && (k0 > p1 - window || k1 < sinks);
+}
+
+// bit i: the position p0 + i sees key (i < 32)
+__host__ __device__ inline uint32_t seeing_positions(int key, int p0, int window, int sinks) {
+    return ~low_bits(key - p0) & (key < sinks ? ~0u : low_bits(key + window - p0));
+}
+
+// Windowed (and grouped-head) form of the backward kernels' arguments; unused by their plain forms.
+struct WinArgs {
+    int Hkv;     // key heads; query head h reads key head h / (H / Hkv)
+    int Nk;      // keys; the query rows are the last N of the Nk positions
+    int window, sinks;
+};
+
+// The forward over the keys that a span of query rows sees (win_fwd.cu, and fwd_bf16.cu for wide heads).
+// Two forms: windowed attention writes O and LSE; the shared-prefix form packs the rows of all sequences
+// into 128-row tiles, sees every key, and writes unnormalised O, m and l partials of key chunks.
+struct SpanArgs {
+    void *o;
+    float *lse;
+    int B, Hq, Hkv, Nq, Nk, D;
+    int window, sinks;
+    float scale_log2;
+    int *status;
+    int num_sms;
+    // windowed: how a block's two query tiles are chosen (kOneTile, kTwoHeads, kTwoRowTiles)
+    int pairing;
+    // shared prefix: R = rows per (sequence, key head); a 128-row tile holds rb rows of each of nb sequences
+    int R, rb, nb, m_tiles;
+    int splits, chunk_tiles;  // key chunks, key tiles per chunk
+    int slots;                // partials per row in the workspace
+    float *part_o;            // [rows][slots][D]
+    float2 *part_ml;          // [rows][slots] (m in log2 units, l)
+};
+enum : int { kOneTile = 0, kTwoHeads = 1, kTwoRowTiles = 2 };
+
+cudaError_t launch_win_fwd(const SpanArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                           const CUtensorMap &tks, const CUtensorMap &tvs, const CUtensorMap &to, cudaStream_t s);
+cudaError_t launch_win_fwd_wide(const SpanArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                                const CUtensorMap &tks, const CUtensorMap &tvs, cudaStream_t s);
+
+}  // namespace fa

@@ -1,0 +1,32 @@
+// win_decode.cuh -- launch interface of the grouped-head decode kernels (win_decode.cu).
+#pragma once
+#include "win.cuh"
+
+namespace fa {
+
+struct WinDecodeArgs {
+    const void *q;     // [B, Hkv, R, D] bf16, R = (Hq / Hkv) n_q: the caller's [B, Hq, n_q, D]
+    const int *lens;   // [B] keys each sequence holds (clamped to [0, N]); null: N
+    void *o;           // [B, Hkv, R, D] bf16
+    float *lse;        // [B, Hkv, R]
+    int B, Hkv, R, n_q, N, D;
+    int window, sinks;
+    float scale_log2;
+    int *status;
+    int splits;        // CTAs a sequence's tiles are dealt to
+    // partials [row][slots]: this launch writes slots slot0 .. slot0 + splits - 1; null part_o: o and lse are
+    // written directly (splits = 1)
+    int slots, slot0;
+    float *part_o;
+    float2 *part_ml;
+};
+
+// CTAs per (sequence, key head, row tile) for caches that need up to `tiles` tiles.
+int win_decode_splits(int B, int Hkv, int R, int tiles, int D, int num_sms);
+int win_decode_tile_keys();
+cudaError_t launch_win_decode(const WinDecodeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s);
+// O and LSE of `rows` rows from `slots` partials each (part_o [row][slot][D], part_ml [row][slot]).
+cudaError_t launch_win_join(const float *part_o, const float2 *part_ml, void *o, float *lse, long long rows, int slots,
+                            int D, cudaStream_t s);
+
+}  // namespace fa

@@ -1,0 +1,609 @@
+// win_fwd.cu -- the forward over the keys that a span of query rows sees: windowed
+// attention (window, sinks, grouped heads, a chunk of rows behind cached keys)
+// and the shared prefix of a decode batch.  D = 64 and 128; wider heads run
+// fwd_bf16.cu.
+//
+// Per row i at position p:  O = sum_j P_ij v_j / l,  P_ij = 2^(c s_ij - m) over the
+// visible keys j <= p with j < sinks or j > p - window, m the running maximum
+// (base 2, c = scale log2 e), l the running sum, L = (m + log2 l) ln 2.
+//
+// The block of a CTA is two 128-row query tiles past one stream of 128-key K/V
+// tiles, as in fwd_bf16_pair.cu (one softmax warpgroup per tile, one tcgen05
+// issuer, P over S in TMEM, persistent grid).  What a block's tiles are:
+//   two heads   the same rows of two query heads that share a key head: the two
+//               tiles read exactly the same keys;
+//   two rows    (one query head per key head) neighbouring row tiles: the stream
+//               is the union of their windows and each skips what it does not see;
+//   one tile    launches with no more tiles than SMs: every tile gets its own SM;
+//   prefix      128-row tiles packed from the rows of many sequences (the group's
+//               heads and the new rows of one sequence are adjacent in memory, so
+//               one 4-D TMA box gathers them), against one chunk of the prefix.
+// A block reads its sink tiles, then its window from the first key that its first
+// row sees (key_span); only tiles that hold a masked pair build masks.
+#include "fa_internal.h"
+#include "sm100_ptx.cuh"
+#include "win.cuh"
+#include <cmath>
+
+namespace fa {
+namespace {
+
+constexpr int kBM = 128;            // rows per query tile (TMEM lanes)
+constexpr int kBN = 128;            // keys per K/V tile
+constexpr int kTiles = 2;           // query tiles per CTA
+constexpr int kFirstSoftmaxWarp = 2;
+constexpr int kThreads = 32 * kFirstSoftmaxWarp + 128 * kTiles;
+
+enum : int { kSiteQ = 181, kSiteSlotEmpty, kSiteSlotFull, kSiteSFull, kSitePFull, kSitePV, kSiteFinal, kSiteDrain,
+             kSiteQEmpty, kSiteOFree, kSiteStage };
+
+template <int D, int NSLOT>
+struct SpanSmem {
+    static constexpr int kPanels = D / 64;
+    static constexpr int kQBytes = kBM * D * 2;    // one query tile
+    static constexpr int kSlotBytes = kBN * D * 2;  // one K or V tile
+    static constexpr int kQOff = 0;
+    static constexpr int kSlotOff = kTiles * kQBytes;
+    static constexpr int kStageOff = kSlotOff + NSLOT * kSlotBytes;  // one query tile's O, staged for TMA stores
+    static constexpr int kBarOff = kStageOff + kQBytes;
+    // q_full, q_empty, slot_full[NSLOT], slot_empty[NSLOT], per tile: s_full, p_full, pv_done, o_free,
+    // stage_full; final, stage_free
+    static constexpr int kNumBars = 2 + 2 * NSLOT + 5 * kTiles + 2;
+    static constexpr int kTmemHolderOff = kBarOff + kNumBars * 8;
+    static constexpr int kAlloc = kTmemHolderOff + 16 + 1024;
+};
+
+// The work of one block of this CTA: the key tiles it streams, and which of them each of its two query
+// tiles reads.  Every role of the CTA walks the same sequence of blocks and computes these alike.
+struct SpanBlock {
+    KeySpan span;             // the key tiles
+    int kv_bh, y_off;         // their K/V slice, and the row that key 0 of the span sits at
+    int from[kTiles], to[kTiles];  // query tile x reads key tiles [0, n_sink) and [from, to)
+    int n[kTiles];            // how many that is (0: no such query tile)
+    int zq[kTiles], yq[kTiles];  // windowed: the tile's head slice and first row; prefix: key head, packed tile
+    int p0[kTiles];           // windowed: position of the tile's first row
+
+    __device__ __forceinline__ bool reads(int x, int j) const {
+        return n[x] > 0 && j < span.n && (j < span.n_sink || (j >= from[x] && j < to[x]));
+    }
+    // which of query tile x's steps key tile j is
+    __device__ __forceinline__ int step_of(int x, int j) const { return j < span.n_sink ? j : span.n_sink + j - from[x]; }
+};
+
+// Windowed blocks in longest-first order: the last rows of every head first.
+__device__ __forceinline__ SpanBlock window_block(const SpanArgs &a, int L) {
+    SpanBlock w;
+    const int G = a.Hq / a.Hkv;
+    const int per_block = a.pairing == kTwoRowTiles ? kTiles * kBM : kBM;
+    const int n_blk = (a.Nq + per_block - 1) / per_block;
+    const int heads = a.pairing == kTwoHeads ? a.Hq / kTiles : a.Hq;  // head pairs, or heads
+    const int bh = L % (a.B * heads);
+    const int row0 = (n_blk - 1 - L / (a.B * heads)) * per_block;
+    const int b = bh / heads, h = (bh % heads) * (a.pairing == kTwoHeads ? kTiles : 1);
+    const int off = a.Nk - a.Nq;
+    w.kv_bh = b * a.Hkv + h / G;
+    w.y_off = 0;
+#pragma unroll
+    for (int x = 0; x < kTiles; ++x) {
+        w.zq[x] = b * a.Hq + h + (a.pairing == kTwoHeads ? x : 0);
+        w.yq[x] = row0 + (a.pairing == kTwoRowTiles ? x * kBM : 0);
+        w.p0[x] = off + w.yq[x];
+    }
+    const bool two = a.pairing == kTwoHeads || (a.pairing == kTwoRowTiles && w.yq[1] < a.Nq);
+    const int last = two ? w.yq[1] : w.yq[0];
+    w.span = key_span(w.p0[0], off + min(a.Nq, last + kBM) - 1, a.window, a.sinks, kBN);
+#pragma unroll
+    for (int x = 0; x < kTiles; ++x) {
+        // the window tiles of this query tile alone: from the first key its first row sees (from key 0 on
+        // when the span is one range that holds the sinks) to its last row's own key
+        const int lo = w.p0[x] - a.window + 1;
+        w.from[x] = w.span.n_sink + (w.span.lo == 0 && a.sinks > 0 ? 0 : max(0, lo - w.span.lo) / kBN);
+        const int end = off + min(a.Nq, w.yq[x] + kBM);
+        w.to[x] = w.span.n_sink + (end - w.span.lo + kBN - 1) / kBN;
+        w.n[x] = (x == 0 || two) ? w.span.n_sink + w.to[x] - w.from[x] : 0;
+    }
+    return w;
+}
+
+// Shared-prefix blocks: two packed query tiles of a key head against one chunk of the prefix.
+__device__ __forceinline__ SpanBlock prefix_block(const SpanArgs &a, int L) {
+    SpanBlock w;
+    const int pairs = (a.m_tiles + kTiles - 1) / kTiles;
+    const int m = (L % pairs) * kTiles;
+    const int rest = L / pairs;
+    const int chunk = rest % a.splits;
+    w.kv_bh = rest / a.splits;
+    w.y_off = chunk * a.chunk_tiles * kBN;
+    w.span.n_sink = 0;
+    w.span.lo = 0;
+    w.span.n = min(a.chunk_tiles, (a.Nk + kBN - 1) / kBN - chunk * a.chunk_tiles);
+#pragma unroll
+    for (int x = 0; x < kTiles; ++x) {
+        w.zq[x] = chunk;
+        w.yq[x] = m + x;
+        w.p0[x] = 0;
+        w.from[x] = 0;
+        w.to[x] = w.span.n;
+        w.n[x] = m + x < a.m_tiles ? w.span.n : 0;
+    }
+    return w;
+}
+
+template <bool PREFIX>
+__device__ __forceinline__ SpanBlock span_block(const SpanArgs &a, int L) {
+    if constexpr (PREFIX) return prefix_block(a, L);
+    return window_block(a, L);
+}
+
+// First sequence and first row (of the R rows of a sequence and key head) of packed query tile t.
+__device__ __forceinline__ void packed_tile(const SpanArgs &a, int t, int *b0, int *r0) {
+    const int row_tiles = (a.R + a.rb - 1) / a.rb;  // 1 unless a sequence alone has more than kBM rows
+    *b0 = t / row_tiles * a.nb;
+    *r0 = t % row_tiles * a.rb;
+}
+
+__host__ __device__ inline int span_blocks(const SpanArgs &a, bool prefix) {
+    if (prefix) return (a.m_tiles + kTiles - 1) / kTiles * a.splits * a.Hkv;
+    const int per_block = a.pairing == kTwoRowTiles ? kTiles * kBM : kBM;
+    return (a.Nq + per_block - 1) / per_block * (a.pairing == kTwoHeads ? a.Hq / kTiles : a.Hq) * a.B;
+}
+
+// Persistent: the grid has at most one CTA per SM, each walking its blocks in turn, so the next block's
+// Q load and first S products overlap the previous block's last products and epilogue.  The K/V ring
+// and every barrier's phase run on across blocks.
+template <int D, int NSLOT, bool PREFIX>
+__global__ void __launch_bounds__(kThreads, 1)
+    win_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                   const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_ks,
+                   const __grid_constant__ CUtensorMap tmap_vs, const __grid_constant__ CUtensorMap tmap_o, SpanArgs a) {
+    using L = SpanSmem<D, NSLOT>;
+    constexpr int kPanels = L::kPanels;
+    constexpr uint32_t kTmemCols = 512;
+    // TMEM columns: S_A, S_B (P_X over the first kBN/2 columns of S_X), then O_A, O_B
+    constexpr uint32_t kColS = 0, kColO = kTiles * kBN;
+    static_assert(kColO + kTiles * D <= kTmemCols, "TMEM budget");
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *q_s = smem + L::kQOff;
+    uint8_t *slots = smem + L::kSlotOff;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
+    uint64_t *q_full = bars;                // block b's Q tiles landed (phase b)
+    uint64_t *q_empty = bars + 1;           // every S MMA of block b has completed (phase b)
+    uint64_t *slot_full = bars + 2;
+    uint64_t *slot_empty = slot_full + NSLOT;
+    uint64_t *s_full = slot_empty + NSLOT;  // [tile]: S_X of step g complete (phase g, steps counted across blocks)
+    uint64_t *p_full = s_full + kTiles;     // [tile]: P_X of step g written (and O_X corrected)
+    uint64_t *pv_done = p_full + kTiles;    // [tile]: PV_X of step g complete
+    uint64_t *o_free = pv_done + kTiles;    // [tile]: the epilogue has read O_X (phase = X's blocks with work)
+    uint64_t *final_bar = o_free + kTiles;  // every MMA of the CTA has completed
+    // The epilogue of a query tile writes O into the one staging buffer and stores it by TMA.  Within a
+    // block tile A uses the buffer before tile B, so every role can count the uses from the blocks:
+    uint64_t *stage_full = final_bar + 1;      // [tile]: the tile's four warps have written the buffer
+    uint64_t *stage_free = stage_full + kTiles;  // the last store has finished reading it (phase = use)
+    uint8_t *stage = smem + L::kStageOff;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kTmemHolderOff);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_work = span_blocks(a, PREFIX);
+
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int s = 0; s < NSLOT; ++s) {
+            mbar_init(&slot_full[s], 1);
+            mbar_init(&slot_empty[s], 1);
+        }
+        for (int x = 0; x < kTiles; ++x) {
+            mbar_init(&s_full[x], 1);
+            mbar_init(&p_full[x], 4);  // one arrive per softmax warp of tile x
+            mbar_init(&pv_done[x], 1);
+            mbar_init(&o_free[x], 4);
+        }
+        mbar_init(final_bar, 1);
+        for (int x = 0; x < kTiles; ++x) mbar_init(&stage_full[x], 4);
+        mbar_init(stage_free, 1);
+        fence_mbarrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            tma_prefetch_desc(&tmap_q);
+            tma_prefetch_desc(&tmap_k);
+            tma_prefetch_desc(&tmap_v);
+            int last_round[NSLOT];
+#pragma unroll
+            for (int s = 0; s < NSLOT; ++s) last_round[s] = -1;
+            int gidx = 0;  // K/V loads so far (ring position)
+            int nb = 0;    // blocks so far
+            bool ok = true;
+            for (int k = 0; ok && k * (int)gridDim.x < n_work; ++k) {
+                const int Lw = persistent_work_index(k, n_work);
+                if (Lw < 0) continue;
+                const SpanBlock w = span_block<PREFIX>(a, Lw);
+                // Q of this block goes after its first K and V tiles: its buffer frees only when the
+                // previous block's last S products complete, and K_0 / V_0 need not wait for that
+                const int q_at = nb == 0 ? 0 : 2;
+                for (int idx = 0; ok && idx <= 2 * w.span.n; ++idx) {
+                    if (idx == q_at) {
+                        if (nb > 0 && !(ok = mbar_wait(q_empty, (nb - 1) & 1, a.status, kSiteQEmpty))) break;
+                        const int n_q_tiles = w.n[1] > 0 ? kTiles : 1;
+                        if constexpr (PREFIX) {
+                            // rb rows of each of nb sequences, packed; the tile's rows behind them keep
+                            // whatever was there (no row's result depends on another row, and they are
+                            // not stored)
+                            mbar_arrive_expect_tx(q_full, n_q_tiles * a.rb * a.nb * D * 2);
+                            for (int x = 0; x < n_q_tiles; ++x) {
+                                int b0, r0;
+                                packed_tile(a, w.yq[x], &b0, &r0);
+#pragma unroll
+                                for (int p = 0; p < kPanels; ++p)
+                                    tma_load_4d(q_s + x * L::kQBytes + p * (kBM * 128), &tmap_q, q_full, p * 64, r0,
+                                                w.kv_bh, b0);
+                            }
+                        } else {
+                            mbar_arrive_expect_tx(q_full, n_q_tiles * L::kQBytes);
+                            for (int x = 0; x < n_q_tiles; ++x)
+#pragma unroll
+                                for (int p = 0; p < kPanels; ++p)
+                                    tma_load_3d(q_s + x * L::kQBytes + p * (kBM * 128), &tmap_q, q_full, p * 64,
+                                                w.yq[x], w.zq[x]);
+                        }
+                    }
+                    if (idx == 2 * w.span.n) break;
+                    const int g = gidx + idx;
+                    const int slot = g % NSLOT, round = g / NSLOT;
+                    if (!(ok = mbar_wait(&slot_empty[slot], (round & 1) ^ 1, a.status, kSiteSlotEmpty))) break;
+                    uint8_t *dst = slots + slot * L::kSlotBytes;
+                    // a sink tile reads keys past the last sink as zeros (its maps end there): whatever the
+                    // rows between the sinks and the window hold cannot reach a product
+                    const int j = idx >> 1;
+                    const bool sink = j < w.span.n_sink;
+                    const CUtensorMap *map = (idx & 1) ? (sink ? &tmap_vs : &tmap_v) : (sink ? &tmap_ks : &tmap_k);
+                    mbar_arrive_expect_tx(&slot_full[slot], L::kSlotBytes);
+#pragma unroll
+                    for (int p = 0; p < kPanels; ++p)
+                        tma_load_3d(dst + p * (kBN * 128), map, &slot_full[slot], p * 64,
+                                    w.y_off + w.span.key0(j, kBN), w.kv_bh);
+#pragma unroll
+                    for (int s = 0; s < NSLOT; ++s)
+                        if (s == slot) last_round[s] = round;
+                }
+                gidx += 2 * w.span.n;
+                ++nb;
+            }
+            // Drain: never leave the CTA with a TMA write still in flight.
+#pragma unroll
+            for (int s = 0; s < NSLOT; ++s)
+                if (last_round[s] >= 0) mbar_wait(&slot_full[s], last_round[s] & 1, a.status, kSiteDrain);
+            if (nb > 0) mbar_wait(q_full, (nb - 1) & 1, a.status, kSiteDrain);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ the tcgen05 issuer
+        // The whole warp runs the loop (operands stay warp-uniform); one elected lane issues the MMAs
+        // and the commits that track them.  Per block the order is
+        //   S_A(0) S_B(0) | PV_A(j) S_A(j+1) PV_B(j) S_B(j+1) | ...
+        constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, kBN, false, false);
+        constexpr uint32_t idesc_o = idesc_bf16_f32(kBM, D, false, true);
+        const uint64_t q_desc = sdesc_sw128(smem_u32(q_s), 16, 1024);
+        const uint32_t slot_addr = smem_u32(slots);
+        const bool leader = elect_one();
+        bool ok = true;
+        int gidx = 0;                 // ring position of this block's K_0
+        int step0[kTiles] = {0, 0};   // steps of tile x before this block
+        int blocks[kTiles] = {0, 0};  // earlier blocks in which tile x had work (epilogues)
+        int nb = 0;
+        for (int k = 0; ok && k * (int)gridDim.x < n_work; ++k) {
+            const int Lw = persistent_work_index(k, n_work);
+            if (Lw < 0) continue;
+            const SpanBlock w = span_block<PREFIX>(a, Lw);
+            if (!(ok = warp_wait(q_full, nb & 1, a.status, kSiteQ))) break;
+            tc_fence_after();
+            // S_X(j) = Q_X K_j^T into S_X
+            auto issue_s = [&](int x, int j) {
+                if (!ok || !w.reads(x, j)) return;
+                const int g = gidx + 2 * j;
+                const int slot = g % NSLOT;
+                if (!(ok = warp_wait(&slot_full[slot], (g / NSLOT) & 1, a.status, kSiteSlotFull))) return;
+                // S_X overwrites P_X of the step before (this block's or the previous one's)
+                const int st = step0[x] + w.step_of(x, j);
+                if (st >= 1 && !(ok = warp_wait(&pv_done[x], (st - 1) & 1, a.status, kSitePV))) return;
+                tc_fence_after();
+                const uint64_t k_desc = sdesc_sw128(slot_addr + slot * L::kSlotBytes, 16, 1024);
+                if (leader) {
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t off = (ks >> 2) * (kBM * 128) + (ks & 3) * 32;
+                        mma_ss(tmem + kColS + x * kBN, sdesc_add(q_desc, x * L::kQBytes + off),
+                               sdesc_add(k_desc, (ks >> 2) * (kBN * 128) + (ks & 3) * 32), idesc_s, ks > 0);
+                    }
+                    mma_commit(&s_full[x]);
+                }
+                __syncwarp();
+            };
+            // O_X += P_X(j) V_j, P_X from TMEM
+            auto issue_pv = [&](int x, int j) {
+                if (!ok || !w.reads(x, j)) return;
+                const int g = gidx + 2 * j + 1;
+                const int slot = g % NSLOT;
+                if (!(ok = warp_wait(&slot_full[slot], (g / NSLOT) & 1, a.status, kSiteSlotFull))) return;
+                if (!(ok = warp_wait(&p_full[x], (step0[x] + w.step_of(x, j)) & 1, a.status, kSitePFull))) return;
+                // the first PV of a block overwrites O_X, which the previous block's epilogue reads
+                const bool first = w.step_of(x, j) == 0;
+                if (first && blocks[x] >= 1 && !(ok = warp_wait(&o_free[x], (blocks[x] - 1) & 1, a.status, kSiteOFree)))
+                    return;
+                tc_fence_after();
+                const uint64_t v_desc = sdesc_sw128(slot_addr + slot * L::kSlotBytes, kBN * 128, 1024);
+                if (leader) {
+#pragma unroll
+                    for (int kk = 0; kk < kBN / 16; ++kk)
+                        mma_ts(tmem + kColO + x * D, tmem + kColS + x * kBN + kk * 8, sdesc_add(v_desc, kk * 2048),
+                               idesc_o, (!first || kk > 0));
+                    mma_commit(&pv_done[x]);
+                }
+                __syncwarp();
+            };
+            // a slot is released by a commit after the last MMA that reads it (a commit tracks every
+            // earlier MMA of this thread); the same goes for the Q buffer after the block's last S
+            auto commit_to = [&](uint64_t *bar) {
+                if (leader) mma_commit(bar);
+                __syncwarp();
+            };
+            issue_s(0, 0);
+            issue_s(1, 0);
+            if (ok && w.span.n == 1) commit_to(q_empty);
+            if (ok) commit_to(&slot_empty[gidx % NSLOT]);  // K_0
+            for (int j = 0; ok && j < w.span.n; ++j) {
+                issue_pv(0, j);
+                issue_s(0, j + 1);
+                issue_pv(1, j);
+                if (ok) commit_to(&slot_empty[(gidx + 2 * j + 1) % NSLOT]);  // V_j
+                issue_s(1, j + 1);
+                if (ok && j + 2 == w.span.n) commit_to(q_empty);  // the block's last S products
+                if (ok && j + 1 < w.span.n) commit_to(&slot_empty[(gidx + 2 * j + 2) % NSLOT]);  // K_{j+1}
+            }
+#pragma unroll
+            for (int x = 0; x < kTiles; ++x) {
+                step0[x] += w.n[x];
+                blocks[x] += w.n[x] > 0;
+            }
+            gidx += 2 * w.span.n;
+            ++nb;
+        }
+        // every MMA complete: TMEM may be released
+        if (leader) mma_commit(final_bar);
+        __syncwarp();
+        warp_wait(final_bar, 0, a.status, kSiteFinal);
+    } else {
+        // ------------------------------------------------------------ softmax / correction / epilogue
+        const int x = (warp - kFirstSoftmaxWarp) >> 2;  // query tile of this warpgroup
+        const int quarter = warp & 3;                   // TMEM lanes [32*quarter, 32*quarter + 32)
+        const int r = quarter * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        const uint32_t s_col = kColS + x * kBN, o_col = kColO + x * D;
+        const float c = a.scale_log2;
+        bool ok = true;
+        int step0 = 0;     // steps of this tile before the current block
+        int uses = 0;      // uses of the staging buffer (by both tiles) before the current block
+        int blocks_x = 0;  // epilogues of this tile so far (phase of stage_full[x])
+        for (int k = 0; ok && k * (int)gridDim.x < n_work; ++k) {
+            const int Lw = persistent_work_index(k, n_work);
+            if (Lw < 0) continue;
+            const SpanBlock w = span_block<PREFIX>(a, Lw);
+            // this tile's fields (x is not a constant here: indexing the arrays would put them in local memory)
+            const int n = x == 0 ? w.n[0] : w.n[1];
+            const int from = x == 0 ? w.from[0] : w.from[1];
+            const int yq = x == 0 ? w.yq[0] : w.yq[1], zq = x == 0 ? w.zq[0] : w.zq[1];
+            const int pos0 = x == 0 ? w.p0[0] : w.p0[1];
+            const int pos = pos0 + r;  // windowed: this row's position
+            float m = -INFINITY, l = 0.f;  // running max (log2 units) and sum
+            for (int step = 0; step < n; ++step) {
+                // this S_X was issued after the step before's PV_X completed, so O_X and the P columns are free as well
+                ok = mbar_wait(&s_full[x], (step0 + step) & 1, a.status, kSiteSFull);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                tc_fence_after();
+                uint32_t raw[kBN];
+#pragma unroll
+                for (int ch = 0; ch < kBN / 32; ++ch) tmem_ld32(tmem + lane_base + s_col + ch * 32, raw + ch * 32);
+                tmem_wait_ld();
+                const int key0 = w.y_off + w.span.key0(step < w.span.n_sink ? step : from + step - w.span.n_sink, kBN);
+                const int window = w.span.window_in(step, a.window);
+                const bool need_mask = PREFIX ? key0 + kBN > a.Nk
+                                              : !all_seen(pos0, pos0 + kBM - 1, key0, key0 + kBN - 1, window, a.sinks);
+                if (need_mask) {
+#pragma unroll
+                    for (int h = 0; h < kBN / 32; ++h) {
+                        const uint32_t seen = PREFIX ? low_bits(a.Nk - key0 - 32 * h)
+                                                     : seen_keys(pos, key0 + 32 * h, window, a.sinks);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(seen & (1u << e))) raw[32 * h + e] = 0xff800000u;  // -inf
+                    }
+                }
+                // row max of the raw scores (scale > 0 commutes with max): four chains of three-input maxima
+                float mx[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) mx[u] = __uint_as_float(raw[u]);
+#pragma unroll
+                for (int i = 4; i + 8 <= kBN; i += 8)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        mx[u] = fmax3(mx[u], __uint_as_float(raw[i + 2 * u]), __uint_as_float(raw[i + 2 * u + 1]));
+#pragma unroll
+                for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __uint_as_float(raw[kBN - 4 + u]));
+                const float mt = c * fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                const float m_new = fmaxf(m, mt);
+                // Lazy correction: keep the stale max unless the row max grew by > 8 (factor 256).
+                const bool need = m_new > m + 8.f;
+                const float m_use = need ? m_new : m;
+                const float m_base = (m_use == -INFINITY) ? 0.f : m_use;
+                const float alpha = need ? ex2_approx(m - m_base) : 1.f;
+                // P = 2^(s c - m) as bf16 pairs over the first kBN/2 columns of S_X, 16 columns per store;
+                // the scaling FMA and the row sum run on fp32 pairs
+                const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-m_base, -m_base);
+                uint64_t acc2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+                for (int h = 0; h < kBN / 32; ++h) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint64_t y2 = f2_fma(f2_pack(__uint_as_float(raw[32 * h + 2 * i]),
+                                                           __uint_as_float(raw[32 * h + 2 * i + 1])), c2, nm2);
+                        float y0, y1;
+                        f2_unpack(y2, y0, y1);
+                        const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
+                        acc2[i & 1] = f2_add(acc2[i & 1], f2_pack(p0, p1));
+                        pk[i] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st16(tmem + lane_base + s_col + h * 16, pk);
+                }
+                float r0, r1, r2, r3;
+                f2_unpack(acc2[0], r0, r1);
+                f2_unpack(acc2[1], r2, r3);
+                l = l * alpha + ((r0 + r1) + (r2 + r3));
+                m = m_use;
+                if (step >= 1 && __any_sync(0xffffffffu, need)) {
+                    uint32_t ov[32];
+#pragma unroll
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        tmem_ld32(tmem + lane_base + o_col + ch * 32, ov);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                        tmem_st32(tmem + lane_base + o_col + ch * 32, ov);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(&p_full[x]);
+            }
+            // the staging buffer's use number of this tile's epilogue in this block (tile A's before tile B's)
+            const int use = uses + (x == 1 && w.n[0] > 0);
+            uses += (w.n[0] > 0) + (w.n[1] > 0);
+            if (!ok || n == 0) continue;
+            // the block's last PV_X has completed: O_X is final
+            step0 += n;
+            ok = mbar_wait(&pv_done[x], (step0 - 1) & 1, a.status, kSiteFinal);
+            // the previous use's TMA store has finished reading the staging buffer
+            if (!PREFIX && ok && use >= 1) ok = mbar_wait(stage_free, (use - 1) & 1, a.status, kSiteStage);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            tc_fence_after();
+            uint32_t ov[32];
+            if constexpr (PREFIX) {
+                // this chunk's partial of the row: O unnormalised, m (log2 units) and l
+                int b0, r0;
+                packed_tile(a, yq, &b0, &r0);
+                const int b = b0 + r / a.rb, rr = r0 + r % a.rb;
+                const bool valid = r < a.rb * a.nb && b < a.B && rr < a.R;
+                const size_t slot = (((size_t)b * a.Hkv + w.kv_bh) * a.R + rr) * a.slots + zq;
+#pragma unroll
+                for (int ch = 0; ch < D / 32; ++ch) {
+                    tmem_ld32(tmem + lane_base + o_col + ch * 32, ov);
+                    tmem_wait_ld();
+                    if (ch == D / 32 - 1) {
+                        tc_fence_before();
+                        warp_arrive(&o_free[x]);
+                    }
+                    if (valid) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.part_o + slot * D + ch * 32);
+#pragma unroll
+                        for (int v4 = 0; v4 < 8; ++v4)
+                            dst[v4] = make_uint4(ov[4 * v4], ov[4 * v4 + 1], ov[4 * v4 + 2], ov[4 * v4 + 3]);
+                    }
+                }
+                if (valid) a.part_ml[slot] = make_float2(m, l);
+                continue;
+            }
+            const float inv_l = 1.f / l;
+            // O / l as bf16 into the staging buffer: 128-byte-swizzled panels of 64 columns, row r of panel
+            // p at p * 16 KB + r * 128, its 16-byte chunk k at k ^ (r % 8) (conflict-free across the lanes)
+#pragma unroll
+            for (int ch = 0; ch < D / 32; ++ch) {
+                tmem_ld32(tmem + lane_base + o_col + ch * 32, ov);
+                tmem_wait_ld();
+                if (ch == D / 32 - 1) {
+                    // every read of O_X is done: the next block's first PV_X may overwrite it
+                    tc_fence_before();
+                    warp_arrive(&o_free[x]);
+                }
+                uint8_t *prow = stage + (ch >> 1) * (kBM * 128) + r * 128;
+#pragma unroll
+                for (int v4 = 0; v4 < 4; ++v4)
+                    st_shared_v4(prow + ((((ch & 1) * 4 + v4) ^ (r & 7)) << 4),
+                                 pack_bf16x2(__uint_as_float(ov[v4 * 8 + 0]) * inv_l, __uint_as_float(ov[v4 * 8 + 1]) * inv_l),
+                                 pack_bf16x2(__uint_as_float(ov[v4 * 8 + 2]) * inv_l, __uint_as_float(ov[v4 * 8 + 3]) * inv_l),
+                                 pack_bf16x2(__uint_as_float(ov[v4 * 8 + 4]) * inv_l, __uint_as_float(ov[v4 * 8 + 5]) * inv_l),
+                                 pack_bf16x2(__uint_as_float(ov[v4 * 8 + 6]) * inv_l, __uint_as_float(ov[v4 * 8 + 7]) * inv_l));
+            }
+            fence_proxy_async_smem();  // the staged tile is read by the TMA (async proxy)
+            warp_arrive(&stage_full[x]);
+            if (yq + r < a.Nq)
+                a.lse[(size_t)zq * a.Nq + yq + r] = (m + __log2f(l)) * 0.69314718055994531f;
+            if (quarter == kFirstSoftmaxWarp % 4 && lane == 0) {
+                // one thread of the tile stores the staged panels (rows past N and columns past the caller's
+                // D are clipped by the tensor map) and frees the buffer once the stores have read it
+                if (mbar_wait(&stage_full[x], blocks_x & 1, a.status, kSiteStage)) {
+#pragma unroll
+                    for (int p = 0; p < kPanels; ++p)
+                        if (p * 64 < a.D) tma_store_3d(&tmap_o, stage + p * (kBM * 128), p * 64, yq, zq);
+                    tma_store_commit();
+                    tma_store_wait_read();
+                    mbar_arrive(stage_free);
+                } else {
+                    ok = false;
+                }
+            }
+            ++blocks_x;
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D, int NSLOT, bool PREFIX>
+cudaError_t launch_spec(const SpanArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                        const CUtensorMap &tks, const CUtensorMap &tvs, const CUtensorMap &to, cudaStream_t s) {
+    using L = SpanSmem<D, NSLOT>;
+    static_assert(L::kAlloc <= 232448, "shared memory budget");
+    auto kern = win_fwd_kernel<D, NSLOT, PREFIX>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+    if (e != cudaSuccess) return e;
+    const int n_work = span_blocks(a, PREFIX);
+    const int sms = a.num_sms > 0 ? a.num_sms : kNumSms;
+    kern<<<n_work < sms ? n_work : sms, kThreads, L::kAlloc, s>>>(tq, tk, tv, tks, tvs, to, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_win_fwd(const SpanArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                           const CUtensorMap &tks, const CUtensorMap &tvs, const CUtensorMap &to, cudaStream_t s) {
+    const bool prefix = a.part_o != nullptr;
+    switch (kernel_head_dim(a.D)) {
+        case 64:
+            return prefix ? launch_spec<64, 4, true>(a, tq, tk, tv, tks, tvs, to, s)
+                          : launch_spec<64, 4, false>(a, tq, tk, tv, tks, tvs, to, s);
+        case 128:
+            return prefix ? launch_spec<128, 4, true>(a, tq, tk, tv, tks, tvs, to, s)
+                          : launch_spec<128, 4, false>(a, tq, tk, tv, tks, tvs, to, s);
+        default: return launch_win_fwd_wide(a, tq, tk, tv, tks, tvs, s);
+    }
+}
+
+}  // namespace fa

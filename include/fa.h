@@ -67,7 +67,7 @@ enum fa_dtype {
 enum fa_status {
     FA_OK = 0,
     FA_ERR_NULL = -1,        /* a required pointer is NULL                              */
-    FA_ERR_SHAPE = -2,       /* B, H or N < 1, or B*H*N*D overflows the index range      */
+    FA_ERR_SHAPE = -2,       /* a size < 1, sizes past the index range or that do not fit together */
     FA_ERR_HEAD_DIM = -3,    /* D not supported for this dtype / pass (see below)        */
     FA_ERR_DTYPE = -4,       /* unknown dtype / grad_dtype, or an unsupported pairing   */
     FA_ERR_ALIGN = -5,       /* a pointer is not 16-byte aligned                         */
@@ -222,6 +222,83 @@ FA_API int fa_decode_workspace_bytes(int B, int H, int n_q, int N, int D, size_t
 FA_API int fa_decode_noalloc(const void *q, const void *k, const void *v, void *o, float *lse,
                              int B, int H, int n_q, int N, int D, float scale, int causal,
                              void *stream);
+
+/*
+ * Windowed attention.  Beside the calls above: grouped heads (Hq query heads, Hkv key heads, Hq a multiple of
+ * Hkv; query head h reads key head h / (Hq / Hkv)), fewer queries than keys, and a mask that keeps a window of
+ * the latest keys and the first few.  Query row i of Nq sits at position p = i + Nk - Nq (Nq <= Nk: the last Nq
+ * of Nk positions) and sees key j iff
+ *     j <= p  and  (j < sinks  or  j > p - window),          window >= 1, sinks >= 0.
+ * Every row sees its own key.  window >= Nk is plain causal attention.
+ *   q, o, dO, dq: [B, Hq, Nq, D];  lse, delta: [B, Hq, Nq] fp32;  dk, dv: [B, Hkv, Nk, D].
+ *   k, v: [B, Hkv, kv_rows, D], of which the first Nk rows of every head are keys (kv_rows >= Nk: a cache with
+ *   room behind them; the backward takes kv_rows = Nk).
+ * Keys that no query row sees (rows Nk and up, and for Nq < Nk those between the sinks and the first window) may
+ * hold anything in the forward; every other element must be finite (a masked weight is an exact 0, and 0 times a
+ * non-finite value is NaN).
+ * Supported: dtype FA_BF16, D a multiple of 8 in [8, 256]; Nk <= 2^29; scale finite and > 0 (FA_ERR_SCALE).
+ * Sizes outside these, Nq > Nk, window < 1, sinks < 0: FA_ERR_SHAPE.
+ */
+
+/* fa_window_forward -- O = softmax over the visible keys, and LSE. */
+FA_API int fa_window_forward(const void *q, const void *k, const void *v, void *o, float *lse,
+                             int B, int Hq, int Hkv, int Nq, int Nk, int kv_rows, int D,
+                             int window, int sinks, float scale, int dtype, void *stream);
+
+/* fa_window_backward_dq -- delta = rowsum(dO * O) (written) and dQ, as fa_backward_dq. */
+FA_API int fa_window_backward_dq(const void *q, const void *k, const void *v, const void *o, const void *dO,
+                                 const float *lse, float *delta, void *dq,
+                                 int B, int Hq, int Hkv, int Nq, int Nk, int D, int window, int sinks,
+                                 float scale, int dtype, int grad_dtype, void *stream);
+
+/*
+ * fa_window_backward_dkdv -- dK and dV, as fa_backward_dkdv, summed over the query heads of each key head (in a
+ * fixed order: equal inputs give equal bits).  Keys that no row sees get zeros.  workspace: device memory of at
+ * least fa_window_backward_workspace_bytes(...) bytes, 16-byte aligned; it may be NULL when that is 0.  Two calls
+ * that run concurrently must not share it.
+ */
+FA_API int fa_window_backward_dkdv(const void *q, const void *k, const void *v, const void *dO, const float *lse,
+                                   const float *delta, void *dk, void *dv,
+                                   int B, int Hq, int Hkv, int Nq, int Nk, int D, int window, int sinks,
+                                   float scale, int dtype, int grad_dtype,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace fa_window_backward_dkdv needs on the current device (may be 0). */
+FA_API int fa_window_backward_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int D, int window, int sinks,
+                                              size_t *bytes);
+
+/*
+ * fa_window_decode -- windowed attention of the n_q <= 16 newest rows of each sequence against its cache.
+ *   q, o: [B, Hq, n_q, D]; lse: [B, Hq, n_q] fp32; k, v: [B, Hkv, N, D] (N rows of room per sequence), bf16.
+ *   lens: device array of B ints, the keys each sequence holds (its new rows' included), values outside [0, N]
+ *   are taken as the nearer end; NULL: every sequence holds N.  Row i sits at position lens[b] - n_q + i and sees
+ *   what the mask above gives; a row that sees nothing (a position below 0) gets O = 0 and LSE = -inf.  Cache
+ *   rows from lens[b] on may hold anything.
+ *   D in {64, 128, 256}; n_q <= N.  Other conditions as for windowed attention.
+ *   workspace: as fa_decode's, of fa_window_decode_workspace_bytes(...) bytes (NULL when that is 0).
+ * Launches one kernel, and a second when the keys of a sequence are split over CTAs.
+ */
+FA_API int fa_window_decode(const void *q, const void *k, const void *v, const int *lens, void *o, float *lse,
+                            int B, int Hq, int Hkv, int n_q, int N, int D, int window, int sinks, float scale,
+                            void *workspace, size_t workspace_bytes, void *stream);
+FA_API int fa_window_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q, int N, int D, int window, int sinks,
+                                            size_t *bytes);
+
+/*
+ * fa_prefix_decode -- decode of a batch whose sequences all begin with the same P keys, which are held once and
+ * read once for the whole batch.
+ *   k_prefix, v_prefix: [Hkv, P, D]; q, o, lse, lens and k, v (the sequences' own caches behind the prefix) as for
+ *   fa_window_decode.  Row i of sequence b sees every prefix key, and key j of its own cache iff
+ *   j <= lens[b] - n_q + i.  lens[b] may be 0.
+ *   P >= 1, N >= 1, D in {64, 128, 256}, 1 <= n_q <= 16, scale finite and > 0.
+ *   workspace: fa_prefix_decode_workspace_bytes(...) bytes, 16-byte aligned; two calls that run concurrently must
+ *   not share it.
+ */
+FA_API int fa_prefix_decode(const void *q, const void *k_prefix, const void *v_prefix, const void *k, const void *v,
+                            const int *lens, void *o, float *lse,
+                            int B, int Hq, int Hkv, int n_q, int P, int N, int D, float scale,
+                            void *workspace, size_t workspace_bytes, void *stream);
+FA_API int fa_prefix_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q, int P, int N, int D, size_t *bytes);
 
 /* Static description of a status code (never NULL). */
 FA_API const char *fa_status_string(int status);

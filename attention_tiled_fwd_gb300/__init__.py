@@ -203,20 +203,40 @@ def fa_decode_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torc
     return o, lse
 
 
-def _bf16(t: torch.Tensor, name: str, shape) -> None:
+# The calls below run in 10-30 us on the device at their smallest, so the binding's own time counts: one comparison
+# per tensor when all is well (_bad says what is not), the current stream's handle without a Stream object, and no
+# size query when the caller brings the workspace.
+def _bf16(t: torch.Tensor, name: str, shape, device: int) -> None:
     """t is a contiguous bf16 CUDA tensor of this shape on the current device."""
-    _tensor(t, name, torch.bfloat16, shape)
+    if t.shape != shape or t.dtype is not torch.bfloat16 or t.get_device() != device or not t.is_contiguous():
+        _bad(t, name, torch.bfloat16, shape)
 
 
-def _tensor(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> None:
+def _tensor(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: int) -> None:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        _bad(t, name, dtype, shape)
+
+
+def _bad(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> None:
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
+
+
+def _device() -> int:
+    return torch.cuda.current_device()
+
+
+def _stream_handle(stream: Optional[torch.cuda.Stream], device: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"stream must belong to the current CUDA device, got {stream.device}")
+    return stream.cuda_stream
 
 
 def _grouped(q: torch.Tensor, k: torch.Tensor):
@@ -234,12 +254,12 @@ def _c_int(x: int) -> int:
     return max(-1, min(int(x), (1 << 31) - 1))
 
 
-def _empty(shape, dtype: torch.dtype, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+def _empty(like: torch.Tensor, shape, dtype: torch.dtype, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
     """Memory of the stream that the call runs on, so that the allocator hands it on in that stream's order."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device="cuda")
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device="cuda")
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _size_query(name: str, *sizes: int) -> int:
@@ -249,13 +269,18 @@ def _size_query(name: str, *sizes: int) -> int:
     return int(out.value)
 
 
-def _workspace(workspace: Optional[torch.Tensor], need: int, stream: Optional[torch.cuda.Stream]):
-    """(pointer, bytes) of the caller's workspace or of a new one; the tensor is returned to keep it alive."""
+def _workspace(workspace: Optional[torch.Tensor], like: torch.Tensor, stream, device: int, query: str, *sizes: int):
+    """The caller's workspace, or a new one of the size that the library asks for; None when it asks for nothing."""
     if workspace is None:
-        workspace = _empty((max(need, 16),), torch.uint8, stream)
-    elif not workspace.is_cuda or workspace.device.index != torch.cuda.current_device() or not workspace.is_contiguous():
+        need = _size_query(query, *sizes)
+        return _empty(like, (need,), torch.uint8, stream) if need else None
+    if workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace
+
+
+def _nbytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def fa_window_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, sinks: int = 0,
@@ -268,14 +293,21 @@ def fa_window_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window:
     Returns (o, lse)."""
     B, Hq, Nq, D, Hkv, rows = _grouped(q, k)
     Nk = rows if kv_len is None else int(kv_len)
-    for t, n, h, r in ((q, "q", Hq, Nq), (k, "k", Hkv, rows), (v, "v", Hkv, rows)):
-        _bf16(t, n, (B, h, r, D))
-    o = _empty(q.shape, q.dtype, stream) if o is None else o
-    lse = _empty((B, Hq, Nq), torch.float32, stream) if lse is None else lse
-    _bf16(o, "o", q.shape)
-    _tensor(lse, "lse", torch.float32, (B, Hq, Nq))
-    rc = _native.load().fa_window_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, Nk, rows, D,
-                                          _c_int(window), _c_int(sinks), _scale(scale, D), FA_BF16, _stream_ptr(stream))
+    dev = _device()
+    _bf16(q, "q", (B, Hq, Nq, D), dev)
+    _bf16(k, "k", (B, Hkv, rows, D), dev)
+    _bf16(v, "v", (B, Hkv, rows, D), dev)
+    if o is None:
+        o = _empty(q, q.shape, q.dtype, stream)
+    else:
+        _bf16(o, "o", q.shape, dev)
+    if lse is None:
+        lse = _empty(q, (B, Hq, Nq), torch.float32, stream)
+    else:
+        _tensor(lse, "lse", torch.float32, (B, Hq, Nq), dev)
+    rc = _native.load().fa_window_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq,
+                                          Hkv, Nq, Nk, rows, D, _c_int(window), _c_int(sinks), _scale(scale, D),
+                                          FA_BF16, _stream_handle(stream, dev))
     _native.check(rc, "fa_window_forward")
     return o, lse
 
@@ -285,17 +317,23 @@ def fa_window_backward_dq(q, k, v, o, dO, lse, window: int, sinks: int = 0, scal
                           delta: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
     """delta = rowsum(dO * O) and dQ of windowed attention (fa_window_backward_dq).  Returns (dq, delta)."""
     B, Hq, Nq, D, Hkv, Nk = _grouped(q, k)
-    for t, n, h, r in ((q, "q", Hq, Nq), (k, "k", Hkv, Nk), (v, "v", Hkv, Nk), (o, "o", Hq, Nq), (dO, "dO", Hq, Nq)):
-        _bf16(t, n, (B, h, r, D))
-    _tensor(lse, "lse", torch.float32, (B, Hq, Nq))
-    dq = _empty(q.shape, grad_dtype, stream) if dq is None else dq
-    delta = _empty((B, Hq, Nq), torch.float32, stream) if delta is None else delta
+    dev = _device()
+    rows, keys = (B, Hq, Nq, D), (B, Hkv, Nk, D)
+    for t, n, shape in ((q, "q", rows), (k, "k", keys), (v, "v", keys), (o, "o", rows), (dO, "dO", rows)):
+        _bf16(t, n, shape, dev)
+    _tensor(lse, "lse", torch.float32, (B, Hq, Nq), dev)
+    if dq is None:
+        dq = _empty(q, q.shape, grad_dtype, stream)
     code = _dtype_code(dq)
-    _tensor(dq, "dq", dq.dtype, q.shape)
-    _tensor(delta, "delta", torch.float32, (B, Hq, Nq))
-    rc = _native.load().fa_window_backward_dq(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dO), _ptr(lse), _ptr(delta),
-                                              _ptr(dq), B, Hq, Hkv, Nq, Nk, D, _c_int(window), _c_int(sinks),
-                                              _scale(scale, D), FA_BF16, code, _stream_ptr(stream))
+    _tensor(dq, "dq", dq.dtype, q.shape, dev)
+    if delta is None:
+        delta = _empty(q, (B, Hq, Nq), torch.float32, stream)
+    else:
+        _tensor(delta, "delta", torch.float32, (B, Hq, Nq), dev)
+    rc = _native.load().fa_window_backward_dq(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dO.data_ptr(),
+                                              lse.data_ptr(), delta.data_ptr(), dq.data_ptr(), B, Hq, Hkv, Nq, Nk, D,
+                                              _c_int(window), _c_int(sinks), _scale(scale, D), FA_BF16, code,
+                                              _stream_handle(stream, dev))
     _native.check(rc, "fa_window_backward_dq")
     return dq, delta
 
@@ -316,36 +354,48 @@ def fa_window_backward_dkdv(q, k, v, dO, lse, delta, window: int, sinks: int = 0
     A workspace of fa_window_backward_workspace_bytes(...) bytes is allocated here when the caller passes none.
     Returns (dk, dv)."""
     B, Hq, Nq, D, Hkv, Nk = _grouped(q, k)
-    for t, n, h, r in ((q, "q", Hq, Nq), (k, "k", Hkv, Nk), (v, "v", Hkv, Nk), (dO, "dO", Hq, Nq)):
-        _bf16(t, n, (B, h, r, D))
-    _tensor(lse, "lse", torch.float32, (B, Hq, Nq))
-    _tensor(delta, "delta", torch.float32, (B, Hq, Nq))
-    dk = _empty(k.shape, grad_dtype, stream) if dk is None else dk
-    dv = _empty(k.shape, grad_dtype, stream) if dv is None else dv
+    dev = _device()
+    rows, keys = (B, Hq, Nq, D), (B, Hkv, Nk, D)
+    for t, n, shape in ((q, "q", rows), (k, "k", keys), (v, "v", keys), (dO, "dO", rows)):
+        _bf16(t, n, shape, dev)
+    _tensor(lse, "lse", torch.float32, (B, Hq, Nq), dev)
+    _tensor(delta, "delta", torch.float32, (B, Hq, Nq), dev)
+    if dk is None:
+        dk = _empty(k, k.shape, grad_dtype, stream)
+    if dv is None:
+        dv = _empty(k, k.shape, grad_dtype, stream)
     code = _dtype_code(dk)
-    _tensor(dk, "dk", dk.dtype, k.shape)
-    _tensor(dv, "dv", dk.dtype, k.shape)
-    need = fa_window_backward_workspace_bytes(B, Hq, Hkv, Nq, Nk, D, _c_int(window), _c_int(sinks))
-    workspace, nbytes = _workspace(workspace, need, stream)
-    rc = _native.load().fa_window_backward_dkdv(_ptr(q), _ptr(k), _ptr(v), _ptr(dO), _ptr(lse), _ptr(delta), _ptr(dk),
-                                                _ptr(dv), B, Hq, Hkv, Nq, Nk, D, _c_int(window), _c_int(sinks),
-                                                _scale(scale, D), FA_BF16, code, _ptr(workspace), nbytes,
-                                                _stream_ptr(stream))
+    _tensor(dk, "dk", dk.dtype, k.shape, dev)
+    _tensor(dv, "dv", dk.dtype, k.shape, dev)
+    window, sinks = _c_int(window), _c_int(sinks)
+    workspace = _workspace(workspace, q, stream, dev, "fa_window_backward_workspace_bytes", B, Hq, Hkv, Nq, Nk, D, window,
+                           sinks)
+    rc = _native.load().fa_window_backward_dkdv(q.data_ptr(), k.data_ptr(), v.data_ptr(), dO.data_ptr(), lse.data_ptr(),
+                                                delta.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Nq, Nk, D,
+                                                window, sinks, _scale(scale, D), FA_BF16, code, _ptr(workspace),
+                                                _nbytes(workspace), _stream_handle(stream, dev))
     _native.check(rc, "fa_window_backward_dkdv")
     return dk, dv
 
 
 def _rows_and_cache(q, k, v, lens, o, lse, stream):
+    """(B, Hq, Hkv, n_q), N, D, the outputs and the device of a decode call, its tensors checked."""
     B, Hq, n_q, D, Hkv, N = _grouped(q, k)
-    for t, n, h, r in ((q, "q", Hq, n_q), (k, "k", Hkv, N), (v, "v", Hkv, N)):
-        _bf16(t, n, (B, h, r, D))
+    dev = _device()
+    _bf16(q, "q", (B, Hq, n_q, D), dev)
+    _bf16(k, "k", (B, Hkv, N, D), dev)
+    _bf16(v, "v", (B, Hkv, N, D), dev)
     if lens is not None:
-        _tensor(lens, "lens", torch.int32, (B,))
-    o = _empty(q.shape, q.dtype, stream) if o is None else o
-    lse = _empty((B, Hq, n_q), torch.float32, stream) if lse is None else lse
-    _bf16(o, "o", q.shape)
-    _tensor(lse, "lse", torch.float32, (B, Hq, n_q))
-    return (B, Hq, Hkv, n_q), N, D, o, lse
+        _tensor(lens, "lens", torch.int32, (B,), dev)
+    if o is None:
+        o = _empty(q, q.shape, q.dtype, stream)
+    else:
+        _bf16(o, "o", q.shape, dev)
+    if lse is None:
+        lse = _empty(q, (B, Hq, n_q), torch.float32, stream)
+    else:
+        _tensor(lse, "lse", torch.float32, (B, Hq, n_q), dev)
+    return (B, Hq, Hkv, n_q), N, D, o, lse, dev
 
 
 def fa_window_decode_workspace_bytes(B: int, Hq: int, Hkv: int, n_q: int, N: int, D: int, window: int,
@@ -361,12 +411,12 @@ def fa_window_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: 
                      workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
     """The n_q <= 16 newest rows q [B, Hq, n_q, D] of each sequence against its cache k, v [B, Hkv, N, D], windowed
     (fa_window_decode).  lens: int32 CUDA tensor [B], the keys each sequence holds (default N).  Returns (o, lse)."""
-    heads, N, D, o, lse = _rows_and_cache(q, k, v, lens, o, lse, stream)
-    need = fa_window_decode_workspace_bytes(*heads, N, D, _c_int(window), _c_int(sinks))
-    workspace, nbytes = _workspace(workspace, need, stream)
-    rc = _native.load().fa_window_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(lens), _ptr(o), _ptr(lse), *heads, N, D,
-                                         _c_int(window), _c_int(sinks), _scale(scale, D), _ptr(workspace), nbytes,
-                                         _stream_ptr(stream))
+    heads, N, D, o, lse, dev = _rows_and_cache(q, k, v, lens, o, lse, stream)
+    window, sinks = _c_int(window), _c_int(sinks)
+    workspace = _workspace(workspace, q, stream, dev, "fa_window_decode_workspace_bytes", *heads, N, D, window, sinks)
+    rc = _native.load().fa_window_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(lens), o.data_ptr(),
+                                         lse.data_ptr(), *heads, N, D, window, sinks, _scale(scale, D), _ptr(workspace),
+                                         _nbytes(workspace), _stream_handle(stream, dev))
     _native.check(rc, "fa_window_decode")
     return o, lse
 
@@ -383,16 +433,17 @@ def fa_prefix_decode(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
     """The n_q <= 16 newest rows q [B, Hq, n_q, D] of each sequence against the prefix k_prefix, v_prefix [Hkv, P, D]
     that all sequences share, and against the sequence's own cache k, v [B, Hkv, N, D] behind it, of which lens[b]
     keys are held (int32 CUDA tensor; default N) (fa_prefix_decode).  Returns (o, lse)."""
-    heads, N, D, o, lse = _rows_and_cache(q, k, v, lens, o, lse, stream)
+    heads, N, D, o, lse, dev = _rows_and_cache(q, k, v, lens, o, lse, stream)
     if k_prefix.dim() != 3:
         raise ValueError(f"k_prefix must be [Hkv, P, D], got {list(k_prefix.shape)}")
     P = k_prefix.shape[1]
-    _bf16(k_prefix, "k_prefix", (heads[2], P, D))
-    _bf16(v_prefix, "v_prefix", (heads[2], P, D))
-    workspace, nbytes = _workspace(workspace, fa_prefix_decode_workspace_bytes(*heads, P, N, D), stream)
-    rc = _native.load().fa_prefix_decode(_ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(k), _ptr(v), _ptr(lens), _ptr(o),
-                                         _ptr(lse), *heads, P, N, D, _scale(scale, D), _ptr(workspace), nbytes,
-                                         _stream_ptr(stream))
+    _bf16(k_prefix, "k_prefix", (heads[2], P, D), dev)
+    _bf16(v_prefix, "v_prefix", (heads[2], P, D), dev)
+    workspace = _workspace(workspace, q, stream, dev, "fa_prefix_decode_workspace_bytes", *heads, P, N, D)
+    rc = _native.load().fa_prefix_decode(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k.data_ptr(),
+                                         v.data_ptr(), _ptr(lens), o.data_ptr(), lse.data_ptr(), *heads, P, N, D,
+                                         _scale(scale, D), _ptr(workspace), _nbytes(workspace),
+                                         _stream_handle(stream, dev))
     _native.check(rc, "fa_prefix_decode")
     return o, lse
 

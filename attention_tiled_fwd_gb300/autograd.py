@@ -16,8 +16,8 @@ from typing import Optional
 
 import torch
 
-from . import (fa_backward_dkdv, fa_backward_dq, fa_forward, fa_window_backward_dkdv, fa_window_backward_dq,
-               fa_window_forward)
+from . import (FA_BF16, _c_int, _device, _native, _nbytes, _ptr, _scale, _stream_handle, _workspace, fa_backward_dkdv,
+               fa_backward_dq, fa_forward, fa_window_forward)
 
 
 class _Attention(torch.autograd.Function):
@@ -46,22 +46,38 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
 
 
 class _WindowAttention(torch.autograd.Function):
+    # The backward calls the library directly: its tensors were checked by the forward or are made here, and the
+    # engine's thread runs this Python 2-3 times slower than the main thread does.
     @staticmethod
     def forward(ctx, q, k, v, window: int, sinks: int, scale: Optional[float]):
-        q, k, v = (t.contiguous() for t in (q, k, v))
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
         o, lse = fa_window_forward(q, k, v, window, sinks, scale=scale)
         ctx.save_for_backward(q, k, v, o, lse)
-        ctx.mask, ctx.scale = (window, sinks), scale
+        B, Hq, Nq, D = q.shape
+        ctx.sizes = (B, Hq, k.shape[1], Nq, k.shape[2], D, _c_int(window), _c_int(sinks))
+        ctx.scale = _scale(scale, D)
         return o
 
     @staticmethod
     def backward(ctx, dO):
         q, k, v, o, lse = ctx.saved_tensors
         dO = dO.to(q.dtype).contiguous()
-        dq, delta = fa_window_backward_dq(q, k, v, o, dO, lse, *ctx.mask, scale=ctx.scale, grad_dtype=q.dtype)
-        dk = dv = None
-        if ctx.needs_input_grad[1] or ctx.needs_input_grad[2]:
-            dk, dv = fa_window_backward_dkdv(q, k, v, dO, lse, delta, *ctx.mask, scale=ctx.scale, grad_dtype=q.dtype)
+        if dO.data_ptr() % 16:  # a view into something else: the library reads 16-byte units
+            dO = dO.clone()
+        lib, stream = _native.load(), _stream_handle(None, _device())
+        dq, delta = torch.empty_like(q), torch.empty_like(lse)
+        common = (*ctx.sizes, ctx.scale, FA_BF16, FA_BF16)
+        rc = lib.fa_window_backward_dq(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dO.data_ptr(),
+                                       lse.data_ptr(), delta.data_ptr(), dq.data_ptr(), *common, stream)
+        _native.check(rc, "fa_window_backward_dq")
+        if not (ctx.needs_input_grad[1] or ctx.needs_input_grad[2]):
+            return dq, None, None, None, None, None
+        dk, dv = torch.empty_like(k), torch.empty_like(v)
+        workspace = _workspace(None, q, None, 0, "fa_window_backward_workspace_bytes", *ctx.sizes)
+        rc = lib.fa_window_backward_dkdv(q.data_ptr(), k.data_ptr(), v.data_ptr(), dO.data_ptr(), lse.data_ptr(),
+                                         delta.data_ptr(), dk.data_ptr(), dv.data_ptr(), *common, _ptr(workspace),
+                                         _nbytes(workspace), stream)
+        _native.check(rc, "fa_window_backward_dkdv")
         return dq, dk, dv, None, None, None
 
 

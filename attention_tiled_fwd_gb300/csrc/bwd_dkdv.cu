@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
                     const __grid_constant__ CUtensorMap tmap_dk, const __grid_constant__ CUtensorMap tmap_dv,
+                    const __grid_constant__ CUtensorMap tmap_pk, const __grid_constant__ CUtensorMap tmap_pv,
                     BwdArgs a) {
     using L = DkdvSmem<D, NSLOT, kStatSlots>;
     constexpr int kPanels = D / 64;
@@ -142,15 +143,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     __shared__ int epi_abort;  // a compute warp's wait ran out: the epilogue stores nothing
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int rank, bh;
-    tile_order(((WIN ? a.win.Nk : a.N) + kBN - 1) / kBN, a.B * (WIN ? a.win.Hkv : a.H), a.causal, a.head_group, &rank,
-               &bh);
-    const int k_tile = rank;  // causal: key tile 0 has the most query tiles
+    int k_tile, bh;  // causal: key tile 0 has the most query tiles
+    WinKeyItem item{};
+    if constexpr (WIN) {
+        item = win_key_item(a, blockIdx.x, kBN, kBQ);
+        k_tile = item.k_tile;
+        bh = item.bh;
+    } else {
+        tile_order((a.N + kBN - 1) / kBN, a.B * a.H, a.causal, a.head_group, &k_tile, &bh);
+    }
+    const bool partial = WIN && item.part >= 0;  // this CTA writes an fp32 partial
     const int N = a.N;
     const int n_q_total = (N + kBQ - 1) / kBQ;
     const int q_begin = a.causal ? (k_tile * kBN) / kBQ : 0;
-    const WinRows rows = WIN ? win_rows(a, k_tile * kBN, kBN, kBQ) : WinRows{0, 0, 0};
-    const int n_q = WIN ? rows.n : n_q_total - q_begin;  // >= 1 (WIN: or 0, and then the gradients are 0)
+    const int n_q = WIN ? item.n : n_q_total - q_begin;  // >= 1 (WIN: or 0, and then the gradients are 0)
     const int do0 = VK ? 0 : blockIdx.y * DO;  // first dV / dK column of this CTA
     const bool role_dv = VK && blockIdx.y == 0;  // VK: this CTA keeps dV only
     const bool role_dk = VK && blockIdx.y == 1;  // VK: this CTA keeps dK only
@@ -221,8 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int p = 0; p < kPanels; ++p)
                     tma_load_3d(dst + p * (kBQ * 128), map, &slot_full[slot], p * 64,
-                                WIN ? rows.row0(idx >> 1, kBQ) : (q_begin + (idx >> 1)) * kBQ,
-                                WIN ? win_query_slice(a, bh, rows, idx >> 1) : bh);
+                                WIN ? item.rows.row0(item.i0 + (idx >> 1), kBQ) : (q_begin + (idx >> 1)) * kBQ,
+                                WIN ? win_query_slice(a, bh, item.rows, item.i0 + (idx >> 1)) : bh);
             }
 #pragma unroll
             for (int s = 0; s < NSLOT; ++s)
@@ -233,8 +239,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = warp_wait(&stat_empty[ss], (sr & 1) ^ 1, a.status, kSiteStats))) break;
             // lane l copies words l, l + 32, ... of the slot's [L_i | D_i]: each copy instruction writes 32
             // consecutive words of shared memory (one bank each) from 32 consecutive floats
-            const int q0 = WIN ? rows.row0(i, kBQ) : (q_begin + i) * kBQ;
-            const size_t slice = WIN ? (size_t)win_query_slice(a, bh, rows, i) * N : 0;
+            const int q0 = WIN ? item.rows.row0(item.i0 + i, kBQ) : (q_begin + i) * kBQ;
+            const size_t slice = WIN ? (size_t)win_query_slice(a, bh, item.rows, item.i0 + i) * N : 0;
             float *dst = stat_s + ss * 2 * kBQ;
 #pragma unroll
             for (int e = 0; e < 2 * kBQ / 32; ++e) {
@@ -380,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             const float4 *ls4 = reinterpret_cast<const float4 *>(stat_s + ss * 2 * kBQ + g * kHalf);
             const float4 *ds4 = reinterpret_cast<const float4 *>(stat_s + ss * 2 * kBQ + kBQ + g * kHalf);
-            const int q0 = (WIN ? rows.row0(i, kBQ) : qt * kBQ) + g * kHalf;  // first query of this thread's range
+            const int q0 = (WIN ? item.rows.row0(item.i0 + i, kBQ) : qt * kBQ) + g * kHalf;  // first query of this thread's range
             // visible iff key <= query (causal), query < N and key < N
             const bool need_mask = WIN ? q0 + kHalf > N || !sees_all(a, key, q0, kHalf)
                                        : (q0 + kHalf > N) || (a.causal && key > q0) || (key >= N);
@@ -474,7 +480,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // and the ring's shared memory, which nothing reads any more once every MMA has completed, as
         // 128-byte-swizzled panels of 128 rows (64 bf16 or 32 fp32 columns; dV's panels first), and written
         // by TMA bulk stores that clip rows past N and columns past the caller's D.
-        const int n_panels = a.grad_bf16 ? DO / 64 : DO / 32;  // per output
+        const bool out_bf16 = a.grad_bf16 && !partial;
+        const int n_panels = out_bf16 ? DO / 64 : DO / 32;  // per output
         static_assert((VK ? 1 : 2) * DO * 4 * kBN <= 2 * L::kKVBytes + NSLOT * L::kTileBytes, "staging fits");
         if (ok) {
             tc_fence_after();
@@ -497,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = 0; t < 32; ++t)
                     v[t] = WIN && n_q == 0 ? 0u : __float_as_uint(__uint_as_float(v[t]) * osc);
                 const int oc = c0 + ch * 32;  // column within this CTA's DO columns
-                if (a.grad_bf16) {
+                if (out_bf16) {
                     uint8_t *prow = stage + (oc / 64) * (kBN * 128);
                     const int cb = (oc % 64) / 8;
 #pragma unroll
@@ -520,12 +527,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();  // the staged tiles are read by the TMA (async proxy)
         asm volatile("bar.sync 1, %0;" ::"r"(128 * kComputeWG) : "memory");
         if (threadIdx.x == 32 * kFirstComputeWarp && !epi_abort) {
-            const int pw = a.grad_bf16 ? 64 : 32;  // panel width in elements
+            const int pw = out_bf16 ? 64 : 32;  // panel width in elements
             for (int p = 0; p < n_panels; ++p) {
                 if (do0 + p * pw >= Dr) break;  // panels wholly past the caller's D are not stored
-                if (!role_dk) tma_store_3d(&tmap_dv, smem + p * (kBN * 128), do0 + p * pw, k_tile * kBN, bh);
-                if (!VK) tma_store_3d(&tmap_dk, smem + (n_panels + p) * (kBN * 128), do0 + p * pw, k_tile * kBN, bh);
-                if (role_dk) tma_store_3d(&tmap_dk, smem + p * (kBN * 128), do0 + p * pw, k_tile * kBN, bh);
+                const CUtensorMap *mv = partial ? &tmap_pv : &tmap_dv, *mk = partial ? &tmap_pk : &tmap_dk;
+                const int y = partial ? 0 : k_tile * kBN, z = partial ? item.part : bh;
+                if (!role_dk) tma_store_3d(mv, smem + p * (kBN * 128), do0 + p * pw, y, z);
+                if (!VK) tma_store_3d(mk, smem + (n_panels + p) * (kBN * 128), do0 + p * pw, y, z);
+                if (role_dk) tma_store_3d(mk, smem + p * (kBN * 128), do0 + p * pw, y, z);
             }
             tma_store_commit();
             tma_store_wait_read();  // the CTA's shared memory must outlive the stores' reads
@@ -542,25 +551,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D, int DO, int NB, int NSLOT, int STATS, bool WIN, bool VK = false>
 cudaError_t launch_spec(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                        const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv, cudaStream_t s) {
+                        const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv, const CUtensorMap *parts,
+                        cudaStream_t s) {
     using L = DkdvSmem<D, NSLOT, STATS>;
     static_assert(L::kAlloc <= 232448, "shared memory budget");
     auto kern = bwd_dkdv_kernel<D, DO, NB, NSLOT, STATS, VK, WIN>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
-    dim3 grid(WIN ? ((a.win.Nk + kBN - 1) / kBN) * a.win.Hkv * a.B : ((a.N + kBN - 1) / kBN) * a.H * a.B,
+    dim3 grid(WIN ? ((a.win.Nk + kBN - 1) / kBN + a.win.sink_tiles * a.win.chunks) * a.win.Hkv * a.B
+                  : ((a.N + kBN - 1) / kBN) * a.H * a.B,
               VK ? 2 : D / DO);
-    kern<<<grid, kThreads, L::kAlloc, s>>>(tq, tk, tv, tdo, tdk, tdv, a);
+    kern<<<grid, kThreads, L::kAlloc, s>>>(tq, tk, tv, tdo, tdk, tdv, parts ? parts[0] : tdk, parts ? parts[1] : tdv, a);
     return cudaGetLastError();
 }
 
 template <bool WIN>
 cudaError_t launch_width(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                         const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv, cudaStream_t s) {
+                         const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv, const CUtensorMap *parts,
+                         cudaStream_t s) {
     switch (kernel_head_dim(a.D)) {
-        case 128: return launch_spec<128, 128, 2, 8, 4, WIN>(a, tq, tk, tv, tdo, tdk, tdv, s);
-        case 192: return launch_spec<192, 192, 1, 5, 4, WIN>(a, tq, tk, tv, tdo, tdk, tdv, s);
-        case 256: return launch_spec<256, 256, 2, 3, 3, WIN, true>(a, tq, tk, tv, tdo, tdk, tdv, s);
+        case 128: return launch_spec<128, 128, 2, 8, 4, WIN>(a, tq, tk, tv, tdo, tdk, tdv, parts, s);
+        case 192: return launch_spec<192, 192, 1, 5, 4, WIN>(a, tq, tk, tv, tdo, tdk, tdv, parts, s);
+        case 256: return launch_spec<256, 256, 2, 3, 3, WIN, true>(a, tq, tk, tv, tdo, tdk, tdv, parts, s);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -569,9 +581,9 @@ cudaError_t launch_width(const BwdArgs &a, const CUtensorMap &tq, const CUtensor
 
 cudaError_t launch_bwd_dkdv(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                             const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv, cudaStream_t s,
-                            bool win) {
-    return win ? launch_width<true>(a, tq, tk, tv, tdo, tdk, tdv, s)
-               : launch_width<false>(a, tq, tk, tv, tdo, tdk, tdv, s);
+                            const CUtensorMap *parts) {
+    return parts ? launch_width<true>(a, tq, tk, tv, tdo, tdk, tdv, parts, s)
+                 : launch_width<false>(a, tq, tk, tv, tdo, tdk, tdv, nullptr, s);
 }
 
 }  // namespace fa

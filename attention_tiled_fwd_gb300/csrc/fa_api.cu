@@ -413,7 +413,7 @@ int check_window(int B, int Hq, int Hkv, int Nq, int Nk, int kv_rows, int D, int
 }
 
 WinArgs window_args(int Hkv, int Nk, int window, int sinks) {
-    WinArgs w{Hkv, Nk, std::min(window, Nk), std::min(sinks, Nk)};
+    WinArgs w{Hkv, Nk, std::min(window, Nk), std::min(sinks, Nk), 0, 0};
     if (w.window == Nk) w.sinks = 0;  // every earlier key is in the window
     return w;
 }
@@ -423,6 +423,31 @@ WinArgs window_args(int Hkv, int Nk, int window, int sinks) {
 int window_pairing(int B, int Hq, int Hkv, int Nq, int num_sms) {
     if ((long long)B * Hq * ((Nq + 127) / 128) <= num_sms) return kOneTile;
     return (Hq / Hkv) % 2 == 0 ? kTwoHeads : kTwoRowTiles;
+}
+
+// Cuts the rows behind the sink tiles' windows (dK/dV) into chunks.  Without it one CTA per sink tile and key head
+// meets every row: at Nq = 4096, window 1024, groups of 4 heads it took 256 of the others' 72 steps and the launch
+// waited for it.
+WinArgs window_args_dkdv(int B, int Hq, int Hkv, int Nq, int Nk, int D, int window, int sinks, int num_sms) {
+    WinArgs w = window_args(Hkv, Nk, window, sinks);
+    if (w.sinks == 0) return w;
+    const long long bq = kernel_head_dim(D) == 64 ? 128 : kDkdvQRows, bk = 128, G = Hq / Hkv;
+    // 64-bit sizes: tiles of rows that a key tile's window meets, rows behind the first sink tile's, and all steps
+    const long long own = G * ((std::min<long long>(Nq, bk - 1 + w.window) + bq - 1) / bq);
+    const long long end = std::max(0ll, std::min<long long>(Nq, bk - 1 + w.window - (Nk - Nq)));
+    const long long rest = G * ((Nq - end + bq - 1) / bq);
+    const long long sink_tiles = (w.sinks + bk - 1) / bk;
+    const long long all = (long long)B * Hkv * ((Nk + bk - 1) / bk * own + sink_tiles * rest);
+    // a chunk is as long as another item, or a quarter of an SM's share of the launch, and 16 steps at least
+    const long long per = std::max({own, all / (4 * num_sms), 16ll});
+    if (rest <= per / 2) return w;
+    w.sink_tiles = (int)sink_tiles;
+    w.chunks = (int)((rest + per - 1) / per);
+    return w;
+}
+
+size_t sink_part_floats(const WinArgs &w, int B, int D) {
+    return (size_t)B * w.Hkv * w.sink_tiles * (w.chunks > 0 ? 1 + w.chunks : 0) * 128 * D;
 }
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -509,7 +534,8 @@ extern "C" int fa_window_backward_workspace_bytes(int B, int Hq, int Hkv, int Nq
     if (!bytes) return FA_ERR_NULL;
     int rc = check_window(B, Hq, Hkv, Nq, Nk, Nk, D, window, sinks, 1.f);
     if (rc != FA_OK) return rc;
-    *bytes = 0;
+    *bytes = 2 * sizeof(float) *
+             sink_part_floats(window_args_dkdv(B, Hq, Hkv, Nq, Nk, D, window, sinks, current_num_sms()), B, D);
     return FA_OK;
 }
 
@@ -528,8 +554,15 @@ extern "C" int fa_window_backward_dkdv(const void *q, const void *k, const void 
     if (rc != FA_OK) return rc;
     BwdArgs a{q, k, v, nullptr, dO, lse, const_cast<float *>(delta), nullptr, dk, dv, B, Hq, Nq, D, scale,
               scale * log2e(), 1, grad_dtype == FA_BF16 ? 1 : 0, st->status_word, B * Hkv,
-              window_args(Hkv, Nk, window, sinks)};
-    CUtensorMap tq, tk, tv, tdo, tdk, tdv;
+              window_args_dkdv(B, Hq, Hkv, Nq, Nk, D, window, sinks, st->num_sms)};
+    const size_t part_floats = sink_part_floats(a.win, B, D);
+    if (part_floats > 0) {
+        rc = check_ptrs({workspace});
+        if (rc != FA_OK) return rc;
+        if (workspace_bytes < 2 * part_floats * sizeof(float)) return FA_ERR_WORKSPACE;
+    }
+    float *part_dk = static_cast<float *>(workspace), *part_dv = part_dk + part_floats;
+    CUtensorMap tq, tk, tv, tdo, tdk, tdv, parts[2];
     const int Dk = kernel_head_dim(D);
     const int q_box = Dk == 64 ? 128 : kDkdvQRows;
     if (encode_rows(&tq, q, B * Hq, Nq, Nq, D, q_box) != FA_OK || encode_rows(&tk, k, B * Hkv, Nk, Nk, D, 128) != FA_OK ||
@@ -537,9 +570,17 @@ extern "C" int fa_window_backward_dkdv(const void *q, const void *k, const void 
         encode_3d(&tdk, dk, B * Hkv, Nk, D, 128, grad_dtype == FA_F32) != FA_OK ||
         encode_3d(&tdv, dv, B * Hkv, Nk, D, 128, grad_dtype == FA_F32) != FA_OK)
         return FA_ERR_CUDA;
+    parts[0] = tdk, parts[1] = tdv;
+    if (part_floats > 0) {
+        const int n = B * Hkv * a.win.sink_tiles * (1 + a.win.chunks);
+        if (encode_3d(&parts[0], part_dk, n, 128, D, 128, true) != FA_OK ||
+            encode_3d(&parts[1], part_dv, n, 128, D, 128, true) != FA_OK)
+            return FA_ERR_CUDA;
+    }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = Dk == 64 ? launch_bwd_dkdv_q128(a, tq, tk, tv, tdo, tdk, tdv, s, true)
-                             : launch_bwd_dkdv(a, tq, tk, tv, tdo, tdk, tdv, s, true);
+    cudaError_t e = Dk == 64 ? launch_bwd_dkdv_q128(a, tq, tk, tv, tdo, tdk, tdv, s, parts)
+                             : launch_bwd_dkdv(a, tq, tk, tv, tdo, tdk, tdv, s, parts);
+    if (e == cudaSuccess && part_floats > 0) e = launch_sink_sum(a, part_dk, part_dv, s);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -110,20 +110,52 @@ struct BwdArgs {
 
 #ifdef __CUDACC__
 // The query rows of windowed attention that keys k0 .. k0 + bk - 1 meet: rows from `first` on in `per_head`
-// tiles of bq rows, for each of the key head's query heads; n tiles in all.
+// tiles of bq rows, for each of the key head's query heads.
 struct WinRows {
-    int first, per_head, n;
+    int first, per_head;
     __device__ __forceinline__ int row0(int i, int bq) const { return first + i % per_head * bq; }
 };
 
-__device__ __forceinline__ WinRows win_rows(const BwdArgs &a, int k0, int bk, int bq) {
+// A work item of the windowed dK/dV kernels: tiles i0 .. i0 + n - 1 of `rows` against one key tile.  part < 0: the
+// item owns its key tile's gradients; else it writes partial `part`.
+struct WinKeyItem {
+    int k_tile, bh, part, i0, n;
+    WinRows rows;
+};
+
+__device__ __forceinline__ WinKeyItem win_key_item(const BwdArgs &a, int x, int bk, int bq) {
+    const int G = a.H / a.win.Hkv, n_bh = a.B * a.win.Hkv;
     const int off = a.win.Nk - a.N;  // position of row 0
-    WinRows r;
-    r.first = max(0, k0 - off);
-    const int end = k0 < a.win.sinks ? a.N : min(a.N, k0 + bk - 1 + a.win.window - off);
-    r.per_head = end > r.first ? (end - r.first + bq - 1) / bq : 0;
-    r.n = r.per_head * (a.H / a.win.Hkv);
-    return r;
+    const int extra = n_bh * a.win.sink_tiles * a.win.chunks;
+    WinKeyItem w;
+    int chunk = -1;
+    if (x < extra) {
+        chunk = x % a.win.chunks;
+        w.k_tile = x / a.win.chunks % a.win.sink_tiles;
+        w.bh = x / (a.win.chunks * a.win.sink_tiles);
+    } else {
+        w.k_tile = (x - extra) / n_bh;
+        w.bh = (x - extra) % n_bh;
+    }
+    const int k0 = w.k_tile * bk;
+    const bool cut = a.win.chunks > 0 && w.k_tile < a.win.sink_tiles;
+    w.part = cut ? (w.bh * a.win.sink_tiles + w.k_tile) * (1 + a.win.chunks) + 1 + chunk : -1;
+    w.rows.first = max(0, k0 - off);
+    // every later row for a sink tile that is not cut, else the rows whose window holds one of the keys
+    const int end = k0 < a.win.sinks && !cut ? a.N : min(a.N, k0 + bk - 1 + a.win.window - off);
+    w.rows.per_head = end > w.rows.first ? (end - w.rows.first + bq - 1) / bq : 0;
+    if (chunk >= 0) {  // the rows behind those
+        w.rows.first += w.rows.per_head * bq;
+        w.rows.per_head = a.N > w.rows.first ? (a.N - w.rows.first + bq - 1) / bq : 0;
+    }
+    w.i0 = 0;
+    w.n = w.rows.per_head * G;
+    if (chunk >= 0) {
+        const int per = (w.n + a.win.chunks - 1) / a.win.chunks;
+        w.i0 = min(w.n, chunk * per);
+        w.n = min(w.n - w.i0, per);
+    }
+    return w;
 }
 
 // Query slice (batch and query head) of tile i of key slice kv_bh.
@@ -206,11 +238,14 @@ cudaError_t launch_bwd_dq_k128(const BwdArgs &a, const CUtensorMap &tq, const CU
 cudaError_t launch_bwd_dkdv_q128(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk,
                                  const CUtensorMap &tv, const CUtensorMap &tdo, const CUtensorMap &tdk,
                                  const CUtensorMap &tdv, cudaStream_t s,
-                          bool win = false);
+                          const CUtensorMap *parts = nullptr);
 cudaError_t launch_bwd_dkdv(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk,
                             const CUtensorMap &tv, const CUtensorMap &tdo, const CUtensorMap &tdk,
                             const CUtensorMap &tdv, cudaStream_t s,
-                          bool win = false);
+                          const CUtensorMap *parts = nullptr);
+// Windowed (parts != null): parts[0], parts[1] are the tensor maps of the sink tiles' fp32 partials of dK and dV
+// ([part][128][D], 32-column boxes); launch_sink_sum adds them.
+cudaError_t launch_sink_sum(const BwdArgs &a, const float *part_dk, const float *part_dv, cudaStream_t s);
 cudaError_t launch_selftest_timeout(int *status, int limit_us, cudaStream_t s);
 
 // Head dimension a bf16 kernel is built for: the smallest of 64, 128, 192, 256 that holds D.  Any

@@ -60,6 +60,10 @@ struct WinArgs {
     int Hkv;     // key heads; query head h reads key head h / (H / Hkv)
     int Nk;      // keys; the query rows are the last N of the Nk positions
     int window, sinks;
+    // dK/dV: rows far behind the sinks see the sinks alone, and one CTA per sink tile would walk all of them.
+    // They are cut into `chunks` work items per sink tile (0: not cut); those items and the sink tile's own
+    // write fp32 partials, which sink_sum_kernel adds in a fixed order.
+    int sink_tiles, chunks;
 };
 
 // The forward over the keys that a span of query rows sees (win_fwd.cu, and fwd_bf16.cu for wide heads).

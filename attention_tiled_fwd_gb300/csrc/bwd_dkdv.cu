@@ -278,12 +278,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int q_slot = (2 * i) % NSLOT, q_round = (2 * i) / NSLOT;
             const int d_slot = (2 * i + 1) % NSLOT, d_round = (2 * i + 1) / NSLOT;
             const uint32_t b = i % NB;
-            if (!(ok = warp_wait(&slot_full[q_slot], q_round & 1, a.status, kSiteSlotFull))) break;
             // buffer b last held P^T_{i-NB}, read by dV_{i-NB} (the dK CTA: by the compute warps, done with
-            // tile i-NB once dK_{i-NB} was issued)
+            // tile i-NB once dK_{i-NB} was issued).  This wait comes before the one for Q_i's slot: with an odd
+            // ring that slot last held a dO tile, which the dV CTA's issuer A waits for nowhere else, and while
+            // that load is still in flight the slot's barrier carries the parity of two rounds back, the one
+            // waited for below.
             if (i >= NB && !(ok = warp_wait(role_dk ? &dk_done[b] : &dv_done[b], ((i - NB) / NB) & 1, a.status,
                                             kSiteDvDone)))
                 break;
+            if (!(ok = warp_wait(&slot_full[q_slot], q_round & 1, a.status, kSiteSlotFull))) break;
             tc_fence_after();
             const uint64_t q_desc = sdesc_sw128(slot_addr + q_slot * L::kTileBytes, 16, 1024);
             if (leader) {

@@ -573,7 +573,9 @@ cudaError_t launch_width(const BwdArgs &a, const CUtensorMap &tq, const CUtensor
                          const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv, const CUtensorMap *parts,
                          cudaStream_t s) {
     switch (kernel_head_dim(a.D)) {
-        case 128: return launch_spec<128, 128, 2, 8, 4, WIN>(a, tq, tk, tv, tdo, tdk, tdv, parts, s);
+        case 128:
+            if constexpr (!WIN) return launch_spec<128, 128, 2, 8, 4, WIN>(a, tq, tk, tv, tdo, tdk, tdv, parts, s);
+            return cudaErrorInvalidValue;  // win_dkdv.cu
         case 192: return launch_spec<192, 192, 1, 5, 4, WIN>(a, tq, tk, tv, tdo, tdk, tdv, parts, s);
         case 256: return launch_spec<256, 256, 2, 3, 3, WIN, true>(a, tq, tk, tv, tdo, tdk, tdv, parts, s);
         default: return cudaErrorInvalidValue;

@@ -27,7 +27,6 @@
 // thread owning one key row (its TMEM lane).
 #include "fa_internal.h"
 #include "sm100_ptx.cuh"
-#include "win.cuh"
 #include <cmath>
 
 namespace fa {
@@ -62,14 +61,10 @@ struct Q128Smem {
     static constexpr int kAlloc = kTmemHolderOff + 16 + 1024;
 };
 
-// WIN: windowed attention (win.cuh): a key tile meets the rows of every query head of its group whose window (or
-// the sinks) holds one of its keys; those tiles start at the first such row.
-template <bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dkdv_q128_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                          const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
                          const __grid_constant__ CUtensorMap tmap_dk, const __grid_constant__ CUtensorMap tmap_dv,
-                         const __grid_constant__ CUtensorMap tmap_pk, const __grid_constant__ CUtensorMap tmap_pv,
                          BwdArgs a) {
     using L = Q128Smem;
     constexpr uint32_t kTmemCols = 512;
@@ -103,20 +98,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     __shared__ int epi_abort;  // a compute warp's wait ran out: the epilogue stores nothing
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int k_tile, bh;  // causal: key tile 0 has the most query tiles
-    WinKeyItem item{};
-    if constexpr (WIN) {
-        item = win_key_item(a, blockIdx.x, kBN, kBQ);
-        k_tile = item.k_tile;
-        bh = item.bh;
-    } else {
-        tile_order((a.N + kBN - 1) / kBN, a.B * a.H, a.causal, a.head_group, &k_tile, &bh);
-    }
-    const bool partial = WIN && item.part >= 0;  // this CTA writes an fp32 partial
+    int rank, bh;
+    tile_order((a.N + kBN - 1) / kBN, a.B * a.H, a.causal, a.head_group, &rank, &bh);
+    const int k_tile = rank;  // causal: key tile 0 has the most query tiles
     const int N = a.N;
     const int n_q_total = (N + kBQ - 1) / kBQ;
     const int q_begin = a.causal ? k_tile : 0;  // kBQ == kBN
-    const int n_q = WIN ? item.n : n_q_total - q_begin;  // >= 1 (WIN: or 0, and then the gradients are 0)
+    const int n_q = n_q_total - q_begin;       // >= 1
 
     if (threadIdx.x == 0) {
         epi_abort = 0;
@@ -162,8 +150,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(k_s, &tmap_k, kv_full, 0, k_tile * kBN, bh);
             tma_load_3d(v_s, &tmap_v, kv_full, 0, k_tile * kBN, bh);
         }
-        const float *lse_g = a.lse + (WIN ? 0 : (size_t)bh * N);
-        const float *del_g = a.delta + (WIN ? 0 : (size_t)bh * N);
+        const float *lse_g = a.lse + (size_t)bh * N;
+        const float *del_g = a.delta + (size_t)bh * N;
         int last_round[kNSlot];
 #pragma unroll
         for (int s = 0; s < kNSlot; ++s) last_round[s] = -1;
@@ -174,9 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 const CUtensorMap *map = (idx & 1) ? &tmap_do : &tmap_q;
                 mbar_arrive_expect_tx(&slot_full[slot], L::kTileBytes);
-                tma_load_3d(slots + slot * L::kTileBytes, map, &slot_full[slot], 0,
-                            WIN ? item.rows.row0(item.i0 + (idx >> 1), kBQ) : (q_begin + (idx >> 1)) * kBQ,
-                            WIN ? win_query_slice(a, bh, item.rows, item.i0 + (idx >> 1)) : bh);
+                tma_load_3d(slots + slot * L::kTileBytes, map, &slot_full[slot], 0, (q_begin + (idx >> 1)) * kBQ, bh);
             }
 #pragma unroll
             for (int s = 0; s < kNSlot; ++s)
@@ -187,8 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = warp_wait(&stat_empty[ss], (sr & 1) ^ 1, a.status, kSiteStats))) break;
             // lane l copies words l, l + 32, ... of the slot's [L_i | D_i]: each copy instruction writes 32
             // consecutive words of shared memory (one bank each) from 32 consecutive floats
-            const int q0 = WIN ? item.rows.row0(item.i0 + i, kBQ) : (q_begin + i) * kBQ;
-            const size_t slice = WIN ? (size_t)win_query_slice(a, bh, item.rows, item.i0 + i) * N : 0;
+            const int q0 = (q_begin + i) * kBQ;
             float *dst = stat_s + ss * 2 * kBQ;
 #pragma unroll
             for (int e = 0; e < 2 * kBQ / 32; ++e) {
@@ -197,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int q = q0 + (is_l ? w : w - kBQ);
                 const bool valid = q < N;
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst + w)),
-                             "l"((is_l ? lse_g : del_g) + slice + (valid ? q : 0)), "r"(valid ? 4 : 0)
+                             "l"((is_l ? lse_g : del_g) + (valid ? q : 0)), "r"(valid ? 4 : 0)
                              : "memory");
             }
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&stat_full[ss]))
@@ -315,20 +300,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             const float4 *ls4 = reinterpret_cast<const float4 *>(stat_s + ss * 2 * kBQ + g * kSpan);
             const float4 *ds4 = reinterpret_cast<const float4 *>(stat_s + ss * 2 * kBQ + kBQ + g * kSpan);
-            const int q0 = (WIN ? item.rows.row0(item.i0 + i, kBQ) : qt * kBQ) + g * kSpan;  // first query of this thread's range
+            const int q0 = qt * kBQ + g * kSpan;  // first query of this thread's range
             // visible iff key <= query (causal), query < N and key < N
-            const bool need_mask = WIN ? q0 + kSpan > N || !sees_all(a, key, q0, kSpan)
-                                       : (q0 + kSpan > N) || (a.causal && key > q0) || (key >= N);
-            const uint32_t seen = WIN ? seen_by(a, key, q0) : 0u;
+            const bool need_mask = (q0 + kSpan > N) || (a.causal && key > q0) || (key >= N);
             const bool any_mask = __any_sync(0xffffffffu, need_mask);
 
             ok = mbar_wait(&s_full[b], (i >> 1) & 1, a.status, kSiteSFull);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             tc_fence_after();
-            // P^T of this thread's 32 queries as bf16 pairs: the dV operand, and (unpacked) the factor of dS^T.  WIN
-            // keeps the fp32 P as that factor: rounding both P and dS^T makes dK's error a quarter larger.
+            // P^T of this thread's 32 queries as bf16 pairs: the dV operand, and (unpacked) the factor of dS^T
             uint32_t pk[kSpan / 2];
-            float pf[WIN ? kSpan : 1];
             {
                 uint32_t raw[kSpan];
                 tmem_ld32(tmem + lane_base + 128 * b + g * kSpan, raw);
@@ -349,14 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int t = 0; t < 4; ++t) {
                             const int qq = q0 + 4 * q4 + t;
-                            if (WIN ? !(seen & (1u << (4 * q4 + t)))
-                                    : qq >= N || key >= N || (a.causal && qq < key))
-                                p[t] = 0.f;
+                            if (qq >= N || key >= N || (a.causal && qq < key)) p[t] = 0.f;
                         }
-                    }
-                    if constexpr (WIN) {
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) pf[4 * q4 + t] = p[t];
                     }
                     pk[2 * q4] = pack_bf16x2(p[0], p[1]);
                     pk[2 * q4 + 1] = pack_bf16x2(p[2], p[3]);
@@ -380,14 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int q4 = 0; q4 < kSpan / 4; ++q4) {
                     const float4 d4 = ds4[q4];
-                    float2 p01, p23;
-                    if constexpr (WIN) {
-                        p01 = make_float2(pf[4 * q4], pf[4 * q4 + 1]);
-                        p23 = make_float2(pf[4 * q4 + 2], pf[4 * q4 + 3]);
-                    } else {
-                        p01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&pk[2 * q4]));
-                        p23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&pk[2 * q4 + 1]));
-                    }
+                    const float2 p01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&pk[2 * q4]));
+                    const float2 p23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&pk[2 * q4 + 1]));
                     // dS^T / scale = P^T * (dP^T - D), on fp32 pairs
                     dsk[2 * q4] = f2_to_bf16x2(f2_mul(
                         f2_sub(f2_pack(__uint_as_float(raw[4 * q4 + 0]), __uint_as_float(raw[4 * q4 + 1])),
@@ -408,17 +377,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok) {
             ok = mbar_wait(final_bar, 0, a.status, kSiteDone);
-            // no product has waited for K and V when no row meets them: their loads must still have landed
-            // before the epilogue stages into their memory
-            if (WIN && ok && n_q == 0) ok = mbar_wait(kv_full, 0, a.status, kSiteKV);
             ok = __all_sync(0xffffffffu, ok);
         }
         // Epilogue: dV and dK (dK times the scale its dS^T operands left out) are staged in the K / V tiles'
         // and the ring's shared memory, which nothing reads any more once every MMA has completed, as
         // 128-byte-swizzled panels of 128 rows (one of 64 bf16 or two of 32 fp32 columns per output; dV's
         // first), and written by TMA bulk stores that clip rows past N and columns past the caller's D.
-        const bool out_bf16 = a.grad_bf16 && !partial;
-        const int n_panels = out_bf16 ? 1 : 2;  // per output
+        const int n_panels = a.grad_bf16 ? 1 : 2;  // per output
         const int Dr = a.D;
         if (ok) {
             tc_fence_after();
@@ -430,11 +395,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(tmem + lane_base + (is_dv ? kColDV : kColDK) + c0, v);
             tmem_wait_ld();
 #pragma unroll
-            for (int t = 0; t < 32; ++t)
-                v[t] = WIN && n_q == 0 ? 0u : __float_as_uint(__uint_as_float(v[t]) * osc);
+            for (int t = 0; t < 32; ++t) v[t] = __float_as_uint(__uint_as_float(v[t]) * osc);
             uint8_t *stage = smem + (is_dv ? 0 : n_panels) * (kBN * 128) + r * 128;
             const int sw = r & 7;
-            if (out_bf16) {
+            if (a.grad_bf16) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     st_shared_v4(stage + (((4 * (g & 1) + c) ^ sw) << 4),
@@ -454,13 +418,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();  // the staged tiles are read by the TMA (async proxy)
         asm volatile("bar.sync 1, %0;" ::"r"(128 * kComputeWG) : "memory");
         if (threadIdx.x == 32 * kFirstComputeWarp && !epi_abort) {
-            const int pw = out_bf16 ? 64 : 32;  // panel width in elements
+            const int pw = a.grad_bf16 ? 64 : 32;  // panel width in elements
             for (int p = 0; p < n_panels; ++p) {
                 if (p * pw >= Dr) break;  // a panel wholly past the caller's D is not stored
-                tma_store_3d(partial ? &tmap_pv : &tmap_dv, smem + p * (kBN * 128), p * pw, partial ? 0 : k_tile * kBN,
-                             partial ? item.part : bh);
-                tma_store_3d(partial ? &tmap_pk : &tmap_dk, smem + (n_panels + p) * (kBN * 128), p * pw,
-                             partial ? 0 : k_tile * kBN, partial ? item.part : bh);
+                tma_store_3d(&tmap_dv, smem + p * (kBN * 128), p * pw, k_tile * kBN, bh);
+                tma_store_3d(&tmap_dk, smem + (n_panels + p) * (kBN * 128), p * pw, k_tile * kBN, bh);
             }
             tma_store_commit();
             tma_store_wait_read();  // the CTA's shared memory must outlive the stores' reads
@@ -475,55 +437,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Adds the partials of one sink tile (its own rows', then the chunks', in that order) into dK and dV; four columns a
-// thread.  partials of a tile: [part][128][D].
-__global__ void sink_sum_kernel(BwdArgs a, const float *part_dk, const float *part_dv) {
-    const int cols = a.D / 4, parts = 1 + a.win.chunks;
-    const int tile = blockIdx.y;  // (key slice, sink tile)
-    const int bh = tile / a.win.sink_tiles, k0 = tile % a.win.sink_tiles * kBN;
-    const int rows = min(kBN, a.win.Nk - k0);
-    for (int e = blockIdx.x * blockDim.x + threadIdx.x; e < rows * cols; e += gridDim.x * blockDim.x) {
-        const size_t in = (size_t)tile * parts * kBN * a.D + (size_t)e * 4;
-        const size_t out = ((size_t)bh * a.win.Nk + k0) * a.D + (size_t)e * 4;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            const float *src = (w ? part_dv : part_dk) + in;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int p = 0; p < parts; ++p) {
-                const float4 v = *reinterpret_cast<const float4 *>(src + (size_t)p * kBN * a.D);
-                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-            }
-            void *dst = w ? a.dv : a.dk;
-            if (a.grad_bf16)
-                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(dst) + out) =
-                    make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
-            else
-                *reinterpret_cast<float4 *>(static_cast<float *>(dst) + out) = s;
-        }
-    }
-}
-
 }  // namespace
-
-cudaError_t launch_sink_sum(const BwdArgs &a, const float *part_dk, const float *part_dv, cudaStream_t s) {
-    const dim3 grid((kBN * a.D / 4 + 255) / 256, a.B * a.win.Hkv * a.win.sink_tiles);
-    sink_sum_kernel<<<grid, 256, 0, s>>>(a, part_dk, part_dv);
-    return cudaGetLastError();
-}
 
 cudaError_t launch_bwd_dkdv_q128(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk,
                                  const CUtensorMap &tv, const CUtensorMap &tdo, const CUtensorMap &tdk,
-                                 const CUtensorMap &tdv, cudaStream_t s, const CUtensorMap *parts) {
+                                 const CUtensorMap &tdv, cudaStream_t s) {
     using L = Q128Smem;
     static_assert(L::kAlloc <= 232448, "shared memory budget");
     if (kernel_head_dim(a.D) != kD) return cudaErrorInvalidValue;
-    auto kern = parts ? bwd_dkdv_q128_kernel<true> : bwd_dkdv_q128_kernel<false>;
+    auto kern = bwd_dkdv_q128_kernel;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
-    dim3 grid(parts ? ((a.win.Nk + kBN - 1) / kBN + a.win.sink_tiles * a.win.chunks) * a.win.Hkv * a.B
-                    : ((a.N + kBN - 1) / kBN) * a.H * a.B);
-    kern<<<grid, kThreads, L::kAlloc, s>>>(tq, tk, tv, tdo, tdk, tdv, parts ? parts[0] : tdk, parts ? parts[1] : tdv, a);
+    dim3 grid(((a.N + kBN - 1) / kBN) * a.H * a.B);
+    kern<<<grid, kThreads, L::kAlloc, s>>>(tq, tk, tv, tdo, tdk, tdv, a);
     return cudaGetLastError();
 }
 

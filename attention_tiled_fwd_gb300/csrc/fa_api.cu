@@ -438,8 +438,9 @@ WinArgs window_args_dkdv(int B, int Hq, int Hkv, int Nq, int Nk, int D, int wind
     const long long rest = G * ((Nq - end + bq - 1) / bq);
     const long long sink_tiles = (w.sinks + bk - 1) / bk;
     const long long all = (long long)B * Hkv * ((Nk + bk - 1) / bk * own + sink_tiles * rest);
-    // a chunk is as long as another item, or a quarter of an SM's share of the launch, and 16 steps at least
-    const long long per = std::max({own, all / (4 * num_sms), 16ll});
+    // a chunk is as long as another item, or up to four of them when that is a quarter of an SM's share of the
+    // launch or less, and 16 steps at least
+    const long long per = std::max({own, std::min(all / (4 * num_sms), 4 * own), 16ll});
     if (rest <= per / 2) return w;
     w.sink_tiles = (int)sink_tiles;
     w.chunks = (int)((rest + per - 1) / per);
@@ -578,8 +579,7 @@ extern "C" int fa_window_backward_dkdv(const void *q, const void *k, const void 
             return FA_ERR_CUDA;
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = Dk == 64 ? launch_bwd_dkdv_q128(a, tq, tk, tv, tdo, tdk, tdv, s, parts)
-                             : launch_bwd_dkdv(a, tq, tk, tv, tdo, tdk, tdv, s, parts);
+    cudaError_t e = launch_win_dkdv(a, tq, tk, tv, tdo, tdk, tdv, parts, st->num_sms, s);
     if (e == cudaSuccess && part_floats > 0) e = launch_sink_sum(a, part_dk, part_dv, s);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -237,14 +237,16 @@ cudaError_t launch_bwd_dq_k128(const BwdArgs &a, const CUtensorMap &tq, const CU
 // bwd_dkdv_q128.cu: the dK/dV kernel for D = 64 with 128-row Q / dO tiles (TMA boxes of 128 rows)
 cudaError_t launch_bwd_dkdv_q128(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk,
                                  const CUtensorMap &tv, const CUtensorMap &tdo, const CUtensorMap &tdk,
-                                 const CUtensorMap &tdv, cudaStream_t s,
-                          const CUtensorMap *parts = nullptr);
+                                 const CUtensorMap &tdv, cudaStream_t s);
 cudaError_t launch_bwd_dkdv(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk,
                             const CUtensorMap &tv, const CUtensorMap &tdo, const CUtensorMap &tdk,
                             const CUtensorMap &tdv, cudaStream_t s,
                           const CUtensorMap *parts = nullptr);
 // Windowed (parts != null): parts[0], parts[1] are the tensor maps of the sink tiles' fp32 partials of dK and dV
 // ([part][128][D], 32-column boxes); launch_sink_sum adds them.
+cudaError_t launch_win_dkdv(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                            const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv,
+                            const CUtensorMap *parts, int num_sms, cudaStream_t s);
 cudaError_t launch_sink_sum(const BwdArgs &a, const float *part_dk, const float *part_dv, cudaStream_t s);
 cudaError_t launch_selftest_timeout(int *status, int limit_us, cudaStream_t s);
 

@@ -94,21 +94,21 @@ struct DqSmem {
 // CTA accumulates (D here; D / DQ CTAs per query tile, grid y choosing the columns); QT: Q kept in
 // TMEM as the A operand of S (else S reads Q from shared memory); WIN: windowed attention (win.cuh): the key
 // tiles are those of key_span, a query head reads its group's key head, and the mask is the window's.
-template <int D, int DQ, bool QT, int NSLOT, bool WIN>
-__global__ void __launch_bounds__(kThreads, 1)
+// kSingle: S and dP in one buffer each, emptied by the compute warps into registers first thing (s_free, dp_free),
+// so that all of dQ fits beside them (D = 256), or two CTAs on an SM (kCtas = 2).
+template <int D, int DQ, bool QT, int NSLOT, bool WIN, bool kSingle, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
                   const __grid_constant__ CUtensorMap tmap_o, const __grid_constant__ CUtensorMap tmap_dq,
                   BwdArgs a) {
     using L = DqSmem<D, NSLOT>;
     constexpr int kPanels = D / 64;
-    constexpr uint32_t kTmemCols = 512;
-    // kSingle (D = 256 with all of dQ in one CTA): S and dP in one buffer each, emptied by the compute warps into
-    // registers first thing (s_free, dp_free), so that dQ's 256 columns fit beside them
-    constexpr bool kSingle = !QT && DQ == D && D == 256;
+    constexpr uint32_t kTmemCols = 512 / kCtas;
     constexpr uint32_t kColDP0 = kSingle ? 64 : 128;  // dP[b] at kColDP0 + 64 b (b = 0 when kSingle)
     constexpr uint32_t kColDQ = kSingle ? 128 : 256, kColDS = kColDQ + DQ, kColQ = kColDS + 64;
-    static_assert(kColQ + (QT ? D / 2 : 0) <= 512, "TMEM budget");
+    static_assert(kColQ + (QT ? D / 2 : 0) <= kTmemCols, "TMEM budget");
+    static_assert(!kSingle || (!QT && DQ == D), "single buffers: SS products, all of dQ");
     static_assert(DQ % 64 == 0 && D % DQ == 0, "dQ columns per CTA: whole panels");
     constexpr bool kSplitDp = !QT;
 
@@ -344,22 +344,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ook = mbar_wait(o_full, 0, a.status, kSiteQ) && mbar_wait(q_full, 0, a.status, kSiteQ);
             if (__all_sync(0xffffffffu, ook)) {
 #pragma unroll
-                for (int p = g * (kDCols / 64); p < (g + 1) * (kDCols / 64); ++p) {
-                    const uint8_t *orow = o_s + p * (kBM * 128) + r * 128;
-                    const uint8_t *drow = do_s + p * (kBM * 128) + r * 128;
+                for (int i = 0; i < kDCols / 8; ++i) {
+                    // chunk k of panel p; its swizzled position: lanes (rows) spread over all 32 banks
+                    const int c8 = g * (kDCols / 8) + i, p = c8 >> 3, k = c8 & 7;
+                    const int off = p * (kBM * 128) + r * 128 + ((k ^ (r & 7)) << 4);
+                    const uint4 ov = *reinterpret_cast<const uint4 *>(o_s + off);
+                    const uint4 dv = *reinterpret_cast<const uint4 *>(do_s + off);
+                    const uint32_t ow[4] = {ov.x, ov.y, ov.z, ov.w}, dw[4] = {dv.x, dv.y, dv.z, dv.w};
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        // the swizzled position of chunk k: lanes (rows) spread over all 32 banks
-                        const uint4 ov = *reinterpret_cast<const uint4 *>(orow + ((k ^ (r & 7)) << 4));
-                        const uint4 dv = *reinterpret_cast<const uint4 *>(drow + ((k ^ (r & 7)) << 4));
-                        const uint32_t ow[4] = {ov.x, ov.y, ov.z, ov.w}, dw[4] = {dv.x, dv.y, dv.z, dv.w};
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const float2 of = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&ow[t]));
-                            const float2 df = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&dw[t]));
-                            delta = fmaf(of.x, df.x, delta);
-                            delta = fmaf(of.y, df.y, delta);
-                        }
+                    for (int t = 0; t < 4; ++t) {
+                        const float2 of = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&ow[t]));
+                        const float2 df = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&dw[t]));
+                        delta = fmaf(of.x, df.x, delta);
+                        delta = fmaf(of.y, df.y, delta);
                     }
                 }
             }
@@ -568,12 +565,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, int DQ, bool QT, int NSLOT, bool WIN>
+template <int D, int DQ, bool QT, int NSLOT, bool WIN, bool SINGLE = false, int CTAS = 1>
 cudaError_t launch_spec(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                         const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, cudaStream_t s) {
     using L = DqSmem<D, NSLOT>;
-    static_assert(L::kAlloc <= 232448, "shared memory budget");
-    auto kern = bwd_dq_kernel<D, DQ, QT, NSLOT, WIN>;
+    static_assert(L::kAlloc <= 232448 / CTAS, "shared memory budget");
+    auto kern = bwd_dq_kernel<D, DQ, QT, NSLOT, WIN, SINGLE, CTAS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
     dim3 grid(((a.N + kBM - 1) / kBM) * a.H * a.B, D / DQ);
@@ -585,9 +582,16 @@ template <bool WIN>
 cudaError_t launch_width(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                          const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, cudaStream_t s) {
     switch (kernel_head_dim(a.D)) {
-        case 128: return launch_spec<128, 128, true, 8, WIN>(a, tq, tk, tv, tdo, to, tdq, s);
+        case 64:
+            if constexpr (WIN)
+                return launch_spec<64, 64, false, 6, true, true, 2>(a, tq, tk, tv, tdo, to, tdq, s);
+            else
+                return cudaErrorInvalidValue;  // bwd_dq_k128.cu
+        case 128:
+            if constexpr (!WIN) return launch_spec<128, 128, true, 8, WIN>(a, tq, tk, tv, tdo, to, tdq, s);
+            return cudaErrorInvalidValue;  // win_dq.cu
         case 192: return launch_spec<192, 192, false, 4, WIN>(a, tq, tk, tv, tdo, to, tdq, s);  // 3, 5 slots slower
-        case 256: return launch_spec<256, 256, false, 3, WIN>(a, tq, tk, tv, tdo, to, tdq, s);
+        case 256: return launch_spec<256, 256, false, 3, WIN, true>(a, tq, tk, tv, tdo, to, tdq, s);
         default: return cudaErrorInvalidValue;
     }
 }

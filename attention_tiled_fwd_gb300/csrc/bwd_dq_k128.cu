@@ -31,7 +31,6 @@
 // owning one query row (its TMEM lane).
 #include "fa_internal.h"
 #include "sm100_ptx.cuh"
-#include "win.cuh"
 #include <cmath>
 
 namespace fa {
@@ -67,9 +66,6 @@ struct K128Smem {
     static constexpr int kAlloc = kTmemHolderOff + 16 + 1024;
 };
 
-// WIN: windowed attention (win.cuh): the key tiles are those of key_span, a query head reads its group's key
-// head, and the mask is the window's.
-template <bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dq_k128_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
@@ -114,12 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q_tile = (a.N + kBM - 1) / kBM - 1 - rank;  // causal: the last query tile has the most keys
     const int N = a.N;
     const int kv_end = a.causal ? min(N, (q_tile + 1) * kBM) : N;
-    // WIN: position of the tile's first row, its key tiles, its key slice
-    const int pos0 = WIN ? a.win.Nk - N + q_tile * kBM : 0;
-    const KeySpan span = WIN ? key_span(pos0, min(a.win.Nk, pos0 + kBM) - 1, a.win.window, a.win.sinks, kBN)
-                             : KeySpan{0, 0, 0};
-    const int kv_bh = WIN ? bh / a.H * a.win.Hkv + bh % a.H / (a.H / a.win.Hkv) : bh;
-    const int n_kv = WIN ? span.n : (kv_end + kBN - 1) / kBN;  // >= 1
+    const int n_kv = (kv_end + kBN - 1) / kBN;  // >= 1
 
     if (threadIdx.x == 0) {
         epi_abort = 0;
@@ -171,8 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!mbar_wait(&slot_empty[slot], (round & 1) ^ 1, a.status, kSiteSlotEmpty)) break;
                 const CUtensorMap *map = (idx & 1) ? &tmap_v : &tmap_k;
                 mbar_arrive_expect_tx(&slot_full[slot], L::kTileBytes);
-                tma_load_3d(slots + slot * L::kTileBytes, map, &slot_full[slot], 0,
-                            WIN ? span.key0(idx >> 1, kBN) : (idx >> 1) * kBN, kv_bh);
+                tma_load_3d(slots + slot * L::kTileBytes, map, &slot_full[slot], 0, (idx >> 1) * kBN, bh);
 #pragma unroll
                 for (int s = 0; s < kNSlot; ++s)
                     if (s == slot) last_round[s] = round;
@@ -326,13 +316,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = mbar_wait(s_full, j & 1, a.status, kSiteSFull);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             tc_fence_after();
-            const int key0 = (WIN ? span.key0(j, kBN) : j * kBN) + g * kSpan;
-            const int window = WIN ? span.window_in(j, a.win.window) : 0;
-            const bool need_mask =
-                WIN ? !all_seen(pos0, pos0 + kBM - 1, key0, key0 + kSpan - 1, window, a.win.sinks)
-                    : (key0 + kSpan > N) || (a.causal && key0 + kSpan - 1 > q_tile * kBM);
-            static_assert(!WIN || kSpan == 32, "one mask word per thread and tile");
-            const uint32_t seen = WIN && need_mask ? seen_keys(pos0 + r, key0, window, a.win.sinks) : 0u;
+            const int key0 = j * kBN + g * kSpan;
+            const bool need_mask = (key0 + kSpan > N) || (a.causal && key0 + kSpan - 1 > q_tile * kBM);
             uint32_t sraw[kSpan], praw[kSpan], dsk[kSpan / 2];
             tmem_ld32(tmem + lane_base + kColS + g * kSpan, sraw);
             tmem_wait_ld();
@@ -355,8 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 p0 = ex2_approx(p0);
                 p1 = ex2_approx(p1);
                 if (need_mask) {
-                    if (WIN ? !(seen & (1u << i)) : key0 + i > lim) p0 = 0.f;
-                    if (WIN ? !(seen & (2u << i)) : key0 + i + 1 > lim) p1 = 0.f;
+                    if (key0 + i > lim) p0 = 0.f;
+                    if (key0 + i + 1 > lim) p1 = 0.f;
                 }
                 dsk[i / 2] = f2_to_bf16x2(
                     f2_mul(f2_sub(f2_pack(__uint_as_float(praw[i]), __uint_as_float(praw[i + 1])), d2), f2_pack(p0, p1)));
@@ -433,11 +418,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 cudaError_t launch_bwd_dq_k128(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                                const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq,
-                               cudaStream_t s, bool win) {
+                               cudaStream_t s) {
     using L = K128Smem;
     static_assert(L::kAlloc <= 232448, "shared memory budget");
     if (kernel_head_dim(a.D) != kD) return cudaErrorInvalidValue;
-    auto kern = win ? bwd_dq_k128_kernel<true> : bwd_dq_k128_kernel<false>;
+    auto kern = bwd_dq_k128_kernel;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
     dim3 grid(((a.N + kBM - 1) / kBM) * a.H * a.B);

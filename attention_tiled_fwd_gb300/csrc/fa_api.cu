@@ -516,17 +516,14 @@ extern "C" int fa_window_backward_dq(const void *q, const void *k, const void *v
     BwdArgs a{q, k, v, o, dO, lse, delta, dq, nullptr, nullptr, B, Hq, Nq, D, scale, scale * log2e(), 1,
               grad_dtype == FA_BF16 ? 1 : 0, st->status_word, B * Hq, window_args(Hkv, Nk, window, sinks)};
     CUtensorMap tq, tk, tv, tdo, to, tdq;
-    const int Dk = kernel_head_dim(D);
-    const int kv_box = Dk == 64 ? 128 : kDqKRows;
     if (encode_rows(&tq, q, B * Hq, Nq, Nq, D, 128) != FA_OK ||
-        encode_rows(&tk, k, B * Hkv, Nk, Nk, D, kv_box) != FA_OK ||
-        encode_rows(&tv, v, B * Hkv, Nk, Nk, D, kv_box) != FA_OK ||
+        encode_rows(&tk, k, B * Hkv, Nk, Nk, D, kDqKRows) != FA_OK ||
+        encode_rows(&tv, v, B * Hkv, Nk, Nk, D, kDqKRows) != FA_OK ||
         encode_rows(&tdo, dO, B * Hq, Nq, Nq, D, 128) != FA_OK || encode_rows(&to, o, B * Hq, Nq, Nq, D, 128) != FA_OK ||
         encode_3d(&tdq, dq, B * Hq, Nq, D, 128, grad_dtype == FA_F32) != FA_OK)
         return FA_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = Dk == 64 ? launch_bwd_dq_k128(a, tq, tk, tv, tdo, to, tdq, s, true)
-                             : launch_bwd_dq(a, tq, tk, tv, tdo, to, tdq, s, true);
+    cudaError_t e = launch_win_dq(a, tq, tk, tv, tdo, to, tdq, st->num_sms, s);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -230,8 +230,7 @@ cudaError_t launch_bwd_dq(const BwdArgs &a, const CUtensorMap &tq, const CUtenso
 // bwd_dq_k128.cu: the dQ kernel for D = 64 with 128-row K / V tiles (TMA boxes of 128 rows)
 cudaError_t launch_bwd_dq_k128(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk,
                                const CUtensorMap &tv, const CUtensorMap &tdo, const CUtensorMap &to,
-                               const CUtensorMap &tdq, cudaStream_t s,
-                          bool win = false);
+                               const CUtensorMap &tdq, cudaStream_t s);
 // The dK/dV kernels also take dK's and dV's tensor maps (grad dtype, 128-byte boxes of 128 rows, 128-byte
 // swizzle: the TMA stores of the epilogue).
 // bwd_dkdv_q128.cu: the dK/dV kernel for D = 64 with 128-row Q / dO tiles (TMA boxes of 128 rows)
@@ -244,6 +243,9 @@ cudaError_t launch_bwd_dkdv(const BwdArgs &a, const CUtensorMap &tq, const CUten
                           const CUtensorMap *parts = nullptr);
 // Windowed (parts != null): parts[0], parts[1] are the tensor maps of the sink tiles' fp32 partials of dK and dV
 // ([part][128][D], 32-column boxes); launch_sink_sum adds them.
+cudaError_t launch_win_dq(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                          const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, int num_sms,
+                          cudaStream_t s);
 cudaError_t launch_win_dkdv(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                             const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv,
                             const CUtensorMap *parts, int num_sms, cudaStream_t s);

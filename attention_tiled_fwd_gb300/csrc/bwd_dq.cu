@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
             const int key0 = (WIN ? span.key0(j, kBN) : j * kBN) + g * kHalf;
             const int window = WIN ? span.window_in(j, a.win.window) : 0;
             const bool need_mask =
-                WIN ? !all_seen(pos0, pos0 + kBM - 1, key0, key0 + kHalf - 1, window, a.win.sinks)
+                WIN ? !all_seen(pos0 + quarter * 32, pos0 + quarter * 32 + 31, key0, key0 + kHalf - 1, window, a.win.sinks)
                     : (key0 + kHalf > N) || (a.causal && key0 + kHalf - 1 > q_tile * kBM);
             static_assert(!WIN || kHalf == 32, "one mask word per thread and tile");
             const uint32_t seen = WIN && need_mask ? seen_keys(pos0 + r, key0, window, a.win.sinks) : 0u;

@@ -305,7 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 static_assert(!kSpan || HB == 32, "one mask word per half tile");
                 const int p0 = a.Nk - N + q_tile * kBM, window = span.window_in(j, a.window);
                 const bool need_mask = PREFIX ? key0 + HB > N
-                                              : !all_seen(p0, p0 + kBM - 1, key0, key0 + HB - 1, window, a.sinks);
+                                              : !all_seen(p0 + quarter * 32, p0 + quarter * 32 + 31, key0, key0 + HB - 1,
+                                                        window, a.sinks);
                 if (need_mask) {
                     const uint32_t seen = PREFIX ? low_bits(N - key0) : seen_keys(p0 + r, key0, window, a.sinks);
 #pragma unroll

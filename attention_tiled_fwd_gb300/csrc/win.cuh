@@ -50,6 +50,11 @@ __host__ __device__ inline bool all_seen(int p0, int p1, int k0, int k1, int win
     return k1 <= p0 && (k0 > p1 - window || k1 < sinks);
 }
 
+// none of positions p0 .. p1 sees any of keys k0 .. k1
+__host__ __device__ inline bool none_seen(int p0, int p1, int k0, int k1, int window, int sinks) {
+    return k0 > p1 || (k1 <= p0 - window && k0 >= sinks);
+}
+
 // bit i: the position p0 + i sees key (i < 32)
 __host__ __device__ inline uint32_t seeing_positions(int key, int p0, int window, int sinks) {
     return ~low_bits(key - p0) & (key < sinks ? ~0u : low_bits(key + window - p0));

@@ -419,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const int key0 = w.span.key0(j, kBN) + g * kHalf;
                 const int window = w.span.window_in(j, a.win.window);
-                const bool need_mask = !all_seen(w.pos0, w.pos0 + kBM - 1, key0, key0 + kHalf - 1, window, a.win.sinks);
+                const bool need_mask = !all_seen(w.pos0 + quarter * 32, w.pos0 + quarter * 32 + 31, key0, key0 + kHalf - 1,
+                                                  window, a.win.sinks);
                 static_assert(kHalf == 32, "one mask word per thread and tile");
                 const uint32_t seen = need_mask ? seen_keys(w.pos0 + r, key0, window, a.win.sinks) : 0u;
                 // dS[b] was last read by the dQ product of step t-2

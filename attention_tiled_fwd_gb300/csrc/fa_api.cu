@@ -648,14 +648,14 @@ extern "C" int fa_window_decode(const void *q, const void *k, const void *v, con
     float *part_o = need > 0 ? static_cast<float *>(workspace) : nullptr;
     float2 *part_ml = need > 0 ? reinterpret_cast<float2 *>(part_o + rows * splits * D) : nullptr;
     WinDecodeArgs a{q, lens, o, lse, B, Hkv, Hq / Hkv * n_q, n_q, N, D, w.window, w.sinks, scale * log2e(),
-                    st->status_word, splits, splits, 0, part_o, part_ml};
+                    st->status_word, splits, splits, 0, part_o, part_ml, part_o == nullptr, 0};
     CUtensorMap tk, tv;
     if (encode_rows(&tk, k, B * Hkv, N, N, D, win_decode_tile_keys()) != FA_OK ||
         encode_rows(&tv, v, B * Hkv, N, N, D, win_decode_tile_keys()) != FA_OK)
         return FA_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = launch_win_decode(a, tk, tv, s);
-    if (e == cudaSuccess && part_o) e = launch_win_join(part_o, part_ml, o, lse, (long long)rows, splits, D, s);
+    if (e == cudaSuccess && part_o) e = launch_win_join(part_o, part_ml, o, lse, (long long)rows, splits, D, true, s);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -664,7 +664,8 @@ namespace {
 // own caches into `own` CTAs each.
 struct PrefixPlan {
     int R, rb, nb, m_tiles, splits, chunk_tiles, own;
-    int slots() const { return splits + own; }
+    // with one CTA per sequence and key head for the own cache, that CTA joins the prefix's partials
+    int slots() const { return splits + (own > 1 ? own : 0); }
 };
 
 PrefixPlan prefix_plan(int B, int Hq, int Hkv, int n_q, int P, int N, int D, int num_sms) {
@@ -758,10 +759,10 @@ extern "C" int fa_prefix_decode(const void *q, const void *k_prefix, const void 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = launch_win_fwd(a, tq, tkp, tvp, tkp, tvp, tkp, s);
     if (e != cudaSuccess) return FA_ERR_CUDA;
-    WinDecodeArgs d{q, lens, nullptr, nullptr, B, Hkv, p.R, n_q, N, D, N, 0, scale * log2e(), st->status_word, p.own,
-                    p.slots(), p.splits, part_o, part_ml};
+    WinDecodeArgs d{q, lens, o, lse, B, Hkv, p.R, n_q, N, D, N, 0, scale * log2e(), st->status_word, p.own,
+                    p.slots(), p.splits, part_o, part_ml, p.own == 1, 1};
     e = launch_win_decode(d, tk, tv, s);
-    if (e == cudaSuccess) e = launch_win_join(part_o, part_ml, o, lse, (long long)rows, p.slots(), D, s);
+    if (e == cudaSuccess && p.own > 1) e = launch_win_join(part_o, part_ml, o, lse, (long long)rows, p.slots(), D, false, s);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -156,6 +156,21 @@ __device__ __forceinline__ void st_shared_v4(void *p, uint32_t a, uint32_t b, ui
                  : "memory");
 }
 
+// ---------------------------------------------------------------- dependent launches
+// Lets a kernel launched behind this one as its programmatic dependent start as SMs become free (its own
+// launch_dependent_wait still waits for this grid's end).
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Waits until the grid that this one was launched behind has ended and its writes are visible (at once when there is
+// none).
+__device__ __forceinline__ void launch_dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// 32-byte store (one whole sector a lane)
+__device__ __forceinline__ void st_global_v8(float *p, const uint32_t *r) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // ---------------------------------------------------------------- tcgen05 / TMEM
 __device__ __forceinline__ void tmem_alloc(uint32_t *smem_result, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(

@@ -18,7 +18,9 @@
 //              (no exchange inside the loop); the four states are joined at the end
 // A sequence's tiles are dealt to `splits` CTAs by its own length (read on the
 // device), and win_join_kernel joins their partials; with one split the CTA
-// writes O and L itself and that launch falls away.
+// writes O and L itself and that launch falls away.  Behind a shared prefix it
+// first joins the prefix's partials; it is launched as that kernel's programmatic
+// dependent, so its loads and products run in the prefix kernel's tail.
 // Keys outside [0, len), between the sinks and the window, or past a sink tile's
 // last sink may hold anything (a cache's unwritten rows): their scores are
 // replaced and their V rows cleared before the products.
@@ -255,6 +257,8 @@ __global__ void __launch_bounds__(kThreads)
         }
     }
     __syncthreads();
+    if (a.behind) launch_dependent_wait();  // every CTA: this grid must not end before the one it runs behind
+    else launch_dependents();
     for (int idx = threadIdx.x; idx < kRowTile * (D / 4); idx += kThreads) {
         const int r = idx / (D / 4), c = idx % (D / 4) * 4;
         const int rr = rt * kRowTile + r;
@@ -277,12 +281,33 @@ __global__ void __launch_bounds__(kThreads)
             acc.w = fmaf(v.w, f, acc.w);
         }
         const size_t row = (size_t)kv * a.R + rr;
-        if (a.part_o) {
+        if (!a.join) {
             const size_t slot = row * a.slots + a.slot0 + split;
             // a chunk that the row sees nothing of: m = -inf, l = 0, and its O is not read
             if (M != -INFINITY) *reinterpret_cast<float4 *>(a.part_o + slot * D + c) = acc;
             if (c == 0) a.part_ml[slot] = make_float2(M, ls);
         } else {
+            if (a.slot0 > 0) {
+                const float2 *ml = a.part_ml + row * a.slots;
+                const float *po = a.part_o + row * a.slots * D + c;
+                float Mn = M;
+                for (int s = 0; s < a.slot0; ++s) Mn = fmaxf(Mn, ml[s].x);  // a prefix chunk's m is finite
+                const float f0 = ex2_approx(M - Mn);
+                ls *= f0;
+                acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
+                M = Mn;
+#pragma unroll 8
+                for (int s = 0; s < a.slot0; ++s) {
+                    const float2 t = ml[s];
+                    const float f = ex2_approx(t.x - Mn);
+                    const float4 v = *reinterpret_cast<const float4 *>(po + (size_t)s * D);
+                    ls = fmaf(t.y, f, ls);
+                    acc.x = fmaf(v.x, f, acc.x);
+                    acc.y = fmaf(v.y, f, acc.y);
+                    acc.z = fmaf(v.z, f, acc.z);
+                    acc.w = fmaf(v.w, f, acc.w);
+                }
+            }
             const float inv = ls > 0.f ? 1.f / ls : 0.f;
             uint2 w;
             w.x = pack_bf16x2(acc.x * inv, acc.y * inv);
@@ -298,6 +323,7 @@ template <int D>
 __global__ void __launch_bounds__(128) win_join_kernel(const float *part_o, const float2 *part_ml, void *o, float *lse,
                                                        long long rows, int slots) {
     constexpr int V = D / 32;
+    launch_dependent_wait();
     const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (row >= rows) return;
@@ -328,14 +354,30 @@ __global__ void __launch_bounds__(128) win_join_kernel(const float *part_o, cons
     if (lane == 0) lse[row] = (M + __log2f(l)) * 0.69314718055994531f;
 }
 
+// A launch, or (behind) one as the programmatic dependent of the launch before it on the stream.
+template <class... Params, class... Args>
+cudaError_t launch_behind(void (*kern)(Params...), dim3 grid, int threads, size_t smem, bool behind, cudaStream_t s,
+                          Args... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = behind ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, Params(args)...);
+}
+
 template <int D>
 cudaError_t launch_decode_d(const WinDecodeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s) {
     auto kern = win_decode_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DecSmem<D>::kAlloc);
     if (e != cudaSuccess) return e;
     const int row_tiles = (a.R + kRowTile - 1) / kRowTile;
-    kern<<<dim3(row_tiles * a.splits, a.Hkv, a.B), kThreads, DecSmem<D>::kAlloc, s>>>(tk, tv, a);
-    return cudaGetLastError();
+    return launch_behind(kern, dim3(row_tiles * a.splits, a.Hkv, a.B), kThreads, DecSmem<D>::kAlloc, a.behind, s, tk, tv, a);
 }
 
 // CTAs an SM holds at once (shared memory: 65 KB at D = 64, 97 KB at 128, 193 KB at 256)
@@ -366,15 +408,9 @@ cudaError_t launch_win_decode(const WinDecodeArgs &a, const CUtensorMap &tk, con
 }
 
 cudaError_t launch_win_join(const float *part_o, const float2 *part_ml, void *o, float *lse, long long rows, int slots,
-                            int D, cudaStream_t s) {
-    const unsigned grid = (unsigned)((rows + 3) / 4);
-    switch (D) {
-        case 64: win_join_kernel<64><<<grid, 128, 0, s>>>(part_o, part_ml, o, lse, rows, slots); break;
-        case 128: win_join_kernel<128><<<grid, 128, 0, s>>>(part_o, part_ml, o, lse, rows, slots); break;
-        case 256: win_join_kernel<256><<<grid, 128, 0, s>>>(part_o, part_ml, o, lse, rows, slots); break;
-        default: return cudaErrorInvalidValue;
-    }
-    return cudaGetLastError();
+                            int D, bool behind, cudaStream_t s) {
+    auto kern = D == 64 ? win_join_kernel<64> : D == 128 ? win_join_kernel<128> : win_join_kernel<256>;
+    return launch_behind(kern, dim3((unsigned)((rows + 3) / 4)), 128, 0, behind, s, part_o, part_ml, o, lse, rows, slots);
 }
 
 }  // namespace fa

@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if constexpr (PREFIX) launch_dependents();
     const uint32_t tmem = *tmem_holder;
 
     if (warp == 0) {
@@ -520,10 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         warp_arrive(&o_free[x]);
                     }
                     if (valid) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(a.part_o + slot * D + ch * 32);
 #pragma unroll
-                        for (int v4 = 0; v4 < 8; ++v4)
-                            dst[v4] = make_uint4(ov[4 * v4], ov[4 * v4 + 1], ov[4 * v4 + 2], ov[4 * v4 + 3]);
+                        for (int v8 = 0; v8 < 4; ++v8) st_global_v8(a.part_o + slot * D + ch * 32 + 8 * v8, ov + 8 * v8);
                     }
                 }
                 if (valid) a.part_ml[slot] = make_float2(m, l);

@@ -158,6 +158,20 @@ __device__ __forceinline__ WinKeyItem win_key_item(const BwdArgs &a, int x, int 
     return w;
 }
 
+// Walks an item's tiles without a division per tile: row of the tile, and its query slice (batch and head).
+struct WinRowWalk {
+    int h, slice, per_head;
+    __device__ __forceinline__ WinRowWalk(const BwdArgs &a, const WinKeyItem &w)
+        : h(w.n > 0 ? w.i0 % w.rows.per_head : 0),
+          slice(w.bh * (a.H / a.win.Hkv) + (w.n > 0 ? w.i0 / w.rows.per_head : 0)), per_head(w.rows.per_head) {}
+    __device__ __forceinline__ void next() {
+        if (++h == per_head) {
+            h = 0;
+            ++slice;
+        }
+    }
+};
+
 // Query slice (batch and query head) of tile i of key slice kv_bh.
 __device__ __forceinline__ int win_query_slice(const BwdArgs &a, int kv_bh, const WinRows &rows, int i) {
     return kv_bh * (a.H / a.win.Hkv) + i / rows.per_head;

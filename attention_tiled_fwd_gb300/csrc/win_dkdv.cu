@@ -31,16 +31,17 @@ constexpr int kBN = 128;  // keys per item (TMEM lanes)
 constexpr int kComputeWG = 4;
 constexpr int kFirstComputeWarp = 3;
 constexpr int kComputeWarps = 4 * kComputeWG;
-constexpr int kThreads = 32 * (kFirstComputeWarp + kComputeWarps);
+constexpr int kStoreWarp = kFirstComputeWarp + kComputeWarps;
+constexpr int kThreads = 32 * (kStoreWarp + 1);
 
 enum : int { kSiteKV = 221, kSiteSlotEmpty, kSiteSlotFull, kSiteSFull, kSitePReady, kSiteDpFull, kSiteDsReady, kSiteDone,
-             kSiteFinal, kSiteDrain, kSiteStats, kSiteBuf, kSiteDpFree, kSiteAcc, kSiteKVEmpty };
+             kSiteFinal, kSiteDrain, kSiteStats, kSiteBuf, kSiteDpFree, kSiteAcc, kSiteKVEmpty, kSiteStage };
 
 template <int D>
 struct Dkdv {
     static constexpr int kBQ = D == 64 ? 128 : 64;        // queries per tile
     static constexpr int kSlots = D == 64 ? 9 : 6;        // Q_i / dO_i ring
-    static constexpr int kStats = D == 64 ? 2 : 3;        // query tiles' L / D in flight
+    static constexpr int kStats = 2;                      // query tiles' L / D in flight: one beside each S^T buffer
     static constexpr int kSpan = kBQ / kComputeWG;        // queries per compute thread and tile
     static constexpr int kDpBufs = D == 64 ? 1 : 2;
     // TMEM columns: S^T[2], dP^T[kDpBufs] (kBQ each), dV, dK (D each).  P^T (bf16) goes over the first half of each
@@ -54,8 +55,8 @@ struct Dkdv {
     static constexpr int kStatOff = kSlotOff + kSlots * kTileBytes;  // [kStats][L kBQ | D kBQ] fp32
     static constexpr int kBarOff = kStatOff + kStats * 2 * kBQ * 4;
     // kv_full[2], kv_empty[2], slot_full/empty[kSlots], s_full[2], dp_full[2], p_ready[2], ds_ready[2], dv_done[2],
-    // dk_done[2], stat_full/empty[kStats], dp_free, acc_full, acc_free, final, a_final
-    static constexpr int kNumBars = 4 + 2 * kSlots + 12 + 2 * kStats + 5;
+    // dk_done[2], stat_empty[kStats], dp_free, acc_full, acc_free, stage_full, stage_free, final, a_final
+    static constexpr int kNumBars = 4 + 2 * kSlots + 12 + kStats + 7;
     static constexpr int kTmemHolderOff = kBarOff + kNumBars * 8;
     static constexpr int kAlloc = kTmemHolderOff + 16 + 1024;
     static_assert(kAlloc <= 232448, "shared memory budget");
@@ -82,18 +83,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *kv_empty = kv_full + 2;           // [2]: item n's gradients, staged over K and V, have been stored
     uint64_t *slot_full = kv_empty + 2;
     uint64_t *slot_empty = slot_full + NSLOT;
-    uint64_t *s_full = slot_empty + NSLOT;      // [2]; steps t are counted across items, buffer b = t % 2
+    // [2]: S^T of step t is complete and the tile's L and D have landed (steps counted across items, b = t % 2)
+    uint64_t *s_full = slot_empty + NSLOT;
     uint64_t *dp_full = s_full + 2;             // [kDpBufs]
     uint64_t *p_ready = dp_full + 2;            // [2]
     uint64_t *ds_ready = p_ready + 2;           // [2]
     uint64_t *dv_done = ds_ready + 2;           // [2]
     uint64_t *dk_done = dv_done + 2;            // [2]: and dV of that step (one issuer thread)
-    uint64_t *stat_full = dk_done + 2;          // [kStats]
-    uint64_t *stat_empty = stat_full + C::kStats;
+    uint64_t *stat_empty = dk_done + 2;         // [2]: every compute warp has read step t's L and D
     uint64_t *dp_free = stat_empty + C::kStats;  // one dP^T buffer: every compute warp has loaded it
     uint64_t *acc_full = dp_free + 1;            // item n's dV and dK are complete
     uint64_t *acc_free = acc_full + 1;           // every compute warp has read them
-    uint64_t *final_bar = acc_free + 1;
+    uint64_t *stage_full = acc_free + 1;         // every compute warp has staged its share of a gradient store
+    uint64_t *stage_free = stage_full + 1;       // that store has read it
+    uint64_t *final_bar = stage_free + 1;
     uint64_t *a_final = final_bar + 1;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::kTmemHolderOff);
 
@@ -103,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(&kv_full[b], 1);
             mbar_init(&kv_empty[b], 1);
-            mbar_init(&s_full[b], 1);
+            mbar_init(&s_full[b], 1 + 32);  // the commit, and one arrival per producer lane, when its copies have landed
             mbar_init(&dp_full[b], 1);
             mbar_init(&p_ready[b], kComputeWarps);  // one arrive per compute warp
             mbar_init(&ds_ready[b], kComputeWarps);
@@ -115,12 +118,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&slot_empty[s], 1);
         }
         for (int t = 0; t < C::kStats; ++t) {
-            mbar_init(&stat_full[t], 32);  // one arrival per producer lane, when its copies have landed
             mbar_init(&stat_empty[t], kComputeWarps);
         }
         mbar_init(dp_free, kComputeWarps);
         mbar_init(acc_full, 1);
         mbar_init(acc_free, kComputeWarps);
+        mbar_init(stage_full, kComputeWarps);
+        mbar_init(stage_free, 1);
         mbar_init(final_bar, 1);
         mbar_init(a_final, 1);
         fence_mbarrier_init();
@@ -163,9 +167,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             ++n;
-            for (int i = 0; ok && i < w.n; ++i, ++t) {
-                const int q0 = w.rows.row0(w.i0 + i, kBQ);
-                const int slice = win_query_slice(a, w.bh, w.rows, w.i0 + i);
+            WinRowWalk at(a, w);
+            for (int i = 0; ok && i < w.n; ++i, ++t, at.next()) {
+                const int q0 = w.rows.first + at.h * kBQ, slice = at.slice;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {  // Q_i, dO_i
                     const int idx = 2 * t + h, slot = idx % NSLOT, round = idx / NSLOT;
@@ -196,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  "l"((is_l ? a.lse : a.delta) + (size_t)slice * N + (valid ? q : 0)), "r"(valid ? 4 : 0)
                                  : "memory");
                 }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&stat_full[ss]))
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&s_full[ss]))
                              : "memory");
             }
         }
@@ -324,6 +328,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (leader) mma_commit(final_bar);
         __syncwarp();
         warp_wait(final_bar, 0, a.status, kSiteFinal);
+    } else if (warp == kStoreWarp) {
+        // Stores the gradients that the compute warps stage over an item's K and V, then hands that memory back.
+        if (lane == 0) {
+            bool ok = true;
+            int n = 0, stores = 0;
+            for (int k = 0; ok && k * (int)gridDim.x < n_items; ++k) {
+                const int x = persistent_work_index(k, n_items);
+                if (x < 0) continue;
+                const WinKeyItem w = win_key_item(a, x, kBN, kBQ);
+                const bool partial = w.part >= 0, out_bf16 = a.grad_bf16 && !partial;
+                const uint8_t *stage = smem + (n & 1) * 2 * C::kKVBytes;
+                const int y = partial ? 0 : w.k_tile * kBN, z = partial ? w.part : w.bh;
+                const int pw = out_bf16 ? 64 : 32, panels = D / pw;
+                for (int which = out_bf16 ? 1 : 0; which < 2; ++which, ++stores) {
+                    if (!(ok = mbar_wait(stage_full, stores & 1, a.status, kSiteStage))) break;
+                    const CUtensorMap *m = which ? (partial ? &tmap_pk : &tmap_dk) : (partial ? &tmap_pv : &tmap_dv);
+                    for (int p = 0; p < panels && p * pw < a.D; ++p) {
+                        if (out_bf16) tma_store_3d(&tmap_dv, stage + p * (kBN * 128), p * pw, y, z);
+                        tma_store_3d(m, stage + (out_bf16 ? C::kKVBytes : 0) + p * (kBN * 128), p * pw, y, z);
+                    }
+                    tma_store_commit();
+                    tma_store_wait_read();  // (and the CTA's shared memory must outlive the reads)
+                    mbar_arrive(stage_free);
+                }
+                if (ok) mbar_arrive(&kv_empty[n & 1]);
+                ++n;
+            }
+        }
+        __syncwarp();
     } else {
         const int quarter = warp & 3;
         const int g = (warp - kFirstComputeWarp) >> 2;  // query range of every tile
@@ -332,23 +365,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr float kLog2e = 1.4426950408889634f;
         const uint64_t c2 = f2_pack(a.scale_log2, a.scale_log2), nlog2e2 = f2_pack(-kLog2e, -kLog2e);
         bool ok = true;
-        int n = 0, t = 0;
-        for (int k = 0; ok && k * (int)gridDim.x < n_items; ++k) {
-            const int x = persistent_work_index(k, n_items);
-            if (x < 0) continue;
-            const WinKeyItem w = win_key_item(a, x, kBN, kBQ);
+        int n = 0, t = 0, stores = 0;
+        const int off = a.win.Nk - N;
+        // the next item is worked out while the current one's last products run
+        int k = 0;
+        auto next_item = [&](WinKeyItem *w) {
+            for (; k * (int)gridDim.x < n_items; ++k) {
+                const int x = persistent_work_index(k, n_items);
+                if (x < 0) continue;
+                *w = win_key_item(a, x, kBN, kBQ);
+                ++k;
+                return true;
+            }
+            return false;
+        };
+        WinKeyItem w;
+        bool more = next_item(&w);
+        while (ok && more) {
+            // the rows that see this thread's key: [lo, hi)
             const int key = w.k_tile * kBN + r;
-            for (int i = 0; i < w.n; ++i, ++t) {
+            const int lo = key - off;
+            const int hi = key >= a.win.Nk ? 0 : key < a.win.sinks ? N : min(N, key - off + a.win.window);
+            WinRowWalk at(a, w);
+            for (int i = 0; i < w.n; ++i, ++t, at.next()) {
                 const uint32_t b = t & 1, db = C::kDpBufs == 1 ? 0 : b;
-                const int ss = t % C::kStats;
-                ok = mbar_wait(&stat_full[ss], (t / C::kStats) & 1, a.status, kSiteStats);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                const float4 *ls4 = reinterpret_cast<const float4 *>(stat_s + ss * 2 * kBQ + g * kSpan);
-                const float4 *ds4 = reinterpret_cast<const float4 *>(stat_s + ss * 2 * kBQ + kBQ + g * kSpan);
-                const int q0 = w.rows.row0(w.i0 + i, kBQ) + g * kSpan;  // first query of this thread's range
-                const bool need_mask = q0 + kSpan > N || !sees_all(a, key, q0, kSpan);
-                const bool any_mask = __any_sync(0xffffffffu, need_mask);
-                const uint32_t seen = any_mask ? seen_by(a, key, q0) : 0u;
+                const float4 *ls4 = reinterpret_cast<const float4 *>(stat_s + b * 2 * kBQ + g * kSpan);
+                const float4 *ds4 = reinterpret_cast<const float4 *>(stat_s + b * 2 * kBQ + kBQ + g * kSpan);
+                const int q0 = w.rows.first + at.h * kBQ + g * kSpan;  // first query of this thread's range
+                const bool any_mask = __any_sync(0xffffffffu, q0 < lo || q0 + kSpan > hi);
 
                 ok = mbar_wait(&s_full[b], (t >> 1) & 1, a.status, kSiteSFull);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -374,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) p[e] = ex2_approx(p[e]);
                         if (any_mask) {
+                            const uint32_t seen = ~low_bits(lo - q0) & low_bits(hi - q0);
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 if (!(seen & (1u << (4 * q4 + e)))) p[e] = 0.f;
@@ -417,29 +462,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(&ds_ready[b]);
-                warp_arrive(&stat_empty[ss]);  // this warp has read the tile's L and D
+                warp_arrive(&stat_empty[b]);  // this warp has read the tile's L and D
             }
+            WinKeyItem nw;
+            more = next_item(&nw);
             if (ok) ok = mbar_wait(acc_full, n & 1, a.status, kSiteDone);
             // K and V have landed (with no query tile nothing has waited for them): their memory is the staging area
             if (ok) ok = mbar_wait(&kv_full[n & 1], (n >> 1) & 1, a.status, kSiteKV);
-            // a wait that ran out in one warp ends the loop in all of them (they meet at the barriers below)
-            int go;
-            asm volatile(
-                "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, %2, p;\n\t"
-                "selp.s32 %0, 1, 0, q;\n\t}"
-                : "=r"(go)
-                : "r"((int)ok), "r"(32 * kComputeWarps)
-                : "memory");
-            if (!go) { ok = false; break; }
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             tc_fence_after();
             // Epilogue: dV, then dK (times the scale its dS^T left out) as 128-byte-swizzled panels of 128 rows (64
-            // bf16 or 32 fp32 columns) over this item's K and V, written by TMA stores that clip rows past Nk and
-            // columns past the caller's D.  bf16: V's half and K's half, one store round; fp32 fills the area twice.
-            const bool partial = w.part >= 0, out_bf16 = a.grad_bf16 && !partial;
+            // bf16 or 32 fp32 columns) over this item's K and V, for the store warp's TMA stores, which clip rows past Nk
+            // and columns past the caller's D.  bf16: both in one store; fp32 fills the area twice.
+            const bool out_bf16 = a.grad_bf16 && w.part < 0;
             uint8_t *stage = smem + (n & 1) * 2 * C::kKVBytes;
             constexpr int kCols = D / kComputeWG;  // this warpgroup's columns of each gradient (16 or 32)
             const int c0 = g * kCols, sw = r & 7;
-            const int pw = out_bf16 ? 64 : 32, panels = D / pw;
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
                 uint8_t *area = stage + (out_bf16 ? which * C::kKVBytes : 0) + r * 128;
@@ -449,11 +487,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (which == 1) {
                     tc_fence_before();
                     warp_arrive(acc_free);
-                    if (!out_bf16) {
-                        // dV's store has read the area
-                        if (threadIdx.x == 32 * kFirstComputeWarp) tma_store_wait_read();
-                        asm volatile("bar.sync 1, %0;" ::"r"(32 * kComputeWarps) : "memory");
-                    }
+                }
+                // The store before has read its area (of this item's: the same one).  Every store's phase is waited
+                // for: a phase passed over would let a later wait through one store early.
+                if ((which == 0 || !out_bf16) && stores >= 1) {
+                    ok = mbar_wait(stage_free, (stores - 1) & 1, a.status, kSiteStage);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 }
                 const float osc = which ? a.scale : 1.f;
 #pragma unroll
@@ -477,22 +516,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (which == 1 || !out_bf16) {
                     fence_proxy_async_smem();  // the staged tile is read by the TMA (async proxy)
-                    asm volatile("bar.sync 1, %0;" ::"r"(32 * kComputeWarps) : "memory");
-                    if (threadIdx.x == 32 * kFirstComputeWarp) {
-                        const int y = partial ? 0 : w.k_tile * kBN, z = partial ? w.part : w.bh;
-                        for (int p = 0; p < panels && p * pw < a.D; ++p) {
-                            if (out_bf16) tma_store_3d(&tmap_dv, stage + p * (kBN * 128), p * pw, y, z);
-                            const CUtensorMap *m = which ? (partial ? &tmap_pk : &tmap_dk) : (partial ? &tmap_pv : &tmap_dv);
-                            tma_store_3d(m, stage + (out_bf16 ? C::kKVBytes : 0) + p * (kBN * 128), p * pw, y, z);
-                        }
-                        tma_store_commit();
-                    }
+                    warp_arrive(stage_full);
+                    ++stores;
                 }
             }
-            if (threadIdx.x == 32 * kFirstComputeWarp) {
-                tma_store_wait_read();
-                mbar_arrive(&kv_empty[n & 1]);
-            }
+            w = nw;
             ++n;
         }
     }

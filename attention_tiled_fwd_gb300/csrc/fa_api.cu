@@ -485,7 +485,9 @@ extern "C" int fa_window_forward(const void *q, const void *k, const void *v, vo
     a.scale_log2 = scale * log2e();
     a.status = st->status_word;
     a.num_sms = st->num_sms;
-    a.pairing = window_pairing(B, Hq, Hkv, Nq, st->num_sms);
+    a.pairing = win_fwd_tiles(D) == 1 ? kOneTile : window_pairing(B, Hq, Hkv, Nq, st->num_sms);
+    const int heads = a.pairing == kTwoHeads ? Hq / 2 : Hq;
+    a.per_rows = FastDiv(B * heads), a.per_seq = FastDiv(heads), a.group = FastDiv(Hq / Hkv);
     // sink tiles read through maps that end at the last sink
     const int bn = fwd_block_n(kernel_head_dim(D)), sink_rows = w.sinks > 0 ? w.sinks : Nk;
     CUtensorMap tq, tk, tv, tks, tvs, to;

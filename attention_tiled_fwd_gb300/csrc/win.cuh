@@ -71,6 +71,21 @@ struct WinArgs {
     int sink_tiles, chunks;
 };
 
+// Division of 0 <= n < 2^31 by a number that the host knows: n / d = (mulhi(n, mul) + n) >> shift.
+struct FastDiv {
+    uint32_t d, mul, shift;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t by) : d(by), mul(0), shift(0) {
+        while ((1ull << shift) < by) ++shift;
+        mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - by)) / by + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int div(int n) const {
+        return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
+    }
+#endif
+};
+
 // The forward over the keys that a span of query rows sees (win_fwd.cu, and fwd_bf16.cu for wide heads).
 // Two forms: windowed attention writes O and LSE; the shared-prefix form packs the rows of all sequences
 // into 128-row tiles, sees every key, and writes unnormalised O, m and l partials of key chunks.
@@ -82,8 +97,10 @@ struct SpanArgs {
     float scale_log2;
     int *status;
     int num_sms;
-    // windowed: how a block's two query tiles are chosen (kOneTile, kTwoHeads, kTwoRowTiles)
+    // windowed: how a block's two query tiles are chosen (kOneTile, kTwoHeads, kTwoRowTiles); blocks of a row range
+    // (B x heads or head pairs), heads or head pairs of a sequence, query heads of a key head
     int pairing;
+    FastDiv per_rows, per_seq, group;
     // shared prefix: R = rows per (sequence, key head); a 128-row tile holds rb rows of each of nb sequences
     int R, rb, nb, m_tiles;
     int splits, chunk_tiles;  // key chunks, key tiles per chunk
@@ -91,6 +108,8 @@ struct SpanArgs {
     float *part_o;            // [rows][slots][D]
     float2 *part_ml;          // [rows][slots] (m in log2 units, l)
 };
+// Query tiles of a CTA of the windowed forward at head dimension D (one: two CTAs share an SM).
+inline int win_fwd_tiles(int D) { return D <= 64 ? 1 : 2; }
 enum : int { kOneTile = 0, kTwoHeads = 1, kTwoRowTiles = 2 };
 
 cudaError_t launch_win_fwd(const SpanArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,

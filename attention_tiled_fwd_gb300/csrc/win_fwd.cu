@@ -30,31 +30,36 @@ namespace {
 
 constexpr int kBM = 128;            // rows per query tile (TMEM lanes)
 constexpr int kBN = 128;            // keys per K/V tile
-constexpr int kTiles = 2;           // query tiles per CTA
 constexpr int kFirstSoftmaxWarp = 2;
-constexpr int kThreads = 32 * kFirstSoftmaxWarp + 128 * kTiles;
 
 enum : int { kSiteQ = 181, kSiteSlotEmpty, kSiteSlotFull, kSiteSFull, kSitePFull, kSitePV, kSiteFinal, kSiteDrain,
-             kSiteQEmpty, kSiteOFree, kSiteStage };
+             kSiteQEmpty, kSiteOFree, kSiteStage, kSiteBlock, kSiteSFree };
 
-template <int D, int NSLOT>
+constexpr int kBlocks = 4;  // blocks that the producer has worked out ahead of the softmax warps
+
+template <int D, int NSLOT, int kTiles>
 struct SpanSmem {
     static constexpr int kPanels = D / 64;
     static constexpr int kQBytes = kBM * D * 2;    // one query tile
     static constexpr int kSlotBytes = kBN * D * 2;  // one K or V tile
+    static constexpr int kQBufs = kTiles == 1 ? 2 : 1;  // one tile a CTA: the next block's Q has a buffer of its own
+    static constexpr int kThreads = 32 * kFirstSoftmaxWarp + 128 * kTiles;
     static constexpr int kQOff = 0;
-    static constexpr int kSlotOff = kTiles * kQBytes;
+    static constexpr int kSlotOff = kQBufs * kTiles * kQBytes;
     static constexpr int kStageOff = kSlotOff + NSLOT * kSlotBytes;  // one query tile's O, staged for TMA stores
     static constexpr int kBarOff = kStageOff + kQBytes;
-    // q_full, q_empty, slot_full[NSLOT], slot_empty[NSLOT], per tile: s_full, p_full, pv_done, o_free,
-    // stage_full; final, stage_free
-    static constexpr int kNumBars = 2 + 2 * NSLOT + 5 * kTiles + 2;
+    // q_full[2], q_empty[2], slot_full[NSLOT], slot_empty[NSLOT], per tile: s_full, p_full, pv_done, o_free,
+    // stage_full; final, stage_free, s_free; block_full[kBlocks], block_empty[kBlocks]
+    static constexpr int kNumBars = 4 + 2 * NSLOT + 5 * kTiles + 3 + 2 * kBlocks;
     static constexpr int kTmemHolderOff = kBarOff + kNumBars * 8;
-    static constexpr int kAlloc = kTmemHolderOff + 16 + 1024;
+    static constexpr int kBlockOff = (kTmemHolderOff + 16 + 15) / 16 * 16;  // SoftBlock [kBlocks][kTiles], 16-byte aligned
+    static_assert(kBlockOff % 16 == 0 && kBarOff % 16 == 0, "vector accesses");
+    static constexpr int kAlloc = kBlockOff + kBlocks * kTiles * 32;  // from a 1024-byte boundary
 };
 
 // The work of one block of this CTA: the key tiles it streams, and which of them each of its two query
 // tiles reads.  Every role of the CTA walks the same sequence of blocks and computes these alike.
+template <int kTiles>
 struct SpanBlock {
     KeySpan span;             // the key tiles
     int kv_bh, y_off;         // their K/V slice, and the row that key 0 of the span sits at
@@ -71,26 +76,26 @@ struct SpanBlock {
 };
 
 // Windowed blocks in longest-first order: the last rows of every head first.
-__device__ __forceinline__ SpanBlock window_block(const SpanArgs &a, int L) {
-    SpanBlock w;
-    const int G = a.Hq / a.Hkv;
-    const int per_block = a.pairing == kTwoRowTiles ? kTiles * kBM : kBM;
+template <int kTiles>
+__device__ __forceinline__ SpanBlock<kTiles> window_block(const SpanArgs &a, int L) {
+    SpanBlock<kTiles> w;
+    const int per_block = kTiles == 2 && a.pairing == kTwoRowTiles ? 2 * kBM : kBM;
+    const bool two_heads = kTiles == 2 && a.pairing == kTwoHeads;
     const int n_blk = (a.Nq + per_block - 1) / per_block;
-    const int heads = a.pairing == kTwoHeads ? a.Hq / kTiles : a.Hq;  // head pairs, or heads
-    const int bh = L % (a.B * heads);
-    const int row0 = (n_blk - 1 - L / (a.B * heads)) * per_block;
-    const int b = bh / heads, h = (bh % heads) * (a.pairing == kTwoHeads ? kTiles : 1);
+    const int rank = a.per_rows.div(L), bh = L - rank * (int)a.per_rows.d;
+    const int row0 = (n_blk - 1 - rank) * per_block;
+    const int b = a.per_seq.div(bh), h = (bh - b * (int)a.per_seq.d) * (two_heads ? 2 : 1);
     const int off = a.Nk - a.Nq;
-    w.kv_bh = b * a.Hkv + h / G;
+    w.kv_bh = b * a.Hkv + a.group.div(h);
     w.y_off = 0;
 #pragma unroll
     for (int x = 0; x < kTiles; ++x) {
-        w.zq[x] = b * a.Hq + h + (a.pairing == kTwoHeads ? x : 0);
-        w.yq[x] = row0 + (a.pairing == kTwoRowTiles ? x * kBM : 0);
+        w.zq[x] = b * a.Hq + h + (two_heads ? x : 0);
+        w.yq[x] = row0 + (two_heads ? 0 : x * kBM);
         w.p0[x] = off + w.yq[x];
     }
-    const bool two = a.pairing == kTwoHeads || (a.pairing == kTwoRowTiles && w.yq[1] < a.Nq);
-    const int last = two ? w.yq[1] : w.yq[0];
+    const bool two = two_heads || (kTiles == 2 && a.pairing == kTwoRowTiles && w.yq[kTiles - 1] < a.Nq);
+    const int last = two ? w.yq[kTiles - 1] : w.yq[0];
     w.span = key_span(w.p0[0], off + min(a.Nq, last + kBM) - 1, a.window, a.sinks, kBN);
 #pragma unroll
     for (int x = 0; x < kTiles; ++x) {
@@ -106,8 +111,9 @@ __device__ __forceinline__ SpanBlock window_block(const SpanArgs &a, int L) {
 }
 
 // Shared-prefix blocks: two packed query tiles of a key head against one chunk of the prefix.
-__device__ __forceinline__ SpanBlock prefix_block(const SpanArgs &a, int L) {
-    SpanBlock w;
+template <int kTiles>
+__device__ __forceinline__ SpanBlock<kTiles> prefix_block(const SpanArgs &a, int L) {
+    SpanBlock<kTiles> w;
     const int pairs = (a.m_tiles + kTiles - 1) / kTiles;
     const int m = (L % pairs) * kTiles;
     const int rest = L / pairs;
@@ -129,11 +135,27 @@ __device__ __forceinline__ SpanBlock prefix_block(const SpanArgs &a, int L) {
     return w;
 }
 
-template <bool PREFIX>
-__device__ __forceinline__ SpanBlock span_block(const SpanArgs &a, int L) {
-    if constexpr (PREFIX) return prefix_block(a, L);
-    return window_block(a, L);
+template <bool PREFIX, int kTiles>
+__device__ __forceinline__ SpanBlock<kTiles> span_block(const SpanArgs &a, int L) {
+    if constexpr (PREFIX) return prefix_block<kTiles>(a, L);
+    return window_block<kTiles>(a, L);
 }
+
+// Columns of key tile j that are computed: all of them, or 32 of a sink tile whose sinks fit there.
+template <bool PREFIX>
+__device__ __forceinline__ int tile_cols(const SpanArgs &a, int n_sink, int j) {
+    return PREFIX || j >= n_sink || a.sinks - j * kBN > 32 ? kBN : 32;
+}
+
+// What the softmax of one query tile needs of a block.  The producer thread writes it, some blocks ahead: working it
+// out (a handful of divisions and ranges) took each softmax warp 1000 cycles between two blocks.
+struct __align__(16) SoftBlock {
+    int n;             // key tiles that the query tile reads (-1: no more blocks)
+    int n_sink, key0;  // the first n_sink are sink tiles; the next starts at key key0
+    int use;           // uses of the staging buffer before this tile's epilogue
+    int zq, yq, p0, kv_bh;
+};
+static_assert(sizeof(SoftBlock) == 32, "two 16-byte loads");
 
 // First sequence and first row (of the R rows of a sequence and key head) of packed query tile t.
 __device__ __forceinline__ void packed_tile(const SpanArgs &a, int t, int *b0, int *r0) {
@@ -142,35 +164,42 @@ __device__ __forceinline__ void packed_tile(const SpanArgs &a, int t, int *b0, i
     *r0 = t % row_tiles * a.rb;
 }
 
+template <int kTiles>
 __host__ __device__ inline int span_blocks(const SpanArgs &a, bool prefix) {
     if (prefix) return (a.m_tiles + kTiles - 1) / kTiles * a.splits * a.Hkv;
-    const int per_block = a.pairing == kTwoRowTiles ? kTiles * kBM : kBM;
-    return (a.Nq + per_block - 1) / per_block * (a.pairing == kTwoHeads ? a.Hq / kTiles : a.Hq) * a.B;
+    const int per_block = kTiles == 2 && a.pairing == kTwoRowTiles ? 2 * kBM : kBM;
+    return (a.Nq + per_block - 1) / per_block * (int)a.per_rows.d;
 }
 
-// Persistent: the grid has at most one CTA per SM, each walking its blocks in turn, so the next block's
+// Persistent: the grid has at most kCtas CTAs per SM, each walking its blocks in turn, so the next block's
 // Q load and first S products overlap the previous block's last products and epilogue.  The K/V ring
 // and every barrier's phase run on across blocks.
-template <int D, int NSLOT, bool PREFIX>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int NSLOT, bool PREFIX, int kTiles, int kCtas>
+__global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
     win_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_ks,
                    const __grid_constant__ CUtensorMap tmap_vs, const __grid_constant__ CUtensorMap tmap_o, SpanArgs a) {
-    using L = SpanSmem<D, NSLOT>;
+    using L = SpanSmem<D, NSLOT, kTiles>;
     constexpr int kPanels = L::kPanels;
-    constexpr uint32_t kTmemCols = 512;
-    // TMEM columns: S_A, S_B (P_X over the first kBN/2 columns of S_X), then O_A, O_B
-    constexpr uint32_t kColS = 0, kColO = kTiles * kBN;
-    static_assert(kColO + kTiles * D <= kTmemCols, "TMEM budget");
+    constexpr uint32_t kTmemCols = 512 / kCtas;
+    constexpr int kQBufs = L::kQBufs;
+    // TMEM columns: S_A, S_B (P_X over the first kBN/2 columns of S_X), then O_A, O_B.  One tile a CTA: P has columns of its
+    // own behind O, so that the next S runs while the softmax works on this one.
+    constexpr bool kOwnP = kTiles == 1;
+    constexpr uint32_t kColS = 0, kColO = kTiles * kBN, kColP = kOwnP ? kColO + D : kColS;
+    static_assert(kColO + kTiles * D + (kOwnP ? kBN / 2 : 0) <= kTmemCols, "TMEM budget");
 
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it, and there is no room to round up where two CTAs share an SM
+        if (threadIdx.x == 0) record_failure(a.status, 5 /* FA_ERR_ALIGN */, kSiteQ);
+        return;
+    }
     uint8_t *q_s = smem + L::kQOff;
     uint8_t *slots = smem + L::kSlotOff;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
-    uint64_t *q_full = bars;                // block b's Q tiles landed (phase b)
-    uint64_t *q_empty = bars + 1;           // every S MMA of block b has completed (phase b)
-    uint64_t *slot_full = bars + 2;
+    uint64_t *q_full = bars;                // [kQBufs]: block b's Q tiles landed (buffer b % kQBufs)
+    uint64_t *q_empty = bars + 2;           // [kQBufs]: every S MMA of block b has completed
+    uint64_t *slot_full = bars + 4;
     uint64_t *slot_empty = slot_full + NSLOT;
     uint64_t *s_full = slot_empty + NSLOT;  // [tile]: S_X of step g complete (phase g, steps counted across blocks)
     uint64_t *p_full = s_full + kTiles;     // [tile]: P_X of step g written (and O_X corrected)
@@ -181,15 +210,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // block tile A uses the buffer before tile B, so every role can count the uses from the blocks:
     uint64_t *stage_full = final_bar + 1;      // [tile]: the tile's four warps have written the buffer
     uint64_t *stage_free = stage_full + kTiles;  // the last store has finished reading it (phase = use)
+    uint64_t *s_free = stage_free + 1;              // kOwnP: the softmax has loaded S of step g
+    uint64_t *block_full = s_free + 1;              // [kBlocks]
+    uint64_t *block_empty = block_full + kBlocks;   // [kBlocks]: every softmax warp has read it
+    SoftBlock *soft_blocks = reinterpret_cast<SoftBlock *>(smem + L::kBlockOff);
     uint8_t *stage = smem + L::kStageOff;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kTmemHolderOff);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_work = span_blocks(a, PREFIX);
+    const int n_work = span_blocks<kTiles>(a, PREFIX);
 
     if (threadIdx.x == 0) {
-        mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
+        for (int b = 0; b < kQBufs; ++b) {
+            mbar_init(&q_full[b], 1);
+            mbar_init(&q_empty[b], 1);
+        }
         for (int s = 0; s < NSLOT; ++s) {
             mbar_init(&slot_full[s], 1);
             mbar_init(&slot_empty[s], 1);
@@ -203,6 +238,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(final_bar, 1);
         for (int x = 0; x < kTiles; ++x) mbar_init(&stage_full[x], 4);
         mbar_init(stage_free, 1);
+        mbar_init(s_free, 4);
+        for (int b = 0; b < kBlocks; ++b) {
+            mbar_init(&block_full[b], 1);
+            mbar_init(&block_empty[b], 4 * kTiles);
+        }
         fence_mbarrier_init();
     }
     if (warp == 1) {
@@ -226,37 +266,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s = 0; s < NSLOT; ++s) last_round[s] = -1;
             int gidx = 0;  // K/V loads so far (ring position)
             int nb = 0;    // blocks so far
+            int uses = 0;  // uses of the staging buffer so far
             bool ok = true;
+            auto publish = [&](const SoftBlock *sb) {  // block nb (or the end) for the softmax warps
+                const int e = nb % kBlocks;
+                if (nb >= kBlocks && !mbar_wait(&block_empty[e], (nb / kBlocks - 1) & 1, a.status, kSiteBlock)) return false;
+#pragma unroll
+                for (int x = 0; x < kTiles; ++x) soft_blocks[e * kTiles + x] = sb[x];
+                mbar_arrive(&block_full[e]);  // release: the entry is visible to the warps that wait on this phase
+                return true;
+            };
             for (int k = 0; ok && k * (int)gridDim.x < n_work; ++k) {
                 const int Lw = persistent_work_index(k, n_work);
                 if (Lw < 0) continue;
-                const SpanBlock w = span_block<PREFIX>(a, Lw);
+                const SpanBlock<kTiles> w = span_block<PREFIX, kTiles>(a, Lw);
+                SoftBlock sb[kTiles];
+#pragma unroll
+                for (int x = 0; x < kTiles; ++x)
+                    sb[x] = SoftBlock{w.n[x], w.span.n_sink, w.y_off + w.span.lo + (w.from[x] - w.span.n_sink) * kBN,
+                                      uses + (x == 1 && w.n[0] > 0), w.zq[x], w.yq[x], w.p0[x], w.kv_bh};
+#pragma unroll
+                for (int x = 0; x < kTiles; ++x) uses += w.n[x] > 0;
+                if (!(ok = publish(sb))) break;
                 // Q of this block goes after its first K and V tiles: its buffer frees only when the
                 // previous block's last S products complete, and K_0 / V_0 need not wait for that
-                const int q_at = nb == 0 ? 0 : 2;
+                // (a second buffer has been free since the block before that)
+                const int q_at = nb < kQBufs || kQBufs == 2 ? 0 : 2;
+                const int qb = nb % kQBufs;
+                uint8_t *q_dst = q_s + qb * kTiles * L::kQBytes;
                 for (int idx = 0; ok && idx <= 2 * w.span.n; ++idx) {
                     if (idx == q_at) {
-                        if (nb > 0 && !(ok = mbar_wait(q_empty, (nb - 1) & 1, a.status, kSiteQEmpty))) break;
-                        const int n_q_tiles = w.n[1] > 0 ? kTiles : 1;
+                        if (nb >= kQBufs && !(ok = mbar_wait(&q_empty[qb], (nb / kQBufs - 1) & 1, a.status, kSiteQEmpty)))
+                            break;
+                        const int n_q_tiles = kTiles == 2 && w.n[kTiles - 1] > 0 ? 2 : 1;
                         if constexpr (PREFIX) {
                             // rb rows of each of nb sequences, packed; the tile's rows behind them keep
                             // whatever was there (no row's result depends on another row, and they are
                             // not stored)
-                            mbar_arrive_expect_tx(q_full, n_q_tiles * a.rb * a.nb * D * 2);
+                            mbar_arrive_expect_tx(&q_full[qb], n_q_tiles * a.rb * a.nb * D * 2);
                             for (int x = 0; x < n_q_tiles; ++x) {
                                 int b0, r0;
                                 packed_tile(a, w.yq[x], &b0, &r0);
 #pragma unroll
                                 for (int p = 0; p < kPanels; ++p)
-                                    tma_load_4d(q_s + x * L::kQBytes + p * (kBM * 128), &tmap_q, q_full, p * 64, r0,
+                                    tma_load_4d(q_dst + x * L::kQBytes + p * (kBM * 128), &tmap_q, &q_full[qb], p * 64, r0,
                                                 w.kv_bh, b0);
                             }
                         } else {
-                            mbar_arrive_expect_tx(q_full, n_q_tiles * L::kQBytes);
+                            mbar_arrive_expect_tx(&q_full[qb], n_q_tiles * L::kQBytes);
                             for (int x = 0; x < n_q_tiles; ++x)
 #pragma unroll
                                 for (int p = 0; p < kPanels; ++p)
-                                    tma_load_3d(q_s + x * L::kQBytes + p * (kBM * 128), &tmap_q, q_full, p * 64,
+                                    tma_load_3d(q_dst + x * L::kQBytes + p * (kBM * 128), &tmap_q, &q_full[qb], p * 64,
                                                 w.yq[x], w.zq[x]);
                         }
                     }
@@ -282,11 +343,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 gidx += 2 * w.span.n;
                 ++nb;
             }
+            if (ok) {
+                SoftBlock end[kTiles];
+#pragma unroll
+                for (int x = 0; x < kTiles; ++x) end[x] = SoftBlock{-1, 0, 0, 0, 0, 0, 0, 0};
+                publish(end);
+            }
             // Drain: never leave the CTA with a TMA write still in flight.
 #pragma unroll
             for (int s = 0; s < NSLOT; ++s)
                 if (last_round[s] >= 0) mbar_wait(&slot_full[s], last_round[s] & 1, a.status, kSiteDrain);
-            if (nb > 0) mbar_wait(q_full, (nb - 1) & 1, a.status, kSiteDrain);
+            for (int b = max(0, nb - kQBufs); b < nb; ++b)
+                mbar_wait(&q_full[b % kQBufs], (b / kQBufs) & 1, a.status, kSiteDrain);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -294,21 +362,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The whole warp runs the loop (operands stay warp-uniform); one elected lane issues the MMAs
         // and the commits that track them.  Per block the order is
         //   S_A(0) S_B(0) | PV_A(j) S_A(j+1) PV_B(j) S_B(j+1) | ...
-        constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, kBN, false, false);
+        constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, kBN, false, false), idesc_sink = idesc_bf16_f32(kBM, 32, false, false);
         constexpr uint32_t idesc_o = idesc_bf16_f32(kBM, D, false, true);
-        const uint64_t q_desc = sdesc_sw128(smem_u32(q_s), 16, 1024);
         const uint32_t slot_addr = smem_u32(slots);
         const bool leader = elect_one();
         bool ok = true;
         int gidx = 0;                 // ring position of this block's K_0
-        int step0[kTiles] = {0, 0};   // steps of tile x before this block
-        int blocks[kTiles] = {0, 0};  // earlier blocks in which tile x had work (epilogues)
+        int step0[kTiles] = {};   // steps of tile x before this block
+        int blocks[kTiles] = {};  // earlier blocks in which tile x had work (epilogues)
         int nb = 0;
         for (int k = 0; ok && k * (int)gridDim.x < n_work; ++k) {
             const int Lw = persistent_work_index(k, n_work);
             if (Lw < 0) continue;
-            const SpanBlock w = span_block<PREFIX>(a, Lw);
-            if (!(ok = warp_wait(q_full, nb & 1, a.status, kSiteQ))) break;
+            const SpanBlock<kTiles> w = span_block<PREFIX, kTiles>(a, Lw);
+            const int qb = nb % kQBufs;
+            const uint64_t q_desc = sdesc_sw128(smem_u32(q_s + qb * kTiles * L::kQBytes), 16, 1024);
+            if (!(ok = warp_wait(&q_full[qb], (nb / kQBufs) & 1, a.status, kSiteQ))) break;
             tc_fence_after();
             // S_X(j) = Q_X K_j^T into S_X
             auto issue_s = [&](int x, int j) {
@@ -316,9 +385,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int g = gidx + 2 * j;
                 const int slot = g % NSLOT;
                 if (!(ok = warp_wait(&slot_full[slot], (g / NSLOT) & 1, a.status, kSiteSlotFull))) return;
-                // S_X overwrites P_X of the step before (this block's or the previous one's)
+                // S_X overwrites P_X of the step before (this block's or the previous one's); kOwnP: S itself, loaded by now
                 const int st = step0[x] + w.step_of(x, j);
-                if (st >= 1 && !(ok = warp_wait(&pv_done[x], (st - 1) & 1, a.status, kSitePV))) return;
+                if (st >= 1 && !(ok = warp_wait(kOwnP ? s_free : &pv_done[x], (st - 1) & 1, a.status,
+                                                kOwnP ? kSiteSFree : kSitePV)))
+                    return;
                 tc_fence_after();
                 const uint64_t k_desc = sdesc_sw128(slot_addr + slot * L::kSlotBytes, 16, 1024);
                 if (leader) {
@@ -326,7 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int ks = 0; ks < D / 16; ++ks) {
                         const uint32_t off = (ks >> 2) * (kBM * 128) + (ks & 3) * 32;
                         mma_ss(tmem + kColS + x * kBN, sdesc_add(q_desc, x * L::kQBytes + off),
-                               sdesc_add(k_desc, (ks >> 2) * (kBN * 128) + (ks & 3) * 32), idesc_s, ks > 0);
+                               sdesc_add(k_desc, (ks >> 2) * (kBN * 128) + (ks & 3) * 32),
+                               tile_cols<PREFIX>(a, w.span.n_sink, j) == 32 ? idesc_sink : idesc_s, ks > 0);
                     }
                     mma_commit(&s_full[x]);
                 }
@@ -345,10 +417,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return;
                 tc_fence_after();
                 const uint64_t v_desc = sdesc_sw128(slot_addr + slot * L::kSlotBytes, kBN * 128, 1024);
+                const int steps = tile_cols<PREFIX>(a, w.span.n_sink, j) / 16;
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < kBN / 16; ++kk)
-                        mma_ts(tmem + kColO + x * D, tmem + kColS + x * kBN + kk * 8, sdesc_add(v_desc, kk * 2048),
+                        if (kk < 2 || kk < steps) mma_ts(tmem + kColO + x * D, tmem + kColP + x * kBN + kk * 8, sdesc_add(v_desc, kk * 2048),
                                idesc_o, (!first || kk > 0));
                     mma_commit(&pv_done[x]);
                 }
@@ -360,18 +433,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (leader) mma_commit(bar);
                 __syncwarp();
             };
-            issue_s(0, 0);
-            issue_s(1, 0);
-            if (ok && w.span.n == 1) commit_to(q_empty);
-            if (ok) commit_to(&slot_empty[gidx % NSLOT]);  // K_0
-            for (int j = 0; ok && j < w.span.n; ++j) {
-                issue_pv(0, j);
-                issue_s(0, j + 1);
-                issue_pv(1, j);
-                if (ok) commit_to(&slot_empty[(gidx + 2 * j + 1) % NSLOT]);  // V_j
-                issue_s(1, j + 1);
-                if (ok && j + 2 == w.span.n) commit_to(q_empty);  // the block's last S products
-                if (ok && j + 1 < w.span.n) commit_to(&slot_empty[(gidx + 2 * j + 2) % NSLOT]);  // K_{j+1}
+            if constexpr (kOwnP) {
+                for (int j = 0; ok && j <= w.span.n; ++j) {
+                    if (j < w.span.n) {
+                        issue_s(0, j);
+                        if (ok && j + 1 == w.span.n) commit_to(&q_empty[qb]);
+                        if (ok) commit_to(&slot_empty[(gidx + 2 * j) % NSLOT]);  // K_j
+                    }
+                    if (j > 0) {
+                        issue_pv(0, j - 1);
+                        if (ok) commit_to(&slot_empty[(gidx + 2 * j - 1) % NSLOT]);  // V_{j-1}
+                    }
+                }
+            } else {
+                issue_s(0, 0);
+                issue_s(1, 0);
+                if (ok && w.span.n == 1) commit_to(&q_empty[qb]);
+                if (ok) commit_to(&slot_empty[gidx % NSLOT]);  // K_0
+                for (int j = 0; ok && j < w.span.n; ++j) {
+                    issue_pv(0, j);
+                    issue_s(0, j + 1);
+                    issue_pv(1, j);
+                    if (ok) commit_to(&slot_empty[(gidx + 2 * j + 1) % NSLOT]);  // V_j
+                    issue_s(1, j + 1);
+                    if (ok && j + 2 == w.span.n) commit_to(&q_empty[qb]);  // the block's last S products
+                    if (ok && j + 1 < w.span.n) commit_to(&slot_empty[(gidx + 2 * j + 2) % NSLOT]);  // K_{j+1}
+                }
             }
 #pragma unroll
             for (int x = 0; x < kTiles; ++x) {
@@ -391,21 +478,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quarter = warp & 3;                   // TMEM lanes [32*quarter, 32*quarter + 32)
         const int r = quarter * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        const uint32_t s_col = kColS + x * kBN, o_col = kColO + x * D;
+        const uint32_t s_col = kColS + x * kBN, o_col = kColO + x * D, p_col = kColP + x * kBN;
         const float c = a.scale_log2;
         bool ok = true;
         int step0 = 0;     // steps of this tile before the current block
-        int uses = 0;      // uses of the staging buffer (by both tiles) before the current block
         int blocks_x = 0;  // epilogues of this tile so far (phase of stage_full[x])
-        for (int k = 0; ok && k * (int)gridDim.x < n_work; ++k) {
-            const int Lw = persistent_work_index(k, n_work);
-            if (Lw < 0) continue;
-            const SpanBlock w = span_block<PREFIX>(a, Lw);
-            // this tile's fields (x is not a constant here: indexing the arrays would put them in local memory)
-            const int n = x == 0 ? w.n[0] : w.n[1];
-            const int from = x == 0 ? w.from[0] : w.from[1];
-            const int yq = x == 0 ? w.yq[0] : w.yq[1], zq = x == 0 ? w.zq[0] : w.zq[1];
-            const int pos0 = x == 0 ? w.p0[0] : w.p0[1];
+        for (int k = 0; ok; ++k) {
+            const int e = k % kBlocks;
+            ok = mbar_wait(&block_full[e], (k / kBlocks) & 1, a.status, kSiteBlock);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            const SoftBlock w = soft_blocks[e * kTiles + x];
+            warp_arrive(&block_empty[e]);
+            if (w.n < 0) break;
+            const int n = w.n, yq = w.yq, zq = w.zq, pos0 = w.p0;
             const int pos = pos0 + r;  // windowed: this row's position
             float m = -INFINITY, l = 0.f;  // running max (log2 units) and sum
             for (int step = 0; step < n; ++step) {
@@ -413,71 +498,137 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = mbar_wait(&s_full[x], (step0 + step) & 1, a.status, kSiteSFull);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 tc_fence_after();
-                uint32_t raw[kBN];
-#pragma unroll
-                for (int ch = 0; ch < kBN / 32; ++ch) tmem_ld32(tmem + lane_base + s_col + ch * 32, raw + ch * 32);
-                tmem_wait_ld();
-                const int key0 = w.y_off + w.span.key0(step < w.span.n_sink ? step : from + step - w.span.n_sink, kBN);
-                const int window = w.span.window_in(step, a.window);
-                const bool need_mask = PREFIX ? key0 + kBN > a.Nk
-                                              : !all_seen(pos0, pos0 + kBM - 1, key0, key0 + kBN - 1, window, a.sinks);
-                if (need_mask) {
-                    // 32 keys at a time: this warp's 32 rows see all or nothing of most such chunks at the ends of a
-                    // window.  (Leaving the exponentials of unseen chunks out, by branches or in a path of its own,
-                    // measured 6-20 % slower: two warps a scheduler hide no latency, straight code does.)
-                    const int pw = pos0 + quarter * 32;
-#pragma unroll
-                    for (int h = 0; h < kBN / 32; ++h) {
-                        const int k0 = key0 + 32 * h;
-                        if (PREFIX ? k0 + 32 <= a.Nk : all_seen(pw, pw + 31, k0, k0 + 31, window, a.sinks)) continue;
-                        const uint32_t seen = PREFIX ? low_bits(a.Nk - k0) : seen_keys(pos, k0, window, a.sinks);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(seen & (1u << e))) raw[32 * h + e] = 0xff800000u;  // -inf
-                    }
-                }
-                // row max of the raw scores (scale > 0 commutes with max): four chains of three-input maxima
-                float mx[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) mx[u] = __uint_as_float(raw[u]);
-#pragma unroll
-                for (int i = 4; i + 8 <= kBN; i += 8)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        mx[u] = fmax3(mx[u], __uint_as_float(raw[i + 2 * u]), __uint_as_float(raw[i + 2 * u + 1]));
-#pragma unroll
-                for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __uint_as_float(raw[kBN - 4 + u]));
-                const float mt = c * fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-                const float m_new = fmaxf(m, mt);
                 // Lazy correction: keep the stale max unless the row max grew by > 8 (factor 256).
-                const bool need = m_new > m + 8.f;
-                const float m_use = need ? m_new : m;
-                const float m_base = (m_use == -INFINITY) ? 0.f : m_use;
-                const float alpha = need ? ex2_approx(m - m_base) : 1.f;
-                // P = 2^(s c - m) as bf16 pairs over the first kBN/2 columns of S_X, 16 columns per store;
-                // the scaling FMA and the row sum run on fp32 pairs
-                const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-m_base, -m_base);
-                uint64_t acc2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-#pragma unroll
-                for (int h = 0; h < kBN / 32; ++h) {
+                bool need;
+                float m_base, alpha;
+                auto new_max = [&](float mt) {
+                    const float m_new = fmaxf(m, mt);
+                    need = m_new > m + 8.f;
+                    const float m_use = need ? m_new : m;
+                    m_base = (m_use == -INFINITY) ? 0.f : m_use;
+                    alpha = need ? ex2_approx(m - m_base) : 1.f;
+                    m = m_use;
+                };
+                const uint64_t c2 = f2_pack(c, c);
+                uint64_t nm2, acc2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+                // kOwnP: S is in registers, the next one may overwrite it; P is free, and O holds every earlier product, once
+                // the step before's PV has completed.  (Otherwise this S was issued after that product.)
+                auto s_loaded = [&] {
+                    if constexpr (kOwnP) {
+                        tc_fence_before();
+                        warp_arrive(s_free);
+                    }
+                };
+                auto p_free = [&] {
+                    if constexpr (kOwnP) {
+                        if (step0 + step >= 1) ok = mbar_wait(&pv_done[x], (step0 + step - 1) & 1, a.status, kSitePV);
+                        ok = __all_sync(0xffffffffu, ok);
+                        tc_fence_after();
+                    }
+                };
+                // P = 2^(s c - m) of 32 keys as bf16 pairs over columns [16h, 16h + 16) of P_X; the scaling FMA and the
+                // row sum run on fp32 pairs
+                auto store_p = [&](const uint32_t *raw, int h) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const uint64_t y2 = f2_fma(f2_pack(__uint_as_float(raw[32 * h + 2 * i]),
-                                                           __uint_as_float(raw[32 * h + 2 * i + 1])), c2, nm2);
+                        const uint64_t y2 = f2_fma(f2_pack(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1])), c2, nm2);
                         float y0, y1;
                         f2_unpack(y2, y0, y1);
                         const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
                         acc2[i & 1] = f2_add(acc2[i & 1], f2_pack(p0, p1));
                         pk[i] = pack_bf16x2(p0, p1);
                     }
-                    tmem_st16(tmem + lane_base + s_col + h * 16, pk);
+                    tmem_st16(tmem + lane_base + p_col + h * 16, pk);
+                };
+                if (tile_cols<PREFIX>(a, w.n_sink, step) == 32) {
+                    // a sink tile whose sinks fit into 32 columns: every row of the query tile sees all of them
+                    uint32_t raw[32];
+                    tmem_ld32(tmem + lane_base + s_col, raw);
+                    tmem_wait_ld();
+                    s_loaded();
+                    const int left = a.sinks - step * kBN;
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        if (e >= left) raw[e] = 0xff800000u;  // -inf
+                        mx = fmaxf(mx, __uint_as_float(raw[e]));
+                    }
+                    new_max(c * mx);
+                    nm2 = f2_pack(-m_base, -m_base);
+                    p_free();
+                    if (kOwnP && !ok) break;
+                    store_p(raw, 0);
+                } else {
+                    const bool sink = step < w.n_sink;
+                    const int key0 = sink ? step * kBN : w.key0 + (step - w.n_sink) * kBN;
+                    const int window = sink ? 0 : a.window;
+                    uint32_t raw[kBN];
+#pragma unroll
+                    for (int ch = 0; ch < kBN / 32; ++ch) tmem_ld32(tmem + lane_base + s_col + ch * 32, raw + ch * 32);
+                    tmem_wait_ld();
+                    s_loaded();
+                    bool unseen = false;  // this row sees none of the tile's keys
+                    if (PREFIX ? key0 + kBN > a.Nk
+                               : !all_seen(pos0, pos0 + kBM - 1, key0, key0 + kBN - 1, window, a.sinks)) {
+                        // Column e of the tile is seen iff e in [lo, hi) (or e < left, where the sinks reach into it).
+                        const int hi = PREFIX ? a.Nk - key0 : pos + 1 - key0;
+                        const int lo = PREFIX ? 0 : pos + 1 - window - key0;
+                        const int left = PREFIX ? 0 : a.sinks - key0;
+                        if (left <= 0) {
+                            // raw = min(raw, (hi - 1/2 - e) 2^118, (e + 1/2 - lo) 2^118): one bound is hugely negative
+                            // where the column is not seen, both are hugely positive where it is (all exact).  Two
+                            // packed additions and a three-input minimum a pair, and no predicates: selecting by mask
+                            // bits took 900-1300 cycles more per tile, a third of a plain step.
+                            constexpr float kBig = 0x1p118f;
+                            const float h0 = ((float)max(-1, min(kBN, hi)) - 0.5f) * kBig;
+                            const float l0 = (0.5f - (float)max(-1, min(kBN, lo))) * kBig;
+                            uint64_t th = f2_pack(h0, h0 - kBig), tl = f2_pack(l0, l0 + kBig);
+                            const uint64_t dn = f2_pack(-2.f * kBig, -2.f * kBig), up = f2_pack(2.f * kBig, 2.f * kBig);
+#pragma unroll
+                            for (int i = 0; i < kBN; i += 2) {
+                                float a0, a1, b0, b1;
+                                f2_unpack(th, a0, a1);
+                                f2_unpack(tl, b0, b1);
+                                raw[i] = __float_as_uint(fmin3(__uint_as_float(raw[i]), a0, b0));
+                                raw[i + 1] = __float_as_uint(fmin3(__uint_as_float(raw[i + 1]), a1, b1));
+                                th = f2_add(th, dn);
+                                tl = f2_add(tl, up);
+                            }
+                            unseen = hi <= 0 || lo >= kBN || hi <= lo;
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < kBN / 32; ++h) {
+                                const uint32_t seen = seen_keys(pos, key0 + 32 * h, window, a.sinks);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (!(seen & (1u << e))) raw[32 * h + e] = 0xff800000u;  // -inf
+                            }
+                        }
+                    }
+                    // row max of the raw scores (scale > 0 commutes with max): four chains of three-input maxima
+                    float mx[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) mx[u] = __uint_as_float(raw[u]);
+#pragma unroll
+                    for (int i = 4; i + 8 <= kBN; i += 8)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            mx[u] = fmax3(mx[u], __uint_as_float(raw[i + 2 * u]), __uint_as_float(raw[i + 2 * u + 1]));
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __uint_as_float(raw[kBN - 4 + u]));
+                    const float mt = c * fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                    new_max(unseen ? -INFINITY : mt);
+                    nm2 = f2_pack(-m_base, -m_base);
+                    p_free();
+                    if (kOwnP && !ok) break;
+#pragma unroll
+                    for (int h = 0; h < kBN / 32; ++h) store_p(raw + 32 * h, h);
                 }
                 float r0, r1, r2, r3;
                 f2_unpack(acc2[0], r0, r1);
                 f2_unpack(acc2[1], r2, r3);
                 l = l * alpha + ((r0 + r1) + (r2 + r3));
-                m = m_use;
                 if (step >= 1 && __any_sync(0xffffffffu, need)) {
                     uint32_t ov[32];
 #pragma unroll
@@ -494,13 +645,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 warp_arrive(&p_full[x]);
             }
             // the staging buffer's use number of this tile's epilogue in this block (tile A's before tile B's)
-            const int use = uses + (x == 1 && w.n[0] > 0);
-            uses += (w.n[0] > 0) + (w.n[1] > 0);
+            const int use = w.use;
             if (!ok || n == 0) continue;
             // the block's last PV_X has completed: O_X is final
             step0 += n;
             ok = mbar_wait(&pv_done[x], (step0 - 1) & 1, a.status, kSiteFinal);
-            // the previous use's TMA store has finished reading the staging buffer
+            // the previous use's TMA store has finished reading the staging buffer (one tile a CTA: its own store of a
+            // block ago, which the thread that issued it waits for only here)
+            if (kTiles == 1 && !PREFIX && use >= 1 && quarter == kFirstSoftmaxWarp % 4 && lane == 0) {
+                tma_store_wait_read();
+                mbar_arrive(stage_free);
+            }
             if (!PREFIX && ok && use >= 1) ok = mbar_wait(stage_free, (use - 1) & 1, a.status, kSiteStage);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             tc_fence_after();
@@ -561,8 +716,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int p = 0; p < kPanels; ++p)
                         if (p * 64 < a.D) tma_store_3d(&tmap_o, stage + p * (kBM * 128), p * 64, yq, zq);
                     tma_store_commit();
-                    tma_store_wait_read();
-                    mbar_arrive(stage_free);
+                    if (kTiles == 2) {
+                        tma_store_wait_read();
+                        mbar_arrive(stage_free);
+                    }
                 } else {
                     ok = false;
                 }
@@ -570,6 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++blocks_x;
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         }
+        tma_store_wait_read();  // the CTA's shared memory must outlive the stores' reads
     }
 
     tc_fence_before();
@@ -580,17 +738,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, int NSLOT, bool PREFIX>
+template <int D, int NSLOT, bool PREFIX, int kTiles = 2, int kCtas = 1>
 cudaError_t launch_spec(const SpanArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                         const CUtensorMap &tks, const CUtensorMap &tvs, const CUtensorMap &to, cudaStream_t s) {
-    using L = SpanSmem<D, NSLOT>;
-    static_assert(L::kAlloc <= 232448, "shared memory budget");
-    auto kern = win_fwd_kernel<D, NSLOT, PREFIX>;
+    using L = SpanSmem<D, NSLOT, kTiles>;
+    static_assert(L::kAlloc <= 233472 / kCtas - 1024, "shared memory budget (a CTA's own, and 1 KB that the system takes)");
+    auto kern = win_fwd_kernel<D, NSLOT, PREFIX, kTiles, kCtas>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
-    const int n_work = span_blocks(a, PREFIX);
-    const int sms = a.num_sms > 0 ? a.num_sms : kNumSms;
-    kern<<<n_work < sms ? n_work : sms, kThreads, L::kAlloc, s>>>(tq, tk, tv, tks, tvs, to, a);
+    const int n_work = span_blocks<kTiles>(a, PREFIX);
+    const int ctas = (a.num_sms > 0 ? a.num_sms : kNumSms) * kCtas;
+    kern<<<n_work < ctas ? n_work : ctas, L::kThreads, L::kAlloc, s>>>(tq, tk, tv, tks, tvs, to, a);
     return cudaGetLastError();
 }
 
@@ -602,7 +760,7 @@ cudaError_t launch_win_fwd(const SpanArgs &a, const CUtensorMap &tq, const CUten
     switch (kernel_head_dim(a.D)) {
         case 64:
             return prefix ? launch_spec<64, 4, true>(a, tq, tk, tv, tks, tvs, to, s)
-                          : launch_spec<64, 4, false>(a, tq, tk, tv, tks, tvs, to, s);
+                          : launch_spec<64, 4, false, 1, 2>(a, tq, tk, tv, tks, tvs, to, s);
         case 128:
             return prefix ? launch_spec<128, 4, true>(a, tq, tk, tv, tks, tvs, to, s)
                           : launch_spec<128, 4, false>(a, tq, tk, tv, tks, tvs, to, s);

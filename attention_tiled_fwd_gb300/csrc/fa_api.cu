@@ -662,12 +662,12 @@ extern "C" int fa_window_decode(const void *q, const void *k, const void *v, con
 }
 
 namespace {
-// How shared-prefix decode cuts its work: the prefix into chunks for packed 128-row query tiles, the sequences'
-// own caches into `own` CTAs each.
+// How shared-prefix decode cuts its work: the prefix into chunks for packed 128-row query tiles on `ctas` SMs, the
+// sequences' own caches into `own` CTAs each, which run on the other SMs meanwhile and on all of them afterwards.
 struct PrefixPlan {
-    int R, rb, nb, m_tiles, splits, chunk_tiles, own;
-    // with one CTA per sequence and key head for the own cache, that CTA joins the prefix's partials
-    int slots() const { return splits + (own > 1 ? own : 0); }
+    int R, rb, nb, m_tiles, splits, chunk_tiles, own, ctas;
+    bool fused;  // both fit on the GPU at once: the own caches' CTAs join the prefix's partials
+    int slots() const { return splits + (fused ? 0 : own); }
 };
 
 PrefixPlan prefix_plan(int B, int Hq, int Hkv, int n_q, int P, int N, int D, int num_sms) {
@@ -676,24 +676,34 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int n_q, int P, int N, int D, int
     p.rb = std::min(p.R, 128);
     p.nb = std::min(128 / p.rb, B);
     p.m_tiles = p.R <= 128 ? (B + p.nb - 1) / p.nb : B * ((p.R + 127) / 128);
-    const int bn = fwd_block_n(kernel_head_dim(D)), tiles = (P + bn - 1) / bn;
-    const int per_block = kernel_head_dim(D) <= 128 ? 2 : 1;  // query tiles a block streams the chunk past
-    const long long units = (long long)Hkv * ((p.m_tiles + per_block - 1) / per_block);
-    // the chunk count that minimises waves of CTAs x (tiles per chunk + a block's fixed cost, about 3 tiles)
-    long long best = 0;
-    p.splits = 1;
-    p.chunk_tiles = tiles;
-    for (int s = 1; s <= tiles && (s == 1 || units * s <= 4ll * num_sms); ++s) {
-        const int c = (tiles + s - 1) / s;
-        if ((tiles + c - 1) / c != s) continue;  // the same chunks as a smaller count
-        const long long cost = (units * s + num_sms - 1) / num_sms * (c + 3);
-        if (s == 1 || cost < best) {
-            best = cost;
-            p.splits = s;
-            p.chunk_tiles = c;
-        }
-    }
+    const int Dk = kernel_head_dim(D), bn = fwd_block_n(Dk), tiles = (P + bn - 1) / bn;
+    const int per_block = Dk <= 128 ? 2 : 1;  // query tiles a block streams the chunk past
+    const int units = Hkv * ((p.m_tiles + per_block - 1) / per_block);
     p.own = win_decode_splits(B, Hkv, p.R, (N + win_decode_tile_keys() - 1) / win_decode_tile_keys(), D, num_sms);
+    const int own_sms = win_decode_sms(B, Hkv, p.R, p.own, D);
+    p.fused = p.own == 1 && own_sms + std::min(units, num_sms) <= num_sms;
+    // Measured: a key tile takes a block about 1.4 us (D = 64), 1.7 (128), 1.0 (256, 64 keys), a block 3 tiles' time
+    // besides; an SM on its own streams about 80 KB/us of caches, all of them 6500.  Half of N is taken for the length.
+    const double tile_us = Dk == 64 ? 1.4 : Dk == 128 ? 1.7 : 1.0;
+    const double own_kb = (double)B * Hkv * N * D * 2 / 1000;
+    double best = 1e300;
+    for (int left = 0; left <= num_sms / 3; left += 8) {
+        const int ctas = p.fused ? num_sms - own_sms : num_sms - left;
+        for (int s = 1; s <= tiles && (s == 1 || (long long)units * s <= 4ll * ctas); ++s) {
+            const int c = (tiles + s - 1) / s;
+            if ((tiles + c - 1) / c != s) continue;  // the same chunks as a smaller count
+            const double prefix_us = (double)((units * s + ctas - 1) / ctas) * (c + 3) * tile_us;
+            const double rest = own_kb - std::min(own_kb, left * 80.0 * prefix_us);
+            const double us = p.fused ? prefix_us : prefix_us + rest / 6500;
+            if (us < best) {
+                best = us;
+                p.splits = s;
+                p.chunk_tiles = c;
+                p.ctas = ctas;
+            }
+        }
+        if (p.fused) break;
+    }
     return p;
 }
 
@@ -737,7 +747,7 @@ extern "C" int fa_prefix_decode(const void *q, const void *k_prefix, const void 
     a.window = P;
     a.scale_log2 = scale * log2e();
     a.status = st->status_word;
-    a.num_sms = st->num_sms;
+    a.num_sms = p.ctas;
     a.R = p.R, a.rb = p.rb, a.nb = p.nb, a.m_tiles = p.m_tiles;
     a.splits = p.splits, a.chunk_tiles = p.chunk_tiles;
     a.slots = p.slots();
@@ -762,9 +772,9 @@ extern "C" int fa_prefix_decode(const void *q, const void *k_prefix, const void 
     cudaError_t e = launch_win_fwd(a, tq, tkp, tvp, tkp, tvp, tkp, s);
     if (e != cudaSuccess) return FA_ERR_CUDA;
     WinDecodeArgs d{q, lens, o, lse, B, Hkv, p.R, n_q, N, D, N, 0, scale * log2e(), st->status_word, p.own,
-                    p.slots(), p.splits, part_o, part_ml, p.own == 1, 1};
+                    p.slots(), p.splits, part_o, part_ml, p.fused, 1};
     e = launch_win_decode(d, tk, tv, s);
-    if (e == cudaSuccess && p.own > 1) e = launch_win_join(part_o, part_ml, o, lse, (long long)rows, p.slots(), D, false, s);
+    if (e == cudaSuccess && !p.fused) e = launch_win_join(part_o, part_ml, o, lse, (long long)rows, p.slots(), D, true, s);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

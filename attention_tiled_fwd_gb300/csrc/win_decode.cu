@@ -18,9 +18,11 @@
 //              (no exchange inside the loop); the four states are joined at the end
 // A sequence's tiles are dealt to `splits` CTAs by its own length (read on the
 // device), and win_join_kernel joins their partials; with one split the CTA
-// writes O and L itself and that launch falls away.  Behind a shared prefix it
-// first joins the prefix's partials; it is launched as that kernel's programmatic
-// dependent, so its loads and products run in the prefix kernel's tail.
+// writes O and L itself and that launch falls away.  Behind a shared prefix it is
+// launched as that kernel's programmatic dependent, so it runs on the SMs that the
+// prefix kernel leaves it and in its tail: the prefix is bound by its products, the
+// caches by HBM.  When all of both fits on the GPU at once, each CTA waits for the
+// prefix's partials and joins them itself; otherwise win_join_kernel does.
 // Keys outside [0, len), between the sinks and the window, or past a sink tile's
 // last sink may hold anything (a cache's unwritten rows): their scores are
 // replaced and their V rows cleared before the products.
@@ -257,8 +259,8 @@ __global__ void __launch_bounds__(kThreads)
         }
     }
     __syncthreads();
-    if (a.behind) launch_dependent_wait();  // every CTA: this grid must not end before the one it runs behind
-    else launch_dependents();
+    launch_dependents();
+    if (a.behind && a.join) launch_dependent_wait();
     for (int idx = threadIdx.x; idx < kRowTile * (D / 4); idx += kThreads) {
         const int r = idx / (D / 4), c = idx % (D / 4) * 4;
         const int rr = rt * kRowTile + r;
@@ -316,6 +318,10 @@ __global__ void __launch_bounds__(kThreads)
             if (c == 0) a.lse[row] = (M + __log2f(ls)) * 0.69314718055994531f;
         }
     }
+    // This grid must not end before the one it runs behind: the join's launch waits for this one alone.  The CTA that
+    // starts last waits, so that no other gives up its place on an SM.
+    if (a.behind && !a.join && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1)
+        launch_dependent_wait();
 }
 
 // One warp per row joins its `slots` partials in order: M = max m_t, O = sum O_t 2^(m_t - M) / l.
@@ -384,6 +390,12 @@ cudaError_t launch_decode_d(const WinDecodeArgs &a, const CUtensorMap &tk, const
 int ctas_per_sm(int D) { return D == 64 ? 3 : D == 128 ? 2 : 1; }
 
 }  // namespace
+
+int win_decode_sms(int B, int Hkv, int R, int splits, int D) {
+    const long long ctas = (long long)B * Hkv * ((R + kRowTile - 1) / kRowTile) * splits;
+    const long long sms = (ctas + ctas_per_sm(D) - 1) / ctas_per_sm(D);
+    return sms < (1 << 20) ? (int)sms : 1 << 20;
+}
 
 int win_decode_splits(int B, int Hkv, int R, int tiles, int D, int num_sms) {
     // Enough CTAs for one full wave, none with less than two tiles: a split costs its CTA a pipeline fill and the

@@ -26,6 +26,8 @@ struct WinDecodeArgs {
 // CTAs per (sequence, key head, row tile) for caches that need up to `tiles` tiles.
 int win_decode_splits(int B, int Hkv, int R, int tiles, int D, int num_sms);
 int win_decode_tile_keys();
+// SMs that all CTAs of such a launch take at once.
+int win_decode_sms(int B, int Hkv, int R, int splits, int D);
 cudaError_t launch_win_decode(const WinDecodeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s);
 // O and LSE of `rows` rows from `slots` partials each (part_o [row][slot][D], part_ml [row][slot]).
 cudaError_t launch_win_join(const float *part_o, const float2 *part_ml, void *o, float *lse, long long rows, int slots,

@@ -649,15 +649,15 @@ extern "C" int fa_window_decode(const void *q, const void *k, const void *v, con
     const size_t rows = (size_t)B * Hq * n_q;
     float *part_o = need > 0 ? static_cast<float *>(workspace) : nullptr;
     float2 *part_ml = need > 0 ? reinterpret_cast<float2 *>(part_o + rows * splits * D) : nullptr;
-    WinDecodeArgs a{q, lens, o, lse, B, Hkv, Hq / Hkv * n_q, n_q, N, D, w.window, w.sinks, scale * log2e(),
-                    st->status_word, splits, splits, 0, part_o, part_ml, part_o == nullptr, 0};
+    const WinDecodeArgs a{q, lens, o, lse, B, Hkv, Hq / Hkv * n_q, n_q, N, D, w.window, w.sinks, scale * log2e(),
+                          st->status_word, splits, part_o, part_ml, part_o == nullptr, PrefixParts{}, 0};
     CUtensorMap tk, tv;
     if (encode_rows(&tk, k, B * Hkv, N, N, D, win_decode_tile_keys()) != FA_OK ||
         encode_rows(&tv, v, B * Hkv, N, N, D, win_decode_tile_keys()) != FA_OK)
         return FA_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = launch_win_decode(a, tk, tv, s);
-    if (e == cudaSuccess && part_o) e = launch_win_join(part_o, part_ml, o, lse, (long long)rows, splits, D, true, s);
+    if (e == cudaSuccess && part_o) e = launch_win_join(a, PrefixParts{}, s);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -667,7 +667,12 @@ namespace {
 struct PrefixPlan {
     int R, rb, nb, m_tiles, splits, chunk_tiles, own, ctas;
     bool fused;  // both fit on the GPU at once: the own caches' CTAs join the prefix's partials
-    int slots() const { return splits + (fused ? 0 : own); }
+    // 128-row partials of the prefix, and partials of the own caches' rows
+    size_t prefix_parts(int Hkv) const { return (size_t)Hkv * m_tiles * splits; }
+    size_t own_parts(size_t rows) const { return fused ? 0 : rows * own; }
+    size_t bytes(int Hkv, size_t rows, int D) const {
+        return (prefix_parts(Hkv) * 128 + own_parts(rows)) * ((size_t)D * 4 + 8);
+    }
 };
 
 PrefixPlan prefix_plan(int B, int Hq, int Hkv, int n_q, int P, int N, int D, int num_sms) {
@@ -719,7 +724,7 @@ extern "C" int fa_prefix_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q,
     int rc = check_prefix(B, Hq, Hkv, n_q, P, N, D, 1.f);
     if (rc != FA_OK) return rc;
     const PrefixPlan p = prefix_plan(B, Hq, Hkv, n_q, P, N, D, current_num_sms());
-    *bytes = partials_bytes((size_t)B * Hq * n_q, p.slots(), D);
+    *bytes = p.bytes(Hkv, (size_t)B * Hq * n_q, D);
     return FA_OK;
 }
 
@@ -738,9 +743,12 @@ extern "C" int fa_prefix_decode(const void *q, const void *k_prefix, const void 
     if (rc != FA_OK) return rc;
     const PrefixPlan p = prefix_plan(B, Hq, Hkv, n_q, P, N, D, st->num_sms);
     const size_t rows = (size_t)B * Hq * n_q;
-    if (workspace_bytes < partials_bytes(rows, p.slots(), D)) return FA_ERR_WORKSPACE;
-    float *part_o = static_cast<float *>(workspace);
-    float2 *part_ml = reinterpret_cast<float2 *>(part_o + rows * p.slots() * D);
+    if (workspace_bytes < p.bytes(Hkv, rows, D)) return FA_ERR_WORKSPACE;
+    // O of the prefix's partials and of the rows' own, then (m, l) of both
+    PrefixParts parts{static_cast<float *>(workspace), nullptr, p.m_tiles, p.splits, p.R, p.rb, p.nb};
+    float *own_o = parts.o + p.prefix_parts(Hkv) * 128 * D;
+    parts.ml = reinterpret_cast<float2 *>(own_o + p.own_parts(rows) * D);
+    float2 *own_ml = parts.ml + p.prefix_parts(Hkv) * 128;
 
     SpanArgs a{};
     a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.Nq = n_q, a.Nk = P, a.D = D;
@@ -748,10 +756,8 @@ extern "C" int fa_prefix_decode(const void *q, const void *k_prefix, const void 
     a.scale_log2 = scale * log2e();
     a.status = st->status_word;
     a.num_sms = p.ctas;
-    a.R = p.R, a.rb = p.rb, a.nb = p.nb, a.m_tiles = p.m_tiles;
-    a.splits = p.splits, a.chunk_tiles = p.chunk_tiles;
-    a.slots = p.slots();
-    a.part_o = part_o, a.part_ml = part_ml;
+    a.parts = parts;
+    a.chunk_tiles = p.chunk_tiles;
     // the rows of a key head: [B, Hkv, R, D], boxes of rb rows of nb sequences
     CUtensorMap tq, tkp, tvp, tk, tv;
     {
@@ -771,10 +777,10 @@ extern "C" int fa_prefix_decode(const void *q, const void *k_prefix, const void 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = launch_win_fwd(a, tq, tkp, tvp, tkp, tvp, tkp, s);
     if (e != cudaSuccess) return FA_ERR_CUDA;
-    WinDecodeArgs d{q, lens, o, lse, B, Hkv, p.R, n_q, N, D, N, 0, scale * log2e(), st->status_word, p.own,
-                    p.slots(), p.splits, part_o, part_ml, p.fused, 1};
+    const WinDecodeArgs d{q, lens, o, lse, B, Hkv, p.R, n_q, N, D, N, 0, scale * log2e(), st->status_word, p.own,
+                          own_o, own_ml, p.fused, parts, 1};
     e = launch_win_decode(d, tk, tv, s);
-    if (e == cudaSuccess && !p.fused) e = launch_win_join(part_o, part_ml, o, lse, (long long)rows, p.slots(), D, true, s);
+    if (e == cudaSuccess && !p.fused) e = launch_win_join(d, parts, s);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

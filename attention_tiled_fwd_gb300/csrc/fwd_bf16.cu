@@ -129,16 +129,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kv_end = a.causal ? min(N, (q_tile + 1) * kBM) : N;
         n_kv = (kv_end + BN - 1) / BN;  // >= 1 because q_tile * kBM < N
     } else if constexpr (PREFIX) {
-        q_tile = blockIdx.x % a.m_tiles;
-        const int rest = blockIdx.x / a.m_tiles;
-        chunk = rest % a.splits;
-        bh = kv_bh = rest / a.splits;
+        q_tile = blockIdx.x % a.parts.m_tiles;
+        const int rest = blockIdx.x / a.parts.m_tiles;
+        chunk = rest % a.parts.splits;
+        bh = kv_bh = rest / a.parts.splits;
         N = a.Nk;
         span.lo = chunk * a.chunk_tiles * BN;
         n_kv = min(a.chunk_tiles, (N + BN - 1) / BN - chunk * a.chunk_tiles);
-        const int row_tiles = (a.R + a.rb - 1) / a.rb;
-        b0 = q_tile / row_tiles * a.nb;
-        r0 = q_tile % row_tiles * a.rb;
+        const int row_tiles = (a.parts.R + a.parts.rb - 1) / a.parts.rb;
+        b0 = q_tile / row_tiles * a.parts.nb;
+        r0 = q_tile % row_tiles * a.parts.rb;
     } else {
         N = a.Nq;
         bh = blockIdx.x % (a.B * a.Hq);
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_prefetch_desc(&tmap_k);
             tma_prefetch_desc(&tmap_v);
             if constexpr (PREFIX) {
-                mbar_arrive_expect_tx(q_full, a.rb * a.nb * D * 2);
+                mbar_arrive_expect_tx(q_full, a.parts.rb * a.parts.nb * D * 2);
 #pragma unroll
                 for (int p = 0; p < kPanels; ++p)
                     tma_load_4d(q_s + p * (kBM * 128), &tmap_q, q_full, p * 64, r0, kv_bh, b0);
@@ -414,21 +414,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if constexpr (PREFIX) {
                 // this chunk's partial of the row: O unnormalised, m (log2 units) and l
-                const int b = b0 + r / a.rb, rr = r0 + r % a.rb;
-                const bool valid = r < a.rb * a.nb && b < a.B && rr < a.R;
-                const size_t slot = (((size_t)b * a.Hkv + kv_bh) * a.R + rr) * a.slots + chunk;
+                // (rows of the tile behind its packed ones are written too and never read)
+                const size_t part = a.parts.at(kv_bh, q_tile) + chunk;
+                float *dst = a.parts.o + part * (kBM * D) + r * 8;
                 uint32_t ov[32];
 #pragma unroll
                 for (int ch = 0; ch < HD / 32; ++ch) {
                     tmem_ld32(tmem + lane_base + kColO + g * HD + ch * 32, ov);
                     tmem_wait_ld();
-                    if (valid) {
-                        float *dst = a.part_o + slot * a.D + g * HD + ch * 32;
 #pragma unroll
-                        for (int v8 = 0; v8 < 4; ++v8) st_global_v8(dst + 8 * v8, ov + 8 * v8);
-                    }
+                    for (int v8 = 0; v8 < 4; ++v8)
+                        st_global_v8(dst + (g * HD / 8 + ch * 4 + v8) * (kBM * 8), ov + 8 * v8);
                 }
-                if (valid && g == 0) a.part_ml[slot] = make_float2(m, l_row);
+                if (g == 0) a.parts.ml[part * kBM + r] = make_float2(m, l_row);
             } else {
             const float inv_l = 1.f / l_row;
             // row stride and stored columns: the caller's D (at most this kernel's D; the columns past it
@@ -487,7 +485,7 @@ cudaError_t launch_span(const SpanArgs &a, const CUtensorMap &tq, const CUtensor
     auto kern = fwd_bf16_kernel<D, BN, NSLOT, SpanArgs, PREFIX>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
-    const int grid = PREFIX ? a.m_tiles * a.splits * a.Hkv : ((a.Nq + kBM - 1) / kBM) * a.Hq * a.B;
+    const int grid = PREFIX ? a.parts.m_tiles * a.parts.splits * a.Hkv : ((a.Nq + kBM - 1) / kBM) * a.Hq * a.B;
     kern<<<grid, kThreads, L::kAlloc, s>>>(tq, tk, tv, tks, tvs, a);
     return cudaGetLastError();
 }
@@ -496,7 +494,7 @@ cudaError_t launch_span(const SpanArgs &a, const CUtensorMap &tq, const CUtensor
 
 cudaError_t launch_win_fwd_wide(const SpanArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                                 const CUtensorMap &tks, const CUtensorMap &tvs, cudaStream_t s) {
-    const bool prefix = a.part_o != nullptr;
+    const bool prefix = a.parts.o != nullptr;
     switch (kernel_head_dim(a.D)) {
         case 192:
             return prefix ? cudaErrorInvalidValue : launch_span<192, 64, fwd_nslot(192), false>(a, tq, tk, tv, tks, tvs, s);

@@ -261,10 +261,11 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     launch_dependents();
     if (a.behind && a.join) launch_dependent_wait();
-    for (int idx = threadIdx.x; idx < kRowTile * (D / 4); idx += kThreads) {
-        const int r = idx / (D / 4), c = idx % (D / 4) * 4;
+    // four columns a thread; the rows of a group of 8 columns are neighbouring lanes, as they lie in the prefix's partials
+    const int n_rows = min(kRowTile, a.R - rt * kRowTile);
+    for (int idx = threadIdx.x; idx < n_rows * (D / 4); idx += kThreads) {
+        const int r = (idx >> 1) % n_rows, c = (idx >> 1) / n_rows * 8 + (idx & 1) * 4;
         const int rr = rt * kRowTile + r;
-        if (rr >= a.R) continue;
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, jml[w * kRowTile + r].x);
@@ -284,25 +285,28 @@ __global__ void __launch_bounds__(kThreads)
         }
         const size_t row = (size_t)kv * a.R + rr;
         if (!a.join) {
-            const size_t slot = row * a.slots + a.slot0 + split;
+            const size_t slot = row * a.splits + split;
             // a chunk that the row sees nothing of: m = -inf, l = 0, and its O is not read
             if (M != -INFINITY) *reinterpret_cast<float4 *>(a.part_o + slot * D + c) = acc;
             if (c == 0) a.part_ml[slot] = make_float2(M, ls);
         } else {
-            if (a.slot0 > 0) {
-                const float2 *ml = a.part_ml + row * a.slots;
-                const float *po = a.part_o + row * a.slots * D + c;
+            if (a.parts.o) {
+                int tile, r;
+                a.parts.place(b, rr, &tile, &r);
+                const size_t part = a.parts.at(h, tile);
+                const float2 *ml = a.parts.ml + part * 128 + r;
+                const float *po = a.parts.o + part * (128 * D) + (c >> 3) * (128 * 8) + r * 8 + (c & 7);
                 float Mn = M;
-                for (int s = 0; s < a.slot0; ++s) Mn = fmaxf(Mn, ml[s].x);  // a prefix chunk's m is finite
+                for (int s = 0; s < a.parts.splits; ++s) Mn = fmaxf(Mn, ml[s * 128].x);  // a prefix chunk's m is finite
                 const float f0 = ex2_approx(M - Mn);
                 ls *= f0;
                 acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
                 M = Mn;
 #pragma unroll 8
-                for (int s = 0; s < a.slot0; ++s) {
-                    const float2 t = ml[s];
+                for (int s = 0; s < a.parts.splits; ++s) {
+                    const float2 t = ml[s * 128];
                     const float f = ex2_approx(t.x - Mn);
-                    const float4 v = *reinterpret_cast<const float4 *>(po + (size_t)s * D);
+                    const float4 v = *reinterpret_cast<const float4 *>(po + (size_t)s * (128 * D));
                     ls = fmaf(t.y, f, ls);
                     acc.x = fmaf(v.x, f, acc.x);
                     acc.y = fmaf(v.y, f, acc.y);
@@ -324,40 +328,98 @@ __global__ void __launch_bounds__(kThreads)
         launch_dependent_wait();
 }
 
-// One warp per row joins its `slots` partials in order: M = max m_t, O = sum O_t 2^(m_t - M) / l.
-template <int D>
-__global__ void __launch_bounds__(128) win_join_kernel(const float *part_o, const float2 *part_ml, void *o, float *lse,
-                                                       long long rows, int slots) {
-    constexpr int V = D / 32;
+// One CTA joins the partials (the prefix's, then its own) of ROWS rows: M = max m_t, O = sum O_t 2^(m_t - M) / l.  A
+// thread owns four columns of a row; the rows of a group of 8 columns are neighbouring lanes, as they lie in the
+// prefix's partials.  The other threads take every kWays-th partial; the ways are added in order.  One row a CTA
+// where there are few (2.4 us for 16 rows of 9 partials, against 4.5 with a warp per row); as many as its threads
+// hold where there are many (one row a CTA took 30 us for 16384 rows of 8 partials, whose 32-byte pieces it fetched
+// from as many lines).
+template <int D, int ROWS>
+__global__ void __launch_bounds__(128) win_join_kernel(WinDecodeArgs a, PrefixParts parts) {
+    constexpr int kCols = D / 4, kWays = 128 / (kCols * ROWS);
+    static_assert(kWays >= 1, "128 threads");
+    __shared__ float4 sum[kWays][ROWS][kCols];
+    __shared__ float2 stat[kWays][ROWS];
+    const int way = threadIdx.x / (kCols * ROWS), in_way = threadIdx.x % (kCols * ROWS);
+    const int sub = (in_way >> 1) % ROWS, c = (in_way >> 1) / ROWS * 2 + (in_way & 1);
+    const size_t rows = (size_t)a.B * a.Hkv * a.R, at = (size_t)blockIdx.x * ROWS + sub;
+    const size_t row = at < rows ? at : rows - 1;  // (a last CTA's extra rows repeat the last one and are not stored)
+    const int P = parts.o ? parts.splits : 0, n = P + a.splits;
+    const float2 *ml = nullptr;
+    const float *po = nullptr;
+    if (P > 0) {
+        const unsigned per_seq = a.Hkv * a.R, b = (unsigned)row / per_seq;
+        const int in = (int)((unsigned)row % per_seq), h = in / a.R;
+        int tile, r;
+        parts.place((int)b, in % a.R, &tile, &r);
+        const size_t part = parts.at(h, tile);
+        ml = parts.ml + part * 128 + r;
+        po = parts.o + part * (128 * D) + (c >> 1) * (128 * 8) + r * 8 + (c & 1) * 4;
+    }
+    const float2 *ml_own = a.part_ml + row * a.splits;
+    const float *po_own = a.part_o + row * a.splits * D + 4 * c;
     launch_dependent_wait();
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= rows) return;
-    const float2 *ml = part_ml + row * slots;
-    const float *po = part_o + row * slots * D + lane * V;
-    float M = -INFINITY;
-    for (int s = lane; s < slots; s += 32) M = fmaxf(M, ml[s].x);
+    // online over this way's partials, eight loads in flight
+    float M = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kBatch = 8;
+    for (int s0 = way; s0 < n; s0 += kWays * kBatch) {
+        float2 t[kBatch];
+        float4 v[kBatch];
+        float Mn = M;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    const float Mb = M == -INFINITY ? 0.f : M;
-    float l = 0.f, acc[V];
+        for (int u = 0; u < kBatch; ++u) {
+            const int s = s0 + u * kWays;
+            t[u] = make_float2(-INFINITY, 0.f);
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (s >= n) continue;
+            t[u] = s < P ? ml[s * 128] : ml_own[s - P];
+            v[u] = *reinterpret_cast<const float4 *>(s < P ? po + (size_t)s * (128 * D) : po_own + (size_t)(s - P) * D);
+        }
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < slots; ++s) {
-        const float2 t = ml[s];
-        if (t.x == -INFINITY) continue;  // a chunk that this row sees nothing of: its O was not written
-        const float f = ex2_approx(t.x - Mb);
-        l = fmaf(t.y, f, l);
+        for (int u = 0; u < kBatch; ++u) Mn = fmaxf(Mn, t[u].x);
+        const float Mb = Mn == -INFINITY ? 0.f : Mn;
+        const float f0 = ex2_approx(M - Mb);
+        l *= f0;
+        acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(po[(size_t)s * D + e], f, acc[e]);
+        for (int u = 0; u < kBatch; ++u) {
+            if (t[u].x == -INFINITY) continue;  // a chunk that this row sees nothing of: its O was not written
+            const float f = ex2_approx(t[u].x - Mb);
+            l = fmaf(t[u].y, f, l);
+            acc.x = fmaf(v[u].x, f, acc.x);
+            acc.y = fmaf(v[u].y, f, acc.y);
+            acc.z = fmaf(v[u].z, f, acc.z);
+            acc.w = fmaf(v[u].w, f, acc.w);
+        }
+        M = Mn;
+    }
+    sum[way][sub][c] = acc;
+    if (c == 0) stat[way][sub] = make_float2(M, l);
+    __syncthreads();
+    if (way > 0 || at >= rows) return;
+    float Mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWays; ++w) Mx = fmaxf(Mx, stat[w][sub].x);
+    const float Mb = Mx == -INFINITY ? 0.f : Mx;
+    l = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWays; ++w) {
+        const float f = ex2_approx(stat[w][sub].x - Mb);
+        const float4 v = sum[w][sub][c];
+        l = fmaf(stat[w][sub].y, f, l);
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z);
+        acc.w = fmaf(v.w, f, acc.w);
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(o) + row * D + lane * V;
-#pragma unroll
-    for (int e = 0; e < V; e += 2)
-        *reinterpret_cast<uint32_t *>(out + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0) lse[row] = (M + __log2f(l)) * 0.69314718055994531f;
+    uint2 w;
+    w.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+    w.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + row * D + 4 * c) = w;
+    if (c == 0) a.lse[row] = (Mx + __log2f(l)) * 0.69314718055994531f;
 }
 
 // A launch, or (behind) one as the programmatic dependent of the launch before it on the stream.
@@ -419,10 +481,14 @@ cudaError_t launch_win_decode(const WinDecodeArgs &a, const CUtensorMap &tk, con
     }
 }
 
-cudaError_t launch_win_join(const float *part_o, const float2 *part_ml, void *o, float *lse, long long rows, int slots,
-                            int D, bool behind, cudaStream_t s) {
-    auto kern = D == 64 ? win_join_kernel<64> : D == 128 ? win_join_kernel<128> : win_join_kernel<256>;
-    return launch_behind(kern, dim3((unsigned)((rows + 3) / 4)), 128, 0, behind, s, part_o, part_ml, o, lse, rows, slots);
+cudaError_t launch_win_join(const WinDecodeArgs &a, const PrefixParts &parts, cudaStream_t s) {
+    const long long rows = (long long)a.B * a.Hkv * a.R;
+    const bool many = rows > 1024;
+    const int per = many ? 128 / (a.D / 4) : 1;
+    auto kern = a.D == 64    ? (many ? win_join_kernel<64, 8> : win_join_kernel<64, 1>)
+                : a.D == 128 ? (many ? win_join_kernel<128, 4> : win_join_kernel<128, 1>)
+                             : (many ? win_join_kernel<256, 2> : win_join_kernel<256, 1>);
+    return launch_behind(kern, dim3((unsigned)((rows + per - 1) / per)), 128, 0, true, s, a, parts);
 }
 
 }  // namespace fa

@@ -14,13 +14,13 @@ struct WinDecodeArgs {
     float scale_log2;
     int *status;
     int splits;        // CTAs a sequence's tiles are dealt to
-    // partials [row][slots]: this launch writes slots slot0 .. slot0 + splits - 1.  join (splits = 1): instead, each CTA
-    // joins its rows with the slot0 partials that the launch before it wrote (none: slot0 = 0) and writes o and lse.
-    int slots, slot0;
-    float *part_o;
-    float2 *part_ml;
+    float *part_o;     // partials [row][splits][D]
+    float2 *part_ml;   // [row][splits]
+    // join (splits = 1): instead of a partial, each CTA joins its rows with the prefix's partials (none: parts.o null) and
+    // writes o and lse
     int join;
-    int behind;  // launched as the programmatic dependent of the launch that writes those partials
+    PrefixParts parts;
+    int behind;  // launched as the programmatic dependent of the launch that writes the prefix's partials
 };
 
 // CTAs per (sequence, key head, row tile) for caches that need up to `tiles` tiles.
@@ -29,8 +29,7 @@ int win_decode_tile_keys();
 // SMs that all CTAs of such a launch take at once.
 int win_decode_sms(int B, int Hkv, int R, int splits, int D);
 cudaError_t launch_win_decode(const WinDecodeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s);
-// O and LSE of `rows` rows from `slots` partials each (part_o [row][slot][D], part_ml [row][slot]).
-cudaError_t launch_win_join(const float *part_o, const float2 *part_ml, void *o, float *lse, long long rows, int slots,
-                            int D, bool behind, cudaStream_t s);
+// O and LSE of every row from its a.splits partials and the prefix's (parts.o null: none); a dependent launch.
+cudaError_t launch_win_join(const WinDecodeArgs &a, const PrefixParts &parts, cudaStream_t s);
 
 }  // namespace fa

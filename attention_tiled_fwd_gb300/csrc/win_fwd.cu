@@ -114,11 +114,11 @@ __device__ __forceinline__ SpanBlock<kTiles> window_block(const SpanArgs &a, int
 template <int kTiles>
 __device__ __forceinline__ SpanBlock<kTiles> prefix_block(const SpanArgs &a, int L) {
     SpanBlock<kTiles> w;
-    const int pairs = (a.m_tiles + kTiles - 1) / kTiles;
+    const int pairs = (a.parts.m_tiles + kTiles - 1) / kTiles;
     const int m = (L % pairs) * kTiles;
     const int rest = L / pairs;
-    const int chunk = rest % a.splits;
-    w.kv_bh = rest / a.splits;
+    const int chunk = rest % a.parts.splits;
+    w.kv_bh = rest / a.parts.splits;
     w.y_off = chunk * a.chunk_tiles * kBN;
     w.span.n_sink = 0;
     w.span.lo = 0;
@@ -130,7 +130,7 @@ __device__ __forceinline__ SpanBlock<kTiles> prefix_block(const SpanArgs &a, int
         w.p0[x] = 0;
         w.from[x] = 0;
         w.to[x] = w.span.n;
-        w.n[x] = m + x < a.m_tiles ? w.span.n : 0;
+        w.n[x] = m + x < a.parts.m_tiles ? w.span.n : 0;
     }
     return w;
 }
@@ -159,14 +159,14 @@ static_assert(sizeof(SoftBlock) == 32, "two 16-byte loads");
 
 // First sequence and first row (of the R rows of a sequence and key head) of packed query tile t.
 __device__ __forceinline__ void packed_tile(const SpanArgs &a, int t, int *b0, int *r0) {
-    const int row_tiles = (a.R + a.rb - 1) / a.rb;  // 1 unless a sequence alone has more than kBM rows
-    *b0 = t / row_tiles * a.nb;
-    *r0 = t % row_tiles * a.rb;
+    const int row_tiles = (a.parts.R + a.parts.rb - 1) / a.parts.rb;  // 1 unless a sequence alone has more than kBM rows
+    *b0 = t / row_tiles * a.parts.nb;
+    *r0 = t % row_tiles * a.parts.rb;
 }
 
 template <int kTiles>
 __host__ __device__ inline int span_blocks(const SpanArgs &a, bool prefix) {
-    if (prefix) return (a.m_tiles + kTiles - 1) / kTiles * a.splits * a.Hkv;
+    if (prefix) return (a.parts.m_tiles + kTiles - 1) / kTiles * a.parts.splits * a.Hkv;
     const int per_block = kTiles == 2 && a.pairing == kTwoRowTiles ? 2 * kBM : kBM;
     return (a.Nq + per_block - 1) / per_block * (int)a.per_rows.d;
 }
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
                             // rb rows of each of nb sequences, packed; the tile's rows behind them keep
                             // whatever was there (no row's result depends on another row, and they are
                             // not stored)
-                            mbar_arrive_expect_tx(&q_full[qb], n_q_tiles * a.rb * a.nb * D * 2);
+                            mbar_arrive_expect_tx(&q_full[qb], n_q_tiles * a.parts.rb * a.parts.nb * D * 2);
                             for (int x = 0; x < n_q_tiles; ++x) {
                                 int b0, r0;
                                 packed_tile(a, w.yq[x], &b0, &r0);
@@ -662,11 +662,9 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
             uint32_t ov[32];
             if constexpr (PREFIX) {
                 // this chunk's partial of the row: O unnormalised, m (log2 units) and l
-                int b0, r0;
-                packed_tile(a, yq, &b0, &r0);
-                const int b = b0 + r / a.rb, rr = r0 + r % a.rb;
-                const bool valid = r < a.rb * a.nb && b < a.B && rr < a.R;
-                const size_t slot = (((size_t)b * a.Hkv + w.kv_bh) * a.R + rr) * a.slots + zq;
+                // (rows of the tile behind its packed ones are written too and never read)
+                const size_t part = a.parts.at(w.kv_bh, yq) + zq;
+                float *dst = a.parts.o + part * (kBM * D) + r * 8;
 #pragma unroll
                 for (int ch = 0; ch < D / 32; ++ch) {
                     tmem_ld32(tmem + lane_base + o_col + ch * 32, ov);
@@ -675,12 +673,10 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
                         tc_fence_before();
                         warp_arrive(&o_free[x]);
                     }
-                    if (valid) {
 #pragma unroll
-                        for (int v8 = 0; v8 < 4; ++v8) st_global_v8(a.part_o + slot * D + ch * 32 + 8 * v8, ov + 8 * v8);
-                    }
+                    for (int v8 = 0; v8 < 4; ++v8) st_global_v8(dst + (ch * 4 + v8) * (kBM * 8), ov + 8 * v8);
                 }
-                if (valid) a.part_ml[slot] = make_float2(m, l);
+                a.parts.ml[part * kBM + r] = make_float2(m, l);
                 continue;
             }
             const float inv_l = 1.f / l;
@@ -756,7 +752,7 @@ cudaError_t launch_spec(const SpanArgs &a, const CUtensorMap &tq, const CUtensor
 
 cudaError_t launch_win_fwd(const SpanArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                            const CUtensorMap &tks, const CUtensorMap &tvs, const CUtensorMap &to, cudaStream_t s) {
-    const bool prefix = a.part_o != nullptr;
+    const bool prefix = a.parts.o != nullptr;
     switch (kernel_head_dim(a.D)) {
         case 64:
             return prefix ? launch_spec<64, 4, true>(a, tq, tk, tv, tks, tvs, to, s)

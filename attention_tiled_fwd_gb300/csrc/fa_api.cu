@@ -489,7 +489,7 @@ extern "C" int fa_window_forward(const void *q, const void *k, const void *v, vo
     const int heads = a.pairing == kTwoHeads ? Hq / 2 : Hq;
     a.per_rows = FastDiv(B * heads), a.per_seq = FastDiv(heads), a.group = FastDiv(Hq / Hkv);
     // sink tiles read through maps that end at the last sink
-    const int bn = fwd_block_n(kernel_head_dim(D)), sink_rows = w.sinks > 0 ? w.sinks : Nk;
+    const int bn = win_fwd_keys(D), sink_rows = w.sinks > 0 ? w.sinks : Nk;
     CUtensorMap tq, tk, tv, tks, tvs, to;
     if (encode_rows(&tq, q, B * Hq, Nq, Nq, D, 128) != FA_OK ||
         encode_rows(&tk, k, B * Hkv, Nk, kv_rows, D, bn) != FA_OK ||

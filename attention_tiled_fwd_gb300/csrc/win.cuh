@@ -130,7 +130,9 @@ struct SpanArgs {
     int chunk_tiles;
 };
 // Query tiles of a CTA of the windowed forward at head dimension D (one: two CTAs share an SM).
-inline int win_fwd_tiles(int D) { return D <= 64 ? 1 : 2; }
+inline int win_fwd_tiles(int D) { return 1; }
+// Keys of its K/V tiles.
+inline int win_fwd_keys(int D) { return D <= 64 ? 128 : 64; }
 enum : int { kOneTile = 0, kTwoHeads = 1, kTwoRowTiles = 2 };
 
 cudaError_t launch_win_fwd(const SpanArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,

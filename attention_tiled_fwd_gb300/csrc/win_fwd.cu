@@ -29,7 +29,6 @@ namespace fa {
 namespace {
 
 constexpr int kBM = 128;            // rows per query tile (TMEM lanes)
-constexpr int kBN = 128;            // keys per K/V tile
 constexpr int kFirstSoftmaxWarp = 2;
 
 enum : int { kSiteQ = 181, kSiteSlotEmpty, kSiteSlotFull, kSiteSFull, kSitePFull, kSitePV, kSiteFinal, kSiteDrain,
@@ -37,17 +36,19 @@ enum : int { kSiteQ = 181, kSiteSlotEmpty, kSiteSlotFull, kSiteSFull, kSitePFull
 
 constexpr int kBlocks = 4;  // blocks that the producer has worked out ahead of the softmax warps
 
-template <int D, int NSLOT, int kTiles>
+template <int D, int NSLOT, int kTiles, int kBN>
 struct SpanSmem {
     static constexpr int kPanels = D / 64;
     static constexpr int kQBytes = kBM * D * 2;    // one query tile
     static constexpr int kSlotBytes = kBN * D * 2;  // one K or V tile
-    static constexpr int kQBufs = kTiles == 1 ? 2 : 1;  // one tile a CTA: the next block's Q has a buffer of its own
+    // one tile a CTA: the next block's Q has a buffer of its own (D = 64), O is staged 64 columns at a time
+    static constexpr int kQBufs = kTiles == 1 && D == 64 ? 2 : 1;
+    static constexpr int kStageCols = kTiles == 1 ? 64 : D;
     static constexpr int kThreads = 32 * kFirstSoftmaxWarp + 128 * kTiles;
     static constexpr int kQOff = 0;
     static constexpr int kSlotOff = kQBufs * kTiles * kQBytes;
     static constexpr int kStageOff = kSlotOff + NSLOT * kSlotBytes;  // one query tile's O, staged for TMA stores
-    static constexpr int kBarOff = kStageOff + kQBytes;
+    static constexpr int kBarOff = kStageOff + kBM * kStageCols * 2;
     // q_full[2], q_empty[2], slot_full[NSLOT], slot_empty[NSLOT], per tile: s_full, p_full, pv_done, o_free,
     // stage_full; final, stage_free, s_free; block_full[kBlocks], block_empty[kBlocks]
     static constexpr int kNumBars = 4 + 2 * NSLOT + 5 * kTiles + 3 + 2 * kBlocks;
@@ -76,7 +77,7 @@ struct SpanBlock {
 };
 
 // Windowed blocks in longest-first order: the last rows of every head first.
-template <int kTiles>
+template <int kTiles, int kBN>
 __device__ __forceinline__ SpanBlock<kTiles> window_block(const SpanArgs &a, int L) {
     SpanBlock<kTiles> w;
     const int per_block = kTiles == 2 && a.pairing == kTwoRowTiles ? 2 * kBM : kBM;
@@ -111,7 +112,7 @@ __device__ __forceinline__ SpanBlock<kTiles> window_block(const SpanArgs &a, int
 }
 
 // Shared-prefix blocks: two packed query tiles of a key head against one chunk of the prefix.
-template <int kTiles>
+template <int kTiles, int kBN>
 __device__ __forceinline__ SpanBlock<kTiles> prefix_block(const SpanArgs &a, int L) {
     SpanBlock<kTiles> w;
     const int pairs = (a.parts.m_tiles + kTiles - 1) / kTiles;
@@ -135,14 +136,14 @@ __device__ __forceinline__ SpanBlock<kTiles> prefix_block(const SpanArgs &a, int
     return w;
 }
 
-template <bool PREFIX, int kTiles>
+template <bool PREFIX, int kTiles, int kBN>
 __device__ __forceinline__ SpanBlock<kTiles> span_block(const SpanArgs &a, int L) {
-    if constexpr (PREFIX) return prefix_block<kTiles>(a, L);
-    return window_block<kTiles>(a, L);
+    if constexpr (PREFIX) return prefix_block<kTiles, kBN>(a, L);
+    return window_block<kTiles, kBN>(a, L);
 }
 
 // Columns of key tile j that are computed: all of them, or 32 of a sink tile whose sinks fit there.
-template <bool PREFIX>
+template <bool PREFIX, int kBN>
 __device__ __forceinline__ int tile_cols(const SpanArgs &a, int n_sink, int j) {
     return PREFIX || j >= n_sink || a.sinks - j * kBN > 32 ? kBN : 32;
 }
@@ -174,12 +175,13 @@ __host__ __device__ inline int span_blocks(const SpanArgs &a, bool prefix) {
 // Persistent: the grid has at most kCtas CTAs per SM, each walking its blocks in turn, so the next block's
 // Q load and first S products overlap the previous block's last products and epilogue.  The K/V ring
 // and every barrier's phase run on across blocks.
-template <int D, int NSLOT, bool PREFIX, int kTiles, int kCtas>
+// kBN: keys per K/V tile.
+template <int D, int NSLOT, bool PREFIX, int kTiles, int kCtas, int kBN>
 __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
     win_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_ks,
                    const __grid_constant__ CUtensorMap tmap_vs, const __grid_constant__ CUtensorMap tmap_o, SpanArgs a) {
-    using L = SpanSmem<D, NSLOT, kTiles>;
+    using L = SpanSmem<D, NSLOT, kTiles, kBN>;
     constexpr int kPanels = L::kPanels;
     constexpr uint32_t kTmemCols = 512 / kCtas;
     constexpr int kQBufs = L::kQBufs;
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
             for (int k = 0; ok && k * (int)gridDim.x < n_work; ++k) {
                 const int Lw = persistent_work_index(k, n_work);
                 if (Lw < 0) continue;
-                const SpanBlock<kTiles> w = span_block<PREFIX, kTiles>(a, Lw);
+                const SpanBlock<kTiles> w = span_block<PREFIX, kTiles, kBN>(a, Lw);
                 SoftBlock sb[kTiles];
 #pragma unroll
                 for (int x = 0; x < kTiles; ++x)
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
         for (int k = 0; ok && k * (int)gridDim.x < n_work; ++k) {
             const int Lw = persistent_work_index(k, n_work);
             if (Lw < 0) continue;
-            const SpanBlock<kTiles> w = span_block<PREFIX, kTiles>(a, Lw);
+            const SpanBlock<kTiles> w = span_block<PREFIX, kTiles, kBN>(a, Lw);
             const int qb = nb % kQBufs;
             const uint64_t q_desc = sdesc_sw128(smem_u32(q_s + qb * kTiles * L::kQBytes), 16, 1024);
             if (!(ok = warp_wait(&q_full[qb], (nb / kQBufs) & 1, a.status, kSiteQ))) break;
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
                         const uint32_t off = (ks >> 2) * (kBM * 128) + (ks & 3) * 32;
                         mma_ss(tmem + kColS + x * kBN, sdesc_add(q_desc, x * L::kQBytes + off),
                                sdesc_add(k_desc, (ks >> 2) * (kBN * 128) + (ks & 3) * 32),
-                               tile_cols<PREFIX>(a, w.span.n_sink, j) == 32 ? idesc_sink : idesc_s, ks > 0);
+                               tile_cols<PREFIX, kBN>(a, w.span.n_sink, j) == 32 ? idesc_sink : idesc_s, ks > 0);
                     }
                     mma_commit(&s_full[x]);
                 }
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
                     return;
                 tc_fence_after();
                 const uint64_t v_desc = sdesc_sw128(slot_addr + slot * L::kSlotBytes, kBN * 128, 1024);
-                const int steps = tile_cols<PREFIX>(a, w.span.n_sink, j) / 16;
+                const int steps = tile_cols<PREFIX, kBN>(a, w.span.n_sink, j) / 16;
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < kBN / 16; ++kk)
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
         const float c = a.scale_log2;
         bool ok = true;
         int step0 = 0;     // steps of this tile before the current block
-        int blocks_x = 0;  // epilogues of this tile so far (phase of stage_full[x])
+        int stores = 0;    // stores of this tile's O so far (phase of stage_full[x])
         for (int k = 0; ok; ++k) {
             const int e = k % kBlocks;
             ok = mbar_wait(&block_full[e], (k / kBlocks) & 1, a.status, kSiteBlock);
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
                     }
                     tmem_st16(tmem + lane_base + p_col + h * 16, pk);
                 };
-                if (tile_cols<PREFIX>(a, w.n_sink, step) == 32) {
+                if (tile_cols<PREFIX, kBN>(a, w.n_sink, step) == 32) {
                     // a sink tile whose sinks fit into 32 columns: every row of the query tile sees all of them
                     uint32_t raw[32];
                     tmem_ld32(tmem + lane_base + s_col, raw);
@@ -645,18 +647,10 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
                 warp_arrive(&p_full[x]);
             }
             // the staging buffer's use number of this tile's epilogue in this block (tile A's before tile B's)
-            const int use = w.use;
             if (!ok || n == 0) continue;
             // the block's last PV_X has completed: O_X is final
             step0 += n;
             ok = mbar_wait(&pv_done[x], (step0 - 1) & 1, a.status, kSiteFinal);
-            // the previous use's TMA store has finished reading the staging buffer (one tile a CTA: its own store of a
-            // block ago, which the thread that issued it waits for only here)
-            if (kTiles == 1 && !PREFIX && use >= 1 && quarter == kFirstSoftmaxWarp % 4 && lane == 0) {
-                tma_store_wait_read();
-                mbar_arrive(stage_free);
-            }
-            if (!PREFIX && ok && use >= 1) ok = mbar_wait(stage_free, (use - 1) & 1, a.status, kSiteStage);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             tc_fence_after();
             uint32_t ov[32];
@@ -680,47 +674,62 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
                 continue;
             }
             const float inv_l = 1.f / l;
-            // O / l as bf16 into the staging buffer: 128-byte-swizzled panels of 64 columns, row r of panel
-            // p at p * 16 KB + r * 128, its 16-byte chunk k at k ^ (r % 8) (conflict-free across the lanes)
+            if (yq + r < a.Nq) a.lse[(size_t)zq * a.Nq + yq + r] = (m + __log2f(l)) * 0.69314718055994531f;
+            // O / l as bf16 through the staging buffer, kStageCols columns at a time: 128-byte-swizzled panels of 64
+            // columns, row r of panel p at p * 16 KB + r * 128, its 16-byte chunk k at k ^ (r % 8) (conflict-free
+            // across the lanes)
+            constexpr int kParts = D / L::kStageCols, kPartPanels = L::kStageCols / 64;
+            const bool storer = quarter == kFirstSoftmaxWarp % 4 && lane == 0;  // one thread of the tile stores
 #pragma unroll
-            for (int ch = 0; ch < D / 32; ++ch) {
-                tmem_ld32(tmem + lane_base + o_col + ch * 32, ov);
-                tmem_wait_ld();
-                if (ch == D / 32 - 1) {
-                    // every read of O_X is done: the next block's first PV_X may overwrite it
-                    tc_fence_before();
-                    warp_arrive(&o_free[x]);
+            for (int part = 0; part < kParts; ++part) {
+                const int use = w.use * kParts + part;
+                // the previous use's TMA store has finished reading the buffer (one tile a CTA: the thread that issued
+                // that store waits for it only here)
+                if (kTiles == 1 && use >= 1 && storer) {
+                    tma_store_wait_read();
+                    mbar_arrive(stage_free);
                 }
-                uint8_t *prow = stage + (ch >> 1) * (kBM * 128) + r * 128;
+                if (use >= 1) ok = mbar_wait(stage_free, (use - 1) & 1, a.status, kSiteStage);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
 #pragma unroll
-                for (int v4 = 0; v4 < 4; ++v4)
-                    st_shared_v4(prow + ((((ch & 1) * 4 + v4) ^ (r & 7)) << 4),
-                                 pack_bf16x2(__uint_as_float(ov[v4 * 8 + 0]) * inv_l, __uint_as_float(ov[v4 * 8 + 1]) * inv_l),
-                                 pack_bf16x2(__uint_as_float(ov[v4 * 8 + 2]) * inv_l, __uint_as_float(ov[v4 * 8 + 3]) * inv_l),
-                                 pack_bf16x2(__uint_as_float(ov[v4 * 8 + 4]) * inv_l, __uint_as_float(ov[v4 * 8 + 5]) * inv_l),
-                                 pack_bf16x2(__uint_as_float(ov[v4 * 8 + 6]) * inv_l, __uint_as_float(ov[v4 * 8 + 7]) * inv_l));
-            }
-            fence_proxy_async_smem();  // the staged tile is read by the TMA (async proxy)
-            warp_arrive(&stage_full[x]);
-            if (yq + r < a.Nq)
-                a.lse[(size_t)zq * a.Nq + yq + r] = (m + __log2f(l)) * 0.69314718055994531f;
-            if (quarter == kFirstSoftmaxWarp % 4 && lane == 0) {
-                // one thread of the tile stores the staged panels (rows past N and columns past the caller's
-                // D are clipped by the tensor map) and frees the buffer once the stores have read it
-                if (mbar_wait(&stage_full[x], blocks_x & 1, a.status, kSiteStage)) {
-#pragma unroll
-                    for (int p = 0; p < kPanels; ++p)
-                        if (p * 64 < a.D) tma_store_3d(&tmap_o, stage + p * (kBM * 128), p * 64, yq, zq);
-                    tma_store_commit();
-                    if (kTiles == 2) {
-                        tma_store_wait_read();
-                        mbar_arrive(stage_free);
+                for (int ch = 0; ch < L::kStageCols / 32; ++ch) {
+                    tmem_ld32(tmem + lane_base + o_col + part * L::kStageCols + ch * 32, ov);
+                    tmem_wait_ld();
+                    if (part == kParts - 1 && ch == L::kStageCols / 32 - 1) {
+                        // every read of O_X is done: the next block's first PV_X may overwrite it
+                        tc_fence_before();
+                        warp_arrive(&o_free[x]);
                     }
-                } else {
-                    ok = false;
+                    uint8_t *prow = stage + (ch >> 1) * (kBM * 128) + r * 128;
+#pragma unroll
+                    for (int v4 = 0; v4 < 4; ++v4)
+                        st_shared_v4(prow + ((((ch & 1) * 4 + v4) ^ (r & 7)) << 4),
+                                     pack_bf16x2(__uint_as_float(ov[v4 * 8 + 0]) * inv_l, __uint_as_float(ov[v4 * 8 + 1]) * inv_l),
+                                     pack_bf16x2(__uint_as_float(ov[v4 * 8 + 2]) * inv_l, __uint_as_float(ov[v4 * 8 + 3]) * inv_l),
+                                     pack_bf16x2(__uint_as_float(ov[v4 * 8 + 4]) * inv_l, __uint_as_float(ov[v4 * 8 + 5]) * inv_l),
+                                     pack_bf16x2(__uint_as_float(ov[v4 * 8 + 6]) * inv_l, __uint_as_float(ov[v4 * 8 + 7]) * inv_l));
                 }
+                fence_proxy_async_smem();  // the staged tile is read by the TMA (async proxy)
+                warp_arrive(&stage_full[x]);
+                if (storer) {
+                    // rows past Nq and columns past the caller's D are clipped by the tensor map
+                    if (mbar_wait(&stage_full[x], stores & 1, a.status, kSiteStage)) {
+#pragma unroll
+                        for (int p = 0; p < kPartPanels; ++p) {
+                            const int col = part * L::kStageCols + p * 64;
+                            if (col < a.D) tma_store_3d(&tmap_o, stage + p * (kBM * 128), col, yq, zq);
+                        }
+                        tma_store_commit();
+                        if (kTiles == 2) {
+                            tma_store_wait_read();
+                            mbar_arrive(stage_free);
+                        }
+                    } else {
+                        ok = false;
+                    }
+                }
+                ++stores;
             }
-            ++blocks_x;
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         }
         tma_store_wait_read();  // the CTA's shared memory must outlive the stores' reads
@@ -734,12 +743,12 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
     }
 }
 
-template <int D, int NSLOT, bool PREFIX, int kTiles = 2, int kCtas = 1>
+template <int D, int NSLOT, bool PREFIX, int kTiles = 2, int kCtas = 1, int kBN = 128>
 cudaError_t launch_spec(const SpanArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                         const CUtensorMap &tks, const CUtensorMap &tvs, const CUtensorMap &to, cudaStream_t s) {
-    using L = SpanSmem<D, NSLOT, kTiles>;
+    using L = SpanSmem<D, NSLOT, kTiles, kBN>;
     static_assert(L::kAlloc <= 233472 / kCtas - 1024, "shared memory budget (a CTA's own, and 1 KB that the system takes)");
-    auto kern = win_fwd_kernel<D, NSLOT, PREFIX, kTiles, kCtas>;
+    auto kern = win_fwd_kernel<D, NSLOT, PREFIX, kTiles, kCtas, kBN>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
     const int n_work = span_blocks<kTiles>(a, PREFIX);
@@ -759,7 +768,7 @@ cudaError_t launch_win_fwd(const SpanArgs &a, const CUtensorMap &tq, const CUten
                           : launch_spec<64, 4, false, 1, 2>(a, tq, tk, tv, tks, tvs, to, s);
         case 128:
             return prefix ? launch_spec<128, 4, true>(a, tq, tk, tv, tks, tvs, to, s)
-                          : launch_spec<128, 4, false>(a, tq, tk, tv, tks, tvs, to, s);
+                          : launch_spec<128, 4, false, 1, 2, 64>(a, tq, tk, tv, tks, tvs, to, s);
         default: return launch_win_fwd_wide(a, tq, tk, tv, tks, tvs, s);
     }
 }

@@ -24,7 +24,8 @@ from ._native import FA_BF16, FA_F32, FAError
 
 __all__ = ["fa_forward", "fa_backward_dq", "fa_backward_dkdv", "fa_backward_atomic", "fa_decode", "fa_decode_workspace_bytes",
            "fa_decode_noalloc",
-           "fa_window_forward", "fa_window_backward_dq", "fa_window_backward_dkdv", "fa_window_backward_workspace_bytes",
+           "fa_window_forward", "fa_window_backward_dq", "fa_window_backward_dkdv", "fa_window_backward",
+           "fa_window_backward_workspace_bytes",
            "fa_window_decode", "fa_window_decode_workspace_bytes", "fa_prefix_decode", "fa_prefix_decode_workspace_bytes",
            "fa_device_status", "fa_selftest_timeout", "FAError", "FA_BF16", "FA_F32", "attention_flops",
            "attention", "window_attention"]
@@ -376,6 +377,42 @@ def fa_window_backward_dkdv(q, k, v, dO, lse, delta, window: int, sinks: int = 0
                                                 _nbytes(workspace), _stream_handle(stream, dev))
     _native.check(rc, "fa_window_backward_dkdv")
     return dk, dv
+
+
+def fa_window_backward(q, k, v, o, dO, lse, window: int, sinks: int = 0, scale: Optional[float] = None,
+                       grad_dtype: torch.dtype = torch.float32, dq: Optional[torch.Tensor] = None,
+                       dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
+                       delta: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None):
+    """fa_window_backward_dq and fa_window_backward_dkdv in one call (fa_window_backward).  Returns (dq, dk, dv, delta)."""
+    B, Hq, Nq, D, Hkv, Nk = _grouped(q, k)
+    dev = _device()
+    rows, keys = (B, Hq, Nq, D), (B, Hkv, Nk, D)
+    for t, n, shape in ((q, "q", rows), (k, "k", keys), (v, "v", keys), (o, "o", rows), (dO, "dO", rows)):
+        _bf16(t, n, shape, dev)
+    _tensor(lse, "lse", torch.float32, (B, Hq, Nq), dev)
+    if dq is None:
+        dq = _empty(q, q.shape, grad_dtype, stream)
+    if dk is None:
+        dk = _empty(k, k.shape, dq.dtype, stream)
+    if dv is None:
+        dv = _empty(k, k.shape, dq.dtype, stream)
+    code = _dtype_code(dq)
+    for t, n, shape in ((dq, "dq", rows), (dk, "dk", keys), (dv, "dv", keys)):
+        _tensor(t, n, dq.dtype, shape, dev)
+    if delta is None:
+        delta = _empty(q, (B, Hq, Nq), torch.float32, stream)
+    else:
+        _tensor(delta, "delta", torch.float32, (B, Hq, Nq), dev)
+    window, sinks = _c_int(window), _c_int(sinks)
+    workspace = _workspace(workspace, q, stream, dev, "fa_window_backward_workspace_bytes", B, Hq, Hkv, Nq, Nk, D, window,
+                           sinks)
+    rc = _native.load().fa_window_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dO.data_ptr(),
+                                           lse.data_ptr(), delta.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                           B, Hq, Hkv, Nq, Nk, D, window, sinks, _scale(scale, D), FA_BF16, code,
+                                           _ptr(workspace), _nbytes(workspace), _stream_handle(stream, dev))
+    _native.check(rc, "fa_window_backward")
+    return dq, dk, dv, delta
 
 
 def _rows_and_cache(q, k, v, lens, o, lse, stream):

@@ -23,7 +23,7 @@ FA_DECODE_NOALLOC_SCRATCH_BYTES = 16 << 20  # fa.h: fixed scratch of fa_decode_n
 EXPORTS = ("fa_forward", "fa_backward_dq", "fa_backward_dkdv", "fa_backward_atomic", "fa_decode",
            "fa_decode_workspace_bytes",
            "fa_decode_noalloc", "fa_window_forward", "fa_window_backward_dq", "fa_window_backward_dkdv",
-           "fa_window_backward_workspace_bytes", "fa_window_decode", "fa_window_decode_workspace_bytes",
+           "fa_window_backward", "fa_window_backward_workspace_bytes", "fa_window_decode", "fa_window_decode_workspace_bytes",
            "fa_prefix_decode", "fa_prefix_decode_workspace_bytes", "fa_status_string", "fa_device_status", "fa_selftest_timeout", "fa_selftest_exp2", "fa_version")
 
 _lib = None
@@ -53,6 +53,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_window_forward.argtypes = [_p] * 5 + [_i] * 9 + [_f, _i, _p]
     lib.fa_window_backward_dq.argtypes = [_p] * 8 + [_i] * 8 + [_f, _i, _i, _p]
     lib.fa_window_backward_dkdv.argtypes = [_p] * 8 + [_i] * 8 + [_f, _i, _i, _p, sz, _p]
+    lib.fa_window_backward.argtypes = [_p] * 10 + [_i] * 8 + [_f, _i, _i, _p, sz, _p]
     lib.fa_window_backward_workspace_bytes.argtypes = [_i] * 8 + [szp]
     lib.fa_window_decode.argtypes = [_p] * 6 + [_i] * 8 + [_f, _p, sz, _p]
     lib.fa_window_decode_workspace_bytes.argtypes = [_i] * 8 + [szp]
@@ -66,7 +67,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_version.argtypes = []
     for name in ("fa_forward", "fa_backward_dq", "fa_backward_dkdv", "fa_backward_atomic", "fa_decode", "fa_decode_workspace_bytes",
                  "fa_decode_noalloc", "fa_window_forward", "fa_window_backward_dq", "fa_window_backward_dkdv",
-                 "fa_window_backward_workspace_bytes", "fa_window_decode", "fa_window_decode_workspace_bytes",
+                 "fa_window_backward", "fa_window_backward_workspace_bytes", "fa_window_decode", "fa_window_decode_workspace_bytes",
                  "fa_prefix_decode", "fa_prefix_decode_workspace_bytes", "fa_device_status",
                  "fa_selftest_timeout", "fa_selftest_exp2", "fa_version"):
         getattr(lib, name).restype = _i

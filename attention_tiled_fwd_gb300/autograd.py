@@ -67,17 +67,17 @@ class _WindowAttention(torch.autograd.Function):
         lib, stream = _native.load(), _stream_handle(None, _device())
         dq, delta = torch.empty_like(q), torch.empty_like(lse)
         common = (*ctx.sizes, ctx.scale, FA_BF16, FA_BF16)
-        rc = lib.fa_window_backward_dq(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dO.data_ptr(),
-                                       lse.data_ptr(), delta.data_ptr(), dq.data_ptr(), *common, stream)
-        _native.check(rc, "fa_window_backward_dq")
         if not (ctx.needs_input_grad[1] or ctx.needs_input_grad[2]):
+            rc = lib.fa_window_backward_dq(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dO.data_ptr(),
+                                           lse.data_ptr(), delta.data_ptr(), dq.data_ptr(), *common, stream)
+            _native.check(rc, "fa_window_backward_dq")
             return dq, None, None, None, None, None
         dk, dv = torch.empty_like(k), torch.empty_like(v)
         workspace = _workspace(None, q, None, 0, "fa_window_backward_workspace_bytes", *ctx.sizes)
-        rc = lib.fa_window_backward_dkdv(q.data_ptr(), k.data_ptr(), v.data_ptr(), dO.data_ptr(), lse.data_ptr(),
-                                         delta.data_ptr(), dk.data_ptr(), dv.data_ptr(), *common, _ptr(workspace),
-                                         _nbytes(workspace), stream)
-        _native.check(rc, "fa_window_backward_dkdv")
+        rc = lib.fa_window_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dO.data_ptr(), lse.data_ptr(),
+                                    delta.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *common,
+                                    _ptr(workspace), _nbytes(workspace), stream)
+        _native.check(rc, "fa_window_backward")
         return dq, dk, dv, None, None, None
 
 

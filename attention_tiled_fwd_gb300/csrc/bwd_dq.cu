@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if constexpr (WIN) launch_dependents();  // the dK/dV kernel of the same call fills the SMs as they come free
     const uint32_t tmem = *tmem_holder;
 
     if (warp == 0) {

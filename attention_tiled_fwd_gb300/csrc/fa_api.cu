@@ -502,12 +502,80 @@ extern "C" int fa_window_forward(const void *q, const void *k, const void *v, vo
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+namespace {
+struct WinBackward {
+    const void *q, *k, *v, *o, *dO;
+    const float *lse;
+    float *delta;
+    void *dq, *dk, *dv;
+    int B, Hq, Hkv, Nq, Nk, D, window, sinks;
+    float scale;
+    int grad_dtype;
+    void *workspace;
+    size_t workspace_bytes;
+};
+
+int check_window_backward(const WinBackward &w, int dtype) {
+    if (dtype != FA_BF16 || (w.grad_dtype != FA_BF16 && w.grad_dtype != FA_F32)) return FA_ERR_DTYPE;
+    return check_window(w.B, w.Hq, w.Hkv, w.Nq, w.Nk, w.Nk, w.D, w.window, w.sinks, w.scale);
+}
+
+int window_dq(const WinBackward &w, const DeviceState &st, cudaStream_t s) {
+    const int B = w.B, Hq = w.Hq, Hkv = w.Hkv, Nq = w.Nq, Nk = w.Nk, D = w.D;
+    BwdArgs a{w.q, w.k, w.v, w.o, w.dO, w.lse, w.delta, w.dq, nullptr, nullptr, B, Hq, Nq, D, w.scale, w.scale * log2e(), 1,
+              w.grad_dtype == FA_BF16 ? 1 : 0, st.status_word, B * Hq, window_args(Hkv, Nk, w.window, w.sinks)};
+    CUtensorMap tq, tk, tv, tdo, to, tdq;
+    if (encode_rows(&tq, w.q, B * Hq, Nq, Nq, D, 128) != FA_OK || encode_rows(&tk, w.k, B * Hkv, Nk, Nk, D, kDqKRows) != FA_OK ||
+        encode_rows(&tv, w.v, B * Hkv, Nk, Nk, D, kDqKRows) != FA_OK ||
+        encode_rows(&tdo, w.dO, B * Hq, Nq, Nq, D, 128) != FA_OK || encode_rows(&to, w.o, B * Hq, Nq, Nq, D, 128) != FA_OK ||
+        encode_3d(&tdq, w.dq, B * Hq, Nq, D, 128, w.grad_dtype == FA_F32) != FA_OK)
+        return FA_ERR_CUDA;
+    return launch_win_dq(a, tq, tk, tv, tdo, to, tdq, st.num_sms, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// The sink tiles' partials of dK, then of dV, in the workspace; checks that it holds them.
+int check_window_workspace(const WinBackward &w, const WinArgs &win) {
+    const size_t floats = sink_part_floats(win, w.B, w.D);
+    if (floats == 0) return FA_OK;
+    const int rc = check_ptrs({w.workspace});
+    if (rc != FA_OK) return rc;
+    return w.workspace_bytes < 2 * floats * sizeof(float) ? FA_ERR_WORKSPACE : FA_OK;
+}
+
+int window_dkdv(const WinBackward &w, const WinArgs &win, const DeviceState &st, bool behind, cudaStream_t s) {
+    const int B = w.B, Hq = w.Hq, Hkv = w.Hkv, Nq = w.Nq, Nk = w.Nk, D = w.D;
+    BwdArgs a{w.q, w.k, w.v, nullptr, w.dO, w.lse, w.delta, nullptr, w.dk, w.dv, B, Hq, Nq, D, w.scale, w.scale * log2e(), 1,
+              w.grad_dtype == FA_BF16 ? 1 : 0, st.status_word, B * Hkv, win};
+    const size_t part_floats = sink_part_floats(win, B, D);
+    float *part_dk = static_cast<float *>(w.workspace), *part_dv = part_dk + part_floats;
+    CUtensorMap tq, tk, tv, tdo, tdk, tdv, parts[2];
+    const int q_box = kernel_head_dim(D) == 64 ? 128 : kDkdvQRows;
+    const bool f32 = w.grad_dtype == FA_F32;
+    if (encode_rows(&tq, w.q, B * Hq, Nq, Nq, D, q_box) != FA_OK || encode_rows(&tk, w.k, B * Hkv, Nk, Nk, D, 128) != FA_OK ||
+        encode_rows(&tv, w.v, B * Hkv, Nk, Nk, D, 128) != FA_OK ||
+        encode_rows(&tdo, w.dO, B * Hq, Nq, Nq, D, q_box) != FA_OK ||
+        encode_3d(&tdk, w.dk, B * Hkv, Nk, D, 128, f32) != FA_OK || encode_3d(&tdv, w.dv, B * Hkv, Nk, D, 128, f32) != FA_OK)
+        return FA_ERR_CUDA;
+    parts[0] = tdk, parts[1] = tdv;
+    if (part_floats > 0) {
+        const int n = B * Hkv * win.sink_tiles * (1 + win.chunks);
+        if (encode_3d(&parts[0], part_dk, n, 128, D, 128, true) != FA_OK ||
+            encode_3d(&parts[1], part_dv, n, 128, D, 128, true) != FA_OK)
+            return FA_ERR_CUDA;
+    }
+    cudaError_t e = launch_win_dkdv(a, tq, tk, tv, tdo, tdk, tdv, parts, st.num_sms, behind, s);
+    if (e == cudaSuccess && part_floats > 0) e = launch_sink_sum(a, part_dk, part_dv, s);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+}  // namespace
+
 extern "C" int fa_window_backward_dq(const void *q, const void *k, const void *v, const void *o, const void *dO,
                                      const float *lse, float *delta, void *dq, int B, int Hq, int Hkv, int Nq, int Nk,
                                      int D, int window, int sinks, float scale, int dtype, int grad_dtype,
                                      void *stream) {
-    if (dtype != FA_BF16 || (grad_dtype != FA_BF16 && grad_dtype != FA_F32)) return FA_ERR_DTYPE;
-    int rc = check_window(B, Hq, Hkv, Nq, Nk, Nk, D, window, sinks, scale);
+    const WinBackward w{q, k, v, o, dO, lse, delta, dq, nullptr, nullptr, B, Hq, Hkv, Nq, Nk, D, window, sinks, scale,
+                        grad_dtype, nullptr, 0};
+    int rc = check_window_backward(w, dtype);
     if (rc != FA_OK) return rc;
     rc = check_ptrs({q, k, v, o, dO, lse, delta, dq});
     if (rc != FA_OK) return rc;
@@ -515,18 +583,7 @@ extern "C" int fa_window_backward_dq(const void *q, const void *k, const void *v
     DeviceState *st;
     rc = device_state(&dev, &st);
     if (rc != FA_OK) return rc;
-    BwdArgs a{q, k, v, o, dO, lse, delta, dq, nullptr, nullptr, B, Hq, Nq, D, scale, scale * log2e(), 1,
-              grad_dtype == FA_BF16 ? 1 : 0, st->status_word, B * Hq, window_args(Hkv, Nk, window, sinks)};
-    CUtensorMap tq, tk, tv, tdo, to, tdq;
-    if (encode_rows(&tq, q, B * Hq, Nq, Nq, D, 128) != FA_OK ||
-        encode_rows(&tk, k, B * Hkv, Nk, Nk, D, kDqKRows) != FA_OK ||
-        encode_rows(&tv, v, B * Hkv, Nk, Nk, D, kDqKRows) != FA_OK ||
-        encode_rows(&tdo, dO, B * Hq, Nq, Nq, D, 128) != FA_OK || encode_rows(&to, o, B * Hq, Nq, Nq, D, 128) != FA_OK ||
-        encode_3d(&tdq, dq, B * Hq, Nq, D, 128, grad_dtype == FA_F32) != FA_OK)
-        return FA_ERR_CUDA;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_win_dq(a, tq, tk, tv, tdo, to, tdq, st->num_sms, s);
-    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    return window_dq(w, *st, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int fa_window_backward_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int D, int window, int sinks,
@@ -543,8 +600,9 @@ extern "C" int fa_window_backward_dkdv(const void *q, const void *k, const void 
                                        const float *delta, void *dk, void *dv, int B, int Hq, int Hkv, int Nq, int Nk,
                                        int D, int window, int sinks, float scale, int dtype, int grad_dtype,
                                        void *workspace, size_t workspace_bytes, void *stream) {
-    if (dtype != FA_BF16 || (grad_dtype != FA_BF16 && grad_dtype != FA_F32)) return FA_ERR_DTYPE;
-    int rc = check_window(B, Hq, Hkv, Nq, Nk, Nk, D, window, sinks, scale);
+    const WinBackward w{q, k, v, nullptr, dO, lse, const_cast<float *>(delta), nullptr, dk, dv, B, Hq, Hkv, Nq, Nk, D, window,
+                        sinks, scale, grad_dtype, workspace, workspace_bytes};
+    int rc = check_window_backward(w, dtype);
     if (rc != FA_OK) return rc;
     rc = check_ptrs({q, k, v, dO, lse, delta, dk, dv});
     if (rc != FA_OK) return rc;
@@ -552,35 +610,32 @@ extern "C" int fa_window_backward_dkdv(const void *q, const void *k, const void 
     DeviceState *st;
     rc = device_state(&dev, &st);
     if (rc != FA_OK) return rc;
-    BwdArgs a{q, k, v, nullptr, dO, lse, const_cast<float *>(delta), nullptr, dk, dv, B, Hq, Nq, D, scale,
-              scale * log2e(), 1, grad_dtype == FA_BF16 ? 1 : 0, st->status_word, B * Hkv,
-              window_args_dkdv(B, Hq, Hkv, Nq, Nk, D, window, sinks, st->num_sms)};
-    const size_t part_floats = sink_part_floats(a.win, B, D);
-    if (part_floats > 0) {
-        rc = check_ptrs({workspace});
-        if (rc != FA_OK) return rc;
-        if (workspace_bytes < 2 * part_floats * sizeof(float)) return FA_ERR_WORKSPACE;
-    }
-    float *part_dk = static_cast<float *>(workspace), *part_dv = part_dk + part_floats;
-    CUtensorMap tq, tk, tv, tdo, tdk, tdv, parts[2];
-    const int Dk = kernel_head_dim(D);
-    const int q_box = Dk == 64 ? 128 : kDkdvQRows;
-    if (encode_rows(&tq, q, B * Hq, Nq, Nq, D, q_box) != FA_OK || encode_rows(&tk, k, B * Hkv, Nk, Nk, D, 128) != FA_OK ||
-        encode_rows(&tv, v, B * Hkv, Nk, Nk, D, 128) != FA_OK || encode_rows(&tdo, dO, B * Hq, Nq, Nq, D, q_box) != FA_OK ||
-        encode_3d(&tdk, dk, B * Hkv, Nk, D, 128, grad_dtype == FA_F32) != FA_OK ||
-        encode_3d(&tdv, dv, B * Hkv, Nk, D, 128, grad_dtype == FA_F32) != FA_OK)
-        return FA_ERR_CUDA;
-    parts[0] = tdk, parts[1] = tdv;
-    if (part_floats > 0) {
-        const int n = B * Hkv * a.win.sink_tiles * (1 + a.win.chunks);
-        if (encode_3d(&parts[0], part_dk, n, 128, D, 128, true) != FA_OK ||
-            encode_3d(&parts[1], part_dv, n, 128, D, 128, true) != FA_OK)
-            return FA_ERR_CUDA;
-    }
+    const WinArgs win = window_args_dkdv(B, Hq, Hkv, Nq, Nk, D, window, sinks, st->num_sms);
+    rc = check_window_workspace(w, win);
+    if (rc != FA_OK) return rc;
+    return window_dkdv(w, win, *st, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int fa_window_backward(const void *q, const void *k, const void *v, const void *o, const void *dO,
+                                  const float *lse, float *delta, void *dq, void *dk, void *dv, int B, int Hq, int Hkv,
+                                  int Nq, int Nk, int D, int window, int sinks, float scale, int dtype, int grad_dtype,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+    const WinBackward w{q, k, v, o, dO, lse, delta, dq, dk, dv, B, Hq, Hkv, Nq, Nk, D, window, sinks, scale, grad_dtype,
+                        workspace, workspace_bytes};
+    int rc = check_window_backward(w, dtype);
+    if (rc != FA_OK) return rc;
+    rc = check_ptrs({q, k, v, o, dO, lse, delta, dq, dk, dv});
+    if (rc != FA_OK) return rc;
+    int dev;
+    DeviceState *st;
+    rc = device_state(&dev, &st);
+    if (rc != FA_OK) return rc;
+    const WinArgs win = window_args_dkdv(B, Hq, Hkv, Nq, Nk, D, window, sinks, st->num_sms);
+    rc = check_window_workspace(w, win);
+    if (rc != FA_OK) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_win_dkdv(a, tq, tk, tv, tdo, tdk, tdv, parts, st->num_sms, s);
-    if (e == cudaSuccess && part_floats > 0) e = launch_sink_sum(a, part_dk, part_dv, s);
-    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    rc = window_dq(w, *st, s);
+    return rc != FA_OK ? rc : window_dkdv(w, win, *st, true, s);
 }
 
 namespace {

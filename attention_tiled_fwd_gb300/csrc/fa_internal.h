@@ -260,9 +260,10 @@ cudaError_t launch_bwd_dkdv(const BwdArgs &a, const CUtensorMap &tq, const CUten
 cudaError_t launch_win_dq(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                           const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, int num_sms,
                           cudaStream_t s);
+// behind: launched as the programmatic dependent of the dQ kernel before it on the stream (D <= 128)
 cudaError_t launch_win_dkdv(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                             const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv,
-                            const CUtensorMap *parts, int num_sms, cudaStream_t s);
+                            const CUtensorMap *parts, int num_sms, bool behind, cudaStream_t s);
 cudaError_t launch_sink_sum(const BwdArgs &a, const float *part_dk, const float *part_dv, cudaStream_t s);
 cudaError_t launch_selftest_timeout(int *status, int limit_us, cudaStream_t s);
 

@@ -28,6 +28,7 @@
 // replaced and their V rows cleared before the products.
 #include "fa_internal.h"
 #include "sm100_ptx.cuh"
+#include "launch.cuh"
 #include "win_decode.cuh"
 #include <cmath>
 
@@ -422,27 +423,11 @@ __global__ void __launch_bounds__(128) win_join_kernel(WinDecodeArgs a, PrefixPa
     if (c == 0) a.lse[row] = (Mx + __log2f(l)) * 0.69314718055994531f;
 }
 
-// A launch, or (behind) one as the programmatic dependent of the launch before it on the stream.
-template <class... Params, class... Args>
-cudaError_t launch_behind(void (*kern)(Params...), dim3 grid, int threads, size_t smem, bool behind, cudaStream_t s,
-                          Args... args) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = behind ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, Params(args)...);
-}
-
 template <int D>
 cudaError_t launch_decode_d(const WinDecodeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s) {
     auto kern = win_decode_kernel<D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DecSmem<D>::kAlloc);
+    static std::atomic<unsigned long long> allowed{0};
+    cudaError_t e = allow_smem((const void *)kern, DecSmem<D>::kAlloc, allowed);
     if (e != cudaSuccess) return e;
     const int row_tiles = (a.R + kRowTile - 1) / kRowTile;
     return launch_behind(kern, dim3(row_tiles * a.splits, a.Hkv, a.B), kThreads, DecSmem<D>::kAlloc, a.behind, s, tk, tv, a);

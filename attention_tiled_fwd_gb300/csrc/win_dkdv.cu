@@ -20,6 +20,7 @@
 // An item is a key tile, or a chunk of the rows behind a sink tile's window
 // (win_key_item), whose fp32 partial sink_sum_kernel adds up.
 #include "fa_internal.h"
+#include "launch.cuh"
 #include "sm100_ptx.cuh"
 #include "win.cuh"
 #include <cmath>
@@ -151,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < NSLOT; ++s) last_round[s] = -1;
         bool ok = true;
         int n = 0, t = 0;  // items, query tiles so far
+        bool behind = true;
         for (int k = 0; ok && k * (int)gridDim.x < n_items; ++k) {
             const int x = persistent_work_index(k, n_items);
             if (x < 0) continue;
@@ -189,6 +191,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the tile's L_i and D_i: lane l copies words l, l + 32, ... of [L_i | D_i] (zeros past the last row)
                 const int ss = t % C::kStats;
                 if (!(ok = warp_wait(&stat_empty[ss], (t / C::kStats & 1) ^ 1, a.status, kSiteStats))) break;
+                // D comes from the dQ kernel, which may still run when this one was launched behind it
+                if (behind) launch_dependent_wait();
+                behind = false;
                 float *dst = stat_s + ss * 2 * kBQ;
 #pragma unroll
                 for (int e = 0; e < 2 * kBQ / 32; ++e) {
@@ -536,6 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Adds the partials of one sink tile (its own rows', then the chunks', in that order) into dK and dV; four columns a
 // thread.  partials of a tile: [part][128][D].
 __global__ void sink_sum_kernel(BwdArgs a, const float *part_dk, const float *part_dv) {
+    launch_dependent_wait();
     const int cols = a.D / 4, parts = 1 + a.win.chunks;
     const int tile = blockIdx.y;  // (key slice, sink tile)
     const int bh = tile / a.win.sink_tiles, k0 = tile % a.win.sink_tiles * kBN;
@@ -565,32 +571,31 @@ __global__ void sink_sum_kernel(BwdArgs a, const float *part_dk, const float *pa
 template <int D>
 cudaError_t launch_items(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                          const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv, const CUtensorMap *parts,
-                         int num_sms, cudaStream_t s) {
+                         int num_sms, bool behind, cudaStream_t s) {
     using C = Dkdv<D>;
     auto kern = win_dkdv_kernel<D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAlloc);
+    static std::atomic<unsigned long long> allowed{0};
+    cudaError_t e = allow_smem((const void *)kern, C::kAlloc, allowed);
     if (e != cudaSuccess) return e;
     const int n_items = ((a.win.Nk + kBN - 1) / kBN + a.win.sink_tiles * a.win.chunks) * a.win.Hkv * a.B;
     const int sms = num_sms > 0 ? num_sms : kNumSms;
-    kern<<<n_items < sms ? n_items : sms, kThreads, C::kAlloc, s>>>(tq, tk, tv, tdo, tdk, tdv, parts[0], parts[1], a,
-                                                                    n_items);
-    return cudaGetLastError();
+    return launch_behind(kern, dim3(n_items < sms ? n_items : sms), kThreads, C::kAlloc, behind, s, tq, tk, tv, tdo, tdk,
+                         tdv, parts[0], parts[1], a, n_items);
 }
 
 }  // namespace
 
 cudaError_t launch_sink_sum(const BwdArgs &a, const float *part_dk, const float *part_dv, cudaStream_t s) {
     const dim3 grid((kBN * a.D / 4 + 255) / 256, a.B * a.win.Hkv * a.win.sink_tiles);
-    sink_sum_kernel<<<grid, 256, 0, s>>>(a, part_dk, part_dv);
-    return cudaGetLastError();
+    return launch_behind(sink_sum_kernel, grid, 256, 0, true, s, a, part_dk, part_dv);
 }
 
 cudaError_t launch_win_dkdv(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                             const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv,
-                            const CUtensorMap *parts, int num_sms, cudaStream_t s) {
+                            const CUtensorMap *parts, int num_sms, bool behind, cudaStream_t s) {
     switch (kernel_head_dim(a.D)) {
-        case 64: return launch_items<64>(a, tq, tk, tv, tdo, tdk, tdv, parts, num_sms, s);
-        case 128: return launch_items<128>(a, tq, tk, tv, tdo, tdk, tdv, parts, num_sms, s);
+        case 64: return launch_items<64>(a, tq, tk, tv, tdo, tdk, tdv, parts, num_sms, behind, s);
+        case 128: return launch_items<128>(a, tq, tk, tv, tdo, tdk, tdv, parts, num_sms, behind, s);
         default: return launch_bwd_dkdv(a, tq, tk, tv, tdo, tdk, tdv, s, parts);
     }
 }

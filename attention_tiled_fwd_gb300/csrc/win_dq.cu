@@ -16,6 +16,7 @@
 // the compute warps have seen a tile's last S they copy the next tile's Q into TMEM
 // and only then write dQ, so issuer A is two key tiles ahead when they come back.
 #include "fa_internal.h"
+#include "launch.cuh"
 #include "sm100_ptx.cuh"
 #include "win.cuh"
 #include <cmath>
@@ -130,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    launch_dependents();  // the dK/dV kernel of the same call fills the SMs as they come free
     const uint32_t tmem = *tmem_holder;
 
     // Every role walks the same items: persistent_work_index deals them, n counts this CTA's.
@@ -472,7 +474,8 @@ cudaError_t launch_win_dq(const BwdArgs &a, const CUtensorMap &tq, const CUtenso
                           const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, int num_sms,
                           cudaStream_t s) {
     if (kernel_head_dim(a.D) != kD) return launch_bwd_dq(a, tq, tk, tv, tdo, to, tdq, s, true);
-    cudaError_t e = cudaFuncSetAttribute(win_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, WinDqSmem::kAlloc);
+    static std::atomic<unsigned long long> allowed{0};
+    cudaError_t e = allow_smem((const void *)win_dq_kernel, WinDqSmem::kAlloc, allowed);
     if (e != cudaSuccess) return e;
     const int n_items = (a.N + kBM - 1) / kBM * a.H * a.B;
     const int sms = num_sms > 0 ? num_sms : kNumSms;

@@ -21,6 +21,7 @@
 // A block reads its sink tiles, then its window from the first key that its first
 // row sees (key_span); only tiles that hold a masked pair build masks.
 #include "fa_internal.h"
+#include "launch.cuh"
 #include "sm100_ptx.cuh"
 #include "win.cuh"
 #include <cmath>
@@ -749,7 +750,8 @@ cudaError_t launch_spec(const SpanArgs &a, const CUtensorMap &tq, const CUtensor
     using L = SpanSmem<D, NSLOT, kTiles, kBN>;
     static_assert(L::kAlloc <= 233472 / kCtas - 1024, "shared memory budget (a CTA's own, and 1 KB that the system takes)");
     auto kern = win_fwd_kernel<D, NSLOT, PREFIX, kTiles, kCtas, kBN>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+    static std::atomic<unsigned long long> allowed{0};
+    cudaError_t e = allow_smem((const void *)kern, L::kAlloc, allowed);
     if (e != cudaSuccess) return e;
     const int n_work = span_blocks<kTiles>(a, PREFIX);
     const int ctas = (a.num_sms > 0 ? a.num_sms : kNumSms) * kCtas;

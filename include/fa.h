@@ -263,7 +263,17 @@ FA_API int fa_window_backward_dkdv(const void *q, const void *k, const void *v, 
                                    float scale, int dtype, int grad_dtype,
                                    void *workspace, size_t workspace_bytes, void *stream);
 
-/* Bytes of workspace fa_window_backward_dkdv needs on the current device (may be 0). */
+/*
+ * fa_window_backward -- both of the calls above, in that order, on one stream: the dK/dV kernel starts on the SMs that
+ * the dQ kernel has left.  Arguments, results and errors as theirs; nothing is enqueued when either refuses.
+ */
+FA_API int fa_window_backward(const void *q, const void *k, const void *v, const void *o, const void *dO,
+                              const float *lse, float *delta, void *dq, void *dk, void *dv,
+                              int B, int Hq, int Hkv, int Nq, int Nk, int D, int window, int sinks,
+                              float scale, int dtype, int grad_dtype,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace fa_window_backward and fa_window_backward_dkdv need on the current device (may be 0). */
 FA_API int fa_window_backward_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int D, int window, int sinks,
                                               size_t *bytes);
 

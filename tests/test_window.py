@@ -66,7 +66,7 @@ def _err(name):
 
 
 def _calls(lib, **kw):
-    """(status of the forward, of dQ, of dK/dV) with these arguments; pointers are fakes."""
+    """Status of the forward, dQ, dK/dV and the whole backward with these arguments; pointers are fakes."""
     a = dict(SIZES, ptr=A)
     a.update(kw)
     p = a["ptr"]
@@ -74,7 +74,8 @@ def _calls(lib, **kw):
     m = [a["D"], a["window"], a["sinks"], a["scale"], a["dtype"]]
     return (lib.fa_window_forward(p, A, A, A, A, *s, a["kv_rows"], *m, None),
             lib.fa_window_backward_dq(p, A, A, A, A, A, A, A, *s, *m, a["grad"], None),
-            lib.fa_window_backward_dkdv(p, A, A, A, A, A, A, A, *s, *m, a["grad"], A, 1 << 30, None))
+            lib.fa_window_backward_dkdv(p, A, A, A, A, A, A, A, *s, *m, a["grad"], A, 1 << 30, None),
+            lib.fa_window_backward(p, A, A, A, A, A, A, A, A, A, *s, *m, a["grad"], A, 1 << 30, None))
 
 
 @pytest.mark.parametrize("kw,code", BAD)
@@ -84,7 +85,7 @@ def test_window_refusals(lib, kw, code):
 
 def test_window_refusals_of_one_call(lib):
     assert _calls(lib, kv_rows=15)[0] == nat.FA_ERR_SHAPE
-    assert _calls(lib, grad=7)[1:] == (nat.FA_ERR_DTYPE,) * 2
+    assert _calls(lib, grad=7)[1:] == (nat.FA_ERR_DTYPE,) * 3
     assert set(_calls(lib, ptr=None)) == {nat.FA_ERR_NULL}
     assert set(_calls(lib, ptr=A + 8)) == {nat.FA_ERR_ALIGN}
     out = ctypes.c_size_t(0)
@@ -204,8 +205,11 @@ def test_window_backward(case, grad_dtype):
     first = Nk - Nq - window + 1
     if first > sinks:
         assert not dk[:, :, sinks:first].any() and not dv[:, :, sinks:first].any()
+    # again, and both halves in one call: the same bits
     again = fa.fa_window_backward_dkdv(q, k, v, dO, lse, delta, window, sinks, **kw)
     assert torch.equal(again[0], dk) and torch.equal(again[1], dv)
+    for a, b in zip(fa.fa_window_backward(q, k, v, o, dO, lse, window, sinks, **kw), (dq, dk, dv, delta)):
+        assert torch.equal(a, b)
 
 
 @pytest.mark.gpu

@@ -398,6 +398,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float4 *ds4 = reinterpret_cast<const float4 *>(stat_s + b * 2 * kBQ + kBQ + g * kSpan);
                 const int q0 = w.rows.first + at.h * kBQ + g * kSpan;  // first query of this thread's range
                 const bool any_mask = __any_sync(0xffffffffu, q0 < lo || q0 + kSpan > hi);
+                // None of this warp's keys is seen by any of its queries (along the edges of the band, and in the chunks behind
+                // a sink tile): P^T and dS^T are zeros.  Step of 4096 rows, window 1024, D = 128: 157 -> 146 us; no
+                // difference at D = 64 (500 us at 32768 rows and window 512), which has no registers left for it.
+                const bool none = D == 128 && any_mask && __all_sync(0xffffffffu, q0 >= hi || q0 + kSpan <= lo);
 
                 ok = mbar_wait(&s_full[b], (t >> 1) & 1, a.status, kSiteSFull);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -406,7 +410,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // factors would make dK's error a quarter larger)
                 uint32_t pk[kSpan / 2];
                 uint64_t p2[kSpan / 2];
-                {
+                if (none) {
+#pragma unroll
+                    for (int e = 0; e < kSpan / 2; ++e) pk[e] = 0u;
+                } else {
                     uint32_t raw[kSpan];
                     tmem_ld_n<kSpan>(tmem + lane_base + kBQ * b + g * kSpan, raw);
                     tmem_wait_ld();
@@ -422,16 +429,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   p[2], p[3]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) p[e] = ex2_approx(p[e]);
-                        if (any_mask) {
-                            const uint32_t seen = ~low_bits(lo - q0) & low_bits(hi - q0);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (!(seen & (1u << (4 * q4 + e)))) p[e] = 0.f;
-                        }
                         p2[2 * q4] = f2_pack(p[0], p[1]);
                         p2[2 * q4 + 1] = f2_pack(p[2], p[3]);
                         pk[2 * q4] = pack_bf16x2(p[0], p[1]);
                         pk[2 * q4 + 1] = pack_bf16x2(p[2], p[3]);
+                    }
+                    if (any_mask) {
+                        const uint32_t seen = ~low_bits(lo - q0) & low_bits(hi - q0);
+#pragma unroll
+                        for (int e = 0; e < kSpan / 2; ++e) {
+                            float p0, p1;
+                            f2_unpack(p2[e], p0, p1);
+                            if (!(seen & (1u << (2 * e)))) p0 = 0.f;
+                            if (!(seen & (2u << (2 * e)))) p1 = 0.f;
+                            p2[e] = f2_pack(p0, p1);
+                            pk[e] = pack_bf16x2(p0, p1);
+                        }
                     }
                 }
                 tmem_st_n<kSpan / 2>(tmem + lane_base + kBQ * b + g * kSpan, pk);
@@ -442,7 +455,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = mbar_wait(&dp_full[db], (C::kDpBufs == 1 ? t : t >> 1) & 1, a.status, kSiteDpFull);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 tc_fence_after();
-                {
+                if (none) {
+                    if constexpr (C::kDpBufs == 1) warp_arrive(dp_free);
+                    tmem_st_n<kSpan / 2>(tmem + lane_base + C::kColDS + kBQ * b + g * kSpan, pk);
+                } else {
                     uint32_t raw[kSpan], dsk[kSpan / 2];
                     tmem_ld_n<kSpan>(tmem + lane_base + C::kColDP + kBQ * db + g * kSpan, raw);
                     tmem_wait_ld();

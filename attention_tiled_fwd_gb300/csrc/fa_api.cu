@@ -418,13 +418,6 @@ WinArgs window_args(int Hkv, int Nk, int window, int sinks) {
     return w;
 }
 
-// How the forward's blocks pair their query tiles: one tile each while every tile can have an SM of its own;
-// else two heads of a group (they read the same keys), or neighbouring rows where a group's heads do not pair.
-int window_pairing(int B, int Hq, int Hkv, int Nq, int num_sms) {
-    if ((long long)B * Hq * ((Nq + 127) / 128) <= num_sms) return kOneTile;
-    return (Hq / Hkv) % 2 == 0 ? kTwoHeads : kTwoRowTiles;
-}
-
 // Cuts the rows behind the sink tiles' windows (dK/dV) into chunks.  Without it one CTA per sink tile and key head
 // meets every row: at Nq = 4096, window 1024, groups of 4 heads it took 256 of the others' 72 steps and the launch
 // waited for it.
@@ -438,9 +431,12 @@ WinArgs window_args_dkdv(int B, int Hq, int Hkv, int Nq, int Nk, int D, int wind
     const long long rest = G * ((Nq - end + bq - 1) / bq);
     const long long sink_tiles = (w.sinks + bk - 1) / bk;
     const long long all = (long long)B * Hkv * ((Nk + bk - 1) / bk * own + sink_tiles * rest);
+    // four sink tiles an SM balance each other uncut, and their partials would be as large as the gradients
+    const long long items = (long long)B * Hkv * sink_tiles;
+    if (items >= 4 * num_sms) return w;
     // a chunk is as long as another item, or up to four of them when that is a quarter of an SM's share of the
-    // launch or less, and 16 steps at least
-    const long long per = std::max({own, std::min(all / (4 * num_sms), 4 * own), 16ll});
+    // launch or less; 16 steps at least; and the launch has four chunks an SM at most beside one a sink tile
+    const long long per = std::max({own, std::min(all / (4 * num_sms), 4 * own), 16ll, rest * items / (4 * num_sms)});
     if (rest <= per / 2) return w;
     w.sink_tiles = (int)sink_tiles;
     w.chunks = (int)((rest + per - 1) / per);
@@ -485,9 +481,7 @@ extern "C" int fa_window_forward(const void *q, const void *k, const void *v, vo
     a.scale_log2 = scale * log2e();
     a.status = st->status_word;
     a.num_sms = st->num_sms;
-    a.pairing = win_fwd_tiles(D) == 1 ? kOneTile : window_pairing(B, Hq, Hkv, Nq, st->num_sms);
-    const int heads = a.pairing == kTwoHeads ? Hq / 2 : Hq;
-    a.per_rows = FastDiv(B * heads), a.per_seq = FastDiv(heads), a.group = FastDiv(Hq / Hkv);
+    a.per_rows = FastDiv(B * Hq), a.per_seq = FastDiv(Hq), a.group = FastDiv(Hq / Hkv);
     // sink tiles read through maps that end at the last sink
     const int bn = win_fwd_keys(D), sink_rows = w.sinks > 0 ? w.sinks : Nk;
     CUtensorMap tq, tk, tv, tks, tvs, to;

@@ -50,11 +50,6 @@ __host__ __device__ inline bool all_seen(int p0, int p1, int k0, int k1, int win
     return k1 <= p0 && (k0 > p1 - window || k1 < sinks);
 }
 
-// none of positions p0 .. p1 sees any of keys k0 .. k1
-__host__ __device__ inline bool none_seen(int p0, int p1, int k0, int k1, int window, int sinks) {
-    return k0 > p1 || (k1 <= p0 - window && k0 >= sinks);
-}
-
 // bit i: the position p0 + i sees key (i < 32)
 __host__ __device__ inline uint32_t seeing_positions(int key, int p0, int window, int sinks) {
     return ~low_bits(key - p0) & (key < sinks ? ~0u : low_bits(key + window - p0));
@@ -121,19 +116,14 @@ struct SpanArgs {
     float scale_log2;
     int *status;
     int num_sms;
-    // windowed: how a block's two query tiles are chosen (kOneTile, kTwoHeads, kTwoRowTiles); blocks of a row range
-    // (B x heads or head pairs), heads or head pairs of a sequence, query heads of a key head
-    int pairing;
+    // windowed: query heads of all sequences, of one, of a key head
     FastDiv per_rows, per_seq, group;
     // shared prefix (parts.o set): chunks of chunk_tiles key tiles
     PrefixParts parts;
     int chunk_tiles;
 };
-// Query tiles of a CTA of the windowed forward at head dimension D (one: two CTAs share an SM).
-inline int win_fwd_tiles(int D) { return 1; }
-// Keys of its K/V tiles.
+// Keys of the K/V tiles of the windowed forward at head dimension D.
 inline int win_fwd_keys(int D) { return D <= 64 ? 128 : 64; }
-enum : int { kOneTile = 0, kTwoHeads = 1, kTwoRowTiles = 2 };
 
 cudaError_t launch_win_fwd(const SpanArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                            const CUtensorMap &tks, const CUtensorMap &tvs, const CUtensorMap &to, cudaStream_t s);

@@ -7,19 +7,17 @@
 // visible keys j <= p with j < sinks or j > p - window, m the running maximum
 // (base 2, c = scale log2 e), l the running sum, L = (m + log2 l) ln 2.
 //
-// The block of a CTA is two 128-row query tiles past one stream of 128-key K/V
-// tiles, as in fwd_bf16_pair.cu (one softmax warpgroup per tile, one tcgen05
-// issuer, P over S in TMEM, persistent grid).  What a block's tiles are:
-//   two heads   the same rows of two query heads that share a key head: the two
-//               tiles read exactly the same keys;
-//   two rows    (one query head per key head) neighbouring row tiles: the stream
-//               is the union of their windows and each skips what it does not see;
-//   one tile    launches with no more tiles than SMs: every tile gets its own SM;
-//   prefix      128-row tiles packed from the rows of many sequences (the group's
-//               heads and the new rows of one sequence are adjacent in memory, so
-//               one 4-D TMA box gathers them), against one chunk of the prefix.
-// A block reads its sink tiles, then its window from the first key that its first
-// row sees (key_span); only tiles that hold a masked pair build masks.
+// One tcgen05 issuer, one softmax warpgroup per 128-row query tile (a thread per row, its TMEM lane), a persistent grid
+// past a TMA ring of K/V tiles.  Two forms:
+//   window      one query tile a CTA and two CTAs an SM: while one waits at the end of a block or for a product, the
+//               other's softmax has the SM.  S(j + 1) is issued before PV(j), P has columns of its own, the producer
+//               works the blocks out ahead.  A block reads its sink tiles, then its window from the first key that its
+//               first row sees (key_span); only tiles that hold a masked pair build masks.  (Two tiles past one stream of
+//               keys, as the prefix form has them: 1197 us instead of 1032 for a 32K prompt at D = 64.)  Bound by the
+//               softmax: ~1300 cycles of exponentials and conversions for a 128 x 128 tile.
+//   prefix      128-row tiles packed from the rows of many sequences (the group's heads and the new rows of one
+//               sequence are adjacent in memory, so one 4-D TMA box gathers them), two of them past one stream of
+//               128-key tiles (one chunk of the prefix), P over S in TMEM; partials instead of O.
 #include "fa_internal.h"
 #include "launch.cuh"
 #include "sm100_ptx.cuh"
@@ -59,66 +57,44 @@ struct SpanSmem {
     static constexpr int kAlloc = kBlockOff + kBlocks * kTiles * 32;  // from a 1024-byte boundary
 };
 
-// The work of one block of this CTA: the key tiles it streams, and which of them each of its two query
-// tiles reads.  Every role of the CTA walks the same sequence of blocks and computes these alike.
+// The work of one block of this CTA: its query tiles and the key tiles that they read.  The producer and the issuer
+// walk the same sequence of blocks and compute these alike.
 template <int kTiles>
 struct SpanBlock {
-    KeySpan span;             // the key tiles
-    int kv_bh, y_off;         // their K/V slice, and the row that key 0 of the span sits at
-    int from[kTiles], to[kTiles];  // query tile x reads key tiles [0, n_sink) and [from, to)
-    int n[kTiles];            // how many that is (0: no such query tile)
-    int zq[kTiles], yq[kTiles];  // windowed: the tile's head slice and first row; prefix: key head, packed tile
-    int p0[kTiles];           // windowed: position of the tile's first row
+    KeySpan span;                // the key tiles
+    int kv_bh, y_off;            // their K/V slice, and the row that key 0 of the span sits at
+    int n[kTiles];               // key tiles that query tile x reads: span.n, or 0 where there is no such query tile
+    int zq[kTiles], yq[kTiles];  // windowed: the tile's head slice and first row; prefix: chunk, packed tile
+    int p0[kTiles];              // windowed: position of the tile's first row
 
-    __device__ __forceinline__ bool reads(int x, int j) const {
-        return n[x] > 0 && j < span.n && (j < span.n_sink || (j >= from[x] && j < to[x]));
-    }
-    // which of query tile x's steps key tile j is
-    __device__ __forceinline__ int step_of(int x, int j) const { return j < span.n_sink ? j : span.n_sink + j - from[x]; }
+    __device__ __forceinline__ bool reads(int x, int j) const { return j < n[x]; }
 };
 
 // Windowed blocks in longest-first order: the last rows of every head first.
-template <int kTiles, int kBN>
-__device__ __forceinline__ SpanBlock<kTiles> window_block(const SpanArgs &a, int L) {
-    SpanBlock<kTiles> w;
-    const int per_block = kTiles == 2 && a.pairing == kTwoRowTiles ? 2 * kBM : kBM;
-    const bool two_heads = kTiles == 2 && a.pairing == kTwoHeads;
-    const int n_blk = (a.Nq + per_block - 1) / per_block;
+template <int kBN>
+__device__ __forceinline__ SpanBlock<1> window_block(const SpanArgs &a, int L) {
+    SpanBlock<1> w;
     const int rank = a.per_rows.div(L), bh = L - rank * (int)a.per_rows.d;
-    const int row0 = (n_blk - 1 - rank) * per_block;
-    const int b = a.per_seq.div(bh), h = (bh - b * (int)a.per_seq.d) * (two_heads ? 2 : 1);
+    const int row0 = ((a.Nq + kBM - 1) / kBM - 1 - rank) * kBM;
+    const int b = a.per_seq.div(bh), h = bh - b * (int)a.per_seq.d;
     const int off = a.Nk - a.Nq;
     w.kv_bh = b * a.Hkv + a.group.div(h);
     w.y_off = 0;
-#pragma unroll
-    for (int x = 0; x < kTiles; ++x) {
-        w.zq[x] = b * a.Hq + h + (two_heads ? x : 0);
-        w.yq[x] = row0 + (two_heads ? 0 : x * kBM);
-        w.p0[x] = off + w.yq[x];
-    }
-    const bool two = two_heads || (kTiles == 2 && a.pairing == kTwoRowTiles && w.yq[kTiles - 1] < a.Nq);
-    const int last = two ? w.yq[kTiles - 1] : w.yq[0];
-    w.span = key_span(w.p0[0], off + min(a.Nq, last + kBM) - 1, a.window, a.sinks, kBN);
-#pragma unroll
-    for (int x = 0; x < kTiles; ++x) {
-        // the window tiles of this query tile alone: from the first key its first row sees (from key 0 on
-        // when the span is one range that holds the sinks) to its last row's own key
-        const int lo = w.p0[x] - a.window + 1;
-        w.from[x] = w.span.n_sink + (w.span.lo == 0 && a.sinks > 0 ? 0 : max(0, lo - w.span.lo) / kBN);
-        const int end = off + min(a.Nq, w.yq[x] + kBM);
-        w.to[x] = w.span.n_sink + (end - w.span.lo + kBN - 1) / kBN;
-        w.n[x] = (x == 0 || two) ? w.span.n_sink + w.to[x] - w.from[x] : 0;
-    }
+    w.zq[0] = bh;
+    w.yq[0] = row0;
+    w.p0[0] = off + row0;
+    w.span = key_span(off + row0, off + min(a.Nq, row0 + kBM) - 1, a.window, a.sinks, kBN);
+    w.n[0] = w.span.n;
     return w;
 }
 
-// Shared-prefix blocks: two packed query tiles of a key head against one chunk of the prefix.
+// Shared-prefix blocks: packed query tiles of a key head against one chunk of the prefix.
 template <int kTiles, int kBN>
 __device__ __forceinline__ SpanBlock<kTiles> prefix_block(const SpanArgs &a, int L) {
     SpanBlock<kTiles> w;
-    const int pairs = (a.parts.m_tiles + kTiles - 1) / kTiles;
-    const int m = (L % pairs) * kTiles;
-    const int rest = L / pairs;
+    const int groups = (a.parts.m_tiles + kTiles - 1) / kTiles;
+    const int m = (L % groups) * kTiles;
+    const int rest = L / groups;
     const int chunk = rest % a.parts.splits;
     w.kv_bh = rest / a.parts.splits;
     w.y_off = chunk * a.chunk_tiles * kBN;
@@ -130,8 +106,6 @@ __device__ __forceinline__ SpanBlock<kTiles> prefix_block(const SpanArgs &a, int
         w.zq[x] = chunk;
         w.yq[x] = m + x;
         w.p0[x] = 0;
-        w.from[x] = 0;
-        w.to[x] = w.span.n;
         w.n[x] = m + x < a.parts.m_tiles ? w.span.n : 0;
     }
     return w;
@@ -140,7 +114,7 @@ __device__ __forceinline__ SpanBlock<kTiles> prefix_block(const SpanArgs &a, int
 template <bool PREFIX, int kTiles, int kBN>
 __device__ __forceinline__ SpanBlock<kTiles> span_block(const SpanArgs &a, int L) {
     if constexpr (PREFIX) return prefix_block<kTiles, kBN>(a, L);
-    return window_block<kTiles, kBN>(a, L);
+    else return window_block<kBN>(a, L);
 }
 
 // Columns of key tile j that are computed: all of them, or 32 of a sink tile whose sinks fit there.
@@ -169,8 +143,7 @@ __device__ __forceinline__ void packed_tile(const SpanArgs &a, int t, int *b0, i
 template <int kTiles>
 __host__ __device__ inline int span_blocks(const SpanArgs &a, bool prefix) {
     if (prefix) return (a.parts.m_tiles + kTiles - 1) / kTiles * a.parts.splits * a.Hkv;
-    const int per_block = kTiles == 2 && a.pairing == kTwoRowTiles ? 2 * kBM : kBM;
-    return (a.Nq + per_block - 1) / per_block * (int)a.per_rows.d;
+    return (a.Nq + kBM - 1) / kBM * (int)a.per_rows.d;
 }
 
 // Persistent: the grid has at most kCtas CTAs per SM, each walking its blocks in turn, so the next block's
@@ -286,8 +259,7 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
                 SoftBlock sb[kTiles];
 #pragma unroll
                 for (int x = 0; x < kTiles; ++x)
-                    sb[x] = SoftBlock{w.n[x], w.span.n_sink, w.y_off + w.span.lo + (w.from[x] - w.span.n_sink) * kBN,
-                                      uses + (x == 1 && w.n[0] > 0), w.zq[x], w.yq[x], w.p0[x], w.kv_bh};
+                    sb[x] = SoftBlock{w.n[x], w.span.n_sink, w.y_off + w.span.lo, uses + (x == 1 && w.n[0] > 0), w.zq[x], w.yq[x], w.p0[x], w.kv_bh};
 #pragma unroll
                 for (int x = 0; x < kTiles; ++x) uses += w.n[x] > 0;
                 if (!(ok = publish(sb))) break;
@@ -364,7 +336,8 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
         // ------------------------------------------------------------ the tcgen05 issuer
         // The whole warp runs the loop (operands stay warp-uniform); one elected lane issues the MMAs
         // and the commits that track them.  Per block the order is
-        //   S_A(0) S_B(0) | PV_A(j) S_A(j+1) PV_B(j) S_B(j+1) | ...
+        //   one tile   S(0) | S(j+1) PV(j) | ...
+        //   two tiles  S_A(0) S_B(0) | PV_A(j) S_A(j+1) PV_B(j) S_B(j+1) | ...
         constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, kBN, false, false), idesc_sink = idesc_bf16_f32(kBM, 32, false, false);
         constexpr uint32_t idesc_o = idesc_bf16_f32(kBM, D, false, true);
         const uint32_t slot_addr = smem_u32(slots);
@@ -389,7 +362,7 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
                 const int slot = g % NSLOT;
                 if (!(ok = warp_wait(&slot_full[slot], (g / NSLOT) & 1, a.status, kSiteSlotFull))) return;
                 // S_X overwrites P_X of the step before (this block's or the previous one's); kOwnP: S itself, loaded by now
-                const int st = step0[x] + w.step_of(x, j);
+                const int st = step0[x] + j;
                 if (st >= 1 && !(ok = warp_wait(kOwnP ? s_free : &pv_done[x], (st - 1) & 1, a.status,
                                                 kOwnP ? kSiteSFree : kSitePV)))
                     return;
@@ -413,9 +386,9 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
                 const int g = gidx + 2 * j + 1;
                 const int slot = g % NSLOT;
                 if (!(ok = warp_wait(&slot_full[slot], (g / NSLOT) & 1, a.status, kSiteSlotFull))) return;
-                if (!(ok = warp_wait(&p_full[x], (step0[x] + w.step_of(x, j)) & 1, a.status, kSitePFull))) return;
+                if (!(ok = warp_wait(&p_full[x], (step0[x] + j) & 1, a.status, kSitePFull))) return;
                 // the first PV of a block overwrites O_X, which the previous block's epilogue reads
-                const bool first = w.step_of(x, j) == 0;
+                const bool first = j == 0;
                 if (first && blocks[x] >= 1 && !(ok = warp_wait(&o_free[x], (blocks[x] - 1) & 1, a.status, kSiteOFree)))
                     return;
                 tc_fence_after();

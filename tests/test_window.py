@@ -94,6 +94,15 @@ def test_window_refusals_of_one_call(lib):
     assert lib.fa_window_backward_workspace_bytes(1, 4, 2, 8, 16, 64, 4, 1, ctypes.byref(out)) == nat.FA_OK
 
 
+@pytest.mark.parametrize("Hkv,N,sinks", [(8, 8192, 2560), (64, 32768, 4096), (512, 4096, 1), (1, 65536, 60000)])
+def test_backward_workspace_stays_small(lib, Hkv, N, sinks):
+    # partials of the sink tiles: at most four chunks an SM, beside two for each of less than four sink tiles an SM
+    out = ctypes.c_size_t(0)
+    for D in (64, 128, 256):
+        assert lib.fa_window_backward_workspace_bytes(1, 4 * Hkv, Hkv, N, N, D, 256, sinks, ctypes.byref(out)) == nat.FA_OK
+        assert out.value <= 12 * 160 * 2 * 4 * 128 * D
+
+
 def _token(lib, **kw):
     a = dict(q=A, lens=A, B=2, Hq=4, Hkv=2, n_q=1, N=64, D=128, window=8, sinks=1, scale=0.1)
     a.update(kw)

@@ -426,33 +426,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int v8 = 0; v8 < 4; ++v8)
                         st_global_v8(dst + (g * HD / 8 + ch * 4 + v8) * (kBM * 8), ov + 8 * v8);
                 }
-                if (g == 0) a.parts.ml[part * kBM + r] = make_float2(m, l_row);
+                // every score a NaN: m stays -inf, which would read as "sees nothing"
+                if (g == 0) a.parts.ml[part * kBM + r] = make_float2(l_row != l_row ? fmaxf(m, 0.f) : m, l_row);
             } else {
-            const float inv_l = 1.f / l_row;
-            // row stride and stored columns: the caller's D (at most this kernel's D; the columns past it
-            // hold zeros from the TMA's out-of-bounds fill)
-            const int Dr = a.D;
-            __nv_bfloat16 *orow = static_cast<__nv_bfloat16 *>(a.o) + ((size_t)bh * N + row) * Dr + g * HD;
-            uint32_t ov[32];
+                const float inv_l = 1.f / l_row;
+                // row stride and stored columns: the caller's D (at most this kernel's D; the columns past it
+                // hold zeros from the TMA's out-of-bounds fill)
+                const int Dr = a.D;
+                __nv_bfloat16 *orow = static_cast<__nv_bfloat16 *>(a.o) + ((size_t)bh * N + row) * Dr + g * HD;
+                uint32_t ov[32];
 #pragma unroll
-            for (int ch = 0; ch < HD / 32; ++ch) {
-                tmem_ld32(tmem + lane_base + kColO + g * HD + ch * 32, ov);
-                tmem_wait_ld();
-                if (row < N) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(orow + ch * 32);
+                for (int ch = 0; ch < HD / 32; ++ch) {
+                    tmem_ld32(tmem + lane_base + kColO + g * HD + ch * 32, ov);
+                    tmem_wait_ld();
+                    if (row < N) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(orow + ch * 32);
 #pragma unroll
-                    for (int v4 = 0; v4 < 4; ++v4) {
-                        if (g * HD + ch * 32 + v4 * 8 >= Dr) break;
-                        uint4 w;
-                        w.x = pack_bf16x2(__uint_as_float(ov[v4 * 8 + 0]) * inv_l, __uint_as_float(ov[v4 * 8 + 1]) * inv_l);
-                        w.y = pack_bf16x2(__uint_as_float(ov[v4 * 8 + 2]) * inv_l, __uint_as_float(ov[v4 * 8 + 3]) * inv_l);
-                        w.z = pack_bf16x2(__uint_as_float(ov[v4 * 8 + 4]) * inv_l, __uint_as_float(ov[v4 * 8 + 5]) * inv_l);
-                        w.w = pack_bf16x2(__uint_as_float(ov[v4 * 8 + 6]) * inv_l, __uint_as_float(ov[v4 * 8 + 7]) * inv_l);
-                        dst[v4] = w;
+                        for (int v4 = 0; v4 < 4; ++v4) {
+                            if (g * HD + ch * 32 + v4 * 8 >= Dr) break;
+                            uint4 w;
+                            w.x = pack_bf16x2(__uint_as_float(ov[v4 * 8 + 0]) * inv_l, __uint_as_float(ov[v4 * 8 + 1]) * inv_l);
+                            w.y = pack_bf16x2(__uint_as_float(ov[v4 * 8 + 2]) * inv_l, __uint_as_float(ov[v4 * 8 + 3]) * inv_l);
+                            w.z = pack_bf16x2(__uint_as_float(ov[v4 * 8 + 4]) * inv_l, __uint_as_float(ov[v4 * 8 + 5]) * inv_l);
+                            w.w = pack_bf16x2(__uint_as_float(ov[v4 * 8 + 6]) * inv_l, __uint_as_float(ov[v4 * 8 + 7]) * inv_l);
+                            dst[v4] = w;
+                        }
                     }
                 }
-            }
-            if (row < N && g == 0) a.lse[(size_t)bh * N + row] = (m + __log2f(l_row)) * 0.69314718055994531f;
+                if (row < N && g == 0) a.lse[(size_t)bh * N + row] = (m + __log2f(l_row)) * 0.69314718055994531f;
             }
         }
     }

@@ -284,6 +284,7 @@ __global__ void __launch_bounds__(kThreads)
             acc.z = fmaf(v.z, f, acc.z);
             acc.w = fmaf(v.w, f, acc.w);
         }
+        if (ls != ls) M = Mb;  // scores that are NaN leave m at -inf, which would read as "sees nothing"
         const size_t row = (size_t)kv * a.R + rr;
         if (!a.join) {
             const size_t slot = row * a.splits + split;

@@ -546,41 +546,32 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
                     s_loaded();
                     bool unseen = false;  // this row sees none of the tile's keys
                     if (PREFIX ? key0 + kBN > a.Nk
-                               : !all_seen(pos0, pos0 + kBM - 1, key0, key0 + kBN - 1, window, a.sinks)) {
-                        // Column e of the tile is seen iff e in [lo, hi) (or e < left, where the sinks reach into it).
-                        const int hi = PREFIX ? a.Nk - key0 : pos + 1 - key0;
-                        const int lo = PREFIX ? 0 : pos + 1 - window - key0;
-                        const int left = PREFIX ? 0 : a.sinks - key0;
-                        if (left <= 0) {
-                            // raw = min(raw, (hi - 1/2 - e) 2^118, (e + 1/2 - lo) 2^118): one bound is hugely negative
-                            // where the column is not seen, both are hugely positive where it is (all exact).  Two
-                            // packed additions and a three-input minimum a pair, and no predicates: selecting by mask
-                            // bits took 900-1300 cycles more per tile, a third of a plain step.
-                            constexpr float kBig = 0x1p118f;
-                            const float h0 = ((float)max(-1, min(kBN, hi)) - 0.5f) * kBig;
-                            const float l0 = (0.5f - (float)max(-1, min(kBN, lo))) * kBig;
-                            uint64_t th = f2_pack(h0, h0 - kBig), tl = f2_pack(l0, l0 + kBig);
-                            const uint64_t dn = f2_pack(-2.f * kBig, -2.f * kBig), up = f2_pack(2.f * kBig, 2.f * kBig);
+                               : !all_seen(pos0 + 32 * quarter, pos0 + 32 * quarter + 31, key0, key0 + kBN - 1, window, a.sinks)) {
+                        // s = min(s, bound): bound is a NaN where the key is seen (a minimum ignores it, so s stays,
+                        // be it a NaN itself) and -inf where it is not (whatever s is, a NaN too).  A bound is one
+                        // byte permutation that spreads a mask bit's sign; selecting by predicates took 900-1300 cycles
+                        // more per 128 x 128 tile, a third of an unmasked one.
+                        uint32_t any = 0;
 #pragma unroll
-                            for (int i = 0; i < kBN; i += 2) {
-                                float a0, a1, b0, b1;
-                                f2_unpack(th, a0, a1);
-                                f2_unpack(tl, b0, b1);
-                                raw[i] = __float_as_uint(fmin3(__uint_as_float(raw[i]), a0, b0));
-                                raw[i + 1] = __float_as_uint(fmin3(__uint_as_float(raw[i + 1]), a1, b1));
-                                th = f2_add(th, dn);
-                                tl = f2_add(tl, up);
-                            }
-                            unseen = hi <= 0 || lo >= kBN || hi <= lo;
-                        } else {
+                        for (int h = 0; h < kBN / 32; ++h) {
+                            const uint32_t seen = PREFIX ? low_bits(a.Nk - key0 - 32 * h)
+                                                         : seen_keys(pos, key0 + 32 * h, window, a.sinks);
+                            any |= seen;
 #pragma unroll
-                            for (int h = 0; h < kBN / 32; ++h) {
-                                const uint32_t seen = seen_keys(pos, key0 + 32 * h, window, a.sinks);
+                            for (int k = 0; k < 8; ++k) {
+                                const uint32_t w8 = seen << (7 - k);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (!(seen & (1u << e))) raw[32 * h + e] = 0xff800000u;  // -inf
+                                for (int y = 0; y < 4; ++y) {
+                                    uint32_t bound;
+                                    asm("prmt.b32 %0, %1, %2, %3;"
+                                        : "=r"(bound)
+                                        : "r"(w8), "r"(0xff800000u), "r"(0x7600u + (8u + y) * 0x11u));
+                                    uint32_t &s = raw[32 * h + 8 * y + k];
+                                    s = __float_as_uint(fminf(__uint_as_float(s), __uint_as_float(bound)));
+                                }
                             }
                         }
+                        unseen = any == 0;
                     }
                     // row max of the raw scores (scale > 0 commutes with max): four chains of three-input maxima
                     float mx[4];
@@ -593,8 +584,8 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
                             mx[u] = fmax3(mx[u], __uint_as_float(raw[i + 2 * u]), __uint_as_float(raw[i + 2 * u + 1]));
 #pragma unroll
                     for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __uint_as_float(raw[kBN - 4 + u]));
-                    const float mt = c * fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-                    new_max(unseen ? -INFINITY : mt);
+                    const float mt = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                    new_max(unseen ? -INFINITY : c * mt);
                     nm2 = f2_pack(-m_base, -m_base);
                     p_free();
                     if (kOwnP && !ok) break;
@@ -644,7 +635,8 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
 #pragma unroll
                     for (int v8 = 0; v8 < 4; ++v8) st_global_v8(dst + (ch * 4 + v8) * (kBM * 8), ov + 8 * v8);
                 }
-                a.parts.ml[part * kBM + r] = make_float2(m, l);
+                // every score a NaN: m stays -inf, which would read as "sees nothing"
+                a.parts.ml[part * kBM + r] = make_float2(l != l ? fmaxf(m, 0.f) : m, l);
                 continue;
             }
             const float inv_l = 1.f / l;

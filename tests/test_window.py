@@ -151,8 +151,7 @@ def _gen(seed):
     return g
 
 
-# B, Hq, Hkv, Nq, Nk, D, window, sinks.  Beyond 152 tiles the forward pairs query tiles: two heads of a group
-# (even groups) or neighbouring rows (odd ones).
+# B, Hq, Hkv, Nq, Nk, D, window, sinks.
 WINDOWS = [
     (1, 1, 1, 1, 1, 64, 1, 0), (1, 2, 1, 1, 300, 128, 7, 2), (2, 4, 2, 200, 200, 128, 128, 1),
     (1, 4, 1, 129, 1000, 64, 100, 0), (1, 2, 2, 77, 640, 128, 64, 130), (1, 3, 1, 300, 300, 80, 1000, 3),
@@ -459,3 +458,53 @@ def test_binding_refusals():
     assert e.value.code == nat.FA_ERR_WORKSPACE
     with pytest.raises(ValueError):
         fa.fa_prefix_decode(q, big, big, k, k)                                         # a prefix has no batch
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Nq,window,sinks", [(300, 70, 0), (300, 70, 3), (300, 500, 0), (20, 9, 0), (200, 40, 50)])
+def test_a_nan_shows_where_it_is_seen_and_nowhere_else(D, Nq, window, sinks):
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    g = _gen(D + Nq)
+    q, k, v = (_randn(g, 1, 2, Nq, D) for _ in range(3))
+    ref = window_reference(q, k, v, window, sinks, 1 / math.sqrt(D))
+    seen = visible(torch.arange(Nq, device="cuda"), Nq, window, sinks)
+    for head, key, row, value in ((0, Nq // 2, Nq // 3, "nan"), (1, 0, Nq - 1, "inf")):
+        kk, qq = k.clone(), q.clone()
+        kk[0, head, key] = float("nan")
+        qq[0, head, row] = float(value)  # an infinite q makes scores of +-inf and NaN: its row is NaN
+        bad = torch.zeros(2, Nq, dtype=torch.bool, device="cuda")
+        bad[head] = seen[:, key]
+        bad[head, row] = True
+        o, lse = fa.fa_window_forward(qq, kk, v, window, sinks)
+        assert torch.equal(torch.isnan(lse[0]), bad)
+        assert torch.isnan(o[0][bad]).all()
+        check(o[0][~bad], ref["o"][0][~bad], ref["o_bound"][0][~bad], "O")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("N,P", [(40, 60), (5000, 3000), (64, 20000)])
+def test_a_nan_shows_in_the_decodes(D, N, P):
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    g = _gen(D + N)
+    B, Hq, Hkv = 3, 4, 2
+    q, k, v = _randn(g, B, Hq, 1, D), _randn(g, B, Hkv, N, D), _randn(g, B, Hkv, N, D)
+    kp, vp = _randn(g, Hkv, P, D), _randn(g, Hkv, P, D)
+    lens = torch.tensor([N, 0, N // 2], dtype=torch.int32, device="cuda")
+    q[0, 1] = float("nan")            # every score of a row
+    k[2, 0, N // 2 - 1] = float("nan")  # the newest key of a sequence
+    k[2, 1, N // 2] = float("nan")      # a key that nothing sees
+    bad = torch.zeros(B, Hq, dtype=torch.bool, device="cuda")
+    bad[0, 1], bad[2, 0], bad[2, 1] = True, True, True
+    for call in (lambda: fa.fa_window_decode(q, k, v, 7, 1, lens=lens), lambda: fa.fa_window_decode(q, k, v, N, 0, lens=lens),
+                 lambda: fa.fa_prefix_decode(q, kp, vp, k, v, lens=lens)):
+        o, lse = call()
+        assert torch.equal(torch.isnan(lse[..., 0]), bad)
+        assert torch.equal(torch.isnan(o[:, :, 0]).all(-1), bad) and torch.equal(torch.isnan(o[:, :, 0]).any(-1), bad)
+    kp[1, P - 1] = float("nan")         # the prefix's last key, for one key head
+    bad[:, 2:] = True
+    o, lse = fa.fa_prefix_decode(q, kp, vp, k, v, lens=lens)
+    assert torch.equal(torch.isnan(lse[..., 0]), bad) and torch.equal(torch.isnan(o[:, :, 0]).all(-1), bad)

@@ -14,6 +14,8 @@ dv with Hkv heads, Hq a multiple of Hkv.
 """
 from __future__ import annotations
 
+import ctypes
+import functools
 import math
 from typing import Optional, Tuple
 
@@ -263,17 +265,26 @@ def _empty(like: torch.Tensor, shape, dtype: torch.dtype, stream: Optional[torch
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _empty_like(like: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    return torch.empty_like(like) if stream is None else _empty(like, like.shape, like.dtype, stream)
+
+
 def _size_query(name: str, *sizes: int) -> int:
-    import ctypes
     out = ctypes.c_size_t(0)
     _native.check(getattr(_native.load(), name)(*sizes, ctypes.byref(out)), name)
     return int(out.value)
 
 
+@functools.lru_cache(maxsize=1024)
+def _device_size_query(device: int, name: str, *sizes: int) -> int:
+    """The same number every time: it depends on the sizes and on the current device's SM count alone."""
+    return _size_query(name, *sizes)
+
+
 def _workspace(workspace: Optional[torch.Tensor], like: torch.Tensor, stream, device: int, query: str, *sizes: int):
     """The caller's workspace, or a new one of the size that the library asks for; None when it asks for nothing."""
     if workspace is None:
-        need = _size_query(query, *sizes)
+        need = _device_size_query(device, query, *sizes)
         return _empty(like, (need,), torch.uint8, stream) if need else None
     if workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
@@ -299,7 +310,7 @@ def fa_window_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window:
     _bf16(k, "k", (B, Hkv, rows, D), dev)
     _bf16(v, "v", (B, Hkv, rows, D), dev)
     if o is None:
-        o = _empty(q, q.shape, q.dtype, stream)
+        o = _empty_like(q, stream)
     else:
         _bf16(o, "o", q.shape, dev)
     if lse is None:
@@ -425,7 +436,7 @@ def _rows_and_cache(q, k, v, lens, o, lse, stream):
     if lens is not None:
         _tensor(lens, "lens", torch.int32, (B,), dev)
     if o is None:
-        o = _empty(q, q.shape, q.dtype, stream)
+        o = _empty_like(q, stream)
     else:
         _bf16(o, "o", q.shape, dev)
     if lse is None:

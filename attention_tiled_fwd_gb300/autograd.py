@@ -16,7 +16,7 @@ from typing import Optional
 
 import torch
 
-from . import (FA_BF16, _c_int, _device, _native, _nbytes, _ptr, _scale, _stream_handle, _workspace, fa_backward_dkdv,
+from . import (FA_BF16, _c_int, _device, _device_size_query, _native, _scale, _stream_handle, fa_backward_dkdv,
                fa_backward_dq, fa_forward, fa_window_forward)
 
 
@@ -61,22 +61,28 @@ class _WindowAttention(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dO):
         q, k, v, o, lse = ctx.saved_tensors
-        dO = dO.to(q.dtype).contiguous()
+        if dO.dtype is not q.dtype or not dO.is_contiguous():
+            dO = dO.to(q.dtype).contiguous()
         if dO.data_ptr() % 16:  # a view into something else: the library reads 16-byte units
             dO = dO.clone()
-        lib, stream = _native.load(), _stream_handle(None, _device())
-        dq, delta = torch.empty_like(q), torch.empty_like(lse)
+        dev = _device()
+        lib, stream = _native.load(), _stream_handle(None, dev)
         common = (*ctx.sizes, ctx.scale, FA_BF16, FA_BF16)
+        dq = torch.empty_like(q)
         if not (ctx.needs_input_grad[1] or ctx.needs_input_grad[2]):
+            delta = torch.empty_like(lse)
             rc = lib.fa_window_backward_dq(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dO.data_ptr(),
                                            lse.data_ptr(), delta.data_ptr(), dq.data_ptr(), *common, stream)
             _native.check(rc, "fa_window_backward_dq")
             return dq, None, None, None, None, None
         dk, dv = torch.empty_like(k), torch.empty_like(v)
-        workspace = _workspace(None, q, None, 0, "fa_window_backward_workspace_bytes", *ctx.sizes)
+        # delta, then the workspace, in one piece of memory
+        head = (lse.numel() * 4 + 255) // 256 * 256
+        need = _device_size_query(dev, "fa_window_backward_workspace_bytes", *ctx.sizes)
+        scratch = torch.empty((head + need,), dtype=torch.uint8, device=q.device)  # (held until both launches are made)
         rc = lib.fa_window_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dO.data_ptr(), lse.data_ptr(),
-                                    delta.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *common,
-                                    _ptr(workspace), _nbytes(workspace), stream)
+                                    scratch.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *common,
+                                    scratch.data_ptr() + head, need, stream)
         _native.check(rc, "fa_window_backward")
         return dq, dk, dv, None, None, None
 

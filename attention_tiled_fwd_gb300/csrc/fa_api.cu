@@ -645,16 +645,21 @@ int check_rows(int B, int Hq, int Hkv, int n_q, int N, int D, float scale) {
     return FA_OK;
 }
 
-// CTAs per (sequence, key head, row tile) of windowed decode.
-int token_splits(int B, int Hq, int Hkv, int n_q, int N, int D, const WinArgs &w, int num_sms) {
+// CTAs per (sequence, key head, row tile) of windowed decode, and whether they join their rows as a cluster.
+struct TokenPlan {
+    int splits, cluster;
+};
+TokenPlan token_plan(int B, int Hq, int Hkv, int n_q, int N, int D, const WinArgs &w, int num_sms) {
     // the most key tiles any sequence can need: a cache full of keys, or the window of the n_q rows and the sinks
     const int bn = win_decode_tile_keys();
     const KeySpan sp = key_span(std::max(0, N - n_q), N - 1, w.window, w.sinks, bn);
-    return win_decode_splits(B, Hkv, Hq / Hkv * n_q, sp.n, D, num_sms);
+    const int splits = win_decode_splits(B, Hkv, Hq / Hkv * n_q, sp.n, D, num_sms);
+    const int cluster = win_decode_cluster(splits, sp.n);
+    return TokenPlan{cluster > 0 ? cluster : splits, cluster > 0 ? 1 : 0};
 }
 
-size_t token_workspace(int B, int Hq, int n_q, int D, int splits) {
-    return splits > 1 ? partials_bytes((size_t)B * Hq * n_q, splits, D) : 0;
+size_t token_workspace(int B, int Hq, int n_q, int D, const TokenPlan &p) {
+    return p.splits > 1 && !p.cluster ? partials_bytes((size_t)B * Hq * n_q, p.splits, D) : 0;
 }
 
 int check_token(int B, int Hq, int Hkv, int n_q, int N, int D, int window, int sinks, float scale) {
@@ -670,7 +675,7 @@ extern "C" int fa_window_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q,
     int rc = check_token(B, Hq, Hkv, n_q, N, D, window, sinks, 1.f);
     if (rc != FA_OK) return rc;
     const WinArgs w = window_args(Hkv, N, window, sinks);
-    *bytes = token_workspace(B, Hq, n_q, D, token_splits(B, Hq, Hkv, n_q, N, D, w, current_num_sms()));
+    *bytes = token_workspace(B, Hq, n_q, D, token_plan(B, Hq, Hkv, n_q, N, D, w, current_num_sms()));
     return FA_OK;
 }
 
@@ -688,8 +693,8 @@ extern "C" int fa_window_decode(const void *q, const void *k, const void *v, con
     rc = device_state(&dev, &st);
     if (rc != FA_OK) return rc;
     const WinArgs w = window_args(Hkv, N, window, sinks);
-    const int splits = token_splits(B, Hq, Hkv, n_q, N, D, w, st->num_sms);
-    const size_t need = token_workspace(B, Hq, n_q, D, splits);
+    const TokenPlan plan = token_plan(B, Hq, Hkv, n_q, N, D, w, st->num_sms);
+    const size_t need = token_workspace(B, Hq, n_q, D, plan);
     if (need > 0) {
         rc = check_ptrs({workspace});
         if (rc != FA_OK) return rc;
@@ -697,9 +702,9 @@ extern "C" int fa_window_decode(const void *q, const void *k, const void *v, con
     }
     const size_t rows = (size_t)B * Hq * n_q;
     float *part_o = need > 0 ? static_cast<float *>(workspace) : nullptr;
-    float2 *part_ml = need > 0 ? reinterpret_cast<float2 *>(part_o + rows * splits * D) : nullptr;
+    float2 *part_ml = need > 0 ? reinterpret_cast<float2 *>(part_o + rows * plan.splits * D) : nullptr;
     const WinDecodeArgs a{q, lens, o, lse, B, Hkv, Hq / Hkv * n_q, n_q, N, D, w.window, w.sinks, scale * log2e(),
-                          st->status_word, splits, part_o, part_ml, part_o == nullptr, PrefixParts{}, 0};
+                          st->status_word, plan.splits, part_o, part_ml, plan.cluster, part_o == nullptr, PrefixParts{}, 0};
     CUtensorMap tk, tv;
     if (encode_rows(&tk, k, B * Hkv, N, N, D, win_decode_tile_keys()) != FA_OK ||
         encode_rows(&tv, v, B * Hkv, N, N, D, win_decode_tile_keys()) != FA_OK)
@@ -743,9 +748,10 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int n_q, int P, int N, int D, int
     double best = 1e300;
     for (int left = 0; left <= num_sms / 3; left += 8) {
         const int ctas = p.fused ? num_sms - own_sms : num_sms - left;
-        for (int s = 1; s <= tiles && (s == 1 || (long long)units * s <= 4ll * ctas); ++s) {
-            const int c = (tiles + s - 1) / s;
-            if ((tiles + c - 1) / c != s) continue;  // the same chunks as a smaller count
+        for (int c = tiles; c >= 1; --c) {  // s chunks of c tiles, each s that a chunk size gives once, with the smallest
+            const int s = (tiles + c - 1) / c;
+            c = (tiles + s - 1) / s;
+            if (s > 1 && (long long)units * s > 4ll * ctas) break;
             const double prefix_us = (double)((units * s + ctas - 1) / ctas) * (c + 3) * tile_us;
             const double rest = own_kb - std::min(own_kb, left * 80.0 * prefix_us);
             const double us = p.fused ? prefix_us : prefix_us + rest / 6500;
@@ -755,6 +761,7 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int n_q, int P, int N, int D, int
                 p.chunk_tiles = c;
                 p.ctas = ctas;
             }
+            c = std::min(c, (tiles + s) / (s + 1) + 1);  // on to s + 1 chunks
         }
         if (p.fused) break;
     }
@@ -827,7 +834,7 @@ extern "C" int fa_prefix_decode(const void *q, const void *k_prefix, const void 
     cudaError_t e = launch_win_fwd(a, tq, tkp, tvp, tkp, tvp, tkp, s);
     if (e != cudaSuccess) return FA_ERR_CUDA;
     const WinDecodeArgs d{q, lens, o, lse, B, Hkv, p.R, n_q, N, D, N, 0, scale * log2e(), st->status_word, p.own,
-                          own_o, own_ml, p.fused, parts, 1};
+                          own_o, own_ml, 0, p.fused, parts, 1};
     e = launch_win_decode(d, tk, tv, s);
     if (e == cudaSuccess && !p.fused) e = launch_win_join(d, parts, s);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;

@@ -5,20 +5,30 @@
 
 namespace fa {
 
-// A launch, or (behind) one as the programmatic dependent of the launch before it on the stream.
+// A launch, or (behind) one as the programmatic dependent of the launch before it on the stream; `cluster` neighbouring
+// CTAs along x form a cluster.
 template <class... Params, class... Args>
-cudaError_t launch_behind(void (*kern)(Params...), dim3 grid, int threads, size_t smem, bool behind, cudaStream_t s,
-                          Args... args) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+cudaError_t launch_behind(void (*kern)(Params...), dim3 grid, int threads, size_t smem, bool behind, int cluster,
+                          cudaStream_t s, Args... args) {
+    cudaLaunchAttribute attrs[2];
+    int n = 0;
+    if (behind) {
+        attrs[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attrs[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attrs[n].id = cudaLaunchAttributeClusterDimension;
+        attrs[n].val.clusterDim.x = cluster;
+        attrs[n].val.clusterDim.y = attrs[n].val.clusterDim.z = 1;
+        ++n;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = behind ? 1 : 0;
+    cfg.attrs = attrs;
+    cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, kern, Params(args)...);
 }
 

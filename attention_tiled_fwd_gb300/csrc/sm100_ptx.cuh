@@ -391,6 +391,30 @@ __device__ __forceinline__ uint32_t f2_to_bf16x2(uint64_t v) {
     f2_unpack(v, lo, hi);
     return pack_bf16x2(lo, hi);
 }
+// Thread-block clusters: a barrier of all their threads (shared-memory writes before it are seen behind it), and reads of
+// another CTA's shared memory.
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
 // Three-input maximum (sm_100 family); NaN inputs are ignored as in fmaxf.
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float d;

@@ -16,6 +16,9 @@ struct WinDecodeArgs {
     int splits;        // CTAs a sequence's tiles are dealt to
     float *part_o;     // partials [row][splits][D]
     float2 *part_ml;   // [row][splits]
+    // cluster: the splits of a row tile are a cluster (2 to 8 CTAs), which joins their partials through distributed
+    // shared memory and writes o and lse; nothing else is launched
+    int cluster;
     // join (splits = 1): instead of a partial, each CTA joins its rows with the prefix's partials (none: parts.o null) and
     // writes o and lse
     int join;
@@ -26,6 +29,8 @@ struct WinDecodeArgs {
 // CTAs per (sequence, key head, row tile) for caches that need up to `tiles` tiles.
 int win_decode_splits(int B, int Hkv, int R, int tiles, int D, int num_sms);
 int win_decode_tile_keys();
+// The same where the splits of a row tile form a cluster, or 0 where more of them than it holds are worth a second launch.
+int win_decode_cluster(int splits, int tiles);
 // SMs that all CTAs of such a launch take at once.
 int win_decode_sms(int B, int Hkv, int R, int splits, int D);
 cudaError_t launch_win_decode(const WinDecodeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s);

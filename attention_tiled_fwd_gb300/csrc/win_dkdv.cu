@@ -595,7 +595,7 @@ cudaError_t launch_items(const BwdArgs &a, const CUtensorMap &tq, const CUtensor
     if (e != cudaSuccess) return e;
     const int n_items = ((a.win.Nk + kBN - 1) / kBN + a.win.sink_tiles * a.win.chunks) * a.win.Hkv * a.B;
     const int sms = num_sms > 0 ? num_sms : kNumSms;
-    return launch_behind(kern, dim3(n_items < sms ? n_items : sms), kThreads, C::kAlloc, behind, s, tq, tk, tv, tdo, tdk,
+    return launch_behind(kern, dim3(n_items < sms ? n_items : sms), kThreads, C::kAlloc, behind, 1, s, tq, tk, tv, tdo, tdk,
                          tdv, parts[0], parts[1], a, n_items);
 }
 
@@ -603,7 +603,7 @@ cudaError_t launch_items(const BwdArgs &a, const CUtensorMap &tq, const CUtensor
 
 cudaError_t launch_sink_sum(const BwdArgs &a, const float *part_dk, const float *part_dv, cudaStream_t s) {
     const dim3 grid((kBN * a.D / 4 + 255) / 256, a.B * a.win.Hkv * a.win.sink_tiles);
-    return launch_behind(sink_sum_kernel, grid, 256, 0, true, s, a, part_dk, part_dv);
+    return launch_behind(sink_sum_kernel, grid, 256, 0, true, 1, s, a, part_dk, part_dv);
 }
 
 cudaError_t launch_win_dkdv(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,

@@ -60,6 +60,8 @@ class _WindowAttention(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dO):
+        if torch.is_grad_enabled():  # the gradients would be constants in the graph that create_graph asks for
+            raise RuntimeError("window_attention has no second derivatives: create_graph=True is not supported")
         q, k, v, o, lse = ctx.saved_tensors
         if dO.dtype is not q.dtype or not dO.is_contiguous():
             dO = dO.to(q.dtype).contiguous()
@@ -91,5 +93,5 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: 
                      scale: Optional[float] = None) -> torch.Tensor:
     """Windowed attention, differentiable in q, k and v: q [B, Hq, Nq, D] are the last Nq positions of k, v
     [B, Hkv, Nk, D] (bf16 CUDA tensors, Hq a multiple of Hkv); a row at position p sees key j iff j <= p and
-    (j < sinks or j > p - window)."""
+    (j < sinks or j > p - window).  First derivatives only."""
     return _WindowAttention.apply(q, k, v, int(window), int(sinks), scale)

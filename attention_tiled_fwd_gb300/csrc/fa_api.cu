@@ -399,15 +399,18 @@ extern "C" int fa_decode_noalloc(const void *q, const void *k, const void *v, vo
 
 // ---------------------------------------------------------------- windowed and shared-prefix attention
 namespace {
+// Finite in units of log2 as well, and positive: the row maximum is taken before the scale.
+bool scale_ok(float scale) { return scale > 0.f && std::isfinite(scale * log2e()); }
+
 // Sizes and mask of windowed attention: 1 <= Nq <= Nk, Hq a multiple of Hkv.
 int check_window(int B, int Hq, int Hkv, int Nq, int Nk, int kv_rows, int D, int window, int sinks, float scale) {
     if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Nk < 1 || D < 1) return FA_ERR_SHAPE;
     if (B > 65535 || Hq > 65535 || Hq % Hkv != 0) return FA_ERR_SHAPE;
     if (Nq > Nk || kv_rows < Nk || Nk > kMaxPositions) return FA_ERR_SHAPE;
     if (window < 1 || sinks < 0) return FA_ERR_SHAPE;
-    const long long max = (1ll << 31) - 1;
+    const long long max = (1ll << 31) - (1 << 20);  // an index, and a persistent grid's stride past it
     if ((long long)B * Hq * Nq > max || (long long)B * Hkv * kv_rows > max) return FA_ERR_SHAPE;
-    if (!std::isfinite(scale) || scale <= 0.f) return FA_ERR_SCALE;  // the masks are -inf in units of the scale
+    if (!scale_ok(scale)) return FA_ERR_SCALE;
     if (!bf16_head_dim_ok(D)) return FA_ERR_HEAD_DIM;
     return FA_OK;
 }
@@ -638,9 +641,9 @@ constexpr int kMaxDecodeRows = 16;  // new rows per sequence
 int check_rows(int B, int Hq, int Hkv, int n_q, int N, int D, float scale) {
     if (B < 1 || Hq < 1 || Hkv < 1 || n_q < 1 || N < 1 || D < 1) return FA_ERR_SHAPE;
     if (B > 65535 || Hq > 65535 || Hq % Hkv != 0 || n_q > kMaxDecodeRows || N > kMaxPositions) return FA_ERR_SHAPE;
-    const long long max = (1ll << 31) - 1;
+    const long long max = (1ll << 31) - (1 << 20);
     if ((long long)B * Hkv * N > max || (long long)B * Hq * n_q > max) return FA_ERR_SHAPE;
-    if (!std::isfinite(scale) || scale <= 0.f) return FA_ERR_SCALE;
+    if (!scale_ok(scale)) return FA_ERR_SCALE;
     if (D != 64 && D != 128 && D != 256) return FA_ERR_HEAD_DIM;
     return FA_OK;
 }
@@ -848,7 +851,7 @@ extern "C" const char *fa_status_string(int status) {
         case FA_ERR_HEAD_DIM: return "head dimension not supported for this dtype / pass";
         case FA_ERR_DTYPE: return "unsupported dtype or grad_dtype";
         case FA_ERR_ALIGN: return "pointer not 16-byte aligned";
-        case FA_ERR_SCALE: return "scale is not finite";
+        case FA_ERR_SCALE: return "scale is not finite, or not positive where it has to be";
         case FA_ERR_CUDA: return "CUDA runtime error";
         case FA_ERR_TIMEOUT: return "a bounded in-kernel wait ran out";
         case FA_ERR_DEVICE_PTR: return "pointer is not device-accessible memory";

@@ -236,7 +236,8 @@ FA_API int fa_decode_noalloc(const void *q, const void *k, const void *v, void *
  * Keys that no query row sees (rows Nk and up, and for Nq < Nk those between the sinks and the first window) may
  * hold anything in the forward; every other element must be finite (a masked weight is an exact 0, and 0 times a
  * non-finite value is NaN).
- * Supported: dtype FA_BF16, D a multiple of 8 in [8, 256]; Nk <= 2^29; scale finite and > 0 (FA_ERR_SCALE).
+ * Supported: dtype FA_BF16, D a multiple of 8 in [8, 256]; Nk <= 2^29; scale > 0 and scale log2(e) finite
+ * (FA_ERR_SCALE); less than 2^31 - 2^20 rows in a tensor.
  * Sizes outside these, Nq > Nk, window < 1, sinks < 0: FA_ERR_SHAPE.
  */
 
@@ -286,7 +287,7 @@ FA_API int fa_window_backward_workspace_bytes(int B, int Hq, int Hkv, int Nq, in
  *   rows from lens[b] on may hold anything.
  *   D in {64, 128, 256}; n_q <= N.  Other conditions as for windowed attention.
  *   workspace: as fa_decode's, of fa_window_decode_workspace_bytes(...) bytes (NULL when that is 0).
- * Launches one kernel, and a second when the keys of a sequence are split over CTAs.
+ * Launches one kernel, and a second when the keys of a sequence are split over more CTAs than a cluster holds.
  */
 FA_API int fa_window_decode(const void *q, const void *k, const void *v, const int *lens, void *o, float *lse,
                             int B, int Hq, int Hkv, int n_q, int N, int D, int window, int sinks, float scale,
@@ -300,7 +301,7 @@ FA_API int fa_window_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q, int
  *   k_prefix, v_prefix: [Hkv, P, D]; q, o, lse, lens and k, v (the sequences' own caches behind the prefix) as for
  *   fa_window_decode.  Row i of sequence b sees every prefix key, and key j of its own cache iff
  *   j <= lens[b] - n_q + i.  lens[b] may be 0.
- *   P >= 1, N >= 1, D in {64, 128, 256}, 1 <= n_q <= 16, scale finite and > 0.
+ *   P >= 1, N >= 1, D in {64, 128, 256}, 1 <= n_q <= 16, scale as for windowed attention.
  *   workspace: fa_prefix_decode_workspace_bytes(...) bytes, 16-byte aligned; two calls that run concurrently must
  *   not share it.
  */

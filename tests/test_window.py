@@ -58,7 +58,7 @@ BAD = [(dict(B=0), "SHAPE"), (dict(Hq=0), "SHAPE"), (dict(Hkv=0), "SHAPE"), (dic
        (dict(sinks=-1), "SHAPE"), (dict(Nk=(1 << 29) + 1, kv_rows=(1 << 29) + 1), "SHAPE"),
        (dict(B=65535, Hq=65535, Hkv=65535, Nq=16), "SHAPE"), (dict(D=12), "HEAD_DIM"), (dict(D=264), "HEAD_DIM"),
        (dict(scale=0.0), "SCALE"), (dict(scale=-1.0), "SCALE"), (dict(scale=math.nan), "SCALE"),
-       (dict(scale=math.inf), "SCALE"), (dict(dtype=nat.FA_F32), "DTYPE"), (dict(dtype=9), "DTYPE")]
+       (dict(scale=math.inf), "SCALE"), (dict(scale=3e38), "SCALE"), (dict(dtype=nat.FA_F32), "DTYPE"), (dict(dtype=9), "DTYPE")]
 
 
 def _err(name):
@@ -508,3 +508,13 @@ def test_a_nan_shows_in_the_decodes(D, N, P):
     bad[:, 2:] = True
     o, lse = fa.fa_prefix_decode(q, kp, vp, k, v, lens=lens)
     assert torch.equal(torch.isnan(lse[..., 0]), bad) and torch.equal(torch.isnan(o[:, :, 0]).all(-1), bad)
+
+
+@pytest.mark.gpu
+def test_second_derivatives_are_refused():
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    q = _randn(_gen(1), 1, 1, 40, 64).requires_grad_()
+    o = fa.window_attention(q, q, q, 9)
+    with pytest.raises(RuntimeError, match="create_graph"):
+        torch.autograd.grad(o.float().square().sum(), q, create_graph=True)

@@ -296,6 +296,7 @@ PREFIXES = [
     (40, 8, 2, 1, 513, 40, 128, None), (2, 16, 1, 16, 700, 50, 128, [50, 7]), (3, 16, 1, 16, 300, 200, 256, [16, 0, 200]),
     (7, 6, 2, 2, 3000, 300, 256, [2, 300, 5, 64, 65, 0, 1]), (130, 4, 4, 1, 260, 9, 64, None),
     (2, 40, 1, 4, 400, 30, 64, [30, 4]), (33, 5, 5, 1, 20000, 16, 128, None), (1, 2, 1, 1, 128, 4000, 128, [3333]),
+    (300, 4, 4, 1, 260, 9, 64, None), (140, 16, 2, 1, 300, 20, 256, None), (90, 16, 1, 1, 1500, 700, 128, None),
 ]
 
 
@@ -518,3 +519,91 @@ def test_second_derivatives_are_refused():
     o = fa.window_attention(q, q, q, 9)
     with pytest.raises(RuntimeError, match="create_graph"):
         torch.autograd.grad(o.float().square().sum(), q, create_graph=True)
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """The same calls from two streams, each with workspaces of its own, give what they give one after the other."""
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    g = _gen(11)
+    q, k, v = _randn(g, 2, 8, 900, 128), _randn(g, 2, 2, 900, 128), _randn(g, 2, 2, 900, 128)
+    dO = _randn(g, 2, 8, 900, 128)
+    tq, kp, vp = _randn(g, 2, 8, 1, 128), _randn(g, 2, 5000, 128), _randn(g, 2, 5000, 128)
+
+    def calls(stream):
+        o, lse = fa.fa_window_forward(q, k, v, 100, 5, stream=stream)
+        grads = fa.fa_window_backward(q, k, v, o, dO, lse, 100, 5, stream=stream)
+        return (o, lse, *grads, *fa.fa_window_decode(tq, k, v, 900, 0, stream=stream),
+                *fa.fa_prefix_decode(tq, kp, vp, k, v, stream=stream))
+
+    expect = calls(None)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [calls(s) for _ in range(20) for s in streams]
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 0
+    for outs in got:
+        for a, b in zip(outs, expect):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_caches_beyond_32_bit_offsets():
+    """A sequence at the end of a cache of more than 2^32 elements; what its rows do not see is left unwritten."""
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    g = _gen(12)
+    N, D, window, sinks = (1 << 24) + 77, 256, 100, 3
+    k, v = (torch.empty(1, 1, N, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    small = [_randn(g, 1, 1, 203, D) for _ in range(2)]
+    for big, s in zip((k, v), small):  # rows 0 .. 2 and the last 200
+        big[:, :, :3] = s[:, :, :3]
+        big[:, :, N - 200:] = s[:, :, 3:]
+    q = _randn(g, 1, 2, 16, D)
+    ref = window_reference(q, *small, window, sinks, 1 / math.sqrt(D))
+    for o, lse in (fa.fa_window_decode(q, k, v, window, sinks), fa.fa_window_forward(q, k, v, window, sinks)):
+        check(o, ref["o"], ref["o_bound"], "O")
+        check_lse(lse, ref["lse"], "LSE")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_heads_beyond_32_bit_offsets(D):
+    """The last head of tensors of more than 2^32 elements, forward and backward, is what it is by itself."""
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    g = _gen(13)
+    H, N, window = 8, (1 << 32) // (8 * D) + 1000, 70
+    q, k, v, dO = (torch.zeros(1, H, N, D, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    for t in (q, k, v, dO):
+        t[:, -1] = _randn(g, 1, N, D)
+    last = [t[:, -1:].contiguous() for t in (q, k, v, dO)]
+    o, lse = fa.fa_window_forward(q, k, v, window)
+    o1, lse1 = fa.fa_window_forward(*last[:3], window)
+    assert torch.equal(o[:, -1:], o1) and torch.equal(lse[:, -1:], lse1)
+    dq, dk, dv, delta = fa.fa_window_backward(q, k, v, o, dO, lse, window, grad_dtype=torch.bfloat16)
+    alone = fa.fa_window_backward(*last[:3], o1, last[3], lse1, window, grad_dtype=torch.bfloat16)
+    for a, b in zip((dq, dk, dv, delta), alone):
+        assert torch.equal(a[:, -1:], b)
+
+
+@pytest.mark.gpu
+def test_gradients_of_broadcast_and_strided_inputs():
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    g = _gen(14)
+    B, H, N, D = 3, 4, 150, 64
+    q = _randn(g, B, N, H, D).requires_grad_()        # heads behind rows: a strided view
+    kv = _randn(g, 1, 1, N, D).requires_grad_()       # one tensor for keys and values of every sequence
+    dO = _randn(g, B, H, N, D)
+    k = kv.expand(B, 1, N, D)
+    o = fa.window_attention(q.transpose(1, 2), k, k, 40, 2)
+    dq, dkv = torch.autograd.grad(o, (q, kv), dO)
+    ref = window_reference(q.detach().transpose(1, 2), k.detach(), k.detach(), 40, 2, 1 / math.sqrt(D), dO)
+    check(dq.transpose(1, 2), ref["dq"], ref["dq_bound"] + U * ref["dq"].abs(), "dq")
+    # three sequences' dK and dV, each rounded to bf16, added by autograd in two sums that each round once more: at most
+    # (2 + 3) half steps of the magnitudes that are added
+    parts = [ref[n].abs() for n in ("dk", "dv")]
+    bound = (ref["dk_bound"] + ref["dv_bound"]).sum(0, keepdim=True) + 5 * U * (parts[0] + parts[1]).sum(0, keepdim=True)
+    check(dkv, (ref["dk"] + ref["dv"]).sum(0, keepdim=True), bound, "dk + dv")

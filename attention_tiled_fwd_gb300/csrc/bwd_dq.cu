@@ -27,7 +27,8 @@
 // TMEM (128 lanes = queries): S[b] = [64b, 64b+64), dP[b] = [128+64b, ...),
 // dQ [256, 256+D), b = j % 2, dS[b] = [256+D+32b, +32), then Q as bf16
 // pairs.  This kernel serves D = 128 (D = 64 runs bwd_dq_k128.cu, whose
-// 128-key tiles make S and dP N = 128 products).  The key tile is 64 rows so
+// 128-key tiles make S and dP N = 128 products; of the windowed forms, D = 64 runs here
+// and D = 128 runs win_dq.cu).  The key tile is 64 rows so
 // that S and dP are double-buffered: the tensor core computes S_{j+1},
 // dP_{j+1} and dQ_{j-1} while the compute warps turn tile j into dS.  Q sits in TMEM so that
 // S = Q K_j^T runs as a TS MMA reading only K_j from shared memory: an N = 64
@@ -584,6 +585,8 @@ cudaError_t launch_width(const BwdArgs &a, const CUtensorMap &tq, const CUtensor
                          const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, cudaStream_t s) {
     switch (kernel_head_dim(a.D)) {
         case 64:
+            // Windowed: a short window is ten 64-key tiles beside 4 us of a CTA's fixed cost, which a second CTA on the SM
+            // hides (B1 H32 N32768 window 512: 348 us; one CTA an SM 476; a persistent grid of such pairs 378).
             if constexpr (WIN)
                 return launch_spec<64, 64, false, 6, true, true, 2>(a, tq, tk, tv, tdo, to, tdq, s);
             else

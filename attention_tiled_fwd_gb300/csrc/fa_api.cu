@@ -416,7 +416,7 @@ int check_window(int B, int Hq, int Hkv, int Nq, int Nk, int kv_rows, int D, int
 }
 
 WinArgs window_args(int Hkv, int Nk, int window, int sinks) {
-    WinArgs w{Hkv, Nk, std::min(window, Nk), std::min(sinks, Nk), 0, 0};
+    WinArgs w{Hkv, Nk, std::min(window, Nk), std::min(sinks, Nk), 0, 0, 0};
     if (w.window == Nk) w.sinks = 0;  // every earlier key is in the window
     return w;
 }
@@ -437,6 +437,21 @@ WinArgs window_args_dkdv(int B, int Hq, int Hkv, int Nq, int Nk, int D, int wind
     // four sink tiles an SM balance each other uncut, and their partials would be as large as the gradients
     const long long items = (long long)B * Hkv * sink_tiles;
     if (items >= 4 * num_sms) return w;
+    // Few sinks at D = 64: a step of a chunk costs as much as any other (1.5 us) for 16 keys or less, so win_sinks.cu takes
+    // the chunks where that saves more than it costs (a launch, and Q and dO once more from HBM), unless SMs that have
+    // nothing else to do would take them.  Both gradients at window 512: 32 heads of 32768 rows 806 us instead of 848, but
+    // 2 x 16 (4 key heads) of 4096 rows 125 instead of 112.
+    if (kernel_head_dim(D) == 64 && w.sinks <= kFewSinks) {
+        const long long idle = std::max(0ll, own * num_sms - own * B * Hkv * ((Nk + bk - 1) / bk));
+        const double saved_us = 1.5 * (double)(items * rest - idle) / num_sms;
+        const double cost_us = 5 + (double)B * Hq * std::max(0ll, Nq - end) * D * 4 / 5.5e6;
+        if (saved_us > cost_us) {
+            w.few = 1;
+            w.sink_tiles = 1;
+            w.chunks = (int)std::max(1ll, std::min(2 * num_sms / items, rest / 4));  // one wave, two CTAs an SM
+            return w;
+        }
+    }
     // a chunk is as long as another item, or up to four of them when that is a quarter of an SM's share of the
     // launch or less; 16 steps at least; and the launch has four chunks an SM at most beside one a sink tile
     const long long per = std::max({own, std::min(all / (4 * num_sms), 4 * own), 16ll, rest * items / (4 * num_sms)});
@@ -561,6 +576,7 @@ int window_dkdv(const WinBackward &w, const WinArgs &win, const DeviceState &st,
             return FA_ERR_CUDA;
     }
     cudaError_t e = launch_win_dkdv(a, tq, tk, tv, tdo, tdk, tdv, parts, st.num_sms, behind, s);
+    if (e == cudaSuccess && win.few) e = launch_win_sinks(a, tq, tdo, part_dk, part_dv, s);
     if (e == cudaSuccess && part_floats > 0) e = launch_sink_sum(a, part_dk, part_dv, s);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -126,7 +126,7 @@ struct WinKeyItem {
 __device__ __forceinline__ WinKeyItem win_key_item(const BwdArgs &a, int x, int bk, int bq) {
     const int G = a.H / a.win.Hkv, n_bh = a.B * a.win.Hkv;
     const int off = a.win.Nk - a.N;  // position of row 0
-    const int extra = n_bh * a.win.sink_tiles * a.win.chunks;
+    const int extra = n_bh * a.win.sink_tiles * a.win.chunks;  // the chunks come first
     WinKeyItem w;
     int chunk = -1;
     if (x < extra) {
@@ -265,6 +265,9 @@ cudaError_t launch_win_dkdv(const BwdArgs &a, const CUtensorMap &tq, const CUten
                             const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv,
                             const CUtensorMap *parts, int num_sms, bool behind, cudaStream_t s);
 cudaError_t launch_sink_sum(const BwdArgs &a, const float *part_dk, const float *part_dv, cudaStream_t s);
+// The chunks of the rows behind few sinks, launched behind the dK/dV kernel (win_sinks.cu).
+cudaError_t launch_win_sinks(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tdo, float *part_dk, float *part_dv,
+                             cudaStream_t s);
 cudaError_t launch_selftest_timeout(int *status, int limit_us, cudaStream_t s);
 
 // Head dimension a bf16 kernel is built for: the smallest of 64, 128, 192, 256 that holds D.  Any

@@ -64,7 +64,9 @@ struct WinArgs {
     // They are cut into `chunks` work items per sink tile (0: not cut); those items and the sink tile's own
     // write fp32 partials, which sink_sum_kernel adds in a fixed order.
     int sink_tiles, chunks;
+    int few;  // the chunks run in win_sinks.cu instead (one sink tile of at most kFewSinks sinks, D = 64)
 };
+constexpr int kFewSinks = 16;
 
 // Division of 0 <= n < 2^31 by a number that the host knows: n / d = (mulhi(n, mul) + n) >> shift.
 struct FastDiv {

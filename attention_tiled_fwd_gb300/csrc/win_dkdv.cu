@@ -18,7 +18,11 @@
 // and issuer A runs its first products, while the compute warps still write the
 // current item's gradients; only dV and dK in TMEM are handed over (acc_free).
 // An item is a key tile, or a chunk of the rows behind a sink tile's window
-// (win_key_item), whose fp32 partial sink_sum_kernel adds up.
+// (win_key_item), whose fp32 partial sink_sum_kernel adds up; with few sinks those
+// chunks can run in win_sinks.cu.  Bound by the compute
+// warps (TMEM in, exponentials, TMEM out twice a tile) more than by the products:
+// B2 H16/4 N4096 D128 window 1024: 146 us, 827 TFLOP/s of the visible pairs (four
+// products each); B1 H32 N32768 D64 window 512: 501 us, 545.
 #include "fa_internal.h"
 #include "launch.cuh"
 #include "sm100_ptx.cuh"
@@ -103,6 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int N = a.N;
+    const int skip = D == 64 && a.win.few ? a.B * a.win.Hkv * a.win.chunks : 0;  // those run in win_sinks.cu
     if (threadIdx.x == 0) {
         for (int b = 0; b < 2; ++b) {
             mbar_init(&kv_full[b], 1);
@@ -156,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; ok && k * (int)gridDim.x < n_items; ++k) {
             const int x = persistent_work_index(k, n_items);
             if (x < 0) continue;
-            const WinKeyItem w = win_key_item(a, x, kBN, kBQ);
+            const WinKeyItem w = win_key_item(a, x + skip, kBN, kBQ);
             const int buf = n & 1;
             if (n >= 2 && !(ok = warp_wait(&kv_empty[buf], ((n >> 1) - 1) & 1, a.status, kSiteKVEmpty))) break;
             if (lane == 0) {
@@ -229,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; ok && k * (int)gridDim.x < n_items; ++k) {
             const int x = persistent_work_index(k, n_items);
             if (x < 0) continue;
-            const WinKeyItem w = win_key_item(a, x, kBN, kBQ);
+            const WinKeyItem w = win_key_item(a, x + skip, kBN, kBQ);
             const int buf = n & 1;
             if (!(ok = warp_wait(&kv_full[buf], (n >> 1) & 1, a.status, kSiteKV))) break;
             ++n;
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; ok && k * (int)gridDim.x < n_items; ++k) {
             const int x = persistent_work_index(k, n_items);
             if (x < 0) continue;
-            const WinKeyItem w = win_key_item(a, x, kBN, kBQ);
+            const WinKeyItem w = win_key_item(a, x + skip, kBN, kBQ);
             auto acc_ready = [&] { return n == 0 || warp_wait(acc_free, (n - 1) & 1, a.status, kSiteAcc); };
             // an item without rows waits too: every phase of acc_free has to be waited for
             if (w.n == 0 && !(ok = acc_ready())) break;
@@ -341,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; ok && k * (int)gridDim.x < n_items; ++k) {
                 const int x = persistent_work_index(k, n_items);
                 if (x < 0) continue;
-                const WinKeyItem w = win_key_item(a, x, kBN, kBQ);
+                const WinKeyItem w = win_key_item(a, x + skip, kBN, kBQ);
                 const bool partial = w.part >= 0, out_bf16 = a.grad_bf16 && !partial;
                 const uint8_t *stage = smem + (n & 1) * 2 * C::kKVBytes;
                 const int y = partial ? 0 : w.k_tile * kBN, z = partial ? w.part : w.bh;
@@ -378,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (; k * (int)gridDim.x < n_items; ++k) {
                 const int x = persistent_work_index(k, n_items);
                 if (x < 0) continue;
-                *w = win_key_item(a, x, kBN, kBQ);
+                *w = win_key_item(a, x + skip, kBN, kBQ);
                 ++k;
                 return true;
             }
@@ -569,8 +574,9 @@ __global__ void sink_sum_kernel(BwdArgs a, const float *part_dk, const float *pa
         for (int w = 0; w < 2; ++w) {
             const float *src = (w ? part_dv : part_dk) + in;
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int n = a.win.few && e / cols >= kFewSinks ? 1 : parts;  // the others of win_sinks.cu hold 16 rows
 #pragma unroll 4
-            for (int p = 0; p < parts; ++p) {
+            for (int p = 0; p < n; ++p) {
                 const float4 v = *reinterpret_cast<const float4 *>(src + (size_t)p * kBN * a.D);
                 s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
             }
@@ -593,7 +599,8 @@ cudaError_t launch_items(const BwdArgs &a, const CUtensorMap &tq, const CUtensor
     static std::atomic<unsigned long long> allowed{0};
     cudaError_t e = allow_smem((const void *)kern, C::kAlloc, allowed);
     if (e != cudaSuccess) return e;
-    const int n_items = ((a.win.Nk + kBN - 1) / kBN + a.win.sink_tiles * a.win.chunks) * a.win.Hkv * a.B;
+    const int chunks = a.win.few ? 0 : a.win.sink_tiles * a.win.chunks;
+    const int n_items = ((a.win.Nk + kBN - 1) / kBN + chunks) * a.win.Hkv * a.B;
     const int sms = num_sms > 0 ? num_sms : kNumSms;
     return launch_behind(kern, dim3(n_items < sms ? n_items : sms), kThreads, C::kAlloc, behind, 1, s, tq, tk, tv, tdo, tdk,
                          tdv, parts[0], parts[1], a, n_items);

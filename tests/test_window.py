@@ -189,7 +189,8 @@ def test_window_forward(case):
 @pytest.mark.parametrize("case", WINDOWS + [(1, 2, 1, 40, 900, 64, 50, 0), (1, 2, 1, 40, 900, 128, 50, 3),
                                             (1, 2, 1, 40, 900, 256, 50, 1), (1, 4, 2, 1500, 1500, 128, 64, 4), (1, 4, 2, 1500, 1500, 64, 64, 4),
                                             (2, 3, 1, 1700, 1800, 256, 60, 200), (1, 6, 2, 2000, 2000, 80, 100, 300),
-                                            (1, 2, 2, 2000, 4000, 40, 30, 7)])
+                                            (1, 2, 2, 2000, 4000, 40, 30, 7), (1, 128, 32, 1999, 1999, 64, 64, 4),
+                                            (2, 64, 64, 2000, 2100, 40, 60, 16)])
 def test_window_backward(case, grad_dtype):
     import attention_tiled_fwd_gb300 as fa
     cuda_or_skip()

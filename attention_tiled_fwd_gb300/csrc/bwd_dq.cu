@@ -27,8 +27,8 @@
 // TMEM (128 lanes = queries): S[b] = [64b, 64b+64), dP[b] = [128+64b, ...),
 // dQ [256, 256+D), b = j % 2, dS[b] = [256+D+32b, +32), then Q as bf16
 // pairs.  This kernel serves D = 128 (D = 64 runs bwd_dq_k128.cu, whose
-// 128-key tiles make S and dP N = 128 products; of the windowed forms, D = 64 runs here
-// and D = 128 runs win_dq.cu).  The key tile is 64 rows so
+// 128-key tiles make S and dP N = 128 products; the windowed forms of both have
+// kernels of their own, win_dq.cu and win_dq_k128.cu).  The key tile is 64 rows so
 // that S and dP are double-buffered: the tensor core computes S_{j+1},
 // dP_{j+1} and dQ_{j-1} while the compute warps turn tile j into dS.  Q sits in TMEM so that
 // S = Q K_j^T runs as a TS MMA reading only K_j from shared memory: an N = 64
@@ -96,16 +96,16 @@ struct DqSmem {
 // TMEM as the A operand of S (else S reads Q from shared memory); WIN: windowed attention (win.cuh): the key
 // tiles are those of key_span, a query head reads its group's key head, and the mask is the window's.
 // kSingle: S and dP in one buffer each, emptied by the compute warps into registers first thing (s_free, dp_free),
-// so that all of dQ fits beside them (D = 256), or two CTAs on an SM (kCtas = 2).
-template <int D, int DQ, bool QT, int NSLOT, bool WIN, bool kSingle, int kCtas>
-__global__ void __launch_bounds__(kThreads, kCtas)
+// so that all of dQ fits beside them (D = 256).
+template <int D, int DQ, bool QT, int NSLOT, bool WIN, bool kSingle>
+__global__ void __launch_bounds__(kThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
                   const __grid_constant__ CUtensorMap tmap_o, const __grid_constant__ CUtensorMap tmap_dq,
                   BwdArgs a) {
     using L = DqSmem<D, NSLOT>;
     constexpr int kPanels = D / 64;
-    constexpr uint32_t kTmemCols = 512 / kCtas;
+    constexpr uint32_t kTmemCols = 512;
     constexpr uint32_t kColDP0 = kSingle ? 64 : 128;  // dP[b] at kColDP0 + 64 b (b = 0 when kSingle)
     constexpr uint32_t kColDQ = kSingle ? 128 : 256, kColDS = kColDQ + DQ, kColQ = kColDS + 64;
     static_assert(kColQ + (QT ? D / 2 : 0) <= kTmemCols, "TMEM budget");
@@ -183,7 +183,6 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if constexpr (WIN) launch_dependents();  // the dK/dV kernel of the same call fills the SMs as they come free
     const uint32_t tmem = *tmem_holder;
 
     if (warp == 0) {
@@ -346,19 +345,22 @@ __global__ void __launch_bounds__(kThreads, kCtas)
             bool ook = mbar_wait(o_full, 0, a.status, kSiteQ) && mbar_wait(q_full, 0, a.status, kSiteQ);
             if (__all_sync(0xffffffffu, ook)) {
 #pragma unroll
-                for (int i = 0; i < kDCols / 8; ++i) {
-                    // chunk k of panel p; its swizzled position: lanes (rows) spread over all 32 banks
-                    const int c8 = g * (kDCols / 8) + i, p = c8 >> 3, k = c8 & 7;
-                    const int off = p * (kBM * 128) + r * 128 + ((k ^ (r & 7)) << 4);
-                    const uint4 ov = *reinterpret_cast<const uint4 *>(o_s + off);
-                    const uint4 dv = *reinterpret_cast<const uint4 *>(do_s + off);
-                    const uint32_t ow[4] = {ov.x, ov.y, ov.z, ov.w}, dw[4] = {dv.x, dv.y, dv.z, dv.w};
+                for (int p = g * (kDCols / 64); p < (g + 1) * (kDCols / 64); ++p) {
+                    const uint8_t *orow = o_s + p * (kBM * 128) + r * 128;
+                    const uint8_t *drow = do_s + p * (kBM * 128) + r * 128;
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const float2 of = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&ow[t]));
-                        const float2 df = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&dw[t]));
-                        delta = fmaf(of.x, df.x, delta);
-                        delta = fmaf(of.y, df.y, delta);
+                    for (int k = 0; k < 8; ++k) {
+                        // the swizzled position of chunk k: lanes (rows) spread over all 32 banks
+                        const uint4 ov = *reinterpret_cast<const uint4 *>(orow + ((k ^ (r & 7)) << 4));
+                        const uint4 dv = *reinterpret_cast<const uint4 *>(drow + ((k ^ (r & 7)) << 4));
+                        const uint32_t ow[4] = {ov.x, ov.y, ov.z, ov.w}, dw[4] = {dv.x, dv.y, dv.z, dv.w};
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            const float2 of = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&ow[t]));
+                            const float2 df = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&dw[t]));
+                            delta = fmaf(of.x, df.x, delta);
+                            delta = fmaf(of.y, df.y, delta);
+                        }
                     }
                 }
             }
@@ -567,12 +569,12 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     }
 }
 
-template <int D, int DQ, bool QT, int NSLOT, bool WIN, bool SINGLE = false, int CTAS = 1>
+template <int D, int DQ, bool QT, int NSLOT, bool WIN, bool SINGLE = false>
 cudaError_t launch_spec(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                         const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, cudaStream_t s) {
     using L = DqSmem<D, NSLOT>;
-    static_assert(L::kAlloc <= 232448 / CTAS, "shared memory budget");
-    auto kern = bwd_dq_kernel<D, DQ, QT, NSLOT, WIN, SINGLE, CTAS>;
+    static_assert(L::kAlloc <= 232448, "shared memory budget");
+    auto kern = bwd_dq_kernel<D, DQ, QT, NSLOT, WIN, SINGLE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
     dim3 grid(((a.N + kBM - 1) / kBM) * a.H * a.B, D / DQ);
@@ -584,13 +586,6 @@ template <bool WIN>
 cudaError_t launch_width(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                          const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, cudaStream_t s) {
     switch (kernel_head_dim(a.D)) {
-        case 64:
-            // Windowed: a short window is ten 64-key tiles beside 4 us of a CTA's fixed cost, which a second CTA on the SM
-            // hides (B1 H32 N32768 window 512: 348 us; one CTA an SM 476; a persistent grid of such pairs 378).
-            if constexpr (WIN)
-                return launch_spec<64, 64, false, 6, true, true, 2>(a, tq, tk, tv, tdo, to, tdq, s);
-            else
-                return cudaErrorInvalidValue;  // bwd_dq_k128.cu
         case 128:
             if constexpr (!WIN) return launch_spec<128, 128, true, 8, WIN>(a, tq, tk, tv, tdo, to, tdq, s);
             return cudaErrorInvalidValue;  // win_dq.cu

@@ -537,8 +537,9 @@ int window_dq(const WinBackward &w, const DeviceState &st, cudaStream_t s) {
     BwdArgs a{w.q, w.k, w.v, w.o, w.dO, w.lse, w.delta, w.dq, nullptr, nullptr, B, Hq, Nq, D, w.scale, w.scale * log2e(), 1,
               w.grad_dtype == FA_BF16 ? 1 : 0, st.status_word, B * Hq, window_args(Hkv, Nk, w.window, w.sinks)};
     CUtensorMap tq, tk, tv, tdo, to, tdq;
-    if (encode_rows(&tq, w.q, B * Hq, Nq, Nq, D, 128) != FA_OK || encode_rows(&tk, w.k, B * Hkv, Nk, Nk, D, kDqKRows) != FA_OK ||
-        encode_rows(&tv, w.v, B * Hkv, Nk, Nk, D, kDqKRows) != FA_OK ||
+    const int k_box = kernel_head_dim(D) == 64 ? 128 : kDqKRows;
+    if (encode_rows(&tq, w.q, B * Hq, Nq, Nq, D, 128) != FA_OK || encode_rows(&tk, w.k, B * Hkv, Nk, Nk, D, k_box) != FA_OK ||
+        encode_rows(&tv, w.v, B * Hkv, Nk, Nk, D, k_box) != FA_OK ||
         encode_rows(&tdo, w.dO, B * Hq, Nq, Nq, D, 128) != FA_OK || encode_rows(&to, w.o, B * Hq, Nq, Nq, D, 128) != FA_OK ||
         encode_3d(&tdq, w.dq, B * Hq, Nq, D, 128, w.grad_dtype == FA_F32) != FA_OK)
         return FA_ERR_CUDA;

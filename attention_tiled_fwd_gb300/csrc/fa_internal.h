@@ -260,6 +260,9 @@ cudaError_t launch_bwd_dkdv(const BwdArgs &a, const CUtensorMap &tq, const CUten
 cudaError_t launch_win_dq(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                           const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, int num_sms,
                           cudaStream_t s);
+cudaError_t launch_win_dq_k128(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                          const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, int num_sms,
+                          cudaStream_t s);
 // behind: launched as the programmatic dependent of the dQ kernel before it on the stream (D <= 128)
 cudaError_t launch_win_dkdv(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                             const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv,

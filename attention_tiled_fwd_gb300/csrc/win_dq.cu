@@ -1,4 +1,5 @@
-// win_dq.cu -- dQ of windowed attention for D = 128 (other widths run bwd_dq.cu).  Per
+// win_dq.cu -- dQ of windowed attention for D = 128 (D = 64 runs win_dq_k128.cu, wider
+// heads bwd_dq.cu).  Per
 // 128-row query tile, over the key tiles that its rows see (key_span):
 //
 //   D_i = sum_d dO_id O_id (written out),
@@ -475,6 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 cudaError_t launch_win_dq(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                           const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, int num_sms,
                           cudaStream_t s) {
+    if (kernel_head_dim(a.D) == 64) return launch_win_dq_k128(a, tq, tk, tv, tdo, to, tdq, num_sms, s);
     if (kernel_head_dim(a.D) != kD) return launch_bwd_dq(a, tq, tk, tv, tdo, to, tdq, s, true);
     static std::atomic<unsigned long long> allowed{0};
     cudaError_t e = allow_smem((const void *)win_dq_kernel, WinDqSmem::kAlloc, allowed);

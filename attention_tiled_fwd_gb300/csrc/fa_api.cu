@@ -439,8 +439,8 @@ WinArgs window_args_dkdv(int B, int Hq, int Hkv, int Nq, int Nk, int D, int wind
     if (items >= 4 * num_sms) return w;
     // Few sinks at D = 64: a step of a chunk costs as much as any other (1.5 us) for 16 keys or less, so win_sinks.cu takes
     // the chunks where that saves more than it costs (a launch, and Q and dO once more from HBM), unless SMs that have
-    // nothing else to do would take them.  Both gradients at window 512: 32 heads of 32768 rows 806 us instead of 848, but
-    // 2 x 16 (4 key heads) of 4096 rows 125 instead of 112.
+    // nothing else to do would take them.  dK/dV at window 512: 32 heads of 32768 rows 464 us instead of 502, but
+    // 2 x 16 (4 key heads) of 4096 rows 79 instead of 66.
     if (kernel_head_dim(D) == 64 && w.sinks <= kFewSinks) {
         const long long idle = std::max(0ll, own * num_sms - own * B * Hkv * ((Nk + bk - 1) / bk));
         const double saved_us = 1.5 * (double)(items * rest - idle) / num_sms;

@@ -22,7 +22,8 @@
 // chunks can run in win_sinks.cu.  Bound by the compute
 // warps (TMEM in, exponentials, TMEM out twice a tile) more than by the products:
 // B2 H16/4 N4096 D128 window 1024: 146 us, 827 TFLOP/s of the visible pairs (four
-// products each); B1 H32 N32768 D64 window 512: 501 us, 545.
+// products each); B1 H32 N32768 D64 window 512: 405 us (and win_sinks.cu's 50 for one
+// sink), 590 over both.
 #include "fa_internal.h"
 #include "launch.cuh"
 #include "sm100_ptx.cuh"
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool any_mask = __any_sync(0xffffffffu, q0 < lo || q0 + kSpan > hi);
                 // None of this warp's keys is seen by any of its queries (along the edges of the band, and in the chunks behind
                 // a sink tile): P^T and dS^T are zeros.  Step of 4096 rows, window 1024, D = 128: 157 -> 146 us; no
-                // difference at D = 64 (500 us at 32768 rows and window 512), which has no registers left for it.
+                // difference at D = 64, which has no registers left for it.
                 const bool none = D == 128 && any_mask && __all_sync(0xffffffffu, q0 >= hi || q0 + kSpan <= lo);
 
                 ok = mbar_wait(&s_full[b], (t >> 1) & 1, a.status, kSiteSFull);

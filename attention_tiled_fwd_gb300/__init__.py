@@ -327,7 +327,8 @@ def fa_window_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window:
 def fa_window_backward_dq(q, k, v, o, dO, lse, window: int, sinks: int = 0, scale: Optional[float] = None,
                           grad_dtype: torch.dtype = torch.float32, dq: Optional[torch.Tensor] = None,
                           delta: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
-    """delta = rowsum(dO * O) and dQ of windowed attention (fa_window_backward_dq).  Returns (dq, delta)."""
+    """delta = rowsum(dO * O) (the first 128 positions: sum P dP) and dQ of windowed attention (fa_window_backward_dq).
+    Returns (dq, delta)."""
     B, Hq, Nq, D, Hkv, Nk = _grouped(q, k)
     dev = _device()
     rows, keys = (B, Hq, Nq, D), (B, Hkv, Nk, D)

@@ -54,6 +54,7 @@
 // one half of dQ and both computing S and dP over all of D, measured 37-42 %
 // slower: the tensor core did 5/3 of the useful products.)
 #include "fa_internal.h"
+#include "launch.cuh"
 #include "sm100_ptx.cuh"
 #include "win.cuh"
 #include <cmath>
@@ -389,7 +390,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         delta = 0.f;
 #pragma unroll
         for (int t = 0; t < kComputeWG; ++t) delta += delta_s[t * kBM + r];
-        if (valid && g == 0 && blockIdx.y == 0) a.delta[(size_t)bh * N + row] = delta;
+        if (WIN && pos0 < kExactDelta) launch_dependent_wait();  // win_delta.cu's results
+        if (WIN && valid && pos0 + r < kExactDelta)
+            delta = a.delta[(size_t)bh * N + row];
+        else if (valid && g == 0 && blockIdx.y == 0)
+            a.delta[(size_t)bh * N + row] = delta;
         // Q rows into TMEM as bf16 pairs, one 64-column panel per warpgroup (row r of a panel is 128 B at
         // r * 128, its 16-byte chunk k stored at k ^ (r % 8)).  Copying Q before summing D_i lets S_0 and dP_0
         // start earlier but measured 6 % slower per key tile over long rows, so D_i comes first.
@@ -571,26 +576,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D, int DQ, bool QT, int NSLOT, bool WIN, bool SINGLE = false>
 cudaError_t launch_spec(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                        const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, cudaStream_t s) {
+                        const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, bool behind, cudaStream_t s) {
     using L = DqSmem<D, NSLOT>;
     static_assert(L::kAlloc <= 232448, "shared memory budget");
     auto kern = bwd_dq_kernel<D, DQ, QT, NSLOT, WIN, SINGLE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
     dim3 grid(((a.N + kBM - 1) / kBM) * a.H * a.B, D / DQ);
+    if constexpr (WIN) return launch_behind(kern, grid, kThreads, L::kAlloc, behind, 1, s, tq, tk, tv, tdo, to, tdq, a);
     kern<<<grid, kThreads, L::kAlloc, s>>>(tq, tk, tv, tdo, to, tdq, a);
     return cudaGetLastError();
 }
 
 template <bool WIN>
 cudaError_t launch_width(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                         const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, cudaStream_t s) {
+                         const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, bool behind, cudaStream_t s) {
     switch (kernel_head_dim(a.D)) {
         case 128:
-            if constexpr (!WIN) return launch_spec<128, 128, true, 8, WIN>(a, tq, tk, tv, tdo, to, tdq, s);
+            if constexpr (!WIN) return launch_spec<128, 128, true, 8, WIN>(a, tq, tk, tv, tdo, to, tdq, behind, s);
             return cudaErrorInvalidValue;  // win_dq.cu
-        case 192: return launch_spec<192, 192, false, 4, WIN>(a, tq, tk, tv, tdo, to, tdq, s);  // 3, 5 slots slower
-        case 256: return launch_spec<256, 256, false, 3, WIN, true>(a, tq, tk, tv, tdo, to, tdq, s);
+        case 192: return launch_spec<192, 192, false, 4, WIN>(a, tq, tk, tv, tdo, to, tdq, behind, s);  // 3, 5 slots slower
+        case 256: return launch_spec<256, 256, false, 3, WIN, true>(a, tq, tk, tv, tdo, to, tdq, behind, s);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -599,8 +605,9 @@ cudaError_t launch_width(const BwdArgs &a, const CUtensorMap &tq, const CUtensor
 
 cudaError_t launch_bwd_dq(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                           const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, cudaStream_t s,
-                          bool win) {
-    return win ? launch_width<true>(a, tq, tk, tv, tdo, to, tdq, s) : launch_width<false>(a, tq, tk, tv, tdo, to, tdq, s);
+                          bool win, bool behind) {
+    return win ? launch_width<true>(a, tq, tk, tv, tdo, to, tdq, behind, s)
+               : launch_width<false>(a, tq, tk, tv, tdo, to, tdq, false, s);
 }
 
 }  // namespace fa

@@ -543,7 +543,10 @@ int window_dq(const WinBackward &w, const DeviceState &st, cudaStream_t s) {
         encode_rows(&tdo, w.dO, B * Hq, Nq, Nq, D, 128) != FA_OK || encode_rows(&to, w.o, B * Hq, Nq, Nq, D, 128) != FA_OK ||
         encode_3d(&tdq, w.dq, B * Hq, Nq, D, 128, w.grad_dtype == FA_F32) != FA_OK)
         return FA_ERR_CUDA;
-    return launch_win_dq(a, tq, tk, tv, tdo, to, tdq, st.num_sms, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    const bool early = Nk - Nq < kExactDelta;
+    cudaError_t e = early ? launch_win_delta(a, s) : cudaSuccess;
+    if (e == cudaSuccess) e = launch_win_dq(a, tq, tk, tv, tdo, to, tdq, st.num_sms, early, s);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 // The sink tiles' partials of dK, then of dV, in the workspace; checks that it holds them.

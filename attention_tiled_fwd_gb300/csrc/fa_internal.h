@@ -240,7 +240,7 @@ cudaError_t launch_fwd_bf16_duo(const FwdArgs &a, const CUtensorMap &tq, const C
 cudaError_t launch_bwd_dq(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk,
                           const CUtensorMap &tv, const CUtensorMap &tdo, const CUtensorMap &to,
                           const CUtensorMap &tdq, cudaStream_t s,
-                          bool win = false);
+                          bool win = false, bool behind = false);
 // bwd_dq_k128.cu: the dQ kernel for D = 64 with 128-row K / V tiles (TMA boxes of 128 rows)
 cudaError_t launch_bwd_dq_k128(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk,
                                const CUtensorMap &tv, const CUtensorMap &tdo, const CUtensorMap &to,
@@ -255,15 +255,18 @@ cudaError_t launch_bwd_dkdv(const BwdArgs &a, const CUtensorMap &tq, const CUten
                             const CUtensorMap &tv, const CUtensorMap &tdo, const CUtensorMap &tdk,
                             const CUtensorMap &tdv, cudaStream_t s,
                           const CUtensorMap *parts = nullptr);
-// Windowed (parts != null): parts[0], parts[1] are the tensor maps of the sink tiles' fp32 partials of dK and dV
-// ([part][128][D], 32-column boxes); launch_sink_sum adds them.
+// Windowed dQ.  D_i of the rows at the first kExactDelta positions comes from win_delta.cu, launched before it (behind:
+// the dQ kernel is that one's programmatic dependent).
+cudaError_t launch_win_delta(const BwdArgs &a, cudaStream_t s);
 cudaError_t launch_win_dq(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                           const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, int num_sms,
-                          cudaStream_t s);
+                          bool behind, cudaStream_t s);
 cudaError_t launch_win_dq_k128(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                           const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, int num_sms,
-                          cudaStream_t s);
-// behind: launched as the programmatic dependent of the dQ kernel before it on the stream (D <= 128)
+                          bool behind, cudaStream_t s);
+// Windowed dK/dV.  behind: launched as the programmatic dependent of the dQ kernel before it on the stream (D <= 128);
+// parts[0], parts[1] are the tensor maps of the sink tiles' fp32 partials of dK and dV
+// ([part][128][D], 32-column boxes); launch_sink_sum adds them.
 cudaError_t launch_win_dkdv(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                             const CUtensorMap &tdo, const CUtensorMap &tdk, const CUtensorMap &tdv,
                             const CUtensorMap *parts, int num_sms, bool behind, cudaStream_t s);

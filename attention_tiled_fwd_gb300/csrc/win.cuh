@@ -67,6 +67,8 @@ struct WinArgs {
     int few;  // the chunks run in win_sinks.cu instead (one sink tile of at most kFewSinks sinks, D = 64)
 };
 constexpr int kFewSinks = 16;
+// Rows at positions below this have their D_i from win_delta.cu.
+constexpr int kExactDelta = 128;
 
 // Division of 0 <= n < 2^31 by a number that the host knows: n / d = (mulhi(n, mul) + n) >> shift.
 struct FastDiv {

@@ -17,7 +17,8 @@
 // the compute warps have seen a tile's last S they copy the next tile's Q into TMEM
 // and only then write dQ, so issuer A is two key tiles ahead when they come back.
 // Bound by the chain S, dP -> compute -> dQ of its 64-key tiles: B2 H16/4 N4096 window
-// 1024: 102 us, 884 TFLOP/s of the visible pairs (three products each).
+// 1024: 105 us with win_delta.cu's kernel before it, 864 TFLOP/s of the visible pairs
+// (three products each).
 #include "fa_internal.h"
 #include "launch.cuh"
 #include "sm100_ptx.cuh"
@@ -415,7 +416,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             warp_arrive(qo_empty);  // this warp has read Q and O
             if (!(ok = all_ok(ok))) break;
             delta = delta_s[r] + delta_s[kBM + r];
-            if (valid && g == 0) a.delta[(size_t)w.bh * a.N + row] = delta;
+            if (w.pos0 < kExactDelta) launch_dependent_wait();  // win_delta.cu's results
+            if (valid && w.pos0 + r < kExactDelta)
+                delta = a.delta[(size_t)w.bh * a.N + row];
+            else if (valid && g == 0)
+                a.delta[(size_t)w.bh * a.N + row] = delta;
             const uint64_t nl2 = f2_pack(-lse2, -lse2), d2 = f2_pack(delta, delta);
             for (int j = 0; j < w.span.n; ++j, ++t) {
                 const uint32_t b = t & 1;
@@ -475,16 +480,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 cudaError_t launch_win_dq(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                           const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, int num_sms,
-                          cudaStream_t s) {
-    if (kernel_head_dim(a.D) == 64) return launch_win_dq_k128(a, tq, tk, tv, tdo, to, tdq, num_sms, s);
-    if (kernel_head_dim(a.D) != kD) return launch_bwd_dq(a, tq, tk, tv, tdo, to, tdq, s, true);
+                          bool behind, cudaStream_t s) {
+    if (kernel_head_dim(a.D) == 64) return launch_win_dq_k128(a, tq, tk, tv, tdo, to, tdq, num_sms, behind, s);
+    if (kernel_head_dim(a.D) != kD) return launch_bwd_dq(a, tq, tk, tv, tdo, to, tdq, s, true, behind);
     static std::atomic<unsigned long long> allowed{0};
     cudaError_t e = allow_smem((const void *)win_dq_kernel, WinDqSmem::kAlloc, allowed);
     if (e != cudaSuccess) return e;
     const int n_items = (a.N + kBM - 1) / kBM * a.H * a.B;
     const int sms = num_sms > 0 ? num_sms : kNumSms;
-    win_dq_kernel<<<n_items < sms ? n_items : sms, kThreads, WinDqSmem::kAlloc, s>>>(tq, tk, tv, tdo, to, tdq, a, n_items);
-    return cudaGetLastError();
+    return launch_behind(win_dq_kernel, dim3(n_items < sms ? n_items : sms), kThreads, WinDqSmem::kAlloc, behind, 1, s, tq, tk,
+                         tv, tdo, to, tdq, a, n_items);
 }
 
 }  // namespace fa

@@ -18,7 +18,7 @@
 // Sinks that fit into 32 columns are a product of 32 keys (idesc_sink), which only the
 // first warpgroup works on.
 // Bound by the chain S, dP -> compute -> dQ, a step of 128 keys in 0.9 us: B1 H32 N32768
-// window 512, 1 sink: 343 us, 600 TFLOP/s of the visible pairs (three products each);
+// window 512, 1 sink: 346 us, 592 TFLOP/s of the visible pairs (three products each);
 // B1 H8 N16384 window 2048: 113 us, 910.  bwd_dq.cu's 64-key tiles with two CTAs an SM
 // took 347 and 121 (and 24.6 instead of 26 at window 128), a persistent grid of those 378.
 #include "fa_internal.h"
@@ -445,7 +445,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             delta = 0.f;
 #pragma unroll
             for (int u = 0; u < kComputeWG; ++u) delta += sums[u * kBM + r];
-            if (valid && g == 0) a.delta[at] = delta;
+            if (pos0 < kExactDelta) launch_dependent_wait();  // win_delta.cu's results
+            if (valid && pos0 + r < kExactDelta)
+                delta = a.delta[at];
+            else if (valid && g == 0)
+                a.delta[at] = delta;
             const float lse2 = lse * 1.4426950408889634f;
             const uint64_t nl2 = f2_pack(-lse2, -lse2), d2 = f2_pack(delta, delta);
             int first = 0;
@@ -536,14 +540,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 cudaError_t launch_win_dq_k128(const BwdArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                                const CUtensorMap &tdo, const CUtensorMap &to, const CUtensorMap &tdq, int num_sms,
-                               cudaStream_t s) {
+                               bool behind, cudaStream_t s) {
     static std::atomic<unsigned long long> allowed{0};
     cudaError_t e = allow_smem((const void *)win_dq_k128_kernel, K128Smem::kAlloc, allowed);
     if (e != cudaSuccess) return e;
     const int n_items = (a.N + kBM - 1) / kBM * a.H * a.B;
     const int sms = num_sms > 0 ? num_sms : kNumSms;
-    win_dq_k128_kernel<<<n_items < sms ? n_items : sms, kThreads, K128Smem::kAlloc, s>>>(tq, tk, tv, tdo, to, tdq, a, n_items);
-    return cudaGetLastError();
+    return launch_behind(win_dq_k128_kernel, dim3(n_items < sms ? n_items : sms), kThreads, K128Smem::kAlloc, behind, 1, s, tq,
+                         tk, tv, tdo, to, tdq, a, n_items);
 }
 
 }  // namespace fa

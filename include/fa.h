@@ -246,7 +246,11 @@ FA_API int fa_window_forward(const void *q, const void *k, const void *v, void *
                              int B, int Hq, int Hkv, int Nq, int Nk, int kv_rows, int D,
                              int window, int sinks, float scale, int dtype, void *stream);
 
-/* fa_window_backward_dq -- delta = rowsum(dO * O) (written) and dQ, as fa_backward_dq. */
+/*
+ * fa_window_backward_dq -- delta = rowsum(dO * O) (written) and dQ, as fa_backward_dq.  For the rows at the first 128
+ * positions delta is computed as sum_j P dP instead, which O's rounding to bf16 does not touch: those rows see few keys,
+ * and that rounding would be a third of their gradients' error.
+ */
 FA_API int fa_window_backward_dq(const void *q, const void *k, const void *v, const void *o, const void *dO,
                                  const float *lse, float *delta, void *dq,
                                  int B, int Hq, int Hkv, int Nq, int Nk, int D, int window, int sinks,

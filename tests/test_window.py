@@ -608,3 +608,28 @@ def test_gradients_of_broadcast_and_strided_inputs():
     parts = [ref[n].abs() for n in ("dk", "dv")]
     bound = (ref["dk_bound"] + ref["dv_bound"]).sum(0, keepdim=True) + 5 * U * (parts[0] + parts[1]).sum(0, keepdim=True)
     check(dkv, (ref["dk"] + ref["dv"]).sum(0, keepdim=True), bound, "dk + dv")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [(2, 6, 2, 300, 300, 64, 40, 3), (1, 4, 4, 90, 90, 128, 500, 0), (1, 3, 1, 200, 260, 80, 33, 0),
+                                  (1, 2, 1, 130, 257, 256, 9, 140), (2, 2, 2, 150, 278, 192, 64, 1), (1, 1, 1, 1, 1, 128, 1, 0),
+                                  (2, 2, 2, 150, 277, 192, 64, 1)])
+def test_delta_of_the_first_rows_does_not_carry_o_rounding(case):
+    """Rows at positions below 128: delta = sum P dP.  P is off by 2^-11 of its value (its score and its row's LSE), the
+    rest is fp32, so delta by 2^-10 sum P |dP|; with the stored O it would be up to 2^-8 sum |dO O|."""
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    B, Hq, Hkv, Nq, Nk, D, window, sinks = case
+    g = _gen(sum(case))
+    q, k, v, dO = (_randn(g, B, h, n, D) for h, n in ((Hq, Nq), (Hkv, Nk), (Hkv, Nk), (Hq, Nq)))
+    o, lse = fa.fa_window_forward(q, k, v, window, sinks)
+    _, delta = fa.fa_window_backward_dq(q, k, v, o, dO, lse, window, sinks)
+    G, off = Hq // Hkv, Nk - Nq
+    kk, vv = (t.double().repeat_interleave(G, 1) for t in (k, v))
+    pos = torch.arange(off, Nk, device="cuda")
+    _, _, P, _ = attend(q.double(), kk, vv, visible(pos, Nk, window, sinks), 1 / math.sqrt(D))
+    dP = torch.matmul(dO.double(), vv.transpose(-1, -2))
+    early = pos < 128
+    assert early.any() == (off < 128)
+    if off < 128:
+        check(delta[:, :, early], (P * dP).sum(-1)[:, :, early], 2.0 ** -10 * (P * dP.abs()).sum(-1)[:, :, early], "delta")

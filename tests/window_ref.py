@@ -7,7 +7,7 @@ A rounding to bf16 is off by at most half a step, U = 2^-8 of the value.  With A
   less than D 2^-24 sum|q k| scale (below 2^-13 for these inputs), 2^x by 2^-22 of its value, a sum of n keys'
   products (16 at a time) by n/16 2^-24 A (below 2^-13 up to n = 32768); together below 2^-11 A.
 * LSE: the score's error, the sum's, and fp32 at magnitude below 32 (2^-20): below 2^-12.
-* delta uses the stored O: off by at most E = sum_d |dO| bound(O), plus fp32 (2^-16 sum|dO O|).
+* delta uses the stored O (but for the first 128 positions): off by at most E = sum_d |dO| bound(O), plus fp32 (2^-16 sum|dO O|).
 * dV: P as a bf16 operand, with the LSE's error in it: (U + 2^-11) sum_i P |dO|.
 * dS = P (dP - delta) is a bf16 operand, and one kernel takes the bf16 P as its factor:
   (2 U + 2^-10) |dS| + P E; dQ adds it against |k|, dK against |q|.

@@ -9,7 +9,7 @@
 // exact 1.4, which is what dS as a bf16 operand leaves).
 //
 // One CTA a query head: 128 rows x 128 keys, 8 warps of 16 rows, mma.sync (16 rows x 8 keys
-// x 16 columns) on 64-column panels in shared memory.  Bound by its latency (4-6 us, most of
+// x 16 columns) on 64-column panels in shared memory.  Bound by its latency (9 us at D = 128, most of
 // it behind the dQ kernel's start, which is launched as its dependent).
 #include "fa_internal.h"
 #include "launch.cuh"
@@ -56,13 +56,15 @@ __global__ void __launch_bounds__(kThreads) win_delta_kernel(BwdArgs a) {
         __syncthreads();  // the panel before has been read
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-            for (int x = threadIdx.x; x < kRows * 8; x += kThreads) {
-                const int r = x >> 3, c = x & 7;
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);  // columns past D, rows past the last
-                if (r < (t < 2 ? rows : keys) && c0 + 8 * c < a.D)
-                    v = *reinterpret_cast<const uint4 *>(src[t] + (size_t)r * a.D + c0 + 8 * c);
-                *reinterpret_cast<uint4 *>(tiles + t * kTile + r * 128 + ((c ^ (r & 7)) << 4)) = v;
+#pragma unroll
+            for (int i = 0; i < kRows * 8 / kThreads; ++i) {
+                const int x = threadIdx.x + i * kThreads, r = x >> 3, c = x & 7;
+                const bool in = r < (t < 2 ? rows : keys) && c0 + 8 * c < a.D;  // else zeros
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + t * kTile + r * 128 + ((c ^ (r & 7)) << 4)),
+                             "l"(src[t] + (in ? (size_t)r * a.D + c0 + 8 * c : 0)), "r"(in ? 16 : 0)
+                             : "memory");
             }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {

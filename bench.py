@@ -110,7 +110,7 @@ CSRC = "attention_tiled_fwd_gb300/csrc/"
 def kernel_sources(kernel: str, D: int, dtype: str = "bf16"):
     """The source files whose kernels run for `kernel` at head dimension D (for keying ncu figures)."""
     # fa_api.cu picks the causal work order (the head groups), which sets the DRAM traffic
-    common = [CSRC + "sm100_ptx.cuh", CSRC + "fa_internal.h", CSRC + "fa_api.cu"]
+    common = [CSRC + "sm100_ptx.cuh", CSRC + "fa_internal.h", CSRC + "win.cuh", CSRC + "fa_api.cu"]
     if kernel == "fwd":
         if dtype == "f32":
             return [CSRC + "fwd_f32.cu", CSRC + "fa_internal.h"]

@@ -61,8 +61,8 @@ struct Dkdv {
     static constexpr int kStatOff = kSlotOff + kSlots * kTileBytes;  // [kStats][L kBQ | D kBQ] fp32
     static constexpr int kBarOff = kStatOff + kStats * 2 * kBQ * 4;
     // kv_full[2], kv_empty[2], slot_full/empty[kSlots], s_full[2], dp_full[2], p_ready[2], ds_ready[2], dv_done[2],
-    // dk_done[2], stat_empty[kStats], dp_free, acc_full, acc_free, stage_full, stage_free, final, a_final
-    static constexpr int kNumBars = 4 + 2 * kSlots + 12 + kStats + 7;
+    // dk_done[2], dp_free, acc_full, acc_free, stage_full, stage_free, final, a_final
+    static constexpr int kNumBars = 4 + 2 * kSlots + 12 + 7;
     static constexpr int kTmemHolderOff = kBarOff + kNumBars * 8;
     static constexpr int kAlloc = kTmemHolderOff + 16 + 1024;
     static_assert(kAlloc <= 232448, "shared memory budget");
@@ -93,11 +93,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *s_full = slot_empty + NSLOT;
     uint64_t *dp_full = s_full + 2;             // [kDpBufs]
     uint64_t *p_ready = dp_full + 2;            // [2]
-    uint64_t *ds_ready = p_ready + 2;           // [2]
+    uint64_t *ds_ready = p_ready + 2;           // [2] (and every compute warp has read step t's L and D)
     uint64_t *dv_done = ds_ready + 2;           // [2]
     uint64_t *dk_done = dv_done + 2;            // [2]: and dV of that step (one issuer thread)
-    uint64_t *stat_empty = dk_done + 2;         // [2]: every compute warp has read step t's L and D
-    uint64_t *dp_free = stat_empty + C::kStats;  // one dP^T buffer: every compute warp has loaded it
+    uint64_t *dp_free = dk_done + 2;  // one dP^T buffer: every compute warp has loaded it
     uint64_t *acc_full = dp_free + 1;            // item n's dV and dK are complete
     uint64_t *acc_free = acc_full + 1;           // every compute warp has read them
     uint64_t *stage_full = acc_free + 1;         // every compute warp has staged its share of a gradient store
@@ -123,9 +122,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < NSLOT; ++s) {
             mbar_init(&slot_full[s], 1);
             mbar_init(&slot_empty[s], 1);
-        }
-        for (int t = 0; t < C::kStats; ++t) {
-            mbar_init(&stat_empty[t], kComputeWarps);
         }
         mbar_init(dp_free, kComputeWarps);
         mbar_init(acc_full, 1);
@@ -196,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 // the tile's L_i and D_i: lane l copies words l, l + 32, ... of [L_i | D_i] (zeros past the last row)
                 const int ss = t % C::kStats;
-                if (!(ok = warp_wait(&stat_empty[ss], (t / C::kStats & 1) ^ 1, a.status, kSiteStats))) break;
+                if (t >= 2 && !(ok = warp_wait(&ds_ready[ss], ((t - 2) >> 1) & 1, a.status, kSiteStats))) break;
                 // D comes from the dQ kernel, which may still run when this one was launched behind it
                 if (behind) launch_dependent_wait();
                 behind = false;
@@ -489,7 +485,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(&ds_ready[b]);
-                warp_arrive(&stat_empty[b]);  // this warp has read the tile's L and D
             }
             WinKeyItem nw;
             more = next_item(&nw);

@@ -55,6 +55,7 @@
 // each CTA with half of dV and dK and both computing S^T and dP^T, did 6/4 and
 // measured 15 % slower.)
 #include "fa_internal.h"
+#include "launch.cuh"
 #include "sm100_ptx.cuh"
 #include "win.cuh"
 #include <cmath>
@@ -559,7 +560,8 @@ cudaError_t launch_spec(const BwdArgs &a, const CUtensorMap &tq, const CUtensorM
     using L = DkdvSmem<D, NSLOT, STATS>;
     static_assert(L::kAlloc <= 232448, "shared memory budget");
     auto kern = bwd_dkdv_kernel<D, DO, NB, NSLOT, STATS, VK, WIN>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+    static std::atomic<unsigned long long> allowed{0};
+    cudaError_t e = allow_smem((const void *)kern, L::kAlloc, allowed);
     if (e != cudaSuccess) return e;
     dim3 grid(WIN ? ((a.win.Nk + kBN - 1) / kBN + a.win.sink_tiles * a.win.chunks) * a.win.Hkv * a.B
                   : ((a.N + kBN - 1) / kBN) * a.H * a.B,

@@ -580,7 +580,8 @@ cudaError_t launch_spec(const BwdArgs &a, const CUtensorMap &tq, const CUtensorM
     using L = DqSmem<D, NSLOT>;
     static_assert(L::kAlloc <= 232448, "shared memory budget");
     auto kern = bwd_dq_kernel<D, DQ, QT, NSLOT, WIN, SINGLE>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+    static std::atomic<unsigned long long> allowed{0};
+    cudaError_t e = allow_smem((const void *)kern, L::kAlloc, allowed);
     if (e != cudaSuccess) return e;
     dim3 grid(((a.N + kBM - 1) / kBM) * a.H * a.B, D / DQ);
     if constexpr (WIN) return launch_behind(kern, grid, kThreads, L::kAlloc, behind, 1, s, tq, tk, tv, tdo, to, tdq, a);

@@ -48,6 +48,7 @@
 // head; with PREFIX the 128 rows are packed from several sequences, every CTA
 // takes one chunk of the prefix and writes the row's partial (O, m, l).
 #include "fa_internal.h"
+#include "launch.cuh"
 #include "sm100_ptx.cuh"
 #include "win.cuh"
 #include <cmath>
@@ -472,7 +473,8 @@ cudaError_t launch_spec(const FwdArgs &a, const CUtensorMap &tq, const CUtensorM
     using L = FwdSmem<D, BN, NSLOT>;
     static_assert(L::kAlloc <= 232448, "shared memory budget");
     auto kern = fwd_bf16_kernel<D, BN, NSLOT, FwdArgs, false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+    static std::atomic<unsigned long long> allowed{0};
+    cudaError_t e = allow_smem((const void *)kern, L::kAlloc, allowed);
     if (e != cudaSuccess) return e;
     dim3 grid(((a.N + kBM - 1) / kBM) * a.H * a.B);
     kern<<<grid, kThreads, L::kAlloc, s>>>(tq, tk, tv, tk, tv, a);
@@ -484,7 +486,8 @@ cudaError_t launch_span(const SpanArgs &a, const CUtensorMap &tq, const CUtensor
                         const CUtensorMap &tks, const CUtensorMap &tvs, cudaStream_t s) {
     using L = FwdSmem<D, BN, NSLOT>;
     auto kern = fwd_bf16_kernel<D, BN, NSLOT, SpanArgs, PREFIX>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+    static std::atomic<unsigned long long> allowed{0};
+    cudaError_t e = allow_smem((const void *)kern, L::kAlloc, allowed);
     if (e != cudaSuccess) return e;
     const int grid = PREFIX ? a.parts.m_tiles * a.parts.splits * a.Hkv : ((a.Nq + kBM - 1) / kBM) * a.Hq * a.B;
     kern<<<grid, kThreads, L::kAlloc, s>>>(tq, tk, tv, tks, tvs, a);

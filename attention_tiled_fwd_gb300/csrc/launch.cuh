@@ -1,4 +1,4 @@
-// launch.cuh -- kernel launches of the windowed and shared-prefix operators.
+// launch.cuh -- launches with attributes, and the shared-memory allowance of a kernel.
 #pragma once
 #include <atomic>
 #include <cuda_runtime.h>

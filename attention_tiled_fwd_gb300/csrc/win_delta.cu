@@ -3,107 +3,134 @@
 //
 // Everywhere else D_i = sum_d dO_id O_id with the stored O, whose rounding to bf16 puts an
 // error of |dO||O| 2^-9 or so into every dS_ij / P_ij of the row.  |O| falls with the root of
-// the keys a row sees, so a short sequence's gradients, which the first rows dominate,
-// carried as much error from it as from half of dS's own rounding (dQ's error 1.6 times
-// that of an fp32 computation rounded once at N = 101, 1.55 at 227; with these rows
-// exact 1.4, which is what dS as a bf16 operand leaves).
+// the keys a row sees, and a short sequence's gradients are dominated by its first rows:
+// dQ's error was 1.6 times that of an fp32 computation rounded once at N = 101 (1.55 at
+// 227), with these rows exact it is 1.4, which is what dS as a bf16 operand leaves.
 //
-// One CTA a query head: 128 rows x 128 keys, 8 warps of 16 rows, mma.sync (16 rows x 8 keys
-// x 16 columns) on 64-column panels in shared memory.  Bound by its latency (9 us at D = 128, most of
-// it behind the dQ kernel's start, which is launched as its dependent).
+// A CTA has 32 rows of a query head and up to 128 keys: a warp has 16 rows and 32 keys, mma.sync
+// (16 rows x 8 keys x 16 columns) on 64-column panels in shared memory, two at a time.
+// Bound by its latency (6 us at D = 128; one CTA a head with 16 rows x 128 keys a warp took 9),
+// most of it behind the dQ kernel's start, which is launched as its dependent.
 #include "fa_internal.h"
 #include "launch.cuh"
 #include "sm100_ptx.cuh"
 #include "win.cuh"
+#include <algorithm>
 
 namespace fa {
 namespace {
 
-constexpr int kRows = kExactDelta;  // rows, and keys: the rows see no later key
-constexpr int kWarps = kRows / 16;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = kRows * 64 * 2;  // one 64-column panel of Q, dO, K or V
-constexpr int kAlloc = 4 * kTile;
-static_assert(kRows == 128, "eight warps, eight blocks of 16 keys");
+constexpr int kKeys = kExactDelta;  // the rows see no later key
+constexpr int kRows = 32;           // rows of a CTA
+constexpr int kThreads = 256;
+// a 64-column panel of Q, dO, K and V; two of them in shared memory at once
+constexpr int kRowTile = kRows * 128, kKeyTile = kKeys * 128, kPanel = 2 * kRowTile + 2 * kKeyTile;
+constexpr int kPanels = 2;
+constexpr int kAlloc = kPanels * kPanel;
+static_assert(kKeys == 128, "eight warps: two groups of 16 rows, four of 32 keys");
 
-__global__ void __launch_bounds__(kThreads) win_delta_kernel(BwdArgs a) {
+__global__ void __launch_bounds__(kThreads) win_delta_kernel(BwdArgs a, int parts) {
     launch_dependents();
-    extern __shared__ __align__(128) uint8_t tiles[];  // Q, dO, K, V: 16-byte chunk c of row r at c ^ (r % 8)
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int bh = blockIdx.x, kv_bh = bh / a.H * a.win.Hkv + bh % a.H / (a.H / a.win.Hkv);
+    extern __shared__ __align__(128) uint8_t tiles[];  // 16-byte chunk c of row r at c ^ (r % 8)
+    __shared__ float sums[kKeys / 32][kRows];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row_group = warp & 1, key_group = warp >> 1;
+    const int bh = blockIdx.x / parts, kv_bh = bh / a.H * a.win.Hkv + bh % a.H / (a.H / a.win.Hkv);
     const int off = a.win.Nk - a.N;  // position of row 0
-    const int rows = min(a.N, kRows - off), keys = min(a.win.Nk, kRows);
-    const __nv_bfloat16 *src[4] = {static_cast<const __nv_bfloat16 *>(a.q) + (size_t)bh * a.N * a.D,
-                                   static_cast<const __nv_bfloat16 *>(a.dO) + (size_t)bh * a.N * a.D,
-                                   static_cast<const __nv_bfloat16 *>(a.k) + (size_t)kv_bh * a.win.Nk * a.D,
-                                   static_cast<const __nv_bfloat16 *>(a.v) + (size_t)kv_bh * a.win.Nk * a.D};
+    const int row0 = blockIdx.x % parts * kRows, rows = min(min(a.N, kExactDelta - off) - row0, kRows);  // >= 1
+    const int keys = off + row0 + rows;  // the keys that the CTA's rows can see
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + ((size_t)bh * a.N + row0) * a.D;
+    const __nv_bfloat16 *dO = static_cast<const __nv_bfloat16 *>(a.dO) + ((size_t)bh * a.N + row0) * a.D;
+    const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + (size_t)kv_bh * a.win.Nk * a.D;
+    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + (size_t)kv_bh * a.win.Nk * a.D;
+    // one panel's tile; columns past D and rows past `n` are zeros
+    auto load = [&](uint32_t to, const __nv_bfloat16 *from, int tile_rows, int n, int c0) {
+        for (int x = threadIdx.x; x < tile_rows * 8; x += kThreads) {
+            const int r = x >> 3, c = x & 7;
+            const bool in = r < n && c0 + 8 * c < a.D;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + r * 128 + ((c ^ (r & 7)) << 4)),
+                         "l"(from + (in ? (size_t)r * a.D + c0 + 8 * c : 0)), "r"(in ? 16 : 0)
+                         : "memory");
+        }
+    };
     // fragments of S and dP: [16-key block][keys 0-7, 8-15]; element 2 r + e: row g + 8 r, key 2 tq + e
-    float s[kRows / 16][2][4], dp[kRows / 16][2][4];
+    float s[2][2][4], dp[2][2][4];
 #pragma unroll
-    for (int b = 0; b < kRows / 16; ++b)
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[b][h][e] = dp[b][h][e] = 0.f;
-    const int last = off + 16 * warp + 15;  // this warp's last position
     // ldmatrix addresses: lane l gives row (l % 8) of matrix l / 8.
     //   rows as A: (rows 0-7, cols 0-7), (rows 8-15, cols 0-7), (rows 0-7, cols 8-15), (rows 8-15, cols 8-15)
     //   keys as B: (keys 0-7, cols 0-7), (keys 0-7, cols 8-15), (keys 8-15, ...) x 2
     const int mi = lane >> 3, mr = lane & 7;
-    const uint32_t a_row = 16 * warp + mr + (mi & 1) * 8, a_chunk = mi >> 1, b_row = mr + (mi >> 1) * 8, b_chunk = mi & 1;
+    const uint32_t a_row = 16 * row_group + mr + (mi & 1) * 8, a_chunk = mi >> 1;
+    const uint32_t b_row = 32 * key_group + mr + (mi >> 1) * 8, b_chunk = mi & 1;
     const uint32_t base = smem_u32(tiles);
-    for (int c0 = 0; c0 < a.D; c0 += 64) {
-        __syncthreads();  // the panel before has been read
+    const bool busy = 32 * key_group < keys;  // some row sees a key of this warp's
+    for (int c0 = 0; c0 < a.D; c0 += 64 * kPanels) {
+        __syncthreads();  // the panels before have been read
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int i = 0; i < kRows * 8 / kThreads; ++i) {
-                const int x = threadIdx.x + i * kThreads, r = x >> 3, c = x & 7;
-                const bool in = r < (t < 2 ? rows : keys) && c0 + 8 * c < a.D;  // else zeros
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + t * kTile + r * 128 + ((c ^ (r & 7)) << 4)),
-                             "l"(src[t] + (in ? (size_t)r * a.D + c0 + 8 * c : 0)), "r"(in ? 16 : 0)
-                             : "memory");
-            }
+        for (int p = 0; p < kPanels; ++p) {
+            const uint32_t at = base + p * kPanel;
+            const int c = c0 + 64 * p;
+            if (c >= a.D) break;
+            load(at, q, kRows, rows, c);
+            load(at + kRowTile, dO, kRows, rows, c);
+            load(at + 2 * kRowTile, k, kKeys, keys, c);
+            load(at + 2 * kRowTile + kKeyTile, v, kKeys, keys, c);
+        }
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
+        if (!busy) continue;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            uint32_t qf[4], gf[4];
-            ldsm4(qf, base + a_row * 128 + (((2 * kk + a_chunk) ^ mr) << 4));
-            ldsm4(gf, base + kTile + a_row * 128 + (((2 * kk + a_chunk) ^ mr) << 4));
+        for (int p = 0; p < kPanels; ++p) {
+            if (c0 + 64 * p >= a.D) break;
+            const uint32_t qs = base + p * kPanel, ks = qs + 2 * kRowTile;
 #pragma unroll
-            for (int b = 0; b < kRows / 16; ++b) {
-                if (16 * b > last) continue;  // no row of this warp sees those keys
-                uint32_t kf[4], vf[4];
-                ldsm4(kf, base + 2 * kTile + (16 * b + b_row) * 128 + (((2 * kk + b_chunk) ^ mr) << 4));
-                ldsm4(vf, base + 3 * kTile + (16 * b + b_row) * 128 + (((2 * kk + b_chunk) ^ mr) << 4));
-                mma16816(s[b][0], qf, kf[0], kf[1]);
-                mma16816(s[b][1], qf, kf[2], kf[3]);
-                mma16816(dp[b][0], gf, vf[0], vf[1]);
-                mma16816(dp[b][1], gf, vf[2], vf[3]);
+            for (int kk = 0; kk < 4; ++kk) {
+                uint32_t qf[4], gf[4];
+                ldsm4(qf, qs + a_row * 128 + (((2 * kk + a_chunk) ^ mr) << 4));
+                ldsm4(gf, qs + kRowTile + a_row * 128 + (((2 * kk + a_chunk) ^ mr) << 4));
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t kf[4], vf[4];
+                    ldsm4(kf, ks + (16 * b + b_row) * 128 + (((2 * kk + b_chunk) ^ mr) << 4));
+                    ldsm4(vf, ks + kKeyTile + (16 * b + b_row) * 128 + (((2 * kk + b_chunk) ^ mr) << 4));
+                    mma16816(s[b][0], qf, kf[0], kf[1]);
+                    mma16816(s[b][1], qf, kf[2], kf[3]);
+                    mma16816(dp[b][0], gf, vf[0], vf[1]);
+                    mma16816(dp[b][1], gf, vf[2], vf[3]);
+                }
             }
         }
     }
     const int g = lane >> 2, tq = lane & 3;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        const int row = 16 * warp + g + 8 * r, p = off + row;
-        const size_t at = (size_t)bh * a.N + row;
-        const float l2 = row < rows ? a.lse[at] * 1.4426950408889634f : 0.f;
+        const int row = 16 * row_group + g + 8 * r, p = off + row0 + row;
+        const float l2 = row < rows ? a.lse[(size_t)bh * a.N + row0 + row] * 1.4426950408889634f : 0.f;
         float delta = 0.f;
 #pragma unroll
-        for (int b = 0; b < kRows / 16; ++b)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int key = 16 * b + 8 * h + 2 * tq + e;
+                    const int key = 32 * key_group + 16 * b + 8 * h + 2 * tq + e;
                     if (key <= p && (key < a.win.sinks || key > p - a.win.window))
                         delta = fmaf(ex2_approx(fmaf(s[b][h][2 * r + e], a.scale_log2, -l2)), dp[b][h][2 * r + e], delta);
                 }
         delta += __shfl_xor_sync(0xffffffffu, delta, 1);
         delta += __shfl_xor_sync(0xffffffffu, delta, 2);
-        if (row < rows && tq == 0) a.delta[at] = delta;
+        if (tq == 0) sums[key_group][row] = delta;
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < rows) {
+        float delta = 0.f;
+#pragma unroll
+        for (int x = 0; x < kKeys / 32; ++x) delta += sums[x][threadIdx.x];
+        a.delta[(size_t)bh * a.N + row0 + threadIdx.x] = delta;
     }
 }
 
@@ -113,7 +140,8 @@ cudaError_t launch_win_delta(const BwdArgs &a, cudaStream_t s) {
     static std::atomic<unsigned long long> allowed{0};
     cudaError_t e = allow_smem((const void *)win_delta_kernel, kAlloc, allowed);
     if (e != cudaSuccess) return e;
-    return launch_behind(win_delta_kernel, dim3(a.B * a.H), kThreads, kAlloc, false, 1, s, a);
+    const int rows = std::min(a.N, kExactDelta - (a.win.Nk - a.N)), parts = (rows + kRows - 1) / kRows;
+    return launch_behind(win_delta_kernel, dim3(a.B * a.H * parts), kThreads, kAlloc, false, 1, s, a, parts);
 }
 
 }  // namespace fa

@@ -17,7 +17,7 @@
 // the compute warps have seen a tile's last S they copy the next tile's Q into TMEM
 // and only then write dQ, so issuer A is two key tiles ahead when they come back.
 // Bound by the chain S, dP -> compute -> dQ of its 64-key tiles: B2 H16/4 N4096 window
-// 1024: 105 us with win_delta.cu's kernel before it, 864 TFLOP/s of the visible pairs
+// 1024: 103 us with win_delta.cu's kernel before it, 878 TFLOP/s of the visible pairs
 // (three products each).
 #include "fa_internal.h"
 #include "launch.cuh"

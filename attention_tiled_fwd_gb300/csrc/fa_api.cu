@@ -791,6 +791,11 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int n_q, int P, int N, int D, int
     return p;
 }
 
+// The prefix kernels store their partials 32 bytes at a time, and a caller's workspace is 16-byte aligned: the partials
+// begin at its first 32-byte boundary, and the size query has room for that.
+constexpr size_t kPartAlign = 32;
+size_t part_shift(const void *workspace) { return -reinterpret_cast<uintptr_t>(workspace) & (kPartAlign - 1); }
+
 int check_prefix(int B, int Hq, int Hkv, int n_q, int P, int N, int D, float scale) {
     int rc = check_rows(B, Hq, Hkv, n_q, N, D, scale);
     if (rc == FA_OK && (P < 1 || P > kMaxPositions || (long long)Hkv * P > (1ll << 31) - 1)) rc = FA_ERR_SHAPE;
@@ -803,7 +808,7 @@ extern "C" int fa_prefix_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q,
     int rc = check_prefix(B, Hq, Hkv, n_q, P, N, D, 1.f);
     if (rc != FA_OK) return rc;
     const PrefixPlan p = prefix_plan(B, Hq, Hkv, n_q, P, N, D, current_num_sms());
-    *bytes = p.bytes(Hkv, (size_t)B * Hq * n_q, D);
+    *bytes = p.bytes(Hkv, (size_t)B * Hq * n_q, D) + kPartAlign - 16;
     return FA_OK;
 }
 
@@ -822,9 +827,10 @@ extern "C" int fa_prefix_decode(const void *q, const void *k_prefix, const void 
     if (rc != FA_OK) return rc;
     const PrefixPlan p = prefix_plan(B, Hq, Hkv, n_q, P, N, D, st->num_sms);
     const size_t rows = (size_t)B * Hq * n_q;
-    if (workspace_bytes < p.bytes(Hkv, rows, D)) return FA_ERR_WORKSPACE;
+    const size_t shift = part_shift(workspace);
+    if (workspace_bytes < shift + p.bytes(Hkv, rows, D)) return FA_ERR_WORKSPACE;
     // O of the prefix's partials and of the rows' own, then (m, l) of both
-    PrefixParts parts{static_cast<float *>(workspace), nullptr, p.m_tiles, p.splits, p.R, p.rb, p.nb};
+    PrefixParts parts{reinterpret_cast<float *>(static_cast<char *>(workspace) + shift), nullptr, p.m_tiles, p.splits, p.R, p.rb, p.nb};
     float *own_o = parts.o + p.prefix_parts(Hkv) * 128 * D;
     parts.ml = reinterpret_cast<float2 *>(own_o + p.own_parts(rows) * D);
     float2 *own_ml = parts.ml + p.prefix_parts(Hkv) * 128;

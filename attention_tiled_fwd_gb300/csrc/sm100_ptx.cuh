@@ -164,7 +164,7 @@ __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontr
 // none).
 __device__ __forceinline__ void launch_dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// 32-byte store (one whole sector a lane)
+// 32-byte store (one whole sector a lane); p is 32-byte aligned
 __device__ __forceinline__ void st_global_v8(float *p, const uint32_t *r) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                  "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])

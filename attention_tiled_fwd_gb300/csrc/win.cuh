@@ -89,7 +89,7 @@ struct FastDiv {
 // the prefix.  O lies in groups of 8 columns, [key head][tile][chunk][D / 8][128 rows][8], so that the 32 rows of a warp
 // write one contiguous KB per instruction (rows of D floats each: 3900 cycles a tile instead of 1100).
 struct PrefixParts {
-    float *o;
+    float *o;                 // 32-byte aligned
     float2 *ml;               // [key head][tile][chunk][128 rows]
     int m_tiles, splits;
     int R, rb, nb;            // rows of a (sequence, key head); a tile holds rb rows of each of nb sequences

@@ -242,11 +242,18 @@ def _stream_handle(stream: Optional[torch.cuda.Stream], device: int) -> int:
     return stream.cuda_stream
 
 
+def _no_c_int(where: str) -> None:
+    """A size that the C interface's int cannot hold (ctypes would pass on its low 32 bits)."""
+    raise FAError(_native.FA_ERR_SHAPE, where)
+
+
 def _grouped(q: torch.Tensor, k: torch.Tensor):
     """Sizes (B, Hq, Nq, D, Hkv, rows of k) of grouped-head tensors."""
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError(f"q and k must have 4 dimensions, got {list(q.shape)} and {list(k.shape)}")
     (B, Hq, Nq, D), (_, Hkv, rows, _) = q.shape, k.shape
+    if (B | Hq | Nq | D | Hkv | rows) >> 31:
+        _no_c_int("a size of q or k")
     if Hkv < 1 or Hq % Hkv != 0:
         raise ValueError(f"q's {Hq} heads must be a multiple of k's {Hkv}")
     return B, Hq, Nq, D, Hkv, rows
@@ -270,6 +277,9 @@ def _empty_like(like: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torc
 
 
 def _size_query(name: str, *sizes: int) -> int:
+    for n in sizes:
+        if n >> 31:
+            _no_c_int(name)
     out = ctypes.c_size_t(0)
     _native.check(getattr(_native.load(), name)(*sizes, ctypes.byref(out)), name)
     return int(out.value)
@@ -305,6 +315,8 @@ def fa_window_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window:
     Returns (o, lse)."""
     B, Hq, Nq, D, Hkv, rows = _grouped(q, k)
     Nk = rows if kv_len is None else int(kv_len)
+    if Nk >> 31:
+        _no_c_int("kv_len")
     dev = _device()
     _bf16(q, "q", (B, Hq, Nq, D), dev)
     _bf16(k, "k", (B, Hkv, rows, D), dev)
@@ -482,10 +494,12 @@ def fa_prefix_decode(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
     """The n_q <= 16 newest rows q [B, Hq, n_q, D] of each sequence against the prefix k_prefix, v_prefix [Hkv, P, D]
     that all sequences share, and against the sequence's own cache k, v [B, Hkv, N, D] behind it, of which lens[b]
     keys are held (int32 CUDA tensor; default N) (fa_prefix_decode).  Returns (o, lse)."""
-    heads, N, D, o, lse, dev = _rows_and_cache(q, k, v, lens, o, lse, stream)
     if k_prefix.dim() != 3:
         raise ValueError(f"k_prefix must be [Hkv, P, D], got {list(k_prefix.shape)}")
     P = k_prefix.shape[1]
+    if P >> 31:
+        _no_c_int("k_prefix's length")
+    heads, N, D, o, lse, dev = _rows_and_cache(q, k, v, lens, o, lse, stream)
     _bf16(k_prefix, "k_prefix", (heads[2], P, D), dev)
     _bf16(v_prefix, "v_prefix", (heads[2], P, D), dev)
     workspace = _workspace(workspace, q, stream, dev, "fa_prefix_decode_workspace_bytes", *heads, P, N, D)

@@ -56,3 +56,39 @@ def test_prefix_workspace_at_16_mod_32(case):
     with pytest.raises(fa.FAError) as e:
         fa.fa_prefix_decode(q, kp, vp, k, v, workspace=buf[base + 16:base + need - 16])
     assert e.value.code == nat.FA_ERR_WORKSPACE
+
+
+# ------------------------------------------------------------------ sizes are C ints: a longer one must not wrap around
+def test_size_queries_refuse_what_is_no_c_int(lib):
+    import attention_tiled_fwd_gb300 as fa
+    calls = ((fa.fa_window_backward_workspace_bytes, [1, 4, 2, 8, 16, 64, 4, 1], 6),  # (window and sinks saturate)
+             (fa.fa_window_decode_workspace_bytes, [1, 4, 2, 1, 64, 64, 4, 1], 6),
+             (fa.fa_prefix_decode_workspace_bytes, [1, 4, 2, 1, 100, 64, 64], 7))
+    for call, sizes, n in calls:
+        call(*sizes)
+        for i in range(n):
+            for wrong in (sizes[i] + (1 << 32), sizes[i] - (1 << 32)):
+                with pytest.raises(fa.FAError) as e:
+                    call(*sizes[:i], wrong, *sizes[i + 1:])
+                assert e.value.code == nat.FA_ERR_SHAPE
+
+
+def test_calls_refuse_sizes_that_are_no_c_int(lib):
+    """Refused before anything else of the tensors is looked at: these have no memory."""
+    import attention_tiled_fwd_gb300 as fa
+
+    def t(*shape):
+        return torch.empty(shape, dtype=torch.bfloat16, device="meta")
+
+    q, k, kp = t(1, 4, 1, 64), t(1, 2, 16, 64), t(2, 16, 64)
+    long = (1 << 32) + 16
+    for call in (lambda: fa.fa_window_forward(q, k, k, 4, kv_len=long), lambda: fa.fa_window_forward(q, k, k, 4, kv_len=16 - (1 << 32)),
+                 lambda: fa.fa_window_forward(t(1, 4, long, 8), t(1, 2, long, 8), t(1, 2, long, 8), 4),
+                 lambda: fa.fa_window_forward(q, t(1, 2, long, 64), t(1, 2, long, 64), 4, kv_len=16),
+                 lambda: fa.window_attention(t(long, 4, 8, 8), t(long, 4, 8, 8), t(long, 4, 8, 8), 4),
+                 lambda: fa.fa_window_decode(q, t(1, 2, long, 64), t(1, 2, long, 64), 4),
+                 lambda: fa.fa_prefix_decode(q, t(2, long, 64), t(2, long, 64), k, k),
+                 lambda: fa.fa_prefix_decode(q, kp, kp, t(1, 2, long, 64), t(1, 2, long, 64))):
+        with pytest.raises(fa.FAError) as e:
+            call()
+        assert e.value.code == nat.FA_ERR_SHAPE

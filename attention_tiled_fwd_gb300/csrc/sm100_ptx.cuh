@@ -15,9 +15,6 @@ namespace fa {
 // Limit for one in-kernel wait.  Legitimate waits in these kernels last
 // microseconds; this bound only ends a kernel whose pipeline is broken.
 constexpr uint64_t kWaitLimitNs = 1500000000ull;  // 1.5 s
-// Limit for a wait that spans `steps` steps of a kernel's main loop, each a few microseconds at most: 2^17 of them are
-// a fraction of a second.
-__device__ __forceinline__ uint64_t wait_limit_of(int steps) { return kWaitLimitNs * (1 + (uint64_t)(steps >> 17)); }
 
 // Status-word layout: low 16 bits = fa_status code (negative, stored as
 // its absolute value), high 16 bits = wait-site id of the first failure.

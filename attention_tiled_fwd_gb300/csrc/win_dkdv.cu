@@ -349,8 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int y = partial ? 0 : w.k_tile * kBN, z = partial ? w.part : w.bh;
                 const int pw = out_bf16 ? 64 : 32, panels = D / pw;
                 for (int which = out_bf16 ? 1 : 0; which < 2; ++which, ++stores) {
-                    // (the item's first: a wait for all of its steps)
-                    if (!(ok = mbar_wait(stage_full, stores & 1, a.status, kSiteStage, wait_limit_of(w.n)))) break;
+                    if (!(ok = mbar_wait(stage_full, stores & 1, a.status, kSiteStage))) break;
                     const CUtensorMap *m = which ? (partial ? &tmap_pk : &tmap_dk) : (partial ? &tmap_pv : &tmap_dv);
                     for (int p = 0; p < panels && p * pw < a.D; ++p) {
                         if (out_bf16) tma_store_3d(&tmap_dv, stage + p * (kBN * 128), p * pw, y, z);

@@ -339,8 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int x = persistent_work_index(k, n_items);
                 if (x < 0) continue;
                 const WinRowItem w = win_row_item(a, x);
-                // (a wait for all of the item's steps)
-                if (!mbar_wait(stage_full, n & 1, a.status, kSiteStage, wait_limit_of(w.span.n))) break;
+                if (!mbar_wait(stage_full, n & 1, a.status, kSiteStage)) break;
                 for (int col = 0; col < a.D; col += pw)
                     tma_store_3d(&tmap_dq, smem + L::kStageOff + col / pw * (kBM * 128), col, w.row0, w.bh);
                 tma_store_commit();

@@ -92,56 +92,3 @@ def test_calls_refuse_sizes_that_are_no_c_int(lib):
         with pytest.raises(fa.FAError) as e:
             call()
         assert e.value.code == nat.FA_ERR_SHAPE
-
-
-# ------------------------------------------------------------------ waits inside a kernel are bounded by 1.5 s a step
-# The longest window: every key step takes about a microsecond, and one query tile 2^22 of them.  The head dimension is 8
-# so that the tensors stay small.  Closed forms: q is orthogonal to every key, so all scores are 0 and P_ij = 1 / (p_i + 1);
-# the first half of the keys has k = +1 in column 0 and v = 0, the second k = -1 and v = 1 in every column.
-N_LONG, ROWS = 1 << 29, 128
-
-
-def _room(gigabytes):
-    torch.cuda.empty_cache()
-    if torch.cuda.mem_get_info()[0] < gigabytes << 30:
-        pytest.skip(f"needs {gigabytes} GB of free device memory")
-
-
-def _long_window():
-    D = 8
-    k, v = (torch.zeros(1, 1, N_LONG, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
-    k[:, :, :, 0] = 1.0
-    k[:, :, N_LONG // 2:, 0] = -1.0
-    v[:, :, N_LONG // 2:] = 1.0
-    q = torch.ones(1, 1, ROWS, D, dtype=torch.bfloat16, device="cuda")
-    q[..., 0] = 0.0
-    seen = torch.arange(N_LONG - ROWS, N_LONG, dtype=torch.float64, device="cuda") + 1
-    x = (seen - N_LONG // 2) / seen  # the weight of the second half
-    o = x.to(torch.bfloat16)[None, None, :, None].expand(1, 1, ROWS, D).contiguous()
-    lse = torch.log(seen).float().reshape(1, 1, ROWS)
-    return q, k, v, o, torch.ones_like(q), lse, seen, x
-
-
-def _check_long_dq(dq, delta, x, scale):
-    # dP = 0 or 8, delta = 8 x, dS = P (dP - delta): dQ_0 = scale (-8 x (1 - x) - 8 (1 - x) x).  x is within 2^-22 of 1/2
-    # and o in bf16 is 1/2, P within 2^-11 of 2^-29 (its row's LSE in fp32): dS is +-4 P rounded to bf16, off by 2^-8 + 2^-11
-    # of its value and the same for all keys of a half.  A step's 128 equal summands are m 2^-20 with m of 8 bits, sums
-    # below 4 hold 2^-22 exactly: each of the 2^21 steps of a half is off by 2^-23 of a share of 2^-20 if m is not 1, by
-    # nothing if it is (4 P is 2^-27 up to 2^-19 of its value, and the nearest bf16 value is 2^-27 itself).  Below 2^-6.
-    want = -16 * x * (1 - x) * scale
-    assert torch.isfinite(dq).all() and not dq[..., 1:].any()
-    assert ((dq[0, 0, :, 0].double() - want).abs() <= 2.0 ** -6 * want.abs()).all()
-    assert ((delta[0, 0].double() - 8 * x).abs() <= 2.0 ** -7 * 8 * x).all()
-
-
-@pytest.mark.gpu
-def test_a_query_tile_of_the_longest_window():
-    """dQ of one query tile: its store waits for all of the tile's steps."""
-    import attention_tiled_fwd_gb300 as fa
-    cuda_or_skip()
-    _room(40)
-    q, k, v, o, dO, lse, _, x = _long_window()
-    dq = torch.full(q.shape, float("nan"), device="cuda")
-    dq, delta = fa.fa_window_backward_dq(q, k, v, o, dO, lse, N_LONG, scale=0.5, dq=dq)
-    assert fa.fa_device_status() == 0
-    _check_long_dq(dq, delta, x, 0.5)

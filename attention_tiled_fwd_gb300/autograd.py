@@ -93,6 +93,7 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: 
                      scale: Optional[float] = None) -> torch.Tensor:
     """Windowed attention, differentiable in q, k and v: q [B, Hq, Nq, D] are the last Nq positions of k, v
     [B, Hkv, Nk, D] (bf16 CUDA tensors, Hq a multiple of Hkv); a row at position p sees key j iff j <= p and
-    (j < sinks or j > p - window).  First derivatives only.  A backward pass can be captured into a CUDA graph while no
+    (j < sinks or j > p - window).  A row sees at most 2^21 keys, and at most 2^21 rows of a key head's query heads see a
+    key in their window.  First derivatives only.  A backward pass can be captured into a CUDA graph while no
     other autograd graph of the same leaves is alive (torch synchronises with that one's stream, which ends a capture)."""
     return _WindowAttention.apply(q, k, v, int(window), int(sinks), scale)

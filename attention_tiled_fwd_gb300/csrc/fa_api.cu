@@ -408,11 +408,19 @@ int check_window(int B, int Hq, int Hkv, int Nq, int Nk, int kv_rows, int D, int
     if (B > 65535 || Hq > 65535 || Hq % Hkv != 0) return FA_ERR_SHAPE;
     if (Nq > Nk || kv_rows < Nk || Nk > kMaxPositions) return FA_ERR_SHAPE;
     if (window < 1 || sinks < 0) return FA_ERR_SHAPE;
+    if (std::min<long long>(Nk, (long long)window + sinks) > kMaxSum) return FA_ERR_SHAPE;  // the keys that a row sees
     const long long max = (1ll << 31) - (1 << 20);  // an index, and a persistent grid's stride past it
     if ((long long)B * Hq * Nq > max || (long long)B * Hkv * kv_rows > max) return FA_ERR_SHAPE;
     if (!scale_ok(scale)) return FA_ERR_SCALE;
     if (!bf16_head_dim_ok(D)) return FA_ERR_HEAD_DIM;
     return FA_OK;
+}
+
+// The backward's: the rows of a group whose window holds a key.  (Those that see it as a sink are cut into chunks.)
+int check_window_grads(int B, int Hq, int Hkv, int Nq, int Nk, int D, int window, int sinks, float scale) {
+    const int rc = check_window(B, Hq, Hkv, Nq, Nk, Nk, D, window, sinks, scale);
+    if (rc != FA_OK) return rc;
+    return (long long)(Hq / Hkv) * std::min(Nq, window) > kMaxSum ? FA_ERR_SHAPE : FA_OK;
 }
 
 WinArgs window_args(int Hkv, int Nk, int window, int sinks) {
@@ -434,9 +442,11 @@ WinArgs window_args_dkdv(int B, int Hq, int Hkv, int Nq, int Nk, int D, int wind
     const long long rest = G * ((Nq - end + bq - 1) / bq);
     const long long sink_tiles = (w.sinks + bk - 1) / bk;
     const long long all = (long long)B * Hkv * ((Nk + bk - 1) / bk * own + sink_tiles * rest);
-    // four sink tiles an SM balance each other uncut, and their partials would be as large as the gradients
+    // four sink tiles an SM balance each other uncut, and their partials would be as large as the gradients (but no sum
+    // is longer than kMaxSum rows)
     const long long items = (long long)B * Hkv * sink_tiles;
-    if (items >= 4 * num_sms) return w;
+    const bool fits = (own + rest) * bq <= kMaxSum;
+    if (items >= 4 * num_sms && fits) return w;
     // Few sinks at D = 64: a step of a chunk costs as much as any other (1.5 us) for 16 keys or less, so win_sinks.cu takes
     // the chunks where that saves more than it costs (a launch, and Q and dO once more from HBM), unless SMs that have
     // nothing else to do would take them.  dK/dV at window 512: 32 heads of 32768 rows 464 us instead of 502, but
@@ -454,8 +464,9 @@ WinArgs window_args_dkdv(int B, int Hq, int Hkv, int Nq, int Nk, int D, int wind
     }
     // a chunk is as long as another item, or up to four of them when that is a quarter of an SM's share of the
     // launch or less; 16 steps at least; and the launch has four chunks an SM at most beside one a sink tile
-    const long long per = std::max({own, std::min(all / (4 * num_sms), 4 * own), 16ll, rest * items / (4 * num_sms)});
-    if (rest <= per / 2) return w;
+    const long long per = std::min<long long>(
+        std::max({own, std::min(all / (4 * num_sms), 4 * own), 16ll, rest * items / (4 * num_sms)}), kMaxSum / bq);
+    if (rest <= per / 2 && fits) return w;
     w.sink_tiles = (int)sink_tiles;
     w.chunks = (int)((rest + per - 1) / per);
     return w;
@@ -529,7 +540,7 @@ struct WinBackward {
 
 int check_window_backward(const WinBackward &w, int dtype) {
     if (dtype != FA_BF16 || (w.grad_dtype != FA_BF16 && w.grad_dtype != FA_F32)) return FA_ERR_DTYPE;
-    return check_window(w.B, w.Hq, w.Hkv, w.Nq, w.Nk, w.Nk, w.D, w.window, w.sinks, w.scale);
+    return check_window_grads(w.B, w.Hq, w.Hkv, w.Nq, w.Nk, w.D, w.window, w.sinks, w.scale);
 }
 
 int window_dq(const WinBackward &w, const DeviceState &st, cudaStream_t s) {
@@ -606,7 +617,7 @@ extern "C" int fa_window_backward_dq(const void *q, const void *k, const void *v
 extern "C" int fa_window_backward_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int D, int window, int sinks,
                                                   size_t *bytes) {
     if (!bytes) return FA_ERR_NULL;
-    int rc = check_window(B, Hq, Hkv, Nq, Nk, Nk, D, window, sinks, 1.f);
+    int rc = check_window_grads(B, Hq, Hkv, Nq, Nk, D, window, sinks, 1.f);
     if (rc != FA_OK) return rc;
     *bytes = 2 * sizeof(float) *
              sink_part_floats(window_args_dkdv(B, Hq, Hkv, Nq, Nk, D, window, sinks, current_num_sms()), B, D);

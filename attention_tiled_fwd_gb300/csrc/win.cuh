@@ -15,6 +15,12 @@ namespace fa {
 // then stay inside 32 bits.
 constexpr int kMaxPositions = 1 << 29;
 
+// The most products that one accumulator adds up.  The tensor cores align a sum's addends and drop what lies 2^-25 and
+// more below it, so n products of one sign and about the same size lose n 2^-27 of their sum, up to n 2^-26 (measured, O of
+// one row and dV of one key: 0.8 % at 2^20, 1.4 % at 2^21, 5 % at 2^23; at 2^25 the sum stops growing).  Up to here
+// that is within the 2e-2 that the bf16 results are held to.
+constexpr int kMaxSum = 1 << 21;
+
 // The key tiles (bn keys each) that positions p0 .. p1 read: n_sink tiles from key 0 on, then tiles from
 // key lo on, n in all.  A window tile starts at the first key that p0 sees rather than at a multiple of
 // bn, so a tile of 128 rows reads window + 127 keys and not up to bn - 1 more.  Where the window reaches the

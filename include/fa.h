@@ -237,7 +237,9 @@ FA_API int fa_decode_noalloc(const void *q, const void *k, const void *v, void *
  * hold anything in the forward; every other element must be finite (a masked weight is an exact 0, and 0 times a
  * non-finite value is NaN).
  * Supported: dtype FA_BF16, D a multiple of 8 in [8, 256]; Nk <= 2^29; scale > 0 and scale log2(e) finite
- * (FA_ERR_SCALE); less than 2^31 - 2^20 rows in a tensor.
+ * (FA_ERR_SCALE); less than 2^31 - 2^20 rows in a tensor; at most 2^21 keys that a row sees (min(Nk, window + sinks)) and,
+ * in the backward, at most 2^21 rows of a group that see a key in their window ((Hq / Hkv) min(Nq, window)): the tensor
+ * cores' sums drop what lies 2^-25 below them, which costs n products of one sign and size n 2^-27 of their sum, 1.4 % there.
  * Sizes outside these, Nq > Nk, window < 1, sinks < 0: FA_ERR_SHAPE.
  */
 

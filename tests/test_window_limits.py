@@ -92,3 +92,66 @@ def test_calls_refuse_sizes_that_are_no_c_int(lib):
         with pytest.raises(fa.FAError) as e:
             call()
         assert e.value.code == nat.FA_ERR_SHAPE
+
+
+# ------------------------------------------------------------------ no accumulator sums more than 2^21 products
+MOST = 1 << 21
+A = 4096  # a fake address: what passes the checks of sizes is refused as no device memory
+
+
+def _statuses(lib, B, Hq, Hkv, Nq, Nk, D, window, sinks):
+    """The forward's, dQ's, dK/dV's, the whole backward's and the size query's."""
+    s, m = (B, Hq, Hkv, Nq, Nk), (D, window, sinks, 0.1, nat.FA_BF16)
+    out = ctypes.c_size_t(0)
+    return (lib.fa_window_forward(A, A, A, A, A, *s, Nk, *m, None),
+            lib.fa_window_backward_dq(A, A, A, A, A, A, A, A, *s, *m, nat.FA_F32, None),
+            lib.fa_window_backward_dkdv(A, A, A, A, A, A, A, A, *s, *m, nat.FA_F32, A, 1 << 40, None),
+            lib.fa_window_backward(A, A, A, A, A, A, A, A, A, A, *s, *m, nat.FA_F32, A, 1 << 40, None),
+            lib.fa_window_backward_workspace_bytes(*s, D, window, sinks, ctypes.byref(out)))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_sums_that_are_too_long_are_refused(lib, D):
+    bad, passed = nat.FA_ERR_SHAPE, nat.FA_ERR_DEVICE_PTR
+    # keys that a row sees
+    assert _statuses(lib, 1, 1, 1, 128, MOST + 1, D, MOST + 1, 0) == (bad,) * 5
+    assert _statuses(lib, 1, 1, 1, 128, 1 << 29, D, MOST - 3, 4) == (bad,) * 5
+    assert _statuses(lib, 1, 1, 1, 128, 1 << 29, D, 4, (1 << 31) - 1) == (bad,) * 5
+    assert _statuses(lib, 1, 1, 1, 128, 1 << 29, D, MOST - 4, 4) == (passed,) * 4 + (nat.FA_OK,)
+    assert _statuses(lib, 1, 1, 1, 128, MOST, D, (1 << 31) - 1, 0) == (passed,) * 4 + (nat.FA_OK,)
+    # rows of a group that see a key in their window
+    assert _statuses(lib, 1, 16, 2, MOST // 8 + 1, MOST // 8 + 1, D, MOST // 8 + 1, 0) == (passed,) + (bad,) * 4
+    assert _statuses(lib, 1, 16, 2, MOST // 8, MOST // 8, D, MOST, 0) == (passed,) * 4 + (nat.FA_OK,)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,N,window,sinks", [(128, 8, 1, 1 << 22, 1 << 17, 4), (64, 8, 1, 1 << 22, 1 << 17, 40),
+                                                     (256, 4, 2, 1 << 23, 1 << 18, 1), (256, 64, 1, 1 << 17, 64, 1 << 17)])
+def test_rows_behind_the_sinks_are_cut_to_what_a_sum_holds(lib, D, Hq, Hkv, N, window, sinks):
+    # partials: 1 + chunks of 128 x D floats for dK and dV of every sink tile; a chunk has 2^21 rows at most
+    out = ctypes.c_size_t(0)
+    assert lib.fa_window_backward_workspace_bytes(1, Hq, Hkv, N, N, D, window, sinks, ctypes.byref(out)) == nat.FA_OK
+    rest = Hq // Hkv * (N - 127 - window)
+    tiles = -(-sinks // 128)
+    chunks = out.value // (8 * 128 * D * Hkv * tiles) - 1
+    assert chunks * MOST >= rest
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_row_that_sees_the_most_keys(D):
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(D)
+    q = torch.zeros(1, 1, 3, D, dtype=torch.bfloat16, device="cuda")  # all scores are 0: O is the mean of v
+    k, v = _randn(g, 1, 1, MOST, D), (0.3 * torch.randn(1, 1, MOST, D, generator=g, device="cuda") + 1).bfloat16()
+    want = (v[0, 0].double().sum(0, keepdim=True) - torch.cat((v[0, 0, -2:].double().flip(0).cumsum(0).flip(0),
+                                                                torch.zeros(1, D, dtype=torch.float64, device="cuda"))))
+    seen = torch.arange(MOST - 2, MOST + 1, dtype=torch.float64, device="cuda")
+    want /= seen[:, None]
+    o, lse = fa.fa_window_forward(q, k, v, MOST)
+    assert fa.fa_device_status() == 0
+    # each of 2^21 addends loses less than 2^-25 of the sum so far, half of the final one on average: 2^-5 of the mean of
+    # |v| (below 1.1), beside the roundings of P (exact here) and O (2^-8)
+    assert ((o[0, 0].double() - want).abs() <= 1.1 * 2.0 ** -5 + 2.0 ** -8 * want).all()
+    assert ((lse[0, 0].double() - torch.log(seen)).abs() <= 2.0 ** -12).all()

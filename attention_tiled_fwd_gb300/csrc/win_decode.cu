@@ -484,6 +484,8 @@ int win_decode_splits(int B, int Hkv, int R, int tiles, int D, int num_sms) {
     const long long slots = (long long)(num_sms > 0 ? num_sms : kNumSms) * ctas_per_sm(D);
     long long sp = slots / units;
     if (sp > (tiles + 1) / 2) sp = (tiles + 1) / 2;
+    const long long least = ((long long)tiles * (kKeys / kWarps) + kMaxSum - 1) / kMaxSum;  // a warp adds up 16 keys of a tile
+    if (sp < least) sp = least;
     if (sp < 1) sp = 1;
     return (int)sp;
 }

@@ -155,3 +155,12 @@ def test_a_row_that_sees_the_most_keys(D):
     # |v| (below 1.1), beside the roundings of P (exact here) and O (2^-8)
     assert ((o[0, 0].double() - want).abs() <= 1.1 * 2.0 ** -5 + 2.0 ** -8 * want).all()
     assert ((lse[0, 0].double() - torch.log(seen)).abs() <= 2.0 ** -12).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_token_splits_of_many_rows_and_long_caches(lib, D):
+    # 128 heads of 16 rows on one key head fill the GPU with few splits; a warp adds up a quarter of a split's keys
+    out = ctypes.c_size_t(0)
+    rows, N = 128 * 16, 1 << 28
+    assert lib.fa_window_decode_workspace_bytes(1, 128, 1, 16, N, D, N, 0, ctypes.byref(out)) == nat.FA_OK
+    assert out.value // (rows * (D * 4 + 8)) * 4 * MOST >= N

@@ -780,13 +780,14 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int n_q, int P, int N, int D, int
     const double tile_us = Dk == 64 ? 1.4 : Dk == 128 ? 1.7 : 1.0;
     const double own_kb = (double)B * Hkv * N * D * 2 / 1000;
     double best = 1e300;
+    const int most = std::min(tiles, kMaxSum / bn), least = (tiles + most - 1) / most;  // a chunk's sums stay within kMaxSum
     for (int left = 0; left <= num_sms / 3; left += 8) {
         const int ctas = p.fused ? num_sms - own_sms : num_sms - left;
-        for (int c = tiles; c >= 1; --c) {  // s chunks of c tiles, each s that a chunk size gives once, with the smallest
+        for (int c = most; c >= 1; --c) {  // s chunks of c tiles, each s that a chunk size gives once, with the smallest
             const int s = (tiles + c - 1) / c;
             c = (tiles + s - 1) / s;
-            if (s > 1 && (long long)units * s > 4ll * ctas) break;
-            const double prefix_us = (double)((units * s + ctas - 1) / ctas) * (c + 3) * tile_us;
+            if (s > least && (long long)units * s > 4ll * ctas) break;
+            const double prefix_us = (double)(((long long)units * s + ctas - 1) / ctas) * (c + 3) * tile_us;
             const double rest = own_kb - std::min(own_kb, left * 80.0 * prefix_us);
             const double us = p.fused ? prefix_us : prefix_us + rest / 6500;
             if (us < best) {

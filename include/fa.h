@@ -291,7 +291,8 @@ FA_API int fa_window_backward_workspace_bytes(int B, int Hq, int Hkv, int Nq, in
  *   are taken as the nearer end; NULL: every sequence holds N.  Row i sits at position lens[b] - n_q + i and sees
  *   what the mask above gives; a row that sees nothing (a position below 0) gets O = 0 and LSE = -inf.  Cache
  *   rows from lens[b] on may hold anything.
- *   D in {64, 128, 256}; n_q <= N.  Other conditions as for windowed attention.
+ *   D in {64, 128, 256}; n_q <= N.  Other conditions as for windowed attention, but a row may see any number of keys
+ *   (they are split over sums of 2^21 at most).
  *   workspace: as fa_decode's, of fa_window_decode_workspace_bytes(...) bytes (NULL when that is 0).
  * Launches one kernel, and a second when the keys of a sequence are split over more CTAs than a cluster holds.
  */
@@ -307,7 +308,7 @@ FA_API int fa_window_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q, int
  *   k_prefix, v_prefix: [Hkv, P, D]; q, o, lse, lens and k, v (the sequences' own caches behind the prefix) as for
  *   fa_window_decode.  Row i of sequence b sees every prefix key, and key j of its own cache iff
  *   j <= lens[b] - n_q + i.  lens[b] may be 0.
- *   P >= 1, N >= 1, D in {64, 128, 256}, 1 <= n_q <= 16, scale as for windowed attention.
+ *   1 <= P <= 2^29, N as there, D in {64, 128, 256}, 1 <= n_q <= 16, scale as for windowed attention.
  *   workspace: fa_prefix_decode_workspace_bytes(...) bytes, 16-byte aligned; two calls that run concurrently must
  *   not share it.
  */

@@ -164,3 +164,42 @@ def test_token_splits_of_many_rows_and_long_caches(lib, D):
     rows, N = 128 * 16, 1 << 28
     assert lib.fa_window_decode_workspace_bytes(1, 128, 1, 16, N, D, N, 0, ctypes.byref(out)) == nat.FA_OK
     assert out.value // (rows * (D * 4 + 8)) * 4 * MOST >= N
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prefix_chunks_of_a_long_prefix(lib, D):
+    # 65535 rows of one key head fill the GPU uncut: 512 tiles of 128 rows, whose partials need D floats, m and l a chunk
+    out = ctypes.c_size_t(0)
+    P = 1 << 29
+    assert lib.fa_prefix_decode_workspace_bytes(65535, 1, 1, 1, P, 1, D, ctypes.byref(out)) == nat.FA_OK
+    assert out.value >= P // MOST * 512 * 128 * (D * 4 + 8)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows_behind_a_long_prefix(D):
+    """Scores of 0: O is the mean of v over the prefix and the own key, chunk by chunk within a sum of 2^21 keys."""
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    _room(30)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(D)
+    B, P = 40000, 4 * MOST + 77
+    q = torch.zeros(B, 1, 1, D, dtype=torch.bfloat16, device="cuda")
+    kp, vp = torch.zeros(1, P, D, dtype=torch.bfloat16, device="cuda"), torch.empty(1, P, D, dtype=torch.bfloat16, device="cuda")
+    for c in range(0, P, MOST):
+        vp[:, c:c + MOST] = (0.3 * torch.randn(1, min(MOST, P - c), D, generator=g, device="cuda") + 1).bfloat16()
+    k, v = _randn(g, B, 1, 1, D), _randn(g, B, 1, 1, D)
+    total = sum(vp[0, c:c + MOST].double().sum(0) for c in range(0, P, MOST))
+    want = (total + v[:, 0, 0].double()) / (P + 1)
+    o, lse = fa.fa_prefix_decode(q, kp, vp, k, v)
+    assert fa.fa_device_status() == 0
+    # as for a row that sees the most keys: 2^-5 of the mean of |v| (below 1.1), and O's rounding
+    assert ((o[:, 0, 0].double() - want).abs() <= 1.1 * 2.0 ** -5 + 2.0 ** -8 * want.abs()).all()
+    assert ((lse.double() - torch.log(torch.tensor(P + 1.0, dtype=torch.float64))).abs() <= 2.0 ** -12).all()
+
+
+def _room(gigabytes):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gigabytes << 30:
+        pytest.skip(f"needs {gigabytes} GB of free device memory")

@@ -45,17 +45,17 @@ struct SpanSmem {
     static constexpr int kPanels = D / 64;
     static constexpr int kQBytes = kBM * D * 2;    // one query tile
     static constexpr int kSlotBytes = kBN * D * 2;  // one K or V tile
-    // one tile a CTA: the next block's Q has a buffer of its own (D = 64), O is staged 64 columns at a time
+    // one tile a CTA (windowed): the next block's Q has a buffer of its own (D = 64), O is staged 64 columns at a time
     static constexpr int kQBufs = kTiles == 1 && D == 64 ? 2 : 1;
-    static constexpr int kStageCols = kTiles == 1 ? 64 : D;
+    static constexpr int kStageCols = kTiles == 1 ? 64 : 0;
     static constexpr int kThreads = 32 * kFirstSoftmaxWarp + 128 * kTiles;
     static constexpr int kQOff = 0;
     static constexpr int kSlotOff = kQBufs * kTiles * kQBytes;
-    static constexpr int kStageOff = kSlotOff + NSLOT * kSlotBytes;  // one query tile's O, staged for TMA stores
+    static constexpr int kStageOff = kSlotOff + NSLOT * kSlotBytes;  // 64 columns of O, staged for TMA stores
     static constexpr int kBarOff = kStageOff + kBM * kStageCols * 2;
-    // q_full[2], q_empty[2], slot_full[NSLOT], slot_empty[NSLOT], per tile: s_full, p_full, pv_done, o_free,
-    // stage_full; final, stage_free, s_free; block_full[kBlocks], block_empty[kBlocks]
-    static constexpr int kNumBars = 4 + 2 * NSLOT + 5 * kTiles + 3 + 2 * kBlocks;
+    // q_full[2], q_empty[2], slot_full[NSLOT], slot_empty[NSLOT], per tile: s_full, p_full, pv_done, o_free; final,
+    // stage_full, stage_free, s_free; block_full[kBlocks], block_empty[kBlocks]
+    static constexpr int kNumBars = 4 + 2 * NSLOT + 4 * kTiles + 4 + 2 * kBlocks;
     static constexpr int kTmemHolderOff = kBarOff + kNumBars * 8;
     static constexpr int kBlockOff = (kTmemHolderOff + 16 + 15) / 16 * 16;  // SoftBlock [kBlocks][kTiles], 16-byte aligned
     static_assert(kBlockOff % 16 == 0 && kBarOff % 16 == 0, "vector accesses");
@@ -133,7 +133,7 @@ __device__ __forceinline__ int tile_cols(const SpanArgs &a, int n_sink, int j) {
 struct __align__(16) SoftBlock {
     int n;             // key tiles that the query tile reads (-1: no more blocks)
     int n_sink, key0;  // the first n_sink are sink tiles; the next starts at key key0
-    int use;           // uses of the staging buffer before this tile's epilogue
+    int use;           // windowed: blocks of this CTA before this one, each with an epilogue through the staging buffer
     int zq, yq, p0, kv_bh;
 };
 static_assert(sizeof(SoftBlock) == 32, "two 16-byte loads");
@@ -187,11 +187,10 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
     uint64_t *pv_done = p_full + kTiles;    // [tile]: PV_X of step g complete
     uint64_t *o_free = pv_done + kTiles;    // [tile]: the epilogue has read O_X (phase = X's blocks with work)
     uint64_t *final_bar = o_free + kTiles;  // every MMA of the CTA has completed
-    // The epilogue of a query tile writes O into the one staging buffer and stores it by TMA.  Within a
-    // block tile A uses the buffer before tile B, so every role can count the uses from the blocks:
-    uint64_t *stage_full = final_bar + 1;      // [tile]: the tile's four warps have written the buffer
-    uint64_t *stage_free = stage_full + kTiles;  // the last store has finished reading it (phase = use)
-    uint64_t *s_free = stage_free + 1;              // kOwnP: the softmax has loaded S of step g
+    // Windowed: a block's epilogue writes O into the one staging buffer, 64 columns at a time, and stores it by TMA.
+    uint64_t *stage_full = final_bar + 1;   // the four softmax warps have written the buffer
+    uint64_t *stage_free = stage_full + 1;  // the store before has finished reading it
+    uint64_t *s_free = stage_free + 1;      // kOwnP: the softmax has loaded S of step g
     uint64_t *block_full = s_free + 1;              // [kBlocks]
     uint64_t *block_empty = block_full + kBlocks;   // [kBlocks]: every softmax warp has read it
     SoftBlock *soft_blocks = reinterpret_cast<SoftBlock *>(smem + L::kBlockOff);
@@ -217,7 +216,7 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
             mbar_init(&o_free[x], 4);
         }
         mbar_init(final_bar, 1);
-        for (int x = 0; x < kTiles; ++x) mbar_init(&stage_full[x], 4);
+        mbar_init(stage_full, 4);
         mbar_init(stage_free, 1);
         mbar_init(s_free, 4);
         for (int b = 0; b < kBlocks; ++b) {
@@ -247,7 +246,6 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
             for (int s = 0; s < NSLOT; ++s) last_round[s] = -1;
             int gidx = 0;  // K/V loads so far (ring position)
             int nb = 0;    // blocks so far
-            int uses = 0;  // uses of the staging buffer so far
             bool ok = true;
             auto publish = [&](const SoftBlock *sb) {  // block nb (or the end) for the softmax warps
                 const int e = nb % kBlocks;
@@ -264,9 +262,7 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
                 SoftBlock sb[kTiles];
 #pragma unroll
                 for (int x = 0; x < kTiles; ++x)
-                    sb[x] = SoftBlock{w.n[x], w.span.n_sink, w.y_off + w.span.lo, uses + (x == 1 && w.n[0] > 0), w.zq[x], w.yq[x], w.p0[x], w.kv_bh};
-#pragma unroll
-                for (int x = 0; x < kTiles; ++x) uses += w.n[x] > 0;
+                    sb[x] = SoftBlock{w.n[x], w.span.n_sink, w.y_off + w.span.lo, nb, w.zq[x], w.yq[x], w.p0[x], w.kv_bh};
                 if (!(ok = publish(sb))) break;
                 // Q of this block goes after its first K and V tiles: its buffer frees only when the
                 // previous block's last S products complete, and K_0 / V_0 need not wait for that
@@ -463,7 +459,7 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
         const float c = a.scale_log2;
         bool ok = true;
         int step0 = 0;     // steps of this tile before the current block
-        int stores = 0;    // stores of this tile's O so far (phase of stage_full[x])
+        int stores = 0;    // windowed: stores of O so far (phase of stage_full)
         for (int k = 0; ok; ++k) {
             const int e = k % kBlocks;
             ok = mbar_wait(&block_full[e], (k / kBlocks) & 1, a.status, kSiteBlock);
@@ -616,7 +612,6 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
                 tc_fence_before();
                 warp_arrive(&p_full[x]);
             }
-            // the staging buffer's use number of this tile's epilogue in this block (tile A's before tile B's)
             if (!ok || n == 0) continue;
             // the block's last PV_X has completed: O_X is final
             step0 += n;
@@ -642,66 +637,62 @@ __global__ void __launch_bounds__(32 * kFirstSoftmaxWarp + 128 * kTiles, kCtas)
                 }
                 // every score a NaN: m stays -inf, which would read as "sees nothing"
                 a.parts.ml[part * kBM + r] = make_float2(l != l ? fmaxf(m, 0.f) : m, l);
-                continue;
-            }
-            const float inv_l = 1.f / l;
-            if (yq + r < a.Nq) a.lse[(size_t)zq * a.Nq + yq + r] = (m + __log2f(l)) * 0.69314718055994531f;
-            // O / l as bf16 through the staging buffer, kStageCols columns at a time: 128-byte-swizzled panels of 64
-            // columns, row r of panel p at p * 16 KB + r * 128, its 16-byte chunk k at k ^ (r % 8) (conflict-free
-            // across the lanes)
-            constexpr int kParts = D / L::kStageCols, kPartPanels = L::kStageCols / 64;
-            const bool storer = quarter == kFirstSoftmaxWarp % 4 && lane == 0;  // one thread of the tile stores
+            } else {
+                const float inv_l = 1.f / l;
+                if (yq + r < a.Nq) a.lse[(size_t)zq * a.Nq + yq + r] = (m + __log2f(l)) * 0.69314718055994531f;
+                // O / l as bf16 through the staging buffer, kStageCols columns at a time: 128-byte-swizzled panels of 64
+                // columns, row r of panel p at p * 16 KB + r * 128, its 16-byte chunk k at k ^ (r % 8) (conflict-free
+                // across the lanes)
+                constexpr int kParts = D / L::kStageCols, kPartPanels = L::kStageCols / 64;
+                const bool storer = quarter == kFirstSoftmaxWarp % 4 && lane == 0;  // one thread stores
 #pragma unroll
-            for (int part = 0; part < kParts; ++part) {
-                const int use = w.use * kParts + part;
-                // the previous use's TMA store has finished reading the buffer (one tile a CTA: the thread that issued
-                // that store waits for it only here)
-                if (kTiles == 1 && use >= 1 && storer) {
-                    tma_store_wait_read();
-                    mbar_arrive(stage_free);
+                for (int part = 0; part < kParts; ++part) {
+                    const int use = w.use * kParts + part;
+                    // the previous use's TMA store has finished reading the buffer (the thread that issued it waits for it
+                    // only here)
+                    if (use >= 1 && storer) {
+                        tma_store_wait_read();
+                        mbar_arrive(stage_free);
+                    }
+                    if (use >= 1) ok = mbar_wait(stage_free, (use - 1) & 1, a.status, kSiteStage);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+#pragma unroll
+                    for (int ch = 0; ch < L::kStageCols / 32; ++ch) {
+                        tmem_ld32(tmem + lane_base + o_col + part * L::kStageCols + ch * 32, ov);
+                        tmem_wait_ld();
+                        if (part == kParts - 1 && ch == L::kStageCols / 32 - 1) {
+                            // every read of O_X is done: the next block's first PV_X may overwrite it
+                            tc_fence_before();
+                            warp_arrive(&o_free[x]);
+                        }
+                        uint8_t *prow = stage + (ch >> 1) * (kBM * 128) + r * 128;
+#pragma unroll
+                        for (int v4 = 0; v4 < 4; ++v4)
+                            st_shared_v4(prow + ((((ch & 1) * 4 + v4) ^ (r & 7)) << 4),
+                                         pack_bf16x2(__uint_as_float(ov[v4 * 8 + 0]) * inv_l, __uint_as_float(ov[v4 * 8 + 1]) * inv_l),
+                                         pack_bf16x2(__uint_as_float(ov[v4 * 8 + 2]) * inv_l, __uint_as_float(ov[v4 * 8 + 3]) * inv_l),
+                                         pack_bf16x2(__uint_as_float(ov[v4 * 8 + 4]) * inv_l, __uint_as_float(ov[v4 * 8 + 5]) * inv_l),
+                                         pack_bf16x2(__uint_as_float(ov[v4 * 8 + 6]) * inv_l, __uint_as_float(ov[v4 * 8 + 7]) * inv_l));
+                    }
+                    fence_proxy_async_smem();  // the staged tile is read by the TMA (async proxy)
+                    warp_arrive(stage_full);
+                    if (storer) {
+                        // rows past Nq and columns past the caller's D are clipped by the tensor map
+                        if (mbar_wait(stage_full, stores & 1, a.status, kSiteStage)) {
+#pragma unroll
+                            for (int p = 0; p < kPartPanels; ++p) {
+                                const int col = part * L::kStageCols + p * 64;
+                                if (col < a.D) tma_store_3d(&tmap_o, stage + p * (kBM * 128), col, yq, zq);
+                            }
+                            tma_store_commit();
+                        } else {
+                            ok = false;
+                        }
+                    }
+                    ++stores;
                 }
-                if (use >= 1) ok = mbar_wait(stage_free, (use - 1) & 1, a.status, kSiteStage);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-#pragma unroll
-                for (int ch = 0; ch < L::kStageCols / 32; ++ch) {
-                    tmem_ld32(tmem + lane_base + o_col + part * L::kStageCols + ch * 32, ov);
-                    tmem_wait_ld();
-                    if (part == kParts - 1 && ch == L::kStageCols / 32 - 1) {
-                        // every read of O_X is done: the next block's first PV_X may overwrite it
-                        tc_fence_before();
-                        warp_arrive(&o_free[x]);
-                    }
-                    uint8_t *prow = stage + (ch >> 1) * (kBM * 128) + r * 128;
-#pragma unroll
-                    for (int v4 = 0; v4 < 4; ++v4)
-                        st_shared_v4(prow + ((((ch & 1) * 4 + v4) ^ (r & 7)) << 4),
-                                     pack_bf16x2(__uint_as_float(ov[v4 * 8 + 0]) * inv_l, __uint_as_float(ov[v4 * 8 + 1]) * inv_l),
-                                     pack_bf16x2(__uint_as_float(ov[v4 * 8 + 2]) * inv_l, __uint_as_float(ov[v4 * 8 + 3]) * inv_l),
-                                     pack_bf16x2(__uint_as_float(ov[v4 * 8 + 4]) * inv_l, __uint_as_float(ov[v4 * 8 + 5]) * inv_l),
-                                     pack_bf16x2(__uint_as_float(ov[v4 * 8 + 6]) * inv_l, __uint_as_float(ov[v4 * 8 + 7]) * inv_l));
-                }
-                fence_proxy_async_smem();  // the staged tile is read by the TMA (async proxy)
-                warp_arrive(&stage_full[x]);
-                if (storer) {
-                    // rows past Nq and columns past the caller's D are clipped by the tensor map
-                    if (mbar_wait(&stage_full[x], stores & 1, a.status, kSiteStage)) {
-#pragma unroll
-                        for (int p = 0; p < kPartPanels; ++p) {
-                            const int col = part * L::kStageCols + p * 64;
-                            if (col < a.D) tma_store_3d(&tmap_o, stage + p * (kBM * 128), col, yq, zq);
-                        }
-                        tma_store_commit();
-                        if (kTiles == 2) {
-                            tma_store_wait_read();
-                            mbar_arrive(stage_free);
-                        }
-                    } else {
-                        ok = false;
-                    }
-                }
-                ++stores;
             }
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         }
         tma_store_wait_read();  // the CTA's shared memory must outlive the stores' reads
     }

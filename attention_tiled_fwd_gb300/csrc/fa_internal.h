@@ -109,6 +109,24 @@ struct BwdArgs {
 };
 
 #ifdef __CUDACC__
+// Query tile x (bm rows) of the windowed dQ kernels and its key tiles (bn keys), in longest-first order: the last rows of
+// every head first.
+struct WinRowItem {
+    int bh, kv_bh, row0, pos0;
+    KeySpan span;
+};
+
+__device__ __forceinline__ WinRowItem win_row_item(const BwdArgs &a, int x, int bm, int bn) {
+    const int n_bh = a.B * a.H;
+    WinRowItem w;
+    w.bh = x % n_bh;
+    w.row0 = ((a.N + bm - 1) / bm - 1 - x / n_bh) * bm;
+    w.kv_bh = w.bh / a.H * a.win.Hkv + w.bh % a.H / (a.H / a.win.Hkv);
+    w.pos0 = a.win.Nk - a.N + w.row0;
+    w.span = key_span(w.pos0, min(a.win.Nk, w.pos0 + bm) - 1, a.win.window, a.win.sinks, bn);
+    return w;
+}
+
 // The query rows of windowed attention that keys k0 .. k0 + bk - 1 meet: rows from `first` on in `per_head`
 // tiles of bq rows, for each of the key head's query heads.
 struct WinRows {

@@ -57,23 +57,6 @@ struct WinDqSmem {
     static_assert(kAlloc <= 232448, "shared memory budget");
 };
 
-// Query tile x in longest-first order: the last rows of every head first.
-struct WinRowItem {
-    int bh, kv_bh, row0, pos0;
-    KeySpan span;
-};
-
-__device__ __forceinline__ WinRowItem win_row_item(const BwdArgs &a, int x) {
-    const int n_bh = a.B * a.H;
-    WinRowItem w;
-    w.bh = x % n_bh;
-    w.row0 = ((a.N + kBM - 1) / kBM - 1 - x / n_bh) * kBM;
-    w.kv_bh = w.bh / a.H * a.win.Hkv + w.bh % a.H / (a.H / a.win.Hkv);
-    w.pos0 = a.win.Nk - a.N + w.row0;
-    w.span = key_span(w.pos0, min(a.win.Nk, w.pos0 + kBM) - 1, a.win.window, a.win.sinks, kBN);
-    return w;
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
     win_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
@@ -154,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; ok && k * (int)gridDim.x < n_items; ++k) {
                 const int x = persistent_work_index(k, n_items);
                 if (x < 0) continue;
-                const WinRowItem w = win_row_item(a, x);
+                const WinRowItem w = win_row_item(a, x, kBM, kBN);
                 if (n >= 1 && !(ok = mbar_wait(qo_empty, (n - 1) & 1, a.status, kSiteQEmpty))) break;
                 mbar_arrive_expect_tx(qo_full, 2 * L::kQBytes);
 #pragma unroll
@@ -208,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; ok && k * (int)gridDim.x < n_items; ++k) {
             const int x = persistent_work_index(k, n_items);
             if (x < 0) continue;
-            const WinRowItem w = win_row_item(a, x);
+            const WinRowItem w = win_row_item(a, x, kBM, kBN);
             if (!(ok = warp_wait(&do_full[n & 1], (n >> 1) & 1, a.status, kSiteQ))) break;
             if (!(ok = warp_wait(qt_ready, n & 1, a.status, kSiteQt))) break;
             const uint64_t do_desc = sdesc_sw128(smem_u32(smem + L::kDoOff + (n & 1) * L::kQBytes), 16, 1024);
@@ -251,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; ok && k * (int)gridDim.x < n_items; ++k) {
             const int x = persistent_work_index(k, n_items);
             if (x < 0) continue;
-            const WinRowItem w = win_row_item(a, x);
+            const WinRowItem w = win_row_item(a, x, kBM, kBN);
             for (int j = 0; j < w.span.n; ++j, ++t) {
                 const uint32_t b = t & 1;
                 const int k_slot = (2 * t) % kSlots;
@@ -382,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; ok && k * (int)gridDim.x < n_items; ++k) {
             const int x = persistent_work_index(k, n_items);
             if (x < 0) continue;
-            const WinRowItem w = win_row_item(a, x);
+            const WinRowItem w = win_row_item(a, x, kBM, kBN);
             const int row = w.row0 + r;
             const bool valid = row < a.N;
             // P = 2^(S c - L log2 e); rows past the last get P = 0

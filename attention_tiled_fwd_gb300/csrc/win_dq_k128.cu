@@ -63,23 +63,6 @@ struct K128Smem {
     static_assert(kAlloc <= 232448, "shared memory budget");
 };
 
-// Query tile x in longest-first order: the last rows of every head first.
-struct WinRowItem {
-    int bh, kv_bh, row0, pos0;
-    KeySpan span;
-};
-
-__device__ __forceinline__ WinRowItem win_row_item(const BwdArgs &a, int x) {
-    const int n_bh = a.B * a.H;
-    WinRowItem w;
-    w.bh = x % n_bh;
-    w.row0 = ((a.N + kBM - 1) / kBM - 1 - x / n_bh) * kBM;
-    w.kv_bh = w.bh / a.H * a.win.Hkv + w.bh % a.H / (a.H / a.win.Hkv);
-    w.pos0 = a.win.Nk - a.N + w.row0;
-    w.span = key_span(w.pos0, min(a.win.Nk, w.pos0 + kBM) - 1, a.win.window, a.win.sinks, kBN);
-    return w;
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
     win_dq_k128_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
@@ -170,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; ok && k * (int)gridDim.x < n_items; ++k) {
                 const int x = persistent_work_index(k, n_items);
                 if (x < 0) continue;
-                const WinRowItem w = win_row_item(a, x);
+                const WinRowItem w = win_row_item(a, x, kBM, kBN);
                 if (n >= 1 && !(ok = mbar_wait(in_empty, (n - 1) & 1, a.status, kSiteQEmpty))) break;
                 item_s[0] = make_int4(w.bh, w.row0, w.pos0, w.span.n);
                 item_s[1] = make_int4(w.span.n_sink, w.span.lo, 0, 0);
@@ -212,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; ok && k * (int)gridDim.x < n_items; ++k) {
             const int x = persistent_work_index(k, n_items);
             if (x < 0) continue;
-            const WinRowItem w = win_row_item(a, x);
+            const WinRowItem w = win_row_item(a, x, kBM, kBN);
             if (!(ok = warp_wait(qt_ready, n & 1, a.status, kSiteQt))) break;
             ++n;
             const bool sink_step = few && w.span.n_sink > 0;
@@ -283,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; ok && k * (int)gridDim.x < n_items; ++k) {
             const int x = persistent_work_index(k, n_items);
             if (x < 0) continue;
-            const WinRowItem w = win_row_item(a, x);
+            const WinRowItem w = win_row_item(a, x, kBM, kBN);
             const bool sink_step = few && w.span.n_sink > 0;
             if (sink_step) {
                 const uint32_t b = t & 1;
@@ -338,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k * (int)gridDim.x < n_items; ++k) {
                 const int x = persistent_work_index(k, n_items);
                 if (x < 0) continue;
-                const WinRowItem w = win_row_item(a, x);
+                const WinRowItem w = win_row_item(a, x, kBM, kBN);
                 if (!mbar_wait(stage_full, n & 1, a.status, kSiteStage)) break;
                 for (int col = 0; col < a.D; col += pw)
                     tma_store_3d(&tmap_dq, smem + L::kStageOff + col / pw * (kBM * 128), col, w.row0, w.bh);

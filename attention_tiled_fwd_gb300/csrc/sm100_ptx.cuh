@@ -13,7 +13,9 @@
 namespace fa {
 
 // Limit for one in-kernel wait.  Legitimate waits in these kernels last
-// microseconds; this bound only ends a kernel whose pipeline is broken.
+// microseconds (those for a whole query or key tile of windowed attention up to
+// tens of milliseconds, at the longest windows); this bound only ends a kernel
+// whose pipeline is broken.
 constexpr uint64_t kWaitLimitNs = 1500000000ull;  // 1.5 s
 
 // Status-word layout: low 16 bits = fa_status code (negative, stored as

@@ -76,7 +76,8 @@ constexpr int kFewSinks = 16;
 // Rows at positions below this have their D_i from win_delta.cu.
 constexpr int kExactDelta = 128;
 
-// Division of 0 <= n < 2^31 by a number that the host knows: n / d = (mulhi(n, mul) + n) >> shift.
+// Division of 0 <= n < 2^31 by a number that the host knows, by a multiplication (Granlund and Montgomery, "Division by
+// invariant integers using multiplication", 1994): n / d = (mulhi(n, mul) + n) >> shift.
 struct FastDiv {
     uint32_t d, mul, shift;
     FastDiv() = default;

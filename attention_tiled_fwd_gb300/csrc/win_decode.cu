@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads)
                 const float p10 = ex2_approx(fmaf(sc[1][2 * r], a.scale_log2, -mb));
                 const float p11 = ex2_approx(fmaf(sc[1][2 * r + 1], a.scale_log2, -mb));
                 l[r] += (p00 + p01) + (p10 + p11);  // this lane's columns; the quad is added at the end
-                // P is the bf16 operand of the second product (half a step, 2^-9, per weight); l adds it unrounded
+                // P is the bf16 operand of the second product (half a step: up to 2^-8 of a weight); l adds it unrounded
                 pf[r] = pack_bf16x2(p00, p01);
                 pf[2 + r] = pack_bf16x2(p10, p11);
             }

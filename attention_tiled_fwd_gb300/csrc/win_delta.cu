@@ -2,15 +2,18 @@
 // attention's backward: D_i = sum_j P_ij dP_ij, P = 2^(c S - L log2 e), dP = dO V^T.
 //
 // Everywhere else D_i = sum_d dO_id O_id with the stored O, whose rounding to bf16 puts an
-// error of |dO||O| 2^-9 or so into every dS_ij / P_ij of the row.  |O| falls with the root of
+// error of up to 2^-8 sum_d |dO_id O_id| into every dS_ij / P_ij of the row.  |O| falls with the root of
 // the keys a row sees, and a short sequence's gradients are dominated by its first rows:
 // dQ's error was 1.6 times that of an fp32 computation rounded once at N = 101 (1.55 at
-// 227), with these rows exact it is 1.4, which is what dS as a bf16 operand leaves.
+// 227), with these rows exact it is 1.4, which is what dS as a bf16 operand leaves.  128
+// positions are what one tile of keys serves; behind them the share fades slowly (with that
+// root), it does not end.
 //
 // A CTA has 32 rows of a query head and up to 128 keys: a warp has 16 rows and 32 keys, mma.sync
 // (16 rows x 8 keys x 16 columns) on 64-column panels in shared memory, two at a time.
-// Bound by its latency (6 us at D = 128; one CTA a head with 16 rows x 128 keys a warp took 9),
-// most of it behind the dQ kernel's start, which is launched as its dependent.
+// Bound by its latency (7.3 us at D = 128 with cold caches, under the profiler), most of it
+// beside the dQ kernel's start, which is launched as its dependent: one CTA a head with 16 rows x
+// 128 keys a warp made the two kernels together 1.8 us slower (B3 H6/2 N1531 D80: 29.4 us, now 27.6).
 #include "fa_internal.h"
 #include "launch.cuh"
 #include "sm100_ptx.cuh"

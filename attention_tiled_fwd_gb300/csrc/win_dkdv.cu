@@ -193,7 +193,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the tile's L_i and D_i: lane l copies words l, l + 32, ... of [L_i | D_i] (zeros past the last row)
                 const int ss = t % C::kStats;
                 if (t >= 2 && !(ok = warp_wait(&ds_ready[ss], ((t - 2) >> 1) & 1, a.status, kSiteStats))) break;
-                // D comes from the dQ kernel, which may still run when this one was launched behind it
+                // D comes from the dQ kernel, which may still run when this one was launched behind it.  The other
+                // roles' bounded waits meanwhile span what is left of that kernel once it has SMs to spare: a query tile
+                // or two of at most kMaxSum keys, 20 ms each.
                 if (behind) launch_dependent_wait();
                 behind = false;
                 float *dst = stat_s + ss * 2 * kBQ;

@@ -13,11 +13,13 @@
 //               other's softmax has the SM.  S(j + 1) is issued before PV(j), P has columns of its own, the producer
 //               works the blocks out ahead.  A block reads its sink tiles, then its window from the first key that its
 //               first row sees (key_span); only tiles that hold a masked pair build masks.  (Two tiles past one stream of
-//               keys, as the prefix form has them: 1197 us instead of 1027 for a 32K prompt at D = 64.)  Bound by the
-//               softmax: ~1300 cycles of exponentials and conversions for a 128 x 128 tile of one warp a
-//               scheduler, ~1100 a tile with the other CTA's between them; at D = 128 by that and the chain
-//               S -> softmax -> PV.  B1 H32/8 N32768 D64 window 4096: 1027 us, 1005 TFLOP/s; B2 H16/4 N4096 D128
-//               window 1024: 66 us, 920; B1 H32 N32768 D64 window 512: 253 us, 540.
+//               keys, as the prefix form has them: 1197 us instead of 1035 for a 32K prompt at D = 64.)  Bound by the
+//               chain S -> softmax -> PV: a tile's exponentials and conversions take ~1300 cycles with one warp a
+//               scheduler (~1100 a tile with the other CTA's between them), and they begin when the PV before has
+//               ended (p_free: there is one P), so the two overlap between the CTAs only.  No pipe is full (window 512,
+//               D = 64: issue slots 50 %, XU 31 %, tensor 30 %; window 1024, D = 128: 41, 26, 46).  B1 H32/8 N32768 D64
+//               window 4096: 1035 us, 997 TFLOP/s; B2 H16/4 N4096 D128 window 1024: 66 us, 920; B1 H32 N32768
+//               D64 window 512: 253 us, 540.
 //   prefix      128-row tiles packed from the rows of many sequences (the group's heads and the new rows of one
 //               sequence are adjacent in memory, so one 4-D TMA box gathers them), two of them past one stream of
 //               128-key tiles (one chunk of the prefix), P over S in TMEM; partials instead of O.  Bound by its products

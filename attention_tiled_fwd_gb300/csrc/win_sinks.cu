@@ -12,6 +12,8 @@
 //   warps 0-3  16 rows of each half of every tile, dK_s and dV_s in registers; joined at the
 //              end (8 warps of two CTAs an SM; twice as many spilled and took 95 us
 //              instead of 50 for 32 heads of 32768 rows: 5.3 TB/s)
+// For D = 64 only: a warp keeps dK_s and dV_s (16 keys x 64 columns each) in 64 registers a lane
+// of the 168 that two CTAs leave; twice the columns would have to be dealt to twice the warps.
 // A CTA takes one chunk of a key head's rows (win_key_item) and writes an fp32 partial,
 // which sink_sum_kernel adds in a fixed order.
 #include "fa_internal.h"

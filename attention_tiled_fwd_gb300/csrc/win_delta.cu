@@ -11,7 +11,7 @@
 //
 // A CTA has 32 rows of a query head and up to 128 keys: a warp has 16 rows and 32 keys, mma.sync
 // (16 rows x 8 keys x 16 columns) on 64-column panels in shared memory, two at a time.
-// Bound by its latency (7.3 us at D = 128 with cold caches, under the profiler), most of it
+// Bound by its latency (about 7 us at D = 128 with cold caches, under the profiler), most of it
 // beside the dQ kernel's start, which is launched as its dependent: one CTA a head with 16 rows x
 // 128 keys a warp made the two kernels together 1.8 us slower (B3 H6/2 N1531 D80: 29.4 us, now 27.6).
 #include "fa_internal.h"

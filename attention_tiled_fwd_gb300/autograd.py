@@ -56,6 +56,8 @@ class _WindowAttention(torch.autograd.Function):
         B, Hq, Nq, D = q.shape
         ctx.sizes = (B, Hq, k.shape[1], Nq, k.shape[2], D, _c_int(window), _c_int(sinks))
         ctx.scale = _scale(scale, D)
+        if True in ctx.needs_input_grad:  # sizes that the backward refuses are refused here
+            _device_size_query(_device(), "fa_window_backward_workspace_bytes", *ctx.sizes)
         return o
 
     @staticmethod

@@ -203,3 +203,16 @@ def _room(gigabytes):
     torch.cuda.empty_cache()
     if torch.cuda.mem_get_info()[0] < gigabytes << 30:
         pytest.skip(f"needs {gigabytes} GB of free device memory")
+
+
+@pytest.mark.gpu
+def test_a_step_that_the_backward_refuses_is_refused_at_once():
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    N = MOST // 8 + 1
+    q, k = (torch.zeros(1, h, N, 8, dtype=torch.bfloat16, device="cuda") for h in (8, 1))
+    assert fa.window_attention(q, k, k, N).shape == q.shape  # a forward alone
+    with pytest.raises(fa.FAError) as e:
+        fa.window_attention(q.requires_grad_(), k, k, N)
+    assert e.value.code == nat.FA_ERR_SHAPE
+    assert fa.window_attention(q, k, k, N - 1).requires_grad

@@ -22,14 +22,16 @@ from typing import Optional, Tuple
 import torch
 
 from . import _native
-from ._native import FA_BF16, FA_F32, FAError
+from ._native import FA_BF16, FA_F32, FA_INT4, FAError
 
 __all__ = ["fa_forward", "fa_backward_dq", "fa_backward_dkdv", "fa_backward_atomic", "fa_decode", "fa_decode_workspace_bytes",
            "fa_decode_noalloc",
            "fa_window_forward", "fa_window_backward_dq", "fa_window_backward_dkdv", "fa_window_backward",
            "fa_window_backward_workspace_bytes",
            "fa_window_decode", "fa_window_decode_workspace_bytes", "fa_prefix_decode", "fa_prefix_decode_workspace_bytes",
-           "fa_device_status", "fa_selftest_timeout", "FAError", "FA_BF16", "FA_F32", "attention_flops",
+           "fa_paged_append", "fa_paged_decode", "fa_paged_decode_workspace_bytes", "fa_paged_gather", "paged_cache",
+           "rotation_table",
+           "fa_device_status", "fa_selftest_timeout", "FAError", "FA_BF16", "FA_F32", "FA_INT4", "attention_flops",
            "attention", "window_attention"]
 
 _DT = {torch.bfloat16: FA_BF16, torch.float32: FA_F32}
@@ -509,6 +511,196 @@ def fa_prefix_decode(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
                                          _stream_handle(stream, dev))
     _native.check(rc, "fa_prefix_decode")
     return o, lse
+
+
+# A paged cache: two tensors k_pages, v_pages of bf16 [n_pages, Hkv, page, D], or of bytes [n_pages, Hkv, page, 9 D / 16]
+# (4 bits a value and a scale for 32 of them; include/fa.h has the order), a page table and the sequences' lengths.
+def paged_cache(n_pages: int, heads: int, page: int, D: int, dtype: int = FA_BF16,
+                device: Optional[torch.device] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Zeroed pages for the keys and the values of `heads` key heads: FA_BF16 or FA_INT4 (4 bits a value)."""
+    if dtype not in (FA_BF16, FA_INT4):
+        raise ValueError(f"dtype must be FA_BF16 or FA_INT4, got {dtype}")
+    shape = (n_pages, heads, page, D if dtype == FA_BF16 else 9 * D // 16)
+    kind = torch.bfloat16 if dtype == FA_BF16 else torch.uint8
+    device = torch.device("cuda") if device is None else device
+    return torch.zeros(shape, dtype=kind, device=device), torch.zeros(shape, dtype=kind, device=device)
+
+
+def rotation_table(positions: int, rot: int, base: float = 10000.0,
+                   device: Optional[torch.device] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """cos and sin [positions, rot / 2] fp32 of the angles p * base ** (-2 i / rot), taken in 64 bits."""
+    i = torch.arange(0, rot, 2, dtype=torch.float64)
+    angle = torch.arange(positions, dtype=torch.float64)[:, None] * torch.pow(torch.tensor(base, dtype=torch.float64), -i / rot)
+    device = torch.device("cuda") if device is None else device
+    return angle.cos().float().to(device), angle.sin().float().to(device)
+
+
+def _pages(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, lens: Optional[torch.Tensor], B: int,
+           device: int):
+    """(D, Hkv), (n_pages, page, slots) and the type of a paged cache, its tensors checked."""
+    if k_pages.dim() != 4 or table.dim() != 2:
+        raise ValueError(f"k_pages must have 4 dimensions and table 2, got {list(k_pages.shape)} and {list(table.shape)}")
+    n_pages, Hkv, page, row = k_pages.shape
+    slots = table.shape[1]
+    if (n_pages | Hkv | page | row | slots | B) >> 31:
+        _no_c_int("a size of the pages or the table")
+    if k_pages.dtype is torch.bfloat16:
+        D, kind = row, FA_BF16
+    elif k_pages.dtype is torch.uint8:
+        D, kind = row * 16 // 9, FA_INT4
+        if row % 9 != 0:
+            raise ValueError(f"4-bit pages have 9 D / 16 bytes a position, got {row}")
+    else:
+        raise TypeError(f"k_pages must be bfloat16, or uint8 for 4-bit pages, got {k_pages.dtype}")
+    _tensor(k_pages, "k_pages", k_pages.dtype, (n_pages, Hkv, page, row), device)
+    _tensor(v_pages, "v_pages", k_pages.dtype, k_pages.shape, device)
+    _tensor(table, "table", torch.int32, (B, slots), device)
+    if lens is not None:
+        _tensor(lens, "lens", torch.int32, (B,), device)
+    return D, Hkv, n_pages, page, slots, kind
+
+
+def _rows(t: torch.Tensor, name: str, shape, device: int, strides: list) -> int:
+    """The address of bf16 rows [B, H, n, D] whose D channels are neighbours; adds their strides."""
+    if t.shape != shape or t.dtype is not torch.bfloat16 or t.get_device() != device:
+        _bad(t, name, torch.bfloat16, shape)
+    sb, sh, sn, sd = t.stride()
+    B, H, n, D = shape
+    if sd != 1 and D > 1:
+        raise ValueError(f"{name}'s channels must be neighbours, got strides {list(t.stride())}")
+    strides += (sb if B > 1 else 0, sh if H > 1 else 0, sn if n > 1 else 0)
+    return t.data_ptr()
+
+
+def fa_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
+                    lens: torch.Tensor, q: Optional[torch.Tensor] = None, cos: Optional[torch.Tensor] = None,
+                    sin: Optional[torch.Tensor] = None, interleaved: bool = False, counts: Optional[torch.Tensor] = None,
+                    q_out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """The n newest rows of each sequence into its pages, rotated by their positions (fa_paged_append).
+
+    k, v [B, Hkv, n, D] and q [B, Hq, n, D] are bf16 views of any strides (multiples of 8) with neighbouring channels, such
+    as parts of one projection's output.  lens: int32 [B], the keys each sequence holds with these rows; counts: int32 [B],
+    how many of the n rows (the last ones) are new.  cos, sin: fp32 [positions, rot / 2] (rotation_table), None: no
+    rotation.  Returns q rotated and contiguous (None without q)."""
+    if k.dim() != 4:
+        raise ValueError(f"k must be [B, Hkv, n, D], got {list(k.shape)}")
+    if lens is None:
+        raise ValueError("lens is needed: it says where the rows go")
+    B, Hkv, n, D = k.shape
+    dev = _device()
+    row, heads, n_pages, page, slots, kind = _pages(k_pages, v_pages, table, lens, B, dev)
+    if row != D or heads != Hkv:
+        raise ValueError(f"the pages hold {heads} heads of {row}, got k {list(k.shape)}")
+    if (n | D) >> 31:
+        _no_c_int("a size of k")
+    strides: list = []
+    Hq = 0
+    if q is not None:
+        if q.dim() != 4 or q.shape[1] < 1 or q.shape[1] >> 31:
+            raise ValueError(f"q must be [B, Hq, n, D], got {list(q.shape)}")
+        Hq = q.shape[1]
+        q_ptr = _rows(q, "q", (B, Hq, n, D), dev, strides)
+        if q_out is None:
+            q_out = _empty(q, (B, Hq, n, D), torch.bfloat16, stream)
+        else:
+            _bf16(q_out, "q_out", (B, Hq, n, D), dev)
+            if q_out.data_ptr() == q_ptr:
+                raise ValueError("q_out must not be q")
+    elif q_out is not None:
+        raise ValueError("q_out is given without q")
+    else:
+        q_ptr, strides = None, [0, 0, 0]
+    k_ptr, v_ptr = _rows(k, "k", (B, Hkv, n, D), dev, strides), _rows(v, "v", (B, Hkv, n, D), dev, strides)
+    rot = positions = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    if cos is not None:
+        if cos.dim() != 2:
+            raise ValueError(f"cos must be [positions, rot / 2], got {list(cos.shape)}")
+        positions, rot = cos.shape[0], 2 * cos.shape[1]
+        if (positions | rot) >> 31:
+            _no_c_int("a size of cos")
+        _tensor(cos, "cos", torch.float32, cos.shape, dev)
+        _tensor(sin, "sin", torch.float32, cos.shape, dev)
+    if counts is not None:
+        _tensor(counts, "counts", torch.int32, (B,), dev)
+    rc = _native.load().fa_paged_append(q_ptr, k_ptr, v_ptr, (ctypes.c_longlong * 9)(*strides), _ptr(cos), _ptr(sin),
+                                        table.data_ptr(), lens.data_ptr(), _ptr(counts), _ptr(q_out), k_pages.data_ptr(),
+                                        v_pages.data_ptr(), B, Hq, Hkv, n, D, rot, int(bool(interleaved)), positions, n_pages,
+                                        page, slots, kind, _stream_handle(stream, dev))
+    _native.check(rc, "fa_paged_append")
+    return q_out
+
+
+def fa_paged_decode_workspace_bytes(B: int, Hq: int, Hkv: int, n_q: int, D: int, page: int, slots: int,
+                                    dtype: int = FA_BF16) -> int:
+    """Workspace bytes fa_paged_decode needs (may be 0; never more than 16 MB)."""
+    return _size_query("fa_paged_decode_workspace_bytes", B, Hq, Hkv, n_q, D, page, slots, dtype)
+
+
+def fa_paged_decode(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
+                    lens: Optional[torch.Tensor] = None, window: Optional[int] = None, sinks: int = 0,
+                    scale: Optional[float] = None, o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """The n_q <= 16 newest rows q [B, Hq, n_q, D] of each sequence against its pages (fa_paged_decode).
+
+    table: int32 [B, slots], the sequences' pages; lens: int32 [B], the keys each holds (default: all its pages);
+    window None: every earlier key.  Returns (o, lse)."""
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, Hq, n_q, D], got {list(q.shape)}")
+    B, Hq, n_q, D = q.shape
+    dev = _device()
+    row, Hkv, n_pages, page, slots, kind = _pages(k_pages, v_pages, table, lens, B, dev)
+    if row != D or Hkv < 1 or Hq % Hkv != 0:
+        raise ValueError(f"the pages hold {Hkv} heads of {row}, got q {list(q.shape)}")
+    if (Hq | n_q) >> 31:
+        _no_c_int("a size of q")
+    _bf16(q, "q", (B, Hq, n_q, D), dev)
+    if o is None:
+        o = _empty_like(q, stream)
+    else:
+        _bf16(o, "o", q.shape, dev)
+    if lse is None:
+        lse = _empty(q, (B, Hq, n_q), torch.float32, stream)
+    else:
+        _tensor(lse, "lse", torch.float32, (B, Hq, n_q), dev)
+    workspace = _workspace(workspace, q, stream, dev, "fa_paged_decode_workspace_bytes", B, Hq, Hkv, n_q, D, page, slots, kind)
+    rc = _native.load().fa_paged_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), _ptr(lens),
+                                        o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, n_q, D, n_pages, page, slots,
+                                        _c_int(slots * page if window is None else window), _c_int(sinks), _scale(scale, D),
+                                        kind, _ptr(workspace), _nbytes(workspace), _stream_handle(stream, dev))
+    _native.check(rc, "fa_paged_decode")
+    return o, lse
+
+
+def fa_paged_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, lens: Optional[torch.Tensor] = None,
+                    rows: Optional[int] = None, k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None):
+    """The sequences' rows out of their pages (fa_paged_gather): k, v [B, Hkv, rows, D] bf16 (rows: default all of a
+    sequence's pages), of which the first min(lens[b], rows) are written.  Returns (k, v)."""
+    if table.dim() != 2:
+        raise ValueError(f"table must be [B, slots], got {list(table.shape)}")
+    B = table.shape[0]
+    dev = _device()
+    D, Hkv, n_pages, page, slots, kind = _pages(k_pages, v_pages, table, lens, B, dev)
+    if (k is None) != (v is None):
+        raise ValueError("k and v come together")
+    if k is None:
+        shape = (B, Hkv, slots * page if rows is None else rows, D)
+        k, v = (_empty(k_pages, shape, torch.bfloat16, stream) for _ in range(2))
+    else:
+        if k.dim() != 4 or (rows is not None and k.shape[2] != rows):
+            raise ValueError(f"k must be [B, Hkv, rows, D], got {list(k.shape)}")
+        shape = (B, Hkv, k.shape[2], D)
+        _bf16(k, "k", shape, dev)
+        _bf16(v, "v", shape, dev)
+    if shape[2] >> 31:
+        _no_c_int("rows")
+    rc = _native.load().fa_paged_gather(k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), _ptr(lens), k.data_ptr(),
+                                        v.data_ptr(), B, Hkv, shape[2], D, n_pages, page, slots, kind,
+                                        _stream_handle(stream, dev))
+    _native.check(rc, "fa_paged_gather")
+    return k, v
 
 
 def fa_device_status(stream: Optional[torch.cuda.Stream] = None) -> int:

@@ -12,11 +12,11 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libfa.so")
 
 # enum fa_dtype / fa_status (include/fa.h)
-FA_F32, FA_BF16 = 0, 1
+FA_F32, FA_BF16, FA_INT4 = 0, 1, 2
 FA_OK = 0
 FA_ERR_NULL, FA_ERR_SHAPE, FA_ERR_HEAD_DIM, FA_ERR_DTYPE, FA_ERR_ALIGN = -1, -2, -3, -4, -5
 FA_ERR_SCALE, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_DEVICE_PTR, FA_ERR_DEVICE = -6, -7, -8, -9, -10
-FA_ERR_WORKSPACE, FA_ERR_SCRATCH_LIMIT = -11, -12
+FA_ERR_WORKSPACE, FA_ERR_SCRATCH_LIMIT, FA_ERR_PAGE = -11, -12, -13
 FA_DECODE_NOALLOC_SCRATCH_BYTES = 16 << 20  # fa.h: fixed scratch of fa_decode_noalloc, per device
 
 # Every symbol include/fa.h declares.
@@ -24,7 +24,8 @@ EXPORTS = ("fa_forward", "fa_backward_dq", "fa_backward_dkdv", "fa_backward_atom
            "fa_decode_workspace_bytes",
            "fa_decode_noalloc", "fa_window_forward", "fa_window_backward_dq", "fa_window_backward_dkdv",
            "fa_window_backward", "fa_window_backward_workspace_bytes", "fa_window_decode", "fa_window_decode_workspace_bytes",
-           "fa_prefix_decode", "fa_prefix_decode_workspace_bytes", "fa_status_string", "fa_device_status", "fa_selftest_timeout", "fa_selftest_exp2", "fa_version")
+           "fa_prefix_decode", "fa_prefix_decode_workspace_bytes", "fa_paged_append", "fa_paged_decode",
+           "fa_paged_decode_workspace_bytes", "fa_paged_gather", "fa_status_string", "fa_device_status", "fa_selftest_timeout", "fa_selftest_exp2", "fa_version")
 
 _lib = None
 
@@ -59,6 +60,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_window_decode_workspace_bytes.argtypes = [_i] * 8 + [szp]
     lib.fa_prefix_decode.argtypes = [_p] * 8 + [_i] * 7 + [_f, _p, sz, _p]
     lib.fa_prefix_decode_workspace_bytes.argtypes = [_i] * 7 + [szp]
+    lib.fa_paged_append.argtypes = [_p] * 12 + [_i] * 12 + [_p]
+    lib.fa_paged_decode.argtypes = [_p] * 7 + [_i] * 10 + [_f, _i, _p, sz, _p]
+    lib.fa_paged_decode_workspace_bytes.argtypes = [_i] * 8 + [szp]
+    lib.fa_paged_gather.argtypes = [_p] * 6 + [_i] * 8 + [_p]
     lib.fa_status_string.argtypes = [_i]
     lib.fa_status_string.restype = ctypes.c_char_p
     lib.fa_device_status.argtypes = [_p]
@@ -68,7 +73,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     for name in ("fa_forward", "fa_backward_dq", "fa_backward_dkdv", "fa_backward_atomic", "fa_decode", "fa_decode_workspace_bytes",
                  "fa_decode_noalloc", "fa_window_forward", "fa_window_backward_dq", "fa_window_backward_dkdv",
                  "fa_window_backward", "fa_window_backward_workspace_bytes", "fa_window_decode", "fa_window_decode_workspace_bytes",
-                 "fa_prefix_decode", "fa_prefix_decode_workspace_bytes", "fa_device_status",
+                 "fa_prefix_decode", "fa_prefix_decode_workspace_bytes", "fa_paged_append", "fa_paged_decode",
+                 "fa_paged_decode_workspace_bytes", "fa_paged_gather", "fa_device_status",
                  "fa_selftest_timeout", "fa_selftest_exp2", "fa_version"):
         getattr(lib, name).restype = _i
     _lib = lib

@@ -10,6 +10,7 @@
 #include "fa_internal.h"
 #include "sm100_ptx.cuh"
 #include "win_decode.cuh"
+#include "paged.cuh"
 
 #include <algorithm>
 #include <atomic>
@@ -881,6 +882,129 @@ extern "C" int fa_prefix_decode(const void *q, const void *k_prefix, const void 
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+namespace {
+// A paged cache of B sequences, and what its pool is.
+int check_pages(int B, int Hkv, int D, int n_pages, int page, int slots, int cache_dtype) {
+    if (cache_dtype != FA_BF16 && cache_dtype != FA_INT4) return FA_ERR_DTYPE;
+    if (B < 1 || Hkv < 1 || D < 1 || n_pages < 1 || slots < 1) return FA_ERR_SHAPE;
+    if (B > 65535 || Hkv > 65535) return FA_ERR_SHAPE;
+    if (page < kUnit || page > kMaxPage || (page & (page - 1)) != 0) return FA_ERR_SHAPE;
+    if ((long long)slots * page > kMaxCapacity) return FA_ERR_SHAPE;
+    if ((long long)n_pages * Hkv > (1ll << 31) - (1 << 20)) return FA_ERR_SHAPE;
+    if (D != 64 && D != 128 && D != 256) return FA_ERR_HEAD_DIM;
+    return FA_OK;
+}
+
+PagePool page_pool(const void *k, const void *v, const int *table, int Hkv, int n_pages, int page, int slots) {
+    int shift = 4;
+    while ((1 << shift) < page) ++shift;
+    return PagePool{static_cast<uint8_t *>(const_cast<void *>(k)), static_cast<uint8_t *>(const_cast<void *>(v)), table, n_pages,
+                    shift, slots, Hkv};
+}
+
+int check_paged_decode(int B, int Hq, int Hkv, int n_q, int D, int n_pages, int page, int slots, int cache_dtype) {
+    int rc = check_pages(B, Hkv, D, n_pages, page, slots, cache_dtype);
+    if (rc != FA_OK) return rc;
+    if (Hq < 1 || Hq > 65535 || Hq % Hkv != 0 || n_q < 1 || n_q > kMaxDecodeRows) return FA_ERR_SHAPE;
+    if ((long long)B * Hq * n_q > (1ll << 31) - (1 << 20)) return FA_ERR_SHAPE;
+    return FA_OK;
+}
+}  // namespace
+
+extern "C" int fa_paged_append(const void *q, const void *k, const void *v, const long long *strides, const float *cos,
+                               const float *sin, const int *table, const int *lens, const int *counts, void *q_out,
+                               void *k_pages, void *v_pages, int B, int Hq, int Hkv, int n, int D, int rot, int interleaved,
+                               int positions, int n_pages, int page, int slots, int cache_dtype, void *stream) {
+    int rc = check_pages(B, Hkv, D, n_pages, page, slots, cache_dtype);
+    if (rc != FA_OK) return rc;
+    if (n < 1 || Hq < 0 || Hq > 65535 || (Hq == 0) != (q == nullptr)) return FA_ERR_SHAPE;
+    if ((long long)B * n * (Hq + 2ll * Hkv) > (1ll << 31) - (1 << 20)) return FA_ERR_SHAPE;
+    if (rot < 0 || rot > D || rot % 16 != 0) return FA_ERR_SHAPE;
+    if (rot > 0 && positions < slots * page) return FA_ERR_SHAPE;
+    AppendArgs a{};
+    for (int t = 0; t < 3; ++t) {
+        const int heads = t == 0 ? Hq : Hkv;
+        long long *to = t == 0 ? a.sq : t == 1 ? a.sk : a.sv;
+        const long long plain[3] = {(long long)heads * n * D, (long long)n * D, D};
+        for (int i = 0; i < 3; ++i) {
+            to[i] = strides ? strides[3 * t + i] : plain[i];
+            if (to[i] % 8 != 0) return FA_ERR_ALIGN;
+        }
+    }
+    if (!table || !lens) return FA_ERR_NULL;
+    // (k stands in for what the call does without)
+    rc = check_ptrs({k, v, k_pages, v_pages, q ? q : k, q ? q_out : k, rot > 0 ? cos : k, rot > 0 ? sin : k});
+    for (const int *p : {table, lens, counts})
+        if (rc == FA_OK) rc = check_lens(p);
+    if (rc != FA_OK) return rc;
+    int dev;
+    DeviceState *st;
+    rc = device_state(&dev, &st);
+    if (rc != FA_OK) return rc;
+    a.q = q, a.k = k, a.v = v;
+    a.cos = cos, a.sin = sin;
+    a.lens = lens, a.counts = counts;
+    a.q_out = q_out;
+    a.pool = page_pool(k_pages, v_pages, table, Hkv, n_pages, page, slots);
+    a.B = B, a.Hq = Hq, a.n = n, a.D = D, a.rot = rot, a.interleaved = interleaved != 0;
+    a.status = st->status_word;
+    const cudaError_t e = launch_paged_append(a, cache_dtype == FA_INT4, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+extern "C" int fa_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q, int D, int page, int slots, int cache_dtype,
+                                               size_t *bytes) {
+    if (!bytes) return FA_ERR_NULL;
+    int rc = check_paged_decode(B, Hq, Hkv, n_q, D, 1, page, slots, cache_dtype);
+    if (rc != FA_OK) return rc;
+    *bytes = 0;
+    return FA_OK;
+}
+
+extern "C" int fa_paged_decode(const void *q, const void *k_pages, const void *v_pages, const int *table, const int *lens,
+                               void *o, float *lse, int B, int Hq, int Hkv, int n_q, int D, int n_pages, int page, int slots,
+                               int window, int sinks, float scale, int cache_dtype, void *workspace, size_t workspace_bytes,
+                               void *stream) {
+    int rc = check_paged_decode(B, Hq, Hkv, n_q, D, n_pages, page, slots, cache_dtype);
+    if (rc != FA_OK) return rc;
+    if (window < 1 || sinks < 0) return FA_ERR_SHAPE;
+    if (!scale_ok(scale)) return FA_ERR_SCALE;
+    if (!table) return FA_ERR_NULL;
+    rc = check_ptrs({q, k_pages, v_pages, o, lse});
+    if (rc == FA_OK) rc = check_lens(table);
+    if (rc == FA_OK) rc = check_lens(lens);
+    if (rc != FA_OK) return rc;
+    int dev;
+    DeviceState *st;
+    rc = device_state(&dev, &st);
+    if (rc != FA_OK) return rc;
+    const WinArgs w = window_args(Hkv, slots * page, window, sinks);
+    const PagedDecodeArgs a{q, lens, o, lse, page_pool(k_pages, v_pages, table, Hkv, n_pages, page, slots), B, Hq / Hkv * n_q, n_q, D,
+                            w.window, w.sinks, scale * log2e(), st->status_word};
+    const cudaError_t e = launch_paged_decode(a, cache_dtype == FA_INT4, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+extern "C" int fa_paged_gather(const void *k_pages, const void *v_pages, const int *table, const int *lens, void *k, void *v,
+                               int B, int Hkv, int rows, int D, int n_pages, int page, int slots, int cache_dtype,
+                               void *stream) {
+    int rc = check_pages(B, Hkv, D, n_pages, page, slots, cache_dtype);
+    if (rc != FA_OK) return rc;
+    if (rows < 1 || (long long)B * Hkv * rows > (1ll << 31) - (1 << 20)) return FA_ERR_SHAPE;
+    if (!table) return FA_ERR_NULL;
+    rc = check_ptrs({k_pages, v_pages, k, v});
+    if (rc == FA_OK) rc = check_lens(table);
+    if (rc == FA_OK) rc = check_lens(lens);
+    if (rc != FA_OK) return rc;
+    int dev;
+    DeviceState *st;
+    rc = device_state(&dev, &st);
+    if (rc != FA_OK) return rc;
+    const GatherArgs a{page_pool(k_pages, v_pages, table, Hkv, n_pages, page, slots), lens, k, v, B, rows, D, st->status_word};
+    const cudaError_t e = launch_paged_gather(a, cache_dtype == FA_INT4, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 extern "C" const char *fa_status_string(int status) {
     switch (status) {
         case FA_OK: return "ok";
@@ -897,6 +1021,7 @@ extern "C" const char *fa_status_string(int status) {
         case FA_ERR_WORKSPACE: return "workspace smaller than its size query requires";
         case FA_ERR_SCRATCH_LIMIT:
             return "sizes need more than FA_DECODE_NOALLOC_SCRATCH_BYTES of scratch; use fa_decode with a workspace";
+        case FA_ERR_PAGE: return "a page table has no page of the pool where one is needed";
         default: return "unknown status";
     }
 }

@@ -1,0 +1,382 @@
+// paged_cache.cu -- rows into a paged cache (rotated by their positions, bf16 or 4 bits), and out of it again.
+//
+// Rotation: channels (a, b) of a pair turn by the angle of the row's position, a cos - b sin and b cos + a sin, and are
+// rounded to bf16 once: sums of two products whose fp32 result lies so near to the border of two bf16 values that its error
+// matters (one in some thousands) are computed again with the products' and the sum's rounding errors.  So the rows do not
+// depend on the order of the operations, and 4-bit codes, which would turn a last bit into a step, are those of the
+// definition.
+// 4 bits: scale = fp16(max |y| / 7) of 32 channels of the bf16 row y, code = 8 + y fp32(1 / scale), rounded to even (one
+// FMA onto 1.5 2^23, so the product is not rounded first) and clamped to 1 .. 15.  Groups with an infinity or a NaN get a
+// NaN scale; a scale past fp16's largest stays there.
+//
+// What bounds both: HBM.
+#include "fa_internal.h"
+#include "paged.cuh"
+#include "sm100_ptx.cuh"
+#include <cuda_fp16.h>
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kHeadsPerLane = 4;  // rows of one token that a lane turns with the same cosines
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+__device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// a c + b s rounded to fp32 so that rounding that to bf16 is rounding the exact sum: TwoSum of the products with their
+// errors (Knuth; Dekker), and a sum that lies halfway between two bf16 values is moved one step to its side.
+__device__ __noinline__ float turn_exact(float a, float c, float b, float s) {
+    const float p = __fmul_rn(a, c), pe = __fmaf_rn(a, c, -p);
+    const float w = __fmul_rn(b, s), we = __fmaf_rn(b, s, -w);
+    const float h = __fadd_rn(p, w), bb = __fsub_rn(h, p);
+    const float he = __fadd_rn(__fsub_rn(p, __fsub_rn(h, bb)), __fsub_rn(w, bb));
+    const float t = __fadd_rn(he, __fadd_rn(pe, we));
+    const float y = __fadd_rn(h, t), rest = __fsub_rn(t, __fsub_rn(y, h));
+    const uint32_t bits = __float_as_uint(y);
+    if (!(fabsf(y) < INFINITY)) return __fmaf_rn(a, c, w);
+    if ((bits & 0xffffu) == 0x8000u && rest != 0.f) return __uint_as_float(bits + ((rest > 0.f) == (y > 0.f) ? 1 : -1));
+    return y;
+}
+
+// The rotation of a lane's 8 channels: its own times cos plus their partners' times (signed) sin.
+struct Turn {
+    float c[8], s[8];
+    bool on;
+    int partner;  // lane offset of the partners' chunk, 0: neighbours within the chunk
+
+    // chunk `cl` of a row at position p
+    __device__ __forceinline__ void load(const AppendArgs &a, int p, int cl) {
+        on = 8 * cl < a.rot;
+        partner = 0;
+        if (!on) return;
+        const int half = a.rot / 2;
+        const float *cs = a.cos + (size_t)p * half, *sn = a.sin + (size_t)p * half;
+        if (a.interleaved) {
+            const float4 x = *reinterpret_cast<const float4 *>(cs + 4 * cl), y = *reinterpret_cast<const float4 *>(sn + 4 * cl);
+            c[0] = c[1] = x.x, c[2] = c[3] = x.y, c[4] = c[5] = x.z, c[6] = c[7] = x.w;
+            s[0] = -y.x, s[1] = y.x, s[2] = -y.y, s[3] = y.y, s[4] = -y.z, s[5] = y.z, s[6] = -y.w, s[7] = y.w;
+            return;
+        }
+        const bool low = 8 * cl < half;
+        const int at = low ? 8 * cl : 8 * cl - half;
+        partner = low ? half / 8 : -(half / 8);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 x = *reinterpret_cast<const float4 *>(cs + at + 4 * i), y = *reinterpret_cast<const float4 *>(sn + at + 4 * i);
+            c[4 * i] = x.x, c[4 * i + 1] = x.y, c[4 * i + 2] = x.z, c[4 * i + 3] = x.w;
+            s[4 * i] = low ? -y.x : y.x, s[4 * i + 1] = low ? -y.y : y.y, s[4 * i + 2] = low ? -y.z : y.z, s[4 * i + 3] = low ? -y.w : y.w;
+        }
+    }
+
+    // All lanes of the warp take part.
+    __device__ __forceinline__ uint4 apply(const AppendArgs &a, const uint4 &x) const {
+        uint4 o;
+        const int from = (threadIdx.x & 31) + partner;
+        if (a.interleaved) {
+            o = make_uint4(x.x >> 16 | x.x << 16, x.y >> 16 | x.y << 16, x.z >> 16 | x.z << 16, x.w >> 16 | x.w << 16);
+        } else {
+            o.x = __shfl_sync(0xffffffffu, x.x, from);
+            o.y = __shfl_sync(0xffffffffu, x.y, from);
+            o.z = __shfl_sync(0xffffffffu, x.z, from);
+            o.w = __shfl_sync(0xffffffffu, x.w, from);
+        }
+        if (!on) return x;
+        float y[8];
+        uint32_t near = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float xa = i & 1 ? bf_hi(word_of(x, i / 2)) : bf_lo(word_of(x, i / 2));
+            const float xb = i & 1 ? bf_hi(word_of(o, i / 2)) : bf_lo(word_of(o, i / 2));
+            const float w = xb * s[i];
+            y[i] = fmaf(xa, c[i], w);
+            // y is off by half a step of itself and of w at most: 2^-24 (|y| + |w|); twice that is looked at
+            const float e = (fabsf(y[i]) + fabsf(w)) * 0x1p-23f;
+            near |= (__float_as_uint(y[i] + e) + 0x8000u) ^ (__float_as_uint(y[i] - e) + 0x8000u);
+        }
+        if (near >> 16) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float xa = i & 1 ? bf_hi(word_of(x, i / 2)) : bf_lo(word_of(x, i / 2));
+                const float xb = i & 1 ? bf_hi(word_of(o, i / 2)) : bf_lo(word_of(o, i / 2));
+                y[i] = turn_exact(xa, c[i], xb, s[i]);
+            }
+        }
+        return make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+    }
+};
+
+// The new rows of sequence b: positions [first, len).  A row past the capacity has no page, and no cosines either.
+struct NewRows {
+    int first, len, start;  // start: the position of row 0 (may be below 0)
+    __device__ __forceinline__ NewRows(const AppendArgs &a, int b) {
+        len = max(0, min(a.lens[b], a.pool.capacity() + a.n));  // (past that no row has a page: sums stay within 32 bits)
+        const int n = a.counts ? max(0, min(a.n, a.counts[b])) : a.n;
+        start = len - a.n;
+        first = max(0, len - n);
+    }
+};
+
+// Rows of one token: lane `cl` of a row's D / 8 holds 8 channels, of kHeadsPerLane heads in turn.  Heads: q's, then (bf16
+// pages) k's and v's.
+template <int D, bool FOUR>
+__device__ void token_rows(const AppendArgs &a, int task) {
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBlock = kRows * kHeadsPerLane;
+    const int lane = threadIdx.x & 31, cl = lane % kLanes, sub = lane / kLanes;
+    const int Hkv = a.pool.Hkv, heads = a.Hq + (FOUR ? 0 : 2 * Hkv), blocks = (heads + kBlock - 1) / kBlock;
+    const int token = task / blocks, h0 = task % blocks * kBlock, b = token / a.n, i = token % a.n;
+    const NewRows rows(a, b);
+    const int p = rows.start + i;
+    const bool fits = p < a.pool.capacity();
+    const bool there = p >= rows.first && fits;
+    uint4 x[kHeadsPerLane];
+#pragma unroll
+    for (int u = 0; u < kHeadsPerLane; ++u) {
+        const int h = h0 + u * kRows + sub;
+        x[u] = make_uint4(0, 0, 0, 0);
+        if (!there || h >= heads) continue;
+        const __nv_bfloat16 *src = h < a.Hq ? static_cast<const __nv_bfloat16 *>(a.q) + b * a.sq[0] + h * a.sq[1] + i * a.sq[2]
+                                   : h < a.Hq + Hkv
+                                       ? static_cast<const __nv_bfloat16 *>(a.k) + b * a.sk[0] + (h - a.Hq) * a.sk[1] + i * a.sk[2]
+                                       : static_cast<const __nv_bfloat16 *>(a.v) + b * a.sv[0] + (h - a.Hq - Hkv) * a.sv[1] + i * a.sv[2];
+        x[u] = __ldg(reinterpret_cast<const uint4 *>(src) + cl);
+    }
+    Turn turn;
+    turn.on = false, turn.partner = 0;
+    int page = -1;
+    if (there) {
+        turn.load(a, p, cl);
+        if (!FOUR) page = a.pool.page_of(b, p);
+    }
+    if (!FOUR && p >= rows.first && page < 0 && lane == 0) record_failure(a.status, kErrPage, 0);
+#pragma unroll
+    for (int u = 0; u < kHeadsPerLane; ++u) {
+        const int h = h0 + u * kRows + sub;
+        const uint4 y = turn.apply(a, x[u]);
+        if (h < a.Hq) {
+            reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.q_out) + (((size_t)b * a.Hq + h) * a.n + i) * D)[cl] = y;
+        } else if (!FOUR && h < heads && page >= 0) {
+            const bool key = h < a.Hq + Hkv;
+            uint8_t *to = (key ? a.pool.k : a.pool.v) + a.pool.at(page, h - a.Hq - (key ? 0 : Hkv), p, 2 * D);
+            reinterpret_cast<uint4 *>(to)[cl] = key ? y : x[u];
+        }
+    }
+}
+
+// 8 channels of a row in 4 bits: its 8 codes, the lowest channel in the lowest bits, and the scale of the 32 channels that
+// its four lanes share.
+__device__ __forceinline__ uint32_t quantise(const uint4 &y, __half *scale) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = word_of(y, i);
+        most = max(most, max(w << 16 & 0x7fff0000u, w & 0x7fff0000u));  // magnitudes order as integers, NaN above all
+    }
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+    const bool finite = most < 0x7f800000u;
+    const __half s = finite ? __float2half_rn(fminf(__fdiv_rn(__uint_as_float(most), 7.f), 65504.f)) : __ushort_as_half(0x7fff);
+    const float f = __half2float(s), inverse = f > 0.f ? __frcp_rn(f) : 0.f;  // (NaN: codes do not matter)
+    *scale = s;
+    uint32_t codes = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float v = i & 1 ? bf_hi(word_of(y, i / 2)) : bf_lo(word_of(y, i / 2));
+        const int step = __float_as_int(__fmaf_rn(v, inverse, 12582912.f)) - 0x4B400000;  // 1.5 2^23
+        codes |= (uint32_t)(max(-7, min(7, step)) + 8) << (4 * i);
+    }
+    return codes;
+}
+
+// One unit of 16 positions of a head's keys or values, those of them that are new.  A lane holds 8 channels of an even
+// position and of the odd one behind it.
+template <int D>
+__device__ void unit_rows(const AppendArgs &a, int task, int units) {
+    using U = Unit4<D>;
+    constexpr int kLanes = D / 8, kPairs = 32 / kLanes;
+    const int lane = threadIdx.x & 31, cl = lane % kLanes, sub = lane / kLanes;
+    const int Hkv = a.pool.Hkv;
+    const bool key = task % (2 * Hkv) < Hkv;
+    const int h = task % Hkv, bu = task / (2 * Hkv), b = bu / units;
+    const NewRows rows(a, b);
+    const int p0 = ((rows.first >> 4) + bu % units) * kUnit;
+    if (p0 >= rows.len || p0 + kUnit <= rows.first) return;
+    const int page = p0 < a.pool.capacity() ? a.pool.page_of(b, p0) : -1;
+    if (page < 0) {
+        if (lane == 0) record_failure(a.status, kErrPage, 0);
+        return;
+    }
+    uint8_t *to = (key ? a.pool.k : a.pool.v) + a.pool.at(page, h, p0, 9 * D / 16);
+    const __nv_bfloat16 *src = key ? static_cast<const __nv_bfloat16 *>(a.k) + b * a.sk[0] + h * a.sk[1]
+                                   : static_cast<const __nv_bfloat16 *>(a.v) + b * a.sv[0] + h * a.sv[1];
+    const long long stride = key ? a.sk[2] : a.sv[2];
+    const int g = cl / 4, t = cl % 4;
+#pragma unroll 2
+    for (int pass = 0; pass < 8 / kPairs; ++pass) {
+        const int u = 2 * (pass * kPairs + sub);
+        bool there[2];
+        uint32_t codes[2];
+        __half scale[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int p = p0 + u + e;
+            there[e] = p >= rows.first && p < rows.len;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            Turn turn;
+            turn.on = false, turn.partner = 0;
+            if (there[e]) {
+                x = __ldg(reinterpret_cast<const uint4 *>(src + (p - rows.start) * stride) + cl);
+                if (key) turn.load(a, p, cl);
+            }
+            if (key) x = turn.apply(a, x);
+            codes[e] = quantise(x, &scale[e]);
+        }
+        __half *scales = reinterpret_cast<__half *>(to + U::kCodes);
+        if (key) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (!there[e]) continue;
+                reinterpret_cast<uint32_t *>(to)[U::word(u >> 3, g, 4 * ((u + e) & 7) + t)] = codes[e];
+                if (t == 0) scales[U::k_scale(u + e, g)] = scale[e];
+            }
+        } else {
+            // channels 8 t .. of the group: lanes' fourths 2 t and 2 t + 1
+            uint32_t *w0 = reinterpret_cast<uint32_t *>(to) + U::word(u >> 3, g, 8 * t + (u & 7) / 2);
+            uint32_t *w1 = reinterpret_cast<uint32_t *>(to) + U::word(u >> 3, g, 8 * t + 4 + (u & 7) / 2);
+            if (there[0] && there[1]) {
+                *w0 = __byte_perm(codes[0], codes[1], 0x5410);
+                *w1 = __byte_perm(codes[0], codes[1], 0x7632);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (!there[e]) continue;
+                    reinterpret_cast<uint16_t *>(w0)[e] = (uint16_t)codes[e];
+                    reinterpret_cast<uint16_t *>(w1)[e] = (uint16_t)(codes[e] >> 16);
+                }
+            }
+            if (t == 0)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (there[e]) scales[U::v_scale(u + e, g)] = scale[e];
+        }
+    }
+}
+
+template <int D, bool FOUR>
+__global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a, int row_blocks, int row_tasks, int units, int unit_tasks) {
+    const int warp = threadIdx.x >> 5;
+    if (blockIdx.x < (unsigned)row_blocks) {
+        const int task = blockIdx.x * (kThreads / 32) + warp;
+        if (task < row_tasks) token_rows<D, FOUR>(a, task);
+    } else if constexpr (FOUR) {
+        const int task = (blockIdx.x - row_blocks) * (kThreads / 32) + warp;
+        if (task < unit_tasks) unit_rows<D>(a, task, units);
+    }
+}
+
+template <int D, bool FOUR>
+cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
+    constexpr int kBlock = 32 / (D / 8) * kHeadsPerLane, kWarps = kThreads / 32;
+    const int heads = a.Hq + (FOUR ? 0 : 2 * a.pool.Hkv);
+    const int row_tasks = a.B * a.n * ((heads + kBlock - 1) / kBlock);
+    const int units = a.n == 1 ? 1 : (a.n + kUnit - 2) / kUnit + 1;  // n rows meet so many units of 16 at most
+    const int unit_tasks = FOUR ? a.B * units * 2 * a.pool.Hkv : 0;
+    const int row_blocks = (row_tasks + kWarps - 1) / kWarps;
+    paged_append_kernel<D, FOUR><<<row_blocks + (unit_tasks + kWarps - 1) / kWarps, kThreads, 0, s>>>(a, row_blocks, row_tasks, units,
+                                                                                                   unit_tasks);
+    return cudaGetLastError();
+}
+
+// One unit of 16 positions of a head's keys or values a warp.
+template <int D, bool FOUR>
+__global__ void __launch_bounds__(kThreads) paged_gather_kernel(GatherArgs a, int units, long long tasks) {
+    const int lane = threadIdx.x & 31;
+    const long long task = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (task >= tasks) return;
+    const int Hkv = a.pool.Hkv;
+    const int p0 = (int)(task % units) * kUnit, bh = (int)(task / units), which = bh % 2, h = bh / 2 % Hkv, b = bh / (2 * Hkv);
+    const int len = min(a.lens ? max(0, min(a.pool.capacity(), a.lens[b])) : a.pool.capacity(), a.rows);
+    if (p0 >= len) return;
+    const int n = min(kUnit, len - p0);
+    const int page = a.pool.page_of(b, p0);
+    if (page < 0 && lane == 0) record_failure(a.status, kErrPage, 0);
+    const uint8_t *pages = which ? a.pool.v : a.pool.k;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(which ? a.v : a.k) + (((size_t)b * Hkv + h) * a.rows + p0) * D;
+    if constexpr (!FOUR) {
+        constexpr int kChunks = D / 8;
+        const uint4 *src = reinterpret_cast<const uint4 *>(pages + a.pool.at(max(page, 0), h, p0, 2 * D));
+        uint4 x[kUnit * kChunks / 32];
+#pragma unroll
+        for (int i = 0; i < kUnit * kChunks / 32; ++i) {
+            const int c = i * 32 + lane;
+            x[i] = page >= 0 && c < n * kChunks ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kUnit * kChunks / 32; ++i) {
+            const int c = i * 32 + lane;
+            if (c < n * kChunks) reinterpret_cast<uint4 *>(out)[c] = x[i];
+        }
+    } else {
+        using U = Unit4<D>;
+        const uint8_t *unit = pages + a.pool.at(max(page, 0), h, p0, 9 * D / 16);
+        const __half *scales = reinterpret_cast<const __half *>(unit + U::kCodes);
+        auto value = [](uint32_t w, int i, float s) { return ((int)(w >> (4 * i) & 15) - 8) * s; };
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int g = 0; g < U::kGroups; ++g) {
+                const uint32_t w = page >= 0 ? __ldg(reinterpret_cast<const uint32_t *>(unit) + U::word(half, g, lane)) : 0x88888888u;
+                if (which == 0) {
+                    const int u = 8 * half + lane / 4;
+                    if (u >= n) continue;
+                    const float s = page >= 0 ? __half2float(scales[U::k_scale(u, g)]) : 0.f;
+                    reinterpret_cast<uint4 *>(out + u * D + 32 * g)[lane % 4] =
+                        make_uint4(pack_bf16x2(value(w, 0, s), value(w, 1, s)), pack_bf16x2(value(w, 2, s), value(w, 3, s)),
+                                   pack_bf16x2(value(w, 4, s), value(w, 5, s)), pack_bf16x2(value(w, 6, s), value(w, 7, s)));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int u = 8 * half + 2 * (lane % 4) + e;
+                        if (u >= n) continue;
+                        const float s = page >= 0 ? __half2float(scales[U::v_scale(u, g)]) : 0.f;
+                        reinterpret_cast<uint2 *>(out + u * D + 32 * g)[lane / 4] =
+                            make_uint2(pack_bf16x2(value(w, 4 * e, s), value(w, 4 * e + 1, s)),
+                                       pack_bf16x2(value(w, 4 * e + 2, s), value(w, 4 * e + 3, s)));
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <int D, bool FOUR>
+cudaError_t launch_gather(const GatherArgs &a, cudaStream_t s) {
+    const int units = (min(a.rows, a.pool.capacity()) + kUnit - 1) / kUnit;
+    const long long tasks = (long long)a.B * a.pool.Hkv * 2 * units;
+    paged_gather_kernel<D, FOUR><<<(unsigned)((tasks + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, s>>>(a, units, tasks);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const AppendArgs &a, bool four, cudaStream_t s) {
+    switch (a.D) {
+        case 64: return four ? launch_append<64, true>(a, s) : launch_append<64, false>(a, s);
+        case 128: return four ? launch_append<128, true>(a, s) : launch_append<128, false>(a, s);
+        case 256: return four ? launch_append<256, true>(a, s) : launch_append<256, false>(a, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_paged_gather(const GatherArgs &a, bool four, cudaStream_t s) {
+    switch (a.D) {
+        case 64: return four ? launch_gather<64, true>(a, s) : launch_gather<64, false>(a, s);
+        case 128: return four ? launch_gather<128, true>(a, s) : launch_gather<128, false>(a, s);
+        case 256: return four ? launch_gather<256, true>(a, s) : launch_gather<256, false>(a, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace fa

@@ -61,7 +61,8 @@ extern "C" {
 /* Element types of q/k/v/o/dO (dtype) and of dq/dk/dv (grad_dtype). */
 enum fa_dtype {
     FA_F32 = 0,   /* IEEE float32                                      */
-    FA_BF16 = 1   /* bfloat16, round-to-nearest-even on every store    */
+    FA_BF16 = 1,  /* bfloat16, round-to-nearest-even on every store    */
+    FA_INT4 = 2   /* 4-bit pages of a paged cache (see there)          */
 };
 
 enum fa_status {
@@ -77,7 +78,8 @@ enum fa_status {
     FA_ERR_DEVICE_PTR = -9,  /* a pointer is not device-accessible memory                */
     FA_ERR_DEVICE = -10,     /* the current device is not sm_103 (GB300)                 */
     FA_ERR_WORKSPACE = -11,  /* a workspace is smaller than its size query requires      */
-    FA_ERR_SCRATCH_LIMIT = -12 /* the sizes need more than FA_DECODE_NOALLOC_SCRATCH_BYTES */
+    FA_ERR_SCRATCH_LIMIT = -12, /* the sizes need more than FA_DECODE_NOALLOC_SCRATCH_BYTES */
+    FA_ERR_PAGE = -13        /* a page table without a page of the pool where one is needed (read by fa_device_status) */
 };
 
 /*
@@ -317,6 +319,69 @@ FA_API int fa_prefix_decode(const void *q, const void *k_prefix, const void *v_p
                             int B, int Hq, int Hkv, int n_q, int P, int N, int D, float scale,
                             void *workspace, size_t workspace_bytes, void *stream);
 FA_API int fa_prefix_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q, int P, int N, int D, size_t *bytes);
+
+/*
+ * A paged cache: the keys and values of many sequences in one pool of pages.
+ *   k_pages, v_pages: [n_pages, Hkv, page, D] in pages of `page` positions, a power of two from 16 to 256.
+ *   cache_dtype FA_BF16: bf16.  FA_INT4: bytes, [n_pages, Hkv, page, 9 D / 16]; every 16 positions of a head are a unit
+ *   of 8 D bytes of codes and then D bytes of scales.  A value is scale * (code - 8), code in 1 .. 15, with one fp16
+ *   scale for 32 channels of one position.  Codes lie in 32-bit words, the lowest channel in the lowest bits; of position
+ *   p (in the unit) and channel c, with w = min(4, D / 32), g = c / 32 and the word's number
+ *   ((p / 8 * (D / 32 / w) + g / w) * 32 + lane) * w + g % w:
+ *     keys    lane = 4 (p % 8) + c % 32 / 8: 8 channels of a position
+ *     values  lane = 4 (c % 32 / 4) + p % 8 / 2: 4 channels of an even position in the low half, of the next in the high
+ *   and scales as [position][g] for keys, [position / 2][g][position % 2] for values.
+ *   table: device array of ints [B, slots]; position p of sequence b is row p % page of page table[b][p / page].  Only
+ *   entries of pages that a call needs are read; one outside [0, n_pages) reads as zeros and takes no rows, and
+ *   FA_ERR_PAGE is recorded in the device status word.  Sequences may share pages that are only read.
+ *   lens: device array of B ints, the keys each sequence holds, its new rows included.  capacity = slots * page.
+ * D in {64, 128, 256}; B, heads <= 65535; capacity <= 2^23; n_pages * Hkv <= 2^31 - 2^20.  Pages may take any
+ * amount of memory.
+ */
+
+/*
+ * fa_paged_append -- the n newest rows of each sequence: q and k rotated by their positions, k and v put in their pages.
+ *   q [B, Hq, n, D], k, v [B, Hkv, n, D] bf16; strides: host array of 9, the distances in elements between sequences,
+ *   heads and rows of q, of k and of v (multiples of 8; rows of D are contiguous), NULL: contiguous tensors.
+ *   Row i sits at position lens[b] - n + i.  counts (device array of B ints, NULL: n): the last counts[b] rows are new;
+ *   rows before them and rows before position 0 are left out.  q may be NULL (then Hq = 0 and q_out NULL);
+ *   q_out [B, Hq, n, D] contiguous, not q itself: rotated rows, zeros for rows that are left out or past the capacity.
+ *   Rotation of the first rot channels (a multiple of 16, 0: none, cos and sin may be NULL): with the pair (a, b) of
+ *   channels (c, c + rot / 2), or (2 c, 2 c + 1) with interleaved != 0, and cos, sin [positions, rot / 2] fp32 of the row's
+ *   position: a cos - b sin, b cos + a sin, rounded to bf16 once.  positions >= capacity.
+ *   FA_INT4: of 32 channels of the bf16 row y, scale = fp16(max |y| / 7) (65504 at most; NaN where y is not finite),
+ *   code = 8 + y fp32(1 / scale) rounded to even, in 1 .. 15.
+ * Positions that are not new keep what their pages hold, in the same unit too.  A page that takes rows belongs to one
+ * sequence, and no position is given twice.  One kernel.
+ */
+FA_API int fa_paged_append(const void *q, const void *k, const void *v, const long long *strides, const float *cos,
+                           const float *sin, const int *table, const int *lens, const int *counts, void *q_out,
+                           void *k_pages, void *v_pages, int B, int Hq, int Hkv, int n, int D, int rot, int interleaved,
+                           int positions, int n_pages, int page, int slots, int cache_dtype, void *stream);
+
+/*
+ * fa_paged_decode -- windowed attention of the n_q <= 16 newest rows of each sequence against its pages, as
+ * fa_window_decode: q, o [B, Hq, n_q, D] bf16, lse [B, Hq, n_q]; row i sits at position lens[b] - n_q + i and sees key j iff
+ * j <= p and (j < sinks or j > p - window); window >= capacity is plain causal attention.  lens outside [0, capacity] are
+ * taken as the nearer end, NULL: capacity.  Rows that see nothing get O = 0 and LSE = -inf.  Rows from lens[b] on, and
+ * those between the sinks and the first window, may hold anything, and pages of theirs alone need no entry.
+ *   workspace: fa_paged_decode_workspace_bytes(...) bytes, 16-byte aligned (NULL when that is 0; never more than 16 MB);
+ *   two calls that run concurrently must not share it.
+ */
+FA_API int fa_paged_decode(const void *q, const void *k_pages, const void *v_pages, const int *table, const int *lens,
+                           void *o, float *lse, int B, int Hq, int Hkv, int n_q, int D, int n_pages, int page, int slots,
+                           int window, int sinks, float scale, int cache_dtype, void *workspace, size_t workspace_bytes,
+                           void *stream);
+FA_API int fa_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q, int D, int page, int slots, int cache_dtype,
+                                           size_t *bytes);
+
+/*
+ * fa_paged_gather -- the sequences' rows out of their pages: k, v [B, Hkv, rows, D] bf16, of which the first
+ * min(lens[b], rows) of each head are written and the others left as they are (lens as for fa_paged_decode).  What a
+ * prompt's attention (fa_window_forward) reads.  One kernel.
+ */
+FA_API int fa_paged_gather(const void *k_pages, const void *v_pages, const int *table, const int *lens, void *k, void *v,
+                           int B, int Hkv, int rows, int D, int n_pages, int page, int slots, int cache_dtype, void *stream);
 
 /* Static description of a status code (never NULL). */
 FA_API const char *fa_status_string(int status);

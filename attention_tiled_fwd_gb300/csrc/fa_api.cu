@@ -952,12 +952,34 @@ extern "C" int fa_paged_append(const void *q, const void *k, const void *v, cons
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+namespace {
+// The grid of paged decode, and the partials of its CTAs.
+struct PagedGrid {
+    PagedPlan plan;
+    int row_tiles, ctas;
+    bool cut;  // whether a list can be cut
+    size_t partials() const { return (size_t)ctas * 2 * plan.rows; }
+    size_t bytes(int D) const { return cut ? partials() * ((size_t)D * 4 + 8) + (size_t)ctas * 8 : 0; }
+};
+
+PagedGrid paged_grid(int B, int Hq, int Hkv, int n_q, int D, int capacity, bool four, int num_sms) {
+    PagedGrid g;
+    const int R = Hq / Hkv * n_q;
+    g.plan = paged_plan(R, D, four);
+    g.row_tiles = (R + g.plan.rows - 1) / g.plan.rows;
+    const long long tiles = (capacity + g.plan.tile - 1) / g.plan.tile, lists = (long long)B * Hkv * g.row_tiles;
+    g.ctas = (int)std::min<long long>(lists * tiles, (long long)num_sms * g.plan.per_sm);
+    g.cut = tiles > 1;
+    return g;
+}
+}  // namespace
+
 extern "C" int fa_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q, int D, int page, int slots, int cache_dtype,
                                                size_t *bytes) {
     if (!bytes) return FA_ERR_NULL;
     int rc = check_paged_decode(B, Hq, Hkv, n_q, D, 1, page, slots, cache_dtype);
     if (rc != FA_OK) return rc;
-    *bytes = 0;
+    *bytes = paged_grid(B, Hq, Hkv, n_q, D, slots * page, cache_dtype == FA_INT4, current_num_sms()).bytes(D);
     return FA_OK;
 }
 
@@ -978,10 +1000,29 @@ extern "C" int fa_paged_decode(const void *q, const void *k_pages, const void *v
     DeviceState *st;
     rc = device_state(&dev, &st);
     if (rc != FA_OK) return rc;
+    const bool four = cache_dtype == FA_INT4;
+    const PagedGrid grid = paged_grid(B, Hq, Hkv, n_q, D, slots * page, four, st->num_sms);
+    if (grid.cut) {
+        rc = check_ptrs({workspace});
+        if (rc != FA_OK) return rc;
+        if (workspace_bytes < grid.bytes(D)) return FA_ERR_WORKSPACE;
+    }
     const WinArgs w = window_args(Hkv, slots * page, window, sinks);
-    const PagedDecodeArgs a{q, lens, o, lse, page_pool(k_pages, v_pages, table, Hkv, n_pages, page, slots), B, Hq / Hkv * n_q, n_q, D,
-                            w.window, w.sinks, scale * log2e(), st->status_word};
-    const cudaError_t e = launch_paged_decode(a, cache_dtype == FA_INT4, reinterpret_cast<cudaStream_t>(stream));
+    PagedDecodeArgs a{q, lens, o, lse, page_pool(k_pages, v_pages, table, Hkv, n_pages, page, slots), B, Hq / Hkv * n_q, n_q, D,
+                      w.window, w.sinks, scale * log2e(), st->status_word, grid.row_tiles, nullptr, nullptr, nullptr};
+    if (grid.cut) {
+        a.part_o = static_cast<float *>(workspace);
+        a.part_ml = reinterpret_cast<float2 *>(a.part_o + grid.partials() * D);
+        a.tails = reinterpret_cast<int2 *>(a.part_ml + grid.partials());
+    }
+    CUtensorMap tk{}, tv{};
+    if (!four) {
+        const int box = std::min(page, grid.plan.tile);
+        if (encode_rows(&tk, k_pages, n_pages * Hkv, page, page, D, box) != FA_OK ||
+            encode_rows(&tv, v_pages, n_pages * Hkv, page, page, D, box) != FA_OK)
+            return FA_ERR_CUDA;
+    }
+    const cudaError_t e = launch_paged_decode(a, four, grid.ctas, tk, tv, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -92,7 +92,20 @@ struct PagedDecodeArgs {
     int window, sinks;
     float scale_log2;
     int *status;
+    int row_tiles;     // CTAs that share a key head's rows
+    // two partials a CTA, [2 CTA + slot][rows of a tile]: O, (m, l); and the list that goes on behind a CTA (its number and
+    // its partials, -1: none).  All null where no list can be cut.
+    float *part_o;
+    float2 *part_ml;
+    int2 *tails;
 };
-cudaError_t launch_paged_decode(const PagedDecodeArgs &a, bool four, cudaStream_t s);
+// Keys of a tile, rows of a row tile, and CTAs an SM holds, for a decode of R rows a key head.
+struct PagedPlan {
+    int tile, rows, per_sm;
+};
+PagedPlan paged_plan(int R, int D, bool four);
+// tk, tv: the pools' tensor maps (bf16 pages: boxes of 64 columns and of the rows of a page, at most a tile's).
+cudaError_t launch_paged_decode(const PagedDecodeArgs &a, bool four, int ctas, const CUtensorMap &tk, const CUtensorMap &tv,
+                                cudaStream_t s);
 
 }  // namespace fa

@@ -35,6 +35,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * (kWarps + 1);
+constexpr float kNone = -3e38f;
 constexpr int kTinyScales = -22;  // E while no scale has reached 2^-15: they are taken times 2^15, the weights times 2^7
 constexpr int kJoinCols = 64;  // channels that the warps join at a time
 
@@ -145,6 +146,11 @@ struct Tiles {
     }
     __device__ __forceinline__ int tile(int i) const { return i < n_sink ? i : first + i - n_sink; }
 };
+
+// bit i: some row sees key k0 + i
+__device__ __forceinline__ uint32_t used_keys(const Tiles &t, int k0, int sinks) {
+    return low_bits(t.len - k0) & (~low_bits(t.lo - k0) | low_bits(sinks - k0));
+}
 
 // This CTA's run of the list of tiles.
 struct Run {
@@ -299,17 +305,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FOUR>::kCtas)
         const size_t first_row = ((size_t)run.b * a.pool.Hkv + h) * a.R + row0;
         const int p_first = max(0, tiles.len - a.n_q), p_last = tiles.len - 1;
 
-        float m[NT][2], l[NT][2], f[NT][2], o[NT][D / 16][4];
+        // off: the running maximum (log2 units), plus the weights' power of two; kNone while a row has seen nothing
+        float off[NT][2], l[NT][2], f[NT][2], o[NT][D / 16][4];
         auto position = [&](int r) { return tiles.len - a.n_q + (row0 + r) % a.n_q; };  // rows past R: any; they are not stored
         uint32_t qf[NT][D / 16][2];
-        float begin[FOUR ? NT : 1][kGroups][2], ones[FOUR ? NT : 1][4];  // 4 bits: -8 sum q of a group; sum P s of group g in row g
-        int E = kTinyScales;
+        uint32_t less[FOUR ? NT : 1][2];  // 4 bits: -8 sum q of each group as an operand against the keys' scales, in two parts
+        float ones[FOUR ? NT : 1][4];     // sum P s of group g in row g
+        int E = kTinyScales, Ep = FOUR ? -7 : 0;  // powers of two of the weights times scales, and of the weights
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                m[n][e] = -INFINITY, l[n][e] = 0.f, f[n][e] = a.scale_log2;
-            }
+            for (int e = 0; e < 2; ++e) off[n][e] = kNone, l[n][e] = 0.f, f[n][e] = a.scale_log2;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -337,14 +343,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FOUR>::kCtas)
                 most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
                 most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
                 // the row's largest magnitude becomes 2^14 .. 2^15 (a row of zeros or of the smallest numbers: less)
-                const int up = 14 - max(-100, (int)(most >> 23) - 127);
-                const float by = __int_as_float((127 + min(up, 114)) << 23);
+                const int up = min(114, 14 - max(-100, (int)(most >> 23) - 127));
+                const float by = __int_as_float((127 + up) << 23);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int shift = -__shfl_sync(0xffffffffu, min(up, 114), 4 * (2 * tq + e)) + 24;  // the codes' 2^-24 too
+                    const int shift = 24 - __shfl_sync(0xffffffffu, up, 4 * (2 * tq + e));  // the codes' 2^-24 too
                     f[n][e] = fmaxf(a.scale_log2 * __int_as_float((127 + shift / 2) << 23) * __int_as_float((127 + shift - shift / 2) << 23),
                                     1.2e-38f);  // (above 0: -inf times it stays -inf)
                 }
+                uint32_t part[2][kGroups];  // fp16 of -8 2^-24 sum q, and of what that leaves
 #pragma unroll
                 for (int j = 0; j < kGroups; ++j) {
                     const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
@@ -363,8 +370,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FOUR>::kCtas)
                     }
                     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    sum *= -0x1p-21f;
+                    const __half high = __float2half_rn(sum);
+                    part[0][j] = __half_as_ushort(high);
+                    part[1][j] = __half_as_ushort(__float2half_rn(sum - __half2float(high)));
+                }
+                // the operand's columns: the groups' first parts, then their second ones (lane tq: two columns of each eight)
+                less[n][0] = less[n][1] = 0u;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) begin[n][j][e] = -0x1p-21f * __shfl_sync(0xffffffffu, sum, 4 * (2 * tq + e));
+                for (int i = 0; i < kGroups; ++i) {
+                    const int at = i % (kGroups / 2), second = i / (kGroups / 2);
+                    const uint32_t two = part[second][2 * at] | part[second][2 * at + 1] << 16;
+                    if (tq == i % 4) less[n][i / 4] = two;
                 }
             }
         }
@@ -373,16 +390,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FOUR>::kCtas)
             if (ok) ok = warp_wait(&full[stage], phase, a.status, kSiteFull);
             if (ok) {
                 const int key_tile = tiles.tile(t) * kTile;
-#pragma unroll 1
+                const uint8_t *ks = smem + stage * 2 * C::kHalf, *vs = ks + C::kHalf;
+                const int mi = lane >> 3, mr = lane & 7;
+                // every key of the tile exists, and every row sees it
+                const bool plain = key_tile + kTile <= tiles.len && all_seen(p_first, p_last, key_tile, key_tile + kTile - 1, a.window, a.sinks);
+                float sc[C::kUnits][NT][4];  // S^T of the warp's units: keys g and g + 8, rows 2 tq and 2 tq + 1
+#pragma unroll
                 for (int w = 0; w < C::kUnits; ++w) {
                     const int unit = w * kWarps + warp, key0 = key_tile + unit * kUnit;
-                    // every key of the unit exists, and every row sees it
-                    const bool plain = key0 + kUnit <= tiles.len && all_seen(p_first, p_last, key0, key0 + kUnit - 1, a.window, a.sinks);
-                    const uint8_t *ks = smem + stage * 2 * C::kHalf, *vs = ks + C::kHalf;
-                    float sc[NT][4];  // S^T: keys g and g + 8, rows 2 tq and 2 tq + 1
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
-                    const int mi = lane >> 3, mr = lane & 7;
+                    for (int n = 0; n < NT; ++n) sc[w][n][0] = sc[w][n][1] = sc[w][n][2] = sc[w][n][3] = 0.f;
                     if constexpr (!FOUR) {
                         const uint32_t row = kUnit * unit + mr + (mi & 1) * 8;
 #pragma unroll
@@ -391,14 +408,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FOUR>::kCtas)
                             const uint32_t chunk = (i & 3) * 2 + (mi >> 1);
                             ldsm4(kf, smem_u32(ks) + (i >> 2) * (kTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4));
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) mma16816(sc[n], kf, qf[n][i][0], qf[n][i][1]);
+                            for (int n = 0; n < NT; ++n) mma16816(sc[w][n], kf, qf[n][i][0], qf[n][i][1]);
                         }
                     } else {
-                        const uint8_t *at = ks + unit * U::kBytes;
-                        uint32_t code[2][kGroups], s2[2][kGroups / 2];
+                        const uint8_t *at = ks + unit * U::kBytes, *scales = at + U::kCodes;
+                        uint32_t code[2][kGroups], s2[2][kGroups / 2], by[4];
                         load_codes<D>(code, at, lane);
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) load_words(s2[half], at + U::kCodes + 2 * U::k_scale(g + 8 * half, 0));
+                        for (int half = 0; half < 2; ++half) {
+                            load_words(s2[half], scales + 2 * U::k_scale(g + 8 * half, 0));
+                            by[half] = by[2 + half] = *reinterpret_cast<const uint32_t *>(scales + 2 * U::k_scale(g + 8 * half, 2 * (tq % (kGroups / 2))));
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma_f16(sc[w][n], by, less[n][0], less[n][1], sc[w][n]);
 #pragma unroll
                         for (int j = 0; j < kGroups; ++j) {
                             uint32_t x[4], y[4];
@@ -412,52 +434,72 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FOUR>::kCtas)
                             const float s_lo = j & 1 ? sa.y : sa.x, s_hi = j & 1 ? sb.y : sb.x;
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                float part[4] = {begin[n][j][0], begin[n][j][1], begin[n][j][0], begin[n][j][1]};
+                                float part[4] = {0.f, 0.f, 0.f, 0.f};
                                 mma_f16(part, x, qf[n][2 * j][0], qf[n][2 * j][1], part);
                                 mma_f16(part, y, qf[n][2 * j + 1][0], qf[n][2 * j + 1][1], part);
-                                sc[n][0] = fmaf(s_lo, part[0], sc[n][0]), sc[n][1] = fmaf(s_lo, part[1], sc[n][1]);
-                                sc[n][2] = fmaf(s_hi, part[2], sc[n][2]), sc[n][3] = fmaf(s_hi, part[3], sc[n][3]);
+                                sc[w][n][0] = fmaf(s_lo, part[0], sc[w][n][0]), sc[w][n][1] = fmaf(s_lo, part[1], sc[w][n][1]);
+                                sc[w][n][2] = fmaf(s_hi, part[2], sc[w][n][2]), sc[w][n][3] = fmaf(s_hi, part[3], sc[w][n][3]);
                             }
                         }
                     }
-                    // values of keys that no row sees: cleared, so that 0 times whatever they hold cannot reach O
-                    uint32_t keep[2] = {~0u, ~0u};
                     if (!plain) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const uint32_t seen = seen_keys(position(8 * n + 2 * tq + e), key0, a.window, a.sinks);
-                                if (!(seen >> g & 1u)) sc[n][e] = -INFINITY;
-                                if (!(seen >> (g + 8) & 1u)) sc[n][2 + e] = -INFINITY;
+                                if (!(seen >> g & 1u)) sc[w][n][e] = -INFINITY;
+                                if (!(seen >> (g + 8) & 1u)) sc[w][n][2 + e] = -INFINITY;
                             }
-                        keep_seen(keep, low_bits(tiles.len - key0) & (~low_bits(tiles.lo - key0) | low_bits(a.sinks - key0)), tq);
                     }
-                    uint32_t s2[FOUR ? 2 : 1][kGroups];  // scales of the values of keys 2 tq and 2 tq + 1 (+ 8)
-                    bool grow = false;
-                    if constexpr (FOUR) {
+                }
+
+                // scales of the values of keys 2 tq and 2 tq + 1 (+ 8)
+                uint32_t s2[FOUR ? C::kUnits : 1][2][kGroups];
+                if constexpr (FOUR) {
+                    uint32_t bits = 0;
+#pragma unroll
+                    for (int w = 0; w < C::kUnits; ++w) {
+                        const int unit = w * kWarps + warp;
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) load_words(s2[w][half], vs + unit * U::kBytes + U::kCodes + 2 * U::v_scale(2 * tq + 8 * half, 0));
+                        if (!plain) {
+                            // keys that no row sees: 0 times whatever their scales are must not reach O.  (A row's own keys alone
+                            // where a lane holds one row: what other rows see may be no number either.)
+                            const int key0 = key_tile + unit * kUnit;
+                            uint32_t keep[2];
+                            keep_seen(keep, NT == 1 ? seen_keys(position(g), key0, a.window, a.sinks) : used_keys(tiles, key0, a.sinks), tq);
+#pragma unroll
+                            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                                for (int j = 0; j < kGroups; ++j) s2[w][half][j] &= keep[half];
+                        }
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+#pragma unroll
+                            for (int j = 0; j < kGroups; ++j) bits |= s2[w][half][j];
+                    }
+                    // A weight is 2^8 at most, so its products with scales below 2^(E + 7) fit in fp16.  The scales' bits
+                    // together are no less than the largest (and less than twice it, or all of 2^(1 + k) - 1 exponents).
+                    const uint32_t limit = max((uint32_t)(E + 7 + 15) << 10, 0x200u);  // 2^(E + 7)
+                    if (__any_sync(0xffffffffu, E < 9 && (bits + (0x8000u - limit) * 0x10001u) & 0x80008000u)) {
                         uint32_t most = 0;
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            load_words(s2[half], vs + unit * U::kBytes + U::kCodes + 2 * U::v_scale(2 * tq + 8 * half, 0));
+                        for (int w = 0; w < C::kUnits; ++w)
 #pragma unroll
-                            for (int j = 0; j < kGroups; ++j) {
-                                if (!plain) s2[half][j] &= keep[half];
-                                most = max_h2(most, s2[half][j] & 0x7fff7fffu);
-                            }
-                        }
+                            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                                for (int j = 0; j < kGroups; ++j) most = max_h2(most, s2[w][half][j]);
                         const float2 mh = unpack_h2(most);
-                        // products of weights of 2^8 at most and these scales fit in fp16 below 2^(E + 7)
-                        const float big = fmaxf(mh.x, mh.y);
-                        if (__any_sync(0xffffffffu, E < 9 && big >= __int_as_float((127 + 7 + E) << 23))) {
-                            const uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
-                            const int to = max(-7, min(9, (int)(all >> 23) - 127 - 6));
-                            const float by = __int_as_float((127 + E - to) << 23), by_l = __int_as_float((127 + max(-7, E) - to) << 23);
-                            E = to;
+                        const uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(mh.x, mh.y)));
+                        const int need = (int)(all >> 23) - 127 - 6;
+                        if (need > E) {
+                            const int to = max(-6, min(9, need));
+                            const float by = __int_as_float((127 + E - to) << 23), by_l = __int_as_float((127 + Ep - to) << 23);
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
 #pragma unroll
-                                for (int e = 0; e < 2; ++e) l[n][e] *= by_l;
+                                for (int e = 0; e < 2; ++e) l[n][e] *= by_l, off[n][e] += (float)(to - Ep);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     ones[n][e] *= by;
@@ -465,52 +507,70 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FOUR>::kCtas)
                                     for (int i = 0; i < D / 16; ++i) o[n][i][e] *= by;
                                 }
                             }
+                            E = Ep = to;
                         }
                     }
-                    if (FOUR && E == kTinyScales) {
+                    if (E == kTinyScales) {
 #pragma unroll
-                        for (int j = 0; j < kGroups; ++j) s2[0][j] = mul_h2(s2[0][j], 0x78007800u), s2[FOUR][j] = mul_h2(s2[FOUR][j], 0x78007800u);
+                        for (int w = 0; w < C::kUnits; ++w)
+#pragma unroll
+                            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                                for (int j = 0; j < kGroups; ++j) s2[w][half][j] = mul_h2(s2[w][half][j], 0x78007800u);
                     }
-                    // rescale only when a maximum grows by more than 2^8
+                }
+
+                // the weights' logarithms; the maxima are taken again only when a weight would grow past 2^8
+                bool grow = false;
+                auto logs = [&](int w, int n, int e) { return fmaf(sc[w][n][e], f[n][e & 1], -off[n][e & 1]); };
+                const float limit = 8.f - (FOUR ? (float)Ep : 0.f);
+#pragma unroll
+                for (int w = 0; w < C::kUnits; ++w)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        grow |= fmaxf(fmax3(logs(w, n, 0), logs(w, n, 1), logs(w, n, 2)), logs(w, n, 3)) > limit;
+                if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) grow |= fmaxf(sc[n][e], sc[n][2 + e]) * f[n][e] > m[n][e] + 8.f;
-                    if (__any_sync(0xffffffffu, grow)) {
+                        for (int e = 0; e < 2; ++e) {
+                            float mt = -INFINITY;
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
+                            for (int w = 0; w < C::kUnits; ++w) mt = fmax3(mt, sc[w][n][e], sc[w][n][2 + e]);
+                            mt *= f[n][e];
+                            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
+                            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
+                            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+                            mt += (float)Ep;
+                            if (mt > off[n][e] + 8.f) {
+                                const float alpha = ex2_approx(off[n][e] - mt);
+                                l[n][e] *= alpha;
+                                if constexpr (FOUR) ones[n][e] *= alpha, ones[n][2 + e] *= alpha;
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float mt = fmaxf(sc[n][e], sc[n][2 + e]) * f[n][e];
-                                mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
-                                mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
-                                mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-                                if (mt > m[n][e] + 8.f) {
-                                    const float alpha = ex2_approx(m[n][e] - mt);
-                                    l[n][e] *= alpha;
-                                    if constexpr (FOUR) ones[n][e] *= alpha, ones[n][2 + e] *= alpha;
-#pragma unroll
-                                    for (int i = 0; i < D / 16; ++i) o[n][i][e] *= alpha, o[n][i][2 + e] *= alpha;
-                                    m[n][e] = mt;
-                                }
+                                for (int i = 0; i < D / 16; ++i) o[n][i][e] *= alpha, o[n][i][2 + e] *= alpha;
+                                off[n][e] = mt;
                             }
-                    }
+                        }
+                }
+
+#pragma unroll
+                for (int w = 0; w < C::kUnits; ++w) {
+                    const int unit = w * kWarps + warp, key0 = key_tile + unit * kUnit;
                     uint32_t pb[NT][2];  // P^T as the second product's operand: row g, keys 2 tq and 2 tq + 1 (+ 8)
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float p[4];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float off = (m[n][e] == -INFINITY ? 0.f : m[n][e]) + (FOUR ? max(-7, E) : 0);
-                            p[e] = ex2_approx(fmaf(sc[n][e], f[n][e], -off));
-                            p[2 + e] = ex2_approx(fmaf(sc[n][2 + e], f[n][e], -off));
-                            l[n][e] += p[e] + p[2 + e];  // this lane's keys, not rounded; the others' are added at the end
-                        }
+                        for (int e = 0; e < 4; ++e) p[e] = ex2_approx(logs(w, n, e));
+                        // this lane's keys, not rounded; the others' are added at the end
+                        l[n][0] += p[0] + p[2], l[n][1] += p[1] + p[3];
                         // the weights as operands: bf16 (half a step: up to 2^-8), or fp16 (2^-11)
                         pb[n][0] = transpose8(FOUR ? pack_h2(p[0], p[1]) : pack_bf16x2(p[0], p[1]));
                         pb[n][1] = transpose8(FOUR ? pack_h2(p[2], p[3]) : pack_bf16x2(p[2], p[3]));
                     }
                     if constexpr (!FOUR) {
+                        uint32_t keep[2] = {~0u, ~0u};
+                        if (!plain) keep_seen(keep, used_keys(tiles, key0, a.sinks), tq);
                         const uint32_t row = kUnit * unit + mr + (mi >> 1) * 8;
                         auto values = [&](uint32_t(&vf)[4], int i, const uint32_t(&only)[2]) {
                             const uint32_t chunk = (i & 3) * 2 + (mi & 1);
@@ -561,11 +621,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FOUR>::kCtas)
                     } else {
                         uint32_t code[2][kGroups];
                         load_codes<D>(code, vs + unit * U::kBytes, lane);
-                        uint32_t sees[NT][2];  // row g: the keys that it sees
+                        uint32_t sees[NT][2];  // row g's own keys, where a lane holds two rows
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             sees[n][0] = sees[n][1] = ~0u;
-                            if (!plain) keep_seen(sees[n], seen_keys(position(8 * n + g), key0, a.window, a.sinks), tq);
+                            if (NT > 1 && !plain) keep_seen(sees[n], seen_keys(position(8 * n + g), key0, a.window, a.sinks), tq);
                         }
 #pragma unroll
                         for (int j = 0; j < kGroups; ++j) {
@@ -579,7 +639,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FOUR>::kCtas)
                             const uint32_t one = g == j ? 0x3c003c00u : 0u, row_j[4] = {one, 0u, one, 0u};
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                const uint32_t b0 = mul_h2(pb[n][0], s2[0][j]) & sees[n][0], b1 = mul_h2(pb[n][1], s2[1][j]) & sees[n][1];
+                                uint32_t b0 = mul_h2(pb[n][0], s2[w][0][j]), b1 = mul_h2(pb[n][1], s2[w][1][j]);
+                                if (NT > 1) b0 &= sees[n][0], b1 &= sees[n][1];
                                 mma_f16(o[n][2 * j], x, b0, b1, o[n][2 * j]);
                                 mma_f16(o[n][2 * j + 1], y, b0, b1, o[n][2 * j + 1]);
                                 mma_f16(ones[n], row_j, b0, b1, ones[n]);
@@ -609,7 +670,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FOUR>::kCtas)
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) o[n][i][e] *= 0x1p-15f;
                 }
-            E = -7;
         }
         float *buf = reinterpret_cast<float *>(smem + C::kJoinOff);  // [warp][place][8 rows]
         float2 *ml = reinterpret_cast<float2 *>(smem + C::kMlOff);   // [warp][8 rows]
@@ -624,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FOUR>::kCtas)
 #pragma unroll
             for (int c = 0; c < D / kJoinCols; ++c) {
                 asm volatile("bar.sync 1, 128;" ::: "memory");  // the buffer is free
-                if (c == 0 && g < 2) ml[8 * warp + 2 * tq + g] = make_float2(m[n][g & 1] + (FOUR ? E : 0), l[n][g & 1]);
+                if (c == 0 && g < 2) ml[8 * warp + 2 * tq + g] = make_float2(l[n][g & 1] == 0.f ? -INFINITY : off[n][g & 1], l[n][g & 1]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float *to = buf + warp * (kJoinCols * 8) + 2 * tq;
@@ -665,7 +725,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FOUR>::kCtas)
                         acc.x = fmaf(buf[w * (kJoinCols * 8) + at * 8 + r], fw, acc.x);
                         acc.y = fmaf(buf[w * (kJoinCols * 8) + next * 8 + r], fw, acc.y);
                     }
-                    if (ls != ls) M = Mb;  // scores that are NaN leave m at -inf, which would read as "sees nothing"
                     const int row = 8 * n + r, col = kJoinCols * c + ch;
                     if (row0 + row >= a.R) continue;
                     if (whole) {

@@ -4,13 +4,16 @@
         [--reps R] [--dtype bf16|f32] [--std S]
     python -m attention_tiled_fwd_gb300.run_case B H N D --window W [--sinks S] [--kv-heads G] [--backward | --tokens]
     python -m attention_tiled_fwd_gb300.run_case B H N D --prefix P [--kv-heads G]
+    python -m attention_tiled_fwd_gb300.run_case B H N D --paged PAGE [--four] [--kv-heads G] [--rows n]
 
 Each repetition runs fa_forward and, with --backward, fa_backward_dq and
 fa_backward_dkdv, on seeded synthetic inputs (seed 4242, the benchmark's
 generator).  With --window it runs fa_window_forward (and fa_window_backward), or
 with --tokens fa_window_decode of one new row per sequence against a full cache of
 N keys; with --prefix fa_prefix_decode of one new row per sequence behind P shared
-keys and N of its own (standard normal inputs, the same seed).  A profiler pointed at one kernel with a launch skip of 1 sees the
+keys and N of its own (standard normal inputs, the same seed).  With --paged it
+appends N rows to every sequence's pages (with --four 4-bit ones), decodes the last n
+(default 1) against them and gathers them.  A profiler pointed at one kernel with a launch skip of 1 sees the
 second, warm launch.  Exits non-zero if the device status word reports a
 failed wait.
 """
@@ -39,6 +42,9 @@ def main(argv=None) -> int:
     ap.add_argument("--kv-heads", type=int)
     ap.add_argument("--tokens", action="store_true")
     ap.add_argument("--prefix", type=int)
+    ap.add_argument("--paged", type=int)
+    ap.add_argument("--four", action="store_true")
+    ap.add_argument("--rows", type=int, default=1)
     a = ap.parse_args(argv)
 
     sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
@@ -46,6 +52,8 @@ def main(argv=None) -> int:
     from synthetic_inputs import make_qkv
 
     dev = torch.device("cuda:0")
+    if a.paged is not None:
+        return paged(fa, a, dev)
     if a.window is not None or a.prefix is not None:
         return grouped(fa, a, dev)
     h = make_qkv(a.B, a.H, a.N, a.D, 4242, a.dtype, a.std, with_dO=a.backward)
@@ -86,6 +94,23 @@ def grouped(fa, a, dev) -> int:
         return report(fa, a, f"kv heads {G}", f"prefix {a.prefix}")
     return report(fa, a, f"kv heads {G}", f"window {a.window} sinks {a.sinks}",
                   "tokens" if a.tokens else "fwd+bwd" if a.backward else "fwd")
+
+
+def paged(fa, a, dev) -> int:
+    """The paged cache's calls, with pages in a random order and rows from one projection's output."""
+    G, slots = a.kv_heads or a.H, -(-a.N // a.paged)
+    g = torch.Generator(device=dev)
+    g.manual_seed(4242)
+    pages = fa.paged_cache(a.B * slots, G, a.paged, a.D, fa.FA_INT4 if a.four else fa.FA_BF16, dev)
+    table = torch.randperm(a.B * slots, generator=g, device=dev).to(torch.int32).view(a.B, slots)
+    lens = torch.full((a.B,), a.N, dtype=torch.int32, device=dev)
+    cos, sin = fa.rotation_table(slots * a.paged, a.D, device=dev)
+    qkv = torch.randn((a.B, a.N, a.H + 2 * G, a.D), generator=g, device=dev, dtype=torch.bfloat16).transpose(1, 2)
+    for _ in range(a.reps):
+        q = fa.fa_paged_append(qkv[:, a.H:a.H + G], qkv[:, a.H + G:], *pages, table, lens, q=qkv[:, :a.H], cos=cos, sin=sin)
+        fa.fa_paged_decode(q[:, :, -a.rows:].contiguous(), *pages, table, lens, window=a.window, sinks=a.sinks)
+        fa.fa_paged_gather(*pages, table, lens)
+    return report(fa, a, f"kv heads {G}", f"pages of {a.paged}", "4 bits" if a.four else "bf16")
 
 
 def report(fa, a, *what) -> int:

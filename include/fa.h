@@ -325,7 +325,7 @@ FA_API int fa_prefix_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q, int
  *   k_pages, v_pages: [n_pages, Hkv, page, D] in pages of `page` positions, a power of two from 16 to 256.
  *   cache_dtype FA_BF16: bf16.  FA_INT4: bytes, [n_pages, Hkv, page, 9 D / 16]; every 16 positions of a head are a unit
  *   of 8 D bytes of codes and then D bytes of scales.  A value is scale * (code - 8), code in 1 .. 15, with one fp16
- *   scale for 32 channels of one position.  Codes lie in 32-bit words, the lowest channel in the lowest bits; of position
+ *   scale, not negative, for 32 channels of one position.  Codes lie in 32-bit words, the lowest channel in the lowest bits; of position
  *   p (in the unit) and channel c, with w = min(4, D / 32), g = c / 32 and the word's number
  *   ((p / 8 * (D / 32 / w) + g / w) * 32 + lane) * w + g % w:
  *     keys    lane = 4 (p % 8) + c % 32 / 8: 8 channels of a position

@@ -63,10 +63,16 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
 }
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same from zero.
+__device__ __forceinline__ void mma_f16_new(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 // The 8 x 8 matrix of 16-bit values that the warp holds, a row in four lanes, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -74,31 +80,33 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
+// N words from shared memory.
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p) {
-    if constexpr (N == 2) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        w[0] = v.x, w[1] = v.y;
-    } else if constexpr (N == 1) {
-        w[0] = *reinterpret_cast<const uint32_t *>(p);
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], uint32_t at) {
+    if constexpr (N == 1) {
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
+    } else if constexpr (N == 2) {
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
     } else {
 #pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-            const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
-            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-        }
+        for (int i = 0; i < N; i += 4)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                         : "r"(at + 4 * i)
+                         : "memory");
     }
 }
 // A lane's words of both halves of a unit's codes, group by group.
 template <int D>
-__device__ __forceinline__ void load_codes(uint32_t (&w)[2][D / 32], const uint8_t *unit, int lane) {
+__device__ __forceinline__ void load_codes(uint32_t (&w)[2][D / 32], uint32_t unit, int lane) {
     using U = Unit4<D>;
+    const uint32_t at = unit + 4 * U::kWide * lane;
 #pragma unroll
     for (int half = 0; half < 2; ++half)
 #pragma unroll
         for (int g = 0; g < U::kGroups; g += U::kWide) {
             uint32_t v[U::kWide];
-            load_words(v, unit + 4 * U::word(half, g, lane));
+            load_words(v, at + 4 * U::word(half, g, 0));
 #pragma unroll
             for (int i = 0; i < U::kWide; ++i) w[half][g + i] = v[i];
         }
@@ -390,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FOUR>::kCtas)
             if (ok) ok = warp_wait(&full[stage], phase, a.status, kSiteFull);
             if (ok) {
                 const int key_tile = tiles.tile(t) * kTile;
-                const uint8_t *ks = smem + stage * 2 * C::kHalf, *vs = ks + C::kHalf;
+                const uint32_t ks = smem_u32(smem) + stage * 2 * C::kHalf, vs = ks + C::kHalf;
                 const int mi = lane >> 3, mr = lane & 7;
                 // every key of the tile exists, and every row sees it
                 const bool plain = key_tile + kTile <= tiles.len && all_seen(p_first, p_last, key_tile, key_tile + kTile - 1, a.window, a.sinks);
@@ -398,29 +406,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FOUR>::kCtas)
 #pragma unroll
                 for (int w = 0; w < C::kUnits; ++w) {
                     const int unit = w * kWarps + warp, key0 = key_tile + unit * kUnit;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) sc[w][n][0] = sc[w][n][1] = sc[w][n][2] = sc[w][n][3] = 0.f;
                     if constexpr (!FOUR) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) sc[w][n][0] = sc[w][n][1] = sc[w][n][2] = sc[w][n][3] = 0.f;
                         const uint32_t row = kUnit * unit + mr + (mi & 1) * 8;
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
                             uint32_t kf[4];  // 16-byte chunk c of row r of a 64-column panel sits at c ^ (r % 8)
                             const uint32_t chunk = (i & 3) * 2 + (mi >> 1);
-                            ldsm4(kf, smem_u32(ks) + (i >> 2) * (kTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4));
+                            ldsm4(kf, ks + (i >> 2) * (kTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4));
 #pragma unroll
                             for (int n = 0; n < NT; ++n) mma16816(sc[w][n], kf, qf[n][i][0], qf[n][i][1]);
                         }
                     } else {
-                        const uint8_t *at = ks + unit * U::kBytes, *scales = at + U::kCodes;
+                        const uint32_t at = ks + unit * U::kBytes, scales = at + U::kCodes;
                         uint32_t code[2][kGroups], s2[2][kGroups / 2], by[4];
                         load_codes<D>(code, at, lane);
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             load_words(s2[half], scales + 2 * U::k_scale(g + 8 * half, 0));
-                            by[half] = by[2 + half] = *reinterpret_cast<const uint32_t *>(scales + 2 * U::k_scale(g + 8 * half, 2 * (tq % (kGroups / 2))));
+                            uint32_t two[1];
+                            load_words(two, scales + 2 * U::k_scale(g + 8 * half, 2 * (tq % (kGroups / 2))));
+                            by[half] = by[2 + half] = two[0];
                         }
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_f16(sc[w][n], by, less[n][0], less[n][1], sc[w][n]);
+                        for (int n = 0; n < NT; ++n) mma_f16_new(sc[w][n], by, less[n][0], less[n][1]);
 #pragma unroll
                         for (int j = 0; j < kGroups; ++j) {
                             uint32_t x[4], y[4];
@@ -434,9 +444,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FOUR>::kCtas)
                             const float s_lo = j & 1 ? sa.y : sa.x, s_hi = j & 1 ? sb.y : sb.x;
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                float part[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma_f16(part, x, qf[n][2 * j][0], qf[n][2 * j][1], part);
-                                mma_f16(part, y, qf[n][2 * j + 1][0], qf[n][2 * j + 1][1], part);
+                                float part[4];
+                                mma_f16_new(part, x, qf[n][2 * j][0], qf[n][2 * j][1]);
+                                mma_f16(part, y, qf[n][2 * j + 1][0], qf[n][2 * j + 1][1]);
                                 sc[w][n][0] = fmaf(s_lo, part[0], sc[w][n][0]), sc[w][n][1] = fmaf(s_lo, part[1], sc[w][n][1]);
                                 sc[w][n][2] = fmaf(s_hi, part[2], sc[w][n][2]), sc[w][n][3] = fmaf(s_hi, part[3], sc[w][n][3]);
                             }
@@ -574,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FOUR>::kCtas)
                         const uint32_t row = kUnit * unit + mr + (mi >> 1) * 8;
                         auto values = [&](uint32_t(&vf)[4], int i, const uint32_t(&only)[2]) {
                             const uint32_t chunk = (i & 3) * 2 + (mi & 1);
-                            ldsm4t(vf, smem_u32(vs) + (i >> 2) * (kTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4));
+                            ldsm4t(vf, vs + (i >> 2) * (kTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4));
                             if (!plain) vf[0] &= only[0], vf[1] &= only[0], vf[2] &= only[1], vf[3] &= only[1];
                         };
                         bool finite = true;
@@ -641,9 +651,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FOUR>::kCtas)
                             for (int n = 0; n < NT; ++n) {
                                 uint32_t b0 = mul_h2(pb[n][0], s2[w][0][j]), b1 = mul_h2(pb[n][1], s2[w][1][j]);
                                 if (NT > 1) b0 &= sees[n][0], b1 &= sees[n][1];
-                                mma_f16(o[n][2 * j], x, b0, b1, o[n][2 * j]);
-                                mma_f16(o[n][2 * j + 1], y, b0, b1, o[n][2 * j + 1]);
-                                mma_f16(ones[n], row_j, b0, b1, ones[n]);
+                                mma_f16(o[n][2 * j], x, b0, b1);
+                                mma_f16(o[n][2 * j + 1], y, b0, b1);
+                                mma_f16(ones[n], row_j, b0, b1);
                             }
                         }
                     }

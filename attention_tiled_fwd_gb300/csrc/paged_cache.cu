@@ -13,6 +13,7 @@
 #include "fa_internal.h"
 #include "paged.cuh"
 #include "sm100_ptx.cuh"
+#include <algorithm>
 #include <cuda_fp16.h>
 
 namespace fa {
@@ -28,7 +29,7 @@ __device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) { return i ==
 
 // a c + b s rounded to fp32 so that rounding that to bf16 is rounding the exact sum: TwoSum of the products with their
 // errors (Knuth; Dekker), and a sum that lies halfway between two bf16 values is moved one step to its side.
-__device__ __noinline__ float turn_exact(float a, float c, float b, float s) {
+__device__ __forceinline__ float turn_exact(float a, float c, float b, float s) {
     const float p = __fmul_rn(a, c), pe = __fmaf_rn(a, c, -p);
     const float w = __fmul_rn(b, s), we = __fmaf_rn(b, s, -w);
     const float h = __fadd_rn(p, w), bb = __fsub_rn(h, p);
@@ -39,6 +40,17 @@ __device__ __noinline__ float turn_exact(float a, float c, float b, float s) {
     if (!(fabsf(y) < INFINITY)) return __fmaf_rn(a, c, w);
     if ((bits & 0xffffu) == 0x8000u && rest != 0.f) return __uint_as_float(bits + ((rest > 0.f) == (y > 0.f) ? 1 : -1));
     return y;
+}
+
+constexpr float kSlack = 0x1.00001p-24f;
+
+// Two channels of a chunk that has one of those: the sums that do not round alike are computed again.
+__device__ __noinline__ uint32_t turn_pair(uint32_t xa, uint32_t xb, float c0, float c1, float s0, float s1) {
+    const float w0 = bf_lo(xb) * s0, w1 = bf_hi(xb) * s1, v0 = fmaf(bf_lo(xa), c0, w0), v1 = fmaf(bf_hi(xa), c1, w1);
+    const float e0 = fabsf(v0) + fabsf(w0), e1 = fabsf(v1) + fabsf(w1);
+    const uint32_t y = pack_bf16x2(__fmaf_ru(e0, kSlack, v0), __fmaf_ru(e1, kSlack, v1));
+    if (y == pack_bf16x2(__fmaf_rd(e0, -kSlack, v0), __fmaf_rd(e1, -kSlack, v1))) return y;
+    return pack_bf16x2(turn_exact(bf_lo(xa), c0, bf_lo(xb), s0), turn_exact(bf_hi(xa), c1, bf_hi(xb), s1));
 }
 
 // The rotation of a lane's 8 channels: its own times cos plus their partners' times (signed) sin.
@@ -84,27 +96,22 @@ struct Turn {
             o.w = __shfl_sync(0xffffffffu, x.w, from);
         }
         if (!on) return x;
-        float y[8];
-        uint32_t near = 0;
+        uint32_t y[4], near = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float xa = i & 1 ? bf_hi(word_of(x, i / 2)) : bf_lo(word_of(x, i / 2));
-            const float xb = i & 1 ? bf_hi(word_of(o, i / 2)) : bf_lo(word_of(o, i / 2));
-            const float w = xb * s[i];
-            y[i] = fmaf(xa, c[i], w);
-            // y is off by half a step of itself and of w at most: 2^-24 (|y| + |w|); twice that is looked at
-            const float e = (fabsf(y[i]) + fabsf(w)) * 0x1p-23f;
-            near |= (__float_as_uint(y[i] + e) + 0x8000u) ^ (__float_as_uint(y[i] - e) + 0x8000u);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t xa = word_of(x, i), xb = word_of(o, i);
+            const float w0 = bf_lo(xb) * s[2 * i], w1 = bf_hi(xb) * s[2 * i + 1];
+            const float v0 = fmaf(bf_lo(xa), c[2 * i], w0), v1 = fmaf(bf_hi(xa), c[2 * i + 1], w1);
+            // v is off by half a step of itself and of w at most, 2^-24 (|v| + |w|): does all of that round alike?
+            const float e0 = fabsf(v0) + fabsf(w0), e1 = fabsf(v1) + fabsf(w1);
+            y[i] = pack_bf16x2(__fmaf_ru(e0, kSlack, v0), __fmaf_ru(e1, kSlack, v1));
+            near |= y[i] ^ pack_bf16x2(__fmaf_rd(e0, -kSlack, v0), __fmaf_rd(e1, -kSlack, v1));
         }
-        if (near >> 16) {
+        if (near) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float xa = i & 1 ? bf_hi(word_of(x, i / 2)) : bf_lo(word_of(x, i / 2));
-                const float xb = i & 1 ? bf_hi(word_of(o, i / 2)) : bf_lo(word_of(o, i / 2));
-                y[i] = turn_exact(xa, c[i], xb, s[i]);
-            }
+            for (int i = 0; i < 4; ++i) y[i] = turn_pair(word_of(x, i), word_of(o, i), c[2 * i], c[2 * i + 1], s[2 * i], s[2 * i + 1]);
         }
-        return make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+        return make_uint4(y[0], y[1], y[2], y[3]);
     }
 };
 
@@ -119,49 +126,52 @@ struct NewRows {
     }
 };
 
-// Rows of one token: lane `cl` of a row's D / 8 holds 8 channels, of kHeadsPerLane heads in turn.  Heads: q's, then (bf16
-// pages) k's and v's.
+// Rows of one token and tensor: lane `cl` of a row's D / 8 holds 8 channels, of kHeadsPerLane heads in turn.  `part`: the
+// block of q's heads, then (bf16 pages) of k's, then of v's.
 template <int D, bool FOUR>
-__device__ void token_rows(const AppendArgs &a, int task) {
+__device__ __forceinline__ void token_rows(const AppendArgs &a, int b, int i, int part) {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBlock = kRows * kHeadsPerLane;
     const int lane = threadIdx.x & 31, cl = lane % kLanes, sub = lane / kLanes;
-    const int Hkv = a.pool.Hkv, heads = a.Hq + (FOUR ? 0 : 2 * Hkv), blocks = (heads + kBlock - 1) / kBlock;
-    const int token = task / blocks, h0 = task % blocks * kBlock, b = token / a.n, i = token % a.n;
+    const int q_parts = (a.Hq + kBlock - 1) / kBlock, kv_parts = (a.pool.Hkv + kBlock - 1) / kBlock;
+    const bool is_q = FOUR || part < q_parts, is_k = !is_q && part < q_parts + kv_parts;
+    if (!is_q) part -= is_k ? q_parts : q_parts + kv_parts;
+    const int heads = is_q ? a.Hq : a.pool.Hkv, h0 = part * kBlock + sub;
+    const long long *st = is_q ? a.sq : is_k ? a.sk : a.sv;
+    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(is_q ? a.q : is_k ? a.k : a.v) + b * st[0] + h0 * st[1] + i * st[2] + 8 * cl;
+    uint4 x[kHeadsPerLane];  // (rows that are not new too: the loads need not wait for the lengths)
+#pragma unroll
+    for (int u = 0; u < kHeadsPerLane; ++u) {
+        x[u] = make_uint4(0, 0, 0, 0);
+        if (h0 + u * kRows < heads) x[u] = __ldg(reinterpret_cast<const uint4 *>(src + u * kRows * st[1]));
+    }
     const NewRows rows(a, b);
     const int p = rows.start + i;
-    const bool fits = p < a.pool.capacity();
-    const bool there = p >= rows.first && fits;
-    uint4 x[kHeadsPerLane];
-#pragma unroll
-    for (int u = 0; u < kHeadsPerLane; ++u) {
-        const int h = h0 + u * kRows + sub;
-        x[u] = make_uint4(0, 0, 0, 0);
-        if (!there || h >= heads) continue;
-        const __nv_bfloat16 *src = h < a.Hq ? static_cast<const __nv_bfloat16 *>(a.q) + b * a.sq[0] + h * a.sq[1] + i * a.sq[2]
-                                   : h < a.Hq + Hkv
-                                       ? static_cast<const __nv_bfloat16 *>(a.k) + b * a.sk[0] + (h - a.Hq) * a.sk[1] + i * a.sk[2]
-                                       : static_cast<const __nv_bfloat16 *>(a.v) + b * a.sv[0] + (h - a.Hq - Hkv) * a.sv[1] + i * a.sv[2];
-        x[u] = __ldg(reinterpret_cast<const uint4 *>(src) + cl);
+    const bool there = p >= rows.first && p < a.pool.capacity();
+    int page = 0;
+    if (!is_q && p >= rows.first) {
+        page = there ? a.pool.page_of(b, p) : -1;
+        if (page < 0 && lane == 0) record_failure(a.status, kErrPage, 0);
     }
+    if (!is_q && (!there || page < 0)) return;
     Turn turn;
     turn.on = false, turn.partner = 0;
-    int page = -1;
-    if (there) {
-        turn.load(a, p, cl);
-        if (!FOUR) page = a.pool.page_of(b, p);
+    const bool turns = there && a.rot > 0 && (is_q || is_k);
+    if (turns) turn.load(a, p, cl);
+    uint8_t *to;
+    size_t step;
+    if (is_q) {
+        to = reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(a.q_out) + (((size_t)b * a.Hq + h0) * a.n + i) * D);
+        step = (size_t)kRows * a.n * D * 2;
+    } else {
+        to = (is_k ? a.pool.k : a.pool.v) + a.pool.at(page, h0, p, 2 * D);
+        step = ((size_t)kRows << a.pool.shift) * 2 * D;
     }
-    if (!FOUR && p >= rows.first && page < 0 && lane == 0) record_failure(a.status, kErrPage, 0);
 #pragma unroll
     for (int u = 0; u < kHeadsPerLane; ++u) {
-        const int h = h0 + u * kRows + sub;
-        const uint4 y = turn.apply(a, x[u]);
-        if (h < a.Hq) {
-            reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.q_out) + (((size_t)b * a.Hq + h) * a.n + i) * D)[cl] = y;
-        } else if (!FOUR && h < heads && page >= 0) {
-            const bool key = h < a.Hq + Hkv;
-            uint8_t *to = (key ? a.pool.k : a.pool.v) + a.pool.at(page, h - a.Hq - (key ? 0 : Hkv), p, 2 * D);
-            reinterpret_cast<uint4 *>(to)[cl] = key ? y : x[u];
-        }
+        if (part * kBlock + u * kRows >= heads) break;
+        uint4 y = turns ? turn.apply(a, x[u]) : x[u];
+        if (!there) y = make_uint4(0, 0, 0, 0);
+        if (h0 + u * kRows < heads) reinterpret_cast<uint4 *>(to + u * step)[cl] = y;
     }
 }
 
@@ -190,102 +200,101 @@ __device__ __forceinline__ uint32_t quantise(const uint4 &y, __half *scale) {
     return codes;
 }
 
-// One unit of 16 positions of a head's keys or values, those of them that are new.  A lane holds 8 channels of an even
-// position and of the odd one behind it.
+// 4-bit rows of a head's keys or values: a lane holds 8 channels of an even position and of the odd one behind it, so a warp
+// the 64 / (D / 8) positions of a block of them (never of two units).
 template <int D>
-__device__ void unit_rows(const AppendArgs &a, int task, int units) {
+__device__ __forceinline__ void unit_rows(const AppendArgs &a, int b, int block, int part) {
     using U = Unit4<D>;
-    constexpr int kLanes = D / 8, kPairs = 32 / kLanes;
+    constexpr int kLanes = D / 8, kBlock = 64 / kLanes;
     const int lane = threadIdx.x & 31, cl = lane % kLanes, sub = lane / kLanes;
-    const int Hkv = a.pool.Hkv;
-    const bool key = task % (2 * Hkv) < Hkv;
-    const int h = task % Hkv, bu = task / (2 * Hkv), b = bu / units;
+    const bool key = part < a.pool.Hkv;
+    const int h = key ? part : part - a.pool.Hkv;
     const NewRows rows(a, b);
-    const int p0 = ((rows.first >> 4) + bu % units) * kUnit;
-    if (p0 >= rows.len || p0 + kUnit <= rows.first) return;
+    const int p0 = (rows.first / kBlock + block) * kBlock + 2 * sub;  // this lane's even position
+    if (p0 - 2 * sub >= rows.len || rows.first >= rows.len) return;
+    const long long *st = key ? a.sk : a.sv;
+    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(key ? a.k : a.v) + b * st[0] + h * st[1] + (p0 - rows.start) * st[2] + 8 * cl;
+    uint4 x[2];
+    bool there[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        there[e] = p0 + e >= rows.first && p0 + e < rows.len;
+        x[e] = there[e] ? __ldg(reinterpret_cast<const uint4 *>(src + e * st[2])) : make_uint4(0, 0, 0, 0);
+    }
     const int page = p0 < a.pool.capacity() ? a.pool.page_of(b, p0) : -1;
     if (page < 0) {
         if (lane == 0) record_failure(a.status, kErrPage, 0);
         return;
     }
-    uint8_t *to = (key ? a.pool.k : a.pool.v) + a.pool.at(page, h, p0, 9 * D / 16);
-    const __nv_bfloat16 *src = key ? static_cast<const __nv_bfloat16 *>(a.k) + b * a.sk[0] + h * a.sk[1]
-                                   : static_cast<const __nv_bfloat16 *>(a.v) + b * a.sv[0] + h * a.sv[1];
-    const long long stride = key ? a.sk[2] : a.sv[2];
-    const int g = cl / 4, t = cl % 4;
-#pragma unroll 2
-    for (int pass = 0; pass < 8 / kPairs; ++pass) {
-        const int u = 2 * (pass * kPairs + sub);
-        bool there[2];
-        uint32_t codes[2];
-        __half scale[2];
+    uint32_t codes[2];
+    __half scale[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int p = p0 + u + e;
-            there[e] = p >= rows.first && p < rows.len;
-            uint4 x = make_uint4(0, 0, 0, 0);
+    for (int e = 0; e < 2; ++e) {
+        if (key && a.rot > 0) {
             Turn turn;
             turn.on = false, turn.partner = 0;
-            if (there[e]) {
-                x = __ldg(reinterpret_cast<const uint4 *>(src + (p - rows.start) * stride) + cl);
-                if (key) turn.load(a, p, cl);
-            }
-            if (key) x = turn.apply(a, x);
-            codes[e] = quantise(x, &scale[e]);
+            if (there[e]) turn.load(a, p0 + e, cl);
+            x[e] = turn.apply(a, x[e]);
         }
-        __half *scales = reinterpret_cast<__half *>(to + U::kCodes);
-        if (key) {
+        codes[e] = quantise(x[e], &scale[e]);
+    }
+    const int u = p0 & (kUnit - 1), g = cl / 4, t = cl % 4;
+    uint8_t *to = (key ? a.pool.k : a.pool.v) + a.pool.at(page, h, p0 - u, 9 * D / 16);
+    __half *scales = reinterpret_cast<__half *>(to + U::kCodes);
+    if (key) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (!there[e]) continue;
-                reinterpret_cast<uint32_t *>(to)[U::word(u >> 3, g, 4 * ((u + e) & 7) + t)] = codes[e];
-                if (t == 0) scales[U::k_scale(u + e, g)] = scale[e];
-            }
-        } else {
-            // channels 8 t .. of the group: lanes' fourths 2 t and 2 t + 1
-            uint32_t *w0 = reinterpret_cast<uint32_t *>(to) + U::word(u >> 3, g, 8 * t + (u & 7) / 2);
-            uint32_t *w1 = reinterpret_cast<uint32_t *>(to) + U::word(u >> 3, g, 8 * t + 4 + (u & 7) / 2);
-            if (there[0] && there[1]) {
-                *w0 = __byte_perm(codes[0], codes[1], 0x5410);
-                *w1 = __byte_perm(codes[0], codes[1], 0x7632);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (!there[e]) continue;
-                    reinterpret_cast<uint16_t *>(w0)[e] = (uint16_t)codes[e];
-                    reinterpret_cast<uint16_t *>(w1)[e] = (uint16_t)(codes[e] >> 16);
-                }
-            }
-            if (t == 0)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (there[e]) scales[U::v_scale(u + e, g)] = scale[e];
+        for (int e = 0; e < 2; ++e) {
+            if (!there[e]) continue;
+            reinterpret_cast<uint32_t *>(to)[U::word(u >> 3, g, 4 * ((u + e) & 7) + t)] = codes[e];
+            if (t == 0) scales[U::k_scale(u + e, g)] = scale[e];
         }
+        return;
+    }
+    // channels 8 t .. of the group: lanes' fourths 2 t and 2 t + 1
+    uint32_t *w0 = reinterpret_cast<uint32_t *>(to) + U::word(u >> 3, g, 8 * t + (u & 7) / 2);
+    uint32_t *w1 = reinterpret_cast<uint32_t *>(to) + U::word(u >> 3, g, 8 * t + 4 + (u & 7) / 2);
+    if (there[0] && there[1]) {
+        *w0 = __byte_perm(codes[0], codes[1], 0x5410);
+        *w1 = __byte_perm(codes[0], codes[1], 0x7632);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (!there[e]) continue;
+            reinterpret_cast<uint16_t *>(w0)[e] = (uint16_t)codes[e];
+            reinterpret_cast<uint16_t *>(w1)[e] = (uint16_t)(codes[e] >> 16);
+        }
+    }
+    if (t == 0) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (there[e]) scales[U::v_scale(u + e, g)] = scale[e];
     }
 }
 
+// blockIdx.y: the sequence.  Along x the rows of tokens, then the 4-bit rows, a warp each.
 template <int D, bool FOUR>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a, int row_blocks, int row_tasks, int units, int unit_tasks) {
-    const int warp = threadIdx.x >> 5;
-    if (blockIdx.x < (unsigned)row_blocks) {
-        const int task = blockIdx.x * (kThreads / 32) + warp;
-        if (task < row_tasks) token_rows<D, FOUR>(a, task);
+__global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(AppendArgs a, FastDiv parts, FastDiv unit_parts, int row_tasks, int unit_tasks) {
+    const int task = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), b = blockIdx.y;
+    if (task < row_tasks) {
+        const int i = parts.div(task);
+        token_rows<D, FOUR>(a, b, i, task - i * parts.d);
     } else if constexpr (FOUR) {
-        const int task = (blockIdx.x - row_blocks) * (kThreads / 32) + warp;
-        if (task < unit_tasks) unit_rows<D>(a, task, units);
+        const int unit = task - row_tasks;
+        if (unit >= unit_tasks) return;
+        const int block = unit_parts.div(unit);
+        unit_rows<D>(a, b, block, unit - block * unit_parts.d);
     }
 }
 
 template <int D, bool FOUR>
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
-    constexpr int kBlock = 32 / (D / 8) * kHeadsPerLane, kWarps = kThreads / 32;
-    const int heads = a.Hq + (FOUR ? 0 : 2 * a.pool.Hkv);
-    const int row_tasks = a.B * a.n * ((heads + kBlock - 1) / kBlock);
-    const int units = a.n == 1 ? 1 : (a.n + kUnit - 2) / kUnit + 1;  // n rows meet so many units of 16 at most
-    const int unit_tasks = FOUR ? a.B * units * 2 * a.pool.Hkv : 0;
-    const int row_blocks = (row_tasks + kWarps - 1) / kWarps;
-    paged_append_kernel<D, FOUR><<<row_blocks + (unit_tasks + kWarps - 1) / kWarps, kThreads, 0, s>>>(a, row_blocks, row_tasks, units,
-                                                                                                   unit_tasks);
+    constexpr int kBlock = 32 / (D / 8) * kHeadsPerLane, kWarps = kThreads / 32, kPositions = 64 / (D / 8);
+    const int Hkv = a.pool.Hkv;
+    const int parts = (a.Hq + kBlock - 1) / kBlock + (FOUR ? 0 : 2 * ((Hkv + kBlock - 1) / kBlock));
+    const int blocks = a.n == 1 ? 1 : (a.n + kPositions - 2) / kPositions + 1;  // of positions that n rows meet at most
+    const int row_tasks = a.n * parts, unit_tasks = FOUR ? blocks * 2 * Hkv : 0;
+    const dim3 grid((row_tasks + unit_tasks + kWarps - 1) / kWarps, a.B);
+    paged_append_kernel<D, FOUR><<<grid, kThreads, 0, s>>>(a, FastDiv(std::max(parts, 1)), FastDiv(2 * Hkv), row_tasks, unit_tasks);
     return cudaGetLastError();
 }
 

@@ -965,7 +965,7 @@ struct PagedGrid {
 PagedGrid paged_grid(int B, int Hq, int Hkv, int n_q, int D, int capacity, bool four, int num_sms) {
     PagedGrid g;
     const int R = Hq / Hkv * n_q;
-    g.plan = paged_plan(R, D, four);
+    g.plan = four ? paged_plan4(R, D) : paged_plan(R, D);
     g.row_tiles = (R + g.plan.rows - 1) / g.plan.rows;
     const long long tiles = (capacity + g.plan.tile - 1) / g.plan.tile, lists = (long long)B * Hkv * g.row_tiles;
     g.ctas = (int)std::min<long long>(lists * tiles, (long long)num_sms * g.plan.per_sm);
@@ -1015,14 +1015,19 @@ extern "C" int fa_paged_decode(const void *q, const void *k_pages, const void *v
         a.part_ml = reinterpret_cast<float2 *>(a.part_o + grid.partials() * D);
         a.tails = reinterpret_cast<int2 *>(a.part_ml + grid.partials());
     }
-    CUtensorMap tk{}, tv{};
-    if (!four) {
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (four) {
+        e = launch_paged_decode4(a, grid.ctas, s);
+    } else {
+        CUtensorMap tk, tv;
         const int box = std::min(page, grid.plan.tile);
         if (encode_rows(&tk, k_pages, n_pages * Hkv, page, page, D, box) != FA_OK ||
             encode_rows(&tv, v_pages, n_pages * Hkv, page, page, D, box) != FA_OK)
             return FA_ERR_CUDA;
+        e = launch_paged_decode(a, grid.ctas, tk, tv, s);
     }
-    const cudaError_t e = launch_paged_decode(a, four, grid.ctas, tk, tv, reinterpret_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess && grid.cut) e = launch_paged_join(a, grid.ctas, grid.plan.rows, s);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -103,9 +103,12 @@ struct PagedDecodeArgs {
 struct PagedPlan {
     int tile, rows, per_sm;
 };
-PagedPlan paged_plan(int R, int D, bool four);
-// tk, tv: the pools' tensor maps (bf16 pages: boxes of 64 columns and of the rows of a page, at most a tile's).
-cudaError_t launch_paged_decode(const PagedDecodeArgs &a, bool four, int ctas, const CUtensorMap &tk, const CUtensorMap &tv,
-                                cudaStream_t s);
+PagedPlan paged_plan(int R, int D);   // bf16 pages
+PagedPlan paged_plan4(int R, int D);  // 4-bit pages
+// tk, tv: the pools' tensor maps (boxes of 64 columns and of the rows of a page, at most a tile's).
+cudaError_t launch_paged_decode(const PagedDecodeArgs &a, int ctas, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s);
+cudaError_t launch_paged_decode4(const PagedDecodeArgs &a, int ctas, cudaStream_t s);
+// Behind either, where a list can be cut: rows of a row tile.
+cudaError_t launch_paged_join(const PagedDecodeArgs &a, int ctas, int rows, cudaStream_t s);
 
 }  // namespace fa

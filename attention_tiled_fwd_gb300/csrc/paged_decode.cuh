@@ -1,0 +1,147 @@
+// paged_decode.cuh -- what the decode kernels over bf16 and over 4-bit pages share: the list of tiles, its cut into runs, and
+// the join of the warps' states.
+#pragma once
+#include "paged.cuh"
+#include "sm100_ptx.cuh"
+
+namespace fa {
+
+constexpr int kDecodeWarps = 4;  // warps that compute
+constexpr int kJoinCols = 64;    // channels that they join at a time
+constexpr float kNone = -3e38f;  // the running maximum of a row that has seen nothing
+
+// The 8 x 8 matrix of 16-bit values that the warp holds, a row in four lanes, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// Masks of the pairs of keys that a lane holds of a unit: 2 tq and 2 tq + 1, and 8 further; bit i of `seen`: key i.
+__device__ __forceinline__ void keep_seen(uint32_t (&keep)[2], uint32_t seen, int tq) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const uint32_t two = seen >> (8 * half + 2 * tq);
+        keep[half] = (two & 1u ? 0xffffu : 0u) | (two & 2u ? 0xffff0000u : 0u);
+    }
+}
+
+// The tiles of a sequence: sink tiles from 0 on, then tiles from `first` on.
+struct Tiles {
+    int len, lo, n_sink, first, n;  // lo: the first key in any row's window
+    template <int TILE>
+    static __device__ __forceinline__ Tiles of(const PagedDecodeArgs &a, int b) {
+        Tiles t;
+        const int cap = a.pool.capacity();
+        t.len = a.lens ? max(0, min(cap, __ldg(a.lens + b))) : cap;
+        t.lo = max(0, max(0, t.len - a.n_q) - a.window + 1);
+        const int sinks = (min(a.sinks, t.len) + TILE - 1) / TILE;
+        const bool gap = t.lo / TILE > sinks;
+        t.n_sink = gap ? sinks : 0;
+        t.first = gap ? t.lo / TILE : 0;
+        t.n = max(1, t.n_sink + (t.len + TILE - 1) / TILE - t.first);  // a sequence without keys has a tile that nobody sees
+        return t;
+    }
+    __device__ __forceinline__ int tile(int i) const { return i < n_sink ? i : first + i - n_sink; }
+};
+
+// bit i: some row sees key k0 + i
+__device__ __forceinline__ uint32_t used_keys(const Tiles &t, int k0, int sinks) {
+    return low_bits(t.len - k0) & (~low_bits(t.lo - k0) | low_bits(sinks - k0));
+}
+
+// This CTA's run of the list of tiles.
+struct Run {
+    int b, u, t;      // sequence, key head and row tile, tile
+    long long count;  // tiles
+};
+
+template <int TILE>
+__device__ __forceinline__ long long tiles_of(const PagedDecodeArgs &a, int b0, int b1) {
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) sum += Tiles::of<TILE>(a, b).n;
+    return sum;
+}
+
+// All threads: each adds up the tiles of its share of the sequences, and the one whose share the run begins in finds where.
+template <int TILE, int THREADS>
+__device__ __forceinline__ Run find_run(const PagedDecodeArgs &a, uint8_t *scratch) {
+    long long *totals = reinterpret_cast<long long *>(scratch);
+    int *where = reinterpret_cast<int *>(scratch + 8 * (THREADS / 32));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = (a.B + THREADS - 1) / THREADS, b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
+    const long long mine = tiles_of<TILE>(a, b0, b1);
+    long long before = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, before, d);
+        if (lane >= d) before += x;
+    }
+    if (lane == 31) totals[warp] = before;
+    before -= mine;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += totals[w];
+        total += totals[w];
+    }
+    const long long per_tile = (long long)a.pool.Hkv * a.row_tiles;
+    const long long share = (total * per_tile + gridDim.x - 1) / gridDim.x, begin = share * blockIdx.x;
+    Run r;
+    r.count = min(share, total * per_tile - begin);
+    if (begin >= before * per_tile && begin < (before + mine) * per_tile) {
+        int b = b0;
+        for (;; ++b) {
+            const int n = Tiles::of<TILE>(a, b).n;
+            if (begin < (before + n) * per_tile) {
+                const long long in = begin - before * per_tile;
+                where[0] = b, where[1] = (int)(in / n), where[2] = (int)(in % n);
+                break;
+            }
+            before += n;
+        }
+    }
+    __syncthreads();
+    r.b = r.u = r.t = 0;
+    if (r.count > 0) r.b = where[0], r.u = where[1], r.t = where[2];
+    return r;
+}
+
+// The four warps' states of 8 rows, joined: ml [warp][8 rows] their maxima and sums, buf [warp][64 places][8 rows] 64 channels
+// of their sums, channel 2 i of a pair at place `at(2 i)` and 2 i + 1 `next` places behind it.  Written as O and L of the rows
+// that exist where the CTA holds the whole list (`whole`), else to the partial `slot`.  128 threads.
+template <int D, int NEXT, class At>
+__device__ __forceinline__ void join_warps(const PagedDecodeArgs &a, const float *buf, const float2 *ml, bool whole, size_t slot,
+                                           size_t first_row, int row8, int rows, int col0, At at) {
+#pragma unroll
+    for (int k = 0; k < kJoinCols * 8 / 2 / 128; ++k) {
+        const int r = threadIdx.x & 7, ch = 2 * ((threadIdx.x >> 3) + 16 * k);  // a row, a pair of channels
+        const int place = at(ch);
+        float M = -INFINITY, ls = 0.f;
+        float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kDecodeWarps; ++w) M = fmaxf(M, ml[8 * w + r].x);
+        const float Mb = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int w = 0; w < kDecodeWarps; ++w) {
+            const float fw = ex2_approx(ml[8 * w + r].x - Mb);
+            ls = fmaf(ml[8 * w + r].y, fw, ls);
+            acc.x = fmaf(buf[w * (kJoinCols * 8) + place * 8 + r], fw, acc.x);
+            acc.y = fmaf(buf[w * (kJoinCols * 8) + (place + NEXT) * 8 + r], fw, acc.y);
+        }
+        const int row = row8 + r, col = col0 + ch;
+        if (row >= rows) continue;
+        if (whole) {
+            const float inv = ls > 0.f ? 1.f / ls : ls == 0.f ? 0.f : ls;
+            reinterpret_cast<uint32_t *>(a.o)[((first_row + row) * D + col) / 2] = pack_bf16x2(acc.x * inv, acc.y * inv);
+            if (col == 0) a.lse[first_row + row] = (M + __log2f(ls)) * 0.69314718055994531f;
+        } else {
+            *reinterpret_cast<float2 *>(a.part_o + (slot + row) * D + col) = acc;
+            if (col == 0) a.part_ml[slot + row] = make_float2(M, ls);
+        }
+    }
+}
+
+__device__ __forceinline__ void sync_warps() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+}  // namespace fa

@@ -1,0 +1,557 @@
+// paged_decode4.cu -- attention of a few new rows per sequence against its 4-bit pages (the mathematics, the list of tiles
+// and the join of partials as in paged_decode.cu).
+//
+// What bounds it: HBM, if the codes become operands cheaply enough: at 4.5 bits a value an SM gets 42 values a clock.  So a
+// code pair takes one instruction: its bits 0-3 of a half-word are the fp16 number code 2^-24, bits 4-7 are code 2^-20, so an
+// AND makes an operand register of two of them; the powers go into q and into O's last factor.
+// Keys: sum_c q_c s (code_c - 8) for 32 channels is s (the product with the codes); the -8 sum q go in as one more product of
+// the scales.  q is scaled by a power of two a row so that fp16 holds its bf16 values.  Values: the weights are multiplied with
+// each group's scales (fp16, one rounding of the weight and one of the product: 2^-11 each), and a product with ones adds up
+// what 8 has to be taken of.  Weights carry a power of two, 2^-E, so that their products with the scales stay in fp16's range
+// and above its subnormals: E grows with the scales.
+//
+//   warp 4     producer: tiles of keys and values into a ring, a bulk copy for every page
+//   warps 0-3  kUnits neighbouring units of 16 keys of every tile each
+// (A ring for every warp, filled by itself, leaves room for 16 warps that compute instead of 12, but the copies' integer work
+// comes four times: 64 sequences of 900 to 16384 keys 170 us instead of 147.)
+//
+// Keys that a row does not see may hold anything: their scores are replaced, and their scales cleared before the product.
+#include "fa_internal.h"
+#include "launch.cuh"
+#include "paged_decode.cuh"
+#include <algorithm>
+#include <cuda_fp16.h>
+
+namespace fa {
+namespace {
+
+constexpr int kWarps = kDecodeWarps;
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kTinyScales = -22;  // E while no scale has reached 2^-15: they are taken times 2^15, the weights times 2^7
+
+enum : int { kSiteEmpty = 311, kSiteFull, kSiteDrain };
+
+template <int D, int NT>
+struct Cfg {
+    static constexpr int kUnits = D < 256 ? 2 : 1;                       // of 16 keys, a warp and tile
+    static constexpr int kTile = kWarps * kUnits * kUnit;                // keys
+    static constexpr int kHalf = kTile * 9 * D / 16;                     // bytes of the tile's keys, or of its values
+    static constexpr int kStages = D == 128 ? 3 : 4;
+    static constexpr int kCtas = D == 64 ? (NT == 1 ? 4 : 3) : D == 128 && NT == 1 ? 3 : 2;  // an SM
+    static constexpr int kJoinOff = kStages * 2 * kHalf;
+    static constexpr int kMlOff = kJoinOff + kWarps * kJoinCols * 8 * 4;
+    static constexpr int kBarOff = kMlOff + kWarps * 8 * 8;
+    static constexpr int kScanOff = kBarOff + 2 * kStages * 8;
+    static constexpr int kAlloc = kScanOff + 64;
+    static_assert(kHalf % 16 == 0 && kBarOff % 8 == 0, "bulk copies start on 16 bytes");
+};
+
+__device__ uint4 g_zero_units[Cfg<128, 1>::kHalf / 16];  // what a page that the pool has not reads as
+static_assert(Cfg<256, 1>::kHalf <= Cfg<128, 1>::kHalf && Cfg<64, 1>::kHalf <= Cfg<128, 1>::kHalf, "a box fits");
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same from zero.
+__device__ __forceinline__ void mma_f16_new(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// N words from shared memory.
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], uint32_t at) {
+    if constexpr (N == 1) {
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
+    } else if constexpr (N == 2) {
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                         : "r"(at + 4 * i)
+                         : "memory");
+    }
+}
+// A lane's words of both halves of a unit's codes, group by group.
+template <int D>
+__device__ __forceinline__ void load_codes(uint32_t (&w)[2][D / 32], uint32_t unit, int lane) {
+    using U = Unit4<D>;
+    const uint32_t at = unit + 4 * U::kWide * lane;
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int g = 0; g < U::kGroups; g += U::kWide) {
+            uint32_t v[U::kWide];
+            load_words(v, at + 4 * U::word(half, g, 0));
+#pragma unroll
+            for (int i = 0; i < U::kWide; ++i) w[half][g + i] = v[i];
+        }
+}
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t max_h2(uint32_t a, uint32_t b) {  // of magnitudes; NaN gives way
+    uint32_t d;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ float2 unpack_h2(uint32_t a) { return __half22float2(*reinterpret_cast<const __half2 *>(&a)); }
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_kernel(PagedDecodeArgs a) {
+    using C = Cfg<D, NT>;
+    using U = Unit4<D>;
+    constexpr int kTile = C::kTile, kGroups = D / 32, kRows = 8 * NT, kStages = C::kStages;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOff), *empty = full + kStages;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kWarps);
+        }
+        fence_mbarrier_init();
+    }
+    Run run = find_run<kTile, kThreads>(a, smem + C::kScanOff);  // (its barriers stand behind the set-up too)
+    launch_dependents();
+    const int per_seq = a.pool.Hkv * a.row_tiles;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+
+    if (warp == kWarps) {
+        // a box: the rows of a tile that a page holds; a lane for each of keys and values
+        const int box_rows = min(1 << a.pool.shift, kTile), boxes = kTile / box_rows;
+        const uint32_t box_bytes = box_rows * (9 * D / 16), page_bytes = (9 * D / 16) << a.pool.shift;
+        const uint64_t page_stride = (uint64_t)page_bytes * a.pool.Hkv;
+        const bool value = lane >= boxes;
+        const int row = lane % boxes * box_rows;  // of the tile
+        const uint32_t dst = smem_u32(smem) + (value ? C::kHalf : 0) + row * (9 * D / 16);
+        const uint8_t *pages = value ? a.pool.v : a.pool.k;
+        for (long long left = run.count; left > 0 && ok;) {
+            const Tiles tiles = Tiles::of<kTile>(a, run.b);
+            const int t1 = (int)min((long long)tiles.n, run.t + left);
+            const uint32_t head = run.u / a.row_tiles * page_bytes;
+            // the lane's page of a tile, -1 where the pool has none; -2 where none is needed
+            auto page_at = [&](int t) {
+                const int k0 = tiles.tile(t) * kTile + row;
+                if (lane >= 2 * boxes || k0 >= tiles.len || !(k0 + box_rows > tiles.lo || k0 < a.sinks)) return -2;
+                return a.pool.page_of(run.b, k0);
+            };
+            int next = page_at(run.t);
+            for (int t = run.t; t < t1; ++t) {
+                const int page = next, k0 = tiles.tile(t) * kTile + row;
+                if (t + 1 < t1) next = page_at(t + 1);
+                ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1, a.status, kSiteEmpty));
+                if (!ok) break;
+                const uint32_t need = __ballot_sync(0xffffffffu, page != -2);
+                if (lane == 0) mbar_arrive_expect_tx(&full[stage], __popc(need) * box_bytes);
+                __syncwarp();
+                if (page != -2) {
+                    const uint8_t *from = pages + (uint32_t)page * page_stride + head + (k0 & ((1 << a.pool.shift) - 1)) * (9 * D / 16);
+                    if (page == -1) {
+                        record_failure(a.status, kErrPage, 0);
+                        from = reinterpret_cast<const uint8_t *>(g_zero_units);
+                    }
+                    bulk_load(dst + stage * 2 * C::kHalf, from, box_bytes, &full[stage]);
+                }
+                if (++stage == kStages) stage = 0, phase ^= 1;
+            }
+            left -= t1 - run.t;
+            run.t = 0;
+            if (++run.u == per_seq) run.u = 0, ++run.b;
+        }
+        // the last loads have landed before the CTA leaves
+        const int last = (int)min((long long)kStages, run.count);
+        for (int i = 0; i < last && ok; ++i) {
+            if (--stage < 0) stage = kStages - 1, phase ^= 1;
+            ok = mbar_wait(&full[stage], phase, a.status, kSiteDrain);
+        }
+        return;
+    }
+
+    const int g = lane >> 2, tq = lane & 3;
+    int tail = -1, tail_parts = 0;
+    for (long long left = run.count; left > 0;) {
+        const Tiles tiles = Tiles::of<kTile>(a, run.b);
+        const int t1 = (int)min((long long)tiles.n, run.t + left);
+        const int h = run.u / a.row_tiles, row0 = run.u % a.row_tiles * kRows;
+        const size_t first_row = ((size_t)run.b * a.pool.Hkv + h) * a.R + row0;
+        const int p_first = max(0, tiles.len - a.n_q), p_last = tiles.len - 1;
+
+        // off: the running maximum (log2 units), plus the weights' power of two; kNone while a row has seen nothing
+        float off[NT][2], l[NT][2], f[NT][2], o[NT][D / 16][4];
+        auto position = [&](int r) { return tiles.len - a.n_q + (row0 + r) % a.n_q; };  // rows past R: any; they are not stored
+        uint32_t qf[NT][D / 16][2];
+        uint32_t less[NT][2];  // -8 sum q of each group as an operand against the keys' scales, in two parts
+        float ones[NT][4];     // sum P s of group g in row g
+        int E = kTinyScales, Ep = -7;  // powers of two of the weights times scales, and of the weights
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) off[n][e] = kNone, l[n][e] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+            const bool there = row0 + 8 * n + g < a.R;
+            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + (first_row + 8 * n + g) * D;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ones[n][e] = 0.f;
+            uint4 x[kGroups];
+            uint32_t most = 0;
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) {
+                x[j] = there ? __ldg(reinterpret_cast<const uint4 *>(q) + 4 * j + tq) : make_uint4(0, 0, 0, 0);
+                const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) most = max(most, max(w[i] << 16 & 0x7fff0000u, w[i] & 0x7fff0000u));
+            }
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            // the row's largest magnitude becomes 2^14 .. 2^15 (a row of zeros or of the smallest numbers: less)
+            const int up = min(114, 14 - max(-100, (int)(most >> 23) - 127));
+            const float by = __int_as_float((127 + up) << 23);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int shift = 24 - __shfl_sync(0xffffffffu, up, 4 * (2 * tq + e));  // the codes' 2^-24 too
+                f[n][e] = fmaxf(a.scale_log2 * __int_as_float((127 + shift / 2) << 23) * __int_as_float((127 + shift - shift / 2) << 23),
+                                1.2e-38f);  // (above 0: -inf times it stays -inf)
+            }
+            uint32_t part[2][kGroups];  // fp16 of -8 2^-24 sum q, and of what that leaves
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) {
+                const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                float c[8], sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    c[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) * by;
+                    if (i & 1) c[i] *= 0.0625f;
+                }
+                qf[n][2 * j][0] = pack_h2(c[0], c[4]), qf[n][2 * j][1] = pack_h2(c[1], c[5]);
+                qf[n][2 * j + 1][0] = pack_h2(c[2], c[6]), qf[n][2 * j + 1][1] = pack_h2(c[3], c[7]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 even = unpack_h2(qf[n][2 * j + i][0]), odd = unpack_h2(qf[n][2 * j + i][1]);
+                    sum += (even.x + even.y) + 16.f * (odd.x + odd.y);
+                }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                sum *= -0x1p-21f;
+                const __half high = __float2half_rn(sum);
+                part[0][j] = __half_as_ushort(high);
+                part[1][j] = __half_as_ushort(__float2half_rn(sum - __half2float(high)));
+            }
+            // the operand's columns: the groups' first parts, then their second ones (lane tq: two columns of each eight)
+            less[n][0] = less[n][1] = 0u;
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                const int at = i % (kGroups / 2), second = i / (kGroups / 2);
+                const uint32_t two = part[second][2 * at] | part[second][2 * at + 1] << 16;
+                if (tq == i % 4) less[n][i / 4] = two;
+            }
+        }
+
+        for (int t = run.t; t < t1; ++t) {
+            const int key_warp = tiles.tile(t) * kTile + warp * (C::kUnits * kUnit), key_end = key_warp + C::kUnits * kUnit;
+            // every key of the warp's exists, and every row sees it
+            const bool plain = key_end <= tiles.len && all_seen(p_first, p_last, key_warp, key_end - 1, a.window, a.sinks);
+            const uint32_t ks = smem_u32(smem) + stage * 2 * C::kHalf + warp * (C::kUnits * U::kBytes), vs = ks + C::kHalf;
+            float sc[C::kUnits][NT][4];  // S^T of the warp's units: keys g and g + 8, rows 2 tq and 2 tq + 1
+            if (ok) ok = warp_wait(&full[stage], phase, a.status, kSiteFull);  // (after a time-out: on whatever is there)
+            {
+#pragma unroll
+                for (int w = 0; w < C::kUnits; ++w) {
+                    const int key0 = key_warp + w * kUnit;
+                    const uint32_t at = ks + w * U::kBytes, scales = at + U::kCodes;
+                    uint32_t code[2][kGroups], s2[2][kGroups / 2], by[4];
+                    load_codes<D>(code, at, lane);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        load_words(s2[half], scales + 2 * U::k_scale(g + 8 * half, 0));
+                        uint32_t two[1];
+                        load_words(two, scales + 2 * U::k_scale(g + 8 * half, 2 * (tq % (kGroups / 2))));
+                        by[half] = by[2 + half] = two[0];
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_f16_new(sc[w][n], by, less[n][0], less[n][1]);
+#pragma unroll
+                    for (int j = 0; j < kGroups; ++j) {
+                        uint32_t x[4], y[4];
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint32_t c = code[half][j], d = c >> 8;
+                            x[half] = c & 0x000f000fu, x[2 + half] = c & 0x00f000f0u;
+                            y[half] = d & 0x000f000fu, y[2 + half] = d & 0x00f000f0u;
+                        }
+                        const float2 sa = unpack_h2(s2[0][j / 2]), sb = unpack_h2(s2[1][j / 2]);
+                        const float s_lo = j & 1 ? sa.y : sa.x, s_hi = j & 1 ? sb.y : sb.x;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            float part[4];
+                            mma_f16_new(part, x, qf[n][2 * j][0], qf[n][2 * j][1]);
+                            mma_f16(part, y, qf[n][2 * j + 1][0], qf[n][2 * j + 1][1]);
+                            sc[w][n][0] = fmaf(s_lo, part[0], sc[w][n][0]), sc[w][n][1] = fmaf(s_lo, part[1], sc[w][n][1]);
+                            sc[w][n][2] = fmaf(s_hi, part[2], sc[w][n][2]), sc[w][n][3] = fmaf(s_hi, part[3], sc[w][n][3]);
+                        }
+                    }
+                    if (!plain) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const uint32_t seen = seen_keys(position(8 * n + 2 * tq + e), key0, a.window, a.sinks);
+                                if (!(seen >> g & 1u)) sc[w][n][e] = -INFINITY;
+                                if (!(seen >> (g + 8) & 1u)) sc[w][n][2 + e] = -INFINITY;
+                            }
+                    }
+                }
+                // scales of the values of keys 2 tq and 2 tq + 1 (+ 8)
+                uint32_t s2[C::kUnits][2][kGroups];
+                uint32_t bits = 0;
+#pragma unroll
+                for (int w = 0; w < C::kUnits; ++w) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) load_words(s2[w][half], vs + w * U::kBytes + U::kCodes + 2 * U::v_scale(2 * tq + 8 * half, 0));
+                    if (!plain) {
+                        // keys that no row sees: 0 times whatever their scales are must not reach O.  (A row's own keys alone
+                        // where a lane holds one row: what other rows see may be no number either.)
+                        const int key0 = key_warp + w * kUnit;
+                        uint32_t keep[2];
+                        keep_seen(keep, NT == 1 ? seen_keys(position(g), key0, a.window, a.sinks) : used_keys(tiles, key0, a.sinks), tq);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+#pragma unroll
+                            for (int j = 0; j < kGroups; ++j) s2[w][half][j] &= keep[half];
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int j = 0; j < kGroups; ++j) bits |= s2[w][half][j];
+                }
+                // A weight is 2^8 at most, so its products with scales below 2^(E + 7) fit in fp16.  The scales' bits
+                // together are no less than the largest (and less than twice it, or all of 2^(1 + k) - 1 exponents).
+                const uint32_t limit = max((uint32_t)(E + 7 + 15) << 10, 0x200u);  // 2^(E + 7)
+                if (__any_sync(0xffffffffu, E < 9 && (bits + (0x8000u - limit) * 0x10001u) & 0x80008000u)) {
+                    uint32_t most = 0;
+#pragma unroll
+                    for (int w = 0; w < C::kUnits; ++w)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+#pragma unroll
+                            for (int j = 0; j < kGroups; ++j) most = max_h2(most, s2[w][half][j]);
+                    const float2 mh = unpack_h2(most);
+                    const uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(mh.x, mh.y)));
+                    const int need = (int)(all >> 23) - 127 - 6;
+                    if (need > E) {
+                        const int to = max(-6, min(9, need));
+                        const float by = __int_as_float((127 + E - to) << 23), by_l = __int_as_float((127 + Ep - to) << 23);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) l[n][e] *= by_l, off[n][e] += (float)(to - Ep);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                ones[n][e] *= by;
+#pragma unroll
+                                for (int i = 0; i < D / 16; ++i) o[n][i][e] *= by;
+                            }
+                        }
+                        E = Ep = to;
+                    }
+                }
+                if (E == kTinyScales) {
+#pragma unroll
+                    for (int w = 0; w < C::kUnits; ++w)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+#pragma unroll
+                            for (int j = 0; j < kGroups; ++j) s2[w][half][j] = mul_h2(s2[w][half][j], 0x78007800u);
+                }
+
+                // the weights' logarithms; the maxima are taken again only when a weight would grow past 2^8
+                bool grow = false;
+                auto logs = [&](int w, int n, int e) { return fmaf(sc[w][n][e], f[n][e & 1], -off[n][e & 1]); };
+                const float most = 8.f - (float)Ep;
+#pragma unroll
+                for (int w = 0; w < C::kUnits; ++w)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        grow |= fmaxf(fmax3(logs(w, n, 0), logs(w, n, 1), logs(w, n, 2)), logs(w, n, 3)) > most;
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float mt = -INFINITY;
+#pragma unroll
+                            for (int w = 0; w < C::kUnits; ++w) mt = fmax3(mt, sc[w][n][e], sc[w][n][2 + e]);
+                            mt *= f[n][e];
+                            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
+                            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
+                            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+                            mt += (float)Ep;
+                            if (mt > off[n][e] + 8.f) {
+                                const float alpha = ex2_approx(off[n][e] - mt);
+                                l[n][e] *= alpha;
+                                ones[n][e] *= alpha, ones[n][2 + e] *= alpha;
+#pragma unroll
+                                for (int i = 0; i < D / 16; ++i) o[n][i][e] *= alpha, o[n][i][2 + e] *= alpha;
+                                off[n][e] = mt;
+                            }
+                        }
+                }
+
+#pragma unroll
+                for (int w = 0; w < C::kUnits; ++w) {
+                    const int key0 = key_warp + w * kUnit;
+                    uint32_t pb[NT][2];  // P^T as the second product's operand: row g, keys 2 tq and 2 tq + 1 (+ 8)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float p[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) p[e] = ex2_approx(logs(w, n, e));
+                        // this lane's keys, not rounded; the others' are added at the end
+                        l[n][0] += p[0] + p[2], l[n][1] += p[1] + p[3];
+                        pb[n][0] = transpose8(pack_h2(p[0], p[1]));  // the weights as operands: fp16, off by 2^-11
+                        pb[n][1] = transpose8(pack_h2(p[2], p[3]));
+                    }
+                    uint32_t code[2][kGroups];
+                    load_codes<D>(code, vs + w * U::kBytes, lane);
+                    uint32_t sees[NT][2];  // row g's own keys, where a lane holds two rows
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        sees[n][0] = sees[n][1] = ~0u;
+                        if (NT > 1 && !plain) keep_seen(sees[n], seen_keys(position(8 * n + g), key0, a.window, a.sinks), tq);
+                    }
+#pragma unroll
+                    for (int j = 0; j < kGroups; ++j) {
+                        uint32_t x[4], y[4];
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint32_t c = code[half][j], d = c >> 8;
+                            x[2 * half] = c & 0x000f000fu, x[2 * half + 1] = c & 0x00f000f0u;
+                            y[2 * half] = d & 0x000f000fu, y[2 * half + 1] = d & 0x00f000f0u;
+                        }
+                        const uint32_t one = g == j ? 0x3c003c00u : 0u, row_j[4] = {one, 0u, one, 0u};
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            uint32_t b0 = mul_h2(pb[n][0], s2[w][0][j]), b1 = mul_h2(pb[n][1], s2[w][1][j]);
+                            if (NT > 1) b0 &= sees[n][0], b1 &= sees[n][1];
+                            mma_f16(o[n][2 * j], x, b0, b1);
+                            mma_f16(o[n][2 * j + 1], y, b0, b1);
+                            mma_f16(ones[n], row_j, b0, b1);
+                        }
+                    }
+                }
+                warp_arrive(&empty[stage]);
+            }
+            if (++stage == kStages) stage = 0, phase ^= 1;
+        }
+
+        // O and L of a list that this CTA holds whole, else a partial: in its first slot what began in a CTA before this one, in
+        // its second what goes on behind it
+        const bool whole = run.t == 0 && t1 == tiles.n;
+        const size_t slot = ((size_t)blockIdx.x * 2 + (run.t == 0)) * kRows;
+        if (run.t == 0 && !whole) {
+            tail = run.b * per_seq + run.u;
+            tail_parts = 1 + (int)((tiles.n - t1 + run.count - 1) / run.count);
+        }
+        const float by = E == kTinyScales ? 0x1p-15f : 1.f;  // the scales' own power of two
+        float *buf = reinterpret_cast<float *>(smem + C::kJoinOff);
+        float2 *ml = reinterpret_cast<float2 *>(smem + C::kMlOff);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
+                l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
+                l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
+            }
+#pragma unroll
+            for (int c = 0; c < D / kJoinCols; ++c) {
+                sync_warps();  // the buffer is free
+                if (c == 0 && g < 2) ml[8 * warp + 2 * tq + g] = make_float2(l[n][g & 1] == 0.f ? -INFINITY : off[n][g & 1], l[n][g & 1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // channel 32 j + 4 g + (0, 1 | 2, 3) at place 8 (channel % 4) + g of its group
+                    const int j = 2 * c + i / 2;
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float sum = 8.f * __shfl_sync(0xffffffffu, ones[n][e], 4 * j + tq);
+                        v[e] = fmaf(o[n][4 * c + i][e], 0x1p24f, -sum) * by;
+                        v[2 + e] = fmaf(o[n][4 * c + i][2 + e], 0x1p20f, -sum) * by;
+                    }
+                    float *to = buf + warp * (kJoinCols * 8) + (32 * (i / 2) + 16 * (i % 2) + g) * 8 + 2 * tq;
+                    *reinterpret_cast<float2 *>(to) = make_float2(v[0], v[1]);
+                    *reinterpret_cast<float2 *>(to + 64) = make_float2(v[2], v[3]);
+                }
+                sync_warps();
+                join_warps<D, 8>(a, buf, ml, whole, slot, first_row, 8 * n, a.R - row0, kJoinCols * c,
+                                 [](int ch) { return 32 * (ch / 32) + 8 * (ch % 4) + ch % 32 / 4; });
+            }
+        }
+        left -= t1 - run.t;
+        run.t = 0;
+        if (++run.u == per_seq) run.u = 0, ++run.b;
+    }
+    if (a.tails && threadIdx.x == 0) a.tails[blockIdx.x] = make_int2(tail, tail_parts);
+}
+
+template <int D, int NT>
+cudaError_t launch_d(const PagedDecodeArgs &a, int ctas, cudaStream_t s) {
+    auto kern = paged_decode4_kernel<D, NT>;
+    static std::atomic<unsigned long long> allowed{0};
+    const cudaError_t e = allow_smem((const void *)kern, Cfg<D, NT>::kAlloc, allowed);
+    if (e != cudaSuccess) return e;
+    return launch_behind(kern, dim3(ctas), kThreads, Cfg<D, NT>::kAlloc, false, 1, s, a);
+}
+
+template <int D, int NT>
+PagedPlan plan_d() {
+    return PagedPlan{Cfg<D, NT>::kTile, 8 * NT, Cfg<D, NT>::kCtas};
+}
+
+// 8 rows a CTA, or 16 where there are more: twice the products for half the reads.  (Heads of 256: 8; with 16 the
+// accumulators alone would take a thread's registers.)
+bool sixteen(int R, int D) { return R > 8 && D < 256; }
+
+}  // namespace
+
+PagedPlan paged_plan4(int R, int D) {
+    const bool two = sixteen(R, D);
+    switch (D) {
+        case 64: return two ? plan_d<64, 2>() : plan_d<64, 1>();
+        case 128: return two ? plan_d<128, 2>() : plan_d<128, 1>();
+        default: return plan_d<256, 1>();
+    }
+}
+
+cudaError_t launch_paged_decode4(const PagedDecodeArgs &a, int ctas, cudaStream_t s) {
+    const bool two = sixteen(a.R, a.D);
+    switch (a.D) {
+        case 64: return two ? launch_d<64, 2>(a, ctas, s) : launch_d<64, 1>(a, ctas, s);
+        case 128: return two ? launch_d<128, 2>(a, ctas, s) : launch_d<128, 1>(a, ctas, s);
+        case 256: return launch_d<256, 1>(a, ctas, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace fa

@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
         auto position = [&](int r) { return tiles.len - a.n_q + (row0 + r) % a.n_q; };  // rows past R: any; they are not stored
         uint32_t qf[NT][D / 16][2];
         uint32_t less[NT][2];  // -8 sum q of each group as an operand against the keys' scales, in two parts
-        float ones[NT][4];     // sum P s of group g in row g
+        float ones[NT][kGroups][4];  // sum P s of a group (the same in the second two)
         int E = kTinyScales, Ep = -7;  // powers of two of the weights times scales, and of the weights
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
             const bool there = row0 + 8 * n + g < a.R;
             const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + (first_row + 8 * n + g) * D;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) ones[n][e] = 0.f;
+            for (int j = 0; j < kGroups; ++j) ones[n][j][0] = ones[n][j][1] = ones[n][j][2] = ones[n][j][3] = 0.f;
             uint4 x[kGroups];
             uint32_t most = 0;
 #pragma unroll
@@ -368,7 +368,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
                             for (int e = 0; e < 2; ++e) l[n][e] *= by_l, off[n][e] += (float)(to - Ep);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                ones[n][e] *= by;
+#pragma unroll
+                                for (int j = 0; j < kGroups; ++j) ones[n][j][e] *= by;
 #pragma unroll
                                 for (int i = 0; i < D / 16; ++i) o[n][i][e] *= by;
                             }
@@ -387,13 +388,22 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
 
                 // the weights' logarithms; the maxima are taken again only when a weight would grow past 2^8
                 bool grow = false;
-                auto logs = [&](int w, int n, int e) { return fmaf(sc[w][n][e], f[n][e & 1], -off[n][e & 1]); };
+                float lg[C::kUnits][NT][4];
+                auto logs = [&] {
+#pragma unroll
+                    for (int w = 0; w < C::kUnits; ++w)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) lg[w][n][e] = fmaf(sc[w][n][e], f[n][e & 1], -off[n][e & 1]);
+                };
+                logs();
                 const float most = 8.f - (float)Ep;
 #pragma unroll
                 for (int w = 0; w < C::kUnits; ++w)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        grow |= fmaxf(fmax3(logs(w, n, 0), logs(w, n, 1), logs(w, n, 2)), logs(w, n, 3)) > most;
+                        grow |= fmaxf(fmax3(lg[w][n][0], lg[w][n][1], lg[w][n][2]), lg[w][n][3]) > most;
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
@@ -410,12 +420,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
                             if (mt > off[n][e] + 8.f) {
                                 const float alpha = ex2_approx(off[n][e] - mt);
                                 l[n][e] *= alpha;
-                                ones[n][e] *= alpha, ones[n][2 + e] *= alpha;
+#pragma unroll
+                                for (int j = 0; j < kGroups; ++j) ones[n][j][e] *= alpha;
 #pragma unroll
                                 for (int i = 0; i < D / 16; ++i) o[n][i][e] *= alpha, o[n][i][2 + e] *= alpha;
                                 off[n][e] = mt;
                             }
                         }
+                    logs();
                 }
 
 #pragma unroll
@@ -426,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
                     for (int n = 0; n < NT; ++n) {
                         float p[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) p[e] = ex2_approx(logs(w, n, e));
+                        for (int e = 0; e < 4; ++e) p[e] = ex2_approx(lg[w][n][e]);
                         // this lane's keys, not rounded; the others' are added at the end
                         l[n][0] += p[0] + p[2], l[n][1] += p[1] + p[3];
                         pb[n][0] = transpose8(pack_h2(p[0], p[1]));  // the weights as operands: fp16, off by 2^-11
@@ -449,14 +461,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
                             x[2 * half] = c & 0x000f000fu, x[2 * half + 1] = c & 0x00f000f0u;
                             y[2 * half] = d & 0x000f000fu, y[2 * half + 1] = d & 0x00f000f0u;
                         }
-                        const uint32_t one = g == j ? 0x3c003c00u : 0u, row_j[4] = {one, 0u, one, 0u};
+                        const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             uint32_t b0 = mul_h2(pb[n][0], s2[w][0][j]), b1 = mul_h2(pb[n][1], s2[w][1][j]);
                             if (NT > 1) b0 &= sees[n][0], b1 &= sees[n][1];
                             mma_f16(o[n][2 * j], x, b0, b1);
                             mma_f16(o[n][2 * j + 1], y, b0, b1);
-                            mma_f16(ones[n], row_j, b0, b1);
+                            mma_f16(ones[n][j], one, b0, b1);
                         }
                     }
                 }
@@ -495,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
                     float v[4];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float sum = 8.f * __shfl_sync(0xffffffffu, ones[n][e], 4 * j + tq);
+                        const float sum = 8.f * ones[n][j][e];
                         v[e] = fmaf(o[n][4 * c + i][e], 0x1p24f, -sum) * by;
                         v[2 + e] = fmaf(o[n][4 * c + i][2 + e], 0x1p20f, -sum) * by;
                     }

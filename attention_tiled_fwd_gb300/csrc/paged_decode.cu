@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
             for (int t = run.t; t < t1; ++t) {
                 const int page = next;
                 if (t + 1 < t1) next = page_at(t + 1);
-                ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1, a.status, kSiteEmpty));
+                ok = sleepy_wait(&empty[stage], phase ^ 1, a.status, kSiteEmpty);
                 if (!ok) break;
                 const uint32_t need = __ballot_sync(0xffffffffu, page != -2);
                 if (lane == 0) mbar_arrive_expect_tx(&full[stage], __popc(need) * box_bytes);
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
         const int last = (int)min((long long)C::kStages, run.count);
         for (int i = 0; i < last && ok; ++i) {
             if (--stage < 0) stage = C::kStages - 1, phase ^= 1;
-            ok = mbar_wait(&full[stage], phase, a.status, kSiteDrain);
+            ok = sleepy_wait(&full[stage], phase, a.status, kSiteDrain);
         }
         return;
     }
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
         }
 
         for (int t = run.t; t < t1; ++t) {
-            if (ok) ok = warp_wait(&full[stage], phase, a.status, kSiteFull);
+            if (ok) ok = sleepy_wait(&full[stage], phase, a.status, kSiteFull);
             if (ok) {
                 const uint32_t ks = smem_u32(smem) + stage * 2 * C::kHalf, vs = ks + C::kHalf;
                 const int key0 = tiles.tile(t) * kTile + kUnit * warp;

@@ -10,6 +10,31 @@ constexpr int kDecodeWarps = 4;  // warps that compute
 constexpr int kJoinCols = 64;    // channels that they join at a time
 constexpr float kNone = -3e38f;  // the running maximum of a row that has seen nothing
 
+// Waits as in sm100_ptx.cuh, by a whole warp, in steps of up to 1 ms that the hardware sleeps through: the polls of warps that
+// wait would take issue slots from those that compute.
+__device__ __forceinline__ bool sleepy_try(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(1000000u)
+        : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ bool sleepy_wait(uint64_t *bar, uint32_t parity, int *status, int site) {
+    const uint32_t b = smem_u32(bar);
+    if (__all_sync(0xffffffffu, sleepy_try(b, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (__all_sync(0xffffffffu, sleepy_try(b, parity))) return true;
+        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs)) break;
+    }
+    if ((threadIdx.x & 31) == 0) record_failure(status, 8 /* FA_ERR_TIMEOUT */, site);
+    return false;
+}
+
 // The 8 x 8 matrix of 16-bit values that the warp holds, a row in four lanes, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
             for (int t = run.t; t < t1; ++t) {
                 const int page = next, k0 = tiles.tile(t) * kTile + row;
                 if (t + 1 < t1) next = page_at(t + 1);
-                ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1, a.status, kSiteEmpty));
+                ok = sleepy_wait(&empty[stage], phase ^ 1, a.status, kSiteEmpty);
                 if (!ok) break;
                 const uint32_t need = __ballot_sync(0xffffffffu, page != -2);
                 if (lane == 0) mbar_arrive_expect_tx(&full[stage], __popc(need) * box_bytes);
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
         const int last = (int)min((long long)kStages, run.count);
         for (int i = 0; i < last && ok; ++i) {
             if (--stage < 0) stage = kStages - 1, phase ^= 1;
-            ok = mbar_wait(&full[stage], phase, a.status, kSiteDrain);
+            ok = sleepy_wait(&full[stage], phase, a.status, kSiteDrain);
         }
         return;
     }
@@ -193,7 +193,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
         const int t1 = (int)min((long long)tiles.n, run.t + left);
         const int h = run.u / a.row_tiles, row0 = run.u % a.row_tiles * kRows;
         const size_t first_row = ((size_t)run.b * a.pool.Hkv + h) * a.R + row0;
-        const int p_first = max(0, tiles.len - a.n_q), p_last = tiles.len - 1;
+        // tiles whose every key exists and is in every row's window
+        const int p_first = max(0, tiles.len - a.n_q), past = tiles.len - 1 - a.window;
+        const int plain0 = past < 0 ? 0 : past / kTile + 1, plain1 = (p_first + 1) / kTile;
 
         // off: the running maximum (log2 units), plus the weights' power of two; kNone while a row has seen nothing
         float off[NT][2], l[NT][2], f[NT][2], o[NT][D / 16][4];
@@ -269,12 +271,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
         }
 
         for (int t = run.t; t < t1; ++t) {
-            const int key_warp = tiles.tile(t) * kTile + warp * (C::kUnits * kUnit), key_end = key_warp + C::kUnits * kUnit;
-            // every key of the warp's exists, and every row sees it
-            const bool plain = key_end <= tiles.len && all_seen(p_first, p_last, key_warp, key_end - 1, a.window, a.sinks);
+            const int tile = tiles.tile(t), key_warp = tile * kTile + warp * (C::kUnits * kUnit);
+            const bool plain = tile >= plain0 && tile < plain1;
             const uint32_t ks = smem_u32(smem) + stage * 2 * C::kHalf + warp * (C::kUnits * U::kBytes), vs = ks + C::kHalf;
             float sc[C::kUnits][NT][4];  // S^T of the warp's units: keys g and g + 8, rows 2 tq and 2 tq + 1
-            if (ok) ok = warp_wait(&full[stage], phase, a.status, kSiteFull);  // (after a time-out: on whatever is there)
+            if (ok) ok = sleepy_wait(&full[stage], phase, a.status, kSiteFull);  // (after a time-out: on whatever is there)
             {
 #pragma unroll
                 for (int w = 0; w < C::kUnits; ++w) {

@@ -41,6 +41,9 @@ struct Cfg {
     static constexpr int kAlloc = kScanOff + 64 + 1024;
 };
 
+template <int D>
+constexpr int kListCost = D == 64 ? 2 : 1;  // in tiles
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -60,7 +63,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
         }
         fence_mbarrier_init();
     }
-    Run run = find_run<kTile, kThreads>(a, smem + C::kScanOff);  // (its barriers stand behind the set-up too)
+    Run<kListCost<D>> run = find_run<kTile, kThreads, kListCost<D>>(a, smem + C::kScanOff);  // (its barriers stand behind the set-up too)
     launch_dependents();
     const int per_seq = a.pool.Hkv * a.row_tiles;
     int stage = 0;
@@ -78,17 +81,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
             tma_prefetch_desc(&tmap_k);
             tma_prefetch_desc(&tmap_v);
         }
+        long long loaded = 0;
         for (long long left = run.count; left > 0 && ok;) {
             const Tiles tiles = Tiles::of<kTile>(a, run.b);
-            const int t1 = (int)min((long long)tiles.n, run.t + left), h = run.u / a.row_tiles;
+            int t0, t1;
+            run.part(tiles.n, left, &t0, &t1);
+            const int h = run.u / a.row_tiles;
             // the lane's page of a tile, -1 where the pool has none; -2 where none is needed
             auto page_at = [&](int t) {
                 const int k0 = tiles.tile(t) * kTile + box * box_rows;
                 if (lane >= copies || k0 >= tiles.len || !(k0 + box_rows > tiles.lo || k0 < a.sinks)) return -2;
                 return a.pool.page_of(run.b, k0);
             };
-            int next = page_at(run.t);
-            for (int t = run.t; t < t1; ++t) {
+            int next = t0 < t1 ? page_at(t0) : -2;
+            for (int t = t0; t < t1; ++t, ++loaded) {
                 const int page = next;
                 if (t + 1 < t1) next = page_at(t + 1);
                 ok = sleepy_wait(&empty[stage], phase ^ 1, a.status, kSiteEmpty);
@@ -105,12 +111,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
                 }
                 if (++stage == C::kStages) stage = 0, phase ^= 1;
             }
-            left -= t1 - run.t;
-            run.t = 0;
-            if (++run.u == per_seq) run.u = 0, ++run.b;
+            left = run.next(tiles.n, left, per_seq);
         }
         // the last loads have landed before the CTA leaves
-        const int last = (int)min((long long)C::kStages, run.count);
+        const int last = (int)min((long long)C::kStages, loaded);
         for (int i = 0; i < last && ok; ++i) {
             if (--stage < 0) stage = C::kStages - 1, phase ^= 1;
             ok = sleepy_wait(&full[stage], phase, a.status, kSiteDrain);
@@ -126,7 +130,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
     int tail = -1, tail_parts = 0;
     for (long long left = run.count; left > 0;) {
         const Tiles tiles = Tiles::of<kTile>(a, run.b);
-        const int t1 = (int)min((long long)tiles.n, run.t + left);
+        int t0, t1;
+        run.part(tiles.n, left, &t0, &t1);
+        if (t0 == t1) {  // the run begins or ends in front of the list's first tile
+            left = run.next(tiles.n, left, per_seq);
+            continue;
+        }
         const int h = run.u / a.row_tiles, row0 = run.u % a.row_tiles * kRows;
         const size_t first_row = ((size_t)run.b * a.pool.Hkv + h) * a.R + row0;
         const int p_first = max(0, tiles.len - a.n_q), p_last = tiles.len - 1;
@@ -150,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
                 for (int e = 0; e < 2; ++e) qf[n][i][e] = there ? __ldg(q + 8 * i + 4 * e + tq) : 0u;
         }
 
-        for (int t = run.t; t < t1; ++t) {
+        for (int t = t0; t < t1; ++t) {
             if (ok) ok = sleepy_wait(&full[stage], phase, a.status, kSiteFull);
             if (ok) {
                 const uint32_t ks = smem_u32(smem) + stage * 2 * C::kHalf, vs = ks + C::kHalf;
@@ -268,9 +277,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
 
         // O and L of a list that this CTA holds whole, else a partial: in its first slot what began in a CTA before this one, in
         // its second what goes on behind it
-        const bool whole = run.t == 0 && t1 == tiles.n;
-        const size_t slot = ((size_t)blockIdx.x * 2 + (run.t == 0)) * kRows;
-        if (run.t == 0 && !whole) {
+        const bool whole = t0 == 0 && t1 == tiles.n;
+        const size_t slot = ((size_t)blockIdx.x * 2 + (t0 == 0)) * kRows;
+        if (t0 == 0 && !whole) {
             tail = run.b * per_seq + run.u;
             tail_parts = 1 + (int)((tiles.n - t1 + run.count - 1) / run.count);
         }
@@ -299,9 +308,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
                 join_warps<D, 1>(a, buf, ml, whole, slot, first_row, 8 * n, a.R - row0, kJoinCols * c, [](int ch) { return ch; });
             }
         }
-        left -= t1 - run.t;
-        run.t = 0;
-        if (++run.u == per_seq) run.u = 0, ++run.b;
+        left = run.next(tiles.n, left, per_seq);
     }
     if (a.tails && threadIdx.x == 0) a.tails[blockIdx.x] = make_int2(tail, tail_parts);
 }

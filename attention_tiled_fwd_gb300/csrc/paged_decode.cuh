@@ -74,27 +74,35 @@ __device__ __forceinline__ uint32_t used_keys(const Tiles &t, int k0, int sinks)
     return low_bits(t.len - k0) & (~low_bits(t.lo - k0) | low_bits(sinks - k0));
 }
 
-// This CTA's run of the list of tiles.
+// This CTA's run: `count` steps from step v of list u of sequence b on.  A list of n tiles has COST steps for what it costs
+// besides (q, the join, the stores: about that many tiles' time), and then a step for each tile.
+template <int COST>
 struct Run {
-    int b, u, t;      // sequence, key head and row tile, tile
-    long long count;  // tiles
+    int b, u, v;
+    long long count;
+    // Tiles [t0, t1) of the present list of n, of `left` steps.
+    __device__ __forceinline__ void part(int n, long long left, int *t0, int *t1) const {
+        *t0 = max(0, v - COST);
+        *t1 = max(0, (int)min((long long)(n + COST), v + left) - COST);
+    }
+    // On to the next list; the steps that are left then.
+    __device__ __forceinline__ long long next(int n, long long left, int lists) {
+        left -= n + COST - v;
+        v = 0;
+        if (++u == lists) u = 0, ++b;
+        return left;
+    }
 };
 
-template <int TILE>
-__device__ __forceinline__ long long tiles_of(const PagedDecodeArgs &a, int b0, int b1) {
-    long long sum = 0;
-    for (int b = b0; b < b1; ++b) sum += Tiles::of<TILE>(a, b).n;
-    return sum;
-}
-
-// All threads: each adds up the tiles of its share of the sequences, and the one whose share the run begins in finds where.
-template <int TILE, int THREADS>
-__device__ __forceinline__ Run find_run(const PagedDecodeArgs &a, uint8_t *scratch) {
+// All threads: each adds up the steps of its share of the sequences, and the one whose share the run begins in finds where.
+template <int TILE, int THREADS, int COST>
+__device__ __forceinline__ Run<COST> find_run(const PagedDecodeArgs &a, uint8_t *scratch) {
     long long *totals = reinterpret_cast<long long *>(scratch);
     int *where = reinterpret_cast<int *>(scratch + 8 * (THREADS / 32));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int per = (a.B + THREADS - 1) / THREADS, b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
-    const long long mine = tiles_of<TILE>(a, b0, b1);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += Tiles::of<TILE>(a, b).n + COST;
     long long before = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -110,16 +118,15 @@ __device__ __forceinline__ Run find_run(const PagedDecodeArgs &a, uint8_t *scrat
         if (w < warp) before += totals[w];
         total += totals[w];
     }
-    const long long per_tile = (long long)a.pool.Hkv * a.row_tiles;
-    const long long share = (total * per_tile + gridDim.x - 1) / gridDim.x, begin = share * blockIdx.x;
-    Run r;
-    r.count = min(share, total * per_tile - begin);
-    if (begin >= before * per_tile && begin < (before + mine) * per_tile) {
-        int b = b0;
-        for (;; ++b) {
-            const int n = Tiles::of<TILE>(a, b).n;
-            if (begin < (before + n) * per_tile) {
-                const long long in = begin - before * per_tile;
+    const long long lists = (long long)a.pool.Hkv * a.row_tiles;
+    const long long share = (total * lists + gridDim.x - 1) / gridDim.x, begin = share * blockIdx.x;
+    Run<COST> r;
+    r.count = min(share, total * lists - begin);
+    if (begin >= before * lists && begin < (before + mine) * lists) {
+        for (int b = b0;; ++b) {
+            const int n = Tiles::of<TILE>(a, b).n + COST;
+            if (begin < (before + n) * lists) {
+                const long long in = begin - before * lists;
                 where[0] = b, where[1] = (int)(in / n), where[2] = (int)(in % n);
                 break;
             }
@@ -127,8 +134,8 @@ __device__ __forceinline__ Run find_run(const PagedDecodeArgs &a, uint8_t *scrat
         }
     }
     __syncthreads();
-    r.b = r.u = r.t = 0;
-    if (r.count > 0) r.b = where[0], r.u = where[1], r.t = where[2];
+    r.b = r.u = r.v = 0;
+    if (r.count > 0) r.b = where[0], r.u = where[1], r.v = where[2];
     return r;
 }
 

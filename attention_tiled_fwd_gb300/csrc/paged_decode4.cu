@@ -112,6 +112,9 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+template <int D>
+constexpr int kListCost = D == 64 ? 2 : 1;  // in tiles
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_kernel(PagedDecodeArgs a) {
     using C = Cfg<D, NT>;
@@ -128,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
         }
         fence_mbarrier_init();
     }
-    Run run = find_run<kTile, kThreads>(a, smem + C::kScanOff);  // (its barriers stand behind the set-up too)
+    Run<kListCost<D>> run = find_run<kTile, kThreads, kListCost<D>>(a, smem + C::kScanOff);  // (its barriers stand behind the set-up too)
     launch_dependents();
     const int per_seq = a.pool.Hkv * a.row_tiles;
     int stage = 0;
@@ -144,9 +147,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
         const int row = lane % boxes * box_rows;  // of the tile
         const uint32_t dst = smem_u32(smem) + (value ? C::kHalf : 0) + row * (9 * D / 16);
         const uint8_t *pages = value ? a.pool.v : a.pool.k;
+        long long loaded = 0;
         for (long long left = run.count; left > 0 && ok;) {
             const Tiles tiles = Tiles::of<kTile>(a, run.b);
-            const int t1 = (int)min((long long)tiles.n, run.t + left);
+            int t0, t1;
+            run.part(tiles.n, left, &t0, &t1);
             const uint32_t head = run.u / a.row_tiles * page_bytes;
             // the lane's page of a tile, -1 where the pool has none; -2 where none is needed
             auto page_at = [&](int t) {
@@ -154,8 +159,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
                 if (lane >= 2 * boxes || k0 >= tiles.len || !(k0 + box_rows > tiles.lo || k0 < a.sinks)) return -2;
                 return a.pool.page_of(run.b, k0);
             };
-            int next = page_at(run.t);
-            for (int t = run.t; t < t1; ++t) {
+            int next = t0 < t1 ? page_at(t0) : -2;
+            for (int t = t0; t < t1; ++t, ++loaded) {
                 const int page = next, k0 = tiles.tile(t) * kTile + row;
                 if (t + 1 < t1) next = page_at(t + 1);
                 ok = sleepy_wait(&empty[stage], phase ^ 1, a.status, kSiteEmpty);
@@ -173,12 +178,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
                 }
                 if (++stage == kStages) stage = 0, phase ^= 1;
             }
-            left -= t1 - run.t;
-            run.t = 0;
-            if (++run.u == per_seq) run.u = 0, ++run.b;
+            left = run.next(tiles.n, left, per_seq);
         }
         // the last loads have landed before the CTA leaves
-        const int last = (int)min((long long)kStages, run.count);
+        const int last = (int)min((long long)kStages, loaded);
         for (int i = 0; i < last && ok; ++i) {
             if (--stage < 0) stage = kStages - 1, phase ^= 1;
             ok = sleepy_wait(&full[stage], phase, a.status, kSiteDrain);
@@ -190,7 +193,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
     int tail = -1, tail_parts = 0;
     for (long long left = run.count; left > 0;) {
         const Tiles tiles = Tiles::of<kTile>(a, run.b);
-        const int t1 = (int)min((long long)tiles.n, run.t + left);
+        int t0, t1;
+        run.part(tiles.n, left, &t0, &t1);
+        if (t0 == t1) {  // the run begins or ends in front of the list's first tile
+            left = run.next(tiles.n, left, per_seq);
+            continue;
+        }
         const int h = run.u / a.row_tiles, row0 = run.u % a.row_tiles * kRows;
         const size_t first_row = ((size_t)run.b * a.pool.Hkv + h) * a.R + row0;
         // tiles whose every key exists and is in every row's window
@@ -270,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
             }
         }
 
-        for (int t = run.t; t < t1; ++t) {
+        for (int t = t0; t < t1; ++t) {
             const int tile = tiles.tile(t), key_warp = tile * kTile + warp * (C::kUnits * kUnit);
             const bool plain = tile >= plain0 && tile < plain1;
             const uint32_t ks = smem_u32(smem) + stage * 2 * C::kHalf + warp * (C::kUnits * U::kBytes), vs = ks + C::kHalf;
@@ -480,9 +488,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
 
         // O and L of a list that this CTA holds whole, else a partial: in its first slot what began in a CTA before this one, in
         // its second what goes on behind it
-        const bool whole = run.t == 0 && t1 == tiles.n;
-        const size_t slot = ((size_t)blockIdx.x * 2 + (run.t == 0)) * kRows;
-        if (run.t == 0 && !whole) {
+        const bool whole = t0 == 0 && t1 == tiles.n;
+        const size_t slot = ((size_t)blockIdx.x * 2 + (t0 == 0)) * kRows;
+        if (t0 == 0 && !whole) {
             tail = run.b * per_seq + run.u;
             tail_parts = 1 + (int)((tiles.n - t1 + run.count - 1) / run.count);
         }
@@ -521,9 +529,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
                                  [](int ch) { return 32 * (ch / 32) + 8 * (ch % 4) + ch % 32 / 4; });
             }
         }
-        left -= t1 - run.t;
-        run.t = 0;
-        if (++run.u == per_seq) run.u = 0, ++run.b;
+        left = run.next(tiles.n, left, per_seq);
     }
     if (a.tails && threadIdx.x == 0) a.tails[blockIdx.x] = make_int2(tail, tail_parts);
 }

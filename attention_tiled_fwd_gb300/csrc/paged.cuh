@@ -82,6 +82,22 @@ struct GatherArgs {
 };
 cudaError_t launch_paged_gather(const GatherArgs &a, bool four, cudaStream_t s);
 
+// The cut of a list of work among a grid of CTAs, `per` of them (an SM's first, second, ... CTA each) in each of up to four
+// slots: CTA i of slot k begins at start[k] + i step[k], in 2^-64 of all.  A little work is cut into whole equal runs instead, so
+// that no CTA between two that work has none.
+struct WorkCut {
+    int per;
+    unsigned long long start[4], step[4];
+#ifdef __CUDACC__
+    __device__ __forceinline__ long long begin(unsigned cta, long long total) const {
+        if (cta >= gridDim.x) return total;
+        if (total < 16ll * gridDim.x) return min(total, (long long)(((unsigned)total + gridDim.x - 1) / gridDim.x) * cta);
+        const int k = cta / per;
+        return (long long)__umul64hi((unsigned long long)total, start[k] + (cta - k * per) * step[k]);
+    }
+#endif
+};
+
 struct PagedDecodeArgs {
     const void *q;     // [B, Hkv, R, D] bf16, R = (Hq / Hkv) n_q: the caller's [B, Hq, n_q, D]
     const int *lens;   // [B], clamped to [0, capacity]; null: capacity
@@ -93,15 +109,17 @@ struct PagedDecodeArgs {
     float scale_log2;
     int *status;
     int row_tiles;     // CTAs that share a key head's rows
+    WorkCut cut;
     // two partials a CTA, [2 CTA + slot][rows of a tile]: O, (m, l); and the list that goes on behind a CTA (its number and
     // its partials, -1: none).  All null where no list can be cut.
     float *part_o;
     float2 *part_ml;
     int2 *tails;
 };
-// Keys of a tile, rows of a row tile, and CTAs an SM holds, for a decode of R rows a key head.
+// Keys of a tile, rows of a row tile, CTAs an SM holds, and how much more (1/1000) each of those gets done than the next, for a
+// decode of R rows a key head.
 struct PagedPlan {
-    int tile, rows, per_sm;
+    int tile, rows, per_sm, ahead;
 };
 PagedPlan paged_plan(int R, int D);   // bf16 pages
 PagedPlan paged_plan4(int R, int D);  // 4-bit pages

@@ -38,7 +38,7 @@ struct Cfg {
     static constexpr int kMlOff = kJoinOff + kWarps * kJoinCols * 8 * 4;
     static constexpr int kBarOff = kMlOff + kWarps * 8 * 8;
     static constexpr int kScanOff = kBarOff + 2 * kStages * 8;
-    static constexpr int kAlloc = kScanOff + 64 + 1024;
+    static constexpr int kAlloc = kScanOff + kScan + 1024;
 };
 
 template <int D>
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
     // columns 8-15; values, transposed: (keys 0-7, columns 0-7), (keys 0-7, columns 8-15), then keys 8-15.
     const int mi = lane >> 3, mr = lane & 7;
     const uint32_t k_row = kUnit * warp + mr + (mi & 1) * 8, v_row = kUnit * warp + mr + (mi >> 1) * 8;
-    int tail = -1, tail_parts = 0;
+    int tail = -1, tail_rest = 0;
     for (long long left = run.count; left > 0;) {
         const Tiles tiles = Tiles::of<kTile>(a, run.b);
         int t0, t1;
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
         const size_t slot = ((size_t)blockIdx.x * 2 + (t0 == 0)) * kRows;
         if (t0 == 0 && !whole) {
             tail = run.b * per_seq + run.u;
-            tail_parts = 1 + (int)((tiles.n - t1 + run.count - 1) / run.count);
+            tail_rest = tiles.n - t1;
         }
         float *buf = reinterpret_cast<float *>(smem + C::kJoinOff);
         float2 *ml = reinterpret_cast<float2 *>(smem + C::kMlOff);
@@ -310,7 +310,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
         }
         left = run.next(tiles.n, left, per_seq);
     }
-    if (a.tails && threadIdx.x == 0) a.tails[blockIdx.x] = make_int2(tail, tail_parts);
+    if (a.tails && threadIdx.x == 0)
+        a.tails[blockIdx.x] = make_int2(tail, tail < 0 ? 0 : parts_behind(a.cut, *reinterpret_cast<long long *>(smem + C::kScanOff + kAllOff), tail_rest));
 }
 
 // Adds up the partials of the list that goes on behind CTA blockIdx.x of the kernel before, if one does: the CTA's second
@@ -402,7 +403,7 @@ cudaError_t launch_d(const PagedDecodeArgs &a, int ctas, const CUtensorMap &tk, 
 
 // 8 rows a CTA, or 16 where there are more: twice the products for half the reads.
 PagedPlan paged_plan(int R, int D) {
-    return PagedPlan{kTile, R > 8 ? 16 : 8, D == 64 ? Cfg<64>::kCtas : D == 128 ? Cfg<128>::kCtas : Cfg<256>::kCtas};
+    return PagedPlan{kTile, R > 8 ? 16 : 8, D == 64 ? Cfg<64>::kCtas : D == 128 ? Cfg<128>::kCtas : Cfg<256>::kCtas, 0};
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeArgs &a, int ctas, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s) {

@@ -94,6 +94,17 @@ struct Run {
     }
 };
 
+constexpr int kScan = 80;    // bytes of shared memory that finding the run takes, and its result stays in
+constexpr int kAllOff = 72;  // of them, the number of all steps
+
+// CTAs that hold a part of the list that goes on `rest` steps behind this CTA's run, this one among them.
+static __device__ __noinline__ int parts_behind(const WorkCut &cut, long long all, int rest) {
+    const long long end = cut.begin(blockIdx.x + 1, all) + rest;
+    int c = 2;
+    while (cut.begin(blockIdx.x + c, all) < end) ++c;
+    return c;
+}
+
 // All threads: each adds up the steps of its share of the sequences, and the one whose share the run begins in finds where.
 template <int TILE, int THREADS, int COST>
 __device__ __forceinline__ Run<COST> find_run(const PagedDecodeArgs &a, uint8_t *scratch) {
@@ -118,16 +129,19 @@ __device__ __forceinline__ Run<COST> find_run(const PagedDecodeArgs &a, uint8_t 
         if (w < warp) before += totals[w];
         total += totals[w];
     }
-    const long long lists = (long long)a.pool.Hkv * a.row_tiles;
-    const long long share = (total * lists + gridDim.x - 1) / gridDim.x, begin = share * blockIdx.x;
+    const long long lists = (long long)a.pool.Hkv * a.row_tiles, all = total * lists;
+    const long long begin = a.cut.begin(blockIdx.x, all);
     Run<COST> r;
-    r.count = min(share, total * lists - begin);
+    r.count = a.cut.begin(blockIdx.x + 1, all) - begin;
+    if (threadIdx.x == 0) *reinterpret_cast<long long *>(scratch + kAllOff) = all;  // for parts_behind
     if (begin >= before * lists && begin < (before + mine) * lists) {
         for (int b = b0;; ++b) {
             const int n = Tiles::of<TILE>(a, b).n + COST;
             if (begin < (before + n) * lists) {
                 const long long in = begin - before * lists;
-                where[0] = b, where[1] = (int)(in / n), where[2] = (int)(in % n);
+                where[0] = b;
+                where[1] = in >> 31 ? (int)(in / n) : (int)((unsigned)in / (unsigned)n);  // (64 bits take longer)
+                where[2] = (int)(in - (long long)where[1] * n);
                 break;
             }
             before += n;

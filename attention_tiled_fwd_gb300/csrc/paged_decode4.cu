@@ -42,7 +42,7 @@ struct Cfg {
     static constexpr int kMlOff = kJoinOff + kWarps * kJoinCols * 8 * 4;
     static constexpr int kBarOff = kMlOff + kWarps * 8 * 8;
     static constexpr int kScanOff = kBarOff + 2 * kStages * 8;
-    static constexpr int kAlloc = kScanOff + 64;
+    static constexpr int kAlloc = kScanOff + kScan;
     static_assert(kHalf % 16 == 0 && kBarOff % 8 == 0, "bulk copies start on 16 bytes");
 };
 
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
     }
 
     const int g = lane >> 2, tq = lane & 3;
-    int tail = -1, tail_parts = 0;
+    int tail = -1, tail_rest = 0;
     for (long long left = run.count; left > 0;) {
         const Tiles tiles = Tiles::of<kTile>(a, run.b);
         int t0, t1;
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
         const size_t slot = ((size_t)blockIdx.x * 2 + (t0 == 0)) * kRows;
         if (t0 == 0 && !whole) {
             tail = run.b * per_seq + run.u;
-            tail_parts = 1 + (int)((tiles.n - t1 + run.count - 1) / run.count);
+            tail_rest = tiles.n - t1;
         }
         const float by = E == kTinyScales ? 0x1p-15f : 1.f;  // the scales' own power of two
         float *buf = reinterpret_cast<float *>(smem + C::kJoinOff);
@@ -531,7 +531,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
         }
         left = run.next(tiles.n, left, per_seq);
     }
-    if (a.tails && threadIdx.x == 0) a.tails[blockIdx.x] = make_int2(tail, tail_parts);
+    if (a.tails && threadIdx.x == 0)
+        a.tails[blockIdx.x] = make_int2(tail, tail < 0 ? 0 : parts_behind(a.cut, *reinterpret_cast<long long *>(smem + C::kScanOff + kAllOff), tail_rest));
 }
 
 template <int D, int NT>
@@ -543,9 +544,13 @@ cudaError_t launch_d(const PagedDecodeArgs &a, int ctas, cudaStream_t s) {
     return launch_behind(kern, dim3(ctas), kThreads, Cfg<D, NT>::kAlloc, false, 1, s, a);
 }
 
+// An SM's CTAs that started first are served first: with equal runs three of them ended after 178, 190 and 204 us (64 sequences of
+// 16384 keys), four of D = 64 after 54, 57, 61 and 65.
+constexpr int kAhead = 65;
+
 template <int D, int NT>
 PagedPlan plan_d() {
-    return PagedPlan{Cfg<D, NT>::kTile, 8 * NT, Cfg<D, NT>::kCtas};
+    return PagedPlan{Cfg<D, NT>::kTile, 8 * NT, Cfg<D, NT>::kCtas, NT == 1 && D < 256 ? kAhead : 0};
 }
 
 // 8 rows a CTA, or 16 where there are more: twice the products for half the reads.  (Heads of 256: 8; with 16 the

@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -222,12 +223,12 @@ def _tensor(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: int) 
         _bad(t, name, dtype, shape)
 
 
-def _bad(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> None:
+def _bad(t: torch.Tensor, name: str, dtype: torch.dtype, shape, contiguous: bool = True) -> None:
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
+    if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
 
@@ -537,39 +538,44 @@ def rotation_table(positions: int, rot: int, base: float = 10000.0,
 
 def _pages(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, lens: Optional[torch.Tensor], B: int,
            device: int):
-    """(D, Hkv), (n_pages, page, slots) and the type of a paged cache, its tensors checked."""
-    if k_pages.dim() != 4 or table.dim() != 2:
-        raise ValueError(f"k_pages must have 4 dimensions and table 2, got {list(k_pages.shape)} and {list(table.shape)}")
-    n_pages, Hkv, page, row = k_pages.shape
+    """D, Hkv, n_pages, page, slots and the type of a paged cache, its tensors checked."""
+    shape = k_pages.shape
+    if len(shape) != 4 or table.dim() != 2:
+        raise ValueError(f"k_pages must have 4 dimensions and table 2, got {list(shape)} and {list(table.shape)}")
+    n_pages, Hkv, page, row = shape
     slots = table.shape[1]
     if (n_pages | Hkv | page | row | slots | B) >> 31:
         _no_c_int("a size of the pages or the table")
-    if k_pages.dtype is torch.bfloat16:
+    dtype = k_pages.dtype
+    if dtype is torch.bfloat16:
         D, kind = row, FA_BF16
-    elif k_pages.dtype is torch.uint8:
+    elif dtype is torch.uint8:
         D, kind = row * 16 // 9, FA_INT4
         if row % 9 != 0:
             raise ValueError(f"4-bit pages have 9 D / 16 bytes a position, got {row}")
     else:
-        raise TypeError(f"k_pages must be bfloat16, or uint8 for 4-bit pages, got {k_pages.dtype}")
-    _tensor(k_pages, "k_pages", k_pages.dtype, (n_pages, Hkv, page, row), device)
-    _tensor(v_pages, "v_pages", k_pages.dtype, k_pages.shape, device)
+        raise TypeError(f"k_pages must be bfloat16, or uint8 for 4-bit pages, got {dtype}")
+    if k_pages.get_device() != device or not k_pages.is_contiguous():
+        _bad(k_pages, "k_pages", dtype, shape)
+    if v_pages.shape != shape or v_pages.dtype is not dtype or v_pages.get_device() != device or not v_pages.is_contiguous():
+        _bad(v_pages, "v_pages", dtype, shape)
     _tensor(table, "table", torch.int32, (B, slots), device)
     if lens is not None:
         _tensor(lens, "lens", torch.int32, (B,), device)
     return D, Hkv, n_pages, page, slots, kind
 
 
-def _rows(t: torch.Tensor, name: str, shape, device: int, strides: list) -> int:
-    """The address of bf16 rows [B, H, n, D] whose D channels are neighbours; adds their strides."""
+_NINE = struct.Struct("9q").pack  # nine strides as C's long long
+
+
+def _rows(t: torch.Tensor, name: str, shape, device: int):
+    """The strides between sequences, heads and rows of bf16 rows [B, H, n, D] whose D channels are neighbours."""
     if t.shape != shape or t.dtype is not torch.bfloat16 or t.get_device() != device:
-        _bad(t, name, torch.bfloat16, shape)
-    sb, sh, sn, sd = t.stride()
-    B, H, n, D = shape
-    if sd != 1 and D > 1:
-        raise ValueError(f"{name}'s channels must be neighbours, got strides {list(t.stride())}")
-    strides += (sb if B > 1 else 0, sh if H > 1 else 0, sn if n > 1 else 0)
-    return t.data_ptr()
+        _bad(t, name, torch.bfloat16, shape, contiguous=False)
+    strides = t.stride()
+    if strides[3] != 1 and shape[3] > 1:
+        raise ValueError(f"{name}'s channels must be neighbours, got strides {list(strides)}")
+    return strides
 
 
 def fa_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
@@ -582,53 +588,59 @@ def fa_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_p
     as parts of one projection's output.  lens: int32 [B], the keys each sequence holds with these rows; counts: int32 [B],
     how many of the n rows (the last ones) are new.  cos, sin: fp32 [positions, rot / 2] (rotation_table), None: no
     rotation.  Returns q rotated and contiguous (None without q)."""
-    if k.dim() != 4:
-        raise ValueError(f"k must be [B, Hkv, n, D], got {list(k.shape)}")
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError(f"k must be [B, Hkv, n, D], got {list(shape)}")
     if lens is None:
         raise ValueError("lens is needed: it says where the rows go")
-    B, Hkv, n, D = k.shape
+    B, Hkv, n, D = shape
     dev = _device()
     row, heads, n_pages, page, slots, kind = _pages(k_pages, v_pages, table, lens, B, dev)
     if row != D or heads != Hkv:
-        raise ValueError(f"the pages hold {heads} heads of {row}, got k {list(k.shape)}")
+        raise ValueError(f"the pages hold {heads} heads of {row}, got k {list(shape)}")
     if (n | D) >> 31:
         _no_c_int("a size of k")
-    strides: list = []
-    Hq = 0
+    ks, vs = _rows(k, "k", shape, dev), _rows(v, "v", shape, dev)
     if q is not None:
         if q.dim() != 4 or q.shape[1] < 1 or q.shape[1] >> 31:
             raise ValueError(f"q must be [B, Hq, n, D], got {list(q.shape)}")
         Hq = q.shape[1]
-        q_ptr = _rows(q, "q", (B, Hq, n, D), dev, strides)
+        qs, q_ptr = _rows(q, "q", (B, Hq, n, D), dev), q.data_ptr()
         if q_out is None:
-            q_out = _empty(q, (B, Hq, n, D), torch.bfloat16, stream)
+            q_out = q.new_empty((B, Hq, n, D)) if stream is None else _empty(q, (B, Hq, n, D), torch.bfloat16, stream)
+            out_ptr = q_out.data_ptr()
         else:
             _bf16(q_out, "q_out", (B, Hq, n, D), dev)
-            if q_out.data_ptr() == q_ptr:
+            out_ptr = q_out.data_ptr()
+            if out_ptr == q_ptr:
                 raise ValueError("q_out must not be q")
     elif q_out is not None:
         raise ValueError("q_out is given without q")
     else:
-        q_ptr, strides = None, [0, 0, 0]
-    k_ptr, v_ptr = _rows(k, "k", (B, Hkv, n, D), dev, strides), _rows(v, "v", (B, Hkv, n, D), dev, strides)
-    rot = positions = 0
+        Hq, q_ptr, out_ptr, qs = 0, None, None, ks
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
     if cos is not None:
-        if cos.dim() != 2:
-            raise ValueError(f"cos must be [positions, rot / 2], got {list(cos.shape)}")
-        positions, rot = cos.shape[0], 2 * cos.shape[1]
+        angles = cos.shape
+        if len(angles) != 2:
+            raise ValueError(f"cos must be [positions, rot / 2], got {list(angles)}")
+        positions, rot = angles[0], 2 * angles[1]
         if (positions | rot) >> 31:
             _no_c_int("a size of cos")
-        _tensor(cos, "cos", torch.float32, cos.shape, dev)
-        _tensor(sin, "sin", torch.float32, cos.shape, dev)
+        _tensor(cos, "cos", torch.float32, angles, dev)
+        _tensor(sin, "sin", torch.float32, angles, dev)
+        cos_ptr, sin_ptr = cos.data_ptr(), sin.data_ptr()
+    else:
+        positions = rot = 0
+        cos_ptr = sin_ptr = None
     if counts is not None:
         _tensor(counts, "counts", torch.int32, (B,), dev)
-    rc = _native.load().fa_paged_append(q_ptr, k_ptr, v_ptr, (ctypes.c_longlong * 9)(*strides), _ptr(cos), _ptr(sin),
-                                        table.data_ptr(), lens.data_ptr(), _ptr(counts), _ptr(q_out), k_pages.data_ptr(),
-                                        v_pages.data_ptr(), B, Hq, Hkv, n, D, rot, int(bool(interleaved)), positions, n_pages,
+    rc = _native.load().fa_paged_append(q_ptr, k.data_ptr(), v.data_ptr(), _NINE(*qs[:3], *ks[:3], *vs[:3]), cos_ptr, sin_ptr,
+                                        table.data_ptr(), lens.data_ptr(), _ptr(counts), out_ptr, k_pages.data_ptr(),
+                                        v_pages.data_ptr(), B, Hq, Hkv, n, D, rot, 1 if interleaved else 0, positions, n_pages,
                                         page, slots, kind, _stream_handle(stream, dev))
-    _native.check(rc, "fa_paged_append")
+    if rc:
+        _native.check(rc, "fa_paged_append")
     return q_out
 
 
@@ -646,30 +658,33 @@ def fa_paged_decode(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
 
     table: int32 [B, slots], the sequences' pages; lens: int32 [B], the keys each holds (default: all its pages);
     window None: every earlier key.  Returns (o, lse)."""
-    if q.dim() != 4:
-        raise ValueError(f"q must be [B, Hq, n_q, D], got {list(q.shape)}")
-    B, Hq, n_q, D = q.shape
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError(f"q must be [B, Hq, n_q, D], got {list(shape)}")
+    B, Hq, n_q, D = shape
     dev = _device()
     row, Hkv, n_pages, page, slots, kind = _pages(k_pages, v_pages, table, lens, B, dev)
     if row != D or Hkv < 1 or Hq % Hkv != 0:
-        raise ValueError(f"the pages hold {Hkv} heads of {row}, got q {list(q.shape)}")
+        raise ValueError(f"the pages hold {Hkv} heads of {row}, got q {list(shape)}")
     if (Hq | n_q) >> 31:
         _no_c_int("a size of q")
-    _bf16(q, "q", (B, Hq, n_q, D), dev)
+    _bf16(q, "q", shape, dev)
     if o is None:
         o = _empty_like(q, stream)
     else:
-        _bf16(o, "o", q.shape, dev)
+        _bf16(o, "o", shape, dev)
     if lse is None:
-        lse = _empty(q, (B, Hq, n_q), torch.float32, stream)
+        rows = (B, Hq, n_q)
+        lse = q.new_empty(rows, dtype=torch.float32) if stream is None else _empty(q, rows, torch.float32, stream)
     else:
         _tensor(lse, "lse", torch.float32, (B, Hq, n_q), dev)
     workspace = _workspace(workspace, q, stream, dev, "fa_paged_decode_workspace_bytes", B, Hq, Hkv, n_q, D, page, slots, kind)
     rc = _native.load().fa_paged_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), _ptr(lens),
                                         o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, n_q, D, n_pages, page, slots,
-                                        _c_int(slots * page if window is None else window), _c_int(sinks), _scale(scale, D),
-                                        kind, _ptr(workspace), _nbytes(workspace), _stream_handle(stream, dev))
-    _native.check(rc, "fa_paged_decode")
+                                        slots * page if window is None else _c_int(window), _c_int(sinks) if sinks else 0,
+                                        _scale(scale, D), kind, _ptr(workspace), _nbytes(workspace), _stream_handle(stream, dev))
+    if rc:
+        _native.check(rc, "fa_paged_decode")
     return o, lse
 
 

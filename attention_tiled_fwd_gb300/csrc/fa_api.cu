@@ -926,8 +926,9 @@ extern "C" int fa_paged_append(const void *q, const void *k, const void *v, cons
         const int heads = t == 0 ? Hq : Hkv;
         long long *to = t == 0 ? a.sq : t == 1 ? a.sk : a.sv;
         const long long plain[3] = {(long long)heads * n * D, (long long)n * D, D};
+        const int sizes[3] = {B, heads, n};
         for (int i = 0; i < 3; ++i) {
-            to[i] = strides ? strides[3 * t + i] : plain[i];
+            to[i] = sizes[i] <= 1 ? 0 : strides ? strides[3 * t + i] : plain[i];
             if (to[i] % 8 != 0) return FA_ERR_ALIGN;
         }
     }

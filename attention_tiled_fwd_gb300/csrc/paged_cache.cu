@@ -54,6 +54,7 @@ __device__ __noinline__ uint32_t turn_pair(uint32_t xa, uint32_t xb, float c0, f
 }
 
 // The rotation of a lane's 8 channels: its own times cos plus their partners' times (signed) sin.
+template <bool INTERLEAVED>
 struct Turn {
     float c[8], s[8];
     bool on;
@@ -66,7 +67,7 @@ struct Turn {
         if (!on) return;
         const int half = a.rot / 2;
         const float *cs = a.cos + (size_t)p * half, *sn = a.sin + (size_t)p * half;
-        if (a.interleaved) {
+        if constexpr (INTERLEAVED) {
             const float4 x = *reinterpret_cast<const float4 *>(cs + 4 * cl), y = *reinterpret_cast<const float4 *>(sn + 4 * cl);
             c[0] = c[1] = x.x, c[2] = c[3] = x.y, c[4] = c[5] = x.z, c[6] = c[7] = x.w;
             s[0] = -y.x, s[1] = y.x, s[2] = -y.y, s[3] = y.y, s[4] = -y.z, s[5] = y.z, s[6] = -y.w, s[7] = y.w;
@@ -84,10 +85,10 @@ struct Turn {
     }
 
     // All lanes of the warp take part.
-    __device__ __forceinline__ uint4 apply(const AppendArgs &a, const uint4 &x) const {
+    __device__ __forceinline__ uint4 apply(const uint4 &x, int lane) const {
         uint4 o;
-        const int from = (threadIdx.x & 31) + partner;
-        if (a.interleaved) {
+        const int from = lane + partner;
+        if constexpr (INTERLEAVED) {
             o = make_uint4(x.x >> 16 | x.x << 16, x.y >> 16 | x.y << 16, x.z >> 16 | x.z << 16, x.w >> 16 | x.w << 16);
         } else {
             o.x = __shfl_sync(0xffffffffu, x.x, from);
@@ -126,52 +127,64 @@ struct NewRows {
     }
 };
 
-// Rows of one token and tensor: lane `cl` of a row's D / 8 holds 8 channels, of kHeadsPerLane heads in turn.  `part`: the
-// block of q's heads, then (bf16 pages) of k's, then of v's.
-template <int D, bool FOUR>
-__device__ __forceinline__ void token_rows(const AppendArgs &a, int b, int i, int part) {
+// Rows of one token: lane `cl` of a row's D / 8 holds 8 channels, of kHeadsPerLane heads in turn, a block of heads.  `part`: `per`
+// blocks of q, then (bf16 pages) a block of k and v.
+template <int D, bool FOUR, bool INTERLEAVED>
+__device__ __forceinline__ void token_rows(const AppendArgs &a, int b, int i, int part, int per) {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBlock = kRows * kHeadsPerLane;
     const int lane = threadIdx.x & 31, cl = lane % kLanes, sub = lane / kLanes;
-    const int q_parts = (a.Hq + kBlock - 1) / kBlock, kv_parts = (a.pool.Hkv + kBlock - 1) / kBlock;
-    const bool is_q = FOUR || part < q_parts, is_k = !is_q && part < q_parts + kv_parts;
-    if (!is_q) part -= is_k ? q_parts : q_parts + kv_parts;
-    const int heads = is_q ? a.Hq : a.pool.Hkv, h0 = part * kBlock + sub;
-    const long long *st = is_q ? a.sq : is_k ? a.sk : a.sv;
-    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(is_q ? a.q : is_k ? a.k : a.v) + b * st[0] + h0 * st[1] + i * st[2] + 8 * cl;
-    uint4 x[kHeadsPerLane];  // (rows that are not new too: the loads need not wait for the lengths)
+    const int q_parts = (a.Hq + per * kBlock - 1) / (per * kBlock);
+    const bool is_q = FOUR || part < q_parts;
+    const int heads = is_q ? a.Hq : a.pool.Hkv;
+    int h = (is_q ? part * per : part - q_parts) * kBlock + sub;  // this lane's first head of a block
+    auto fetch = [&](uint4(&x)[kHeadsPerLane], const void *t, const long long *st) {
+        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(t) + b * st[0] + h * st[1] + i * st[2] + 8 * cl;
+        const long long step = kRows * st[1];
 #pragma unroll
-    for (int u = 0; u < kHeadsPerLane; ++u) {
-        x[u] = make_uint4(0, 0, 0, 0);
-        if (h0 + u * kRows < heads) x[u] = __ldg(reinterpret_cast<const uint4 *>(src + u * kRows * st[1]));
-    }
+        for (int u = 0; u < kHeadsPerLane; ++u, src += step) {
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (h + u * kRows < heads) x[u] = __ldg(reinterpret_cast<const uint4 *>(src));
+        }
+    };
+    uint4 x[kHeadsPerLane];  // (rows that are not new too: the loads need not wait for the lengths)
+    fetch(x, is_q ? a.q : a.k, is_q ? a.sq : a.sk);
     const NewRows rows(a, b);
     const int p = rows.start + i;
     const bool there = p >= rows.first && p < a.pool.capacity();
-    int page = 0;
-    if (!is_q && p >= rows.first) {
-        page = there ? a.pool.page_of(b, p) : -1;
-        if (page < 0 && lane == 0) record_failure(a.status, kErrPage, 0);
-    }
-    if (!is_q && (!there || page < 0)) return;
-    Turn turn;
+    Turn<INTERLEAVED> turn;
     turn.on = false, turn.partner = 0;
-    const bool turns = there && a.rot > 0 && (is_q || is_k);
-    if (turns) turn.load(a, p, cl);
-    uint8_t *to;
-    size_t step;
+    if (there && a.rot > 0) turn.load(a, p, cl);
     if (is_q) {
-        to = reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(a.q_out) + (((size_t)b * a.Hq + h0) * a.n + i) * D);
-        step = (size_t)kRows * a.n * D * 2;
-    } else {
-        to = (is_k ? a.pool.k : a.pool.v) + a.pool.at(page, h0, p, 2 * D);
-        step = ((size_t)kRows << a.pool.shift) * 2 * D;
-    }
+        uint4 *to = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.q_out) + (((size_t)b * a.Hq + h) * a.n + i) * D) + cl;
+        const size_t step = (size_t)kRows * a.n * (D / 8);
+        for (int block = 0;;) {
 #pragma unroll
-    for (int u = 0; u < kHeadsPerLane; ++u) {
-        if (part * kBlock + u * kRows >= heads) break;
-        uint4 y = turns ? turn.apply(a, x[u]) : x[u];
-        if (!there) y = make_uint4(0, 0, 0, 0);
-        if (h0 + u * kRows < heads) reinterpret_cast<uint4 *>(to + u * step)[cl] = y;
+            for (int u = 0; u < kHeadsPerLane; ++u, to += step) {
+                if (h - sub + u * kRows >= heads) return;
+                const uint4 y = !there ? make_uint4(0, 0, 0, 0) : a.rot > 0 ? turn.apply(x[u], lane) : x[u];
+                if (h + u * kRows < heads) *to = y;
+            }
+            if (++block == per) return;
+            h += kBlock;
+            fetch(x, a.q, a.sq);
+        }
+    } else if constexpr (!FOUR) {
+        if (p < rows.first) return;
+        const int page = there ? a.pool.page_of(b, p) : -1;
+        if (page < 0) {
+            if (lane == 0) record_failure(a.status, kErrPage, 0);
+            return;
+        }
+        uint4 v[kHeadsPerLane];
+        fetch(v, a.v, a.sv);
+        const size_t at = a.pool.at(page, h, p, 2 * D), step = ((size_t)kRows << a.pool.shift) * (D / 8);
+        uint4 *to_k = reinterpret_cast<uint4 *>(a.pool.k + at) + cl, *to_v = reinterpret_cast<uint4 *>(a.pool.v + at) + cl;
+#pragma unroll
+        for (int u = 0; u < kHeadsPerLane; ++u, to_k += step, to_v += step) {
+            if (h - sub + u * kRows >= heads) return;
+            const uint4 y = a.rot > 0 ? turn.apply(x[u], lane) : x[u];
+            if (h + u * kRows < heads) *to_k = y, *to_v = v[u];
+        }
     }
 }
 
@@ -202,7 +215,7 @@ __device__ __forceinline__ uint32_t quantise(const uint4 &y, __half *scale) {
 
 // 4-bit rows of a head's keys or values: a lane holds 8 channels of an even position and of the odd one behind it, so a warp
 // the 64 / (D / 8) positions of a block of them (never of two units).
-template <int D>
+template <int D, bool INTERLEAVED>
 __device__ __forceinline__ void unit_rows(const AppendArgs &a, int b, int block, int part) {
     using U = Unit4<D>;
     constexpr int kLanes = D / 8, kBlock = 64 / kLanes;
@@ -231,10 +244,10 @@ __device__ __forceinline__ void unit_rows(const AppendArgs &a, int b, int block,
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         if (key && a.rot > 0) {
-            Turn turn;
+            Turn<INTERLEAVED> turn;
             turn.on = false, turn.partner = 0;
             if (there[e]) turn.load(a, p0 + e, cl);
-            x[e] = turn.apply(a, x[e]);
+            x[e] = turn.apply(x[e], lane);
         }
         codes[e] = quantise(x[e], &scale[e]);
     }
@@ -272,30 +285,42 @@ __device__ __forceinline__ void unit_rows(const AppendArgs &a, int b, int block,
 }
 
 // blockIdx.y: the sequence.  Along x the rows of tokens, then the 4-bit rows, a warp each.
-template <int D, bool FOUR>
-__global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(AppendArgs a, FastDiv parts, FastDiv unit_parts, int row_tasks, int unit_tasks) {
+template <int D, bool FOUR, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads, 4)
+    paged_append_kernel(AppendArgs a, FastDiv parts, FastDiv unit_parts, int row_tasks, int unit_tasks, int per) {
     const int task = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), b = blockIdx.y;
     if (task < row_tasks) {
         const int i = parts.div(task);
-        token_rows<D, FOUR>(a, b, i, task - i * parts.d);
+        token_rows<D, FOUR, INTERLEAVED>(a, b, i, task - i * parts.d, per);
     } else if constexpr (FOUR) {
         const int unit = task - row_tasks;
         if (unit >= unit_tasks) return;
         const int block = unit_parts.div(unit);
-        unit_rows<D>(a, b, block, unit - block * unit_parts.d);
+        unit_rows<D, INTERLEAVED>(a, b, block, unit - block * unit_parts.d);
     }
 }
 
-template <int D, bool FOUR>
+template <int D, bool FOUR, bool INTERLEAVED>
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
     constexpr int kBlock = 32 / (D / 8) * kHeadsPerLane, kWarps = kThreads / 32, kPositions = 64 / (D / 8);
-    const int Hkv = a.pool.Hkv;
-    const int parts = (a.Hq + kBlock - 1) / kBlock + (FOUR ? 0 : 2 * ((Hkv + kBlock - 1) / kBlock));
+    const int Hkv = a.pool.Hkv, q_blocks = (a.Hq + kBlock - 1) / kBlock;
+    // A warp takes up to four blocks of q where that leaves 32 warps an SM twice over: what it does once (lengths, angles, addresses)
+    // is as much as two blocks' rotation (4 x 4096 rows, 16/4 heads: 41 us with one).
+    const long long warps = (long long)a.B * a.n * q_blocks;
+    const int per = (int)std::max(1ll, std::min<long long>(std::min(4, q_blocks), warps / (64 * kNumSms)));
+    const int parts = (q_blocks + per - 1) / per + (FOUR ? 0 : (Hkv + kBlock - 1) / kBlock);
     const int blocks = a.n == 1 ? 1 : (a.n + kPositions - 2) / kPositions + 1;  // of positions that n rows meet at most
     const int row_tasks = a.n * parts, unit_tasks = FOUR ? blocks * 2 * Hkv : 0;
     const dim3 grid((row_tasks + unit_tasks + kWarps - 1) / kWarps, a.B);
-    paged_append_kernel<D, FOUR><<<grid, kThreads, 0, s>>>(a, FastDiv(std::max(parts, 1)), FastDiv(2 * Hkv), row_tasks, unit_tasks);
+    paged_append_kernel<D, FOUR, INTERLEAVED>
+        <<<grid, kThreads, 0, s>>>(a, FastDiv(std::max(parts, 1)), FastDiv(2 * Hkv), row_tasks, unit_tasks, per);
     return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_append_d(const AppendArgs &a, bool four, cudaStream_t s) {
+    if (a.interleaved) return four ? launch_append<D, true, true>(a, s) : launch_append<D, false, true>(a, s);
+    return four ? launch_append<D, true, false>(a, s) : launch_append<D, false, false>(a, s);
 }
 
 // One unit of 16 positions of a head's keys or values a warp.
@@ -372,9 +397,9 @@ cudaError_t launch_gather(const GatherArgs &a, cudaStream_t s) {
 
 cudaError_t launch_paged_append(const AppendArgs &a, bool four, cudaStream_t s) {
     switch (a.D) {
-        case 64: return four ? launch_append<64, true>(a, s) : launch_append<64, false>(a, s);
-        case 128: return four ? launch_append<128, true>(a, s) : launch_append<128, false>(a, s);
-        case 256: return four ? launch_append<256, true>(a, s) : launch_append<256, false>(a, s);
+        case 64: return launch_append_d<64>(a, four, s);
+        case 128: return launch_append_d<128>(a, four, s);
+        case 256: return launch_append_d<256>(a, four, s);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -342,7 +342,7 @@ FA_API int fa_prefix_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q, int
 /*
  * fa_paged_append -- the n newest rows of each sequence: q and k rotated by their positions, k and v put in their pages.
  *   q [B, Hq, n, D], k, v [B, Hkv, n, D] bf16; strides: host array of 9, the distances in elements between sequences,
- *   heads and rows of q, of k and of v (multiples of 8; rows of D are contiguous), NULL: contiguous tensors.
+ *   heads and rows of q, of k and of v (multiples of 8, but for sizes of 1; rows of D are contiguous), NULL: contiguous.
  *   Row i sits at position lens[b] - n + i.  counts (device array of B ints, NULL: n): the last counts[b] rows are new;
  *   rows before them and rows before position 0 are left out.  q may be NULL (then Hq = 0 and q_out NULL);
  *   q_out [B, Hq, n, D] contiguous, not q itself: rotated rows, zeros for rows that are left out or past the capacity.

@@ -966,7 +966,7 @@ struct PagedGrid {
 PagedGrid paged_grid(int B, int Hq, int Hkv, int n_q, int D, int capacity, bool four, int num_sms) {
     PagedGrid g;
     const int R = Hq / Hkv * n_q;
-    g.plan = four ? paged_plan4(R, D) : paged_plan(R, D);
+    g.plan = four ? paged_plan4(D) : paged_plan(R, D);
     g.row_tiles = (R + g.plan.rows - 1) / g.plan.rows;
     const long long tiles = (capacity + g.plan.tile - 1) / g.plan.tile, lists = (long long)B * Hkv * g.row_tiles;
     g.ctas = (int)std::min<long long>(lists * tiles, (long long)num_sms * g.plan.per_sm);

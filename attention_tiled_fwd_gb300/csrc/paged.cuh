@@ -122,7 +122,7 @@ struct PagedPlan {
     int tile, rows, per_sm, ahead;
 };
 PagedPlan paged_plan(int R, int D);   // bf16 pages
-PagedPlan paged_plan4(int R, int D);  // 4-bit pages
+PagedPlan paged_plan4(int D);        // 4-bit pages
 // tk, tv: the pools' tensor maps (boxes of 64 columns and of the rows of a page, at most a tile's).
 cudaError_t launch_paged_decode(const PagedDecodeArgs &a, int ctas, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s);
 cudaError_t launch_paged_decode4(const PagedDecodeArgs &a, int ctas, cudaStream_t s);

@@ -31,13 +31,13 @@ constexpr int kTinyScales = -22;  // E while no scale has reached 2^-15: they ar
 
 enum : int { kSiteEmpty = 311, kSiteFull, kSiteDrain };
 
-template <int D, int NT>
+template <int D>
 struct Cfg {
     static constexpr int kUnits = D < 256 ? 2 : 1;                       // of 16 keys, a warp and tile
     static constexpr int kTile = kWarps * kUnits * kUnit;                // keys
     static constexpr int kHalf = kTile * 9 * D / 16;                     // bytes of the tile's keys, or of its values
     static constexpr int kStages = D == 128 ? 3 : 4;
-    static constexpr int kCtas = D == 64 ? (NT == 1 ? 4 : 3) : D == 128 && NT == 1 ? 3 : 2;  // an SM
+    static constexpr int kCtas = D == 64 ? 4 : D == 128 ? 3 : 2;         // an SM
     static constexpr int kJoinOff = kStages * 2 * kHalf;
     static constexpr int kMlOff = kJoinOff + kWarps * kJoinCols * 8 * 4;
     static constexpr int kBarOff = kMlOff + kWarps * 8 * 8;
@@ -46,8 +46,8 @@ struct Cfg {
     static_assert(kHalf % 16 == 0 && kBarOff % 8 == 0, "bulk copies start on 16 bytes");
 };
 
-__device__ uint4 g_zero_units[Cfg<128, 1>::kHalf / 16];  // what a page that the pool has not reads as
-static_assert(Cfg<256, 1>::kHalf <= Cfg<128, 1>::kHalf && Cfg<64, 1>::kHalf <= Cfg<128, 1>::kHalf, "a box fits");
+__device__ uint4 g_zero_units[Cfg<128>::kHalf / 16];  // what a page that the pool has not reads as
+static_assert(Cfg<256>::kHalf <= Cfg<128>::kHalf && Cfg<64>::kHalf <= Cfg<128>::kHalf, "a box fits");
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -112,14 +112,75 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// A list's q as the products take it, lane by lane: operands of row g (`there`: it exists), the groups' -8 sum q as an operand
+// against the keys' scales, in two parts, and the factors that take the scores of rows 2 tq and 2 tq + 1 to log2 units.
+template <int D>
+__device__ __forceinline__ void prepare_q(const __nv_bfloat16 *q, bool there, float scale_log2, int lane, uint32_t (&qf)[D / 16][2],
+                                          uint32_t (&less)[2], float (&f)[2]) {
+    constexpr int kGroups = D / 32;
+    const int tq = lane & 3;
+    uint4 x[kGroups];
+    uint32_t most = 0;
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j) {
+        x[j] = there ? __ldg(reinterpret_cast<const uint4 *>(q) + 4 * j + tq) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) most = max(most, max(w[i] << 16 & 0x7fff0000u, w[i] & 0x7fff0000u));
+    }
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+    // the row's largest magnitude becomes 2^14 .. 2^15 (a row of zeros or of the smallest numbers: less)
+    const int up = min(114, 14 - max(-100, (int)(most >> 23) - 127));
+    const float by = __int_as_float((127 + up) << 23);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int shift = 24 - __shfl_sync(0xffffffffu, up, 4 * (2 * tq + e));  // the codes' 2^-24 too
+        f[e] = fmaxf(scale_log2 * __int_as_float((127 + shift / 2) << 23) * __int_as_float((127 + shift - shift / 2) << 23),
+                      1.2e-38f);  // (above 0: -inf times it stays -inf)
+    }
+    uint32_t part[2][kGroups];  // fp16 of -8 2^-24 sum q, and of what that leaves
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j) {
+        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+        float c[8], sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            c[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) * by;
+            if (i & 1) c[i] *= 0.0625f;
+        }
+        qf[2 * j][0] = pack_h2(c[0], c[4]), qf[2 * j][1] = pack_h2(c[1], c[5]);
+        qf[2 * j + 1][0] = pack_h2(c[2], c[6]), qf[2 * j + 1][1] = pack_h2(c[3], c[7]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 even = unpack_h2(qf[2 * j + i][0]), odd = unpack_h2(qf[2 * j + i][1]);
+            sum += (even.x + even.y) + 16.f * (odd.x + odd.y);
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sum *= -0x1p-21f;
+        const __half high = __float2half_rn(sum);
+        part[0][j] = __half_as_ushort(high);
+        part[1][j] = __half_as_ushort(__float2half_rn(sum - __half2float(high)));
+    }
+    // the operand's columns: the groups' first parts, then their second ones (lane tq: two columns of each eight)
+    less[0] = less[1] = 0u;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        const int at = i % (kGroups / 2), second = i / (kGroups / 2);
+        const uint32_t two = part[second][2 * at] | part[second][2 * at + 1] << 16;
+        if (tq == i % 4) less[i / 4] = two;
+    }
+}
+
 template <int D>
 constexpr int kListCost = D == 64 ? 2 : 1;  // in tiles
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_kernel(PagedDecodeArgs a) {
-    using C = Cfg<D, NT>;
+template <int D>
+__global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(PagedDecodeArgs a) {
+    using C = Cfg<D>;
     using U = Unit4<D>;
-    constexpr int kTile = C::kTile, kGroups = D / 32, kRows = 8 * NT, kStages = C::kStages;
+    constexpr int kTile = C::kTile, kGroups = D / 32, kRows = 8, kStages = C::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOff), *empty = full + kStages;
@@ -206,283 +267,194 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
         const int plain0 = past < 0 ? 0 : past / kTile + 1, plain1 = (p_first + 1) / kTile;
 
         // off: the running maximum (log2 units), plus the weights' power of two; kNone while a row has seen nothing
-        float off[NT][2], l[NT][2], f[NT][2], o[NT][D / 16][4];
+        float off[2], l[2], f[2], o[D / 16][4];
         auto position = [&](int r) { return tiles.len - a.n_q + (row0 + r) % a.n_q; };  // rows past R: any; they are not stored
-        uint32_t qf[NT][D / 16][2];
-        uint32_t less[NT][2];  // -8 sum q of each group as an operand against the keys' scales, in two parts
-        float ones[NT][kGroups][4];  // sum P s of a group (the same in the second two)
+        uint32_t qf[D / 16][2], less[2];
+        float ones[kGroups][4];  // sum P s of a group (the same in the second two)
         int E = kTinyScales, Ep = -7;  // powers of two of the weights times scales, and of the weights
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int e = 0; e < 2; ++e) off[e] = kNone, l[e] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) off[n][e] = kNone, l[n][e] = 0.f;
+        for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)
+            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
-            const bool there = row0 + 8 * n + g < a.R;
-            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + (first_row + 8 * n + g) * D;
-#pragma unroll
-            for (int j = 0; j < kGroups; ++j) ones[n][j][0] = ones[n][j][1] = ones[n][j][2] = ones[n][j][3] = 0.f;
-            uint4 x[kGroups];
-            uint32_t most = 0;
-#pragma unroll
-            for (int j = 0; j < kGroups; ++j) {
-                x[j] = there ? __ldg(reinterpret_cast<const uint4 *>(q) + 4 * j + tq) : make_uint4(0, 0, 0, 0);
-                const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) most = max(most, max(w[i] << 16 & 0x7fff0000u, w[i] & 0x7fff0000u));
-            }
-            most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-            most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-            // the row's largest magnitude becomes 2^14 .. 2^15 (a row of zeros or of the smallest numbers: less)
-            const int up = min(114, 14 - max(-100, (int)(most >> 23) - 127));
-            const float by = __int_as_float((127 + up) << 23);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int shift = 24 - __shfl_sync(0xffffffffu, up, 4 * (2 * tq + e));  // the codes' 2^-24 too
-                f[n][e] = fmaxf(a.scale_log2 * __int_as_float((127 + shift / 2) << 23) * __int_as_float((127 + shift - shift / 2) << 23),
-                                1.2e-38f);  // (above 0: -inf times it stays -inf)
-            }
-            uint32_t part[2][kGroups];  // fp16 of -8 2^-24 sum q, and of what that leaves
-#pragma unroll
-            for (int j = 0; j < kGroups; ++j) {
-                const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-                float c[8], sum = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    c[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) * by;
-                    if (i & 1) c[i] *= 0.0625f;
-                }
-                qf[n][2 * j][0] = pack_h2(c[0], c[4]), qf[n][2 * j][1] = pack_h2(c[1], c[5]);
-                qf[n][2 * j + 1][0] = pack_h2(c[2], c[6]), qf[n][2 * j + 1][1] = pack_h2(c[3], c[7]);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float2 even = unpack_h2(qf[n][2 * j + i][0]), odd = unpack_h2(qf[n][2 * j + i][1]);
-                    sum += (even.x + even.y) + 16.f * (odd.x + odd.y);
-                }
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                sum *= -0x1p-21f;
-                const __half high = __float2half_rn(sum);
-                part[0][j] = __half_as_ushort(high);
-                part[1][j] = __half_as_ushort(__float2half_rn(sum - __half2float(high)));
-            }
-            // the operand's columns: the groups' first parts, then their second ones (lane tq: two columns of each eight)
-            less[n][0] = less[n][1] = 0u;
-#pragma unroll
-            for (int i = 0; i < kGroups; ++i) {
-                const int at = i % (kGroups / 2), second = i / (kGroups / 2);
-                const uint32_t two = part[second][2 * at] | part[second][2 * at + 1] << 16;
-                if (tq == i % 4) less[n][i / 4] = two;
-            }
-        }
+        for (int j = 0; j < kGroups; ++j) ones[j][0] = ones[j][1] = ones[j][2] = ones[j][3] = 0.f;
+        prepare_q<D>(static_cast<const __nv_bfloat16 *>(a.q) + (first_row + g) * D, row0 + g < a.R, a.scale_log2, lane, qf, less, f);
 
         for (int t = t0; t < t1; ++t) {
             const int tile = tiles.tile(t), key_warp = tile * kTile + warp * (C::kUnits * kUnit);
             const bool plain = tile >= plain0 && tile < plain1;
             const uint32_t ks = smem_u32(smem) + stage * 2 * C::kHalf + warp * (C::kUnits * U::kBytes), vs = ks + C::kHalf;
-            float sc[C::kUnits][NT][4];  // S^T of the warp's units: keys g and g + 8, rows 2 tq and 2 tq + 1
+            float sc[C::kUnits][4];  // S^T of the warp's units: keys g and g + 8, rows 2 tq and 2 tq + 1
             if (ok) ok = sleepy_wait(&full[stage], phase, a.status, kSiteFull);  // (after a time-out: on whatever is there)
-            {
 #pragma unroll
-                for (int w = 0; w < C::kUnits; ++w) {
-                    const int key0 = key_warp + w * kUnit;
-                    const uint32_t at = ks + w * U::kBytes, scales = at + U::kCodes;
-                    uint32_t code[2][kGroups], s2[2][kGroups / 2], by[4];
-                    load_codes<D>(code, at, lane);
+            for (int w = 0; w < C::kUnits; ++w) {
+                const int key0 = key_warp + w * kUnit;
+                const uint32_t at = ks + w * U::kBytes, scales = at + U::kCodes;
+                uint32_t code[2][kGroups], s2[2][kGroups / 2], by[4];
+                load_codes<D>(code, at, lane);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    load_words(s2[half], scales + 2 * U::k_scale(g + 8 * half, 0));
+                    uint32_t two[1];
+                    load_words(two, scales + 2 * U::k_scale(g + 8 * half, 2 * (tq % (kGroups / 2))));
+                    by[half] = by[2 + half] = two[0];
+                }
+                mma_f16_new(sc[w], by, less[0], less[1]);
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j) {
+                    uint32_t x[4], y[4];
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        load_words(s2[half], scales + 2 * U::k_scale(g + 8 * half, 0));
-                        uint32_t two[1];
-                        load_words(two, scales + 2 * U::k_scale(g + 8 * half, 2 * (tq % (kGroups / 2))));
-                        by[half] = by[2 + half] = two[0];
+                        const uint32_t c = code[half][j], d = c >> 8;
+                        x[half] = c & 0x000f000fu, x[2 + half] = c & 0x00f000f0u;
+                        y[half] = d & 0x000f000fu, y[2 + half] = d & 0x00f000f0u;
                     }
+                    const float2 sa = unpack_h2(s2[0][j / 2]), sb = unpack_h2(s2[1][j / 2]);
+                    const float s_lo = j & 1 ? sa.y : sa.x, s_hi = j & 1 ? sb.y : sb.x;
+                    float part[4];
+                    mma_f16_new(part, x, qf[2 * j][0], qf[2 * j][1]);
+                    mma_f16(part, y, qf[2 * j + 1][0], qf[2 * j + 1][1]);
+                    sc[w][0] = fmaf(s_lo, part[0], sc[w][0]), sc[w][1] = fmaf(s_lo, part[1], sc[w][1]);
+                    sc[w][2] = fmaf(s_hi, part[2], sc[w][2]), sc[w][3] = fmaf(s_hi, part[3], sc[w][3]);
+                }
+                if (!plain) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_f16_new(sc[w][n], by, less[n][0], less[n][1]);
-#pragma unroll
-                    for (int j = 0; j < kGroups; ++j) {
-                        uint32_t x[4], y[4];
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const uint32_t c = code[half][j], d = c >> 8;
-                            x[half] = c & 0x000f000fu, x[2 + half] = c & 0x00f000f0u;
-                            y[half] = d & 0x000f000fu, y[2 + half] = d & 0x00f000f0u;
-                        }
-                        const float2 sa = unpack_h2(s2[0][j / 2]), sb = unpack_h2(s2[1][j / 2]);
-                        const float s_lo = j & 1 ? sa.y : sa.x, s_hi = j & 1 ? sb.y : sb.x;
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            float part[4];
-                            mma_f16_new(part, x, qf[n][2 * j][0], qf[n][2 * j][1]);
-                            mma_f16(part, y, qf[n][2 * j + 1][0], qf[n][2 * j + 1][1]);
-                            sc[w][n][0] = fmaf(s_lo, part[0], sc[w][n][0]), sc[w][n][1] = fmaf(s_lo, part[1], sc[w][n][1]);
-                            sc[w][n][2] = fmaf(s_hi, part[2], sc[w][n][2]), sc[w][n][3] = fmaf(s_hi, part[3], sc[w][n][3]);
-                        }
-                    }
-                    if (!plain) {
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint32_t seen = seen_keys(position(8 * n + 2 * tq + e), key0, a.window, a.sinks);
-                                if (!(seen >> g & 1u)) sc[w][n][e] = -INFINITY;
-                                if (!(seen >> (g + 8) & 1u)) sc[w][n][2 + e] = -INFINITY;
-                            }
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t seen = seen_keys(position(2 * tq + e), key0, a.window, a.sinks);
+                        if (!(seen >> g & 1u)) sc[w][e] = -INFINITY;
+                        if (!(seen >> (g + 8) & 1u)) sc[w][2 + e] = -INFINITY;
                     }
                 }
-                // scales of the values of keys 2 tq and 2 tq + 1 (+ 8)
-                uint32_t s2[C::kUnits][2][kGroups];
-                uint32_t bits = 0;
+            }
+            // scales of the values of keys 2 tq and 2 tq + 1 (+ 8)
+            uint32_t s2[C::kUnits][2][kGroups], bits = 0;
 #pragma unroll
-                for (int w = 0; w < C::kUnits; ++w) {
+            for (int w = 0; w < C::kUnits; ++w) {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) load_words(s2[w][half], vs + w * U::kBytes + U::kCodes + 2 * U::v_scale(2 * tq + 8 * half, 0));
-                    if (!plain) {
-                        // keys that no row sees: 0 times whatever their scales are must not reach O.  (A row's own keys alone
-                        // where a lane holds one row: what other rows see may be no number either.)
-                        const int key0 = key_warp + w * kUnit;
-                        uint32_t keep[2];
-                        keep_seen(keep, NT == 1 ? seen_keys(position(g), key0, a.window, a.sinks) : used_keys(tiles, key0, a.sinks), tq);
-#pragma unroll
-                        for (int half = 0; half < 2; ++half)
-#pragma unroll
-                            for (int j = 0; j < kGroups; ++j) s2[w][half][j] &= keep[half];
-                    }
+                for (int half = 0; half < 2; ++half) load_words(s2[w][half], vs + w * U::kBytes + U::kCodes + 2 * U::v_scale(2 * tq + 8 * half, 0));
+                if (!plain) {
+                    // 0 times whatever the scales are of keys that the lane's row g does not see must not reach O
+                    const int key0 = key_warp + w * kUnit;
+                    uint32_t keep[2];
+                    keep_seen(keep, seen_keys(position(g), key0, a.window, a.sinks), tq);
 #pragma unroll
                     for (int half = 0; half < 2; ++half)
 #pragma unroll
-                        for (int j = 0; j < kGroups; ++j) bits |= s2[w][half][j];
+                        for (int j = 0; j < kGroups; ++j) s2[w][half][j] &= keep[half];
                 }
-                // A weight is 2^8 at most, so its products with scales below 2^(E + 7) fit in fp16.  The scales' bits
-                // together are no less than the largest (and less than twice it, or all of 2^(1 + k) - 1 exponents).
-                const uint32_t limit = max((uint32_t)(E + 7 + 15) << 10, 0x200u);  // 2^(E + 7)
-                if (__any_sync(0xffffffffu, E < 9 && (bits + (0x8000u - limit) * 0x10001u) & 0x80008000u)) {
-                    uint32_t most = 0;
 #pragma unroll
-                    for (int w = 0; w < C::kUnits; ++w)
+                for (int half = 0; half < 2; ++half)
 #pragma unroll
-                        for (int half = 0; half < 2; ++half)
-#pragma unroll
-                            for (int j = 0; j < kGroups; ++j) most = max_h2(most, s2[w][half][j]);
-                    const float2 mh = unpack_h2(most);
-                    const uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(mh.x, mh.y)));
-                    const int need = (int)(all >> 23) - 127 - 6;
-                    if (need > E) {
-                        const int to = max(-6, min(9, need));
-                        const float by = __int_as_float((127 + E - to) << 23), by_l = __int_as_float((127 + Ep - to) << 23);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) l[n][e] *= by_l, off[n][e] += (float)(to - Ep);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-#pragma unroll
-                                for (int j = 0; j < kGroups; ++j) ones[n][j][e] *= by;
-#pragma unroll
-                                for (int i = 0; i < D / 16; ++i) o[n][i][e] *= by;
-                            }
-                        }
-                        E = Ep = to;
-                    }
-                }
-                if (E == kTinyScales) {
-#pragma unroll
-                    for (int w = 0; w < C::kUnits; ++w)
-#pragma unroll
-                        for (int half = 0; half < 2; ++half)
-#pragma unroll
-                            for (int j = 0; j < kGroups; ++j) s2[w][half][j] = mul_h2(s2[w][half][j], 0x78007800u);
-                }
-
-                // the weights' logarithms; the maxima are taken again only when a weight would grow past 2^8
-                bool grow = false;
-                float lg[C::kUnits][NT][4];
-                auto logs = [&] {
-#pragma unroll
-                    for (int w = 0; w < C::kUnits; ++w)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) lg[w][n][e] = fmaf(sc[w][n][e], f[n][e & 1], -off[n][e & 1]);
-                };
-                logs();
-                const float most = 8.f - (float)Ep;
+                    for (int j = 0; j < kGroups; ++j) bits |= s2[w][half][j];
+            }
+            // A weight is 2^8 at most, so its products with scales below 2^(E + 7) fit in fp16.  The bits of all scales together are no
+            // less than the largest of them, and mostly (with exponents 0 and 1 apart) in its power of two: one test does.
+            const uint32_t limit = max((uint32_t)(E + 7 + 15) << 10, 0x200u);  // 2^(E + 7)
+            if (__any_sync(0xffffffffu, E < 9 && (bits + (0x8000u - limit) * 0x10001u) & 0x80008000u)) {
+                uint32_t most = 0;
 #pragma unroll
                 for (int w = 0; w < C::kUnits; ++w)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        grow |= fmaxf(fmax3(lg[w][n][0], lg[w][n][1], lg[w][n][2]), lg[w][n][3]) > most;
-                if (__any_sync(0xffffffffu, grow)) {
+                    for (int half = 0; half < 2; ++half)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                        for (int j = 0; j < kGroups; ++j) most = max_h2(most, s2[w][half][j]);
+                const float2 mh = unpack_h2(most);
+                const uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(mh.x, mh.y)));
+                const int need = (int)(all >> 23) - 127 - 6;
+                if (need > E) {
+                    const int to = max(-6, min(9, need));
+                    const float by = __int_as_float((127 + E - to) << 23), by_l = __int_as_float((127 + Ep - to) << 23);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float mt = -INFINITY;
+                    for (int e = 0; e < 2; ++e) l[e] *= by_l, off[e] += (float)(to - Ep);
 #pragma unroll
-                            for (int w = 0; w < C::kUnits; ++w) mt = fmax3(mt, sc[w][n][e], sc[w][n][2 + e]);
-                            mt *= f[n][e];
-                            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
-                            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
-                            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-                            mt += (float)Ep;
-                            if (mt > off[n][e] + 8.f) {
-                                const float alpha = ex2_approx(off[n][e] - mt);
-                                l[n][e] *= alpha;
+                    for (int e = 0; e < 4; ++e) {
 #pragma unroll
-                                for (int j = 0; j < kGroups; ++j) ones[n][j][e] *= alpha;
+                        for (int j = 0; j < kGroups; ++j) ones[j][e] *= by;
 #pragma unroll
-                                for (int i = 0; i < D / 16; ++i) o[n][i][e] *= alpha, o[n][i][2 + e] *= alpha;
-                                off[n][e] = mt;
-                            }
-                        }
-                    logs();
+                        for (int i = 0; i < D / 16; ++i) o[i][e] *= by;
+                    }
+                    E = Ep = to;
                 }
+            }
+            if (E == kTinyScales) {
+#pragma unroll
+                for (int w = 0; w < C::kUnits; ++w)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int j = 0; j < kGroups; ++j) s2[w][half][j] = mul_h2(s2[w][half][j], 0x78007800u);
+            }
+
+            // the weights' logarithms; the maxima are taken again only when a weight would grow past 2^8
+            bool grow = false;
+            float lg[C::kUnits][4];
+            auto logs = [&] {
+#pragma unroll
+                for (int w = 0; w < C::kUnits; ++w)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) lg[w][e] = fmaf(sc[w][e], f[e & 1], -off[e & 1]);
+            };
+            logs();
+            const float most = 8.f - (float)Ep;
+#pragma unroll
+            for (int w = 0; w < C::kUnits; ++w)
+                grow |= fmaxf(fmax3(lg[w][0], lg[w][1], lg[w][2]), lg[w][3]) > most;
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mt = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < C::kUnits; ++w) mt = fmax3(mt, sc[w][e], sc[w][2 + e]);
+                    mt *= f[e];
+                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
+                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
+                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+                    mt += (float)Ep;
+                    if (mt > off[e] + 8.f) {
+                        const float alpha = ex2_approx(off[e] - mt);
+                        l[e] *= alpha;
+#pragma unroll
+                        for (int j = 0; j < kGroups; ++j) ones[j][e] *= alpha;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) o[i][e] *= alpha, o[i][2 + e] *= alpha;
+                        off[e] = mt;
+                    }
+                }
+                logs();
+            }
 
 #pragma unroll
-                for (int w = 0; w < C::kUnits; ++w) {
-                    const int key0 = key_warp + w * kUnit;
-                    uint32_t pb[NT][2];  // P^T as the second product's operand: row g, keys 2 tq and 2 tq + 1 (+ 8)
+            for (int w = 0; w < C::kUnits; ++w) {
+                const int key0 = key_warp + w * kUnit;
+                uint32_t pb[2];  // P^T as the second product's operand: row g, keys 2 tq and 2 tq + 1 (+ 8)
+                float p[4];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float p[4];
+                for (int e = 0; e < 4; ++e) p[e] = ex2_approx(lg[w][e]);
+                // this lane's keys, not rounded; the others' are added at the end
+                l[0] += p[0] + p[2], l[1] += p[1] + p[3];
+                pb[0] = transpose8(pack_h2(p[0], p[1]));  // the weights as operands: fp16, off by 2^-11
+                pb[1] = transpose8(pack_h2(p[2], p[3]));
+                uint32_t code[2][kGroups];
+                load_codes<D>(code, vs + w * U::kBytes, lane);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) p[e] = ex2_approx(lg[w][n][e]);
-                        // this lane's keys, not rounded; the others' are added at the end
-                        l[n][0] += p[0] + p[2], l[n][1] += p[1] + p[3];
-                        pb[n][0] = transpose8(pack_h2(p[0], p[1]));  // the weights as operands: fp16, off by 2^-11
-                        pb[n][1] = transpose8(pack_h2(p[2], p[3]));
+                for (int j = 0; j < kGroups; ++j) {
+                    uint32_t x[4], y[4];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t c = code[half][j], d = c >> 8;
+                        x[2 * half] = c & 0x000f000fu, x[2 * half + 1] = c & 0x00f000f0u;
+                        y[2 * half] = d & 0x000f000fu, y[2 * half + 1] = d & 0x00f000f0u;
                     }
-                    uint32_t code[2][kGroups];
-                    load_codes<D>(code, vs + w * U::kBytes, lane);
-                    uint32_t sees[NT][2];  // row g's own keys, where a lane holds two rows
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        sees[n][0] = sees[n][1] = ~0u;
-                        if (NT > 1 && !plain) keep_seen(sees[n], seen_keys(position(8 * n + g), key0, a.window, a.sinks), tq);
-                    }
-#pragma unroll
-                    for (int j = 0; j < kGroups; ++j) {
-                        uint32_t x[4], y[4];
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const uint32_t c = code[half][j], d = c >> 8;
-                            x[2 * half] = c & 0x000f000fu, x[2 * half + 1] = c & 0x00f000f0u;
-                            y[2 * half] = d & 0x000f000fu, y[2 * half + 1] = d & 0x00f000f0u;
-                        }
-                        const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            uint32_t b0 = mul_h2(pb[n][0], s2[w][0][j]), b1 = mul_h2(pb[n][1], s2[w][1][j]);
-                            if (NT > 1) b0 &= sees[n][0], b1 &= sees[n][1];
-                            mma_f16(o[n][2 * j], x, b0, b1);
-                            mma_f16(o[n][2 * j + 1], y, b0, b1);
-                            mma_f16(ones[n][j], one, b0, b1);
-                        }
-                    }
+                    const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
+                    const uint32_t b0 = mul_h2(pb[0], s2[w][0][j]), b1 = mul_h2(pb[1], s2[w][1][j]);
+                    mma_f16(o[2 * j], x, b0, b1);
+                    mma_f16(o[2 * j + 1], y, b0, b1);
+                    mma_f16(ones[j], one, b0, b1);
                 }
-                warp_arrive(&empty[stage]);
             }
+            warp_arrive(&empty[stage]);
             if (++stage == kStages) stage = 0, phase ^= 1;
         }
 
@@ -498,36 +470,33 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
         float *buf = reinterpret_cast<float *>(smem + C::kJoinOff);
         float2 *ml = reinterpret_cast<float2 *>(smem + C::kMlOff);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
+        }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
-                l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
-                l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
-            }
+        for (int c = 0; c < D / kJoinCols; ++c) {
+            sync_warps();  // the buffer is free
+            if (c == 0 && g < 2) ml[8 * warp + 2 * tq + g] = make_float2(l[g & 1] == 0.f ? -INFINITY : off[g & 1], l[g & 1]);
 #pragma unroll
-            for (int c = 0; c < D / kJoinCols; ++c) {
-                sync_warps();  // the buffer is free
-                if (c == 0 && g < 2) ml[8 * warp + 2 * tq + g] = make_float2(l[n][g & 1] == 0.f ? -INFINITY : off[n][g & 1], l[n][g & 1]);
+            for (int i = 0; i < 4; ++i) {
+                // channel 32 j + 4 g + (0, 1 | 2, 3) at place 8 (channel % 4) + g of its group
+                const int j = 2 * c + i / 2;
+                float v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // channel 32 j + 4 g + (0, 1 | 2, 3) at place 8 (channel % 4) + g of its group
-                    const int j = 2 * c + i / 2;
-                    float v[4];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float sum = 8.f * ones[n][j][e];
-                        v[e] = fmaf(o[n][4 * c + i][e], 0x1p24f, -sum) * by;
-                        v[2 + e] = fmaf(o[n][4 * c + i][2 + e], 0x1p20f, -sum) * by;
-                    }
-                    float *to = buf + warp * (kJoinCols * 8) + (32 * (i / 2) + 16 * (i % 2) + g) * 8 + 2 * tq;
-                    *reinterpret_cast<float2 *>(to) = make_float2(v[0], v[1]);
-                    *reinterpret_cast<float2 *>(to + 64) = make_float2(v[2], v[3]);
+                for (int e = 0; e < 2; ++e) {
+                    const float sum = 8.f * ones[j][e];
+                    v[e] = fmaf(o[4 * c + i][e], 0x1p24f, -sum) * by;
+                    v[2 + e] = fmaf(o[4 * c + i][2 + e], 0x1p20f, -sum) * by;
                 }
-                sync_warps();
-                join_warps<D, 8>(a, buf, ml, whole, slot, first_row, 8 * n, a.R - row0, kJoinCols * c,
-                                 [](int ch) { return 32 * (ch / 32) + 8 * (ch % 4) + ch % 32 / 4; });
+                float *to = buf + warp * (kJoinCols * 8) + (32 * (i / 2) + 16 * (i % 2) + g) * 8 + 2 * tq;
+                *reinterpret_cast<float2 *>(to) = make_float2(v[0], v[1]);
+                *reinterpret_cast<float2 *>(to + 64) = make_float2(v[2], v[3]);
             }
+            sync_warps();
+            join_warps<D, 8>(a, buf, ml, whole, slot, first_row, 0, a.R - row0, kJoinCols * c,
+                             [](int ch) { return 32 * (ch / 32) + 8 * (ch % 4) + ch % 32 / 4; });
         }
         left = run.next(tiles.n, left, per_seq);
     }
@@ -535,45 +504,35 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) paged_decode4_ker
         a.tails[blockIdx.x] = make_int2(tail, tail < 0 ? 0 : parts_behind(a.cut, *reinterpret_cast<long long *>(smem + C::kScanOff + kAllOff), tail_rest));
 }
 
-template <int D, int NT>
+template <int D>
 cudaError_t launch_d(const PagedDecodeArgs &a, int ctas, cudaStream_t s) {
-    auto kern = paged_decode4_kernel<D, NT>;
+    auto kern = paged_decode4_kernel<D>;
     static std::atomic<unsigned long long> allowed{0};
-    const cudaError_t e = allow_smem((const void *)kern, Cfg<D, NT>::kAlloc, allowed);
+    const cudaError_t e = allow_smem((const void *)kern, Cfg<D>::kAlloc, allowed);
     if (e != cudaSuccess) return e;
-    return launch_behind(kern, dim3(ctas), kThreads, Cfg<D, NT>::kAlloc, false, 1, s, a);
+    return launch_behind(kern, dim3(ctas), kThreads, Cfg<D>::kAlloc, false, 1, s, a);
 }
 
 // An SM's CTAs that started first are served first: with equal runs three of them ended after 178, 190 and 204 us (64 sequences of
 // 16384 keys), four of D = 64 after 54, 57, 61 and 65.
 constexpr int kAhead = 65;
 
-template <int D, int NT>
+template <int D>
 PagedPlan plan_d() {
-    return PagedPlan{Cfg<D, NT>::kTile, 8 * NT, Cfg<D, NT>::kCtas, NT == 1 && D < 256 ? kAhead : 0};
+    return PagedPlan{Cfg<D>::kTile, 8, Cfg<D>::kCtas, D < 256 ? kAhead : 0};
 }
-
-// 8 rows a CTA, or 16 where there are more: twice the products for half the reads.  (Heads of 256: 8; with 16 the
-// accumulators alone would take a thread's registers.)
-bool sixteen(int R, int D) { return R > 8 && D < 256; }
 
 }  // namespace
 
-PagedPlan paged_plan4(int R, int D) {
-    const bool two = sixteen(R, D);
-    switch (D) {
-        case 64: return two ? plan_d<64, 2>() : plan_d<64, 1>();
-        case 128: return two ? plan_d<128, 2>() : plan_d<128, 1>();
-        default: return plan_d<256, 1>();
-    }
-}
+// 8 rows a CTA; more rows read the keys again.  (16 of them, with twice the accumulators, spill: 64 sequences of 8192, heads of 128
+// took 251 us against 215 for two times 8, heads of 64 127 against 137.)
+PagedPlan paged_plan4(int D) { return D == 64 ? plan_d<64>() : D == 128 ? plan_d<128>() : plan_d<256>(); }
 
 cudaError_t launch_paged_decode4(const PagedDecodeArgs &a, int ctas, cudaStream_t s) {
-    const bool two = sixteen(a.R, a.D);
     switch (a.D) {
-        case 64: return two ? launch_d<64, 2>(a, ctas, s) : launch_d<64, 1>(a, ctas, s);
-        case 128: return two ? launch_d<128, 2>(a, ctas, s) : launch_d<128, 1>(a, ctas, s);
-        case 256: return launch_d<256, 1>(a, ctas, s);
+        case 64: return launch_d<64>(a, ctas, s);
+        case 128: return launch_d<128>(a, ctas, s);
+        case 256: return launch_d<256>(a, ctas, s);
         default: return cudaErrorInvalidValue;
     }
 }

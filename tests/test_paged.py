@@ -711,8 +711,64 @@ def test_binding_refusals():
         fa.fa_paged_decode(q, pages[0], pages[1][:3], table, lens)
     with pytest.raises(ValueError):
         fa.fa_paged_decode(q, *pages, table.expand(2, -1), lens)
+    long = _ints([list(range(4)) * 50])
+    with pytest.raises(fa.FAError) as e:
+        fa.fa_paged_decode(q, *pages, long, lens, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == nat.FA_ERR_WORKSPACE
     with pytest.raises(ValueError):
         fa.fa_paged_gather(*pages, table, lens, k=k)
     with pytest.raises(fa.FAError) as e:
         fa.fa_paged_gather(*pages, table, lens, rows=0)
     assert e.value.code == nat.FA_ERR_SHAPE
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("case", [(700, 2, 1, 1, 16, 64, lambda b: b % 40), (5000, 1, 1, 1, 16, 64, lambda b: 17 * b % 50),
+                                  (3, 4, 4, 1, 64, 64, lambda b: 90000 - 40000 * b)])
+def test_decode_of_many_and_of_long_sequences(case, four):
+    """More sequences than a CTA has threads, lengths of zero among them; and lists that go over many CTAs."""
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    B, Hq, Hkv, n_q, page, D, length = case
+    lens = [length(b) for b in range(B)]
+    g = _gen(B)
+    slots = -(-max(lens) // page)
+    n_pages = sum(-(-n // page) for n in lens) + 1
+    table, pages = _tables(lens, page, slots, n_pages), _pool(g, n_pages, Hkv, page, D, four)
+    q = _randn(g, B, Hq, n_q, D)
+    ref = decode_reference(q, pages, table, lens, slots * page, 0, 0.2)
+    o, lse = fa.fa_paged_decode(q, *pages, table, _ints(lens), scale=0.2)
+    assert fa.fa_device_status() == 0
+    check(o, ref["o"], ref["o_bound"], "O")
+    check_lse(lse, ref["lse"], "LSE")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hkv,n", [(1, 1300000), (16, 82000)])
+def test_four_bit_runs_of_unequal_length(Hkv, n):
+    """So many tiles that an SM's CTAs get runs of different lengths: one list over all of them, and several each."""
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB")
+    g = _gen(43)
+    page, D = 256, 64
+    slots = -(-n // page)
+    pages = _pool(g, slots, Hkv, page, D, True)
+    table = torch.randperm(slots, generator=g, device="cuda").to(torch.int32)[None]
+    q = _randn(g, 1, 2 * Hkv, 1, D)
+    k, v = (page_values(p, D, i == 1) for i, p in enumerate(pages))
+    s = unit_values(pages[1], D, True)[1]
+    o, lse = fa.fa_paged_decode(q, *pages, table, _ints([n]), scale=0.3)
+    assert fa.fa_device_status() == 0
+    for h in range(Hkv):  # head by head: 64 bits of all of them at once are much memory
+        kb, vb, sb = (rows_of(t[:, h:h + 1], table, 0, n)[0] for t in (k, v, s))
+        score = 0.3 * q[0, 2 * h:2 * h + 2, 0].double() @ kb.T
+        L = torch.logsumexp(score, -1)
+        P = torch.exp(score - L[:, None])
+        O, A = P @ vb, P @ vb.abs()
+        # as in paged_ref: a warp adds up less than 4096 keys here, the rest are 608 partials (2^-24 of A each)
+        bound = (2.0 ** -10 + 2.0 ** -11) * A + 2.0 ** -8 * O.abs() + 2.0 ** -11 * (P @ sb)
+        check(o[0, 2 * h:2 * h + 2, 0], O, bound, f"O of head {h}")
+        check_lse(lse[0, 2 * h:2 * h + 2, 0], L, f"LSE of head {h}")

@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
         float off[2], l[2], f[2], o[D / 16][4];
         auto position = [&](int r) { return tiles.len - a.n_q + (row0 + r) % a.n_q; };  // rows past R: any; they are not stored
         uint32_t qf[D / 16][2], less[2];
-        float ones[kGroups][4];  // sum P s of a group (the same in the second two)
+        float ones[kGroups / 2][4];  // sum P s of an even group, and of the odd one behind it
         int E = kTinyScales, Ep = -7;  // powers of two of the weights times scales, and of the weights
 #pragma unroll
         for (int e = 0; e < 2; ++e) off[e] = kNone, l[e] = 0.f;
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 #pragma unroll
-        for (int j = 0; j < kGroups; ++j) ones[j][0] = ones[j][1] = ones[j][2] = ones[j][3] = 0.f;
+        for (int j = 0; j < kGroups / 2; ++j) ones[j][0] = ones[j][1] = ones[j][2] = ones[j][3] = 0.f;
         prepare_q<D>(static_cast<const __nv_bfloat16 *>(a.q) + (first_row + g) * D, row0 + g < a.R, a.scale_log2, lane, qf, less, f);
 
         for (int t = t0; t < t1; ++t) {
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
 #pragma unroll
-                        for (int j = 0; j < kGroups; ++j) ones[j][e] *= by;
+                        for (int j = 0; j < kGroups / 2; ++j) ones[j][e] *= by;
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) o[i][e] *= by;
                     }
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
                         const float alpha = ex2_approx(off[e] - mt);
                         l[e] *= alpha;
 #pragma unroll
-                        for (int j = 0; j < kGroups; ++j) ones[j][e] *= alpha;
+                        for (int j = 0; j < kGroups / 2; ++j) ones[j][e] *= alpha, ones[j][2 + e] *= alpha;
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) o[i][e] *= alpha, o[i][2 + e] *= alpha;
                         off[e] = mt;
@@ -447,11 +447,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
                         x[2 * half] = c & 0x000f000fu, x[2 * half + 1] = c & 0x00f000f0u;
                         y[2 * half] = d & 0x000f000fu, y[2 * half + 1] = d & 0x00f000f0u;
                     }
-                    const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
+                    const uint32_t u0 = j & 1 ? 0u : 0x3c003c00u, u1 = 0x3c003c00u - u0, one[4] = {u0, u1, u0, u1};  // rows 0-7, or 8-15
                     const uint32_t b0 = mul_h2(pb[0], s2[w][0][j]), b1 = mul_h2(pb[1], s2[w][1][j]);
                     mma_f16(o[2 * j], x, b0, b1);
                     mma_f16(o[2 * j + 1], y, b0, b1);
-                    mma_f16(ones[j], one, b0, b1);
+                    mma_f16(ones[j / 2], one, b0, b1);
                 }
             }
             warp_arrive(&empty[stage]);
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
                 float v[4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float sum = 8.f * ones[j][e];
+                    const float sum = 8.f * ones[j / 2][2 * (j & 1) + e];
                     v[e] = fmaf(o[4 * c + i][e], 0x1p24f, -sum) * by;
                     v[2 + e] = fmaf(o[4 * c + i][2 + e], 0x1p20f, -sum) * by;
                 }

@@ -9,7 +9,14 @@
 // FMA onto 1.5 2^23, so the product is not rounded first) and clamped to 1 .. 15.  Groups with an infinity or a NaN get a
 // NaN scale; a scale past fp16's largest stays there.
 //
-// What bounds both: HBM.
+// What bounds them.  Rows of bf16 into pages: HBM, less the start and the end of one launch: 4 x 4096 rows of 16/4 heads of 128
+// 37 us, 5.7 TB/s; 8 x 2048 rows of 32/8 heads 67 us, 6.1 TB/s; without a rotation 6.4 TB/s.  4-bit rows: the instructions of
+// rounding and packing (issue slots 70 %): 2 x 2000 rows of 32/8 heads 45 us, 4.9 TB/s.  One token: a launch and three reads that
+// wait on one another (length, page, row), 3.5 us for 64 sequences.  Gather: HBM: 4 sequences of 20000 to 32768 keys of 8 heads
+// in 4 bits 85 us, 6.5 TB/s.
+// Not kept: a lane with both halves of the pairs (nothing exchanged, fp32 pairs; 37.3 us for the 4 x 4096 rows, 6.9 instead of 5.0
+// for 16 tokens in 4 bits); 4-bit rows of several heads in turn (45.9 us for the 2 x 2000 rows with two heads, 47.9 with four);
+// 40 warps an SM with 48 registers (40 us for the 4 x 4096 rows).
 #include "fa_internal.h"
 #include "paged.cuh"
 #include "sm100_ptx.cuh"
@@ -19,7 +26,7 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;  // (append of 4 x 4096 rows, of 2 x 2000 in 4 bits: 37.0, 45.4 us; with 256 38.0, 46.7; with 64 39.3, 45.3)
 constexpr int kHeadsPerLane = 4;  // rows of one token that a lane turns with the same cosines
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -188,29 +195,42 @@ __device__ __forceinline__ void token_rows(const AppendArgs &a, int b, int i, in
     }
 }
 
+__device__ __forceinline__ uint32_t max_u2(uint32_t a, uint32_t b) {  // of pairs of 16-bit integers
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // 8 channels of a row in 4 bits: its 8 codes, the lowest channel in the lowest bits, and the scale of the 32 channels that
 // its four lanes share.
 __device__ __forceinline__ uint32_t quantise(const uint4 &y, __half *scale) {
-    uint32_t most = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t w = word_of(y, i);
-        most = max(most, max(w << 16 & 0x7fff0000u, w & 0x7fff0000u));  // magnitudes order as integers, NaN above all
-    }
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-    const bool finite = most < 0x7f800000u;
-    const __half s = finite ? __float2half_rn(fminf(__fdiv_rn(__uint_as_float(most), 7.f), 65504.f)) : __ushort_as_half(0x7fff);
+    constexpr uint32_t kAbs = 0x7fff7fffu, kMagic = 0x4B400000u;  // 1.5 2^23
+    uint32_t most = max_u2(max_u2(y.x & kAbs, y.y & kAbs), max_u2(y.z & kAbs, y.w & kAbs));  // magnitudes order as integers, NaN above all
+    most = max_u2(most, __shfl_xor_sync(0xffffffffu, most, 1));
+    most = max_u2(most, __shfl_xor_sync(0xffffffffu, most, 2));
+    most = max(most << 16, most & 0xffff0000u);
+    // a seventh, its error taken off: exact where it is a number of fp32, so ties of fp16 are ties
+    const float m = __uint_as_float(most), near = m * (1.f / 7.f), seventh = fmaf(fmaf(-7.f, near, m), 1.f / 7.f, near);
+    const __half s = most < 0x7f800000u ? __float2half_rn(fminf(seventh, 65504.f)) : __ushort_as_half(0x7fff);
     const float f = __half2float(s), inverse = f > 0.f ? __frcp_rn(f) : 0.f;  // (NaN: codes do not matter)
     *scale = s;
-    uint32_t codes = 0;
+    float v[8];
+    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float v = i & 1 ? bf_hi(word_of(y, i / 2)) : bf_lo(word_of(y, i / 2));
-        const int step = __float_as_int(__fmaf_rn(v, inverse, 12582912.f)) - 0x4B400000;  // 1.5 2^23
-        codes |= (uint32_t)(max(-7, min(7, step)) + 8) << (4 * i);
+    for (int i = 0; i < 4; ++i)
+        f2_unpack(f2_fma(f2_pack(bf_lo(w[i]), bf_hi(w[i])), f2_pack(inverse, inverse), f2_pack(12582920.f, 12582920.f)), v[2 * i], v[2 * i + 1]);
+    // a normal scale is at most 2^-11 too small, so 8 + step is in 1 .. 15
+    if ((uint32_t)__half_as_ushort(s) - 0x0400u >= 0x7bffu - 0x0400u) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], 12582913.f), 12582927.f);
     }
-    return codes;
+    uint32_t codes = 0, magic = 0;
+#pragma unroll
+    for (int i = 7; i >= 0; --i) {
+        codes = codes * 16 + __float_as_uint(v[i]);
+        magic = magic * 16 + kMagic;
+    }
+    return codes - magic;
 }
 
 // 4-bit rows of a head's keys or values: a lane holds 8 channels of an even position and of the odd one behind it, so a warp
@@ -286,7 +306,7 @@ __device__ __forceinline__ void unit_rows(const AppendArgs &a, int b, int block,
 
 // blockIdx.y: the sequence.  Along x the rows of tokens, then the 4-bit rows, a warp each.
 template <int D, bool FOUR, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 8)
     paged_append_kernel(AppendArgs a, FastDiv parts, FastDiv unit_parts, int row_tasks, int unit_tasks, int per) {
     const int task = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), b = blockIdx.y;
     if (task < row_tasks) {
@@ -305,7 +325,7 @@ cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
     constexpr int kBlock = 32 / (D / 8) * kHeadsPerLane, kWarps = kThreads / 32, kPositions = 64 / (D / 8);
     const int Hkv = a.pool.Hkv, q_blocks = (a.Hq + kBlock - 1) / kBlock;
     // A warp takes up to four blocks of q where that leaves 32 warps an SM twice over: what it does once (lengths, angles, addresses)
-    // is as much as two blocks' rotation (4 x 4096 rows, 16/4 heads: 41 us with one).
+    // is as much as two blocks' rotation (4 x 4096 rows of 16/4 heads, before other steps: 41 us with one block, 38 with two).
     const long long warps = (long long)a.B * a.n * q_blocks;
     const int per = (int)std::max(1ll, std::min<long long>(std::min(4, q_blocks), warps / (64 * kNumSms)));
     const int parts = (q_blocks + per - 1) / per + (FOUR ? 0 : (Hkv + kBlock - 1) / kBlock);
@@ -330,7 +350,8 @@ __global__ void __launch_bounds__(kThreads) paged_gather_kernel(GatherArgs a, in
     const long long task = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     if (task >= tasks) return;
     const int Hkv = a.pool.Hkv;
-    const int p0 = (int)(task % units) * kUnit, bh = (int)(task / units), which = bh % 2, h = bh / 2 % Hkv, b = bh / (2 * Hkv);
+    const unsigned bh = (unsigned)(task / units);  // (up to 2^32)
+    const int p0 = (int)(task % units) * kUnit, which = bh % 2, h = bh / 2 % Hkv, b = bh / 2 / Hkv;
     const int len = min(a.lens ? max(0, min(a.pool.capacity(), a.lens[b])) : a.pool.capacity(), a.rows);
     if (p0 >= len) return;
     const int n = min(kUnit, len - p0);

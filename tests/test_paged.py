@@ -333,6 +333,28 @@ def test_four_bit_rows_of_all_sizes():
     assert int(unit_values(pages[0], 64, False)[1].isnan().sum()) == 3 * 32
 
 
+@pytest.mark.gpu
+def test_four_bit_rows_of_every_magnitude():
+    """A group for every finite magnitude of bf16 as its largest one: scales and codes are the definition's, bit by bit."""
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    g = _gen(8)
+    most = torch.arange(0x7f80, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.bfloat16).float()
+    rows = most.repeat_interleave(32) * (2 * torch.rand(32 * len(most), generator=g, device="cuda") - 1)
+    rows = rows.view(-1, 32)
+    at, sign = (torch.randint(0, m, (len(most),), generator=g, device="cuda") for m in (32, 2))
+    rows[torch.arange(len(most), device="cuda"), at] = most * (1 - 2 * sign)
+    n = len(most) // 32  # in rows of 8 groups, 4 heads
+    k = rows.to(torch.bfloat16).view(1, 4, n, 256)
+    v = k.flip(2).contiguous()
+    pages, table = _pool(g, 4, 4, 256, 256, True), _ints([[2, 0, 3, 1]])
+    want = append_reference(None, k, v, pages, table, [n], None, None, 0, False)
+    fa.fa_paged_append(k, v, *pages, table, _ints([n]))
+    for a, b in zip(pages, want[1:]):
+        assert torch.equal(a, b)
+    assert fa.fa_device_status() == 0
+
+
 # B, Hq, Hkv, n_q, page, lens (cycled), D, window, sinks; window 0: none
 DECODES = [
     (1, 1, 1, 1, 16, (1,), 64, 0, 0), (2, 4, 4, 1, 16, (70, 3), 128, 0, 0), (3, 8, 2, 1, 32, (500, 33, 64), 128, 0, 0),

@@ -115,7 +115,8 @@ struct Turn {
             y[i] = pack_bf16x2(__fmaf_ru(e0, kSlack, v0), __fmaf_ru(e1, kSlack, v1));
             near |= y[i] ^ pack_bf16x2(__fmaf_rd(e0, -kSlack, v0), __fmaf_rd(e1, -kSlack, v1));
         }
-        if (near) {
+        // (zeros end up here, as 0 and -0; rows of padding need no more)
+        if (near && ((x.x | x.y | x.z | x.w | o.x | o.y | o.z | o.w) & 0x7fff7fffu)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) y[i] = turn_pair(word_of(x, i), word_of(o, i), c[2 * i], c[2 * i + 1], s[2 * i], s[2 * i + 1]);
         }

@@ -607,7 +607,7 @@ def fa_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_p
         Hq = q.shape[1]
         qs, q_ptr = _rows(q, "q", (B, Hq, n, D), dev), q.data_ptr()
         if q_out is None:
-            q_out = q.new_empty((B, Hq, n, D)) if stream is None else _empty(q, (B, Hq, n, D), torch.bfloat16, stream)
+            q_out = _empty(q, (B, Hq, n, D), torch.bfloat16, stream)
             out_ptr = q_out.data_ptr()
         else:
             _bf16(q_out, "q_out", (B, Hq, n, D), dev)
@@ -674,8 +674,7 @@ def fa_paged_decode(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     else:
         _bf16(o, "o", shape, dev)
     if lse is None:
-        rows = (B, Hq, n_q)
-        lse = q.new_empty(rows, dtype=torch.float32) if stream is None else _empty(q, rows, torch.float32, stream)
+        lse = _empty(q, (B, Hq, n_q), torch.float32, stream)
     else:
         _tensor(lse, "lse", torch.float32, (B, Hq, n_q), dev)
     workspace = _workspace(workspace, q, stream, dev, "fa_paged_decode_workspace_bytes", B, Hq, Hkv, n_q, D, page, slots, kind)

@@ -958,19 +958,31 @@ namespace {
 struct PagedGrid {
     PagedPlan plan;
     int row_tiles, ctas;
-    bool cut;  // whether a list can be cut
+    int cluster;  // CTAs of a list, or 0: cut into runs
+    bool cut;  // whether a run can end inside a list
     size_t partials() const { return (size_t)ctas * 2 * plan.rows; }
     size_t bytes(int D) const { return cut ? partials() * ((size_t)D * 4 + 8) + (size_t)ctas * 8 : 0; }
 };
 
-PagedGrid paged_grid(int B, int Hq, int Hkv, int n_q, int D, int capacity, bool four, int num_sms) {
-    PagedGrid g;
+// `keys`: of a sequence, at most.
+PagedGrid paged_grid(int B, int Hq, int Hkv, int n_q, int D, int page, int keys, bool four, int num_sms) {
+    PagedGrid g{};
     const int R = Hq / Hkv * n_q;
-    g.plan = four ? paged_plan4(D) : paged_plan(R, D);
+    g.plan = four ? paged_plan4(D) : paged_plan(R, D, page);
     g.row_tiles = (R + g.plan.rows - 1) / g.plan.rows;
-    const long long tiles = (capacity + g.plan.tile - 1) / g.plan.tile, lists = (long long)B * Hkv * g.row_tiles;
-    g.ctas = (int)std::min<long long>(lists * tiles, (long long)num_sms * g.plan.per_sm);
-    g.cut = tiles > 1;
+    const long long tiles = (keys + g.plan.tile - 1) / g.plan.tile, lists = (long long)B * Hkv * g.row_tiles;
+    const long long slots = (long long)num_sms * g.plan.per_sm;
+    // Few lists of few tiles: clusters.  Without the run's search and the join behind it they are faster on the device up to three
+    // tiles a CTA or, with many lists, up to all (16 sequences of 8 heads of 128, 512 keys: 9.4 us instead of 11.1, in 4 bits 9.2
+    // instead of 10.7), and the host saves a launch and the workspace, 6 us of 25 a call.  At per_cluster tiles they are
+    // 1 us behind (one sequence of 4 heads of 128, 3001 keys: 9.6 us instead of 8.9, in 4 bits 10.3 instead of 9.3).
+    for (int c = 8; c > 1 && g.cluster == 0; c /= 2) {
+        // one wave: a cluster needs c / per_sm SMs of one GPC, which leaves some of a GPC's over, up to half of them for 8
+        const long long room = c > 4 * g.plan.per_sm ? slots / 2 : slots - slots / 8;
+        if (tiles > c / 2 && lists * c <= room && tiles <= (long long)c * g.plan.per_cluster) g.cluster = c;
+    }
+    g.ctas = (int)(g.cluster > 0 ? lists * g.cluster : std::min(lists * tiles, slots));
+    g.cut = g.cluster == 0 && tiles > 1;
     return g;
 }
 
@@ -995,7 +1007,7 @@ extern "C" int fa_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q, 
     if (!bytes) return FA_ERR_NULL;
     int rc = check_paged_decode(B, Hq, Hkv, n_q, D, 1, page, slots, cache_dtype);
     if (rc != FA_OK) return rc;
-    *bytes = paged_grid(B, Hq, Hkv, n_q, D, slots * page, cache_dtype == FA_INT4, current_num_sms()).bytes(D);
+    *bytes = paged_grid(B, Hq, Hkv, n_q, D, page, slots * page, cache_dtype == FA_INT4, current_num_sms()).bytes(D);
     return FA_OK;
 }
 
@@ -1017,15 +1029,18 @@ extern "C" int fa_paged_decode(const void *q, const void *k_pages, const void *v
     rc = device_state(&dev, &st);
     if (rc != FA_OK) return rc;
     const bool four = cache_dtype == FA_INT4;
-    const PagedGrid grid = paged_grid(B, Hq, Hkv, n_q, D, slots * page, four, st->num_sms);
+    const WinArgs w = window_args(Hkv, slots * page, window, sinks);
+    const int tile = (four ? paged_plan4(D) : paged_plan(1, D, page)).tile;
+    // the sinks' tiles and those of the window, which may begin and end inside one
+    const long long seen = w.sinks + (long long)w.window + n_q + 3 * tile;
+    const PagedGrid grid = paged_grid(B, Hq, Hkv, n_q, D, page, (int)std::min<long long>(slots * page, seen), four, st->num_sms);
     if (grid.cut) {
         rc = check_ptrs({workspace});
         if (rc != FA_OK) return rc;
         if (workspace_bytes < grid.bytes(D)) return FA_ERR_WORKSPACE;
     }
-    const WinArgs w = window_args(Hkv, slots * page, window, sinks);
     PagedDecodeArgs a{q, lens, o, lse, page_pool(k_pages, v_pages, table, Hkv, n_pages, page, slots), B, Hq / Hkv * n_q, n_q, D,
-                      w.window, w.sinks, scale * log2e(), st->status_word, grid.row_tiles,
+                      w.window, w.sinks, scale * log2e(), st->status_word, grid.row_tiles, grid.cluster,
                       work_cut(grid, st->num_sms), nullptr, nullptr, nullptr};
     if (grid.cut) {
         a.part_o = static_cast<float *>(workspace);

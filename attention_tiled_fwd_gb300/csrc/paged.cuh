@@ -46,9 +46,11 @@ struct PagePool {
     int n_pages, shift, slots, Hkv;
     __host__ __device__ int capacity() const { return slots << shift; }
 #ifdef __CUDACC__
-    // The page of sequence b that holds position p, or -1 where the table has none of the pool's there.
+    // The table's entry for position p of sequence b.
+    __device__ __forceinline__ int entry(int b, int p) const { return __ldg(table + (size_t)b * slots + (p >> shift)); }
+    // The page that holds it, or -1 where the table has none of the pool's there.
     __device__ __forceinline__ int page_of(int b, int p) const {
-        const int at = __ldg(table + (size_t)b * slots + (p >> shift));
+        const int at = entry(b, p);
         return (unsigned)at < (unsigned)n_pages ? at : -1;
     }
     // First byte of row p % page of a page and head, rows of `bytes` bytes (4-bit pages: p a multiple of 16).
@@ -109,6 +111,7 @@ struct PagedDecodeArgs {
     float scale_log2;
     int *status;
     int row_tiles;     // CTAs that share a key head's rows
+    int cluster;       // 0: the work is cut into runs; else the CTAs of a cluster share a list and join its partials
     WorkCut cut;
     // two partials a CTA, [2 CTA + slot][rows of a tile]: O, (m, l); and the list that goes on behind a CTA (its number and
     // its partials, -1: none).  All null where no list can be cut.
@@ -116,13 +119,13 @@ struct PagedDecodeArgs {
     float2 *part_ml;
     int2 *tails;
 };
-// Keys of a tile, rows of a row tile, CTAs an SM holds, and how much more (1/1000) each of those gets done than the next, for a
-// decode of R rows a key head.
+// Keys of a tile, rows of a row tile, CTAs an SM holds, how much more (1/1000) each of those gets done than the next, and the most
+// tiles for a CTA of a cluster, for a decode of R rows a key head.
 struct PagedPlan {
-    int tile, rows, per_sm, ahead;
+    int tile, rows, per_sm, ahead, per_cluster;
 };
-PagedPlan paged_plan(int R, int D);   // bf16 pages
-PagedPlan paged_plan4(int D);        // 4-bit pages
+PagedPlan paged_plan(int R, int D, int page);  // bf16 pages
+PagedPlan paged_plan4(int D);                  // 4-bit pages
 // tk, tv: the pools' tensor maps (boxes of 64 columns and of the rows of a page, at most a tile's).
 cudaError_t launch_paged_decode(const PagedDecodeArgs &a, int ctas, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s);
 cudaError_t launch_paged_decode4(const PagedDecodeArgs &a, int ctas, cudaStream_t s);

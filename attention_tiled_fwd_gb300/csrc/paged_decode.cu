@@ -11,7 +11,10 @@
 //   warps 0-3  units of 16 keys each, with a softmax state of their own, joined at a list's end
 // The work is one list of tiles, sequence by sequence and head by head, cut into equal runs for a grid of one wave, however
 // long the sequences are (lengths are read on the device).  A CTA writes O and L of what it holds whole; of what it shares
-// with its neighbours it writes a partial, and paged_join_kernel adds those up.
+// with its neighbours it writes a partial, and paged_join_kernel adds those up.  Where there are few lists of few tiles (the rule
+// is paged_grid's, fa_api.cu), the CTAs of a cluster share a list instead and join its partials through distributed shared memory.
+// Measured: 64 sequences of 900 to 16384 keys of 8 heads of 128 (2.27 GB) 326 us, 6.95 TB/s, which is the rate of a copy; one
+// sequence of 3001 keys of 4 heads 9 us: the launch, the search (1 us), q (1 us), a first tile (1.5 us), the join (2.5 us).
 //
 // Keys that a row does not see may hold anything: their scores are replaced; values that no row sees are cleared before the
 // product, and those that some rows see are kept from the others where they are not finite (0 times them would be NaN).
@@ -63,7 +66,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
         }
         fence_mbarrier_init();
     }
-    Run<kListCost<D>> run = find_run<kTile, kThreads, kListCost<D>>(a, smem + C::kScanOff);  // (its barriers stand behind the set-up too)
+    // (the barriers in either stand behind the set-up too)
+    Run<kListCost<D>> run = a.cluster ? cluster_run<kTile, kListCost<D>>(a, smem + C::kScanOff) : find_run<kTile, kThreads, kListCost<D>>(a, smem + C::kScanOff);
     launch_dependents();
     const int per_seq = a.pool.Hkv * a.row_tiles;
     int stage = 0;
@@ -87,25 +91,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
             int t0, t1;
             run.part(tiles.n, left, &t0, &t1);
             const int h = run.u / a.row_tiles;
-            // the lane's page of a tile, -1 where the pool has none; -2 where none is needed
-            auto page_at = [&](int t) {
-                const int k0 = tiles.tile(t) * kTile + box * box_rows;
-                if (lane >= copies || k0 >= tiles.len || !(k0 + box_rows > tiles.lo || k0 < a.sinks)) return -2;
-                return a.pool.page_of(run.b, k0);
+            // the lane's entry of the table for a tile, if it needs one: read three tiles ahead
+            auto entry = [&](int t, int *k0) {
+                *k0 = tiles.tile(t) * kTile + box * box_rows;
+                return t < t1 && lane < copies && *k0 < tiles.len && (*k0 + box_rows > tiles.lo || *k0 < a.sinks);
             };
-            int next = t0 < t1 ? page_at(t0) : -2;
+            auto page_at = [&](int t) {
+                int k0;
+                return entry(t, &k0) ? a.pool.entry(run.b, k0) : -1;
+            };
+            int next[3] = {page_at(t0), page_at(t0 + 1), page_at(t0 + 2)};
             for (int t = t0; t < t1; ++t, ++loaded) {
-                const int page = next;
-                if (t + 1 < t1) next = page_at(t + 1);
+                const int page = next[0];
+                next[0] = next[1], next[1] = next[2], next[2] = page_at(t + 3);
                 ok = sleepy_wait(&empty[stage], phase ^ 1, a.status, kSiteEmpty);
                 if (!ok) break;
-                const uint32_t need = __ballot_sync(0xffffffffu, page != -2);
+                int k0;
+                const bool mine = entry(t, &k0);
+                const uint32_t need = __ballot_sync(0xffffffffu, mine);
                 if (lane == 0) mbar_arrive_expect_tx(&full[stage], __popc(need) * box_bytes);
                 __syncwarp();
-                if (page != -2) {
-                    if (page == -1) record_failure(a.status, kErrPage, 0);
-                    const int k0 = tiles.tile(t) * kTile + box * box_rows;
-                    const int slice = page >= 0 ? page * a.pool.Hkv + h : a.pool.n_pages * a.pool.Hkv;  // past the last: zeros
+                if (mine) {
+                    const bool there = (unsigned)page < (unsigned)a.pool.n_pages;
+                    if (!there) record_failure(a.status, kErrPage, 0);
+                    const int slice = there ? page * a.pool.Hkv + h : a.pool.n_pages * a.pool.Hkv;  // past the last: zeros
                     tma_load_3d(dst + stage * 2 * C::kHalf, value ? &tmap_v : &tmap_k, &full[stage], panel * 64,
                                 k0 & ((1 << a.pool.shift) - 1), slice);
                 }
@@ -118,6 +127,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
         for (int i = 0; i < last && ok; ++i) {
             if (--stage < 0) stage = C::kStages - 1, phase ^= 1;
             ok = sleepy_wait(&full[stage], phase, a.status, kSiteDrain);
+        }
+        if (a.cluster) {
+            cluster_sync();
+            cluster_sync();
         }
         return;
     }
@@ -277,8 +290,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
 
         // O and L of a list that this CTA holds whole, else a partial: in its first slot what began in a CTA before this one, in
         // its second what goes on behind it
-        const bool whole = t0 == 0 && t1 == tiles.n;
-        const size_t slot = ((size_t)blockIdx.x * 2 + (t0 == 0)) * kRows;
+        const bool whole = t0 == 0 && t1 == tiles.n && !a.cluster;
+        const size_t slot = a.cluster ? 0 : ((size_t)blockIdx.x * 2 + (t0 == 0)) * kRows;
+        // (a cluster's in the ring, which has no more to hold)
+        float *part_o = a.cluster ? reinterpret_cast<float *>(smem) : a.part_o;
+        float2 *part_ml = a.cluster ? reinterpret_cast<float2 *>(smem + kRows * D * 4) : a.part_ml;
         if (t0 == 0 && !whole) {
             tail = run.b * per_seq + run.u;
             tail_rest = tiles.n - t1;
@@ -305,10 +321,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
                     *reinterpret_cast<float2 *>(to + 64) = make_float2(v[2], v[3]);
                 }
                 sync_warps();
-                join_warps<D, 1>(a, buf, ml, whole, slot, first_row, 8 * n, a.R - row0, kJoinCols * c, [](int ch) { return ch; });
+                join_warps<D, 1>(a, part_o, part_ml, buf, ml, whole, slot, first_row, 8 * n, a.R - row0, kJoinCols * c, [](int ch) { return ch; });
             }
         }
         left = run.next(tiles.n, left, per_seq);
+    }
+    if (a.cluster) {
+        join_cluster<D>(a, reinterpret_cast<const float *>(smem), reinterpret_cast<const float2 *>(smem + kRows * D * 4),
+                        *reinterpret_cast<const int *>(smem + C::kScanOff), kRows);
+        return;
     }
     if (a.tails && threadIdx.x == 0)
         a.tails[blockIdx.x] = make_int2(tail, tail < 0 ? 0 : parts_behind(a.cut, *reinterpret_cast<long long *>(smem + C::kScanOff + kAllOff), tail_rest));
@@ -396,14 +417,16 @@ cudaError_t launch_d(const PagedDecodeArgs &a, int ctas, const CUtensorMap &tk, 
     static std::atomic<unsigned long long> allowed{0};
     const cudaError_t e = allow_smem((const void *)kern, Cfg<D>::kAlloc, allowed);
     if (e != cudaSuccess) return e;
-    return launch_behind(kern, dim3(ctas), kThreads, Cfg<D>::kAlloc, false, 1, s, tk, tv, a);
+    return launch_behind(kern, dim3(ctas), kThreads, Cfg<D>::kAlloc, false, std::max(1, a.cluster), s, tk, tv, a);
 }
 
 }  // namespace
 
 // 8 rows a CTA, or 16 where there are more: twice the products for half the reads.
-PagedPlan paged_plan(int R, int D) {
-    return PagedPlan{kTile, R > 8 ? 16 : 8, D == 64 ? Cfg<64>::kCtas : D == 128 ? Cfg<128>::kCtas : Cfg<256>::kCtas, 0};
+// Clusters: a tile costs them what its copies cost (25 ns each), so fewer tiles where the pages are small.
+PagedPlan paged_plan(int R, int D, int page) {
+    const int copies = 2 * (D / 64) * (kTile / std::min(page, kTile));
+    return PagedPlan{kTile, R > 8 ? 16 : 8, D == 64 ? Cfg<64>::kCtas : D == 128 ? Cfg<128>::kCtas : Cfg<256>::kCtas, 0, copies <= 8 ? 6 : 4};
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeArgs &a, int ctas, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s) {

@@ -157,8 +157,9 @@ __device__ __forceinline__ Run<COST> find_run(const PagedDecodeArgs &a, uint8_t 
 // of their sums, channel 2 i of a pair at place `at(2 i)` and 2 i + 1 `next` places behind it.  Written as O and L of the rows
 // that exist where the CTA holds the whole list (`whole`), else to the partial `slot`.  128 threads.
 template <int D, int NEXT, class At>
-__device__ __forceinline__ void join_warps(const PagedDecodeArgs &a, const float *buf, const float2 *ml, bool whole, size_t slot,
-                                           size_t first_row, int row8, int rows, int col0, At at) {
+__device__ __forceinline__ void join_warps(const PagedDecodeArgs &a, float *part_o, float2 *part_ml, const float *buf,
+                                           const float2 *ml, bool whole, size_t slot, size_t first_row, int row8, int rows,
+                                           int col0, At at) {
 #pragma unroll
     for (int k = 0; k < kJoinCols * 8 / 2 / 128; ++k) {
         const int r = threadIdx.x & 7, ch = 2 * ((threadIdx.x >> 3) + 16 * k);  // a row, a pair of channels
@@ -182,10 +183,79 @@ __device__ __forceinline__ void join_warps(const PagedDecodeArgs &a, const float
             reinterpret_cast<uint32_t *>(a.o)[((first_row + row) * D + col) / 2] = pack_bf16x2(acc.x * inv, acc.y * inv);
             if (col == 0) a.lse[first_row + row] = (M + __log2f(ls)) * 0.69314718055994531f;
         } else {
-            *reinterpret_cast<float2 *>(a.part_o + (slot + row) * D + col) = acc;
-            if (col == 0) a.part_ml[slot + row] = make_float2(M, ls);
+            *reinterpret_cast<float2 *>(part_o + (slot + row) * D + col) = acc;
+            if (col == 0) part_ml[slot + row] = make_float2(M, ls);
         }
     }
+}
+
+// A CTA's share of a list whose CTAs are a cluster.
+template <int TILE, int COST>
+__device__ __forceinline__ Run<COST> cluster_run(const PagedDecodeArgs &a, uint8_t *scratch) {
+    const int list = blockIdx.x / a.cluster, rank = blockIdx.x - list * a.cluster, per_seq = a.pool.Hkv * a.row_tiles;
+    Run<COST> r;
+    r.b = list / per_seq;
+    r.u = list - r.b * per_seq;
+    const int n = Tiles::of<TILE>(a, r.b).n, t0 = n * rank / a.cluster;
+    r.v = t0 + COST;
+    r.count = n * (rank + 1) / a.cluster - t0;
+    if (threadIdx.x == 0) *reinterpret_cast<int *>(scratch) = n;  // for join_cluster
+    __syncthreads();
+    return r;
+}
+
+// The partials of a cluster's list (each in its CTA's shared memory, the same place in all), joined by all of the CTAs, a share
+// of the rows' columns each.  128 threads.
+template <int D>
+__device__ __noinline__ void join_cluster(const PagedDecodeArgs &a, const float *part_o, const float2 *part_ml, int n, int tile_rows) {
+    const int list = blockIdx.x / a.cluster, rank = blockIdx.x - list * a.cluster;
+    const int row0 = list % a.row_tiles * tile_rows, rows = min(tile_rows, a.R - row0);
+    const size_t first_row = (size_t)(list / a.row_tiles) * a.R + row0;
+    const uint32_t at_o = smem_u32(part_o), at_ml = smem_u32(part_ml);
+    cluster_sync();
+    for (int idx = rank * 128 + threadIdx.x; idx < rows * (D / 4); idx += a.cluster * 128) {
+        const int r = idx / (D / 4), c = idx % (D / 4) * 4;
+        float M = -INFINITY, l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kBatch = 8;
+        for (int s0 = 0; s0 < a.cluster; s0 += kBatch) {
+            float2 ml[kBatch];
+            float4 v[kBatch];
+            float Mn = M;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int s = s0 + i;
+                ml[i] = make_float2(-INFINITY, 0.f);
+                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (s >= a.cluster || n * s / a.cluster == n * (s + 1) / a.cluster) continue;  // (no share: nothing written)
+                ml[i] = ld_cluster_f2(map_to_cta(at_ml + r * 8, s));
+                v[i] = ld_cluster_f4(map_to_cta(at_o + (r * D + c) * 4, s));
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) Mn = fmaxf(Mn, ml[i].x);
+            const float Mb = Mn == -INFINITY ? 0.f : Mn, f0 = ex2_approx(M - Mb);
+            l *= f0;
+            acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const float f = ex2_approx(ml[i].x - Mb);
+                l = fmaf(ml[i].y, f, l);
+                acc.x = fmaf(v[i].x, f, acc.x);
+                acc.y = fmaf(v[i].y, f, acc.y);
+                acc.z = fmaf(v[i].z, f, acc.z);
+                acc.w = fmaf(v[i].w, f, acc.w);
+            }
+            M = Mn;
+        }
+        const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+        const size_t row = first_row + r;
+        uint2 w;
+        w.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+        w.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + row * D + c) = w;
+        if (c == 0) a.lse[row] = (M + __log2f(l)) * 0.69314718055994531f;
+    }
+    cluster_sync();  // no CTA leaves while another reads its partial
 }
 
 __device__ __forceinline__ void sync_warps() { asm volatile("bar.sync 1, 128;" ::: "memory"); }

@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
         }
         fence_mbarrier_init();
     }
-    Run<kListCost<D>> run = find_run<kTile, kThreads, kListCost<D>>(a, smem + C::kScanOff);  // (its barriers stand behind the set-up too)
+    // (the barriers in either stand behind the set-up too)
+    Run<kListCost<D>> run = a.cluster ? cluster_run<kTile, kListCost<D>>(a, smem + C::kScanOff) : find_run<kTile, kThreads, kListCost<D>>(a, smem + C::kScanOff);
     launch_dependents();
     const int per_seq = a.pool.Hkv * a.row_tiles;
     int stage = 0;
@@ -214,24 +215,29 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
             int t0, t1;
             run.part(tiles.n, left, &t0, &t1);
             const uint32_t head = run.u / a.row_tiles * page_bytes;
-            // the lane's page of a tile, -1 where the pool has none; -2 where none is needed
-            auto page_at = [&](int t) {
-                const int k0 = tiles.tile(t) * kTile + row;
-                if (lane >= 2 * boxes || k0 >= tiles.len || !(k0 + box_rows > tiles.lo || k0 < a.sinks)) return -2;
-                return a.pool.page_of(run.b, k0);
+            // the lane's entry of the table for a tile, if it needs one: read three tiles ahead
+            auto entry = [&](int t, int *k0) {
+                *k0 = tiles.tile(t) * kTile + row;
+                return t < t1 && lane < 2 * boxes && *k0 < tiles.len && (*k0 + box_rows > tiles.lo || *k0 < a.sinks);
             };
-            int next = t0 < t1 ? page_at(t0) : -2;
+            auto page_at = [&](int t) {
+                int k0;
+                return entry(t, &k0) ? a.pool.entry(run.b, k0) : -1;
+            };
+            int next[3] = {page_at(t0), page_at(t0 + 1), page_at(t0 + 2)};
             for (int t = t0; t < t1; ++t, ++loaded) {
-                const int page = next, k0 = tiles.tile(t) * kTile + row;
-                if (t + 1 < t1) next = page_at(t + 1);
+                const int page = next[0];
+                next[0] = next[1], next[1] = next[2], next[2] = page_at(t + 3);
                 ok = sleepy_wait(&empty[stage], phase ^ 1, a.status, kSiteEmpty);
                 if (!ok) break;
-                const uint32_t need = __ballot_sync(0xffffffffu, page != -2);
+                int k0;
+                const bool mine = entry(t, &k0);
+                const uint32_t need = __ballot_sync(0xffffffffu, mine);
                 if (lane == 0) mbar_arrive_expect_tx(&full[stage], __popc(need) * box_bytes);
                 __syncwarp();
-                if (page != -2) {
+                if (mine) {
                     const uint8_t *from = pages + (uint32_t)page * page_stride + head + (k0 & ((1 << a.pool.shift) - 1)) * (9 * D / 16);
-                    if (page == -1) {
+                    if ((unsigned)page >= (unsigned)a.pool.n_pages) {
                         record_failure(a.status, kErrPage, 0);
                         from = reinterpret_cast<const uint8_t *>(g_zero_units);
                     }
@@ -246,6 +252,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
         for (int i = 0; i < last && ok; ++i) {
             if (--stage < 0) stage = kStages - 1, phase ^= 1;
             ok = sleepy_wait(&full[stage], phase, a.status, kSiteDrain);
+        }
+        if (a.cluster) {
+            cluster_sync();
+            cluster_sync();
         }
         return;
     }
@@ -460,8 +470,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
 
         // O and L of a list that this CTA holds whole, else a partial: in its first slot what began in a CTA before this one, in
         // its second what goes on behind it
-        const bool whole = t0 == 0 && t1 == tiles.n;
-        const size_t slot = ((size_t)blockIdx.x * 2 + (t0 == 0)) * kRows;
+        const bool whole = t0 == 0 && t1 == tiles.n && !a.cluster;
+        const size_t slot = a.cluster ? 0 : ((size_t)blockIdx.x * 2 + (t0 == 0)) * kRows;
+        // (a cluster's in the ring, which has no more to hold)
+        float *part_o = a.cluster ? reinterpret_cast<float *>(smem) : a.part_o;
+        float2 *part_ml = a.cluster ? reinterpret_cast<float2 *>(smem + kRows * D * 4) : a.part_ml;
         if (t0 == 0 && !whole) {
             tail = run.b * per_seq + run.u;
             tail_rest = tiles.n - t1;
@@ -495,10 +508,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
                 *reinterpret_cast<float2 *>(to + 64) = make_float2(v[2], v[3]);
             }
             sync_warps();
-            join_warps<D, 8>(a, buf, ml, whole, slot, first_row, 0, a.R - row0, kJoinCols * c,
+            join_warps<D, 8>(a, part_o, part_ml, buf, ml, whole, slot, first_row, 0, a.R - row0, kJoinCols * c,
                              [](int ch) { return 32 * (ch / 32) + 8 * (ch % 4) + ch % 32 / 4; });
         }
         left = run.next(tiles.n, left, per_seq);
+    }
+    if (a.cluster) {
+        join_cluster<D>(a, reinterpret_cast<const float *>(smem), reinterpret_cast<const float2 *>(smem + kRows * D * 4),
+                        *reinterpret_cast<const int *>(smem + C::kScanOff), kRows);
+        return;
     }
     if (a.tails && threadIdx.x == 0)
         a.tails[blockIdx.x] = make_int2(tail, tail < 0 ? 0 : parts_behind(a.cut, *reinterpret_cast<long long *>(smem + C::kScanOff + kAllOff), tail_rest));
@@ -510,7 +528,7 @@ cudaError_t launch_d(const PagedDecodeArgs &a, int ctas, cudaStream_t s) {
     static std::atomic<unsigned long long> allowed{0};
     const cudaError_t e = allow_smem((const void *)kern, Cfg<D>::kAlloc, allowed);
     if (e != cudaSuccess) return e;
-    return launch_behind(kern, dim3(ctas), kThreads, Cfg<D>::kAlloc, false, 1, s, a);
+    return launch_behind(kern, dim3(ctas), kThreads, Cfg<D>::kAlloc, false, std::max(1, a.cluster), s, a);
 }
 
 // An SM's CTAs that started first are served first: with equal runs three of them ended after 178, 190 and 204 us (64 sequences of
@@ -519,7 +537,7 @@ constexpr int kAhead = 65;
 
 template <int D>
 PagedPlan plan_d() {
-    return PagedPlan{Cfg<D>::kTile, 8, Cfg<D>::kCtas, D < 256 ? kAhead : 0};
+    return PagedPlan{Cfg<D>::kTile, 8, Cfg<D>::kCtas, D < 256 ? kAhead : 0, D < 256 ? 4 : 6};
 }
 
 }  // namespace

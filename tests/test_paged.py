@@ -363,19 +363,23 @@ DECODES = [
     (2, 24, 2, 2, 32, (300, 100), 256, 0, 0), (3, 4, 2, 1, 16, (900, 20, 300), 128, 100, 0), (2, 4, 1, 4, 64, (1500, 200), 64, 333, 5),
     (2, 8, 2, 3, 256, (2500, 2), 128, 130, 4), (2, 6, 3, 2, 32, (1200, 40), 256, 64, 130), (2, 2, 2, 1, 16, (3000, 600), 64, 1, 1),
     (40, 8, 4, 1, 16, (5, 300, 90, 0, 1000), 64, 0, 0), (9, 16, 2, 1, 64, (3000, 17, 800), 128, 0, 0), (1, 4, 4, 1, 64, (4096,), 256, 0, 0),
+    (1, 4, 2, 2, 16, (9000,), 64, 5000, 40), (2, 8, 2, 3, 64, (9000, 300), 128, 5000, 5), (1, 2, 1, 1, 32, (7000,), 256, 4500, 70),
+    (40, 16, 8, 1, 16, (900, 20, 300), 64, 100, 3),
 ]
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("room", [20, 8500])
 @pytest.mark.parametrize("four", [False, True])
 @pytest.mark.parametrize("case", DECODES)
-def test_decode(case, four):
+def test_decode(case, four, room):
+    """`room`: positions behind the longest sequence; lists of few tiles are shared by the CTAs of a cluster, others cut."""
     import attention_tiled_fwd_gb300 as fa
     cuda_or_skip()
     B, Hq, Hkv, n_q, page, lens, D, window, sinks = case
     g = _gen(sum(case[:5]) + D)
     lens = [lens[b % len(lens)] for b in range(B)]
-    slots = -(-max(lens) // page) + 2
+    slots = -(-(max(lens) + room) // page)
     n_pages = sum(-(-n // page) for n in lens) + 2
     table = _tables(lens, page, slots, n_pages)
     pages = _pool(g, n_pages, Hkv, page, D, four)
@@ -489,16 +493,19 @@ def test_decode_lengths_are_clamped():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("crowd", [0, 600])
 @pytest.mark.parametrize("four", [False, True])
 @pytest.mark.parametrize("D", [64, 128, 256])
-def test_a_nan_shows_where_it_is_seen_and_nowhere_else(D, four):
+def test_a_nan_shows_where_it_is_seen_and_nowhere_else(D, four, crowd):
+    """`crowd`: further sequences, so many that lists are cut into runs instead of being shared by clusters."""
     import attention_tiled_fwd_gb300 as fa
     cuda_or_skip()
     g = _gen(25)
     pages = _pool(g, 40, 1, 16, D, four)
-    table = _ints([list(range(20)), list(range(20, 40))])
-    q = _randn(g, 2, 2, 4, D)
-    base = fa.fa_paged_decode(q, *pages, table, _ints([300, 300]), window=50, sinks=3)
+    table = _ints([list(range(20))] + [list(range(20, 40))] * (1 + crowd))
+    q = _randn(g, 2 + crowd, 2, 4, D)
+    lens = _ints([300] * (2 + crowd))
+    base = fa.fa_paged_decode(q, *pages, table, lens, window=50, sinks=3)
     for which in (0, 1):
         for j in (1, 3, 200, 246, 247, 249, 250, 298, 299):
             bad = [t.clone() for t in pages]
@@ -508,13 +515,13 @@ def test_a_nan_shows_where_it_is_seen_and_nowhere_else(D, four):
                 bad[which].view(40, 1, 1, 9 * D)[page, 0, 0, 8 * D:].view(torch.float16)[at] = math.nan
             else:
                 bad[which][page, 0, p, 5] = math.nan
-            o, lse = fa.fa_paged_decode(q, *bad, table, _ints([300, 300]), window=50, sinks=3)
+            o, lse = fa.fa_paged_decode(q, *bad, table, lens, window=50, sinks=3)
             for i in range(4):
                 seen = j <= 296 + i and (j < 3 or j > 246 + i)
                 assert bool(o[0, :, i].isnan().any()) == seen, (which, j, i)
                 if not seen:
                     assert torch.equal(o[0, :, i], base[0][0, :, i]) and torch.equal(lse[0, :, i], base[1][0, :, i])
-            assert torch.equal(o[1], base[0][1])
+            assert torch.equal(o[1:], base[0][1:])
 
 
 @pytest.mark.gpu

@@ -10,7 +10,8 @@ back to PyTorch or the CPU.
 Layout: q, k, v, o, dO, dq, dk, dv are ``[B, H, N, D]`` contiguous CUDA
 tensors; lse and delta are ``[B, H, N]`` float32.  The windowed and
 shared-prefix calls take grouped heads: q, o, dO, dq with Hq heads, k, v, dk,
-dv with Hkv heads, Hq a multiple of Hkv.
+dv with Hkv heads, Hq a multiple of Hkv.  The paged calls read and write
+``[n_pages, Hkv, page, D]`` pages through a table, in bf16 or in 4 bits.
 """
 from __future__ import annotations
 

@@ -10,13 +10,13 @@
 // NaN scale; a scale past fp16's largest stays there.
 //
 // What bounds them.  Rows of bf16 into pages: HBM, less the start and the end of one launch: 4 x 4096 rows of 16/4 heads of 128
-// 37 us, 5.7 TB/s; 8 x 2048 rows of 32/8 heads 67 us, 6.1 TB/s; without a rotation 6.4 TB/s.  4-bit rows: the instructions of
-// rounding and packing (issue slots 70 %): 2 x 2000 rows of 32/8 heads 45 us, 4.9 TB/s.  One token: a launch and three reads that
-// wait on one another (length, page, row), 3.5 us for 64 sequences.  Gather: HBM: 4 sequences of 20000 to 32768 keys of 8 heads
-// in 4 bits 85 us, 6.5 TB/s.
-// Not kept: a lane with both halves of the pairs (nothing exchanged, fp32 pairs; 37.3 us for the 4 x 4096 rows, 6.9 instead of 5.0
-// for 16 tokens in 4 bits); 4-bit rows of several heads in turn (45.9 us for the 2 x 2000 rows with two heads, 47.9 with four);
-// 40 warps an SM with 48 registers (40 us for the 4 x 4096 rows).
+// 36 us, 5.8 TB/s; 8 x 2048 rows of 32/8 heads 67 us, 6.1 TB/s; without a rotation 6.4 TB/s.  4-bit rows: the instructions of
+// rounding and packing (issue slots 72 %): the 4 x 4096 rows 38 us, 4.7 TB/s.  One token: a launch and three reads that wait on one
+// another (length, page, row), 3.4 us for 64 sequences.  Gather: HBM: 4 sequences of 20000 to 32768 keys of 8 heads in 4 bits
+// 85 us, 6.5 TB/s.
+// Not kept (append of 2 x 2000 rows of 32/8 heads in 4 bits and a gather of 2 x 9000 to 16384 take 45.4 us): a lane with both halves
+// of the pairs (nothing exchanged, fp32 pairs; 46.8 us); 4-bit rows of several heads in turn (45.9 us with two, 47.9 with four);
+// 40 warps an SM with 48 registers (45.9 us, and 40 us for the 4 x 4096 rows of bf16).
 #include "fa_internal.h"
 #include "paged.cuh"
 #include "sm100_ptx.cuh"
@@ -26,7 +26,7 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 128;  // (append of 4 x 4096 rows, of 2 x 2000 in 4 bits: 37.0, 45.4 us; with 256 38.0, 46.7; with 64 39.3, 45.3)
+constexpr int kThreads = 128;  // (append of 4 x 4096 rows, of 2 x 2000 in 4 bits with its gather: 37.0, 45.4 us; with 256 38.0, 46.7)
 constexpr int kHeadsPerLane = 4;  // rows of one token that a lane turns with the same cosines
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }

@@ -44,8 +44,9 @@ struct Cfg {
     static constexpr int kAlloc = kScanOff + kScan + 1024;
 };
 
+// What a list costs besides its tiles, in tiles (q, the join, the stores).
 template <int D>
-constexpr int kListCost = D == 64 ? 2 : 1;  // in tiles
+constexpr int kListCost = D == 64 ? 2 : 1;
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)

@@ -352,7 +352,7 @@ FA_API int fa_prefix_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q, int
  *   FA_INT4: of 32 channels of the bf16 row y, scale = fp16(max |y| / 7) (65504 at most; NaN where y is not finite),
  *   code = 8 + y fp32(1 / scale) rounded to even, in 1 .. 15.
  * Positions that are not new keep what their pages hold, in the same unit too.  A page that takes rows belongs to one
- * sequence, and no position is given twice.  One kernel.
+ * sequence, no position is given twice, and k_pages and v_pages are two buffers.  One kernel.
  */
 FA_API int fa_paged_append(const void *q, const void *k, const void *v, const long long *strides, const float *cos,
                            const float *sin, const int *table, const int *lens, const int *counts, void *q_out,
@@ -366,7 +366,8 @@ FA_API int fa_paged_append(const void *q, const void *k, const void *v, const lo
  * taken as the nearer end, NULL: capacity.  Rows that see nothing get O = 0 and LSE = -inf.  Rows from lens[b] on, and
  * those between the sinks and the first window, may hold anything, and pages of theirs alone need no entry.
  *   workspace: fa_paged_decode_workspace_bytes(...) bytes, 16-byte aligned (NULL when that is 0; never more than 16 MB);
- *   two calls that run concurrently must not share it.
+ *   two calls that run concurrently must not share it.  Sums are taken in an order that the sizes, window and sinks decide: equal
+ *   calls give equal bits.
  */
 FA_API int fa_paged_decode(const void *q, const void *k_pages, const void *v_pages, const int *table, const int *lens,
                            void *o, float *lse, int B, int Hq, int Hkv, int n_q, int D, int n_pages, int page, int slots,

@@ -657,6 +657,46 @@ def test_two_streams_and_a_stream_that_is_not_the_current_one():
 
 
 @pytest.mark.gpu
+def test_two_host_threads():
+    """Two threads, each with its stream and its sequences, step at the same time: what one of them alone does."""
+    import threading
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    cos, sin = fa.rotation_table(4096, 128)
+
+    def start(seed):
+        g = _gen(seed)
+        pages = _pool(g, 130, 2, 64, 128, seed % 2 == 1)
+        table = _tables([4096, 4096], 64, 64, 130)
+        return pages, table, _ints([100, 4000 - seed]), [_randn(g, 2, h, 1, 128) for h in (8, 2, 2)]
+
+    def steps(state, out):
+        pages, table, lens, (q, k, v) = state
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(40):
+                qr = fa.fa_paged_append(k, v, *pages, table, lens, q=q, cos=cos, sin=sin)
+                out.append((qr, *fa.fa_paged_decode(qr, *pages, table, lens)))
+                lens += 1
+            torch.cuda.current_stream().synchronize()
+
+    alone, together = [[], []], [[], []]
+    states = [start(i) for i in (0, 1, 0, 1)]
+    torch.cuda.synchronize()
+    for i in range(2):
+        steps(states[2 + i], alone[i])
+    threads = [threading.Thread(target=steps, args=(states[i], together[i])) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(alone, together):
+        assert len(a) == len(b) == 40
+        for x, y in zip(a, b):
+            assert all(torch.equal(m, n) for m, n in zip(x, y))
+    assert fa.fa_device_status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("four", [False, True])
 def test_pools_beyond_32_bit_offsets(four):
     import attention_tiled_fwd_gb300 as fa

@@ -277,9 +277,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
         }
         const int h = run.u / a.row_tiles, row0 = run.u % a.row_tiles * kRows;
         const size_t first_row = ((size_t)run.b * a.pool.Hkv + h) * a.R + row0;
-        // tiles whose every key exists and is in every row's window
+        // spans of keys (D = 128: a warp's of a tile; else tiles: for D = 64 and 256 a warp's spans measured 2 and 3 % slower) all of which exist
+        // and are in every row's window
+        constexpr int kSpans = D == 128 ? kWarps : 1, kSpan = kTile / kSpans;
         const int p_first = max(0, tiles.len - a.n_q), past = tiles.len - 1 - a.window;
-        const int plain0 = past < 0 ? 0 : past / kTile + 1, plain1 = (p_first + 1) / kTile;
+        const int plain0 = past < 0 ? 0 : past / kSpan + 1, plain1 = (p_first + 1) / kSpan;
 
         // off: the running maximum (log2 units), plus the weights' power of two; kNone while a row has seen nothing
         float off[2], l[2], f[2], o[D / 16][4];
@@ -299,7 +301,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
 
         for (int t = t0; t < t1; ++t) {
             const int tile = tiles.tile(t), key_warp = tile * kTile + warp * (C::kUnits * kUnit);
-            const bool plain = tile >= plain0 && tile < plain1;
+            const int span = kSpans == 1 ? tile : tile * kSpans + warp;
+            const bool plain = span >= plain0 && span < plain1;
             const uint32_t ks = smem_u32(smem) + stage * 2 * C::kHalf + warp * (C::kUnits * U::kBytes), vs = ks + C::kHalf;
             float sc[C::kUnits][4];  // S^T of the warp's units: keys g and g + 8, rows 2 tq and 2 tq + 1
             if (ok) ok = sleepy_wait(&full[stage], phase, a.status, kSiteFull);  // (after a time-out: on whatever is there)

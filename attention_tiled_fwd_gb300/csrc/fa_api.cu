@@ -973,7 +973,7 @@ PagedGrid paged_grid(int B, int Hq, int Hkv, int n_q, int D, int page, int keys,
     const long long tiles = (keys + g.plan.tile - 1) / g.plan.tile, lists = (long long)B * Hkv * g.row_tiles;
     const long long slots = (long long)num_sms * g.plan.per_sm;
     // Few lists of few tiles: clusters.  Without the run's search and the join behind it they are faster on the device up to three
-    // tiles a CTA or, with many lists, up to all (16 sequences of 8 heads of 128, 512 keys: 9.4 us instead of 11.1, in 4 bits 9.2
+    // tiles a CTA or, with many lists, up to all (16 sequences of 8 heads of 128, 512 keys: 8.8 us instead of 11.1, in 4 bits 9.2
     // instead of 10.7), and the host saves a launch and the workspace, 6 us of 25 a call.  At per_cluster tiles they are
     // 1 us behind (one sequence of 4 heads of 128, 3001 keys: 9.6 us instead of 8.9, in 4 bits 10.3 instead of 9.3).
     for (int c = 8; c > 1 && g.cluster == 0; c /= 2) {

@@ -7,14 +7,17 @@
 // What bounds it: HBM.  Every cached row is read once for up to 8 NT of the R rows.  The products run transposed on
 // 16 x 8 x 16 mma.sync, S^T = K q^T and O^T = V^T P^T, with 16 keys (or channels) as the tall side: 8 rows cost one
 // instruction where rows as the tall side would leave half of it empty.  tcgen05 would need 128 of them.
-//   warp 4     producer: 64-key tiles of keys and values into a ring, a TMA box for every page and 64 columns
+//   warp 4     producer: 64-key tiles of keys and values into a ring, a TMA box for every page and 64 columns; above D = 64 keys
+//   (warp 5)   alone, and warp 5 values: a warp's copies go out 25 ns apart, 16 or 32 of them a tile where pages are small (one
+//              sequence of 3001 keys in pages of 16, D = 128, a cluster: 11.4 us with one producer, 9.9 with two)
 //   warps 0-3  units of 16 keys each, with a softmax state of their own, joined at a list's end
 // The work is one list of tiles, sequence by sequence and head by head, cut into equal runs for a grid of one wave, however
 // long the sequences are (lengths are read on the device).  A CTA writes O and L of what it holds whole; of what it shares
 // with its neighbours it writes a partial, and paged_join_kernel adds those up.  Where there are few lists of few tiles (the rule
 // is paged_grid's, fa_api.cu), the CTAs of a cluster share a list instead and join its partials through distributed shared memory.
 // Measured: 64 sequences of 900 to 16384 keys of 8 heads of 128 (2.27 GB) 326 us, 6.95 TB/s, which is the rate of a copy; one
-// sequence of 3001 keys of 4 heads 9 us: the launch, the search (1 us), q (1 us), a first tile (1.5 us), the join (2.5 us).
+// sequence of 3001 keys of 4 heads 9.6 us as a cluster; cut into runs 8.9: the launch, the search (1 us), q (1 us), a first tile
+// (1.5 us), the join (2.5 us).
 //
 // Keys that a row does not see may hold anything: their scores are replaced; values that no row sees are cleared before the
 // product, and those that some rows see are kept from the others where they are not finite (0 times them would be NaN).
@@ -27,13 +30,14 @@ namespace fa {
 namespace {
 
 constexpr int kWarps = kDecodeWarps;
-constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kTile = kUnit * kWarps;  // keys
 
 enum : int { kSiteEmpty = 301, kSiteFull, kSiteDrain };
 
 template <int D>
 struct Cfg {
+    static constexpr int kProducers = D == 64 ? 1 : 2;  // warps that load; two: one for keys, one for values
+    static constexpr int kThreads = 32 * (kWarps + kProducers);
     static constexpr int kHalf = kTile * 2 * D;                // bytes of the tile's keys, or of its values
     static constexpr int kStages = D == 64 ? 4 : 3;
     static constexpr int kCtas = D == 64 ? 3 : D == 128 ? 2 : 1;  // an SM
@@ -49,7 +53,7 @@ template <int D>
 constexpr int kListCost = D == 64 ? 2 : 1;
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
+__global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                         PagedDecodeArgs a) {
     using C = Cfg<D>;
@@ -62,25 +66,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], C::kProducers);
             mbar_init(&empty[s], kWarps);
         }
         fence_mbarrier_init();
     }
     // (the barriers in either stand behind the set-up too)
-    Run<kListCost<D>> run = a.cluster ? cluster_run<kTile, kListCost<D>>(a, smem + C::kScanOff) : find_run<kTile, kThreads, kListCost<D>>(a, smem + C::kScanOff);
+    Run<kListCost<D>> run = a.cluster ? cluster_run<kTile, kListCost<D>>(a, smem + C::kScanOff) : find_run<kTile, C::kThreads, kListCost<D>>(a, smem + C::kScanOff);
     launch_dependents();
     const int per_seq = a.pool.Hkv * a.row_tiles;
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
 
-    if (warp == kWarps) {
-        // a box: 64 columns of the rows of a tile that a page holds
-        const int box_rows = min(1 << a.pool.shift, kTile), boxes = kTile / box_rows, copies = 2 * boxes * kPanels;
+    if (warp >= kWarps) {
+        // a box: 64 columns of the rows of a tile that a page holds; `half`: the boxes of a tile's keys, or of its values
+        const int box_rows = min(1 << a.pool.shift, kTile), boxes = kTile / box_rows, half = boxes * kPanels;
         const uint32_t box_bytes = box_rows * 128;
-        const bool value = lane >= copies / 2;
-        const int box = lane % (copies / 2) / kPanels, panel = lane % kPanels;
+        const bool value = C::kProducers == 2 ? warp > kWarps : lane >= half;
+        const int box = lane % half / kPanels, panel = lane % kPanels;
         uint8_t *dst = smem + (value ? C::kHalf : 0) + panel * (kTile * 128) + box * box_rows * 128;
         if (lane == 0) {
             tma_prefetch_desc(&tmap_k);
@@ -95,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
             // the lane's entry of the table for a tile, if it needs one: read three tiles ahead
             auto entry = [&](int t, int *k0) {
                 *k0 = tiles.tile(t) * kTile + box * box_rows;
-                return t < t1 && lane < copies && *k0 < tiles.len && (*k0 + box_rows > tiles.lo || *k0 < a.sinks);
+                return t < t1 && lane < half * (3 - C::kProducers) && *k0 < tiles.len && (*k0 + box_rows > tiles.lo || *k0 < a.sinks);
             };
             auto page_at = [&](int t) {
                 int k0;
@@ -418,16 +422,20 @@ cudaError_t launch_d(const PagedDecodeArgs &a, int ctas, const CUtensorMap &tk, 
     static std::atomic<unsigned long long> allowed{0};
     const cudaError_t e = allow_smem((const void *)kern, Cfg<D>::kAlloc, allowed);
     if (e != cudaSuccess) return e;
-    return launch_behind(kern, dim3(ctas), kThreads, Cfg<D>::kAlloc, false, std::max(1, a.cluster), s, tk, tv, a);
+    return launch_behind(kern, dim3(ctas), Cfg<D>::kThreads, Cfg<D>::kAlloc, false, std::max(1, a.cluster), s, tk, tv, a);
 }
 
 }  // namespace
 
 // 8 rows a CTA, or 16 where there are more: twice the products for half the reads.
-// Clusters: a tile costs them what its copies cost (25 ns each), so fewer tiles where the pages are small.
+// Clusters: a tile costs them what a warp's copies cost (25 ns each), so fewer tiles where the pages are small.
+template <int D>
+PagedPlan plan_d(int R, int page) {
+    const int copies = 2 * (D / 64) * (kTile / std::min(page, kTile)) / Cfg<D>::kProducers;
+    return PagedPlan{kTile, R > 8 ? 16 : 8, Cfg<D>::kCtas, 0, copies <= 8 ? 6 : 4};
+}
 PagedPlan paged_plan(int R, int D, int page) {
-    const int copies = 2 * (D / 64) * (kTile / std::min(page, kTile));
-    return PagedPlan{kTile, R > 8 ? 16 : 8, D == 64 ? Cfg<64>::kCtas : D == 128 ? Cfg<128>::kCtas : Cfg<256>::kCtas, 0, copies <= 8 ? 6 : 4};
+    return D == 64 ? plan_d<64>(R, page) : D == 128 ? plan_d<128>(R, page) : plan_d<256>(R, page);
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeArgs &a, int ctas, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s) {

@@ -365,6 +365,8 @@ DECODES = [
     (40, 8, 4, 1, 16, (5, 300, 90, 0, 1000), 64, 0, 0), (9, 16, 2, 1, 64, (3000, 17, 800), 128, 0, 0), (1, 4, 4, 1, 64, (4096,), 256, 0, 0),
     (1, 4, 2, 2, 16, (9000,), 64, 5000, 40), (2, 8, 2, 3, 64, (9000, 300), 128, 5000, 5), (1, 2, 1, 1, 32, (7000,), 256, 4500, 70),
     (40, 16, 8, 1, 16, (900, 20, 300), 64, 100, 3),
+    # clusters of four and of two
+    (20, 8, 4, 1, 16, (300, 90, 0, 200), 64, 0, 0), (60, 4, 2, 1, 32, (500, 1, 130), 128, 0, 0), (8, 8, 8, 2, 16, (150, 40), 256, 0, 0),
 ]
 
 

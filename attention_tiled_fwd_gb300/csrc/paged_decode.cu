@@ -314,6 +314,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
                 l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
                 l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
             }
+            JoinedRow joined;
 #pragma unroll
             for (int c = 0; c < D / kJoinCols; ++c) {
                 sync_warps();  // the buffer is free
@@ -326,7 +327,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
                     *reinterpret_cast<float2 *>(to + 64) = make_float2(v[2], v[3]);
                 }
                 sync_warps();
-                join_warps<D, 1>(a, part_o, part_ml, buf, ml, whole, slot, first_row, 8 * n, a.R - row0, kJoinCols * c, [](int ch) { return ch; });
+                if (c == 0) joined.read(ml);
+                join_warps<D, 1>(a, part_o, part_ml, buf, joined, whole, slot, first_row, 8 * n, a.R - row0, kJoinCols * c, [](int ch) { return ch; });
             }
         }
         left = run.next(tiles.n, left, per_seq);

@@ -153,38 +153,48 @@ __device__ __forceinline__ Run<COST> find_run(const PagedDecodeArgs &a, uint8_t 
     return r;
 }
 
-// The four warps' states of 8 rows, joined: ml [warp][8 rows] their maxima and sums, buf [warp][64 places][8 rows] 64 channels
-// of their sums, channel 2 i of a pair at place `at(2 i)` and 2 i + 1 `next` places behind it.  Written as O and L of the rows
-// that exist where the CTA holds the whole list (`whole`), else to the partial `slot`.  128 threads.
-template <int D, int NEXT, class At>
-__device__ __forceinline__ void join_warps(const PagedDecodeArgs &a, float *part_o, float2 *part_ml, const float *buf,
-                                           const float2 *ml, bool whole, size_t slot, size_t first_row, int row8, int rows,
-                                           int col0, At at) {
+// The four warps' states of 8 rows, joined: ml [warp][8 rows] their maxima and sums.  Row threadIdx.x % 8: the factors of the
+// warps' sums, the joined maximum and sum.
+struct JoinedRow {
+    float f[kDecodeWarps], M, l;
+    __device__ __forceinline__ void read(const float2 *ml) {
+        const float2 *row = ml + (threadIdx.x & 7);
+        M = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int k = 0; k < kJoinCols * 8 / 2 / 128; ++k) {
-        const int r = threadIdx.x & 7, ch = 2 * ((threadIdx.x >> 3) + 16 * k);  // a row, a pair of channels
-        const int place = at(ch);
-        float M = -INFINITY, ls = 0.f;
-        float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kDecodeWarps; ++w) M = fmaxf(M, ml[8 * w + r].x);
+        for (int w = 0; w < kDecodeWarps; ++w) M = fmaxf(M, row[8 * w].x);
         const float Mb = M == -INFINITY ? 0.f : M;
 #pragma unroll
         for (int w = 0; w < kDecodeWarps; ++w) {
-            const float fw = ex2_approx(ml[8 * w + r].x - Mb);
-            ls = fmaf(ml[8 * w + r].y, fw, ls);
-            acc.x = fmaf(buf[w * (kJoinCols * 8) + place * 8 + r], fw, acc.x);
-            acc.y = fmaf(buf[w * (kJoinCols * 8) + (place + NEXT) * 8 + r], fw, acc.y);
+            f[w] = ex2_approx(row[8 * w].x - Mb);
+            l = fmaf(row[8 * w].y, f[w], l);
         }
-        const int row = row8 + r, col = col0 + ch;
-        if (row >= rows) continue;
+    }
+};
+
+// buf [warp][64 places][8 rows]: 64 channels of the warps' sums, channel 2 i of a pair at place `at(2 i)` and 2 i + 1 `next` places
+// behind it.  Written as O and L of the rows that exist where the CTA holds the whole list (`whole`), else to the partial `slot`.
+// 128 threads.
+template <int D, int NEXT, class At>
+__device__ __forceinline__ void join_warps(const PagedDecodeArgs &a, float *part_o, float2 *part_ml, const float *buf, const JoinedRow &j,
+                                           bool whole, size_t slot, size_t first_row, int row8, int rows, int col0, At at) {
+    const int r = threadIdx.x & 7, row = row8 + r;
+    if (row >= rows) return;
+    const float inv = !whole ? 1.f : j.l > 0.f ? 1.f / j.l : j.l == 0.f ? 0.f : j.l;
+#pragma unroll
+    for (int k = 0; k < kJoinCols * 8 / 2 / 128; ++k) {
+        const int ch = 2 * ((threadIdx.x >> 3) + 16 * k), place = at(ch), col = col0 + ch;  // a pair of channels
+        float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kDecodeWarps; ++w) {
+            acc.x = fmaf(buf[w * (kJoinCols * 8) + place * 8 + r], j.f[w], acc.x);
+            acc.y = fmaf(buf[w * (kJoinCols * 8) + (place + NEXT) * 8 + r], j.f[w], acc.y);
+        }
         if (whole) {
-            const float inv = ls > 0.f ? 1.f / ls : ls == 0.f ? 0.f : ls;
             reinterpret_cast<uint32_t *>(a.o)[((first_row + row) * D + col) / 2] = pack_bf16x2(acc.x * inv, acc.y * inv);
-            if (col == 0) a.lse[first_row + row] = (M + __log2f(ls)) * 0.69314718055994531f;
+            if (col == 0) a.lse[first_row + row] = (j.M + __log2f(j.l)) * 0.69314718055994531f;
         } else {
             *reinterpret_cast<float2 *>(part_o + (slot + row) * D + col) = acc;
-            if (col == 0) part_ml[slot + row] = make_float2(M, ls);
+            if (col == 0) part_ml[slot + row] = make_float2(j.M, j.l);
         }
     }
 }

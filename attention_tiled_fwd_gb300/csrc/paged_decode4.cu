@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
             tail = run.b * per_seq + run.u;
             tail_rest = tiles.n - t1;
         }
-        const float by = E == kTinyScales ? 0x1p-15f : 1.f;  // the scales' own power of two
+        const float by = E == kTinyScales ? 0x1p-15f : 1.f, by8 = -8.f * by, by20 = 0x1p20f * by, by24 = 0x1p24f * by;  // (the scales' own power of two)
         float *buf = reinterpret_cast<float *>(smem + C::kJoinOff);
         float2 *ml = reinterpret_cast<float2 *>(smem + C::kMlOff);
 #pragma unroll
@@ -496,6 +496,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
         }
+        JoinedRow joined;
 #pragma unroll
         for (int c = 0; c < D / kJoinCols; ++c) {
             sync_warps();  // the buffer is free
@@ -507,16 +508,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
                 float v[4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float sum = 8.f * ones[j / 2][2 * (j & 1) + e];
-                    v[e] = fmaf(o[4 * c + i][e], 0x1p24f, -sum) * by;
-                    v[2 + e] = fmaf(o[4 * c + i][2 + e], 0x1p20f, -sum) * by;
+                    const float less8 = by8 * ones[j / 2][2 * (j & 1) + e];
+                    v[e] = fmaf(o[4 * c + i][e], by24, less8);
+                    v[2 + e] = fmaf(o[4 * c + i][2 + e], by20, less8);
                 }
                 float *to = buf + warp * (kJoinCols * 8) + (32 * (i / 2) + 16 * (i % 2) + g) * 8 + 2 * tq;
                 *reinterpret_cast<float2 *>(to) = make_float2(v[0], v[1]);
                 *reinterpret_cast<float2 *>(to + 64) = make_float2(v[2], v[3]);
             }
             sync_warps();
-            join_warps<D, 8>(a, part_o, part_ml, buf, ml, whole, slot, first_row, 0, a.R - row0, kJoinCols * c,
+            if (c == 0) joined.read(ml);
+            join_warps<D, 8>(a, part_o, part_ml, buf, joined, whole, slot, first_row, 0, a.R - row0, kJoinCols * c,
                              [](int ch) { return 32 * (ch / 32) + 8 * (ch % 4) + ch % 32 / 4; });
         }
         left = run.next(tiles.n, left, per_seq);

@@ -986,20 +986,6 @@ PagedGrid paged_grid(int B, int Hq, int Hkv, int n_q, int D, int page, int keys,
     return g;
 }
 
-// Equal runs; on a full grid the CTAs that an SM got first have longer ones, as the plan says.
-WorkCut work_cut(const PagedGrid &g, int num_sms) {
-    WorkCut c{};
-    const int m = g.ctas == num_sms * g.plan.per_sm && g.plan.per_sm <= 4 ? g.plan.per_sm : 1;
-    c.per = g.ctas / m;
-    double at = 0;
-    for (int k = 0; k < m; ++k) {
-        const double share = (1 + g.plan.ahead * 1e-3 * (m - 1 - 2 * k) / 2) / m;
-        c.start[k] = (unsigned long long)(at * 0x1p64);
-        c.step[k] = g.ctas > 1 ? (unsigned long long)(share / c.per * 0x1p64) : 0;  // (one CTA begins at 0)
-        at += share;
-    }
-    return c;
-}
 }  // namespace
 
 extern "C" int fa_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q, int D, int page, int slots, int cache_dtype,
@@ -1041,7 +1027,7 @@ extern "C" int fa_paged_decode(const void *q, const void *k_pages, const void *v
     }
     PagedDecodeArgs a{q, lens, o, lse, page_pool(k_pages, v_pages, table, Hkv, n_pages, page, slots), B, Hq / Hkv * n_q, n_q, D,
                       w.window, w.sinks, scale * log2e(), st->status_word, grid.row_tiles, grid.cluster,
-                      work_cut(grid, st->num_sms), nullptr, nullptr, nullptr};
+                      WorkCut{grid.ctas > 1 ? ~0ull / grid.ctas : 0}, nullptr, nullptr, nullptr};
     if (grid.cut) {
         a.part_o = static_cast<float *>(workspace);
         a.part_ml = reinterpret_cast<float2 *>(a.part_o + grid.partials() * D);

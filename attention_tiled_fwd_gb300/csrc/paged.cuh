@@ -84,18 +84,15 @@ struct GatherArgs {
 };
 cudaError_t launch_paged_gather(const GatherArgs &a, bool four, cudaStream_t s);
 
-// The cut of a list of work among a grid of CTAs, `per` of them (an SM's first, second, ... CTA each) in each of up to four
-// slots: CTA i of slot k begins at start[k] + i step[k], in 2^-64 of all.  A little work is cut into whole equal runs instead, so
-// that no CTA between two that work has none.
+// The cut of a list of work into equal runs for the CTAs of a grid, `step` of 2^64 each.  A little work is cut into whole equal runs
+// instead, so that no CTA between two that work has none.
 struct WorkCut {
-    int per;
-    unsigned long long start[4], step[4];
+    unsigned long long step;
 #ifdef __CUDACC__
     __device__ __forceinline__ long long begin(unsigned cta, long long total) const {
         if (cta >= gridDim.x) return total;
         if (total < 16ll * gridDim.x) return min(total, (long long)(((unsigned)total + gridDim.x - 1) / gridDim.x) * cta);
-        const int k = cta / per;
-        return (long long)__umul64hi((unsigned long long)total, start[k] + (cta - k * per) * step[k]);
+        return (long long)__umul64hi((unsigned long long)total, cta * step);
     }
 #endif
 };
@@ -119,10 +116,9 @@ struct PagedDecodeArgs {
     float2 *part_ml;
     int2 *tails;
 };
-// Keys of a tile, rows of a row tile, CTAs an SM holds, how much more (1/1000) each of those gets done than the next, and the most
-// tiles for a CTA of a cluster, for a decode of R rows a key head.
+// Keys of a tile, rows of a row tile, CTAs an SM holds, and the most tiles for a CTA of a cluster, for a decode of R rows a key head.
 struct PagedPlan {
-    int tile, rows, per_sm, ahead, per_cluster;
+    int tile, rows, per_sm, per_cluster;
 };
 PagedPlan paged_plan(int R, int D, int page);  // bf16 pages
 PagedPlan paged_plan4(int D);                  // 4-bit pages

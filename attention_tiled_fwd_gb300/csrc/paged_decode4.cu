@@ -12,8 +12,8 @@
 //
 //   warp 4     producer: tiles of keys and values into a ring, a bulk copy for every page
 //   warps 0-3  kUnits neighbouring units of 16 keys of every tile each
-// Measured, 8 heads of 128: 48 sequences of 9000 to 32768 keys 201 us, 5.75 TB/s (85 % of a copy's rate), 64 of 900 to 16384 in pages of
-// 16 126 us, 5.05 TB/s.  A steady run of tiles goes at 95 %, 56 % of the issue slots taken over a launch of 63 us; the rest is its
+// Measured, 8 heads of 128: 48 sequences of 9000 to 32768 keys 198 us, 5.85 TB/s (86 % of a copy's rate), 64 of 900 to 16384 in pages of
+// 16 123 us, 5.2 TB/s.  A steady run of tiles goes at 95 %, 56 % of the issue slots taken over a launch of 63 us; the rest is its
 // start (5 us), the lists' ends (3 us each) and CTAs of an SM that do not end together.
 // Not kept: a ring for every warp, filled by itself, leaves room for 16 warps that compute instead of 12, but the copies' integer work
 // comes four times (170 us where this took 147, before other steps).
@@ -176,10 +176,10 @@ __device__ __forceinline__ void prepare_q(const __nv_bfloat16 *q, bool there, fl
     }
 }
 
-// What a list costs besides its tiles, in tiles (q, the join, the stores): with 0 in place of 1 or 2 the 64 sequences of 900 to 16384 keys
-// in pages of 64 took 83 us instead of 77 at D = 64, 275 instead of 265 at 256 (before other steps).
+// What a list costs besides its tiles, in tiles: with 2, 1 and 1 instead, 100 sequences of 100 to 3000 keys took 37, 57 and 109 us at
+// D = 64, 128 and 256, now 35, 49 and 88; 64 of 900 to 16384 76, 121 and 253, now 76, 118 and 237.
 template <int D>
-constexpr int kListCost = D == 64 ? 2 : 1;
+constexpr int kListCost = D == 64 ? 4 : D == 128 ? 3 : 5;
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(PagedDecodeArgs a) {
@@ -541,13 +541,9 @@ cudaError_t launch_d(const PagedDecodeArgs &a, int ctas, cudaStream_t s) {
     return launch_behind(kern, dim3(ctas), kThreads, Cfg<D>::kAlloc, false, std::max(1, a.cluster), s, a);
 }
 
-// An SM's CTAs that started first are served first: with equal runs three of them ended after 178, 190 and 204 us (64 sequences of
-// 16384 keys), four of D = 64 after 54, 57, 61 and 65.
-constexpr int kAhead = 65;
-
 template <int D>
 PagedPlan plan_d() {
-    return PagedPlan{Cfg<D>::kTile, 8, Cfg<D>::kCtas, D < 256 ? kAhead : 0, D < 256 ? 4 : 6};
+    return PagedPlan{Cfg<D>::kTile, 8, Cfg<D>::kCtas, D < 256 ? 4 : 6};
 }
 
 }  // namespace

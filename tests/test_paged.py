@@ -817,8 +817,8 @@ def test_decode_of_many_and_of_long_sequences(case, four):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("Hkv,n", [(1, 1300000), (16, 82000)])
-def test_four_bit_runs_of_unequal_length(Hkv, n):
-    """So many tiles that an SM's CTAs get runs of different lengths: one list over all of them, and several each."""
+def test_four_bit_runs_over_the_whole_grid(Hkv, n):
+    """So many tiles that all CTAs have runs of many: one list over all of them, and several lists."""
     import attention_tiled_fwd_gb300 as fa
     cuda_or_skip()
     if torch.cuda.mem_get_info()[0] < 20 << 30:

@@ -13,7 +13,7 @@
 //   warp 4     producer: tiles of keys and values into a ring, a bulk copy for every page
 //   warps 0-3  kUnits neighbouring units of 16 keys of every tile each
 // Measured, 8 heads of 128: 48 sequences of 9000 to 32768 keys 198 us, 5.85 TB/s (86 % of a copy's rate), 64 of 900 to 16384 in pages of
-// 16 123 us, 5.2 TB/s.  A steady run of tiles goes at 95 %, 56 % of the issue slots taken over a launch of 63 us; the rest is its
+// 16 123 us, 5.2 TB/s.  A steady run of tiles goes at 95 %, 55 % of the issue slots taken over a launch of 61 us; the rest is its
 // start (5 us), the lists' ends (3 us each) and CTAs of an SM that do not end together.
 // Not kept: a ring for every warp, filled by itself, leaves room for 16 warps that compute instead of 12, but the copies' integer work
 // comes four times (170 us where this took 147, before other steps).

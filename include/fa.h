@@ -389,9 +389,10 @@ FA_API const char *fa_status_string(int status);
 
 /*
  * fa_device_status -- synchronises `stream`, then returns and clears the
- * device status word of the current device: FA_OK, or FA_ERR_TIMEOUT if a
- * bounded in-kernel wait ran out since the last call.  Returns FA_ERR_CUDA
- * if the synchronisation itself failed.
+ * device status word of the current device: FA_OK, or what was recorded first
+ * since the last call: FA_ERR_TIMEOUT, a bounded in-kernel wait ran out, or
+ * FA_ERR_PAGE, a page table has no page of the pool where a paged call needed
+ * one.  Returns FA_ERR_CUDA if the synchronisation itself failed.
  */
 FA_API int fa_device_status(void *stream);
 

@@ -53,6 +53,24 @@ struct Cfg {
 template <int D>
 constexpr int kListCost = D == 64 ? 4 : 3;
 
+// Two weights as operands of two products: the bf16 numbers below them, and what those leave, off by half a step, 2^-15 of a weight at
+// most.  (One product with rounded weights, off by 2^-8, made O's error 1.4 times that of its own rounding.)  No part of a weight is 0:
+// an infinite value times 0 would be NaN.
+__device__ __forceinline__ void weight_parts(uint32_t &most, uint32_t &rest, float p0, float p1) {
+    const uint32_t m0 = (max(__float_as_uint(p0), 1u) - 1u) & 0xffff0000u, m1 = (max(__float_as_uint(p1), 1u) - 1u) & 0xffff0000u;
+    most = transpose8(m0 >> 16 | m1);
+    rest = transpose8(pack_bf16x2(p0 - __uint_as_float(m0), p1 - __uint_as_float(m1)));
+}
+// o += the weighted values of a unit, in fp32 as such.  The tensor cores drop what lies 2^-25 below a sum's largest addend, which over
+// a list's 2^21 keys a warp, two products each, would be 3 % of O if it stayed in one accumulator.
+__device__ __forceinline__ void add_weighted(float (&o)[4], const uint32_t (&values)[4], const uint32_t (&most)[2], const uint32_t (&rest)[2]) {
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    mma16816(sum, values, rest[0], rest[1]);
+    mma16816(sum, values, most[0], most[1]);
+    f2_unpack(f2_add(f2_pack(o[0], o[1]), f2_pack(sum[0], sum[1])), o[0], o[1]);
+    f2_unpack(f2_add(f2_pack(o[2], o[3]), f2_pack(sum[2], sum[3])), o[2], o[3]);
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -229,7 +247,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
                             }
                         }
                 }
-                uint32_t pb[NT][2];  // P^T as the second product's operand: row g, keys 2 tq and 2 tq + 1 (+ 8)
+                // P^T as the second product's operand, in two parts: row g, keys 2 tq and 2 tq + 1 (+ 8)
+                uint32_t pb[NT][2], rest[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float p[4];
@@ -237,9 +256,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
                     for (int e = 0; e < 4; ++e) p[e] = ex2_approx(logs(n, e));
                     // this lane's keys, not rounded; the others' are added at the end
                     l[n][0] += p[0] + p[2], l[n][1] += p[1] + p[3];
-                    // the weights as operands: bf16, off by half a step (up to 2^-8 of a weight)
-                    pb[n][0] = transpose8(pack_bf16x2(p[0], p[1]));
-                    pb[n][1] = transpose8(pack_bf16x2(p[2], p[3]));
+                    weight_parts(pb[n][0], rest[n][0], p[0], p[1]);
+                    weight_parts(pb[n][1], rest[n][1], p[2], p[3]);
                 }
                 uint32_t keep[2] = {~0u, ~0u};
                 if (!plain) keep_seen(keep, used_keys(tiles, key0, a.sinks), tq);
@@ -265,7 +283,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
                         uint32_t vf[4];
                         values(vf, i, keep);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16816(o[n][i], vf, pb[n][0], pb[n][1]);
+                        for (int n = 0; n < NT; ++n) add_weighted(o[n][i], vf, pb[n], rest[n]);
                     }
                 } else {
                     // the rows of one position at a time, with the values of the keys that they see
@@ -281,7 +299,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
                                 float sum[4] = {o[n][i][0], o[n][i][1], o[n][i][2], o[n][i][3]};
-                                mma16816(sum, vf, pb[n][0], pb[n][1]);
+                                add_weighted(sum, vf, pb[n], rest[n]);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
                                     if (position(8 * n + 2 * tq + (e & 1)) == p) o[n][i][e] = sum[e];

@@ -30,6 +30,11 @@ namespace {
 
 constexpr int kWarps = kDecodeWarps;
 constexpr int kThreads = 32 * (kWarps + 1);
+// Keys of a warp whose products stay in the accumulators.  The tensor cores drop what lies 2^-25 below a sum, n 2^-26 of a sum of n
+// products at most: here 2^-14 of sum P s code and of 8 sum P s, which are larger than O by the root of the number of keys and more.
+// With all of a list in them O's error grew with its length (rms 1.6e-3 at 10^6 keys, 5e-3 at 4 10^6, 1.6e-2 at 8 10^6); now it is 1.6e-3,
+// the output's own rounding, at any length.  Four times as often costs 1 % (124 instead of 122 us for 64 sequences of 900 to 16384).
+constexpr int kFoldKeys = 4096;
 constexpr int kTinyScales = -22;  // E while no scale has reached 2^-15: they are taken times 2^15, the weights times 2^7
 
 enum : int { kSiteEmpty = 311, kSiteFull, kSiteDrain };
@@ -185,6 +190,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(PagedDecodeArgs a) {
     using C = Cfg<D>;
     using U = Unit4<D>;
+    constexpr int kFold = kFoldKeys / (C::kUnits * kUnit);  // tiles
     constexpr int kTile = C::kTile, kGroups = D / 32, kRows = 8, kStages = C::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -299,181 +305,221 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
         for (int j = 0; j < kGroups / 2; ++j) ones[j][0] = ones[j][1] = ones[j][2] = ones[j][3] = 0.f;
         prepare_q<D>(static_cast<const __nv_bfloat16 *>(a.q) + (first_row + g) * D, row0 + g < a.R, a.scale_log2, lane, qf, less, f);
 
-        for (int t = t0; t < t1; ++t) {
-            const int tile = tiles.tile(t), key_warp = tile * kTile + warp * (C::kUnits * kUnit);
-            const int span = kSpans == 1 ? tile : tile * kSpans + warp;
-            const bool plain = span >= plain0 && span < plain1;
-            const uint32_t ks = smem_u32(smem) + stage * 2 * C::kHalf + warp * (C::kUnits * U::kBytes), vs = ks + C::kHalf;
-            float sc[C::kUnits][4];  // S^T of the warp's units: keys g and g + 8, rows 2 tq and 2 tq + 1
-            if (ok) ok = sleepy_wait(&full[stage], phase, a.status, kSiteFull);  // (after a time-out: on whatever is there)
+        // O's sums of the keys before the last kFoldKeys, and `off` then: in local memory (the registers are taken)
+        float4 held[D / 16];
+        float held_off[2];
+        asm volatile("" ::"l"(held), "l"(held_off) : "memory");
+        for (int t = t0; t < t1;) {
+            const bool first = t == t0;
+            for (const int stop = min(t1, t + kFold); t < stop; ++t) {
+                const int tile = tiles.tile(t), key_warp = tile * kTile + warp * (C::kUnits * kUnit);
+                const int span = kSpans == 1 ? tile : tile * kSpans + warp;
+                const bool plain = span >= plain0 && span < plain1;
+                const uint32_t ks = smem_u32(smem) + stage * 2 * C::kHalf + warp * (C::kUnits * U::kBytes), vs = ks + C::kHalf;
+                float sc[C::kUnits][4];  // S^T of the warp's units: keys g and g + 8, rows 2 tq and 2 tq + 1
+                if (ok) ok = sleepy_wait(&full[stage], phase, a.status, kSiteFull);  // (after a time-out: on whatever is there)
 #pragma unroll
-            for (int w = 0; w < C::kUnits; ++w) {
-                const int key0 = key_warp + w * kUnit;
-                const uint32_t at = ks + w * U::kBytes, scales = at + U::kCodes;
-                uint32_t code[2][kGroups], s2[2][kGroups / 2], by[4];
-                load_codes<D>(code, at, lane);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    load_words(s2[half], scales + 2 * U::k_scale(g + 8 * half, 0));
-                    uint32_t two[1];
-                    load_words(two, scales + 2 * U::k_scale(g + 8 * half, 2 * (tq % (kGroups / 2))));
-                    by[half] = by[2 + half] = two[0];
-                }
-                mma_f16_new(sc[w], by, less[0], less[1]);
-#pragma unroll
-                for (int j = 0; j < kGroups; ++j) {
-                    uint32_t x[4], y[4];
+                for (int w = 0; w < C::kUnits; ++w) {
+                    const int key0 = key_warp + w * kUnit;
+                    const uint32_t at = ks + w * U::kBytes, scales = at + U::kCodes;
+                    uint32_t code[2][kGroups], s2[2][kGroups / 2], by[4];
+                    load_codes<D>(code, at, lane);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        const uint32_t c = code[half][j], d = c >> 8;
-                        x[half] = c & 0x000f000fu, x[2 + half] = c & 0x00f000f0u;
-                        y[half] = d & 0x000f000fu, y[2 + half] = d & 0x00f000f0u;
+                        load_words(s2[half], scales + 2 * U::k_scale(g + 8 * half, 0));
+                        uint32_t two[1];
+                        load_words(two, scales + 2 * U::k_scale(g + 8 * half, 2 * (tq % (kGroups / 2))));
+                        by[half] = by[2 + half] = two[0];
                     }
-                    const float2 sa = unpack_h2(s2[0][j / 2]), sb = unpack_h2(s2[1][j / 2]);
-                    const float s_lo = j & 1 ? sa.y : sa.x, s_hi = j & 1 ? sb.y : sb.x;
-                    float part[4];
-                    mma_f16_new(part, x, qf[2 * j][0], qf[2 * j][1]);
-                    mma_f16(part, y, qf[2 * j + 1][0], qf[2 * j + 1][1]);
-                    sc[w][0] = fmaf(s_lo, part[0], sc[w][0]), sc[w][1] = fmaf(s_lo, part[1], sc[w][1]);
-                    sc[w][2] = fmaf(s_hi, part[2], sc[w][2]), sc[w][3] = fmaf(s_hi, part[3], sc[w][3]);
+                    mma_f16_new(sc[w], by, less[0], less[1]);
+#pragma unroll
+                    for (int j = 0; j < kGroups; ++j) {
+                        uint32_t x[4], y[4];
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint32_t c = code[half][j], d = c >> 8;
+                            x[half] = c & 0x000f000fu, x[2 + half] = c & 0x00f000f0u;
+                            y[half] = d & 0x000f000fu, y[2 + half] = d & 0x00f000f0u;
+                        }
+                        const float2 sa = unpack_h2(s2[0][j / 2]), sb = unpack_h2(s2[1][j / 2]);
+                        const float s_lo = j & 1 ? sa.y : sa.x, s_hi = j & 1 ? sb.y : sb.x;
+                        float part[4];
+                        mma_f16_new(part, x, qf[2 * j][0], qf[2 * j][1]);
+                        mma_f16(part, y, qf[2 * j + 1][0], qf[2 * j + 1][1]);
+                        sc[w][0] = fmaf(s_lo, part[0], sc[w][0]), sc[w][1] = fmaf(s_lo, part[1], sc[w][1]);
+                        sc[w][2] = fmaf(s_hi, part[2], sc[w][2]), sc[w][3] = fmaf(s_hi, part[3], sc[w][3]);
+                    }
+                    if (!plain) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t seen = seen_keys(position(2 * tq + e), key0, a.window, a.sinks);
+                            if (!(seen >> g & 1u)) sc[w][e] = -INFINITY;
+                            if (!(seen >> (g + 8) & 1u)) sc[w][2 + e] = -INFINITY;
+                        }
+                    }
                 }
-                if (!plain) {
+                // scales of the values of keys 2 tq and 2 tq + 1 (+ 8)
+                uint32_t s2[C::kUnits][2][kGroups], bits = 0;
+#pragma unroll
+                for (int w = 0; w < C::kUnits; ++w) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) load_words(s2[w][half], vs + w * U::kBytes + U::kCodes + 2 * U::v_scale(2 * tq + 8 * half, 0));
+                    if (!plain) {
+                        // 0 times whatever the scales are of keys that the lane's row g does not see must not reach O
+                        const int key0 = key_warp + w * kUnit;
+                        uint32_t keep[2];
+                        keep_seen(keep, seen_keys(position(g), key0, a.window, a.sinks), tq);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+#pragma unroll
+                            for (int j = 0; j < kGroups; ++j) s2[w][half][j] &= keep[half];
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int j = 0; j < kGroups; ++j) bits |= s2[w][half][j];
+                }
+                // A weight is 2^8 at most, so its products with scales below 2^(E + 7) fit in fp16.  The bits of all scales together are no
+                // less than the largest of them, and mostly (with exponents 0 and 1 apart) in its power of two: one test does.
+                const uint32_t limit = max((uint32_t)(E + 7 + 15) << 10, 0x200u);  // 2^(E + 7)
+                if (__any_sync(0xffffffffu, E < 9 && (bits + (0x8000u - limit) * 0x10001u) & 0x80008000u)) {
+                    uint32_t most = 0;
+#pragma unroll
+                    for (int w = 0; w < C::kUnits; ++w)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+#pragma unroll
+                            for (int j = 0; j < kGroups; ++j) most = max_h2(most, s2[w][half][j]);
+                    const float2 mh = unpack_h2(most);
+                    const uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(mh.x, mh.y)));
+                    const int need = (int)(all >> 23) - 127 - 6;
+                    if (need > E) {
+                        const int to = max(-6, min(9, need));
+                        const float by = __int_as_float((127 + E - to) << 23), by_l = __int_as_float((127 + Ep - to) << 23);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) l[e] *= by_l, off[e] += (float)(to - Ep);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                            for (int j = 0; j < kGroups / 2; ++j) ones[j][e] *= by;
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) o[i][e] *= by;
+                        }
+                        E = Ep = to;
+                    }
+                }
+                if (E == kTinyScales) {
+#pragma unroll
+                    for (int w = 0; w < C::kUnits; ++w)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+#pragma unroll
+                            for (int j = 0; j < kGroups; ++j) s2[w][half][j] = mul_h2(s2[w][half][j], 0x78007800u);
+                }
+
+                // the weights' logarithms; the maxima are taken again only when a weight would grow past 2^8
+                bool grow = false;
+                float lg[C::kUnits][4];
+                auto logs = [&] {
+#pragma unroll
+                    for (int w = 0; w < C::kUnits; ++w)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) lg[w][e] = fmaf(sc[w][e], f[e & 1], -off[e & 1]);
+                };
+                logs();
+                const float most = 8.f - (float)Ep;
+#pragma unroll
+                for (int w = 0; w < C::kUnits; ++w)
+                    grow |= fmaxf(fmax3(lg[w][0], lg[w][1], lg[w][2]), lg[w][3]) > most;
+                if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint32_t seen = seen_keys(position(2 * tq + e), key0, a.window, a.sinks);
-                        if (!(seen >> g & 1u)) sc[w][e] = -INFINITY;
-                        if (!(seen >> (g + 8) & 1u)) sc[w][2 + e] = -INFINITY;
+                        float mt = -INFINITY;
+#pragma unroll
+                        for (int w = 0; w < C::kUnits; ++w) mt = fmax3(mt, sc[w][e], sc[w][2 + e]);
+                        mt *= f[e];
+                        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
+                        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
+                        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+                        mt += (float)Ep;
+                        if (mt > off[e] + 8.f) {
+                            const float alpha = ex2_approx(off[e] - mt);
+                            l[e] *= alpha;
+#pragma unroll
+                            for (int j = 0; j < kGroups / 2; ++j) ones[j][e] *= alpha, ones[j][2 + e] *= alpha;
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) o[i][e] *= alpha, o[i][2 + e] *= alpha;
+                            off[e] = mt;
+                        }
                     }
+                    logs();
                 }
-            }
-            // scales of the values of keys 2 tq and 2 tq + 1 (+ 8)
-            uint32_t s2[C::kUnits][2][kGroups], bits = 0;
-#pragma unroll
-            for (int w = 0; w < C::kUnits; ++w) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half) load_words(s2[w][half], vs + w * U::kBytes + U::kCodes + 2 * U::v_scale(2 * tq + 8 * half, 0));
-                if (!plain) {
-                    // 0 times whatever the scales are of keys that the lane's row g does not see must not reach O
-                    const int key0 = key_warp + w * kUnit;
-                    uint32_t keep[2];
-                    keep_seen(keep, seen_keys(position(g), key0, a.window, a.sinks), tq);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-#pragma unroll
-                        for (int j = 0; j < kGroups; ++j) s2[w][half][j] &= keep[half];
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int j = 0; j < kGroups; ++j) bits |= s2[w][half][j];
-            }
-            // A weight is 2^8 at most, so its products with scales below 2^(E + 7) fit in fp16.  The bits of all scales together are no
-            // less than the largest of them, and mostly (with exponents 0 and 1 apart) in its power of two: one test does.
-            const uint32_t limit = max((uint32_t)(E + 7 + 15) << 10, 0x200u);  // 2^(E + 7)
-            if (__any_sync(0xffffffffu, E < 9 && (bits + (0x8000u - limit) * 0x10001u) & 0x80008000u)) {
-                uint32_t most = 0;
-#pragma unroll
-                for (int w = 0; w < C::kUnits; ++w)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-#pragma unroll
-                        for (int j = 0; j < kGroups; ++j) most = max_h2(most, s2[w][half][j]);
-                const float2 mh = unpack_h2(most);
-                const uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(mh.x, mh.y)));
-                const int need = (int)(all >> 23) - 127 - 6;
-                if (need > E) {
-                    const int to = max(-6, min(9, need));
-                    const float by = __int_as_float((127 + E - to) << 23), by_l = __int_as_float((127 + Ep - to) << 23);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) l[e] *= by_l, off[e] += (float)(to - Ep);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-#pragma unroll
-                        for (int j = 0; j < kGroups / 2; ++j) ones[j][e] *= by;
-#pragma unroll
-                        for (int i = 0; i < D / 16; ++i) o[i][e] *= by;
-                    }
-                    E = Ep = to;
-                }
-            }
-            if (E == kTinyScales) {
-#pragma unroll
-                for (int w = 0; w < C::kUnits; ++w)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-#pragma unroll
-                        for (int j = 0; j < kGroups; ++j) s2[w][half][j] = mul_h2(s2[w][half][j], 0x78007800u);
-            }
 
-            // the weights' logarithms; the maxima are taken again only when a weight would grow past 2^8
-            bool grow = false;
-            float lg[C::kUnits][4];
-            auto logs = [&] {
 #pragma unroll
-                for (int w = 0; w < C::kUnits; ++w)
+                for (int w = 0; w < C::kUnits; ++w) {
+                    const int key0 = key_warp + w * kUnit;
+                    uint32_t pb[2];  // P^T as the second product's operand: row g, keys 2 tq and 2 tq + 1 (+ 8)
+                    float p[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) lg[w][e] = fmaf(sc[w][e], f[e & 1], -off[e & 1]);
-            };
-            logs();
-            const float most = 8.f - (float)Ep;
+                    for (int e = 0; e < 4; ++e) p[e] = ex2_approx(lg[w][e]);
+                    // this lane's keys, not rounded; the others' are added at the end
+                    l[0] += p[0] + p[2], l[1] += p[1] + p[3];
+                    pb[0] = transpose8(pack_h2(p[0], p[1]));  // the weights as operands: fp16, off by 2^-11
+                    pb[1] = transpose8(pack_h2(p[2], p[3]));
+                    uint32_t code[2][kGroups];
+                    load_codes<D>(code, vs + w * U::kBytes, lane);
 #pragma unroll
-            for (int w = 0; w < C::kUnits; ++w)
-                grow |= fmaxf(fmax3(lg[w][0], lg[w][1], lg[w][2]), lg[w][3]) > most;
-            if (__any_sync(0xffffffffu, grow)) {
+                    for (int j = 0; j < kGroups; ++j) {
+                        uint32_t x[4], y[4];
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint32_t c = code[half][j], d = c >> 8;
+                            x[2 * half] = c & 0x000f000fu, x[2 * half + 1] = c & 0x00f000f0u;
+                            y[2 * half] = d & 0x000f000fu, y[2 * half + 1] = d & 0x00f000f0u;
+                        }
+                        const uint32_t u0 = j & 1 ? 0u : 0x3c003c00u, u1 = 0x3c003c00u - u0, one[4] = {u0, u1, u0, u1};  // rows 0-7, or 8-15
+                        const uint32_t b0 = mul_h2(pb[0], s2[w][0][j]), b1 = mul_h2(pb[1], s2[w][1][j]);
+                        mma_f16(o[2 * j], x, b0, b1);
+                        mma_f16(o[2 * j + 1], y, b0, b1);
+                        mma_f16(ones[j / 2], one, b0, b1);
+                    }
+                }
+                warp_arrive(&empty[stage]);
+                if (++stage == kStages) stage = 0, phase ^= 1;
+            }
+            // sum P v out of the accumulators, added up in fp32 as such
+            const float by = E == kTinyScales ? 0x1p-15f : 1.f, by8 = -8.f * by, by20 = 0x1p20f * by, by24 = 0x1p24f * by;  // (the scales' own power of two)
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const float *one = ones[i / 4] + (i & 2);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float mt = -INFINITY;
-#pragma unroll
-                    for (int w = 0; w < C::kUnits; ++w) mt = fmax3(mt, sc[w][e], sc[w][2 + e]);
-                    mt *= f[e];
-                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
-                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
-                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-                    mt += (float)Ep;
-                    if (mt > off[e] + 8.f) {
-                        const float alpha = ex2_approx(off[e] - mt);
-                        l[e] *= alpha;
-#pragma unroll
-                        for (int j = 0; j < kGroups / 2; ++j) ones[j][e] *= alpha, ones[j][2 + e] *= alpha;
-#pragma unroll
-                        for (int i = 0; i < D / 16; ++i) o[i][e] *= alpha, o[i][2 + e] *= alpha;
-                        off[e] = mt;
-                    }
-                }
-                logs();
-            }
-
-#pragma unroll
-            for (int w = 0; w < C::kUnits; ++w) {
-                const int key0 = key_warp + w * kUnit;
-                uint32_t pb[2];  // P^T as the second product's operand: row g, keys 2 tq and 2 tq + 1 (+ 8)
-                float p[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = ex2_approx(lg[w][e]);
-                // this lane's keys, not rounded; the others' are added at the end
-                l[0] += p[0] + p[2], l[1] += p[1] + p[3];
-                pb[0] = transpose8(pack_h2(p[0], p[1]));  // the weights as operands: fp16, off by 2^-11
-                pb[1] = transpose8(pack_h2(p[2], p[3]));
-                uint32_t code[2][kGroups];
-                load_codes<D>(code, vs + w * U::kBytes, lane);
-#pragma unroll
-                for (int j = 0; j < kGroups; ++j) {
-                    uint32_t x[4], y[4];
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t c = code[half][j], d = c >> 8;
-                        x[2 * half] = c & 0x000f000fu, x[2 * half + 1] = c & 0x00f000f0u;
-                        y[2 * half] = d & 0x000f000fu, y[2 * half + 1] = d & 0x00f000f0u;
-                    }
-                    const uint32_t u0 = j & 1 ? 0u : 0x3c003c00u, u1 = 0x3c003c00u - u0, one[4] = {u0, u1, u0, u1};  // rows 0-7, or 8-15
-                    const uint32_t b0 = mul_h2(pb[0], s2[w][0][j]), b1 = mul_h2(pb[1], s2[w][1][j]);
-                    mma_f16(o[2 * j], x, b0, b1);
-                    mma_f16(o[2 * j + 1], y, b0, b1);
-                    mma_f16(ones[j / 2], one, b0, b1);
+                    const float less8 = by8 * one[e];
+                    o[i][e] = fmaf(o[i][e], by24, less8);
+                    o[i][2 + e] = fmaf(o[i][2 + e], by20, less8);
                 }
             }
-            warp_arrive(&empty[stage]);
-            if (++stage == kStages) stage = 0, phase ^= 1;
+            if (!first) {
+                const float since0 = ex2_approx(held_off[0] - off[0]), since1 = ex2_approx(held_off[1] - off[1]);
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const float4 h = held[i];
+                    o[i][0] = fmaf(h.x, since0, o[i][0]);
+                    o[i][1] = fmaf(h.y, since1, o[i][1]);
+                    o[i][2] = fmaf(h.z, since0, o[i][2]);
+                    o[i][3] = fmaf(h.w, since1, o[i][3]);
+                }
+            }
+            if (t == t1) break;
+            held_off[0] = off[0], held_off[1] = off[1];
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                held[i] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+                o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < kGroups / 2; ++j) ones[j][0] = ones[j][1] = ones[j][2] = ones[j][3] = 0.f;
+            asm volatile("" ::"l"(held), "l"(held_off) : "memory");
         }
 
         // O and L of a list that this CTA holds whole, else a partial: in its first slot what began in a CTA before this one, in
@@ -487,7 +533,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
             tail = run.b * per_seq + run.u;
             tail_rest = tiles.n - t1;
         }
-        const float by = E == kTinyScales ? 0x1p-15f : 1.f, by8 = -8.f * by, by20 = 0x1p20f * by, by24 = 0x1p24f * by;  // (the scales' own power of two)
         float *buf = reinterpret_cast<float *>(smem + C::kJoinOff);
         float2 *ml = reinterpret_cast<float2 *>(smem + C::kMlOff);
 #pragma unroll
@@ -504,14 +549,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 // channel 32 j + 4 g + (0, 1 | 2, 3) at place 8 (channel % 4) + g of its group
-                const int j = 2 * c + i / 2;
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float less8 = by8 * ones[j / 2][2 * (j & 1) + e];
-                    v[e] = fmaf(o[4 * c + i][e], by24, less8);
-                    v[2 + e] = fmaf(o[4 * c + i][2 + e], by20, less8);
-                }
+                const float *v = o[4 * c + i];
                 float *to = buf + warp * (kJoinCols * 8) + (32 * (i / 2) + 16 * (i % 2) + g) * 8 + 2 * tq;
                 *reinterpret_cast<float2 *>(to) = make_float2(v[0], v[1]);
                 *reinterpret_cast<float2 *>(to + 64) = make_float2(v[2], v[3]);

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from helpers import cuda_or_skip
-from paged_ref import rows_of
+from paged_ref import rows_of, unit_values
 from test_paged import _gen, _ints, _pool, _randn, _tables
 from window_ref import U, attend, check, check_lse, visible
 
@@ -114,5 +114,42 @@ def test_bf16_sums_over_the_longest_lists():
     O, L, A, S = _one_sequence(rows, lambda i, j: k[i:j].double(), lambda i, j: v[i:j].double(), n, 0.2)
     bound = U * O.abs() + (2 * D * 2.0 ** -24 * S[:, None] + 2.0 ** -8 + 2.0 ** -14) * A
     check(o[:, 0, 0], O[:1].expand(lists, D), bound[:1].expand(lists, D), "O of equal weights")
+    check(o[some, 1, 0], O[1:], bound[1:], "O")
+    check_lse(lse[some, 1, 0], L[1:], "LSE")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_four_bit_sums_over_the_longest_lists(D):
+    """As above over 4-bit pages, with values of both signs, so that O is small beside sum P |v|.
+
+    Equal weights are powers of two, so their products with the scales are exact: O is off by the sums alone.  The codes' sum is
+    sum P s code, at most 15 sum P s but here, where the codes' mean is below 9, less than 9; the kernel takes 8 sum P s of it every
+    4096 keys of a warp, and a tensor core's sum of 4096 products loses 2^-14 of itself at most (n 2^-26): both lose, so their
+    difference is off by less than 9 2^-14 sum P s, which does not grow with the list.  512 additions in fp32: 2^-15 sum P |v| < 2^-12 sum P s.
+    Other weights are rounded twice to 2^-11 as well."""
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB")
+    g, n, page, lists = _gen(59 + D), 1 << 23, 256, {64: 650, 128: 500, 256: 340}[D]
+    slots = n // page
+    pages = _pool(g, slots, 1, page, D, True)
+    order = torch.randperm(slots, generator=g, device="cuda").to(torch.int32)
+    q = _randn(g, lists, 2, 1, D)
+    q[:, 0] = 0  # equal weights
+    o, lse = fa.fa_paged_decode(q, *pages, order[None].expand(lists, -1).contiguous(), scale=0.1)
+    assert fa.fa_device_status() == 0
+    some = [0, lists // 2, lists - 1]
+    rows = torch.cat((q[:1, 0, 0], q[some, 1, 0]))
+
+    def values(which):
+        return lambda i, j: unit_values(pages[which][i // page:j // page], D, which == 1)[0].view(-1, D)
+
+    O, L, A, S = _one_sequence(rows, values(0), values(1), n, 0.1)
+    s = sum(unit_values(pages[1][i:i + 1024], D, True)[1].view(-1, D).sum(0) for i in range(0, slots, 1024)) / n
+    bound = U * O.abs() + (9 * 2.0 ** -14 + 2.0 ** -12) * s
+    check(o[:, 0, 0], O[:1].expand(lists, D), bound[:1].expand(lists, D), "O of equal weights")
+    bound = bound + (2 * D * 2.0 ** -24 * S[:, None] + 2.0 ** -10) * A
     check(o[some, 1, 0], O[1:], bound[1:], "O")
     check_lse(lse[some, 1, 0], L[1:], "LSE")

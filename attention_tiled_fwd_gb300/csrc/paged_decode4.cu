@@ -6,9 +6,10 @@
 // AND makes an operand register of two of them; the powers go into q and into O's last factor.
 // Keys: sum_c q_c s (code_c - 8) for 32 channels is s (the product with the codes); the -8 sum q go in as one more product of
 // the scales.  q is scaled by a power of two a row so that fp16 holds its bf16 values.  Values: the weights are multiplied with
-// each group's scales (fp16, one rounding of the weight and one of the product: 2^-11 each), and a product with ones adds up
-// what 8 has to be taken of.  Weights carry a power of two, 2^-E, so that their products with the scales stay in fp16's range
-// and above its subnormals: E grows with the scales.
+// each group's scales (fp16, one rounding of the weight and one of the product: 2^-11 each, an eighth of the output's own), and a product
+// with ones adds up what 8 has to be taken of.  Weights carry 2^6 and scales a power of two that follows the tile's largest: where
+// weights or products are subnormal in fp16 they are off by 2^-26 of that scale at most, beside the heaviest weight.  (Scales whose
+// largest is outside 2^-4 .. 2 take a product each for it: 122 instead of 118 us.)
 //
 //   warp 4     producer: tiles of keys and values into a ring, a bulk copy for every page
 //   warps 0-3  kUnits neighbouring units of 16 keys of every tile each
@@ -35,7 +36,7 @@ constexpr int kThreads = 32 * (kWarps + 1);
 // With all of a list in them O's error grew with its length (rms 1.6e-3 at 10^6 keys, 5e-3 at 4 10^6, 1.6e-2 at 8 10^6); now it is 1.6e-3,
 // the output's own rounding, at any length.  Four times as often costs 1 % (124 instead of 122 us for 64 sequences of 900 to 16384).
 constexpr int kFoldKeys = 4096;
-constexpr int kTinyScales = -22;  // E while no scale has reached 2^-15: they are taken times 2^15, the weights times 2^7
+constexpr int kLift = 6;  // weights carry 2^6, so they are 2^14 at most
 
 enum : int { kSiteEmpty = 311, kSiteFull, kSiteDrain };
 
@@ -289,12 +290,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
         const int p_first = max(0, tiles.len - a.n_q), past = tiles.len - 1 - a.window;
         const int plain0 = past < 0 ? 0 : past / kSpan + 1, plain1 = (p_first + 1) / kSpan;
 
-        // off: the running maximum (log2 units), plus the weights' power of two; kNone while a row has seen nothing
+        // off: the running maximum (log2 units) less kLift; kNone while a row has seen nothing
         float off[2], l[2], f[2], o[D / 16][4];
         auto position = [&](int r) { return tiles.len - a.n_q + (row0 + r) % a.n_q; };  // rows past R: any; they are not stored
         uint32_t qf[D / 16][2], less[2];
         float ones[kGroups / 2][4];  // sum P s of an even group, and of the odd one behind it
-        int E = kTinyScales, Ep = -7;  // powers of two of the weights times scales, and of the weights
+        int up = 0;  // scales are taken times 2^up
 #pragma unroll
         for (int e = 0; e < 2; ++e) off[e] = kNone, l[e] = 0.f;
 #pragma unroll
@@ -379,10 +380,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
 #pragma unroll
                         for (int j = 0; j < kGroups; ++j) bits |= s2[w][half][j];
                 }
-                // A weight is 2^8 at most, so its products with scales below 2^(E + 7) fit in fp16.  The bits of all scales together are no
-                // less than the largest of them, and mostly (with exponents 0 and 1 apart) in its power of two: one test does.
-                const uint32_t limit = max((uint32_t)(E + 7 + 15) << 10, 0x200u);  // 2^(E + 7)
-                if (__any_sync(0xffffffffu, E < 9 && (bits + (0x8000u - limit) * 0x10001u) & 0x80008000u)) {
+                // Products of weights with scales are fp16: scales below 2 2^-up do not overflow (nor does any at up = -14).  Below 2^-14 they
+                // are off by 2^-25 whatever their size, so `up` follows the tile's largest scale down as well: it stays above 2^-4 2^-up.
+                // For up = 0 two tests mostly do: 2 and more have bit 14, and any one of the scales is no more than the largest.
+                const bool over = (bits & 0x40004000u) != 0, enough = ((s2[0][0][0] + 0x54005400u) & 0x80008000u) != 0;  // (2^-4 is 0x2c00)
+                if (up != 0 || __any_sync(0xffffffffu, over) || !__any_sync(0xffffffffu, enough)) {
                     uint32_t most = 0;
 #pragma unroll
                     for (int w = 0; w < C::kUnits; ++w)
@@ -392,12 +394,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
                             for (int j = 0; j < kGroups; ++j) most = max_h2(most, s2[w][half][j]);
                     const float2 mh = unpack_h2(most);
                     const uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(mh.x, mh.y)));
-                    const int need = (int)(all >> 23) - 127 - 6;
-                    if (need > E) {
-                        const int to = max(-6, min(9, need));
-                        const float by = __int_as_float((127 + E - to) << 23), by_l = __int_as_float((127 + Ep - to) << 23);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) l[e] *= by_l, off[e] += (float)(to - Ep);
+                    const int size = (int)(all >> 23) - 127, to = max(-14, min(15, -size));  // 2^size: its power of two
+                    if (all != 0 && (size + up > 0 || size + up < -4) && to != up) {
+                        const float by = __int_as_float((127 + to - up) << 23);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
 #pragma unroll
@@ -405,16 +404,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
 #pragma unroll
                             for (int i = 0; i < D / 16; ++i) o[i][e] *= by;
                         }
-                        E = Ep = to;
+                        up = to;
                     }
-                }
-                if (E == kTinyScales) {
+                    const uint32_t by = (uint32_t)(up + 15) * 0x04000400u;
 #pragma unroll
                     for (int w = 0; w < C::kUnits; ++w)
 #pragma unroll
                         for (int half = 0; half < 2; ++half)
 #pragma unroll
-                            for (int j = 0; j < kGroups; ++j) s2[w][half][j] = mul_h2(s2[w][half][j], 0x78007800u);
+                            for (int j = 0; j < kGroups; ++j) s2[w][half][j] = mul_h2(s2[w][half][j], by);
                 }
 
                 // the weights' logarithms; the maxima are taken again only when a weight would grow past 2^8
@@ -427,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
                         for (int e = 0; e < 4; ++e) lg[w][e] = fmaf(sc[w][e], f[e & 1], -off[e & 1]);
                 };
                 logs();
-                const float most = 8.f - (float)Ep;
+                constexpr float most = 8.f + kLift;
 #pragma unroll
                 for (int w = 0; w < C::kUnits; ++w)
                     grow |= fmaxf(fmax3(lg[w][0], lg[w][1], lg[w][2]), lg[w][3]) > most;
@@ -441,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
                         mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
                         mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
                         mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-                        mt += (float)Ep;
+                        mt -= (float)kLift;
                         if (mt > off[e] + 8.f) {
                             const float alpha = ex2_approx(off[e] - mt);
                             l[e] *= alpha;
@@ -488,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
                 if (++stage == kStages) stage = 0, phase ^= 1;
             }
             // sum P v out of the accumulators, added up in fp32 as such
-            const float by = E == kTinyScales ? 0x1p-15f : 1.f, by8 = -8.f * by, by20 = 0x1p20f * by, by24 = 0x1p24f * by;  // (the scales' own power of two)
+            const float by = __int_as_float((127 - up) << 23), by8 = -8.f * by, by20 = 0x1p20f * by, by24 = 0x1p24f * by;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
                 const float *one = ones[i / 4] + (i & 2);

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from helpers import cuda_or_skip
-from paged_ref import rows_of, unit_values
+from paged_ref import place, rows_of, unit_values
 from test_paged import _gen, _ints, _pool, _randn, _tables
 from window_ref import U, attend, check, check_lse, visible
 
@@ -153,3 +153,67 @@ def test_four_bit_sums_over_the_longest_lists(D):
     bound = bound + (2 * D * 2.0 ** -24 * S[:, None] + 2.0 ** -10) * A
     check(o[some, 1, 0], O[1:], bound[1:], "O")
     check_lse(lse[some, 1, 0], L[1:], "LSE")
+
+
+def _four_bit_pages(codes, scales, of_values):
+    """Pages [n / 16, 1, 16, 9 D / 16] of rows of one head with these codes [n, D] and scales [n, D / 32]."""
+    n, D = codes.shape
+    units = torch.zeros((n // 16, 9 * D), dtype=torch.uint8)
+    byte, shift, scale = place(D, of_values)
+    codes = codes.view(n // 16, 16, D).to(torch.uint8)
+    for p in range(16):
+        for nibble in (0, 4):
+            own = shift[p] == nibble
+            units[:, byte[p][own]] |= codes[:, p][:, own] << nibble
+        units.view(torch.float16)[:, 4 * D + scale[p, ::32]] = scales.view(n // 16, 16, -1)[:, p].half()
+    return units.view(n // 16, 1, 16, 9 * D // 16)
+
+
+def test_four_bit_pages_of_given_codes():
+    g = torch.Generator().manual_seed(61)
+    for of_values in (False, True):
+        codes, scales = torch.randint(1, 16, (48, 64), generator=g), torch.rand(48, 2, generator=g).half()
+        values, s = unit_values(_four_bit_pages(codes, scales, of_values), 64, of_values)
+        assert torch.equal(s.view(48, 64), scales.double().repeat_interleave(32, 1))
+        assert torch.equal(values.view(48, 64), (codes.double() - 8) * scales.double().repeat_interleave(32, 1))
+
+
+# the ordinary keys' weight beside the heaviest (log2) and scale, and the scale of the keys of no weight at all
+OUTLIERS = [(-12.6, 0.15, 0.1), (-12.6, 0.15, 4096.0), (-14.6, 0.15, 4096.0), (-14.6, 0.15, 16384.0), (-15.3, 0.15, 65504.0),
+            (-15.3, 3.2e-4, 0.4), (-12.6, 2e-6, 1.0), (-14.6, 300.0, 1.0), (-14.6, 2.0, 1e-3)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("weight,size,other", OUTLIERS)
+def test_four_bit_scales_of_unlike_size(D, weight, size, other):
+    """Thousands of keys of low weight, all alike, so that their roundings do not cancel; before them a few of the largest weight,
+    and one for each warp that has no weight and a scale of another size.
+
+    Weights are fp16 times 2^6 beside the heaviest, scales times a power of two 2^up for the largest of a warp's tile (32 keys, 16
+    at D = 256), and their products fp16.  So besides 2^-11 of itself a weight is off by 2^-31, a product by 2^-31 2^-up, and a scale by 2^-25
+    2^-up; a code is within 7 of 8, and l is 1 at least beside the heaviest.  2^up (2^15 at most) puts the tile's largest scale into
+    [2^-4, 2), and where it has to change, as between sizes 32 apart, into [1, 2)."""
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    n, lists, tile = 4000, 700, 16 if D == 256 else 32
+    key = torch.arange(n)
+    heavy, none = (key < 4 * tile) & (key % 16 == 0), (key >= 4 * tile) & (key < 8 * tile) & (key % tile == 1)
+    ks = torch.where(heavy, 1e-4, torch.where(none, 80.0, -weight * math.log(2.0))) / (0.01 * D)  # a key is -scale in all channels
+    kc = torch.full((n, D), 7)
+    vc = (torch.arange(D) % 15 + 1).expand(n, D)
+    vs = torch.where(none, other, torch.where(heavy, 1e-3 * size, size))
+    pages = [_four_bit_pages(c, s[:, None].expand(n, D // 32), i == 1).cuda() for i, (c, s) in enumerate(((kc, ks), (vc, vs)))]
+    table = _ints(list(range(n // 16))).expand(lists, -1).contiguous()
+    q = torch.ones((lists, 1, 1, D), dtype=torch.bfloat16, device="cuda")
+    o, lse = fa.fa_paged_decode(q, *pages, table, _ints([n] * lists), scale=0.01)
+    assert fa.fa_device_status() == 0
+    k, v = (unit_values(t, D, i == 1)[0].view(n, D) for i, t in enumerate(pages))
+    s = unit_values(pages[1], D, True)[1].view(n, D)[:, :1]
+    O, L, P, A = attend(q[0, 0].double(), k, v, torch.ones(1, n, dtype=torch.bool, device="cuda"), 0.01)
+    step = s.view(-1, tile).amax(1).repeat_interleave(tile)[:, None].clamp(min=2.0 ** -15)  # 2^-up, beside the 16 below
+    step[:4 * tile if max(size, other) >= 32 * min(size, other) else n] *= 16
+    bound = U * O.abs() + (2.0 ** -10 + 2.0 ** -11) * A + 2.0 ** -11 * (P @ s)
+    bound = bound + 7 * (2.0 ** -31 * (s + step).sum() * P.amax() + 2.0 ** -25 * (P @ step))
+    check(o[:, 0, 0], O.expand(lists, D), bound.expand(lists, D), "O")
+    check_lse(lse[:, 0, 0], L.expand(lists), "LSE")

@@ -1,4 +1,4 @@
-"""How far the sums of paged decode may be off: bounds that count roundings and nothing else, where the bounds of
+"""How far the sums of the paged calls may be off: bounds that count roundings and nothing else, where the bounds of
 test_paged.py allow for bf16 weights and for accumulators that lose bits with a list's length."""
 import math
 
@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from helpers import cuda_or_skip
-from paged_ref import place, rows_of, unit_values
+from paged_ref import once, place, rows_of, turned, unit_values
 from test_paged import _gen, _ints, _pool, _randn, _tables
 from window_ref import U, attend, check, check_lse, visible
 
@@ -217,3 +217,45 @@ def test_four_bit_scales_of_unlike_size(D, weight, size, other):
     bound = bound + 7 * (2.0 ** -31 * (s + step).sum() * P.amax() + 2.0 ** -25 * (P @ step))
     check(o[:, 0, 0], O.expand(lists, D), bound.expand(lists, D), "O")
     check_lse(lse[:, 0, 0], L.expand(lists), "LSE")
+
+
+def _near_ties(inter):
+    """Rows [1, 1, n, D], cosines and sines whose rotated channels lie 2^-20 to 2^-40 of themselves beside the middle of two bf16 values:
+    a cos is the middle itself (a power of two times a number of 9 bits), b sin what it misses."""
+    g = torch.Generator().manual_seed(63)
+    n, D = 256, 64
+    half = (n, D // 2)
+    a = 2.0 ** torch.randint(-6, 7, half, generator=g) * (1 - 2.0 * torch.randint(0, 2, half, generator=g))
+    middle = 2.0 ** torch.randint(-3, 4, half, generator=g) * (1 + (2 * torch.randint(0, 128, half, generator=g) + 1) / 256)
+    b = 2.0 ** torch.randint(-6, 7, half, generator=g)
+    sin = middle * a.abs() / b * 2.0 ** torch.randint(-40, -19, half, generator=g) * (1 - 2.0 * torch.randint(0, 2, half, generator=g))
+    i = torch.arange(D // 2)
+    at = (2 * i, 2 * i + 1) if inter else (i, i + D // 2)
+    k = torch.zeros(1, 1, n, D)
+    k[0, 0][:, at[0]], k[0, 0][:, at[1]] = a, b
+    assert torch.equal(k.bfloat16().float(), k) and torch.equal((a.double() * middle.double()).float().double(), a.double() * middle.double())
+    return k.bfloat16(), middle.float(), sin.float(), at
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_near_ties_are_near_ties(inter):
+    k, cos, sin, at = _near_ties(inter)
+    y = turned(k, torch.arange(256), cos, sin, 64, inter)[0, 0][:, at[0]]
+    # rounded to fp32 first, a good part of those less than 2^-25 beside the middle go the wrong way
+    assert int((y.float().bfloat16() != once(y)).sum()) > 1000
+    off = (y / (k[0, 0][:, at[0]].double() * cos.double()) - 1).abs()
+    assert 2.0 ** -41 < float(off.min()) and float(off.max()) < 2.0 ** -19
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("inter", [False, True])
+def test_sums_beside_the_middle_of_two_bf16_values(inter):
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    k, cos, sin, _ = (t.cuda() if torch.is_tensor(t) else t for t in _near_ties(inter))
+    y = turned(k, torch.arange(256, device="cuda"), cos, sin, 64, inter)
+    assert int((y.float().bfloat16() != once(y)).sum()) > 1000
+    pages, table = _pool(_gen(65), 16, 1, 16, 64, False), _ints([list(range(16))])
+    q = fa.fa_paged_append(k, k, *pages, table, _ints([256]), q=k, cos=cos, sin=sin, interleaved=inter)
+    assert torch.equal(q, once(y)) and torch.equal(pages[0].view(256, 64), once(y)[0, 0])
+    assert fa.fa_device_status() == 0

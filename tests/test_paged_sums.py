@@ -237,10 +237,25 @@ def _near_ties(inter):
     return k.bfloat16(), middle.float(), sin.float(), at
 
 
+def _turned_once(k, cos, sin, at):
+    """Rows [n, D] turned and rounded to bf16 once.  Products of 8 and 24 bits are exact in 64.  Some sums miss the middle by less
+    than 2^-53 of it: one that is the middle in 64 bits moves a step to the side of what it dropped (Knuth's TwoSum)."""
+    a, b, c, s = k[0, 0][:, at[0]].double(), k[0, 0][:, at[1]].double(), cos.double(), sin.double()
+    out = torch.empty(k.shape[2:], dtype=torch.bfloat16, device=k.device)
+    for to, x, y in ((at[0], a * c, -b * s), (at[1], b * c, a * s)):
+        total = x + y
+        part = total - x
+        rest = (x - (total - part)) + (y - part)
+        middle = (total.float().double() == total) & ((total.float().view(torch.int32) & 0xffff) == 0x8000)
+        out[:, to] = once(torch.where(middle & (rest != 0), torch.nextafter(total, rest.sign() * math.inf), total))
+    return out
+
+
 @pytest.mark.parametrize("inter", [False, True])
 def test_near_ties_are_near_ties(inter):
     k, cos, sin, at = _near_ties(inter)
     y = turned(k, torch.arange(256), cos, sin, 64, inter)[0, 0][:, at[0]]
+    assert torch.equal(_turned_once(k, cos, sin, at)[:, at[0]], once(y))
     # rounded to fp32 first, a good part of those less than 2^-25 beside the middle go the wrong way
     assert int((y.float().bfloat16() != once(y)).sum()) > 1000
     off = (y / (k[0, 0][:, at[0]].double() * cos.double()) - 1).abs()
@@ -252,10 +267,11 @@ def test_near_ties_are_near_ties(inter):
 def test_sums_beside_the_middle_of_two_bf16_values(inter):
     import attention_tiled_fwd_gb300 as fa
     cuda_or_skip()
-    k, cos, sin, _ = (t.cuda() if torch.is_tensor(t) else t for t in _near_ties(inter))
-    y = turned(k, torch.arange(256, device="cuda"), cos, sin, 64, inter)
-    assert int((y.float().bfloat16() != once(y)).sum()) > 1000
+    k, cos, sin, at = (t.cuda() if torch.is_tensor(t) else t for t in _near_ties(inter))
+    want = _turned_once(k, cos, sin, at)
+    y = turned(k, torch.arange(256, device="cuda"), cos, sin, 64, inter)[0, 0]
+    assert int((y.float().bfloat16() != want).sum()) > 1000
     pages, table = _pool(_gen(65), 16, 1, 16, 64, False), _ints([list(range(16))])
     q = fa.fa_paged_append(k, k, *pages, table, _ints([256]), q=k, cos=cos, sin=sin, interleaved=inter)
-    assert torch.equal(q, once(y)) and torch.equal(pages[0].view(256, 64), once(y)[0, 0])
+    assert torch.equal(q[0, 0], want) and torch.equal(pages[0].view(256, 64), want)
     assert fa.fa_device_status() == 0

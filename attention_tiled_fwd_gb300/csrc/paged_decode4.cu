@@ -145,8 +145,8 @@ __device__ __forceinline__ void prepare_q(const __nv_bfloat16 *q, bool there, fl
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int shift = 24 - __shfl_sync(0xffffffffu, up, 4 * (2 * tq + e));  // the codes' 2^-24 too
-        f[e] = fmaxf(scale_log2 * __int_as_float((127 + shift / 2) << 23) * __int_as_float((127 + shift - shift / 2) << 23),
-                      1.2e-38f);  // (above 0: -inf times it stays -inf)
+        f[e] = scale_log2 * __int_as_float((127 + shift / 2) << 23) * __int_as_float((127 + shift - shift / 2) << 23);
+        f[e] = fminf(fmaxf(f[e], 1.2e-38f), 3e38f);  // (above 0: -inf times it stays -inf; finite: a product of 0 stays 0)
     }
     uint32_t part[2][kGroups];  // fp16 of -8 2^-24 sum q, and of what that leaves
 #pragma unroll

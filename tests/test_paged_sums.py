@@ -275,3 +275,29 @@ def test_sums_beside_the_middle_of_two_bf16_values(inter):
     q = fa.fa_paged_append(k, k, *pages, table, _ints([256]), q=k, cos=cos, sin=sin, interleaved=inter)
     assert torch.equal(q[0, 0], want) and torch.equal(pages[0].view(256, 64), want)
     assert fa.fa_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("size", [2.0 ** 100, 2.0 ** 127])
+def test_a_huge_query_over_keys_of_zeros(four, size):
+    """Scores of 0, however large q is: O is the values' mean, and L the logarithm of their number."""
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    g = _gen(67)
+    pages = list(fa.paged_cache(20, 1, 16, 64, fa.FA_INT4 if four else fa.FA_BF16))
+    table, lens = _ints([list(range(20))]), _ints([300])
+    k, v = torch.zeros(1, 1, 300, 64, dtype=torch.bfloat16, device="cuda"), _randn(g, 1, 1, 300, 64)
+    fa.fa_paged_append(k, v, *pages, table, lens)
+    if four:  # keys whose codes are 8, of scales that are not 0
+        pages[0].view(20, 9 * 64)[:, 8 * 64:] = torch.full((20, 32), 0.5).half().view(torch.uint8).cuda()
+    q = torch.zeros(1, 2, 1, 64, dtype=torch.bfloat16, device="cuda")
+    q[0, 0, 0, 5], q[0, 1, 0, 60] = size, -size
+    o, lse = fa.fa_paged_decode(q, *pages, table, lens, scale=1.0)
+    values = fa.fa_paged_gather(*pages, table, lens, rows=300)[1][0, 0].double()
+    if four:
+        values = unit_values(pages[1], 64, True)[0].view(320, 64)[:300]
+    O, A = values.mean(0), values.abs().mean(0)
+    check(o[0, :, 0], O.expand(2, 64), (U * O.abs() + 2.0 ** -10 * A).expand(2, 64), "O")
+    check_lse(lse[0, :, 0], torch.full((2,), math.log(300.0), dtype=torch.float64, device="cuda"), "LSE")
+    assert fa.fa_device_status() == 0

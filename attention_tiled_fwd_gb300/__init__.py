@@ -531,6 +531,8 @@ def paged_cache(n_pages: int, heads: int, page: int, D: int, dtype: int = FA_BF1
 def rotation_table(positions: int, rot: int, base: float = 10000.0,
                    device: Optional[torch.device] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """cos and sin [positions, rot / 2] fp32 of the angles p * base ** (-2 i / rot), taken in 64 bits."""
+    if rot % 2 != 0:
+        raise ValueError(f"rot must be even, got {rot}")
     i = torch.arange(0, rot, 2, dtype=torch.float64)
     angle = torch.arange(positions, dtype=torch.float64)[:, None] * torch.pow(torch.tensor(base, dtype=torch.float64), -i / rot)
     device = torch.device("cuda") if device is None else device

@@ -219,6 +219,13 @@ def test_four_bit_scales_of_unlike_size(D, weight, size, other):
     check_lse(lse[:, 0, 0], L.expand(lists), "LSE")
 
 
+def test_an_odd_number_of_rotated_channels_is_refused():
+    """It would give angles of `rot` for rot / 2 + 1 / 2 pairs, which an append then takes for those of rot + 1."""
+    from attention_tiled_fwd_gb300 import rotation_table
+    with pytest.raises(ValueError):
+        rotation_table(10, 15, device="cpu")
+
+
 def _near_ties(inter):
     """Rows [1, 1, n, D], cosines and sines whose rotated channels lie 2^-20 to 2^-40 of themselves beside the middle of two bf16 values:
     a cos is the middle itself (a power of two times a number of 9 bits), b sin what it misses."""

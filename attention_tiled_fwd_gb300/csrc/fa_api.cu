@@ -911,6 +911,22 @@ int check_paged_decode(int B, int Hq, int Hkv, int n_q, int D, int n_pages, int 
 }
 }  // namespace
 
+namespace {
+// The bytes that a tensor reaches, strided rows and what lies between them.
+struct Span {
+    uintptr_t begin, end;
+    Span(const void *p, long long bytes) : begin(reinterpret_cast<uintptr_t>(p)), end(begin + bytes) {}
+    // [sizes, D] bf16 rows, strides in elements
+    Span(const void *p, const long long (&strides)[3], const int (&sizes)[3], int D) : Span(p, 2ll * D) {
+        for (int i = 0; i < 3; ++i) {
+            const long long far = 2 * strides[i] * (sizes[i] - 1);
+            (far < 0 ? begin : end) += far;
+        }
+    }
+    bool meets(const Span &o) const { return begin < o.end && o.begin < end; }
+};
+}  // namespace
+
 extern "C" int fa_paged_append(const void *q, const void *k, const void *v, const long long *strides, const float *cos,
                                const float *sin, const int *table, const int *lens, const int *counts, void *q_out,
                                void *k_pages, void *v_pages, int B, int Hq, int Hkv, int n, int D, int rot, int interleaved,
@@ -938,6 +954,13 @@ extern "C" int fa_paged_append(const void *q, const void *k, const void *v, cons
     for (const int *p : {table, lens, counts})
         if (rc == FA_OK) rc = check_lens(p);
     if (rc != FA_OK) return rc;
+    const long long pool = (long long)n_pages * Hkv * page * page_row_bytes(D, cache_dtype == FA_INT4);
+    const Span out[3] = {{k_pages, pool}, {v_pages, pool}, {q_out, 2ll * B * Hq * n * D}};
+    const Span in[3] = {{k, a.sk, {B, Hkv, n}, D}, {v, a.sv, {B, Hkv, n}, D}, {q, a.sq, {B, Hq, n}, D}};
+    for (int i = 0; i < (q ? 3 : 2); ++i) {
+        for (int j = 0; j < (q ? 3 : 2); ++j)
+            if (out[i].meets(in[j]) || (i != j && out[i].meets(out[j]))) return FA_ERR_SHAPE;
+    }
     int dev;
     DeviceState *st;
     rc = device_state(&dev, &st);

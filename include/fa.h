@@ -345,14 +345,15 @@ FA_API int fa_prefix_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q, int
  *   heads and rows of q, of k and of v (multiples of 8, but for sizes of 1; rows of D are contiguous), NULL: contiguous.
  *   Row i sits at position lens[b] - n + i.  counts (device array of B ints, NULL: n): the last counts[b] rows are new;
  *   rows before them and rows before position 0 are left out.  q may be NULL (then Hq = 0 and q_out NULL);
- *   q_out [B, Hq, n, D] contiguous, not q itself: rotated rows, zeros for rows that are left out or past the capacity.
+ *   q_out [B, Hq, n, D] contiguous: rotated rows, zeros for rows that are left out or past the capacity.
  *   Rotation of the first rot channels (a multiple of 16, 0: none, cos and sin may be NULL): with the pair (a, b) of
  *   channels (c, c + rot / 2), or (2 c, 2 c + 1) with interleaved != 0, and cos, sin [positions, rot / 2] fp32 of the row's
  *   position: a cos - b sin, b cos + a sin, rounded to bf16 once.  positions >= capacity.
  *   FA_INT4: of 32 channels of the bf16 row y, scale = fp16(max |y| / 7) (65504 at most; NaN where y is not finite),
  *   code = 8 + y fp32(1 / scale) rounded to even, in 1 .. 15.
  * Positions that are not new keep what their pages hold, in the same unit too.  A page that takes rows belongs to one
- * sequence, no position is given twice, and k_pages and v_pages are two buffers.  One kernel.
+ * sequence, and no position is given twice.  q_out, k_pages and v_pages lie apart from one another and from where the rows
+ * of q, k and v begin to where they end (FA_ERR_SHAPE).  One kernel.
  */
 FA_API int fa_paged_append(const void *q, const void *k, const void *v, const long long *strides, const float *cos,
                            const float *sin, const int *table, const int *lens, const int *counts, void *q_out,

@@ -31,11 +31,13 @@ namespace {
 
 constexpr int kWarps = kDecodeWarps;
 constexpr int kThreads = 32 * (kWarps + 1);
-// Keys of a warp whose products stay in the accumulators.  The tensor cores drop what lies 2^-25 below a sum, n 2^-26 of a sum of n
-// products at most: here 2^-14 of sum P s code and of 8 sum P s, which are larger than O by the root of the number of keys and more.
-// With all of a list in them O's error grew with its length (rms 1.6e-3 at 10^6 keys, 5e-3 at 4 10^6, 1.6e-2 at 8 10^6); now it is 1.6e-3,
-// the output's own rounding, at any length.  Four times as often costs 1 % (124 instead of 122 us for 64 sequences of 900 to 16384).
-constexpr int kFoldKeys = 4096;
+// The tensor cores drop what lies 2^-25 below a sum, n 2^-26 of a sum of n products at most.  O's accumulators hold sum P s code, and
+// that and 8 sum P s are larger than O by the root of the number of keys and more: every kCentreKeys keys of a warp 8 sum P s is taken off.
+// What is left loses 2^-13 of itself in kFoldKeys keys; then it is taken out and added up in fp32, in local memory.  With all of that at
+// a list's end alone, errors beside the output's own rounding (1.65e-3) were 2.2e-3 for lists of 32768 keys, heads of 128, and O lost 1.6 % at
+// 8 10^6; now they are 3.2e-4, from the weights' roundings, at any length.  48 sequences of 9000 to 32768: 198 us with 512 and 4096 keys,
+// 197 with 512 or 1024 and 8192 (196.5 without any), 202 with all of it every 2048, 204 every 1024.
+constexpr int kCentreKeys = 512, kFoldKeys = 8192;
 constexpr int kLift = 6;  // weights carry 2^6, so they are 2^14 at most
 
 enum : int { kSiteEmpty = 311, kSiteFull, kSiteDrain };
@@ -191,7 +193,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(PagedDecodeArgs a) {
     using C = Cfg<D>;
     using U = Unit4<D>;
-    constexpr int kFold = kFoldKeys / (C::kUnits * kUnit);  // tiles
+    constexpr int kCentre = kCentreKeys / (C::kUnits * kUnit), kFold = kFoldKeys / (C::kUnits * kUnit);  // tiles
     constexpr int kTile = C::kTile, kGroups = D / 32, kRows = 8, kStages = C::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -311,8 +313,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
         float held_off[2];
         asm volatile("" ::"l"(held), "l"(held_off) : "memory");
         for (int t = t0; t < t1;) {
-            const bool first = t == t0;
-            for (const int stop = min(t1, t + kFold); t < stop; ++t) {
+            for (const int stop = min(t1, t + kCentre); t < stop; ++t) {
                 const int tile = tiles.tile(t), key_warp = tile * kTile + warp * (C::kUnits * kUnit);
                 const int span = kSpans == 1 ? tile : tile * kSpans + warp;
                 const bool plain = span >= plain0 && span < plain1;
@@ -485,19 +486,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
                 warp_arrive(&empty[stage]);
                 if (++stage == kStages) stage = 0, phase ^= 1;
             }
-            // sum P v out of the accumulators, added up in fp32 as such
-            const float by = __int_as_float((127 - up) << 23), by8 = -8.f * by, by20 = 0x1p20f * by, by24 = 0x1p24f * by;
+            // 8 sum P s off the codes' sums
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
                 const float *one = ones[i / 4] + (i & 2);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float less8 = by8 * one[e];
-                    o[i][e] = fmaf(o[i][e], by24, less8);
-                    o[i][2 + e] = fmaf(o[i][2 + e], by20, less8);
+                    o[i][e] = fmaf(one[e], -0x1p-21f, o[i][e]);
+                    o[i][2 + e] = fmaf(one[e], -0x1p-17f, o[i][2 + e]);
                 }
             }
-            if (!first) {
+#pragma unroll
+            for (int j = 0; j < kGroups / 2; ++j) ones[j][0] = ones[j][1] = ones[j][2] = ones[j][3] = 0.f;
+            if (t < t1 && (t - t0) % kFold != 0) continue;
+            // O out of the accumulators, added up in fp32 as such
+            const float by = __int_as_float((127 - up) << 23), by20 = 0x1p20f * by, by24 = 0x1p24f * by;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) o[i][0] *= by24, o[i][1] *= by24, o[i][2] *= by20, o[i][3] *= by20;
+            if (t - t0 > kFold) {
                 const float since0 = ex2_approx(held_off[0] - off[0]), since1 = ex2_approx(held_off[1] - off[1]);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
@@ -515,8 +521,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
                 held[i] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
                 o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
             }
-#pragma unroll
-            for (int j = 0; j < kGroups / 2; ++j) ones[j][0] = ones[j][1] = ones[j][2] = ones[j][3] = 0.f;
             asm volatile("" ::"l"(held), "l"(held_off) : "memory");
         }
 

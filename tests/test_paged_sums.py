@@ -155,6 +155,36 @@ def test_four_bit_sums_over_the_longest_lists(D):
     check_lse(lse[some, 1, 0], L[1:], "LSE")
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_four_bit_sums_of_values_that_cancel(D):
+    """131072 keys a list, most lists one CTA's: O is a few thousandths of sum P |v|, and the codes' sum hundreds of times O.
+
+    Of independent roundings that are off by half a step 2^-11 at most, uniformly, the error's root mean square is 2^-11 / sqrt(3) of a
+    product's, and of O's, as the products are independent.  The weights' and the products' are two: 4e-4; 5e-4 with all else.
+    O's own rounding is what rounding the reference gives."""
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    g, n, lists = _gen(73 + D), 1 << 17, {64: 650, 128: 500, 256: 340}[D]
+    codes = [torch.randint(1, 16, (256, 8 * D * 2), generator=g, device="cuda", dtype=torch.uint8) for _ in range(2)]  # of 256 units
+    pages = []
+    for c in codes:
+        units = torch.empty((n // 16, 9 * D), dtype=torch.uint8, device="cuda")
+        at = torch.randint(0, 256, (2, n // 16), generator=g, device="cuda")
+        units[:, :8 * D] = c[at[0]][:, ::2] | c[at[1]][:, 1::2] << 4  # (pairs of any two units' halves: all units differ)
+        scales = torch.rand((n // 16, D // 2), generator=g, device="cuda") * 0.2 + 0.22
+        units[:, 8 * D:] = scales.half().view(torch.uint8)
+        pages.append(units.view(-1, 1, 64, 9 * D // 16))
+    q = _randn(g, lists, 1, 1, D)
+    o, _ = fa.fa_paged_decode(q, *pages, torch.arange(n // 64, device="cuda", dtype=torch.int32).expand(lists, -1).contiguous())
+    assert fa.fa_device_status() == 0
+    some = torch.arange(0, lists, 5, device="cuda")
+    k, v = (unit_values(t, D, i == 1)[0].view(-1, D) for i, t in enumerate(pages))
+    O = _one_sequence(q[some, 0, 0], lambda i, j: k[i:j], lambda i, j: v[i:j], n, 1 / math.sqrt(D))[0]
+    size, store, error = (float(t.square().mean().sqrt()) for t in (O, O.float().bfloat16().double() - O, o[some, 0, 0].double() - O))
+    assert error < math.hypot(store, 5e-4 * size), (error / size, store / size)
+
+
 def _four_bit_pages(codes, scales, of_values):
     """Pages [n / 16, 1, 16, 9 D / 16] of rows of one head with these codes [n, D] and scales [n, D / 32]."""
     n, D = codes.shape

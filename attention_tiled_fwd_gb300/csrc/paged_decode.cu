@@ -224,8 +224,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
                             if (!(seen >> (g + 8) & 1u)) sc[n][2 + e] = -INFINITY;
                         }
                 }
-                // the weights' logarithms; the maxima are taken again only when a weight would grow past 2^8
-                auto logs = [&](int n, int e) { return fmaf(sc[n][e], a.scale_log2, -m[n][e & 1]); };
+                // the weights' logarithms; the maxima are taken again only when a weight would grow past 2^8 (products rounded as those
+                // of the maxima are: unrounded, scores past 2^32 left weights that overflow)
+                auto logs = [&](int n, int e) { return __fmul_rn(sc[n][e], a.scale_log2) - m[n][e & 1]; };
                 bool grow = false;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) grow |= fmaxf(fmax3(logs(n, 0), logs(n, 1), logs(n, 2)), logs(n, 3)) > 8.f;

@@ -416,14 +416,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
                             for (int j = 0; j < kGroups; ++j) s2[w][half][j] = mul_h2(s2[w][half][j], by);
                 }
 
-                // the weights' logarithms; the maxima are taken again only when a weight would grow past 2^8
+                // the weights' logarithms; the maxima are taken again only when a weight would grow past 2^8 (products rounded as those
+                // of the maxima are: unrounded, scores past 2^26 left weights that fp16 does not hold)
                 bool grow = false;
                 float lg[C::kUnits][4];
                 auto logs = [&] {
 #pragma unroll
                     for (int w = 0; w < C::kUnits; ++w)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) lg[w][e] = fmaf(sc[w][e], f[e & 1], -off[e & 1]);
+                        for (int e = 0; e < 4; ++e) lg[w][e] = __fmul_rn(sc[w][e], f[e & 1]) - off[e & 1];
                 };
                 logs();
                 constexpr float most = 8.f + kLift;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from helpers import cuda_or_skip
-from paged_ref import once, place, rows_of, turned, unit_values
+from paged_ref import decode_reference, once, place, rows_of, turned, unit_values
 from test_paged import _gen, _ints, _pool, _randn, _tables
 from window_ref import U, attend, check, check_lse, visible
 
@@ -337,4 +337,21 @@ def test_a_huge_query_over_keys_of_zeros(four, size):
     O, A = values.mean(0), values.abs().mean(0)
     check(o[0, :, 0], O.expand(2, 64), (U * O.abs() + 2.0 ** -10 * A).expand(2, 64), "O")
     check_lse(lse[0, :, 0], torch.full((2,), math.log(300.0), dtype=torch.float64, device="cuda"), "LSE")
+    assert fa.fa_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("size", [1e7, 1e9, 1e14, 1e30])
+def test_scores_of_any_size(four, size):
+    """Scores so large that one key has all the weight: O is its value, L its score to fp32's precision (D products, 2^-24 of them each)."""
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    g = _gen(69)
+    pages, table, lens = _pool(g, 20, 1, 16, 64, four), _ints([list(range(20))]), [300]
+    q = (torch.randn(1, 8, 1, 64, generator=g, device="cuda") * size).bfloat16()
+    o, lse = fa.fa_paged_decode(q, *pages, table, _ints(lens), scale=1.0)
+    ref = decode_reference(q, pages, table, lens, 320, 0, 1.0)
+    check(o, ref["o"], ref["o_bound"], "O")
+    assert float((lse.double() / ref["lse"] - 1).abs().max()) < 64 * 2.0 ** -22
     assert fa.fa_device_status() == 0

@@ -995,10 +995,13 @@ PagedGrid paged_grid(int B, int Hq, int Hkv, int n_q, int D, int page, int keys,
     g.row_tiles = (R + g.plan.rows - 1) / g.plan.rows;
     const long long tiles = (keys + g.plan.tile - 1) / g.plan.tile, lists = (long long)B * Hkv * g.row_tiles;
     const long long slots = (long long)num_sms * g.plan.per_sm;
-    // Few lists of few tiles: clusters.  Without the run's search and the join behind it they are faster on the device up to three
-    // tiles a CTA or, with many lists, up to all (16 sequences of 8 heads of 128, 512 keys: 8.8 us instead of 11.1, in 4 bits 9.2
-    // instead of 10.7), and the host saves a launch and the workspace, 6 us of 25 a call.  At per_cluster tiles they are
-    // 1 us behind (one sequence of 4 heads of 128, 3001 keys: 9.6 us instead of 8.9, in 4 bits 10.3 instead of 9.3).
+    // Few lists of few tiles: clusters.  The rule is for calls made one by one, which the host bounds: a launch and the workspace less
+    // save it 3 to 4 us of 17 to 25 at any size.  On the device alone, in a captured graph, clusters save the run's search and the join
+    // behind it, but spread a list over 8 CTAs at most.  They gain up to 1.9 us at 2 to 4 tiles, and at any number where 64 lists share
+    // the SMs (16 sequences of 4 heads of 128, 1024 keys: 1.3 us; 4-bit heads of 64: nothing); they are level at 8 to 16 (from 1.4 us
+    // behind to 1 ahead); and at per_cluster tiles a CTA they lose 1.3, 2.0 and 2.6 us for one list of heads of 64, 128 and 256, 0.3 to 1
+    // for 16 lists, in 4 bits 1.5, 2.2 and 3.1 (one sequence of 3001 keys of 4 heads of 128: 10.1 us instead of 8.9, in 4 bits 10.2
+    // instead of 9.4).
     for (int c = 8; c > 1 && g.cluster == 0; c /= 2) {
         // one wave: a cluster needs c / per_sm SMs of one GPC, which leaves some of a GPC's over, up to half of them for 8
         const long long room = c > 4 * g.plan.per_sm ? slots / 2 : slots - slots / 8;

@@ -21,7 +21,7 @@ namespace fa {
 
 constexpr int kUnit = 16;                // positions of a unit of 4-bit pages, and the least page
 constexpr int kMaxPage = 256;
-constexpr int kMaxCapacity = 1 << 23;    // positions of a sequence: a warp of the decode kernel adds up a quarter, kMaxSum
+constexpr int kMaxCapacity = 1 << 23;    // positions of a sequence: sums of 2^21 keys a warp are tested, longer ones are not
 constexpr int kErrPage = 13;             // FA_ERR_PAGE in the status word
 
 template <int D>

@@ -10,8 +10,9 @@
 // NaN scale; a scale past fp16's largest stays there.
 //
 // What bounds them.  Rows of bf16 into pages: HBM, less the start and the end of one launch: 4 x 4096 rows of 16/4 heads of 128
-// 36 us, 5.8 TB/s; 8 x 2048 rows of 32/8 heads 67 us, 6.1 TB/s; without a rotation 6.4 TB/s.  4-bit rows: the instructions of
-// rounding and packing (issue slots 72 %): the 4 x 4096 rows 38 us, 4.7 TB/s.  One token: a launch and three reads that wait on one
+// 36 us, 5.8 TB/s; 8 x 2048 rows of 32/8 heads 67 us, 6.1 TB/s; without a rotation 6.4 TB/s.  4-bit rows, 71 % of a copy's rate: waits for
+// loads (a warp's one task is a chain of length, rows and cosines, and page, with 43 % of the warps that an SM can have), on top of the
+// instructions of rounding and packing (issue slots 72 %): the 4 x 4096 rows 38 us, 4.8 TB/s.  One token: a launch and three reads that wait on one
 // another (length, page, row), 3.4 us for 64 sequences.  Gather: HBM: 4 sequences of 20000 to 32768 keys of 8 heads in 4 bits
 // 85 us, 6.5 TB/s.
 // Not kept (append of 2 x 2000 rows of 32/8 heads in 4 bits and a gather of 2 x 9000 to 16384 take 45.4 us): a lane with both halves

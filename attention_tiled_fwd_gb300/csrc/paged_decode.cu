@@ -9,15 +9,15 @@
 // instruction where rows as the tall side would leave half of it empty.  tcgen05 would need 128 of them.
 //   warp 4     producer: 64-key tiles of keys and values into a ring, a TMA box for every page and 64 columns; above D = 64 keys
 //   (warp 5)   alone, and warp 5 values: a warp's copies go out 25 ns apart, 16 or 32 of them a tile where pages are small (one
-//              sequence of 3001 keys in pages of 16, D = 128, a cluster: 11.4 us with one producer, 9.9 with two)
+//              sequence of 3001 keys in pages of 16, D = 128, a cluster: 1.5 us less than with one producer)
 //   warps 0-3  units of 16 keys each, with a softmax state of their own, joined at a list's end
 // The work is one list of tiles, sequence by sequence and head by head, cut into equal runs for a grid of one wave, however
 // long the sequences are (lengths are read on the device).  A CTA writes O and L of what it holds whole; of what it shares
 // with its neighbours it writes a partial, and paged_join_kernel adds those up.  Where there are few lists of few tiles (the rule
 // is paged_grid's, fa_api.cu), the CTAs of a cluster share a list instead and join its partials through distributed shared memory.
-// Measured: 64 sequences of 900 to 16384 keys of 8 heads of 128 (2.27 GB) 326 us, 6.95 TB/s, which is the rate of a copy; one
-// sequence of 3001 keys of 4 heads 9.6 us as a cluster; cut into runs 8.9: the launch, the search (1 us), q (1 us), a first tile
-// (1.5 us), the join (2.5 us).
+// Measured: 64 sequences of 900 to 16384 keys of 8 heads of 128 (2.27 GB) 330 us, 6.9 TB/s, which is the rate of a copy (8192 keys of
+// heads of 64: 168 us, 6.4 TB/s; of 256: 609 us, 7.1 TB/s); one sequence of 3001 keys of 4 heads 10.1 us as a cluster; cut into runs
+// 8.9: the launch, the search (1 us), q (1 us), a first tile (1.5 us), the join (2.5 us).
 //
 // Keys that a row does not see may hold anything: their scores are replaced; values that no row sees are cleared before the
 // product, and those that some rows see are kept from the others where they are not finite (0 times them would be NaN).
@@ -49,7 +49,8 @@ struct Cfg {
 };
 
 // What a list costs besides its tiles, in tiles (its length, q, the join, the stores), so that runs of many lists end with the
-// others: with 1 or 2 instead, 256 sequences of 1 to 300 keys took 27.1, 45.1 and 92 us at D = 64, 128 and 256, now 25.6, 39.1, 75.4.
+// others: with 1 or 2 instead, 256 sequences of 1 to 300 keys took 6, 15 and 22 % longer at D = 64, 128 and 256; they take 27.4, 41.4 and
+// 80.6 us now, 43, 58 and 59 % of the pages' bytes at the rate of a copy.
 template <int D>
 constexpr int kListCost = D == 64 ? 4 : 3;
 

@@ -13,8 +13,8 @@
 //
 //   warp 4     producer: tiles of keys and values into a ring, a bulk copy for every page
 //   warps 0-3  kUnits neighbouring units of 16 keys of every tile each
-// Measured, 8 heads of 128: 48 sequences of 9000 to 32768 keys 198 us, 5.85 TB/s (86 % of a copy's rate), 64 of 900 to 16384 in pages of
-// 16 123 us, 5.2 TB/s.  A steady run of tiles goes at 95 %, 55 % of the issue slots taken over a launch of 61 us; the rest is its
+// Measured, 8 heads of 128: 48 sequences of 9000 to 32768 keys 198 us, 5.83 TB/s (86 % of a copy's rate), 64 of 900 to 16384 in pages of
+// 16 122 us, 5.2 TB/s (77 %).  A steady run of tiles goes at 95 %, 55 % of the issue slots taken over a launch of 61 us; the rest is its
 // start (5 us), the lists' ends (3 us each) and CTAs of an SM that do not end together.
 // Not kept: a ring for every warp, filled by itself, leaves room for 16 warps that compute instead of 12, but the copies' integer work
 // comes four times (170 us where this took 147, before other steps).
@@ -185,7 +185,8 @@ __device__ __forceinline__ void prepare_q(const __nv_bfloat16 *q, bool there, fl
 }
 
 // What a list costs besides its tiles, in tiles: with 2, 1 and 1 instead, 100 sequences of 100 to 3000 keys took 37, 57 and 109 us at
-// D = 64, 128 and 256, now 35, 49 and 88; 64 of 900 to 16384 76, 121 and 253, now 76, 118 and 237.
+// D = 64, 128 and 256, with these 35, 49 and 88 (38, 54 and 60 % of the pages' bytes at the rate of a copy); 64 of 900 to 16384 76, 121 and
+// 253, with these 76, 118 and 237.
 template <int D>
 constexpr int kListCost = D == 64 ? 4 : D == 128 ? 3 : 5;
 

@@ -367,8 +367,9 @@ FA_API int fa_paged_append(const void *q, const void *k, const void *v, const lo
  * taken as the nearer end, NULL: capacity.  Rows that see nothing get O = 0 and LSE = -inf.  Rows from lens[b] on, and
  * those between the sinks and the first window, may hold anything, and pages of theirs alone need no entry.
  *   workspace: fa_paged_decode_workspace_bytes(...) bytes, 16-byte aligned (NULL when that is 0; never more than 16 MB);
- *   two calls that run concurrently must not share it.  Sums are taken in an order that the sizes, window and sinks decide: equal
- *   calls give equal bits.
+ *   two calls that run concurrently must not share it.  Equal calls give equal bits.  The order of the sums depends on the
+ *   sizes, the window, the sinks and the lengths of all sequences (their work is cut into runs together), so a sequence's last
+ *   bits may differ beside other neighbours.
  */
 FA_API int fa_paged_decode(const void *q, const void *k_pages, const void *v_pages, const int *table, const int *lens,
                            void *o, float *lse, int B, int Hq, int Hkv, int n_q, int D, int n_pages, int page, int slots,

@@ -955,11 +955,12 @@ extern "C" int fa_paged_append(const void *q, const void *k, const void *v, cons
         if (rc == FA_OK) rc = check_lens(p);
     if (rc != FA_OK) return rc;
     const long long pool = (long long)n_pages * Hkv * page * page_row_bytes(D, cache_dtype == FA_INT4);
-    const Span out[3] = {{k_pages, pool}, {v_pages, pool}, {q_out, 2ll * B * Hq * n * D}};
-    const Span in[3] = {{k, a.sk, {B, Hkv, n}, D}, {v, a.sv, {B, Hkv, n}, D}, {q, a.sq, {B, Hq, n}, D}};
-    for (int i = 0; i < (q ? 3 : 2); ++i) {
-        for (int j = 0; j < (q ? 3 : 2); ++j)
-            if (out[i].meets(in[j]) || (i != j && out[i].meets(out[j]))) return FA_ERR_SHAPE;
+    const Span kp(k_pages, pool), vp(v_pages, pool);
+    if (kp.meets(vp)) return FA_ERR_SHAPE;
+    if (q) {
+        const Span out(q_out, 2ll * B * Hq * n * D);
+        for (const Span &s : {kp, vp, Span(q, a.sq, {B, Hq, n}, D), Span(k, a.sk, {B, Hkv, n}, D), Span(v, a.sv, {B, Hkv, n}, D)})
+            if (out.meets(s)) return FA_ERR_SHAPE;
     }
     int dev;
     DeviceState *st;

@@ -352,8 +352,9 @@ FA_API int fa_prefix_decode_workspace_bytes(int B, int Hq, int Hkv, int n_q, int
  *   FA_INT4: of 32 channels of the bf16 row y, scale = fp16(max |y| / 7) (65504 at most; NaN where y is not finite),
  *   code = 8 + y fp32(1 / scale) rounded to even, in 1 .. 15.
  * Positions that are not new keep what their pages hold, in the same unit too.  A page that takes rows belongs to one
- * sequence, and no position is given twice.  q_out, k_pages and v_pages lie apart from one another and from where the rows
- * of q, k and v begin to where they end (FA_ERR_SHAPE).  One kernel.
+ * sequence, and no position is given twice.  q_out, k_pages and v_pages lie apart from one another, and q_out from where the
+ * rows of q, k and v begin to where they end (FA_ERR_SHAPE).  k and v may be rows of pages, of positions that are not written.
+ * One kernel.
  */
 FA_API int fa_paged_append(const void *q, const void *k, const void *v, const long long *strides, const float *cos,
                            const float *sin, const int *table, const int *lens, const int *counts, void *q_out,

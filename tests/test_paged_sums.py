@@ -123,10 +123,11 @@ def test_bf16_sums_over_the_longest_lists():
 def test_four_bit_sums_over_the_longest_lists(D):
     """As above over 4-bit pages, with values of both signs, so that O is small beside sum P |v|.
 
-    Equal weights are powers of two, so their products with the scales are exact: O is off by the sums alone.  The codes' sum is
-    sum P s code, at most 15 sum P s but here, where the codes' mean is below 9, less than 9; the kernel takes 8 sum P s of it every
-    4096 keys of a warp, and a tensor core's sum of 4096 products loses 2^-14 of itself at most (n 2^-26): both lose, so their
-    difference is off by less than 9 2^-14 sum P s, which does not grow with the list.  512 additions in fp32: 2^-15 sum P |v| < 2^-12 sum P s.
+    Equal weights are powers of two, so their products with the scales are exact: O is off by the sums alone.  A tensor core's sum of n
+    products loses n 2^-26 of itself at most.  The codes' sum is sum P s code, here less than 9 sum P s, as the codes' mean is below 9;
+    8 sum P s comes off it every 512 keys of a warp: 9 2^-17 sum P s.  What is left stays for 8192 keys: 2^-13 sum P |v|, which is less
+    than 4 sum P s (the mean of |code - 8| is 3.7).  Then it is added up in fp32, 256 times: 2^-16 sum P |v|.  Together less than
+    9 2^-14 + 2^-12 of sum P s, whatever the list's length.
     Other weights are rounded twice to 2^-11 as well."""
     import attention_tiled_fwd_gb300 as fa
     cuda_or_skip()

@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
                             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
                             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
                             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-                            if (mt > m[n][e] + 8.f) {
+                            if (mt - m[n][e] > 8.f) {  // (the very test, in the same roundings)
                                 const float alpha = ex2_approx(m[n][e] - mt);
                                 l[n][e] *= alpha;
 #pragma unroll

@@ -442,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_decode4_kernel(
                         mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
                         mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
                         mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-                        mt -= (float)kLift;
-                        if (mt > off[e] + 8.f) {
+                        if (mt - off[e] > most) {  // (the very test, in the same roundings)
+                            mt -= (float)kLift;
                             const float alpha = ex2_approx(off[e] - mt);
                             l[e] *= alpha;
 #pragma unroll

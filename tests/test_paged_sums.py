@@ -356,3 +356,36 @@ def test_scores_of_any_size(four, size):
     check(o, ref["o"], ref["o_bound"], "O")
     assert float((lse.double() / ref["lse"] - 1).abs().max()) < 64 * 2.0 ** -22
     assert fa.fa_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("size", range(22, 31))
+def test_large_scores_that_grow_from_tile_to_tile(four, size):
+    """Scores about 2^size log2 units, fp32's steps there 2^(size - 23), that grow by 2 to 64 from one 128 keys to the next: O stays among
+    the values, L beside the largest score, whichever of the steps a running maximum takes."""
+    import attention_tiled_fwd_gb300 as fa
+    cuda_or_skip()
+    g, n, D = _gen(71), 1024, 64
+    j = (torch.arange(n) // 128).float()
+    q = torch.zeros(1, 6, 1, D, dtype=torch.bfloat16, device="cuda")
+    q[0, :, 0, 0] = 2.0 ** size / 28672
+    q[0, :, 0, 40] = 2.0 ** torch.arange(1, 7, device="cuda")  # a group of its own
+    if four:
+        kc, ks = torch.full((n, D), 8), torch.zeros(n, 2)
+        kc[:, 0], kc[:, 40], ks[:, 0], ks[:, 1] = 15, 8 + j.long(), 4096.0, 1.0
+        pages = [_four_bit_pages(kc, ks, False).cuda()]
+        vc, vs = torch.randint(1, 16, (n, D), generator=torch.Generator().manual_seed(1)), torch.full((n, 2), 0.25)
+        pages.append(_four_bit_pages(vc, vs, True).cuda())
+    else:
+        pages = [_randn(g, n // 16, 1, 16, D) for _ in range(2)]
+        pages[0].zero_()
+        pages[0][..., 0], pages[0].view(n, D)[:, 40] = 28672.0, j.bfloat16().cuda()
+    table, lens = _ints([list(range(n // 16))]).expand(700, -1).contiguous(), _ints([n] * 700)
+    o, lse = fa.fa_paged_decode(q.expand(700, -1, -1, -1).contiguous(), *pages, table, lens, scale=math.log(2.0))
+    v = unit_values(pages[1], D, True)[0].view(n, D) if four else pages[1].view(n, D).double()
+    k = unit_values(pages[0], D, False)[0].view(n, D) if four else pages[0].view(n, D).double()
+    assert bool(o.isfinite().all()) and bool((o[:, :, 0].double().abs() <= v.abs().amax(0) * (1 + U)).all())
+    top = (q[0, :, 0].double() @ k.T).amax(1) * math.log(2.0)
+    assert float((lse[:, :, 0].double() / top - 1).abs().max()) < 64 * 2.0 ** -22
+    assert fa.fa_device_status() == 0
